@@ -18,9 +18,9 @@ def sources():
 
 
 def source_hash() -> str:
-    """SHA-256 of every source the library is built from (kernels, headers, the public header)."""
+    """SHA-256 of every source the library is built from (kernels, headers, the public headers)."""
     h = hashlib.sha256()
-    files = sorted(glob.glob(os.path.join(HERE, "csrc", "*"))) + [os.path.join(ROOT, "include", "moe_plan.h")]
+    files = sorted(glob.glob(os.path.join(HERE, "csrc", "*"))) + sorted(glob.glob(os.path.join(ROOT, "include", "*.h")))
     for f in files:
         h.update(os.path.basename(f).encode())
         with open(f, "rb") as fh:

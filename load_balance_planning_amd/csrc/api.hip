@@ -2,21 +2,13 @@
 // launch sequence of each call.  See include/moe_plan.h for the contract.
 #include <new>
 
-#include "internal.h"
-
-struct moe_plan {
-  moe::Dims d;
-  moe_plan_config cfg;
-  int device;
-  moe::Workspace ws;
-  void* ws_base;
-  size_t ws_bytes;
-  hipStream_t last_stream;  // stream of the last call that enqueued work (moe_plan_status waits for it)
-  moe::KernelEvents gather_ev;  // moe_plan_set_events / moe_plan_set_gather_order: hooks around every gather launch
-  bool acc_dirty;           // a step failed after its top-k was queued: the accumulator may hold counts
-};
+#include "handle.h"
 
 namespace {
+
+using moe::DeviceScope;
+using moe::begin_call;
+using moe::hip_rc;
 
 constexpr size_t kAlign = 256;
 constexpr size_t kMaxLds = 160 * 1024;
@@ -95,35 +87,6 @@ int moe::derive_dims(const moe_plan_config* c, moe::Dims* d) {
   *d = x;
   return MOE_OK;
 }
-
-namespace {
-
-// Makes `device` current for the duration of a call and gives the caller's
-// current device back when the call returns.
-class DeviceScope {
- public:
-  explicit DeviceScope(int device) {
-    if (hipGetDevice(&prev_) != hipSuccess) return;
-    if (prev_ != device && hipSetDevice(device) != hipSuccess) return;
-    switched_ = prev_ != device;
-    ok_ = true;
-  }
-  ~DeviceScope() {
-    if (switched_) (void)hipSetDevice(prev_);
-  }
-  DeviceScope(const DeviceScope&) = delete;
-  DeviceScope& operator=(const DeviceScope&) = delete;
-  bool ok() const { return ok_; }
-
- private:
-  int prev_ = -1;
-  bool switched_ = false;
-  bool ok_ = false;
-};
-
-int hip_rc(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
-
-}  // namespace
 
 extern "C" int moe_plan_query(const moe_plan_config* cfg, moe_plan_sizes* sz) {
   moe::Dims d;
@@ -229,19 +192,6 @@ int moe::check_step_args(const moe::Dims& d, const float* logits, const uint16_t
   if (d.T > 0 && (!logits || !hidden)) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
-
-namespace {
-
-// Set-up shared by the calls that enqueue work: clears an error an earlier
-// HIP call of the caller left behind (so that a failure reported by this
-// call is its own) and remembers the stream for moe_plan_status.
-hipStream_t begin_call(moe_plan_t h, void* stream) {
-  (void)hipGetLastError();
-  h->last_stream = static_cast<hipStream_t>(stream);
-  return h->last_stream;
-}
-
-}  // namespace
 
 extern "C" int moe_plan_route(moe_plan_t h, const float* logits, const int32_t* prev_topk, const moe_route_out* out,
                               void* stream) {
