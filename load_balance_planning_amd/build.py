@@ -3,6 +3,8 @@ import glob
 import hashlib
 import os
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -36,13 +38,7 @@ def up_to_date() -> bool:
         return fh.read().strip() == source_hash()
 
 
-def build(verbose: bool = False) -> str:
-    tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = ["hipcc", "--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-shared",
-           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-           "-Wall", "-Wno-unused-result",
-           "-I", os.path.join(ROOT, "include"), "-I", os.path.join(HERE, "csrc"),
-           "-o", tmp] + sources()
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd))
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -53,7 +49,21 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
     if verbose and msgs:
         print("\n".join(msgs))
+
+
+def build(verbose: bool = False) -> str:
+    """One hipcc per source, several at a time, then the link."""
+    tmp = LIB + ".tmp%d" % os.getpid()
+    common = ["hipcc", "--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC",
+              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+              "-Wall", "-Wno-unused-result",
+              "-I", os.path.join(ROOT, "include"), "-I", os.path.join(HERE, "csrc")]
     digest = source_hash()
+    with tempfile.TemporaryDirectory(prefix="moe_plan_build_") as obj_dir:
+        objs = {src: os.path.join(obj_dir, os.path.basename(src) + ".o") for src in sources()}
+        with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as pool:
+            list(pool.map(lambda src: _run(common + ["-c", "-o", objs[src], src], verbose), objs))
+        _run(["hipcc", "--offload-arch=" + ARCH, "-fPIC", "-shared", "-o", tmp] + list(objs.values()), verbose)
     os.replace(tmp, LIB)
     with open(HASH + ".tmp", "w") as fh:
         fh.write(digest + "\n")
