@@ -1,0 +1,203 @@
+/*
+ * moe_experts -- the operators of the expert layer around a dispatch plan on
+ * MI355X: the router's scores and weights with their gradient, the experts'
+ * products in 8-bit floating point, and the weighted combine with its
+ * gradient.  Same library, handles, conventions, status word and error codes
+ * as moe_plan.h.
+ *
+ *   moex_gate / moex_gate_grad
+ *                      scores, balance bias, expert groups, top-k and weights
+ *                      of a router, with moe_plan_route's histograms; the
+ *                      gradient of the weights for the logits
+ *   moex_quantize      bf16 rows to e4m3 with one scale per 1 x 128 block
+ *   moex_quantize_weights
+ *                      bf16 expert matrices to e4m3 with one scale per
+ *                      128 x 128 block, and the transposed matrices
+ *   moex_swiglu / moex_swiglu_grad
+ *                      the gated activation between two products and its
+ *                      gradient, quantized as moex_quantize does
+ *   moex_matmul        each instance's rows times its expert's matrix
+ *   moex_wgrad         gradient of the experts' matrices
+ *   moex_combine / moex_combine_grad
+ *                      sum of a token's expert rows by given weights, and the
+ *                      gradients of rows and weights
+ *
+ * A training pass of one layer, forward then backward:
+ *   moex_gate -> moe_plan_plan -> moe_plan_dispatch -> moex_quantize ->
+ *   moex_matmul (gate and up) -> moex_swiglu -> moex_matmul (down) ->
+ *   moex_combine;
+ *   moex_combine_grad -> moex_quantize -> moex_matmul (down, transposed) and
+ *   moex_wgrad -> moex_swiglu_grad -> moex_matmul (gate and up, transposed)
+ *   and moex_wgrad -> moex_combine without weights (gradient of the dispatch);
+ *   moex_gate_grad.
+ *
+ * Blocks of 128.  A quantized row of C columns holds Cp e4m3 bytes (OCP: 4
+ * exponent and 3 mantissa bits, largest value 448, 0x7F and 0xFF not a number),
+ * Cp = C rounded up to 128, zeros from column C on, and one scale byte per 128
+ * columns, S = Cp / 128 rounded up to 4 of them per row, 127 from block Cp/128
+ * on.  Scale byte s stands for 2^(s - 127) (E8M0); 255 marks a block that held
+ * a NaN or an infinity, and every sum over such a block is NaN.
+ *   rows      q uint8 [rows][Cp], scale uint8 [rows][S]: a scale per 1 x 128
+ *   matrices  q uint8 [E][N][Kp], scale uint8 [E][ceil(N/128)][S]: a scale per
+ *             128 x 128
+ * The quantizer's scale is the smallest power of two with which the block's
+ * largest magnitude is at most 448 (not below 2^-126; 1 for a block of zeros),
+ * and each value is x / scale rounded to the nearest e4m3, ties to even.  The
+ * products take any scale bytes.  Rows must start at 16-byte boundaries (Cp
+ * does the rest): q 16-byte aligned, scale 4-byte aligned, else
+ * MOE_ERR_INVALID_ARG.
+ *
+ * No call here needs memory of its own beyond the handle's workspace, and all
+ * but moex_gate leave that workspace alone (the status word aside); every call
+ * can be captured into a HIP graph.
+ */
+#ifndef MOE_EXPERTS_H
+#define MOE_EXPERTS_H
+
+#include "moe_plan.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define MOEX_SOFTMAX 0
+#define MOEX_SIGMOID 1
+
+/*
+ * A router.
+ *   score       MOEX_SOFTMAX: score[e] = softmax over the E logits, or
+ *               MOEX_SIGMOID: score[e] = 1 / (1 + exp(-logit))
+ *   n_group     groups of E / n_group consecutive experts (n_group divides E;
+ *               1: no groups);  n_group <= 64
+ *   topk_group  groups a token may choose from (1 <= topk_group <= n_group and
+ *               topk_group * E / n_group >= k)
+ *   group_top   1 or 2: a group's value is the sum of its group_top largest
+ *               choice values (at most E / n_group)
+ *   renorm      non-zero: weights are divided by their sum + 1e-20
+ *   scale       factor of the weights
+ */
+typedef struct {
+  int32_t score, n_group, topk_group, group_top, renorm;
+  float scale;
+} moex_gate_config;
+
+/*
+ * Routing of T tokens: choice[e] = score[e] + bias[e] (bias float [E], device,
+ * nullable: none).  With groups, the topk_group groups of the largest values
+ * stay (ties to the lower group) and every other expert ranks as -infinity.
+ * The k experts of the largest choice, in that order, ties to the lower
+ * expert; without a bias the order is that of the logits.  Choices and group
+ * values are compared as in 64 bits.  Writes out as moe_plan_route does
+ * (topk_idx, expert_count and omega required; topk_val the selected logits)
+ * and
+ *   weight  float [T][k]: scale * score[e_j], or with renorm
+ *           scale * score[e_j] / (sum of the token's k scores + 1e-20).
+ * A logit of -infinity has score 0, also where all of a token's are; a bias of
+ * -infinity keeps an expert from being chosen while others are left.  A NaN
+ * logit, a logit of +infinity under softmax, or a bias that is NaN or
+ * +infinity sets MOE_STATUS_NAN_LOGIT; the weights are then unspecified and
+ * the indices still k distinct experts.  prev_topk and out->trans as in
+ * moe_plan_route.  MOE_ERR_UNSUPPORTED for n_group > 64.
+ */
+int moex_gate(moe_plan_t h, const moex_gate_config* gate, const float* logits, const float* bias,
+              const int32_t* prev_topk, const moe_route_out* out, float* weight, void* stream);
+
+/*
+ * Gradient of moex_gate's weights for the logits, through the scores of the
+ * selected experts (the selection itself has none, nor has the bias):
+ *   ds_j = scale * g_j, or with renorm, S = sum s_j + 1e-20,
+ *          scale / S * (g_j - (sum_i g_i s_i) / S)
+ *   sigmoid: grad[e_j] = ds_j s_j (1 - s_j), 0 elsewhere
+ *   softmax: grad[e] = s_e (ds_e - sum_j s_j ds_j), ds_e = 0 where not selected
+ * logits float [T][E]; topk_idx int32 [T][k]; grad_weight float [T][k];
+ * grad_logits float [T][E], fully overwritten.  An index outside [0, E) or
+ * repeated within a token sets MOE_STATUS_BAD_TOPK (that token's gradient is
+ * then unspecified), logits as in moex_gate MOE_STATUS_NAN_LOGIT.
+ */
+int moex_gate_grad(moe_plan_t h, const moex_gate_config* gate, const float* logits, const int32_t* topk_idx,
+                   const float* grad_weight, float* grad_logits, void* stream);
+
+/* x bf16 [rows][cols] to blocks of 1 x 128.  0 <= rows < 2^31, cols >= 1. */
+int moex_quantize(moe_plan_t h, const uint16_t* x, int64_t rows, int32_t cols, uint8_t* q, uint8_t* scale,
+                  void* stream);
+
+/*
+ * w bf16 [experts][n][k] to blocks of 128 x 128: q [experts][n][kp] and scale
+ * [experts][ceil(n/128)][.], and (both or neither) the transposed matrices qt
+ * [experts][k][np] with scale_t [experts][ceil(k/128)][.] -- the same values
+ * and scales, in the layout that moex_matmul needs for the input gradient.
+ */
+int moex_quantize_weights(moe_plan_t h, const uint16_t* w, int32_t experts, int32_t n, int32_t k, uint8_t* q,
+                          uint8_t* scale, uint8_t* qt, uint8_t* scale_t, void* stream);
+
+/*
+ * y bf16 [rows][2 f]: gate columns, then up columns.  a = y_gate * sigmoid(y_gate)
+ * * y_up in fp32, quantized as a row of f columns.
+ */
+int moex_swiglu(moe_plan_t h, const uint16_t* y, int64_t rows, int32_t f, uint8_t* q, uint8_t* scale, void* stream);
+
+/*
+ * Its gradient for y from grad bf16 [rows][f]: with s = sigmoid(y_gate),
+ *   d gate = grad * y_up * s * (1 + y_gate (1 - s)),  d up = grad * y_gate * s
+ * in fp32, quantized as a row of 2 f columns (d gate, then d up).
+ */
+int moex_swiglu_grad(moe_plan_t h, const uint16_t* y, const uint16_t* grad, int64_t rows, int32_t f, uint8_t* q,
+                     uint8_t* scale, void* stream);
+
+/*
+ * The experts' products.  The T*k rows of the dispatch buffer belong to the
+ * plan's instances: rows inst_offset[i] .. inst_offset[i+1]-1 to instance i of
+ * expert inst_expert[i], 0 <= i < n_inst (plan->n_inst and plan->inst_expert of
+ * moe_plan_plan, inst_offset of moe_plan_dispatch).
+ *   y[r][c] = bf16( sum over j of x[r][j] * w[e][c][j] )
+ * x: blocks of rows [T*k][k]; w: blocks of matrices [E][n][k] of the handle's E
+ * experts; y: uint16 [T*k][n] bf16.  Sums in fp32 by the matrix instruction
+ * (which aligns the products of a step to the largest of them), rounded
+ * once.  For the input gradient, x is the quantized output gradient [T*k][n]
+ * and w the transposed matrices.  An n_inst outside [0, E+B], offsets that
+ * fall or leave [0, T*k], or an expert outside [0, E) set
+ * MOE_STATUS_PLAN_CHECK; rows of such an instance, and rows of no instance,
+ * are left as they were (with a bad offset, rows of other instances may be
+ * too).  n, k >= 1.
+ */
+int moex_matmul(moe_plan_t h, const moe_plan_out* plan, const int32_t* inst_offset, const uint8_t* x,
+                const uint8_t* x_scale, const uint8_t* w, const uint8_t* w_scale, int32_t n, int32_t k, uint16_t* y,
+                void* stream);
+
+/*
+ * Gradient of the experts' matrices:
+ *   dw[e][c][j] = bf16( sum over the rows r of e's instances of dy[r][c] * x[r][j] )
+ * dy: blocks of rows [T*k][n]; x: blocks of rows [T*k][k] (what the product
+ * took); dw: uint16 [E][n][k] bf16, fully overwritten (zeros for an expert
+ * without rows).  Each value is taken as bf16(e4m3 * scale), which is exact
+ * down to bf16's subnormals, and summed in fp32.  Instances as in moex_matmul;
+ * a bad instance's rows are left out.
+ */
+int moex_wgrad(moe_plan_t h, const moe_plan_out* plan, const int32_t* inst_offset, const uint8_t* dy,
+               const uint8_t* dy_scale, const uint8_t* x, const uint8_t* x_scale, int32_t n, int32_t k, uint16_t* dw,
+               void* stream);
+
+/*
+ * The return path with given weights, as moe_plan_combine with w[t][j] =
+ * weight[t][j] (float [T][k], device; NULL: all 1, the gradient of the
+ * dispatch for its hidden rows).  A position outside [0, T*k) sets
+ * MOE_STATUS_PLAN_CHECK and the slot is skipped.
+ */
+int moex_combine(moe_plan_t h, const float* weight, const int32_t* slot_pos, const uint16_t* expert_out,
+                 uint16_t* out, void* stream);
+
+/*
+ * Gradients of moex_combine from grad_out bf16 [T][H]:
+ *   grad_expert_out[slot_pos[t*k+j]][:] = bf16( weight[t][j] * grad_out[t][:] )
+ *   grad_weight[t][j] = sum of grad_out[t][:] * expert_out[slot_pos[t*k+j]][:]  (fp32)
+ * grad_expert_out uint16 [T*k][H] (every row that a slot points to is
+ * written; it may not overlap expert_out); grad_weight float [T][k].  A
+ * position outside [0, T*k) sets MOE_STATUS_PLAN_CHECK; its weight gradient is 0.
+ */
+int moex_combine_grad(moe_plan_t h, const float* weight, const int32_t* slot_pos, const uint16_t* expert_out,
+                      const uint16_t* grad_out, uint16_t* grad_expert_out, float* grad_weight, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* MOE_EXPERTS_H */

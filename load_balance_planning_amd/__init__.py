@@ -1,7 +1,8 @@
 """MI355X-native expert-parallel dispatch planning for MoE layers.
 
-A thin ctypes binding of the C ABI in include/moe_plan.h (library
-load_balance_planning_amd/libmoe_plan.so, HIP kernels for gfx950).  The
+A thin ctypes binding of the C ABI in include/moe_plan.h and
+include/moe_experts.h (library load_balance_planning_amd/libmoe_plan.so, HIP
+kernels for gfx950).  The
 functions named like the C entry points only marshal arguments; every step of
 the path runs in the library's kernels.  `Layer` is a convenience wrapper that
 allocates the caller-owned buffers as torch tensors on the current HIP device
@@ -90,12 +91,24 @@ class moe_dedup_out(ctypes.Structure):
         "ddispatch")]
 
 
+class moex_gate_config(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+MOEX_SOFTMAX = 0
+MOEX_SIGMOID = 1
+BLOCK = 128  # columns (and, for matrices, rows) under one scale
+
 EXPORTS = ("moe_plan_query", "moe_plan_create", "moe_plan_route", "moe_plan_hist", "moe_plan_plan",
            "moe_plan_dispatch", "moe_plan_step", "moe_plan_step_static", "moe_plan_combine", "moe_plan_place", "moe_plan_dedup_count",
            "moe_plan_dedup_dispatch", "moe_plan_quality", "moe_plan_predict", "moe_plan_slot_map",
            "moe_plan_replica_pull", "moe_plan_replica_push", "moe_plan_set_events", "moe_plan_set_gather_order",
            "moe_plan_device_info",
            "moe_plan_status", "moe_plan_destroy")
+# include/moe_experts.h
+EXPERT_EXPORTS = ("moex_gate", "moex_gate_grad", "moex_quantize", "moex_quantize_weights", "moex_swiglu",
+                  "moex_swiglu_grad", "moex_matmul", "moex_wgrad", "moex_combine", "moex_combine_grad")
 
 _LIB = None
 
@@ -136,7 +149,18 @@ def lib():
         l.moe_plan_status.argtypes = [vp, vp]
         l.moe_plan_destroy.argtypes = [vp]
         l.moe_plan_destroy.restype = None
-        for n in EXPORTS[:-1]:
+        i32, i64 = ctypes.c_int32, ctypes.c_int64
+        l.moex_gate.argtypes = [vp] * 8
+        l.moex_gate_grad.argtypes = [vp] * 7
+        l.moex_quantize.argtypes = [vp, vp, i64, i32, vp, vp, vp]
+        l.moex_quantize_weights.argtypes = [vp, vp, i32, i32, i32, vp, vp, vp, vp, vp]
+        l.moex_swiglu.argtypes = [vp, vp, i64, i32, vp, vp, vp]
+        l.moex_swiglu_grad.argtypes = [vp, vp, vp, i64, i32, vp, vp, vp]
+        l.moex_matmul.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, vp, vp]
+        l.moex_wgrad.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, vp, vp]
+        l.moex_combine.argtypes = [vp] * 6
+        l.moex_combine_grad.argtypes = [vp] * 8
+        for n in EXPORTS[:-1] + EXPERT_EXPORTS:
             getattr(l, n).restype = ctypes.c_int
         _LIB = l
     return _LIB
@@ -231,6 +255,56 @@ def moe_plan_replica_push(h, slot_expert: int, replica_grads: int, param_elems: 
            lib().moe_plan_replica_push(h, slot_expert, replica_grads, param_elems, grad_accum, stream))
 
 
+def moex_gate(h, gate: moex_gate_config, logits: int, bias, prev_topk, out: moe_route_out, weight: int, stream: int):
+    _check("moex_gate", lib().moex_gate(h, ctypes.byref(gate), logits, bias, prev_topk, ctypes.byref(out), weight,
+                                        stream))
+
+
+def moex_gate_grad(h, gate: moex_gate_config, logits: int, topk_idx: int, grad_weight: int, grad_logits: int,
+                   stream: int):
+    _check("moex_gate_grad", lib().moex_gate_grad(h, ctypes.byref(gate), logits, topk_idx, grad_weight, grad_logits,
+                                                  stream))
+
+
+def moex_quantize(h, x: int, rows: int, cols: int, q: int, scale: int, stream: int):
+    _check("moex_quantize", lib().moex_quantize(h, x, rows, cols, q, scale, stream))
+
+
+def moex_quantize_weights(h, w: int, experts: int, n: int, k: int, q: int, scale: int, qt, scale_t, stream: int):
+    _check("moex_quantize_weights",
+           lib().moex_quantize_weights(h, w, experts, n, k, q, scale, qt, scale_t, stream))
+
+
+def moex_swiglu(h, y: int, rows: int, f: int, q: int, scale: int, stream: int):
+    _check("moex_swiglu", lib().moex_swiglu(h, y, rows, f, q, scale, stream))
+
+
+def moex_swiglu_grad(h, y: int, grad: int, rows: int, f: int, q: int, scale: int, stream: int):
+    _check("moex_swiglu_grad", lib().moex_swiglu_grad(h, y, grad, rows, f, q, scale, stream))
+
+
+def moex_matmul(h, plan: moe_plan_out, inst_offset: int, x: int, x_scale: int, w: int, w_scale: int, n: int, k: int,
+                y: int, stream: int):
+    _check("moex_matmul", lib().moex_matmul(h, ctypes.byref(plan), inst_offset, x, x_scale, w, w_scale, n, k, y,
+                                            stream))
+
+
+def moex_wgrad(h, plan: moe_plan_out, inst_offset: int, dy: int, dy_scale: int, x: int, x_scale: int, n: int, k: int,
+               dw: int, stream: int):
+    _check("moex_wgrad", lib().moex_wgrad(h, ctypes.byref(plan), inst_offset, dy, dy_scale, x, x_scale, n, k, dw,
+                                          stream))
+
+
+def moex_combine(h, weight, slot_pos: int, expert_out: int, out: int, stream: int):
+    _check("moex_combine", lib().moex_combine(h, weight, slot_pos, expert_out, out, stream))
+
+
+def moex_combine_grad(h, weight: int, slot_pos: int, expert_out: int, grad_out: int, grad_expert_out: int,
+                      grad_weight: int, stream: int):
+    _check("moex_combine_grad", lib().moex_combine_grad(h, weight, slot_pos, expert_out, grad_out, grad_expert_out,
+                                                        grad_weight, stream))
+
+
 def moe_plan_set_events(h, gather_begin, gather_end):
     _check("moe_plan_set_events", lib().moe_plan_set_events(h, gather_begin, gather_end))
 
@@ -265,6 +339,15 @@ def moe_plan_destroy(h):
 def make_config(T, E, k, R, G, H, B, slots_per_rank=0, expert_bytes=-1, token_bytes=0,
                 max_refine_iters=0) -> moe_plan_config:
     return moe_plan_config(T, E, k, R, G, H, B, slots_per_rank, expert_bytes, token_bytes, max_refine_iters)
+
+
+def make_gate(score: str = "softmax", n_group: int = 1, topk_group: int = 1, group_top: int = 1, renorm: bool = True,
+              scale: float = 1.0) -> moex_gate_config:
+    """A router for Layer.gate: score "softmax" or "sigmoid", expert groups, weights renormalised and scaled."""
+    kinds = {"softmax": MOEX_SOFTMAX, "sigmoid": MOEX_SIGMOID}
+    if score not in kinds:
+        raise ValueError("score must be one of %s" % sorted(kinds))
+    return moex_gate_config(kinds[score], n_group, topk_group, group_top, int(bool(renorm)), scale)
 
 
 def _ptr(t):
@@ -336,6 +419,23 @@ class DedupBuffers:
 
     def struct(self) -> moe_dedup_out:
         return moe_dedup_out(*(_ptr(getattr(self, n)) for n, _ in moe_dedup_out._fields_))
+
+
+@dataclass
+class Blocks:
+    """Quantized rows or matrices (include/moe_experts.h): q float8_e4m3fn [..., cols padded to 128], scale
+    float8_e8m0fnu [..., blocks padded to 4] -- of rows one scale per 1 x 128, of matrices per 128 x 128."""
+    q: object
+    scale: object
+    cols: int
+
+    @staticmethod
+    def padded(cols: int) -> int:
+        return -(-cols // BLOCK) * BLOCK
+
+    @staticmethod
+    def scales(cols: int) -> int:
+        return -(-(-(-cols // BLOCK)) // 4) * 4
 
 
 class Layer:
@@ -434,6 +534,167 @@ class Layer:
         moe_plan_combine(self.handle, _ptr(self.route_out.topk_val), _ptr(self.dispatch_out.slot_pos),
                          _ptr(expert_out), _ptr(out), self._stream(stream))
         return out
+
+    def gate(self, logits, gate: moex_gate_config, bias=None, prev_topk=None, stream=None):
+        """Routing with scores, bias, groups and weights (moex_gate): (route_out, weight [T][k])."""
+        torch, T, E, k = self.torch, self.cfg.T, self.cfg.E, self.cfg.k
+        self._check_tensor(logits, (T, E), torch.float32)
+        if bias is not None:
+            self._check_tensor(bias, (E,), torch.float32)
+        if prev_topk is not None:
+            self._check_tensor(prev_topk, (T, k), torch.int32)
+        weight = torch.empty((T, k), dtype=torch.float32, device=self.device)
+        moex_gate(self.handle, gate, _ptr(logits), _ptr(bias), _ptr(prev_topk), self._route_s, _ptr(weight),
+                  self._stream(stream))
+        return self.route_out, weight
+
+    def gate_grad(self, logits, gate: moex_gate_config, grad_weight, topk_idx=None, out=None, stream=None):
+        """Gradient of gate()'s weights for the logits (moex_gate_grad); topk_idx defaults to this layer's."""
+        torch, T, E, k = self.torch, self.cfg.T, self.cfg.E, self.cfg.k
+        topk_idx = self.route_out.topk_idx if topk_idx is None else topk_idx
+        out = torch.empty((T, E), dtype=torch.float32, device=self.device) if out is None else out
+        self._check_tensor(logits, (T, E), torch.float32)
+        self._check_tensor(topk_idx, (T, k), torch.int32)
+        self._check_tensor(grad_weight, (T, k), torch.float32)
+        self._check_tensor(out, (T, E), torch.float32)
+        moex_gate_grad(self.handle, gate, _ptr(logits), _ptr(topk_idx), _ptr(grad_weight), _ptr(out),
+                       self._stream(stream))
+        return out
+
+    def _empty_blocks(self, lead, cols, scale_lead=None) -> Blocks:
+        torch, scale_lead = self.torch, lead if scale_lead is None else scale_lead
+        return Blocks(torch.empty((*lead, Blocks.padded(cols)), dtype=torch.float8_e4m3fn, device=self.device),
+                      torch.empty((*scale_lead, Blocks.scales(cols)), dtype=torch.float8_e8m0fnu, device=self.device),
+                      cols)
+
+    def _check_16bit(self, t, shape, name):
+        self._check_tensor(t, shape, None)
+        if t.element_size() != 2:
+            raise TypeError("%s must be a 16-bit (bf16) tensor" % name)
+
+    def _check_blocks(self, b: Blocks, lead, scale_lead=None):
+        torch = self.torch
+        self._check_tensor(b.q, (*lead, Blocks.padded(b.cols)), torch.float8_e4m3fn)
+        self._check_tensor(b.scale, (*(lead if scale_lead is None else scale_lead), Blocks.scales(b.cols)),
+                           torch.float8_e8m0fnu)
+
+    def quantize(self, x, stream=None) -> Blocks:
+        """bf16 rows [n][cols] to Blocks of rows (moex_quantize)."""
+        if x.dim() != 2:
+            raise ValueError("x must be [rows][cols]")
+        rows, cols = x.shape
+        self._check_16bit(x, (rows, cols), "x")
+        out = self._empty_blocks((rows,), cols)
+        moex_quantize(self.handle, _ptr(x), rows, cols, _ptr(out.q), _ptr(out.scale), self._stream(stream))
+        return out
+
+    def quantize_weights(self, w, transposed: bool = False, stream=None):
+        """bf16 matrices [E][n][k] to Blocks of matrices (moex_quantize_weights); with transposed also those of the
+        transposed matrices [E][k][n], from the same pass."""
+        if w.dim() != 3:
+            raise ValueError("w must be [experts][n][k]")
+        E, n, k = w.shape
+        self._check_16bit(w, (E, n, k), "w")
+        blocks = lambda c: -(-c // BLOCK)
+        out = self._empty_blocks((E, n), k, (E, blocks(n)))
+        out_t = self._empty_blocks((E, k), n, (E, blocks(k))) if transposed else Blocks(None, None, n)
+        moex_quantize_weights(self.handle, _ptr(w), E, n, k, _ptr(out.q), _ptr(out.scale), _ptr(out_t.q),
+                              _ptr(out_t.scale), self._stream(stream))
+        return (out, out_t) if transposed else out
+
+    def swiglu(self, y, stream=None) -> Blocks:
+        """silu(gate) * up of rows [n][2 f] (gate columns, then up), quantized (moex_swiglu)."""
+        if y.dim() != 2 or y.shape[1] % 2:
+            raise ValueError("y must be [rows][2 f]")
+        rows, f = y.shape[0], y.shape[1] // 2
+        self._check_16bit(y, (rows, 2 * f), "y")
+        out = self._empty_blocks((rows,), f)
+        moex_swiglu(self.handle, _ptr(y), rows, f, _ptr(out.q), _ptr(out.scale), self._stream(stream))
+        return out
+
+    def swiglu_grad(self, y, grad, stream=None) -> Blocks:
+        """Gradient of swiglu for y from grad [n][f], quantized (moex_swiglu_grad)."""
+        if y.dim() != 2 or y.shape[1] % 2:
+            raise ValueError("y must be [rows][2 f]")
+        rows, f = y.shape[0], y.shape[1] // 2
+        self._check_16bit(y, (rows, 2 * f), "y")
+        self._check_16bit(grad, (rows, f), "grad")
+        out = self._empty_blocks((rows,), 2 * f)
+        moex_swiglu_grad(self.handle, _ptr(y), _ptr(grad), rows, f, _ptr(out.q), _ptr(out.scale),
+                         self._stream(stream))
+        return out
+
+    def _product_plan(self, plan, inst_offset):
+        """The struct of the instances a product runs over; by default this layer's plan and dispatch offsets."""
+        inst_offset = self.dispatch_out.inst_offset if inst_offset is None else inst_offset
+        cap = int(self.sizes.inst_cap)
+        self._check_tensor(inst_offset, (cap + 1,), self.torch.int32)
+        if plan is None:
+            return self._plan_s, inst_offset
+        self._check_tensor(plan.n_inst, (1,), self.torch.int32)
+        self._check_tensor(plan.inst_expert, (cap,), self.torch.int32)
+        return plan.struct(), inst_offset
+
+    def matmul(self, x: Blocks, w: Blocks, plan=None, inst_offset=None, out=None, stream=None):
+        """Rows in dispatch order times their experts' matrices (moex_matmul): bf16 [T*k][n] of x, Blocks of rows
+        [T*k][k], and w, Blocks of matrices [E][n][k]."""
+        torch, rows = self.torch, self.cfg.T * self.cfg.k
+        plan_s, inst_offset = self._product_plan(plan, inst_offset)
+        n, k = w.q.shape[1], w.cols
+        if x.cols != k:
+            raise ValueError("x has %d columns, the matrices %d" % (x.cols, k))
+        self._check_blocks(x, (rows,))
+        self._check_blocks(w, (self.cfg.E, n), (self.cfg.E, -(-n // BLOCK)))
+        out = torch.empty((rows, n), dtype=torch.bfloat16, device=self.device) if out is None else out
+        self._check_16bit(out, (rows, n), "out")
+        moex_matmul(self.handle, plan_s, _ptr(inst_offset), _ptr(x.q), _ptr(x.scale), _ptr(w.q), _ptr(w.scale), n, k,
+                    _ptr(out), self._stream(stream))
+        return out
+
+    def wgrad(self, dy: Blocks, x: Blocks, plan=None, inst_offset=None, out=None, stream=None):
+        """Gradient of the experts' matrices (moex_wgrad): bf16 [E][n][k] of dy, Blocks of rows [T*k][n], and x,
+        Blocks of rows [T*k][k]."""
+        torch, rows, E = self.torch, self.cfg.T * self.cfg.k, self.cfg.E
+        plan_s, inst_offset = self._product_plan(plan, inst_offset)
+        self._check_blocks(dy, (rows,))
+        self._check_blocks(x, (rows,))
+        out = torch.empty((E, dy.cols, x.cols), dtype=torch.bfloat16, device=self.device) if out is None else out
+        self._check_16bit(out, (E, dy.cols, x.cols), "out")
+        moex_wgrad(self.handle, plan_s, _ptr(inst_offset), _ptr(dy.q), _ptr(dy.scale), _ptr(x.q), _ptr(x.scale),
+                   dy.cols, x.cols, _ptr(out), self._stream(stream))
+        return out
+
+    def _slot_positions(self, slot_pos):
+        slot_pos = self.dispatch_out.slot_pos if slot_pos is None else slot_pos
+        self._check_tensor(slot_pos, (self.cfg.T * self.cfg.k,), self.torch.int32)
+        return slot_pos
+
+    def combine_weighted(self, expert_out, weight=None, slot_pos=None, out=None, stream=None):
+        """Sum of each token's expert rows by the given weights [T][k] (moex_combine); without weights their plain
+        sum, the gradient of the dispatch for its hidden rows."""
+        torch, T, k, H = self.torch, self.cfg.T, self.cfg.k, self.cfg.H
+        slot_pos = self._slot_positions(slot_pos)
+        self._check_16bit(expert_out, (T * k, H), "expert_out")
+        if weight is not None:
+            self._check_tensor(weight, (T, k), torch.float32)
+        out = torch.empty((T, H), dtype=expert_out.dtype, device=self.device) if out is None else out
+        self._check_16bit(out, (T, H), "out")
+        moex_combine(self.handle, _ptr(weight), _ptr(slot_pos), _ptr(expert_out), _ptr(out), self._stream(stream))
+        return out
+
+    def combine_grad(self, expert_out, grad_out, weight, slot_pos=None, stream=None):
+        """Gradients of combine_weighted for the expert rows and the weights (moex_combine_grad):
+        (grad_expert_out [T*k][H], grad_weight [T][k])."""
+        torch, T, k, H = self.torch, self.cfg.T, self.cfg.k, self.cfg.H
+        slot_pos = self._slot_positions(slot_pos)
+        self._check_16bit(expert_out, (T * k, H), "expert_out")
+        self._check_16bit(grad_out, (T, H), "grad_out")
+        self._check_tensor(weight, (T, k), torch.float32)
+        grad_rows = torch.empty_like(expert_out)
+        grad_weight = torch.empty((T, k), dtype=torch.float32, device=self.device)
+        moex_combine_grad(self.handle, _ptr(weight), _ptr(slot_pos), _ptr(expert_out), _ptr(grad_out),
+                          _ptr(grad_rows), _ptr(grad_weight), self._stream(stream))
+        return grad_rows, grad_weight
 
     def place(self, cooc=None, max_swaps: int = -1, stream=None):
         """Correlated expert placement from co-selection counts (moe_plan_place);

@@ -14,7 +14,15 @@
 // gather.  The expert rows are read once, with non-temporal loads (measured
 // on MI355X: DeepSeek-V3-shaped layer 798 -> 777 us, Kimi-K2-shaped 757 ->
 // 712 us).
-#include "internal.h"
+//
+// The same sum with given weights (moex_combine; no weights: all 1, the
+// gradient of the dispatch) and its gradient:
+//   grad_expert_out[slot_pos[t*k+j]][:] = bf16( w[t][j] * g[t][:] )
+//   grad_weight[t][j] = sum over c of g[t][c] * expert_out[slot_pos[t*k+j]][c]
+// One workgroup per token again: g's row stays in registers while the k rows
+// stream through, each row read once and its gradient's row written once.
+#include "experts.h"
+#include "fp8_block.h"
 
 namespace moe {
 namespace {
@@ -45,26 +53,35 @@ __device__ __forceinline__ void fma_row(float* acc, float w, const uint4& v) {
   acc[7] = fmaf(w, bf16_hi(v.w), acc[7]);
 }
 
-// Weights and row positions of token t into LDS (first wave).  A non-finite
-// selected logit or a position outside the dispatch buffer is recorded in the
-// status word; such a position is stored as -1 and its slot skipped.
+// Weights and row positions of token t into LDS (first wave).  GIVEN: topk_val
+// holds the weights themselves (null: all 1); otherwise the selected logits,
+// whose softmax they are.  A non-finite selected logit or a position outside
+// the dispatch buffer is recorded in the status word; such a position is
+// stored as -1 and its slot skipped.
+template <bool GIVEN>
 __device__ __forceinline__ void gate_weights(const Dims& d, int64_t t, const float* __restrict__ topk_val,
                                              const int32_t* __restrict__ slot_pos, float* w_s, int32_t* p_s,
                                              int32_t* status) {
   const int lane = threadIdx.x;
   if (lane < 64) {
     const bool on = lane < d.k;
-    const float v = on ? topk_val[t * d.k + lane] : -INFINITY;
-    if (on && !__builtin_isfinite(v)) atomicOr(status, MOE_STATUS_NAN_LOGIT);
-    float m = v;
+    float w;
+    if (GIVEN) {
+      w = on && topk_val ? topk_val[t * d.k + lane] : 1.0f;
+    } else {
+      const float v = on ? topk_val[t * d.k + lane] : -INFINITY;
+      if (on && !__builtin_isfinite(v)) atomicOr(status, MOE_STATUS_NAN_LOGIT);
+      float m = v;
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
-    const float e = on ? expf(v - m) : 0.0f;
-    float s = e;
+      for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+      const float e = on ? expf(v - m) : 0.0f;
+      float s = e;
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off);
+      for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off);
+      w = e / s;
+    }
     if (on) {
-      w_s[lane] = e / s;
+      w_s[lane] = w;
       int32_t p = slot_pos[t * d.k + lane];
       const int64_t N = (int64_t)d.T * d.k;
       if (p < 0 || p >= N) {
@@ -77,7 +94,7 @@ __device__ __forceinline__ void gate_weights(const Dims& d, int64_t t, const flo
   __syncthreads();
 }
 
-template <int VPT>
+template <int VPT, bool GIVEN>
 __global__ __launch_bounds__(kCombThreads) void combine_vec_kernel(Dims d, const float* __restrict__ topk_val,
                                                                    const int32_t* __restrict__ slot_pos,
                                                                    const uint4* __restrict__ expert_out,
@@ -85,7 +102,7 @@ __global__ __launch_bounds__(kCombThreads) void combine_vec_kernel(Dims d, const
   __shared__ float w_s[kMaxK];
   __shared__ int32_t p_s[kMaxK];
   const int64_t t = blockIdx.x;
-  gate_weights(d, t, topk_val, slot_pos, w_s, p_s, status);
+  gate_weights<GIVEN>(d, t, topk_val, slot_pos, w_s, p_s, status);
   const int vpr = d.H / 8;
   for (int base = 0; base < vpr; base += kCombThreads * VPT) {
     float acc[VPT][8];
@@ -138,6 +155,7 @@ __global__ __launch_bounds__(kCombThreads) void combine_vec_kernel(Dims d, const
 }
 
 // Any H: one bf16 element per thread and step.
+template <bool GIVEN>
 __global__ __launch_bounds__(kCombThreads) void combine_u16_kernel(Dims d, const float* __restrict__ topk_val,
                                                                    const int32_t* __restrict__ slot_pos,
                                                                    const uint16_t* __restrict__ expert_out,
@@ -146,7 +164,7 @@ __global__ __launch_bounds__(kCombThreads) void combine_u16_kernel(Dims d, const
   __shared__ float w_s[kMaxK];
   __shared__ int32_t p_s[kMaxK];
   const int64_t t = blockIdx.x;
-  gate_weights(d, t, topk_val, slot_pos, w_s, p_s, status);
+  gate_weights<GIVEN>(d, t, topk_val, slot_pos, w_s, p_s, status);
   for (int c = threadIdx.x; c < d.H; c += kCombThreads) {
     float acc = 0.0f;
     for (int j = 0; j < d.k; ++j) {
@@ -157,24 +175,165 @@ __global__ __launch_bounds__(kCombThreads) void combine_u16_kernel(Dims d, const
   }
 }
 
-}  // namespace
+// Sum over the wave, in every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
+  return v;
+}
 
-hipError_t launch_combine(const Dims& d, const float* topk_val, const int32_t* slot_pos, const uint16_t* expert_out,
-                          uint16_t* out, int32_t* status, hipStream_t st) {
+// dot += 8 products of bf16 values, each an fp32 FMA.
+__device__ __forceinline__ void dot_row(float* dot, const v4u& g, const v4u& x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    *dot = fmaf(bf16_low(g[i]), bf16_low(x[i]), *dot);
+    *dot = fmaf(bf16_high(g[i]), bf16_high(x[i]), *dot);
+  }
+}
+
+// w times 8 bf16 values, rounded once.
+__device__ __forceinline__ v4u scaled_row(float w, const v4u& g) {
+  v4u y;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = pack_bf16(w * bf16_low(g[i]), w * bf16_high(g[i]));
+  return y;
+}
+
+constexpr int kGradRows = 4;  // rows in flight per round (with VPT vectors each)
+
+template <int VPT>
+__global__ __launch_bounds__(kCombThreads) void combine_grad_vec_kernel(
+    Dims d, const float* __restrict__ weight, const int32_t* __restrict__ slot_pos,
+    const uint16_t* __restrict__ expert_out, const uint16_t* __restrict__ grad_out,
+    uint16_t* __restrict__ grad_rows, float* __restrict__ grad_weight, int32_t* __restrict__ status) {
+  __shared__ float w_s[kMaxK];
+  __shared__ int32_t p_s[kMaxK];
+  __shared__ float dot_s[kCombThreads / 64][kGradRows];
+  const int64_t t = blockIdx.x;
+  gate_weights<true>(d, t, weight, slot_pos, w_s, p_s, status);
+  const int vpr = d.H / 8;
+  const v4u* __restrict__ g_row = reinterpret_cast<const v4u*>(grad_out) + t * vpr;
+  for (int j0 = 0; j0 < d.k; j0 += kGradRows) {
+    float dot[kGradRows];
+#pragma unroll
+    for (int q = 0; q < kGradRows; ++q) dot[q] = 0.0f;
+    for (int base = 0; base < vpr; base += kCombThreads * VPT) {
+      v4u g[VPT];
+#pragma unroll
+      for (int u = 0; u < VPT; ++u) {
+        const int c = base + threadIdx.x + u * kCombThreads;
+        g[u] = c < vpr ? g_row[c] : v4u{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int q = 0; q < kGradRows; ++q) {
+        const int p = j0 + q < d.k ? p_s[j0 + q] : -1;
+        if (p < 0) continue;  // the same for the whole workgroup
+        const v4u* x_row = reinterpret_cast<const v4u*>(expert_out) + (int64_t)p * vpr;
+        v4u* y_row = reinterpret_cast<v4u*>(grad_rows) + (int64_t)p * vpr;
+        const float w = w_s[j0 + q];
+        v4u x[VPT];
+#pragma unroll
+        for (int u = 0; u < VPT; ++u) {
+          const int c = base + threadIdx.x + u * kCombThreads;
+          x[u] = c < vpr ? __builtin_nontemporal_load(x_row + c) : v4u{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int u = 0; u < VPT; ++u) {
+          const int c = base + threadIdx.x + u * kCombThreads;
+          if (c < vpr) __builtin_nontemporal_store(scaled_row(w, g[u]), y_row + c);
+          dot_row(&dot[q], g[u], x[u]);
+        }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kGradRows; ++q) {
+      const float s = wave_sum(dot[q]);
+      if ((threadIdx.x & 63) == 0) dot_s[threadIdx.x >> 6][q] = s;
+    }
+    __syncthreads();
+    if (threadIdx.x < kGradRows && j0 + (int)threadIdx.x < d.k) {
+      const int q = threadIdx.x;
+      grad_weight[t * d.k + j0 + q] = dot_s[0][q] + dot_s[1][q] + dot_s[2][q] + dot_s[3][q];
+    }
+    __syncthreads();
+  }
+}
+
+// Any H: one bf16 element per thread and step.
+__global__ __launch_bounds__(kCombThreads) void combine_grad_u16_kernel(
+    Dims d, const float* __restrict__ weight, const int32_t* __restrict__ slot_pos,
+    const uint16_t* __restrict__ expert_out, const uint16_t* __restrict__ grad_out,
+    uint16_t* __restrict__ grad_rows, float* __restrict__ grad_weight, int32_t* __restrict__ status) {
+  __shared__ float w_s[kMaxK];
+  __shared__ int32_t p_s[kMaxK];
+  __shared__ float dot_s[kCombThreads / 64];
+  const int64_t t = blockIdx.x;
+  gate_weights<true>(d, t, weight, slot_pos, w_s, p_s, status);
+  for (int j = 0; j < d.k; ++j) {
+    const int p = p_s[j];
+    float dot = 0.0f;
+    if (p >= 0) {
+      for (int c = threadIdx.x; c < d.H; c += kCombThreads) {
+        const float g = bf16_low(grad_out[t * d.H + c]);
+        dot = fmaf(g, bf16_low(expert_out[(int64_t)p * d.H + c]), dot);
+        grad_rows[(int64_t)p * d.H + c] = (uint16_t)to_bf16(w_s[j] * g);
+      }
+    }
+    const float s = wave_sum(dot);
+    if ((threadIdx.x & 63) == 0) dot_s[threadIdx.x >> 6] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) grad_weight[t * d.k + j] = dot_s[0] + dot_s[1] + dot_s[2] + dot_s[3];
+    __syncthreads();
+  }
+}
+
+template <bool GIVEN>
+hipError_t launch_sum(const Dims& d, const float* topk_val, const int32_t* slot_pos, const uint16_t* expert_out,
+                      uint16_t* out, int32_t* status, hipStream_t st) {
   if (d.T == 0) return hipSuccess;
   const bool vec = (d.H % 8) == 0 && ((uintptr_t)expert_out % 16) == 0 && ((uintptr_t)out % 16) == 0;
   if (vec) {
     // a row of at most kCombThreads vectors takes one round: no dead registers
     if (d.H / 8 <= kCombThreads)
-      hipLaunchKernelGGL((combine_vec_kernel<1>), dim3(d.T), dim3(kCombThreads), 0, st, d, topk_val, slot_pos,
+      hipLaunchKernelGGL((combine_vec_kernel<1, GIVEN>), dim3(d.T), dim3(kCombThreads), 0, st, d, topk_val, slot_pos,
                          reinterpret_cast<const uint4*>(expert_out), reinterpret_cast<uint4*>(out), status);
     else
-      hipLaunchKernelGGL((combine_vec_kernel<4>), dim3(d.T), dim3(kCombThreads), 0, st, d, topk_val, slot_pos,
+      hipLaunchKernelGGL((combine_vec_kernel<4, GIVEN>), dim3(d.T), dim3(kCombThreads), 0, st, d, topk_val, slot_pos,
                          reinterpret_cast<const uint4*>(expert_out), reinterpret_cast<uint4*>(out), status);
   } else {
-    hipLaunchKernelGGL(combine_u16_kernel, dim3(d.T), dim3(kCombThreads), 0, st, d, topk_val, slot_pos, expert_out,
+    hipLaunchKernelGGL((combine_u16_kernel<GIVEN>), dim3(d.T), dim3(kCombThreads), 0, st, d, topk_val, slot_pos, expert_out,
                        out, status);
   }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_combine(const Dims& d, const float* topk_val, const int32_t* slot_pos, const uint16_t* expert_out,
+                          uint16_t* out, int32_t* status, hipStream_t st) {
+  return launch_sum<false>(d, topk_val, slot_pos, expert_out, out, status, st);
+}
+
+hipError_t launch_combine_weighted(const Dims& d, const float* weight, const int32_t* slot_pos,
+                                   const uint16_t* expert_out, uint16_t* out, int32_t* status, hipStream_t st) {
+  return launch_sum<true>(d, weight, slot_pos, expert_out, out, status, st);
+}
+
+hipError_t launch_combine_grad(const Dims& d, const float* weight, const int32_t* slot_pos,
+                               const uint16_t* expert_out, const uint16_t* grad_out, uint16_t* grad_expert_out,
+                               float* grad_weight, int32_t* status, hipStream_t st) {
+  if (d.T == 0) return hipSuccess;
+  const bool vec = (d.H % 8) == 0 && ((uintptr_t)expert_out % 16) == 0 && ((uintptr_t)grad_out % 16) == 0 &&
+                   ((uintptr_t)grad_expert_out % 16) == 0;
+  if (!vec)
+    hipLaunchKernelGGL(combine_grad_u16_kernel, dim3(d.T), dim3(kCombThreads), 0, st, d, weight, slot_pos, expert_out,
+                       grad_out, grad_expert_out, grad_weight, status);
+  else if (d.H / 8 <= kCombThreads)
+    hipLaunchKernelGGL((combine_grad_vec_kernel<1>), dim3(d.T), dim3(kCombThreads), 0, st, d, weight, slot_pos,
+                       expert_out, grad_out, grad_expert_out, grad_weight, status);
+  else
+    hipLaunchKernelGGL((combine_grad_vec_kernel<4>), dim3(d.T), dim3(kCombThreads), 0, st, d, weight, slot_pos,
+                       expert_out, grad_out, grad_expert_out, grad_weight, status);
   return hipGetLastError();
 }
 

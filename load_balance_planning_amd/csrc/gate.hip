@@ -1,0 +1,615 @@
+// Router scores, selection, weights and their gradient on gfx950.
+//
+//   score[e]  = softmax over the logits, or 1 / (1 + exp(-x[e]))
+//   choice[e] = score[e] + bias[e]
+//   groups    of consecutive experts rank by the sum of their one or two
+//             largest choices; experts outside the best ones rank as -infinity
+//   top-k     by choice (by logit where there is no bias), ties to the lower
+//             expert;  weight[j] = scale * s_j  or  scale * s_j / (sum s + 1e-20)
+//
+// P lanes hold a token, V consecutive logits each, so a row is read once into
+// registers.  The selection is route.hip's: tau, the k-th largest of the lane
+// maxima, admits about k candidates; they go to LDS and each one's rank among
+// them is its output position.
+//
+// Choices are compared as in 64 bits without computing them in 64 bits: the
+// fp32 choice of an expert is off by at most half of `margin`, so two that
+// differ by more are in the right order.  Where two candidates, or two groups
+// across the cut, lie closer (about one token in a hundred on DeepSeek-V3's
+// router), the token's lanes evaluate only those candidates, or the group
+// values, in 64 bits.  A candidate list that does not fit the lanes (long ties)
+// takes k rounds of a maximum over 64-bit choices.
+#include <math.h>
+
+#include "experts.h"
+#include "lane_group.h"
+
+namespace moe {
+namespace {
+
+constexpr float kTiny = 1e-20f;  // added to the sum of the selected scores
+
+// Tokens per workgroup: route.hip's rule (slices of at least 8 bits of a mask).
+template <int P>
+constexpr int gate_tpw() {
+  return 256 / P < 8 ? 8 : 256 / P;
+}
+
+template <int P>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+  for (int off = P / 2; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off));
+  return v;
+}
+template <int P, typename F>
+__device__ __forceinline__ F group_sum(F v) {
+#pragma unroll
+  for (int off = P / 2; off >= 1; off >>= 1) v += __shfl_xor(v, off);
+  return v;
+}
+
+// Score of a logit; m and inv are the row's maximum and 1 / sum of exp(x - m)
+// (softmax).  -infinity scores 0 in either form.
+__device__ __forceinline__ float score32(bool softmax, float x, float m, float inv) {
+  if (x == -INFINITY) return 0.0f;
+  return softmax ? expf(x - m) * inv : 1.0f / (1.0f + expf(-x));
+}
+__device__ __forceinline__ double score64(bool softmax, float x, float m, double sum) {
+  if (x == -INFINITY) return 0.0;
+  return softmax ? exp((double)x - (double)m) / sum : 1.0 / (1.0 + exp(-(double)x));
+}
+
+// LDS words of one token in gate_kernel: its candidates, and with groups its
+// choices, group values in 32 and 64 bits.
+__host__ __device__ inline int choice_stride(int E) { return E + 8; }
+
+struct GateLds {
+  size_t mask, cand, choice, group, total;
+};
+template <int P>
+__host__ __device__ inline GateLds gate_lds(int E, int n_group, bool prev) {
+  constexpr int TPW = gate_tpw<P>();
+  GateLds l;
+  l.mask = 0;
+  l.cand = sizeof(uint64_t) * (size_t)E * (prev ? 2 : 1);
+  l.choice = l.cand + (size_t)TPW * P * 24;  // 64-bit choice, choice, logit, expert (and 4 bytes over)
+  const size_t choices = n_group > 1 ? sizeof(float) * (size_t)TPW * choice_stride(E) : 0;
+  l.group = (l.choice + choices + 7) / 8 * 8;
+  l.total = l.group + (n_group > 1 ? (size_t)TPW * n_group * sizeof(double) : 0);
+  return l;
+}
+
+template <int P, int V>
+__global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
+    Dims d, moex_gate_config g, bool vec, const float* __restrict__ logits, const float* __restrict__ bias,
+    const int32_t* __restrict__ prev_topk, int32_t* __restrict__ topk_idx, float* __restrict__ topk_val,
+    float* __restrict__ weight, uint64_t* __restrict__ tile_mask, uint64_t* __restrict__ prev_mask,
+    int32_t* __restrict__ status) {
+  constexpr int TPW = gate_tpw<P>();
+  constexpr int SLICES = 64 / TPW;
+  extern __shared__ __align__(16) unsigned char smem_gate[];
+  const bool want_prev = prev_topk != nullptr;
+  const GateLds lay = gate_lds<P>(d.E, g.n_group, want_prev);
+  unsigned long long* smask = reinterpret_cast<unsigned long long*>(smem_gate);
+  unsigned long long* pmask = smask + d.E;
+  const int x_tile = blockIdx.x / SLICES, h = blockIdx.x - x_tile * SLICES;
+  const int s = x_tile / d.C, c = x_tile - s * d.C;
+  const int64_t t0 = (int64_t)s * d.Tr + (int64_t)c * kTile + h * TPW;
+  const int nt = max(0, min(TPW, d.Tr - c * kTile - h * TPW));
+  const int tid = threadIdx.x, nthr = blockDim.x;
+  for (int e = tid; e < d.E; e += nthr) {
+    smask[e] = 0ull;
+    if (want_prev) pmask[e] = 0ull;
+  }
+  __syncthreads();
+
+  const int lane = tid % P;
+  const int grp_base = (tid & 63) - lane;
+  const uint64_t grp_bits = (P == 64 ? ~0ull : ((1ull << P) - 1ull)) << grp_base;
+  const int i = tid / P;
+  // this token's candidates: [P] of each
+  double* cand64 = reinterpret_cast<double*>(smem_gate + lay.cand) + (size_t)i * P;
+  float* cand_c = reinterpret_cast<float*>(smem_gate + lay.cand + (size_t)TPW * P * 8) + (size_t)i * P;
+  float* cand_x = reinterpret_cast<float*>(smem_gate + lay.cand + (size_t)TPW * P * 12) + (size_t)i * P;
+  int* cand_e = reinterpret_cast<int*>(smem_gate + lay.cand + (size_t)TPW * P * 16) + (size_t)i * P;
+  const bool softmax = g.score == MOEX_SOFTMAX;
+  const int k = d.k;
+  bool bad = false;
+  if (i < nt) {
+    const int64_t t = t0 + i;
+    const float* __restrict__ row = logits + t * d.E;
+    const int e0 = lane * V;
+    float x[V], c32[V];
+    if (V >= 4 && vec) {
+      // E a multiple of 4: a vector is inside the row as a whole
+#pragma unroll
+      for (int w = 0; w < V / 4; ++w) {
+        const bool in = e0 + 4 * w < d.E;
+        const float4 f = in ? *reinterpret_cast<const float4*>(row + e0 + 4 * w)
+                            : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        x[4 * w + 0] = f.x;
+        x[4 * w + 1] = f.y;
+        x[4 * w + 2] = f.z;
+        x[4 * w + 3] = f.w;
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[v] = e0 + v < d.E ? row[e0 + v] : -INFINITY;
+    }
+    float xmax = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const bool wrong = x[v] != x[v] || (softmax && x[v] == INFINITY);
+      bad |= wrong;
+      x[v] = wrong ? -INFINITY : x[v];
+      xmax = fmaxf(xmax, x[v]);
+    }
+    float m = 0.0f, inv = 0.0f;
+    if (softmax) {
+      m = group_max<P>(xmax);
+      float sum = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        c32[v] = x[v] == -INFINITY ? 0.0f : expf(x[v] - m);
+        sum += c32[v];
+      }
+      sum = group_sum<P>(sum);
+      inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    }
+    const bool scored = bias != nullptr || g.n_group > 1;  // choices are needed, not the logits' order alone
+    if (scored) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float b = 0.0f;
+        if (bias && e0 + v < d.E) {
+          b = bias[e0 + v];
+          const bool wrong = b != b || b == INFINITY;
+          bad |= wrong;
+          b = wrong ? 0.0f : b;
+        }
+        c32[v] = (softmax ? c32[v] * inv : score32(false, x[v], 0.0f, 0.0f)) + b;
+      }
+    }
+    // Twice the error of an fp32 choice of magnitude up to |c|: the sum of V
+    // exponentials per lane and log2 P levels, expf, the divisions and the
+    // addition of the bias, 2^-24 each, with room.
+    const float margin = 2.0f * (V + 16) * 5.9604645e-8f;
+    double sum64 = 1.0;
+    bool have64 = !softmax;
+    // the softmax denominator in 64 bits, when a comparison needs it
+    auto need64 = [&]() {
+      if (!have64) {
+        double a = 0.0;
+        for (int v = 0; v < V; ++v) a += x[v] == -INFINITY ? 0.0 : exp((double)x[v] - (double)m);
+        sum64 = group_sum<P>(a);
+        have64 = true;
+      }
+    };
+    auto choice64 = [&](int e) {
+      float xe = row[e];
+      if (xe != xe || (softmax && xe == INFINITY)) xe = -INFINITY;
+      double b = 0.0;
+      if (bias) {
+        const float be = bias[e];
+        b = be != be || be == INFINITY ? 0.0 : (double)be;
+      }
+      return score64(softmax, xe, m, sum64) + b;
+    };
+
+    uint64_t kept = ~0ull;  // groups a token may choose from
+    const int per = d.E / g.n_group;
+    if (g.n_group > 1) {
+      float* ch = reinterpret_cast<float*>(smem_gate + lay.choice) + (size_t)i * choice_stride(d.E);
+      double* gv64 = reinterpret_cast<double*>(smem_gate + lay.group) + (size_t)i * g.n_group;
+      float* gv = reinterpret_cast<float*>(gv64);
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (e0 + v < d.E) ch[e0 + v] = c32[v];
+      wave_lds_sync();
+      for (int q = lane; q < g.n_group; q += P) {
+        float a = -INFINITY, b = -INFINITY;
+        int at = q % per;  // lanes start at different places of their groups: other LDS banks
+        for (int j = 0; j < per; ++j) {
+          const float y = ch[q * per + at];
+          b = fmaxf(b, fminf(a, y));
+          a = fmaxf(a, y);
+          at = at + 1 == per ? 0 : at + 1;
+        }
+        gv[q] = g.group_top == 2 ? a + b : a;
+      }
+      wave_lds_sync();
+      bool unsure = false;
+      uint64_t mask = 0ull;
+      for (int q0 = 0; q0 < g.n_group; q0 += P) {
+        const int q = q0 + lane;
+        bool in = false;
+        if (q < g.n_group) {
+          const float y = gv[q], room = 2.0f * margin * (1.0f + fabsf(y));
+          int ahead = 0, near = 0;
+          for (int o = 0; o < g.n_group; ++o) {
+            const float z = gv[o];
+            ahead += z > y + room ? 1 : 0;
+            near += o != q && z >= y - room ? 1 : 0;
+          }
+          in = near < g.topk_group;
+          unsure |= !in && ahead < g.topk_group;
+        }
+        mask |= ((__ballot(in) & grp_bits) >> grp_base) << q0;
+      }
+      if ((__ballot(unsure) & grp_bits) != 0ull) {
+        need64();
+        wave_lds_sync();
+        for (int q = lane; q < g.n_group; q += P) {
+          double a = -INFINITY, b = -INFINITY;
+          for (int j = 0; j < per; ++j) {
+            const double y = choice64(q * per + j);
+            b = fmax(b, fmin(a, y));
+            a = fmax(a, y);
+          }
+          gv64[q] = g.group_top == 2 ? a + b : a;
+        }
+        wave_lds_sync();
+        mask = 0ull;
+        for (int q0 = 0; q0 < g.n_group; q0 += P) {
+          const int q = q0 + lane;
+          bool in = false;
+          if (q < g.n_group) {
+            int ahead = 0;
+            for (int o = 0; o < g.n_group; ++o) ahead += gv64[o] > gv64[q] || (gv64[o] == gv64[q] && o < q) ? 1 : 0;
+            in = ahead < g.topk_group;
+          }
+          mask |= ((__ballot(in) & grp_bits) >> grp_base) << q0;
+        }
+      }
+      kept = mask;
+    }
+
+    // What the k experts are ordered by: choices, or the logits themselves
+    // (-0 as +0).  Past the row's end and outside the kept groups: -infinity.
+    float o32[V];
+    {
+      int q = e0 / per, left = (q + 1) * per - e0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const bool in = e0 + v < d.E && (g.n_group == 1 || ((kept >> (q & 63)) & 1ull) != 0ull);
+        o32[v] = in ? (bias ? c32[v] : x[v] + 0.0f) : -INFINITY;
+        if (--left == 0) {
+          ++q;
+          left = per;
+        }
+      }
+    }
+    float omax = o32[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) omax = fmaxf(omax, o32[v]);
+    const uint32_t sorted = group_sort_desc_u32<P>(order_key(__float_as_uint(omax)), lane);
+    const float kth = __uint_as_float(float_from_order_key((uint32_t)__shfl((int)sorted, grp_base + k - 1)));
+    const float tau = bias ? kth - margin * (1.0f + fabsf(kth)) : kth;
+    int mine = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) mine += e0 + v < d.E && o32[v] >= tau ? 1 : 0;
+    const int incl = group_incl_scan<P>(mine, lane);
+    const int total = group_last<P>(incl);
+    int rank = P, my_e = 0;  // this lane's expert and its place in the top-k
+    float my_x = 0.0f;
+    if (total <= P) {
+      int w = incl - mine;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (e0 + v < d.E && o32[v] >= tau) {
+          cand_c[w] = o32[v];
+          cand_x[w] = x[v];
+          cand_e[w] = e0 + v;
+          ++w;
+        }
+      }
+      wave_lds_sync();
+      const int at = lane < total ? lane : 0;
+      const float my_c = cand_c[at];
+      my_e = cand_e[at];
+      my_x = cand_x[at];
+      rank = 0;
+      bool unsure = false;
+      for (int j = 0; j < total; ++j) {
+        const float cj = cand_c[j];
+        rank += cj > my_c || (cj == my_c && j < at) ? 1 : 0;  // candidates are in expert order
+        if (bias && j != at && fabsf(cj - my_c) <= margin * (1.0f + fminf(fabsf(cj), fabsf(my_c))))
+          unsure |= cand_x[j] != my_x || bias[cand_e[j]] != bias[my_e];  // equal inputs are a tie
+      }
+      if ((__ballot(unsure) & grp_bits) != 0ull) {
+        need64();
+        double y = choice64(my_e);
+        if (my_c == -INFINITY) y = -INFINITY;  // outside the kept groups
+        cand64[lane] = y;
+        wave_lds_sync();
+        rank = 0;
+        for (int j = 0; j < total; ++j) rank += cand64[j] > y || (cand64[j] == y && j < at) ? 1 : 0;
+      }
+      if (lane >= total) rank = P;
+    } else {
+      // k rounds: each the largest choice left, ties to the lower expert
+      if (bias) need64();
+      uint32_t taken = 0u;
+      for (int j = 0; j < k; ++j) {
+        double best = -INFINITY;
+        int at = d.E;  // none
+        int q = e0 / per, left = (q + 1) * per - e0;
+        for (int v = 0; v < V; ++v) {
+          const int e = e0 + v;
+          if (e < d.E && ((taken >> v) & 1u) == 0u) {
+            double y = -INFINITY;
+            if (g.n_group == 1 || ((kept >> (q & 63)) & 1ull) != 0ull) {
+              if (bias) {
+                y = choice64(e);
+              } else {
+                const float xe = row[e];
+                y = xe != xe || (softmax && xe == INFINITY) ? -INFINITY : (double)xe;
+              }
+            }
+            if (y > best || at == d.E) {
+              best = y;
+              at = e;
+            }
+          }
+          if (--left == 0) {
+            ++q;
+            left = per;
+          }
+        }
+#pragma unroll
+        for (int off = P / 2; off >= 1; off >>= 1) {
+          const double ob = __shfl_xor(best, off);
+          const int oa = __shfl_xor(at, off);
+          if (oa < d.E && (at == d.E || ob > best || (ob == best && oa < at))) {
+            best = ob;
+            at = oa;
+          }
+        }
+        if (at >= e0 && at < e0 + V) taken |= 1u << (at - e0);
+        if (lane == j) {
+          rank = j;
+          my_e = at;
+        }
+      }
+      if (rank < k) {
+        my_x = row[my_e];
+        if (my_x != my_x || (softmax && my_x == INFINITY)) my_x = -INFINITY;
+      }
+    }
+    const bool chosen = rank < k;
+    const float sc = chosen ? score32(softmax, my_x, m, inv) : 0.0f;
+    float factor = g.scale;
+    if (g.renorm) factor = g.scale / (group_sum<P>(sc) + kTiny);
+    if (chosen) {
+      topk_idx[t * k + rank] = my_e;
+      if (topk_val) topk_val[t * k + rank] = row[my_e];
+      weight[t * k + rank] = sc * factor;
+      atomicOr(&smask[my_e], 1ull << i);
+    }
+  }
+  if (want_prev) {
+    for (int q = tid; q < nt * k; q += nthr) {
+      const int ip = q / k;
+      const int e = prev_topk[(t0 + ip) * k + (q - ip * k)];
+      if ((unsigned)e < (unsigned)d.E) {
+        const unsigned long long old = atomicOr(&pmask[e], 1ull << ip);
+        if (old & (1ull << ip)) atomicOr(status, MOE_STATUS_BAD_TOPK);
+      } else {
+        atomicOr(status, MOE_STATUS_BAD_TOPK);
+      }
+    }
+  }
+  if (bad) atomicOr(status, MOE_STATUS_NAN_LOGIT);
+  __syncthreads();
+  // This workgroup's TPW-bit slice of every mask word of the tile.
+  auto store = [&](uint64_t* word, unsigned long long mk) {
+    if (TPW == 32) reinterpret_cast<uint32_t*>(word)[h] = (uint32_t)mk;
+    else if (TPW == 16) reinterpret_cast<uint16_t*>(word)[h] = (uint16_t)mk;
+    else reinterpret_cast<uint8_t*>(word)[h] = (uint8_t)mk;
+  };
+  for (int e = tid; e < d.E; e += nthr) {
+    store(tile_mask + (int64_t)x_tile * d.E + e, smask[e]);
+    if (want_prev) store(prev_mask + (int64_t)x_tile * d.E + e, pmask[e]);
+  }
+}
+
+template <int P, int V>
+hipError_t launch_gate_pv(const Dims& d, const moex_gate_config& g, bool vec, const float* logits, const float* bias,
+                          const int32_t* prev_topk, int32_t* topk_idx, float* topk_val, float* weight,
+                          uint64_t* tile_mask, uint64_t* prev_mask, int32_t* status, hipStream_t st) {
+  constexpr int slices = 64 / gate_tpw<P>();
+  const size_t lds = gate_lds<P>(d.E, g.n_group, prev_topk != nullptr).total;
+  if (lds > 65536) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(gate_kernel<P, V>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((gate_kernel<P, V>), dim3((unsigned)(d.NT * slices)), dim3(gate_tpw<P>() * P), lds, st, d, g, vec,
+                     logits, bias, prev_topk, topk_idx, topk_val, weight, tile_mask, prev_mask, status);
+  return hipGetLastError();
+}
+
+// ---- gradient ----------------------------------------------------------------
+
+// P lanes (a power of two, at least k) hold a token's row, NV 16-byte vectors
+// (or 4 NV single logits) each.  The k scores and their gradients sit one to a
+// lane; the sums over them are butterflies, and the row is written once, the
+// selected experts' terms read from a row of LDS.
+template <int NV, bool VEC>
+__global__ __launch_bounds__(256) void gate_grad_kernel(Dims d, moex_gate_config g, int P,
+                                                        const float* __restrict__ logits,
+                                                        const int32_t* __restrict__ topk_idx,
+                                                        const float* __restrict__ grad_weight,
+                                                        float* __restrict__ grad_logits, int32_t* __restrict__ status) {
+  extern __shared__ __align__(16) float smem_grad[];
+  const int lane = threadIdx.x & (P - 1), i = threadIdx.x / P;
+  const int64_t t = (int64_t)blockIdx.x * (256 / P) + i;
+  if (t >= d.T) return;  // whole lane groups; no barrier below
+  const int row_words = (d.E + 3) / 4 * 4;
+  float* ds_row = smem_grad + (size_t)i * row_words;
+  const bool softmax = g.score == MOEX_SOFTMAX;
+  const float* __restrict__ row = logits + t * d.E;
+  auto gmax = [&](float v) {
+    for (int off = P / 2; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off));
+    return v;
+  };
+  auto gsum = [&](float v) {
+    for (int off = P / 2; off >= 1; off >>= 1) v += __shfl_xor(v, off);
+    return v;
+  };
+  auto expert = [&](int w, int q) { return VEC ? 4 * (lane + P * w) + q : lane + P * (4 * w + q); };
+  float x[4 * NV];
+  bool bad = false;
+#pragma unroll
+  for (int w = 0; w < NV; ++w) {
+    if (VEC) {
+      if (expert(w, 0) < d.E) *reinterpret_cast<float4*>(ds_row + expert(w, 0)) = make_float4(0, 0, 0, 0);
+      if (softmax) {
+        const float4 f = expert(w, 0) < d.E ? *reinterpret_cast<const float4*>(row + expert(w, 0))
+                                            : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        x[4 * w] = f.x;
+        x[4 * w + 1] = f.y;
+        x[4 * w + 2] = f.z;
+        x[4 * w + 3] = f.w;
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int e = expert(w, q);
+        if (e < d.E) ds_row[e] = 0.0f;
+        if (softmax) x[4 * w + q] = e < d.E ? row[e] : -INFINITY;
+      }
+    }
+  }
+  float m = 0.0f, inv = 0.0f;
+  if (softmax) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < 4 * NV; ++v) {
+      const bool wrong = x[v] != x[v] || x[v] == INFINITY;
+      bad |= wrong;
+      x[v] = wrong ? -INFINITY : x[v];
+      top = fmaxf(top, x[v]);
+    }
+    m = gmax(top);
+    float sum = 0.0f;
+#pragma unroll
+    for (int v = 0; v < 4 * NV; ++v) {
+      x[v] = x[v] == -INFINITY ? 0.0f : expf(x[v] - m);
+      sum += x[v];
+    }
+    sum = gsum(sum);
+    inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  }
+  // the selected experts, one to a lane
+  int e = -1;
+  float gw = 0.0f, s = 0.0f, one_minus = 0.0f;
+  if (lane < d.k) {
+    e = topk_idx[t * d.k + lane];
+    gw = grad_weight[t * d.k + lane];
+    if ((unsigned)e >= (unsigned)d.E) {
+      atomicOr(status, MOE_STATUS_BAD_TOPK);
+      e = -1;
+      gw = 0.0f;
+    } else {
+      float xe = row[e];
+      if (xe != xe || (softmax && xe == INFINITY)) {
+        bad = true;
+        xe = -INFINITY;
+      }
+      s = score32(softmax, xe, m, inv);
+      one_minus = 1.0f / (1.0f + expf(xe));  // sigmoid: 1 - s without cancellation
+    }
+  }
+  const int base = (threadIdx.x & 63) - lane;
+  bool twice = false;
+  for (int j = 0; j < d.k; ++j) twice |= __shfl(e, base + j) == e && j < lane;
+  if (e >= 0 && twice) {
+    atomicOr(status, MOE_STATUS_BAD_TOPK);
+    e = -1;
+  }
+  float ds = g.scale * gw;
+  if (g.renorm) {
+    const float r = 1.0f / (gsum(s) + kTiny);
+    ds = g.scale * r * (gw - gsum(gw * s) * r);
+  }
+  const float dot = softmax ? gsum(e >= 0 ? s * ds : 0.0f) : 0.0f;
+  wave_lds_sync();
+  if (e >= 0) ds_row[e] = softmax ? ds : ds * s * one_minus;
+  wave_lds_sync();
+  float* __restrict__ out = grad_logits + t * d.E;
+#pragma unroll
+  for (int w = 0; w < NV; ++w) {
+    if (VEC) {
+      if (expert(w, 0) < d.E) {
+        float4 y = *reinterpret_cast<const float4*>(ds_row + expert(w, 0));
+        if (softmax) {
+          y.x = x[4 * w] * inv * (y.x - dot);
+          y.y = x[4 * w + 1] * inv * (y.y - dot);
+          y.z = x[4 * w + 2] * inv * (y.z - dot);
+          y.w = x[4 * w + 3] * inv * (y.w - dot);
+        }
+        *reinterpret_cast<float4*>(out + expert(w, 0)) = y;
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int o = expert(w, q);
+        if (o < d.E) out[o] = softmax ? x[4 * w + q] * inv * (ds_row[o] - dot) : ds_row[o];
+      }
+    }
+  }
+  if (bad) atomicOr(status, MOE_STATUS_NAN_LOGIT);
+}
+
+}  // namespace
+
+// Lanes per token P: at least 2k where it can be, so that the candidates
+// rarely outgrow the lanes, and at most 32 logits a lane.
+hipError_t launch_gate(const Dims& d, const moex_gate_config& g, const float* logits, const float* bias,
+                       const int32_t* prev_topk, int32_t* topk_idx, float* topk_val, float* weight,
+                       uint64_t* tile_mask, uint64_t* prev_mask, int32_t* status, hipStream_t st) {
+  if (d.NT == 0) return hipSuccess;
+  const bool vec = (d.E % 4) == 0 && ((uintptr_t)logits % 16) == 0;
+  int P = 8;
+  while (P < 64 && (P < 2 * d.k || P * 32 < d.E)) P *= 2;
+  int V = 1;
+  while (P * V < d.E) V *= 2;
+#define MOE_GATE_CASE(P_, V_)                                                                                        \
+  if (P == (P_) && V == (V_))                                                                                        \
+    return launch_gate_pv<P_, V_>(d, g, vec, logits, bias, prev_topk, topk_idx, topk_val, weight, tile_mask,         \
+                                  prev_mask, status, st);
+#define MOE_GATE_P(P_) \
+  MOE_GATE_CASE(P_, 1) MOE_GATE_CASE(P_, 2) MOE_GATE_CASE(P_, 4) MOE_GATE_CASE(P_, 8) MOE_GATE_CASE(P_, 16) \
+  MOE_GATE_CASE(P_, 32)
+  MOE_GATE_P(8)
+  MOE_GATE_P(16)
+  MOE_GATE_P(32)
+  MOE_GATE_P(64)
+#undef MOE_GATE_P
+#undef MOE_GATE_CASE
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_gate_grad(const Dims& d, const moex_gate_config& g, const float* logits, const int32_t* topk_idx,
+                            const float* grad_weight, float* grad_logits, int32_t* status, hipStream_t st) {
+  if (d.T == 0) return hipSuccess;
+  const bool vec = (d.E % 4) == 0 && ((uintptr_t)logits % 16) == 0 && ((uintptr_t)grad_logits % 16) == 0;
+  int P = 8;
+  while (P < 64 && (P < d.k || P * 4 < d.E)) P *= 2;
+  const int nv = (d.E + 4 * P - 1) / (4 * P);  // at most 8: E <= 2048
+  const size_t lds = sizeof(float) * (size_t)(256 / P) * ((d.E + 3) / 4 * 4);
+  const dim3 grid((unsigned)((d.T + 256 / P - 1) / (256 / P)));
+#define MOE_GRAD_CASE(NV_, VEC_)                                                                                    \
+  if (nv <= (NV_) && vec == (VEC_)) {                                                                               \
+    hipLaunchKernelGGL((gate_grad_kernel<NV_, VEC_>), grid, dim3(256), lds, st, d, g, P, logits, topk_idx,          \
+                       grad_weight, grad_logits, status);                                                           \
+    return hipGetLastError();                                                                                       \
+  }
+  MOE_GRAD_CASE(1, true) MOE_GRAD_CASE(2, true) MOE_GRAD_CASE(4, true) MOE_GRAD_CASE(8, true)
+  MOE_GRAD_CASE(1, false) MOE_GRAD_CASE(2, false) MOE_GRAD_CASE(4, false) MOE_GRAD_CASE(8, false)
+#undef MOE_GRAD_CASE
+  return hipErrorInvalidValue;
+}
+
+}  // namespace moe
