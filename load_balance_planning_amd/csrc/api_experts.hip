@@ -29,8 +29,8 @@ bool blocks_ok(const void* q, const void* scale) { return q && scale && aligned(
 
 int check_product(moe_plan_t h, const moe_plan_out* plan, const int32_t* inst_offset, int32_t n, int32_t k) {
   if (!h || !plan || !plan->n_inst || !plan->inst_expert || !inst_offset || n < 1 || k < 1) return MOE_ERR_INVALID_ARG;
-  // element offsets inside one row are 32-bit
-  if (n > (1 << 24) || k > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+  // a tile of 256 rows is addressed with 32-bit offsets
+  if (n > (1 << 20) || k > (1 << 20)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

@@ -60,6 +60,15 @@ __device__ __forceinline__ bool find_row_tile(const Instances& in, int n_inst, i
   return *row >= span->begin && *row < span->end;
 }
 
+// The same tile in scalar registers (rows < 2^31): every lane holds the same
+// values, which the compiler cannot see.
+__device__ __forceinline__ void keep_in_scalars(Span* s, int64_t* row) {
+  s->begin = __builtin_amdgcn_readfirstlane((int)s->begin);
+  s->end = __builtin_amdgcn_readfirstlane((int)s->end);
+  s->expert = __builtin_amdgcn_readfirstlane(s->expert);
+  *row = __builtin_amdgcn_readfirstlane((int)*row);
+}
+
 // Upper bound of the tile ids.
 inline int64_t row_tile_ids(const Instances& in, int rows) { return in.rows / rows + in.cap; }
 

@@ -98,11 +98,236 @@ __global__ __launch_bounds__(256) void matmul_rows16_kernel(Instances in, const 
   }
 }
 
+// ---- tiles ---------------------------------------------------------------------
+//
+// BC channels x BT rows per workgroup of WC x WT waves.  Both operands' blocks
+// of 128 go to LDS by direct loads, one step ahead of the products; a step is
+// one block of the long axis.
+//
+// LDS rows are 128 bytes, eight 16-byte pieces.  A direct load writes its
+// lanes' pieces one after the other, so the placement is chosen on the memory
+// side: the piece of linear place L belongs to row pair L / 16, and within the
+// pair's 256 bytes piece p of row R lies at place (8 (R % 2) + p) ^ s(R).  The
+// 16 lanes of a read then find their pieces in 16 different places of 256
+// bytes.  They read rows 16j + 0..15 of the rows operand and rows 64h + 16a +
+// 4i + b, a, b < 4, of the channels, so s takes three bits that vary there and
+// not with j, h or i (one address serves a step's reads, the rest are
+// immediate offsets): bits 1, 2, 3 of R, and bits 1, 4, 5.
+template <bool CHANNELS>
+__device__ __forceinline__ int piece_swizzle(int pair) {  // pair = R / 2
+  return CHANNELS ? (pair & 1) | ((pair >> 2) & 6) : pair & 7;
+}
+template <bool CHANNELS>
+__device__ __forceinline__ int piece_at(int row, int p) {
+  return (row >> 1) * 256 + ((((row & 1) << 3) | p) ^ piece_swizzle<CHANNELS>(row >> 1)) * 16;
+}
+
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+// Only the device pass knows buffer descriptors; the host pass needs the
+// kernels' names alone.
+#ifdef __HIP_DEVICE_COMPILE__
+// A buffer descriptor over `bytes` from p: loads then take a 32-bit offset per
+// lane, which stays the same from step to step, and the step's in a scalar.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00027000);
+}
+#endif
+
+// Barrier after which every wave sees every wave's loads into LDS.  A barrier
+// alone does not wait for them: to the compiler they are loads, which a
+// workgroup fence need not order.
+__device__ __forceinline__ void sync_with_loads() {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+}
+
+template <int BC, int BT, int WC, int WT>
+struct TileShape {
+  static constexpr int kWaves = WC * WT, kThreads = 64 * kWaves;
+  static constexpr int kWaveC = BC / WC, kWaveT = BT / WT;       // a wave's channels and rows
+  static constexpr int kC = kWaveC / 16, kT = kWaveT / 16;       // in instruction tiles
+  static constexpr int kPassC = BC * kBlk / (16 * kThreads), kPassT = BT * kBlk / (16 * kThreads);
+  static_assert(kWaveC % 64 == 0 && kBlk % kWaveC == 0, "a wave's channels share one scale and make whole 64s");
+  static_assert(BC * kBlk % (16 * kThreads) == 0 && BT * kBlk % (16 * kThreads) == 0, "whole passes");
+};
+
+template <int BC, int BT, int WC, int WT>
+__global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads)) void matmul_tile_kernel(
+    Instances in, const uint8_t* __restrict__ x, const uint8_t* __restrict__ xs, const uint8_t* __restrict__ w,
+    const uint8_t* __restrict__ ws, int n, int k, int64_t row_tiles, uint16_t* __restrict__ y,
+    int32_t* __restrict__ status) {
+#ifdef __HIP_DEVICE_COMPILE__
+  using S = TileShape<BC, BT, WC, WT>;
+  __shared__ __align__(256) unsigned char c0_s[BC * kBlk];
+  __shared__ __align__(256) unsigned char t0_s[BT * kBlk];
+  __shared__ __align__(256) unsigned char c1_s[BC * kBlk];
+  __shared__ __align__(256) unsigned char t1_s[BT * kBlk];
+  if (blockIdx.x == 0) check_instances(in, status);
+  const int nct = (n + BC - 1) / BC;
+  // Workgroups go to the eight XCDs in turn: each XCD takes a run of
+  // consecutive tiles, four row tiles by all channel tiles at a time, so that
+  // the tiles that it works on at once share their operands in its L2.
+  const int64_t total = row_tiles * nct;
+  const int64_t per = (total + 7) / 8;
+  const int64_t id = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if ((int64_t)(blockIdx.x >> 3) >= per || id >= total) return;
+  const int64_t band = id / (4 * nct);
+  const int in_band = (int)(id - band * 4 * nct);
+  const int band_rows = (int)min((int64_t)4, row_tiles - band * 4);
+  const int64_t rt = band * 4 + in_band % band_rows;
+  const int cbase = __builtin_amdgcn_readfirstlane(in_band / band_rows * BC);
+  Span sp;
+  int64_t r0;
+  if (!find_row_tile<BT>(in, instance_count(in), rt, &sp, &r0)) return;
+  keep_in_scalars(&sp, &r0);
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int nb = (k + kBlk - 1) / kBlk, ns = (nb + 3) / 4 * 4;
+  const uint32_t kp = (uint32_t)nb * kBlk;
+  const int nbn = (n + kBlk - 1) / kBlk;
+  const int rows_left = (int)min((int64_t)BT, sp.end - r0), chans_left = min(BC, n - cbase);
+  // where this thread's pieces come from: the same place of every pass
+  constexpr int kRowsPerPass = S::kThreads / 8;
+  static_assert(kRowsPerPass % 64 == 0, "the swizzle does not change from pass to pass");
+  const int pair = threadIdx.x >> 4;
+  const int place_c = (threadIdx.x & 15) ^ piece_swizzle<true>(pair);
+  const int place_t = (threadIdx.x & 15) ^ piece_swizzle<false>(pair);
+  uint32_t off_c[S::kPassC], off_t[S::kPassT];
+#pragma unroll
+  for (int q = 0; q < S::kPassC; ++q)
+    off_c[q] = (uint32_t)min(q * kRowsPerPass + 2 * pair + (place_c >> 3), chans_left - 1) * kp + 16 * (place_c & 7);
+#pragma unroll
+  for (int q = 0; q < S::kPassT; ++q)
+    off_t[q] = (uint32_t)min(q * kRowsPerPass + 2 * pair + (place_t >> 3), rows_left - 1) * kp + 16 * (place_t & 7);
+  const auto w_buf = buffer_of(w + ((int64_t)sp.expert * n + cbase) * kp, (uint32_t)chans_left * kp);
+  const auto x_buf = buffer_of(x + r0 * kp, (uint32_t)rows_left * kp);
+  auto load = [&](unsigned char* c_s, unsigned char* t_s, int b) {
+#pragma unroll
+    for (int q = 0; q < S::kPassC; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(w_buf, (lds_ptr)(c_s + (q * S::kThreads + wave * 64) * 16), 16, off_c[q],
+                                               b * kBlk, 0, 0);
+#pragma unroll
+    for (int q = 0; q < S::kPassT; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(x_buf, (lds_ptr)(t_s + (q * S::kThreads + wave * 64) * 16), 16, off_t[q],
+                                               b * kBlk, 0, 0);
+  };
+  const int wc = wave % WC * S::kWaveC, wt = wave / WC * S::kWaveT;
+  // scales, four blocks to a word: of this lane's row in each instruction
+  // tile, and of the wave's channels
+  const auto xs_buf = buffer_of(xs + r0 * ns, (uint32_t)(rows_left * ns));
+  uint32_t xs_off[S::kT];
+#pragma unroll
+  for (int j = 0; j < S::kT; ++j) xs_off[j] = (uint32_t)(min(wt + 16 * j + r, rows_left - 1) * ns);
+  const uint8_t* ws_base = ws + ((int64_t)sp.expert * nbn + min((cbase + wc) / kBlk, nbn - 1)) * ns;
+  int sx[S::kT], sw, sx_next[S::kT], sw_next;
+  auto load_scales = [&](int b) {
+#pragma unroll
+    for (int j = 0; j < S::kT; ++j) sx_next[j] = (int)__builtin_amdgcn_raw_buffer_load_b32(xs_buf, xs_off[j], b & ~3, 0);
+    sw_next = *reinterpret_cast<const int*>(ws_base + (b & ~3));
+  };
+  auto take_scales = [&](int b) {  // those of block b, b even, to the lowest byte
+#pragma unroll
+    for (int j = 0; j < S::kT; ++j) sx[j] = sx_next[j] >> (8 * (b & 2));
+    sw = sw_next >> (8 * (b & 2));
+  };
+  // LDS places of this lane's pieces in the first tile; the others lie at constant distances
+  const int at_c = piece_at<true>(wc + 16 * (r >> 2) + (r & 3), g);
+  const int at_t = piece_at<false>(wt + r, g);
+  v4f acc[S::kC][S::kT];
+#pragma unroll
+  for (int i = 0; i < S::kC; ++i)
+#pragma unroll
+    for (int j = 0; j < S::kT; ++j) acc[i][j] = v4f{0, 0, 0, 0};
+  auto frag = [&](const unsigned char* s, int at, int add) {
+    union {
+      v8i v;
+      v4i h[2];
+    } u;
+    u.h[0] = *reinterpret_cast<const v4i*>(s + at + add);
+    u.h[1] = *reinterpret_cast<const v4i*>(s + (at ^ 64) + add);  // piece g + 4
+    return u.v;
+  };
+  auto step = [&](const unsigned char* c_s, const unsigned char* t_s) {
+    v8i tv[S::kT];
+#pragma unroll
+    for (int j = 0; j < S::kT; ++j) tv[j] = frag(t_s, at_t, 16 * j * kBlk);
+    v8i cv[2];
+    cv[0] = frag(c_s, at_c, 0);
+#pragma unroll
+    for (int i = 0; i < S::kC; ++i) {
+      if (i + 1 < S::kC) cv[(i + 1) & 1] = frag(c_s, at_c, (64 * ((i + 1) / 4) + 4 * ((i + 1) & 3)) * kBlk);
+#pragma unroll
+      for (int j = 0; j < S::kT; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(cv[i & 1], tv[j], acc[i][j], 0, 0, 0, sw, 0, sx[j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int j = 0; j < S::kT; ++j) sx[j] >>= 8;
+    sw >>= 8;
+  };
+  load_scales(0);
+  load(c0_s, t0_s, 0);
+  // No branch inside a round: the last round loads a block and scales again
+  // that nothing reads (a conditional load lets the compiler sink a step's
+  // products below the next barrier, with all their operands kept alive).
+  for (int b = 0; b + 2 <= nb; b += 2) {
+    sync_with_loads();  // block b has arrived, and every wave is done with block b - 1
+    take_scales(b);
+    load(c1_s, t1_s, b + 1);
+    step(c0_s, t0_s);
+    sync_with_loads();
+    const int next = min(b + 2, nb - 1);
+    load_scales(next);
+    load(c0_s, t0_s, next);
+    step(c1_s, t1_s);
+  }
+  sync_with_loads();  // also: no load into LDS may be under way when the workgroup ends
+  if (nb & 1) {
+    take_scales(nb - 1);
+    step(c0_s, t0_s);
+  }
+  const bool vec = n % 8 == 0 && ((uintptr_t)y & 15) == 0;
+#pragma unroll
+  for (int j = 0; j < S::kT; ++j) {
+    const int row = wt + 16 * j + r;
+    if (row >= rows_left) continue;
+#pragma unroll
+    for (int i = 0; i < S::kC; i += 2) {
+      // two instruction tiles: eight consecutive channels
+      const int c = wc + 64 * (i / 4) + 16 * g + 4 * (i & 3);
+      if (c >= chans_left) continue;
+      uint16_t* dst = y + (r0 + row) * n + cbase + c;
+      const u32x4 o = {pack_bf16(acc[i][j][0], acc[i][j][1]), pack_bf16(acc[i][j][2], acc[i][j][3]),
+                       pack_bf16(acc[i + 1][j][0], acc[i + 1][j][1]), pack_bf16(acc[i + 1][j][2], acc[i + 1][j][3])};
+      if (vec) {
+        *reinterpret_cast<u32x4*>(dst) = o;
+      } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (c + q < chans_left) dst[q] = (uint16_t)(o[q / 2] >> (16 * (q & 1)));
+      }
+    }
+  }
+#endif
+}
+
+template <int BC, int BT, int WC, int WT>
+hipError_t launch_tiles(const Instances& in, const uint8_t* x, const uint8_t* xs, const uint8_t* w, const uint8_t* ws,
+                        int n, int k, uint16_t* y, int32_t* status, hipStream_t st) {
+  const int64_t row_tiles = row_tile_ids(in, BT), total = row_tiles * ((n + BC - 1) / BC);
+  hipLaunchKernelGGL((matmul_tile_kernel<BC, BT, WC, WT>), dim3((unsigned)((total + 7) / 8 * 8)),
+                     dim3(TileShape<BC, BT, WC, WT>::kThreads), 0, st, in, x, xs, w, ws, n, k, row_tiles, y, status);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_matmul(const Instances& in, const uint8_t* x, const uint8_t* xs, const uint8_t* w, const uint8_t* ws,
                          int32_t n, int32_t k, uint16_t* y, int32_t* status, hipStream_t st) {
   if (in.rows == 0) return hipSuccess;
+  if (in.rows >= (int64_t)32 * in.E) return launch_tiles<256, 256, 2, 4>(in, x, xs, w, ws, n, k, y, status, st);
   const int64_t tiles = row_tile_ids(in, kRowsS) * ((n + kChanS - 1) / kChanS);
   const int64_t grid = tiles < (1 << 20) ? tiles : (1 << 20);
   hipLaunchKernelGGL(matmul_rows16_kernel, dim3((unsigned)grid), dim3(256), 0, st, in, x, xs, w, ws, n, k, tiles, y,
