@@ -17,6 +17,7 @@ namespace {
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
 
 // 32 of a row's 128 bytes: the 16 of lane group g in each half.  (Both
 // operands use the same order, so any order of the block does.)
@@ -101,21 +102,34 @@ __global__ __launch_bounds__(256) void matmul_rows16_kernel(Instances in, const 
 // ---- tiles ---------------------------------------------------------------------
 //
 // BC channels x BT rows per workgroup of WC x WT waves.  Both operands' blocks
-// of 128 go to LDS by direct loads, one step ahead of the products; a step is
-// one block of the long axis.
+// of 128 go to LDS by direct loads, a step (one block of the long axis) ahead
+// of the products.  A step is two halves of 64 bytes, one 32x32x64 instruction
+// deep; while a half's products run, the other half's operands are read from
+// LDS into a second set of registers.  There is one barrier a step, between
+// its halves: there the block's reads are all done, so the block after next
+// may be loaded over it, and the next block has arrived.
+//
+// The wave tile decides what LDS has to deliver: 128 x 64 tiles of eight waves
+// read 192 KB a step and 64 KB are written, at 128 bytes a cycle as long as
+// the products themselves take (2048 cycles; the kernel ran at 40 % of the
+// matrix unit's rate), 128 x 128 tiles of four waves read 128 KB.
 //
 // LDS rows are 128 bytes, eight 16-byte pieces.  A direct load writes its
 // lanes' pieces one after the other, so the placement is chosen on the memory
 // side: the piece of linear place L belongs to row pair L / 16, and within the
 // pair's 256 bytes piece p of row R lies at place (8 (R % 2) + p) ^ s(R).  The
 // 16 lanes of a read then find their pieces in 16 different places of 256
-// bytes.  They read rows 16j + 0..15 of the rows operand and rows 64h + 16a +
-// 4i + b, a, b < 4, of the channels, so s takes three bits that vary there and
-// not with j, h or i (one address serves a step's reads, the rest are
-// immediate offsets): bits 1, 2, 3 of R, and bits 1, 4, 5.
+// bytes: s takes three bits in which the rows of 16 lanes differ and which do
+// not change from one instruction tile to the next (one address serves all
+// reads of a step, the rest are immediate offsets) -- bits 1, 2, 3 of R for
+// the rows operand, and 1, 2, 4 for the channels.
+//
+// A lane's 16 results are matrix rows 8a + 4h + j, h its half of the wave, of
+// one column.  Matrix row 8a + 4h + j stands for channel 16h + 4a + j, so they
+// are 16 consecutive channels of one row of y.
 template <bool CHANNELS>
 __device__ __forceinline__ int piece_swizzle(int pair) {  // pair = R / 2
-  return CHANNELS ? (pair & 1) | ((pair >> 2) & 6) : pair & 7;
+  return CHANNELS ? (pair & 3) | ((pair >> 1) & 4) : pair & 7;
 }
 template <bool CHANNELS>
 __device__ __forceinline__ int piece_at(int row, int p) {
@@ -146,14 +160,14 @@ template <int BC, int BT, int WC, int WT>
 struct TileShape {
   static constexpr int kWaves = WC * WT, kThreads = 64 * kWaves;
   static constexpr int kWaveC = BC / WC, kWaveT = BT / WT;       // a wave's channels and rows
-  static constexpr int kC = kWaveC / 16, kT = kWaveT / 16;       // in instruction tiles
+  static constexpr int kC = kWaveC / 32, kT = kWaveT / 32;       // in instruction tiles
   static constexpr int kPassC = BC * kBlk / (16 * kThreads), kPassT = BT * kBlk / (16 * kThreads);
-  static_assert(kWaveC % 64 == 0 && kBlk % kWaveC == 0, "a wave's channels share one scale and make whole 64s");
+  static_assert(kWaveC % 32 == 0 && kBlk % kWaveC == 0, "a wave's channels share one scale and make whole tiles");
   static_assert(BC * kBlk % (16 * kThreads) == 0 && BT * kBlk % (16 * kThreads) == 0, "whole passes");
 };
 
 template <int BC, int BT, int WC, int WT>
-__global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads)) void matmul_tile_kernel(
+__global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), 1) void matmul_tile_kernel(
     Instances in, const uint8_t* __restrict__ x, const uint8_t* __restrict__ xs, const uint8_t* __restrict__ w,
     const uint8_t* __restrict__ ws, int n, int k, int64_t row_tiles, uint16_t* __restrict__ y,
     int32_t* __restrict__ status) {
@@ -183,14 +197,14 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads)) void matmul_
   keep_in_scalars(&sp, &r0);
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, g = lane >> 4;
+  const int r = lane & 31, g = lane >> 5;
   const int nb = (k + kBlk - 1) / kBlk, ns = (nb + 3) / 4 * 4;
   const uint32_t kp = (uint32_t)nb * kBlk;
   const int nbn = (n + kBlk - 1) / kBlk;
   const int rows_left = (int)min((int64_t)BT, sp.end - r0), chans_left = min(BC, n - cbase);
   // where this thread's pieces come from: the same place of every pass
   constexpr int kRowsPerPass = S::kThreads / 8;
-  static_assert(kRowsPerPass % 64 == 0, "the swizzle does not change from pass to pass");
+  static_assert(kRowsPerPass % 32 == 0, "the swizzle does not change from pass to pass");
   const int pair = threadIdx.x >> 4;
   const int place_c = (threadIdx.x & 15) ^ piece_swizzle<true>(pair);
   const int place_t = (threadIdx.x & 15) ^ piece_swizzle<false>(pair);
@@ -219,7 +233,7 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads)) void matmul_
   const auto xs_buf = buffer_of(xs + r0 * ns, (uint32_t)(rows_left * ns));
   uint32_t xs_off[S::kT];
 #pragma unroll
-  for (int j = 0; j < S::kT; ++j) xs_off[j] = (uint32_t)(min(wt + 16 * j + r, rows_left - 1) * ns);
+  for (int j = 0; j < S::kT; ++j) xs_off[j] = (uint32_t)(min(wt + 32 * j + r, rows_left - 1) * ns);
   const uint8_t* ws_base = ws + ((int64_t)sp.expert * nbn + min((cbase + wc) / kBlk, nbn - 1)) * ns;
   int sx[S::kT], sw, sx_next[S::kT], sw_next;
   auto load_scales = [&](int b) {
@@ -232,81 +246,117 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads)) void matmul_
     for (int j = 0; j < S::kT; ++j) sx[j] = sx_next[j] >> (8 * (b & 2));
     sw = sw_next >> (8 * (b & 2));
   };
-  // LDS places of this lane's pieces in the first tile; the others lie at constant distances
-  const int at_c = piece_at<true>(wc + 16 * (r >> 2) + (r & 3), g);
-  const int at_t = piece_at<false>(wt + r, g);
-  v4f acc[S::kC][S::kT];
-#pragma unroll
-  for (int i = 0; i < S::kC; ++i)
-#pragma unroll
-    for (int j = 0; j < S::kT; ++j) acc[i][j] = v4f{0, 0, 0, 0};
-  auto frag = [&](const unsigned char* s, int at, int add) {
-    union {
-      v8i v;
-      v4i h[2];
-    } u;
-    u.h[0] = *reinterpret_cast<const v4i*>(s + at + add);
-    u.h[1] = *reinterpret_cast<const v4i*>(s + (at ^ 64) + add);  // piece g + 4
-    return u.v;
-  };
-  auto step = [&](const unsigned char* c_s, const unsigned char* t_s) {
-    v8i tv[S::kT];
-#pragma unroll
-    for (int j = 0; j < S::kT; ++j) tv[j] = frag(t_s, at_t, 16 * j * kBlk);
-    v8i cv[2];
-    cv[0] = frag(c_s, at_c, 0);
-#pragma unroll
-    for (int i = 0; i < S::kC; ++i) {
-      if (i + 1 < S::kC) cv[(i + 1) & 1] = frag(c_s, at_c, (64 * ((i + 1) / 4) + 4 * ((i + 1) & 3)) * kBlk);
-#pragma unroll
-      for (int j = 0; j < S::kT; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(cv[i & 1], tv[j], acc[i][j], 0, 0, 0, sw, 0, sx[j]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+  auto next_scales = [&]() {
 #pragma unroll
     for (int j = 0; j < S::kT; ++j) sx[j] >>= 8;
     sw >>= 8;
   };
+  // LDS places of this lane's pieces in the first tiles; the others lie at
+  // constant distances.  Half h of a block is pieces 4h .. 4h+3, lanes 0..31
+  // take the first and third of them, lanes 32..63 the others.
+  const int at_c = piece_at<true>(wc + 16 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3), g);
+  const int at_t = piece_at<false>(wt + r, g);
+  v16f acc[S::kC][S::kT];
+#pragma unroll
+  for (int i = 0; i < S::kC; ++i)
+#pragma unroll
+    for (int j = 0; j < S::kT; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
+  struct Half {
+    v8i c[S::kC], t[S::kT];
+  };
+  auto frag = [&](const unsigned char* s, int at, int half, int add) {
+    union {
+      v8i v;
+      v4i h[2];
+    } u;
+    u.h[0] = *reinterpret_cast<const v4i*>(s + (at ^ (half * 64)) + add);         // piece 4 half + g
+    u.h[1] = *reinterpret_cast<const v4i*>(s + (at ^ (half * 64 + 32)) + add);    // piece 4 half + g + 2
+    return u.v;
+  };
+  auto read = [&](Half* f, const unsigned char* c_s, const unsigned char* t_s, int half) {
+#pragma unroll
+    for (int j = 0; j < S::kT; ++j) f->t[j] = frag(t_s, at_t, half, 32 * j * kBlk);
+#pragma unroll
+    for (int i = 0; i < S::kC; ++i) f->c[i] = frag(c_s, at_c, half, 32 * i * kBlk);
+  };
+  auto multiply = [&](const Half& f) {
+#pragma unroll
+    for (int i = 0; i < S::kC; ++i)
+#pragma unroll
+      for (int j = 0; j < S::kT; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.c[i], f.t[j], acc[i][j], 0, 0, 0, sw, 0, sx[j]);
+  };
+  // a half's products, with the other half's reads (and LOADS direct loads)
+  // spread between them
+  constexpr int kProducts = S::kC * S::kT, kReads = 2 * (S::kC + S::kT);
+  auto spread = [&](bool loads) {
+#pragma unroll
+    for (int q = 0; q < kProducts; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a product
+      __builtin_amdgcn_sched_group_barrier(0x100, (kReads + kProducts - 1) / kProducts, 0);
+      if (loads) __builtin_amdgcn_sched_group_barrier(0x020, (S::kPassC + S::kPassT + kProducts - 1) / kProducts, 0);
+    }
+  };
+  Half f0, f1;
   load_scales(0);
   load(c0_s, t0_s, 0);
-  // No branch inside a round: the last round loads a block and scales again
-  // that nothing reads (a conditional load lets the compiler sink a step's
-  // products below the next barrier, with all their operands kept alive).
+  sync_with_loads();
+  load(c1_s, t1_s, min(1, nb - 1));
+  read(&f0, c0_s, t0_s, 0);
+  // No branch inside a round: past the last block the loads and reads take
+  // some block again, which nothing uses.
   for (int b = 0; b + 2 <= nb; b += 2) {
-    sync_with_loads();  // block b has arrived, and every wave is done with block b - 1
     take_scales(b);
-    load(c1_s, t1_s, b + 1);
-    step(c0_s, t0_s);
+    read(&f1, c0_s, t0_s, 1);
+    multiply(f0);
+    spread(false);
     sync_with_loads();
-    const int next = min(b + 2, nb - 1);
-    load_scales(next);
-    load(c0_s, t0_s, next);
-    step(c1_s, t1_s);
+    load(c0_s, t0_s, min(b + 2, nb - 1));
+    read(&f0, c1_s, t1_s, 0);
+    multiply(f1);
+    spread(true);
+    next_scales();
+    read(&f1, c1_s, t1_s, 1);
+    multiply(f0);
+    spread(false);
+    sync_with_loads();
+    load_scales(min(b + 2, nb - 1));
+    load(c1_s, t1_s, min(b + 3, nb - 1));
+    read(&f0, c0_s, t0_s, 0);
+    multiply(f1);
+    spread(true);
   }
   sync_with_loads();  // also: no load into LDS may be under way when the workgroup ends
   if (nb & 1) {
     take_scales(nb - 1);
-    step(c0_s, t0_s);
+    read(&f1, c0_s, t0_s, 1);
+    multiply(f0);
+    multiply(f1);
   }
   const bool vec = n % 8 == 0 && ((uintptr_t)y & 15) == 0;
 #pragma unroll
   for (int j = 0; j < S::kT; ++j) {
-    const int row = wt + 16 * j + r;
+    const int row = wt + 32 * j + r;
     if (row >= rows_left) continue;
 #pragma unroll
-    for (int i = 0; i < S::kC; i += 2) {
-      // two instruction tiles: eight consecutive channels
-      const int c = wc + 64 * (i / 4) + 16 * g + 4 * (i & 3);
-      if (c >= chans_left) continue;
-      uint16_t* dst = y + (r0 + row) * n + cbase + c;
-      const u32x4 o = {pack_bf16(acc[i][j][0], acc[i][j][1]), pack_bf16(acc[i][j][2], acc[i][j][3]),
-                       pack_bf16(acc[i + 1][j][0], acc[i + 1][j][1]), pack_bf16(acc[i + 1][j][2], acc[i + 1][j][3])};
-      if (vec) {
-        *reinterpret_cast<u32x4*>(dst) = o;
-      } else {
+    for (int i = 0; i < S::kC; ++i) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (c + q < chans_left) dst[q] = (uint16_t)(o[q / 2] >> (16 * (q & 1)));
+      for (int h = 0; h < 2; ++h) {  // eight consecutive channels
+        const int c = wc + 32 * i + 16 * g + 8 * h;
+        if (c >= chans_left) continue;
+        uint16_t* dst = y + (r0 + row) * n + cbase + c;
+        u32x4 o;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[q] = pack_bf16(acc[i][j][8 * h + 2 * q], acc[i][j][8 * h + 2 * q + 1]);
+        if (vec) {
+          *reinterpret_cast<u32x4*>(dst) = o;
+        } else {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (c + q < chans_left) dst[q] = (uint16_t)(o[q / 2] >> (16 * (q & 1)));
+        }
       }
     }
   }
@@ -327,7 +377,7 @@ hipError_t launch_tiles(const Instances& in, const uint8_t* x, const uint8_t* xs
 hipError_t launch_matmul(const Instances& in, const uint8_t* x, const uint8_t* xs, const uint8_t* w, const uint8_t* ws,
                          int32_t n, int32_t k, uint16_t* y, int32_t* status, hipStream_t st) {
   if (in.rows == 0) return hipSuccess;
-  if (in.rows >= (int64_t)32 * in.E) return launch_tiles<256, 256, 2, 4>(in, x, xs, w, ws, n, k, y, status, st);
+  if (in.rows >= (int64_t)32 * in.E) return launch_tiles<256, 256, 2, 2>(in, x, xs, w, ws, n, k, y, status, st);
   const int64_t tiles = row_tile_ids(in, kRowsS) * ((n + kChanS - 1) / kChanS);
   const int64_t grid = tiles < (1 << 20) ? tiles : (1 << 20);
   hipLaunchKernelGGL(matmul_rows16_kernel, dim3((unsigned)grid), dim3(256), 0, st, in, x, xs, w, ws, n, k, tiles, y,
