@@ -139,6 +139,8 @@ extern "C" int moex_wgrad(moe_plan_t h, const moe_plan_out* plan, const int32_t*
   const int rc = check_product(h, plan, inst_offset, n, k);
   if (rc != MOE_OK) return rc;
   if (!dw || (h->d.T > 0 && (!blocks_ok(dy, dy_scale) || !blocks_ok(x, x_scale)))) return MOE_ERR_INVALID_ARG;
+  // one 256-thread workgroup per tile, fewer than 2^32 work-items a launch
+  if (moe::wgrad_tiles(instances(h->d, plan, inst_offset), n, k) >= (int64_t)1 << 24) return MOE_ERR_UNSUPPORTED;
   const DeviceScope on_device(h->device);
   if (!on_device.ok()) return MOE_ERR_HIP;
   return hip_rc(moe::launch_wgrad(instances(h->d, plan, inst_offset), dy, dy_scale, x, x_scale, n, k, dw,

@@ -37,6 +37,7 @@ struct Instances {
 };
 hipError_t launch_matmul(const Instances& in, const uint8_t* x, const uint8_t* xs, const uint8_t* w, const uint8_t* ws,
                          int32_t n, int32_t k, uint16_t* y, int32_t* status, hipStream_t st);
+int64_t wgrad_tiles(const Instances& in, int32_t n, int32_t k);  // workgroups of launch_wgrad
 hipError_t launch_wgrad(const Instances& in, const uint8_t* dy, const uint8_t* dys, const uint8_t* x,
                         const uint8_t* xs, int32_t n, int32_t k, uint16_t* dw, int32_t* status, hipStream_t st);
 

@@ -7,6 +7,7 @@
 // results are then four channels of one row.  Which channel a matrix row of
 // the instruction stands for is free; row 4g + j of tile i is channel
 // 16g + 4i + j, so four tiles give a lane 16 consecutive channels (32 bytes).
+#include "buffers.h"
 #include "experts.h"
 #include "fp8_block.h"
 #include "instances.h"
@@ -135,18 +136,6 @@ template <bool CHANNELS>
 __device__ __forceinline__ int piece_at(int row, int p) {
   return (row >> 1) * 256 + ((((row & 1) << 3) | p) ^ piece_swizzle<CHANNELS>(row >> 1)) * 16;
 }
-
-typedef __attribute__((address_space(3))) void* lds_ptr;
-
-// Only the device pass knows buffer descriptors; the host pass needs the
-// kernels' names alone.
-#ifdef __HIP_DEVICE_COMPILE__
-// A buffer descriptor over `bytes` from p: loads then take a 32-bit offset per
-// lane, which stays the same from step to step, and the step's in a scalar.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00027000);
-}
-#endif
 
 // Barrier after which every wave sees every wave's loads into LDS.  A barrier
 // alone does not wait for them: to the compiler they are loads, which a

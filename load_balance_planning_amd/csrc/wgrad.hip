@@ -3,16 +3,30 @@
 //
 // The sum runs over rows, along which both operands change scale, so the
 // scaled 8-bit instruction does not apply; the values are widened to bf16 --
-// e4m3 times a power of two is a bf16 value exactly -- and multiplied by the
-// bf16 instruction.  The instruction wants eight consecutive rows of one
-// column in a lane, memory has columns next to each other: a thread loads an
-// 8 x 8 piece, widens it, transposes it in registers and writes eight 16-byte
-// pieces (eight rows of a column) to LDS.
+// e4m3 times a power of two is a bf16 value exactly, down to bf16's subnormals
+// -- and multiplied by the bf16 instruction.  It wants eight consecutive rows
+// of one column in a lane, memory has columns next to each other: a thread
+// loads an 8 x 8 piece, widens it, pairs rows in registers and writes eight
+// 16-byte pieces (eight rows of a column) to LDS.
 //
-// LDS holds [column][64 rows], 128 bytes a column.  Its 16-byte pieces are
-// placed so that both the writes (columns 8 apart) and the reads (consecutive
-// columns) of 16 lanes fall into 16 different places of 256 bytes: piece p of
-// column c lies at 256 * (c / 2) + 16 * ((8 * (c % 2) + p) ^ s(c)).
+// 256 x 256 of dw[e] per workgroup of four waves, 128 x 128 each, in steps of
+// 64 rows: 2048 cycles of products against 1024 of LDS reads, 512 of writes and
+// some 800 of widening, which a wave issues between its products.  A step is
+// four slices of 16 rows.  While a slice's products run, the next slice's
+// operands are read, and a quarter of the next step's values (loaded a step
+// earlier) is widened and written to the other half of LDS.  The last slice
+// runs behind the step's only barrier.
+//
+// LDS: [slice][column][2 pieces], 32 bytes a column.  Within 256 bytes (eight
+// columns), piece g of column c lies at place (2 (c % 8) + g) ^ s(c), with s
+// from bits 3 to 6 of c, so that 16 lanes that write (columns 8 apart) and 16
+// that read (consecutive columns of dy; 16a + 4i + j of x, see below) find 16
+// different places.
+//
+// x's columns are the instruction's rows, dy's its columns: a lane's 16
+// results are then 16 consecutive columns of x (matrix row 8a + 4h + j stands
+// for column 16h + 4a + j, h the lane's half of the wave) in one row of dw.
+#include "buffers.h"
 #include "experts.h"
 #include "fp8_block.h"
 #include "instances.h"
@@ -20,45 +34,115 @@
 namespace moe {
 namespace {
 
-typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
 constexpr int kStepRows = 64;
+constexpr int kCols = 256;                        // columns of either operand
+constexpr int kSliceBytes = kCols * 32;
+constexpr int kOperandBytes = 4 * kSliceBytes;    // one operand's step in LDS
 
-__device__ __forceinline__ int lds_piece(int c, int p) {
-  const int s = ((c >> 1) & 7) ^ ((c >> 4) & 3) ^ (((c >> 6) & 1) << 3);
-  return (c >> 1) * 256 + ((((c & 1) << 3) | p) ^ s) * 16;
+// Byte of piece g of column c within its slice.
+template <bool X>
+__device__ __forceinline__ int lds_place(int c, int g) {
+  const int h = c >> 3;
+  // bit 0 of s has to be the fourth bit in which the columns of 16 reading
+  // lanes differ: bit 3 of dy's, bit 4 of x's
+  const int s = X ? ((h >> 1) & 1) | ((h & 1) << 1) | (h & 12) : h & 15;
+  return (c >> 3) * 256 + ((2 * (c & 7) + g) ^ s) * 16;
 }
 
-// Eight rows of eight columns, widened: rows begin + 0..7 (zeros from `end`
-// on), columns c .. c+7 of a row of cp bytes.
+// The steps of an expert: 64 rows of one instance at a time, instances in
+// order.  Every lane of a wave steps alike.
+struct Steps {
+  int n_inst, expert;
+  int i0;            // instances from here on are in `mask`
+  uint64_t mask;
+  int row, end;      // rows < 2^31
+};
+__device__ __forceinline__ void steps_begin(Steps* s, const Instances& in, int expert) {
+  s->n_inst = __builtin_amdgcn_readfirstlane(instance_count(in));
+  s->expert = expert;
+  s->i0 = -64;
+  s->mask = 0ull;
+  s->row = s->end = 0;
+}
+// The next step's first row and its rows (0: no more).
+__device__ __forceinline__ void next_step(Steps* s, const Instances& in, int* row, int* rows) {
+  const int lane = threadIdx.x & 63;
+  while (s->row >= s->end) {
+    if (s->mask == 0ull) {
+      if (s->i0 + 64 >= s->n_inst) break;
+      s->i0 += 64;
+      s->mask = __ballot(s->i0 + lane < s->n_inst && in.expert[min(s->i0 + lane, s->n_inst - 1)] == s->expert);
+      continue;
+    }
+    const int i = s->i0 + __ffsll((unsigned long long)s->mask) - 1;
+    s->mask &= s->mask - 1;
+    Span sp;
+    const bool ok = instance_span(in, i, &sp);
+    s->row = __builtin_amdgcn_readfirstlane(ok ? (int)sp.begin : 0);
+    s->end = __builtin_amdgcn_readfirstlane(ok ? (int)sp.end : 0);
+  }
+  *row = s->row;
+  *rows = min(kStepRows, s->end - s->row);
+  s->row += kStepRows;
+  if (*rows <= 0) {
+    *rows = 0;
+    s->row = s->end;
+  }
+}
+
+// Eight rows of eight columns as loaded.
 struct Piece {
   u32x2 q[8];
   uint32_t s[8];
 };
-__device__ __forceinline__ void load_piece(Piece* p, const uint8_t* __restrict__ q, const uint8_t* __restrict__ scale,
-                                           int64_t begin, int64_t end, int64_t cp, int ns, int c) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const bool in = begin + j < end && c < cp;
-    p->q[j] = in ? *reinterpret_cast<const u32x2*>(q + (begin + j) * cp + c) : u32x2{0u, 0u};
-    p->s[j] = in ? scale[(begin + j) * ns + c / kBlk] : 127u;
-  }
-}
 
-// Transposed to LDS: for each column its eight rows as one 16-byte piece.
-__device__ __forceinline__ void store_piece(const Piece& p, unsigned char* lds, int c, int piece) {
-  float f[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(p.s[j] << 23);  // 255 gives NaN for the whole block
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t w[8][2];  // [row][columns 4h, 4h+1 | 4h+2, 4h+3]
+__global__ __launch_bounds__(256, 1) void wgrad_kernel(Instances in, const uint8_t* __restrict__ dy,
+                                                       const uint8_t* __restrict__ dys, const uint8_t* __restrict__ x,
+                                                       const uint8_t* __restrict__ xs, int n, int k,
+                                                       uint16_t* __restrict__ dw, int32_t* __restrict__ status) {
+#ifdef __HIP_DEVICE_COMPILE__
+  __shared__ __align__(256) unsigned char x0_s[kOperandBytes];
+  __shared__ __align__(256) unsigned char y0_s[kOperandBytes];
+  __shared__ __align__(256) unsigned char x1_s[kOperandBytes];
+  __shared__ __align__(256) unsigned char y1_s[kOperandBytes];
+  if (blockIdx.x == 0) check_instances(in, status);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ntk = (k + kCols - 1) / kCols, ntn = (n + kCols - 1) / kCols;
+  const int tk = blockIdx.x % ntk, rest = blockIdx.x / ntk;
+  const int tn = rest % ntn, e = rest / ntn;
+  const int nbn = (n + kBlk - 1) / kBlk, nbk = (k + kBlk - 1) / kBlk;
+  const int nsn = (nbn + 3) / 4 * 4, nsk = (nbk + 3) / 4 * 4;
+  const int np = nbn * kBlk, kp = nbk * kBlk;
+  // this thread's piece of either operand: columns 8 c8 .. of the tile, rows 8 rg .. of the step
+  const int c8 = threadIdx.x & 31, rg = threadIdx.x >> 5;
+  const uint32_t off_x = (uint32_t)(8 * rg * kp + tk * kCols + 8 * c8), off_y = (uint32_t)(8 * rg * np + tn * kCols + 8 * c8);
+  const uint32_t soff_x = (uint32_t)(8 * rg * nsk + (tk * kCols + 8 * c8) / kBlk);
+  const uint32_t soff_y = (uint32_t)(8 * rg * nsn + (tn * kCols + 8 * c8) / kBlk);
+  // Past the step's rows the descriptor ends: values and scales there are 0.
+  // Columns past the row's end are some other row's; nothing stores them.
+  auto load = [&](Piece* p, const uint8_t* q, const uint8_t* scale, int row, int rows, int cp, int ns, uint32_t off,
+                  uint32_t soff) {
+    row = __builtin_amdgcn_readfirstlane(row);  // the same in every lane, which the compiler cannot see
+    rows = __builtin_amdgcn_readfirstlane(rows);
+    const auto buf = buffer_of(q + (int64_t)row * cp, (uint32_t)rows * (uint32_t)cp);
+    const auto sbuf = buffer_of(scale + (int64_t)row * ns, (uint32_t)(rows * ns));
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      w[j][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p.q[j][h], f[j], false));
-      w[j][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p.q[j][h], f[j], true));
+      p->q[j] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(buf, off + (uint32_t)(j * cp), 0, 0));
+      p->s[j] = __builtin_amdgcn_raw_buffer_load_b8(sbuf, soff + (uint32_t)(j * ns), 0, 0);
+    }
+  };
+  // columns 4h .. 4h+3 of a piece, widened, to LDS
+  auto widen = [&](const Piece& p, unsigned char* lds, bool is_x, int h) {
+    uint32_t w[8][2];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float f = __uint_as_float(p.s[j] << 23);  // 255 gives NaN for the whole block
+      w[j][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p.q[j][h], f, false));
+      w[j][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p.q[j][h], f, true));
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -66,117 +150,135 @@ __device__ __forceinline__ void store_piece(const Piece& p, unsigned char* lds, 
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         o[j] = __builtin_amdgcn_perm(w[2 * j + 1][i / 2], w[2 * j][i / 2], i & 1 ? 0x07060302u : 0x05040100u);
-      *reinterpret_cast<u32x4*>(lds + lds_piece(c + 4 * h + i, piece)) = o;
+      const int c = 8 * c8 + 4 * h + i;
+      const int at = (rg >> 1) * kSliceBytes + (is_x ? lds_place<true>(c, rg & 1) : lds_place<false>(c, rg & 1));
+      *reinterpret_cast<u32x4*>(lds + at) = o;
     }
+  };
+  const int wk = (wave & 1) * 128, wn = (wave >> 1) * 128;
+  const int r = lane & 31, g = lane >> 5;
+  int at_x[4], at_y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    at_x[i] = lds_place<true>(wk + 32 * i + 16 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3), g);
+    at_y[i] = lds_place<false>(wn + 32 * i + r, g);
   }
-}
-
-// A 128 x 128 piece of dw[e] per workgroup of four waves, 64 x 64 each.
-constexpr int kTile128 = 128;
-__global__ __launch_bounds__(256) void wgrad_kernel(Instances in, const uint8_t* __restrict__ dy,
-                                                    const uint8_t* __restrict__ dys, const uint8_t* __restrict__ x,
-                                                    const uint8_t* __restrict__ xs, int n, int k,
-                                                    uint16_t* __restrict__ dw, int32_t* __restrict__ status) {
-  __shared__ __align__(16) unsigned char a_s[kTile128 * kStepRows * 2];  // columns of x
-  __shared__ __align__(16) unsigned char b_s[kTile128 * kStepRows * 2];  // columns of dy
-  __shared__ int list[kMaxE + kMaxB];
-  __shared__ int list_n;
-  if (blockIdx.x == 0) check_instances(in, status);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int ntk = (k + kTile128 - 1) / kTile128, ntn = (n + kTile128 - 1) / kTile128;
-  const int tk = blockIdx.x % ntk, rest = blockIdx.x / ntk;
-  const int tn = rest % ntn, e = rest / ntn;
-  const int n_inst = instance_count(in);
-  if (wave == 0) {
-    int m = 0;
-    for (int i0 = 0; i0 < n_inst; i0 += 64) {
-      const bool hit = i0 + lane < n_inst && in.expert[i0 + lane] == e;
-      const uint64_t bits = __ballot(hit);
-      if (hit) list[m + __popcll(bits & ((1ull << lane) - 1ull))] = i0 + lane;
-      m += __popcll(bits);
+  struct Slice {
+    v8bf x[4], y[4];
+  };
+  auto read = [&](Slice* f, const unsigned char* x_s, const unsigned char* y_s, int slice) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f->x[i] = *reinterpret_cast<const v8bf*>(x_s + at_x[i] + slice * kSliceBytes);
+      f->y[i] = *reinterpret_cast<const v8bf*>(y_s + at_y[i] + slice * kSliceBytes);
     }
-    if (lane == 0) list_n = m;
-  }
-  __syncthreads();
-  const int nbn = (n + kBlk - 1) / kBlk, nbk = (k + kBlk - 1) / kBlk;
-  const int nsn = (nbn + 3) / 4 * 4, nsk = (nbk + 3) / 4 * 4;
-  const int64_t np = (int64_t)nbn * kBlk, kp = (int64_t)nbk * kBlk;
-  // thread: columns 8 c8 .. of the tile, rows 8 rg .. of the step, for rg and rg + ...
-  const int c8 = threadIdx.x % 16, rg0 = threadIdx.x / 16;
-  const int wk = (wave & 1) * 64, wn = (wave >> 1) * 64;
-  v4f acc[4][4];
+  };
+  v16f acc[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0, 0, 0, 0};
-  const int m = list_n;
-  for (int q = 0; q < m; ++q) {
-    Span sp;
-    if (!instance_span(in, list[q], &sp)) continue;
-    for (int64_t r0 = sp.begin; r0 < sp.end; r0 += kStepRows) {
-      {
-        // 16 column groups x 8 row groups for each operand: the first half of the threads takes x
-        const int rg = rg0 & 7;
-        const bool is_x = rg0 < 8;
-        Piece p;
-        if (is_x) load_piece(&p, x, xs, r0 + 8 * rg, sp.end, kp, nsk, tk * kTile128 + 8 * c8);
-        else load_piece(&p, dy, dys, r0 + 8 * rg, sp.end, np, nsn, tn * kTile128 + 8 * c8);
-        __syncthreads();
-        store_piece(p, is_x ? a_s : b_s, 8 * c8, rg);
-        __syncthreads();
-      }
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int s = 0; s < kStepRows / 32; ++s) {
-        v8bf a[4], b[4];
-        const int l16 = lane & 15, g = lane >> 4;
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
+  auto multiply = [&](const Slice& f) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int ca = wk + 16 * (l16 >> 2) + 4 * i + (l16 & 3);
-          a[i] = *reinterpret_cast<const v8bf*>(a_s + lds_piece(ca, 4 * s + g));
-          b[i] = *reinterpret_cast<const v8bf*>(b_s + lds_piece(wn + 16 * i + l16, 4 * s + g));
-        }
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
-      }
-    }
+      for (int j = 0; j < 4; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.x[i], f.y[j], acc[i][j], 0, 0, 0);
+  };
+  Steps steps;
+  steps_begin(&steps, in, e);
+  int row, rows;
+  next_step(&steps, in, &row, &rows);
+  if (rows > 0) {
+    Piece px, py;
+    auto load_step = [&]() {
+      load(&px, x, xs, row, rows, kp, nsk, off_x, soff_x);
+      load(&py, dy, dys, row, rows, np, nsn, off_y, soff_y);
+    };
+    load_step();
+    widen(px, x0_s, true, 0);
+    widen(px, x0_s, true, 1);
+    widen(py, y0_s, false, 0);
+    widen(py, y0_s, false, 1);
+    next_step(&steps, in, &row, &rows);
+    load_step();
+    __syncthreads();
+    Slice f0, f1;
+    read(&f0, x0_s, y0_s, 0);
+    // One step from (x_s, y_s); the next one's values, in px and py, go to
+    // (xn_s, yn_s).  `rows` of the next step are 0 when this is the last: its
+    // values are then zeros.
+    auto step = [&](unsigned char* x_s, unsigned char* y_s, unsigned char* xn_s, unsigned char* yn_s) {
+      const int have = rows;
+      int row2 = 0, rows2 = 0;
+      if (have > 0) next_step(&steps, in, &row2, &rows2);
+      read(&f1, x_s, y_s, 1);
+      widen(px, xn_s, true, 0);
+      multiply(f0);
+      read(&f0, x_s, y_s, 2);
+      widen(px, xn_s, true, 1);
+      multiply(f1);
+      load(&px, x, xs, row2, rows2, kp, nsk, off_x, soff_x);
+      read(&f1, x_s, y_s, 3);
+      widen(py, yn_s, false, 0);
+      multiply(f0);
+      widen(py, yn_s, false, 1);
+      load(&py, dy, dys, row2, rows2, np, nsn, off_y, soff_y);
+      __syncthreads();
+      read(&f0, xn_s, yn_s, 0);
+      multiply(f1);
+      row = row2;
+      rows = rows2;
+      return have;  // rows that now lie in (xn_s, yn_s)
+    };
+    // two steps a round, without a way out between them (it would have the
+    // sums copied); behind an odd number of steps the second adds zeros
+    int left;
+    do {
+      step(x0_s, y0_s, x1_s, y1_s);
+      left = step(x1_s, y1_s, x0_s, y0_s);
+    } while (left > 0);
   }
-  const int l16 = lane & 15, g = lane >> 4;
   const bool vec = k % 8 == 0 && ((uintptr_t)dw & 15) == 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int row = tn * kTile128 + wn + 16 * j + l16;
-    const int col = tk * kTile128 + wk + 16 * g;
-    if (row >= n) continue;
-    uint16_t* dst = dw + ((int64_t)e * n + row) * k + col;
+    const int c = tn * kCols + wn + 32 * j + r;
+    if (c >= n) continue;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      u32x4 o;
+    for (int i = 0; i < 4; ++i) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        o[2 * i] = pack_bf16(acc[2 * h + i][j][0], acc[2 * h + i][j][1]);
-        o[2 * i + 1] = pack_bf16(acc[2 * h + i][j][2], acc[2 * h + i][j][3]);
-      }
-      if (vec && col + 8 * h + 8 <= k) {
-        *reinterpret_cast<u32x4*>(dst + 8 * h) = o;
-      } else {
+      for (int h = 0; h < 2; ++h) {  // eight consecutive columns
+        const int col = tk * kCols + wk + 32 * i + 16 * g + 8 * h;
+        if (col >= k) continue;
+        uint16_t* dst = dw + ((int64_t)e * n + c) * k + col;
+        u32x4 o;
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          if (col + 8 * h + c < k) dst[8 * h + c] = (uint16_t)(o[c / 2] >> (16 * (c & 1)));
+        for (int q = 0; q < 4; ++q) o[q] = pack_bf16(acc[i][j][8 * h + 2 * q], acc[i][j][8 * h + 2 * q + 1]);
+        if (vec) {
+          *reinterpret_cast<u32x4*>(dst) = o;
+        } else {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (col + q < k) dst[q] = (uint16_t)(o[q / 2] >> (16 * (q & 1)));
+        }
       }
     }
   }
+#endif
 }
 
 }  // namespace
 
+int64_t wgrad_tiles(const Instances& in, int32_t n, int32_t k) {
+  return (int64_t)in.E * ((n + kCols - 1) / kCols) * ((k + kCols - 1) / kCols);
+}
+
 hipError_t launch_wgrad(const Instances& in, const uint8_t* dy, const uint8_t* dys, const uint8_t* x,
                         const uint8_t* xs, int32_t n, int32_t k, uint16_t* dw, int32_t* status, hipStream_t st) {
-  const int64_t tiles = (int64_t)in.E * ((n + kTile128 - 1) / kTile128) * ((k + kTile128 - 1) / kTile128);
-  if (tiles >= (int64_t)1 << 24) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(wgrad_kernel, dim3((unsigned)tiles), dim3(256), 0, st, in, dy, dys, x, xs, n, k, dw, status);
+  hipLaunchKernelGGL(wgrad_kernel, dim3((unsigned)wgrad_tiles(in, n, k)), dim3(256), 0, st, in, dy, dys, x, xs, n, k,
+                     dw, status);
   return hipGetLastError();
 }
 
