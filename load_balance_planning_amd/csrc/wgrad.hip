@@ -187,58 +187,77 @@ __global__ __launch_bounds__(256, 1) void wgrad_kernel(Instances in, const uint8
       for (int j = 0; j < 4; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.x[i], f.y[j], acc[i][j], 0, 0, 0);
   };
+  // a slice's products with the other work between them: eight reads, then the
+  // writes, three vector instructions and `loads` loads to a product
+  auto spread = [&](int loads) {
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if (q < 8) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
+      if (q >= 4 && q % 3 == 0) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+      if (loads == 1) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      if (loads == 2) __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);
+    }
+  };
   Steps steps;
   steps_begin(&steps, in, e);
   int row, rows;
   next_step(&steps, in, &row, &rows);
   if (rows > 0) {
-    Piece px, py;
-    auto load_step = [&]() {
-      load(&px, x, xs, row, rows, kp, nsk, off_x, soff_x);
-      load(&py, dy, dys, row, rows, np, nsn, off_y, soff_y);
+    struct Pieces {
+      Piece x, y;
     };
-    load_step();
-    widen(px, x0_s, true, 0);
-    widen(px, x0_s, true, 1);
-    widen(py, y0_s, false, 0);
-    widen(py, y0_s, false, 1);
+    auto load_step = [&](Pieces* p) {
+      load(&p->x, x, xs, row, rows, kp, nsk, off_x, soff_x);
+      load(&p->y, dy, dys, row, rows, np, nsn, off_y, soff_y);
+    };
+    Pieces pa, pb;
+    load_step(&pa);
     next_step(&steps, in, &row, &rows);
-    load_step();
+    load_step(&pb);
+    int have = rows;  // rows of the step whose values are in registers
+    widen(pa.x, x0_s, true, 0);
+    widen(pa.x, x0_s, true, 1);
+    widen(pa.y, y0_s, false, 0);
+    widen(pa.y, y0_s, false, 1);
     __syncthreads();
     Slice f0, f1;
     read(&f0, x0_s, y0_s, 0);
-    // One step from (x_s, y_s); the next one's values, in px and py, go to
-    // (xn_s, yn_s).  `rows` of the next step are 0 when this is the last: its
-    // values are then zeros.
-    auto step = [&](unsigned char* x_s, unsigned char* y_s, unsigned char* xn_s, unsigned char* yn_s) {
-      const int have = rows;
-      int row2 = 0, rows2 = 0;
-      if (have > 0) next_step(&steps, in, &row2, &rows2);
+    // One step from (x_s, y_s); the next one's values, in p, go to (xn_s,
+    // yn_s), and those of the step after are loaded to pn.  Past the last step
+    // the values are zeros.  Returns the rows that then lie in (xn_s, yn_s).
+    auto step = [&](unsigned char* x_s, unsigned char* y_s, unsigned char* xn_s, unsigned char* yn_s, const Pieces& p,
+                    Pieces* pn) {
+      const int ready = have;
+      if (have > 0) next_step(&steps, in, &row, &rows);
+      load_step(pn);
       read(&f1, x_s, y_s, 1);
-      widen(px, xn_s, true, 0);
+      widen(p.x, xn_s, true, 0);
       multiply(f0);
+      spread(2);
       read(&f0, x_s, y_s, 2);
-      widen(px, xn_s, true, 1);
+      widen(p.x, xn_s, true, 1);
       multiply(f1);
-      load(&px, x, xs, row2, rows2, kp, nsk, off_x, soff_x);
+      spread(0);
       read(&f1, x_s, y_s, 3);
-      widen(py, yn_s, false, 0);
+      widen(p.y, yn_s, false, 0);
+      widen(p.y, yn_s, false, 1);
       multiply(f0);
-      widen(py, yn_s, false, 1);
-      load(&py, dy, dys, row2, rows2, np, nsn, off_y, soff_y);
+      spread(0);
       __syncthreads();
       read(&f0, xn_s, yn_s, 0);
       multiply(f1);
-      row = row2;
-      rows = rows2;
-      return have;  // rows that now lie in (xn_s, yn_s)
+      spread(0);
+      have = rows;
+      return ready;
     };
     // two steps a round, without a way out between them (it would have the
     // sums copied); behind an odd number of steps the second adds zeros
     int left;
     do {
-      step(x0_s, y0_s, x1_s, y1_s);
-      left = step(x1_s, y1_s, x0_s, y0_s);
+      step(x0_s, y0_s, x1_s, y1_s, pb, &pa);
+      left = step(x1_s, y1_s, x0_s, y0_s, pa, &pb);
     } while (left > 0);
   }
   const bool vec = k % 8 == 0 && ((uintptr_t)dw & 15) == 0;
