@@ -4,24 +4,25 @@
 // The sum runs over rows, along which both operands change scale, so the
 // scaled 8-bit instruction does not apply; the values are widened to bf16 --
 // e4m3 times a power of two is a bf16 value exactly, down to bf16's subnormals
-// -- and multiplied by the bf16 instruction.  It wants eight consecutive rows
-// of one column in a lane, memory has columns next to each other: a thread
-// loads an 8 x 8 piece, widens it, pairs rows in registers and writes eight
-// 16-byte pieces (eight rows of a column) to LDS.
+// -- and multiplied by the bf16 instruction.  It wants eight rows of one column
+// in a lane, memory has columns next to each other: LDS holds the values as
+// they come, rows of 256 columns, and the transposing LDS read hands every 16
+// lanes four rows of 16 columns, a column to a lane.  (Transposing in registers
+// on the way into LDS took twice the vector instructions: 1.14 against
+// @@DENSE@@ PFLOP/s on one dense 8192 cubed.)
 //
 // 256 x 256 of dw[e] per workgroup of four waves, 128 x 128 each, in steps of
-// 64 rows: 2048 cycles of products against 1024 of LDS reads, 512 of writes and
-// some 800 of widening, which a wave issues between its products.  A step is
-// four slices of 16 rows.  While a slice's products run, the next slice's
-// operands are read, and a quarter of the next step's values (loaded a step
-// earlier) is widened and written to the other half of LDS.  The last slice
-// runs behind the step's only barrier.
+// 64 rows: 2048 cycles of products, and some 4 other instructions to a product
+// that a wave issues in its shadow.  A step is four slices of 16 rows.  While a
+// slice's products run, the next slice's operands are read, and part of the
+// next step's values (loaded a step earlier) is widened and written to the
+// other half of LDS.  The last slice runs behind the step's only barrier.
 //
-// LDS: [slice][column][2 pieces], 32 bytes a column.  Within 256 bytes (eight
-// columns), piece g of column c lies at place (2 (c % 8) + g) ^ s(c), with s
-// from bits 3 to 6 of c, so that 16 lanes that write (columns 8 apart) and 16
-// that read (consecutive columns of dy; 16a + 4i + j of x, see below) find 16
-// different places.
+// LDS rows are 512 bytes, 16 units of 32 (16 columns).  Unit u of row R lies at
+// place u ^ 2 (R % 4): the four rows by 32 columns that 32 lanes read together
+// are then eight different units of 256 bytes.  Units 8 to 15 have their two
+// 16-byte halves exchanged, so that 16 lanes' writes, one half each of a row's
+// units, go to 16 different places of 256 bytes.
 //
 // x's columns are the instruction's rows, dy's its columns: a lane's 16
 // results are then 16 consecutive columns of x (matrix row 8a + 4h + j stands
@@ -39,18 +40,9 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 constexpr int kStepRows = 64;
 constexpr int kCols = 256;                        // columns of either operand
-constexpr int kSliceBytes = kCols * 32;
-constexpr int kOperandBytes = 4 * kSliceBytes;    // one operand's step in LDS
-
-// Byte of piece g of column c within its slice.
-template <bool X>
-__device__ __forceinline__ int lds_place(int c, int g) {
-  const int h = c >> 3;
-  // bit 0 of s has to be the fourth bit in which the columns of 16 reading
-  // lanes differ: bit 3 of dy's, bit 4 of x's
-  const int s = X ? ((h >> 1) & 1) | ((h & 1) << 1) | (h & 12) : h & 15;
-  return (c >> 3) * 256 + ((2 * (c & 7) + g) ^ s) * 16;
-}
+constexpr int kRowBytes = kCols * 2;
+constexpr int kSliceBytes = 16 * kRowBytes;
+constexpr int kOperandBytes = kStepRows * kRowBytes;  // one operand's step in LDS
 
 // The steps of an expert: 64 rows of one instance at a time, instances in
 // order.  Every lane of a wave steps alike.
@@ -93,10 +85,10 @@ __device__ __forceinline__ void next_step(Steps* s, const Instances& in, int* ro
   }
 }
 
-// Eight rows of eight columns as loaded.
+// Four rows of 16 columns as loaded.
 struct Piece {
-  u32x2 q[8];
-  uint32_t s[8];
+  u32x4 q[4];
+  uint32_t s[4];
 };
 
 __global__ __launch_bounds__(256, 1) void wgrad_kernel(Instances in, const uint8_t* __restrict__ dy,
@@ -116,11 +108,11 @@ __global__ __launch_bounds__(256, 1) void wgrad_kernel(Instances in, const uint8
   const int nbn = (n + kBlk - 1) / kBlk, nbk = (k + kBlk - 1) / kBlk;
   const int nsn = (nbn + 3) / 4 * 4, nsk = (nbk + 3) / 4 * 4;
   const int np = nbn * kBlk, kp = nbk * kBlk;
-  // this thread's piece of either operand: columns 8 c8 .. of the tile, rows 8 rg .. of the step
-  const int c8 = threadIdx.x & 31, rg = threadIdx.x >> 5;
-  const uint32_t off_x = (uint32_t)(8 * rg * kp + tk * kCols + 8 * c8), off_y = (uint32_t)(8 * rg * np + tn * kCols + 8 * c8);
-  const uint32_t soff_x = (uint32_t)(8 * rg * nsk + (tk * kCols + 8 * c8) / kBlk);
-  const uint32_t soff_y = (uint32_t)(8 * rg * nsn + (tn * kCols + 8 * c8) / kBlk);
+  // this thread's piece of either operand: columns 16 c16 .. of the tile, rows 4 rq .. of the step
+  const int c16 = threadIdx.x & 15, rq = threadIdx.x >> 4;
+  const uint32_t off_x = (uint32_t)(4 * rq * kp + tk * kCols + 16 * c16), off_y = (uint32_t)(4 * rq * np + tn * kCols + 16 * c16);
+  const uint32_t soff_x = (uint32_t)(4 * rq * nsk + (tk * kCols + 16 * c16) / kBlk);
+  const uint32_t soff_y = (uint32_t)(4 * rq * nsn + (tn * kCols + 16 * c16) / kBlk);
   // Past the step's rows the descriptor ends: values and scales there are 0.
   // Columns past the row's end are some other row's; nothing stores them.
   auto load = [&](Piece* p, const uint8_t* q, const uint8_t* scale, int row, int rows, int cp, int ns, uint32_t off,
@@ -130,47 +122,60 @@ __global__ __launch_bounds__(256, 1) void wgrad_kernel(Instances in, const uint8
     const auto buf = buffer_of(q + (int64_t)row * cp, (uint32_t)rows * (uint32_t)cp);
     const auto sbuf = buffer_of(scale + (int64_t)row * ns, (uint32_t)(rows * ns));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      p->q[j] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(buf, off + (uint32_t)(j * cp), 0, 0));
+    for (int j = 0; j < 4; ++j) {
+      p->q[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(buf, off + (uint32_t)(j * cp), 0, 0));
       p->s[j] = __builtin_amdgcn_raw_buffer_load_b8(sbuf, soff + (uint32_t)(j * ns), 0, 0);
     }
   };
-  // columns 4h .. 4h+3 of a piece, widened, to LDS
-  auto widen = [&](const Piece& p, unsigned char* lds, bool is_x, int h) {
-    uint32_t w[8][2];
+  // rows 2h and 2h + 1 of a piece, widened, to LDS
+  const int swap = (c16 >> 3) & 1;
+  auto widen = [&](const Piece& p, unsigned char* lds, int h) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 2 * h; j < 2 * h + 2; ++j) {
       const float f = __uint_as_float(p.s[j] << 23);  // 255 gives NaN for the whole block
-      w[j][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p.q[j][h], f, false));
-      w[j][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p.q[j][h], f, true));
-    }
+      u32x4 w[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      u32x4 o;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        o[j] = __builtin_amdgcn_perm(w[2 * j + 1][i / 2], w[2 * j][i / 2], i & 1 ? 0x07060302u : 0x05040100u);
-      const int c = 8 * c8 + 4 * h + i;
-      const int at = (rg >> 1) * kSliceBytes + (is_x ? lds_place<true>(c, rg & 1) : lds_place<false>(c, rg & 1));
-      *reinterpret_cast<u32x4*>(lds + at) = o;
+      for (int i = 0; i < 4; ++i) {
+        w[i / 2][2 * (i & 1)] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p.q[j][i], f, false));
+        w[i / 2][2 * (i & 1) + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p.q[j][i], f, true));
+      }
+      unsigned char* row = lds + (4 * rq + j) * kRowBytes + (c16 ^ (2 * j)) * 32;
+      *reinterpret_cast<u32x4*>(row + 16 * swap) = w[0];
+      *reinterpret_cast<u32x4*>(row + 16 - 16 * swap) = w[1];
     }
   };
   const int wk = (wave & 1) * 128, wn = (wave >> 1) * 128;
   const int r = lane & 31, g = lane >> 5;
+  // Reads: lane 4t + q of 16 lends the address of row t, four columns, which
+  // go to lanes 4q .. 4q + 3.  dy's columns stay in order; x's are taken so that
+  // matrix row 8a + 4h + j is column 16h + 4a + j.
+  const int t = (lane >> 2) & 3, q = lane & 3, half = (lane >> 4) & 1;
   int at_x[4], at_y[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    at_x[i] = lds_place<true>(wk + 32 * i + 16 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3), g);
-    at_y[i] = lds_place<false>(wn + 32 * i + r, g);
+    const int row = (8 * g + t) * kRowBytes;
+    at_x[i] = row + (((wk + 32 * i) / 16 + (q & 1)) ^ (2 * t)) * 32 + (((8 * half + 4 * (q >> 1)) * 2) ^ (wk / 8));
+    at_y[i] = row + (((wn + 32 * i) / 16 + half) ^ (2 * t)) * 32 + ((4 * q * 2) ^ (wn / 8));
   }
   struct Slice {
     v8bf x[4], y[4];
   };
+  auto read8 = [&](const unsigned char* s) {  // rows 8g .. 8g + 7 of the slice, this lane's column
+    typedef short v4s __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) v4s* lds4;
+    union {
+      v8bf v;
+      v4s h[2];
+    } u;
+    u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)s);
+    u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(s + 4 * kRowBytes));
+    return u.v;
+  };
   auto read = [&](Slice* f, const unsigned char* x_s, const unsigned char* y_s, int slice) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      f->x[i] = *reinterpret_cast<const v8bf*>(x_s + at_x[i] + slice * kSliceBytes);
-      f->y[i] = *reinterpret_cast<const v8bf*>(y_s + at_y[i] + slice * kSliceBytes);
+      f->x[i] = read8(x_s + at_x[i] + slice * kSliceBytes);
+      f->y[i] = read8(y_s + at_y[i] + slice * kSliceBytes);
     }
   };
   v16f acc[4][4];
@@ -187,17 +192,16 @@ __global__ __launch_bounds__(256, 1) void wgrad_kernel(Instances in, const uint8
       for (int j = 0; j < 4; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.x[i], f.y[j], acc[i][j], 0, 0, 0);
   };
-  // a slice's products with the other work between them: eight reads, then the
-  // writes, three vector instructions and `loads` loads to a product
-  auto spread = [&](int loads) {
+  // a slice's products with the other work between them: a read each, the
+  // writes and loads spread out, vector instructions
+  auto spread = [&](bool loads) {
 #pragma unroll
-    for (int q = 0; q < 16; ++q) {
+    for (int i = 0; i < 16; ++i) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      if (q < 8) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
-      if (q >= 4 && q % 3 == 0) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
-      if (loads == 1) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-      if (loads == 2) __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+      if (i % 3 == 2) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+      if (loads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
     }
   };
   Steps steps;
@@ -217,10 +221,10 @@ __global__ __launch_bounds__(256, 1) void wgrad_kernel(Instances in, const uint8
     next_step(&steps, in, &row, &rows);
     load_step(&pb);
     int have = rows;  // rows of the step whose values are in registers
-    widen(pa.x, x0_s, true, 0);
-    widen(pa.x, x0_s, true, 1);
-    widen(pa.y, y0_s, false, 0);
-    widen(pa.y, y0_s, false, 1);
+    widen(pa.x, x0_s, 0);
+    widen(pa.x, x0_s, 1);
+    widen(pa.y, y0_s, 0);
+    widen(pa.y, y0_s, 1);
     __syncthreads();
     Slice f0, f1;
     read(&f0, x0_s, y0_s, 0);
@@ -233,22 +237,22 @@ __global__ __launch_bounds__(256, 1) void wgrad_kernel(Instances in, const uint8
       if (have > 0) next_step(&steps, in, &row, &rows);
       load_step(pn);
       read(&f1, x_s, y_s, 1);
-      widen(p.x, xn_s, true, 0);
+      widen(p.x, xn_s, 0);
       multiply(f0);
-      spread(2);
+      spread(true);
       read(&f0, x_s, y_s, 2);
-      widen(p.x, xn_s, true, 1);
+      widen(p.x, xn_s, 1);
       multiply(f1);
-      spread(0);
+      spread(false);
       read(&f1, x_s, y_s, 3);
-      widen(p.y, yn_s, false, 0);
-      widen(p.y, yn_s, false, 1);
+      widen(p.y, yn_s, 0);
+      widen(p.y, yn_s, 1);
       multiply(f0);
-      spread(0);
+      spread(false);
       __syncthreads();
       read(&f0, xn_s, yn_s, 0);
       multiply(f1);
-      spread(0);
+      spread(false);
       have = rows;
       return ready;
     };
