@@ -20,9 +20,9 @@
 //
 // LDS rows are 512 bytes, 16 units of 32 (16 columns).  Unit u of row R lies at
 // place u ^ 2 (R % 4): the four rows by 32 columns that 32 lanes read together
-// are then eight different units of 256 bytes.  Units 8 to 15 have their two
-// 16-byte halves exchanged, so that 16 lanes' writes, one half each of a row's
-// units, go to 16 different places of 256 bytes.
+// are then eight different units of 256 bytes.  Units with bit 2 set have their
+// 16-byte halves exchanged, so that eight lanes' writes, one half each of
+// consecutive units, go to eight different places of 128 bytes.
 //
 // x's columns are the instruction's rows, dy's its columns: a lane's 16
 // results are then 16 consecutive columns of x (matrix row 8a + 4h + j stands
@@ -128,7 +128,7 @@ __global__ __launch_bounds__(256, 1) void wgrad_kernel(Instances in, const uint8
     }
   };
   // rows 2h and 2h + 1 of a piece, widened, to LDS
-  const int swap = (c16 >> 3) & 1;
+  const int swap = (c16 >> 2) & 1;
   auto widen = [&](const Piece& p, unsigned char* lds, int h) {
 #pragma unroll
     for (int j = 2 * h; j < 2 * h + 2; ++j) {
@@ -154,8 +154,8 @@ __global__ __launch_bounds__(256, 1) void wgrad_kernel(Instances in, const uint8
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = (8 * g + t) * kRowBytes;
-    at_x[i] = row + (((wk + 32 * i) / 16 + (q & 1)) ^ (2 * t)) * 32 + (((8 * half + 4 * (q >> 1)) * 2) ^ (wk / 8));
-    at_y[i] = row + (((wn + 32 * i) / 16 + half) ^ (2 * t)) * 32 + ((4 * q * 2) ^ (wn / 8));
+    at_x[i] = row + (((wk + 32 * i) / 16 + (q & 1)) ^ (2 * t)) * 32 + (((8 * half + 4 * (q >> 1)) * 2) ^ (16 * (i >> 1)));
+    at_y[i] = row + (((wn + 32 * i) / 16 + half) ^ (2 * t)) * 32 + ((4 * q * 2) ^ (16 * (i >> 1)));
   }
   struct Slice {
     v8bf x[4], y[4];
