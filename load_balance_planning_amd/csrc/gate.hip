@@ -9,16 +9,19 @@
 //
 // P lanes hold a token, V consecutive logits each, so a row is read once into
 // registers.  The selection is route.hip's: tau, the k-th largest of the lane
-// maxima, admits about k candidates; they go to LDS and each one's rank among
-// them is its output position.
+// maxima, admits about k candidates; up to 2 P of them go to LDS and each one's
+// rank among them is its output position.  (With room for P candidates alone,
+// 4 % of the tokens of a 256-expert top-8 router had too many, and a decoding
+// step waited 40 us for them.)
 //
 // Choices are compared as in 64 bits without computing them in 64 bits: the
 // fp32 choice of an expert is off by at most half of `margin`, so two that
-// differ by more are in the right order.  Where two candidates, or two groups
-// across the cut, lie closer (about one token in a hundred on DeepSeek-V3's
-// router), the token's lanes evaluate only those candidates, or the group
-// values, in 64 bits.  A candidate list that does not fit the lanes (long ties)
-// takes k rounds of a maximum over 64-bit choices.
+// differ by more are in the right order, and equal inputs are a tie.  Where two
+// candidates, or two groups across the cut, lie closer (about one token in a
+// hundred), the token's lanes evaluate only those candidates, or the group
+// values, in 64 bits.  Where there are more candidates (long ties: a row of
+// equal or of masked logits), the token takes rounds of a maximum, first over
+// the fp32 choices, and over 64-bit ones if two picks lie too close.
 #include <math.h>
 
 #include "experts.h"
@@ -59,20 +62,20 @@ __device__ __forceinline__ double score64(bool softmax, float x, float m, double
   return softmax ? exp((double)x - (double)m) / sum : 1.0 / (1.0 + exp(-(double)x));
 }
 
-// LDS words of one token in gate_kernel: its candidates, and with groups its
-// choices, group values in 32 and 64 bits.
+// LDS of gate_kernel: presence masks; per token 2 P candidates (64-bit choice,
+// choice, logit, expert) and P selected experts with their logits; with groups
+// a row of choices (8 words apart, for other banks) and the group values.
 __host__ __device__ inline int choice_stride(int E) { return E + 8; }
-
 struct GateLds {
-  size_t mask, cand, choice, group, total;
+  size_t cand, chosen, choice, group, total;
 };
 template <int P>
 __host__ __device__ inline GateLds gate_lds(int E, int n_group, bool prev) {
   constexpr int TPW = gate_tpw<P>();
   GateLds l;
-  l.mask = 0;
   l.cand = sizeof(uint64_t) * (size_t)E * (prev ? 2 : 1);
-  l.choice = l.cand + (size_t)TPW * P * 24;  // 64-bit choice, choice, logit, expert (and 4 bytes over)
+  l.chosen = l.cand + (size_t)TPW * 2 * P * 20;
+  l.choice = l.chosen + (size_t)TPW * P * 8;
   const size_t choices = n_group > 1 ? sizeof(float) * (size_t)TPW * choice_stride(E) : 0;
   l.group = (l.choice + choices + 7) / 8 * 8;
   l.total = l.group + (n_group > 1 ? (size_t)TPW * n_group * sizeof(double) : 0);
@@ -107,11 +110,14 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
   const int grp_base = (tid & 63) - lane;
   const uint64_t grp_bits = (P == 64 ? ~0ull : ((1ull << P) - 1ull)) << grp_base;
   const int i = tid / P;
-  // this token's candidates: [P] of each
-  double* cand64 = reinterpret_cast<double*>(smem_gate + lay.cand) + (size_t)i * P;
-  float* cand_c = reinterpret_cast<float*>(smem_gate + lay.cand + (size_t)TPW * P * 8) + (size_t)i * P;
-  float* cand_x = reinterpret_cast<float*>(smem_gate + lay.cand + (size_t)TPW * P * 12) + (size_t)i * P;
-  int* cand_e = reinterpret_cast<int*>(smem_gate + lay.cand + (size_t)TPW * P * 16) + (size_t)i * P;
+  // this token's candidates, [2 P] of each, and its selected experts
+  unsigned char* mine_s = smem_gate + lay.cand;
+  double* cand64 = reinterpret_cast<double*>(mine_s) + (size_t)i * 2 * P;
+  float* cand_c = reinterpret_cast<float*>(mine_s + (size_t)TPW * 2 * P * 8) + (size_t)i * 2 * P;
+  float* cand_x = reinterpret_cast<float*>(mine_s + (size_t)TPW * 2 * P * 12) + (size_t)i * 2 * P;
+  int* cand_e = reinterpret_cast<int*>(mine_s + (size_t)TPW * 2 * P * 16) + (size_t)i * 2 * P;
+  int* chosen_e = reinterpret_cast<int*>(smem_gate + lay.chosen) + (size_t)i * P;
+  float* chosen_x = reinterpret_cast<float*>(smem_gate + lay.chosen + (size_t)TPW * P * 4) + (size_t)i * P;
   const bool softmax = g.score == MOEX_SOFTMAX;
   const int k = d.k;
   bool bad = false;
@@ -202,20 +208,38 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
       float* ch = reinterpret_cast<float*>(smem_gate + lay.choice) + (size_t)i * choice_stride(d.E);
       double* gv64 = reinterpret_cast<double*>(smem_gate + lay.group) + (size_t)i * g.n_group;
       float* gv = reinterpret_cast<float*>(gv64);
+      const int lanes = per / V;  // lanes of a group, where groups are whole lanes
+      if (per % V == 0 && (lanes & (lanes - 1)) == 0) {
+        // the two largest of this lane's choices, then of the group's lanes
+        float a = c32[0], b = -INFINITY;
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (e0 + v < d.E) ch[e0 + v] = c32[v];
-      wave_lds_sync();
-      for (int q = lane; q < g.n_group; q += P) {
-        float a = -INFINITY, b = -INFINITY;
-        int at = q % per;  // lanes start at different places of their groups: other LDS banks
-        for (int j = 0; j < per; ++j) {
-          const float y = ch[q * per + at];
-          b = fmaxf(b, fminf(a, y));
-          a = fmaxf(a, y);
-          at = at + 1 == per ? 0 : at + 1;
+        for (int v = 1; v < V; ++v) {
+          b = fmaxf(b, fminf(a, c32[v]));
+          a = fmaxf(a, c32[v]);
         }
-        gv[q] = g.group_top == 2 ? a + b : a;
+        for (int off = 1; off < lanes; off <<= 1) {
+          const float oa = __shfl_xor(a, off), ob = __shfl_xor(b, off);
+          b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+          a = fmaxf(a, oa);
+        }
+        if ((lane & (lanes - 1)) == 0 && e0 < d.E) gv[e0 / per] = g.group_top == 2 ? a + b : a;
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (e0 + v < d.E) ch[e0 + v] = c32[v];
+        wave_lds_sync();
+        for (int q = lane; q < g.n_group; q += P) {
+          float a = -INFINITY, b = -INFINITY;
+          int at = q % per;  // lanes start at different places of their groups: other LDS banks
+#pragma unroll 4
+          for (int j = 0; j < per; ++j) {
+            const float y = ch[q * per + at];
+            b = fmaxf(b, fminf(a, y));
+            a = fmaxf(a, y);
+            at = at + 1 == per ? 0 : at + 1;
+          }
+          gv[q] = g.group_top == 2 ? a + b : a;
+        }
       }
       wave_lds_sync();
       bool unsure = false;
@@ -282,7 +306,22 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
     float omax = o32[0];
 #pragma unroll
     for (int v = 1; v < V; ++v) omax = fmaxf(omax, o32[v]);
-    const uint32_t sorted = group_sort_desc_u32<P>(order_key(__float_as_uint(omax)), lane);
+    uint32_t sorted = group_sort_desc_u32<P>(order_key(__float_as_uint(omax)), lane);
+    if (g.n_group > 1) {
+      // Kept groups leave some lanes without a choice, and the k-th largest
+      // maximum of the others admits too much: take each lane's two largest.
+      // The larger of the i-th maximum and the i-th smallest second are the P
+      // largest of them all.
+      float a = o32[0], b = -INFINITY;
+#pragma unroll
+      for (int v = 1; v < V; ++v) {
+        b = fmaxf(b, fminf(a, o32[v]));
+        a = fmaxf(a, o32[v]);
+      }
+      const uint32_t seconds = group_sort_desc_u32<P>(order_key(__float_as_uint(b)), lane);
+      sorted = max(sorted, (uint32_t)__shfl_xor((int)seconds, P - 1));
+      sorted = group_sort_desc_u32<P>(sorted, lane);
+    }
     const float kth = __uint_as_float(float_from_order_key((uint32_t)__shfl((int)sorted, grp_base + k - 1)));
     const float tau = bias ? kth - margin * (1.0f + fabsf(kth)) : kth;
     int mine = 0;
@@ -290,9 +329,8 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
     for (int v = 0; v < V; ++v) mine += e0 + v < d.E && o32[v] >= tau ? 1 : 0;
     const int incl = group_incl_scan<P>(mine, lane);
     const int total = group_last<P>(incl);
-    int rank = P, my_e = 0;  // this lane's expert and its place in the top-k
-    float my_x = 0.0f;
-    if (total <= P) {
+    auto same_inputs = [&](int ea, float xa, int eb, float xb) { return xa == xb && bias[ea] == bias[eb]; };
+    if (total <= 2 * P) {
       int w = incl - mine;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -304,78 +342,106 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
         }
       }
       wave_lds_sync();
-      const int at = lane < total ? lane : 0;
-      const float my_c = cand_c[at];
-      my_e = cand_e[at];
-      my_x = cand_x[at];
-      rank = 0;
       bool unsure = false;
-      for (int j = 0; j < total; ++j) {
-        const float cj = cand_c[j];
-        rank += cj > my_c || (cj == my_c && j < at) ? 1 : 0;  // candidates are in expert order
-        if (bias && j != at && fabsf(cj - my_c) <= margin * (1.0f + fminf(fabsf(cj), fabsf(my_c))))
-          unsure |= cand_x[j] != my_x || bias[cand_e[j]] != bias[my_e];  // equal inputs are a tie
+      for (int at = lane; at < total; at += P) {  // once, but for the few tokens with more than P
+        const float my_c = cand_c[at];
+        int rank = 0;
+        for (int j = 0; j < total; ++j) {
+          const float cj = cand_c[j];
+          rank += cj > my_c || (cj == my_c && j < at) ? 1 : 0;  // candidates are in expert order
+          if (bias && j != at && fabsf(cj - my_c) <= margin * (1.0f + fminf(fabsf(cj), fabsf(my_c))))
+            unsure |= !same_inputs(cand_e[j], cand_x[j], cand_e[at], cand_x[at]);
+        }
+        if (rank < k) {
+          chosen_e[rank] = cand_e[at];
+          chosen_x[rank] = cand_x[at];
+        }
       }
       if ((__ballot(unsure) & grp_bits) != 0ull) {
         need64();
-        double y = choice64(my_e);
-        if (my_c == -INFINITY) y = -INFINITY;  // outside the kept groups
-        cand64[lane] = y;
+        for (int at = lane; at < total; at += P)  // -infinity stays: outside the kept groups, or its bias
+          cand64[at] = cand_c[at] == -INFINITY ? -INFINITY : choice64(cand_e[at]);
         wave_lds_sync();
-        rank = 0;
-        for (int j = 0; j < total; ++j) rank += cand64[j] > y || (cand64[j] == y && j < at) ? 1 : 0;
+        for (int at = lane; at < total; at += P) {
+          const double y = cand64[at];
+          int rank = 0;
+          for (int j = 0; j < total; ++j) rank += cand64[j] > y || (cand64[j] == y && j < at) ? 1 : 0;
+          if (rank < k) {
+            chosen_e[rank] = cand_e[at];
+            chosen_x[rank] = cand_x[at];
+          }
+        }
       }
-      if (lane >= total) rank = P;
+      wave_lds_sync();
     } else {
-      // k rounds: each the largest choice left, ties to the lower expert
-      if (bias) need64();
+      // Rounds, each the largest left, ties to the lower expert; with a bias one
+      // more, to see whether the last pick is sure.  Taken experts' bits: V <= 32.
       uint32_t taken = 0u;
-      for (int j = 0; j < k; ++j) {
-        double best = -INFINITY;
-        int at = d.E;  // none
-        int q = e0 / per, left = (q + 1) * per - e0;
+      bool unsure = false;
+      float last_c = 0.0f, last_x = 0.0f;
+      int last_e = -1;
+      const int rounds = bias && k < d.E ? k + 1 : k;
+      for (int j = 0; j < rounds; ++j) {
+        uint64_t best = 0ull;
+#pragma unroll
         for (int v = 0; v < V; ++v) {
-          const int e = e0 + v;
-          if (e < d.E && ((taken >> v) & 1u) == 0u) {
-            double y = -INFINITY;
-            if (g.n_group == 1 || ((kept >> (q & 63)) & 1ull) != 0ull) {
-              if (bias) {
-                y = choice64(e);
-              } else {
-                const float xe = row[e];
-                y = xe != xe || (softmax && xe == INFINITY) ? -INFINITY : (double)xe;
-              }
-            }
+          const uint64_t key = ((uint64_t)order_key(__float_as_uint(o32[v])) << 32) | (uint32_t)(0x7fffffff - (e0 + v));
+          best = e0 + v < d.E && ((taken >> v) & 1u) == 0u && key > best ? key : best;
+        }
+        const uint64_t top = group_max_u64<P>(best);
+        const int e = 0x7fffffff - (int)(uint32_t)top;
+        if (e >= e0 && e < e0 + V) taken |= 1u << (e - e0);
+        const float ce = __uint_as_float(float_from_order_key((uint32_t)(top >> 32)));
+        if (j < k && lane == 0) chosen_e[j] = e;
+        if (bias) {
+          const float xe = row[e];
+          if (last_e >= 0 && fabsf(ce - last_c) <= margin * (1.0f + fminf(fabsf(ce), fabsf(last_c))))
+            unsure |= !same_inputs(e, xe, last_e, last_x);
+          last_c = ce;
+          last_x = xe;
+          last_e = e;
+        }
+      }
+      if ((__ballot(unsure) & grp_bits) != 0ull) {
+        need64();
+        taken = 0u;
+        for (int j = 0; j < k; ++j) {
+          double best = -INFINITY;
+          int at = d.E;  // none
+          for (int v = 0; v < V; ++v) {
+            const int e = e0 + v;
+            if (e >= d.E || ((taken >> v) & 1u) != 0u) continue;
+            const bool in = g.n_group == 1 || ((kept >> ((e / per) & 63)) & 1ull) != 0ull;
+            const double y = in ? choice64(e) : -INFINITY;
             if (y > best || at == d.E) {
               best = y;
               at = e;
             }
           }
-          if (--left == 0) {
-            ++q;
-            left = per;
-          }
-        }
 #pragma unroll
-        for (int off = P / 2; off >= 1; off >>= 1) {
-          const double ob = __shfl_xor(best, off);
-          const int oa = __shfl_xor(at, off);
-          if (oa < d.E && (at == d.E || ob > best || (ob == best && oa < at))) {
-            best = ob;
-            at = oa;
+          for (int off = P / 2; off >= 1; off >>= 1) {
+            const double ob = __shfl_xor(best, off);
+            const int oa = __shfl_xor(at, off);
+            if (oa < d.E && (at == d.E || ob > best || (ob == best && oa < at))) {
+              best = ob;
+              at = oa;
+            }
           }
-        }
-        if (at >= e0 && at < e0 + V) taken |= 1u << (at - e0);
-        if (lane == j) {
-          rank = j;
-          my_e = at;
+          if (at >= e0 && at < e0 + V) taken |= 1u << (at - e0);
+          if (lane == 0) chosen_e[j] = at;
         }
       }
-      if (rank < k) {
-        my_x = row[my_e];
-        if (my_x != my_x || (softmax && my_x == INFINITY)) my_x = -INFINITY;
+      wave_lds_sync();
+      if (lane < k) {
+        float xe = row[chosen_e[lane]];
+        if (xe != xe || (softmax && xe == INFINITY)) xe = -INFINITY;
+        chosen_x[lane] = xe;
       }
+      wave_lds_sync();
     }
+    const int rank = lane;
+    const int my_e = lane < k ? chosen_e[lane] : 0;
+    const float my_x = lane < k ? chosen_x[lane] : 0.0f;
     const bool chosen = rank < k;
     const float sc = chosen ? score32(softmax, my_x, m, inv) : 0.0f;
     float factor = g.scale;
