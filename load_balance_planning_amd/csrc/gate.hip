@@ -62,24 +62,43 @@ __device__ __forceinline__ double score64(bool softmax, float x, float m, double
   return softmax ? exp((double)x - (double)m) / sum : 1.0 / (1.0 + exp(-(double)x));
 }
 
-// LDS of gate_kernel: presence masks; per token 2 P candidates (64-bit choice,
-// choice, logit, expert) and P selected experts with their logits; with groups
-// a row of choices (8 words apart, for other banks) and the group values.
+// Whether a group of `per` experts is a power of two of lanes of V experts:
+// its value then comes from registers, otherwise from a row of choices in LDS.
+template <int V>
+__host__ __device__ inline bool groups_of_lanes(int per) {
+  const int lanes = per / V;
+  return per % V == 0 && (lanes & (lanes - 1)) == 0;
+}
+
+// LDS of gate_kernel: presence masks; the bias; per token 2 P candidates
+// (64-bit choice, choice, expert) and P selected experts; with groups their
+// values and, unless they are whole lanes, a row of choices (8 words apart, for
+// other banks).
 __host__ __device__ inline int choice_stride(int E) { return E + 8; }
 struct GateLds {
-  size_t cand, chosen, choice, group, total;
+  size_t bias, cand, chosen, group, choice, total;
 };
-template <int P>
-__host__ __device__ inline GateLds gate_lds(int E, int n_group, bool prev) {
-  constexpr int TPW = gate_tpw<P>();
+template <int P, int V>
+__host__ __device__ inline GateLds gate_lds(int E, int n_group, bool prev, bool biased) {
+  constexpr size_t TPW = gate_tpw<P>();
   GateLds l;
-  l.cand = sizeof(uint64_t) * (size_t)E * (prev ? 2 : 1);
-  l.chosen = l.cand + (size_t)TPW * 2 * P * 20;
-  l.choice = l.chosen + (size_t)TPW * P * 8;
-  const size_t choices = n_group > 1 ? sizeof(float) * (size_t)TPW * choice_stride(E) : 0;
-  l.group = (l.choice + choices + 7) / 8 * 8;
-  l.total = l.group + (n_group > 1 ? (size_t)TPW * n_group * sizeof(double) : 0);
+  l.bias = sizeof(uint64_t) * (size_t)E * (prev ? 2 : 1);
+  l.cand = l.bias + (biased ? ((size_t)E + 3) / 4 * 16 : 0);
+  l.chosen = l.cand + TPW * 2 * P * 16;
+  l.group = l.chosen + TPW * P * 4;
+  l.choice = l.group + (n_group > 1 ? TPW * n_group * sizeof(double) : 0);
+  const bool rows = n_group > 1 && !groups_of_lanes<V>(E / n_group);
+  l.total = l.choice + (rows ? TPW * choice_stride(E) * sizeof(float) : 0);
   return l;
+}
+
+constexpr float kLog2e = 1.44269504f;
+constexpr float kUlp = 5.9604645e-8f;  // 2^-24
+
+// The two largest of two pairs (a >= b, oa >= ob).
+__device__ __forceinline__ void merge_top2(float* a, float* b, float oa, float ob) {
+  *b = fmaxf(fminf(*a, oa), fmaxf(*b, ob));
+  *a = fmaxf(*a, oa);
 }
 
 template <int P, int V>
@@ -92,17 +111,25 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
   constexpr int SLICES = 64 / TPW;
   extern __shared__ __align__(16) unsigned char smem_gate[];
   const bool want_prev = prev_topk != nullptr;
-  const GateLds lay = gate_lds<P>(d.E, g.n_group, want_prev);
+  const GateLds lay = gate_lds<P, V>(d.E, g.n_group, want_prev, bias != nullptr);
   unsigned long long* smask = reinterpret_cast<unsigned long long*>(smem_gate);
   unsigned long long* pmask = smask + d.E;
+  float* bias_s = reinterpret_cast<float*>(smem_gate + lay.bias);
   const int x_tile = blockIdx.x / SLICES, h = blockIdx.x - x_tile * SLICES;
   const int s = x_tile / d.C, c = x_tile - s * d.C;
   const int64_t t0 = (int64_t)s * d.Tr + (int64_t)c * kTile + h * TPW;
   const int nt = max(0, min(TPW, d.Tr - c * kTile - h * TPW));
   const int tid = threadIdx.x, nthr = blockDim.x;
+  bool bad = false;
   for (int e = tid; e < d.E; e += nthr) {
     smask[e] = 0ull;
     if (want_prev) pmask[e] = 0ull;
+    if (bias) {
+      const float b = bias[e];
+      const bool wrong = b != b || b == INFINITY;
+      bad |= wrong;
+      bias_s[e] = wrong ? 0.0f : b;
+    }
   }
   __syncthreads();
 
@@ -111,26 +138,23 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
   const uint64_t grp_bits = (P == 64 ? ~0ull : ((1ull << P) - 1ull)) << grp_base;
   const int i = tid / P;
   // this token's candidates, [2 P] of each, and its selected experts
-  unsigned char* mine_s = smem_gate + lay.cand;
-  double* cand64 = reinterpret_cast<double*>(mine_s) + (size_t)i * 2 * P;
-  float* cand_c = reinterpret_cast<float*>(mine_s + (size_t)TPW * 2 * P * 8) + (size_t)i * 2 * P;
-  float* cand_x = reinterpret_cast<float*>(mine_s + (size_t)TPW * 2 * P * 12) + (size_t)i * 2 * P;
-  int* cand_e = reinterpret_cast<int*>(mine_s + (size_t)TPW * 2 * P * 16) + (size_t)i * 2 * P;
+  double* cand64 = reinterpret_cast<double*>(smem_gate + lay.cand) + (size_t)i * 2 * P;
+  float* cand_c = reinterpret_cast<float*>(smem_gate + lay.cand + (size_t)TPW * 2 * P * 8) + (size_t)i * 2 * P;
+  int* cand_e = reinterpret_cast<int*>(smem_gate + lay.cand + (size_t)TPW * 2 * P * 12) + (size_t)i * 2 * P;
   int* chosen_e = reinterpret_cast<int*>(smem_gate + lay.chosen) + (size_t)i * P;
-  float* chosen_x = reinterpret_cast<float*>(smem_gate + lay.chosen + (size_t)TPW * P * 4) + (size_t)i * P;
   const bool softmax = g.score == MOEX_SOFTMAX;
   const int k = d.k;
-  bool bad = false;
   if (i < nt) {
     const int64_t t = t0 + i;
     const float* __restrict__ row = logits + t * d.E;
     const int e0 = lane * V;
-    float x[V], c32[V];
+    const bool full = P * V == d.E;  // every slot holds an expert
+    float x[V], o32[V];              // logits; what the experts are ordered by
     if (V >= 4 && vec) {
       // E a multiple of 4: a vector is inside the row as a whole
 #pragma unroll
       for (int w = 0; w < V / 4; ++w) {
-        const bool in = e0 + 4 * w < d.E;
+        const bool in = full || e0 + 4 * w < d.E;
         const float4 f = in ? *reinterpret_cast<const float4*>(row + e0 + 4 * w)
                             : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
         x[4 * w + 0] = f.x;
@@ -145,97 +169,95 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
     float xmax = -INFINITY;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const bool wrong = x[v] != x[v] || (softmax && x[v] == INFINITY);
-      bad |= wrong;
-      x[v] = wrong ? -INFINITY : x[v];
+      bad |= x[v] != x[v];
+      x[v] = fmaxf(x[v], -INFINITY);  // a NaN becomes -infinity
       xmax = fmaxf(xmax, x[v]);
     }
     float m = 0.0f, inv = 0.0f;
     if (softmax) {
       m = group_max<P>(xmax);
+      if (m == INFINITY) {
+        bad = true;
+        xmax = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          x[v] = x[v] == INFINITY ? -INFINITY : x[v];
+          xmax = fmaxf(xmax, x[v]);
+        }
+        m = group_max<P>(xmax);
+      }
+      m = m == -INFINITY ? 0.0f : m;  // nothing but -infinity: every exponential is 0
+    }
+    // Choices in fp32, by the hardware's exponential and reciprocal (each good
+    // to one unit).  The argument of an exponential is off by 2^-24 of itself,
+    // which costs at most 2^-24 of 0.3 in a sigmoid and 0.6 in a softmax share;
+    // with the other roundings, the sum of a softmax (V terms per lane, log2 P
+    // levels) and the addition of the bias, a choice is off by less than
+    // margin / 2 (1 + |choice|), where margin = 16 units, or 2 V + 32 of them.
+    const bool scored = bias != nullptr || g.n_group > 1;  // choices are needed, not the logits' order alone
+    const float margin = (softmax ? 2.0f * V + 32.0f : 16.0f) * kUlp;
+    if (softmax) {
       float sum = 0.0f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        c32[v] = x[v] == -INFINITY ? 0.0f : expf(x[v] - m);
-        sum += c32[v];
+        o32[v] = __builtin_amdgcn_exp2f((x[v] - m) * kLog2e);
+        sum += o32[v];
       }
       sum = group_sum<P>(sum);
       inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     }
-    const bool scored = bias != nullptr || g.n_group > 1;  // choices are needed, not the logits' order alone
     if (scored) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float b = 0.0f;
-        if (bias && e0 + v < d.E) {
-          b = bias[e0 + v];
-          const bool wrong = b != b || b == INFINITY;
-          bad |= wrong;
-          b = wrong ? 0.0f : b;
-        }
-        c32[v] = (softmax ? c32[v] * inv : score32(false, x[v], 0.0f, 0.0f)) + b;
+      for (int v = 0; v < V; ++v)
+        o32[v] = softmax ? o32[v] * inv : __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x[v] * -kLog2e));
+      if (bias) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) o32[v] += full || e0 + v < d.E ? bias_s[e0 + v] : 0.0f;
       }
     }
-    // Twice the error of an fp32 choice of magnitude up to |c|: the sum of V
-    // exponentials per lane and log2 P levels, expf, the divisions and the
-    // addition of the bias, 2^-24 each, with room.
-    const float margin = 2.0f * (V + 16) * 5.9604645e-8f;
+    // in 64 bits, where a comparison needs it
     double sum64 = 1.0;
     bool have64 = !softmax;
-    // the softmax denominator in 64 bits, when a comparison needs it
+    auto logit = [&](int e) {
+      const float xe = row[e];
+      return xe != xe || (softmax && xe == INFINITY) ? -INFINITY : xe;
+    };
     auto need64 = [&]() {
-      if (!have64) {
-        double a = 0.0;
-        for (int v = 0; v < V; ++v) a += x[v] == -INFINITY ? 0.0 : exp((double)x[v] - (double)m);
-        sum64 = group_sum<P>(a);
-        have64 = true;
-      }
+      if (have64) return;
+      double a = 0.0;
+#pragma unroll 1
+      for (int e = e0; e < min(e0 + V, d.E); ++e) a += score64(true, logit(e), m, 1.0);
+      sum64 = group_sum<P>(a);
+      have64 = true;
     };
-    auto choice64 = [&](int e) {
-      float xe = row[e];
-      if (xe != xe || (softmax && xe == INFINITY)) xe = -INFINITY;
-      double b = 0.0;
-      if (bias) {
-        const float be = bias[e];
-        b = be != be || be == INFINITY ? 0.0 : (double)be;
-      }
-      return score64(softmax, xe, m, sum64) + b;
-    };
+    auto choice64 = [&](int e) { return score64(softmax, logit(e), m, sum64) + (bias ? (double)bias_s[e] : 0.0); };
+    auto same_inputs = [&](int a, int b) { return logit(a) == logit(b) && bias_s[a] == bias_s[b]; };
 
     uint64_t kept = ~0ull;  // groups a token may choose from
     const int per = d.E / g.n_group;
     if (g.n_group > 1) {
-      float* ch = reinterpret_cast<float*>(smem_gate + lay.choice) + (size_t)i * choice_stride(d.E);
       double* gv64 = reinterpret_cast<double*>(smem_gate + lay.group) + (size_t)i * g.n_group;
       float* gv = reinterpret_cast<float*>(gv64);
-      const int lanes = per / V;  // lanes of a group, where groups are whole lanes
-      if (per % V == 0 && (lanes & (lanes - 1)) == 0) {
+      if (groups_of_lanes<V>(per)) {
         // the two largest of this lane's choices, then of the group's lanes
-        float a = c32[0], b = -INFINITY;
+        const int lanes = per / V;
+        float a = o32[0], b = -INFINITY;
 #pragma unroll
-        for (int v = 1; v < V; ++v) {
-          b = fmaxf(b, fminf(a, c32[v]));
-          a = fmaxf(a, c32[v]);
-        }
-        for (int off = 1; off < lanes; off <<= 1) {
-          const float oa = __shfl_xor(a, off), ob = __shfl_xor(b, off);
-          b = fmaxf(fminf(a, oa), fmaxf(b, ob));
-          a = fmaxf(a, oa);
-        }
+        for (int v = 1; v < V; ++v) merge_top2(&a, &b, o32[v], -INFINITY);
+        for (int off = 1; off < lanes; off <<= 1) merge_top2(&a, &b, __shfl_xor(a, off), __shfl_xor(b, off));
         if ((lane & (lanes - 1)) == 0 && e0 < d.E) gv[e0 / per] = g.group_top == 2 ? a + b : a;
       } else {
+        float* ch = reinterpret_cast<float*>(smem_gate + lay.choice) + (size_t)i * choice_stride(d.E);
 #pragma unroll
         for (int v = 0; v < V; ++v)
-          if (e0 + v < d.E) ch[e0 + v] = c32[v];
+          if (e0 + v < d.E) ch[e0 + v] = o32[v];
         wave_lds_sync();
         for (int q = lane; q < g.n_group; q += P) {
           float a = -INFINITY, b = -INFINITY;
           int at = q % per;  // lanes start at different places of their groups: other LDS banks
 #pragma unroll 4
           for (int j = 0; j < per; ++j) {
-            const float y = ch[q * per + at];
-            b = fmaxf(b, fminf(a, y));
-            a = fmaxf(a, y);
+            merge_top2(&a, &b, ch[q * per + at], -INFINITY);
             at = at + 1 == per ? 0 : at + 1;
           }
           gv[q] = g.group_top == 2 ? a + b : a;
@@ -250,12 +272,13 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
         if (q < g.n_group) {
           const float y = gv[q], room = 2.0f * margin * (1.0f + fabsf(y));
           int ahead = 0, near = 0;
+#pragma unroll 4
           for (int o = 0; o < g.n_group; ++o) {
             const float z = gv[o];
             ahead += z > y + room ? 1 : 0;
-            near += o != q && z >= y - room ? 1 : 0;
+            near += z >= y - room ? 1 : 0;  // itself among them
           }
-          in = near < g.topk_group;
+          in = near <= g.topk_group;
           unsure |= !in && ahead < g.topk_group;
         }
         mask |= ((__ballot(in) & grp_bits) >> grp_base) << q0;
@@ -265,6 +288,7 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
         wave_lds_sync();
         for (int q = lane; q < g.n_group; q += P) {
           double a = -INFINITY, b = -INFINITY;
+#pragma unroll 1
           for (int j = 0; j < per; ++j) {
             const double y = choice64(q * per + j);
             b = fmax(b, fmin(a, y));
@@ -290,53 +314,64 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
 
     // What the k experts are ordered by: choices, or the logits themselves
     // (-0 as +0).  Past the row's end and outside the kept groups: -infinity.
-    float o32[V];
-    {
-      int q = e0 / per, left = (q + 1) * per - e0;
+    if (!bias) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const bool in = e0 + v < d.E && (g.n_group == 1 || ((kept >> (q & 63)) & 1ull) != 0ull);
-        o32[v] = in ? (bias ? c32[v] : x[v] + 0.0f) : -INFINITY;
-        if (--left == 0) {
-          ++q;
-          left = per;
+      for (int v = 0; v < V; ++v) o32[v] = x[v] + 0.0f;
+    }
+    if (g.n_group > 1) {
+      int q = e0 / per;
+      if (per % V == 0) {
+        const bool in = ((kept >> (q & 63)) & 1ull) != 0ull;  // the lane's experts are of one group
+#pragma unroll
+        for (int v = 0; v < V; ++v) o32[v] = in ? o32[v] : -INFINITY;
+      } else {
+        int left = (q + 1) * per - e0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          o32[v] = ((kept >> (q & 63)) & 1ull) != 0ull ? o32[v] : -INFINITY;
+          if (--left == 0) {
+            ++q;
+            left = per;
+          }
         }
       }
     }
-    float omax = o32[0];
+    if (!full) {
 #pragma unroll
-    for (int v = 1; v < V; ++v) omax = fmaxf(omax, o32[v]);
-    uint32_t sorted = group_sort_desc_u32<P>(order_key(__float_as_uint(omax)), lane);
+      for (int v = 0; v < V; ++v) o32[v] = e0 + v < d.E ? o32[v] : -INFINITY;
+    }
+    uint32_t sorted;
     if (g.n_group > 1) {
       // Kept groups leave some lanes without a choice, and the k-th largest
       // maximum of the others admits too much: take each lane's two largest.
       // The larger of the i-th maximum and the i-th smallest second are the P
-      // largest of them all.
+      // largest of them all, in bitonic order.
       float a = o32[0], b = -INFINITY;
 #pragma unroll
-      for (int v = 1; v < V; ++v) {
-        b = fmaxf(b, fminf(a, o32[v]));
-        a = fmaxf(a, o32[v]);
-      }
+      for (int v = 1; v < V; ++v) merge_top2(&a, &b, o32[v], -INFINITY);
+      sorted = group_sort_desc_u32<P>(order_key(__float_as_uint(a)), lane);
       const uint32_t seconds = group_sort_desc_u32<P>(order_key(__float_as_uint(b)), lane);
-      sorted = max(sorted, (uint32_t)__shfl_xor((int)seconds, P - 1));
-      sorted = group_sort_desc_u32<P>(sorted, lane);
+      sorted = group_merge_desc_u32<P>(max(sorted, (uint32_t)__shfl_xor((int)seconds, P - 1)), lane);
+    } else {
+      float a = o32[0];
+#pragma unroll
+      for (int v = 1; v < V; ++v) a = fmaxf(a, o32[v]);
+      sorted = group_sort_desc_u32<P>(order_key(__float_as_uint(a)), lane);
     }
     const float kth = __uint_as_float(float_from_order_key((uint32_t)__shfl((int)sorted, grp_base + k - 1)));
     const float tau = bias ? kth - margin * (1.0f + fabsf(kth)) : kth;
     int mine = 0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) mine += e0 + v < d.E && o32[v] >= tau ? 1 : 0;
+    for (int v = 0; v < V; ++v) mine += o32[v] >= tau ? 1 : 0;
+    if (!full && tau == -INFINITY) mine = max(0, min(V, d.E - e0));  // slots past the row's end count for nothing
     const int incl = group_incl_scan<P>(mine, lane);
     const int total = group_last<P>(incl);
-    auto same_inputs = [&](int ea, float xa, int eb, float xb) { return xa == xb && bias[ea] == bias[eb]; };
     if (total <= 2 * P) {
       int w = incl - mine;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        if (e0 + v < d.E && o32[v] >= tau) {
+        if (o32[v] >= tau && (full || e0 + v < d.E)) {
           cand_c[w] = o32[v];
-          cand_x[w] = x[v];
           cand_e[w] = e0 + v;
           ++w;
         }
@@ -345,17 +380,20 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
       bool unsure = false;
       for (int at = lane; at < total; at += P) {  // once, but for the few tokens with more than P
         const float my_c = cand_c[at];
-        int rank = 0;
+        // a choice this near is not told from this one (-infinity is sure)
+        const float room = bias && my_c != -INFINITY ? margin * (1.0f + fabsf(my_c)) : -1.0f;
+        int rank = 0, near = 0;
+#pragma unroll 4
         for (int j = 0; j < total; ++j) {
           const float cj = cand_c[j];
           rank += cj > my_c || (cj == my_c && j < at) ? 1 : 0;  // candidates are in expert order
-          if (bias && j != at && fabsf(cj - my_c) <= margin * (1.0f + fminf(fabsf(cj), fabsf(my_c))))
-            unsure |= !same_inputs(cand_e[j], cand_x[j], cand_e[at], cand_x[at]);
+          near += fabsf(cj - my_c) <= room ? 1 : 0;             // itself among them
         }
-        if (rank < k) {
-          chosen_e[rank] = cand_e[at];
-          chosen_x[rank] = cand_x[at];
-        }
+        const int e = cand_e[at];
+        if (near > 1)
+          for (int j = 0; j < total; ++j)
+            if (fabsf(cand_c[j] - my_c) <= room) unsure |= !same_inputs(cand_e[j], e);
+        if (rank < k) chosen_e[rank] = e;
       }
       if ((__ballot(unsure) & grp_bits) != 0ull) {
         need64();
@@ -366,19 +404,15 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
           const double y = cand64[at];
           int rank = 0;
           for (int j = 0; j < total; ++j) rank += cand64[j] > y || (cand64[j] == y && j < at) ? 1 : 0;
-          if (rank < k) {
-            chosen_e[rank] = cand_e[at];
-            chosen_x[rank] = cand_x[at];
-          }
+          if (rank < k) chosen_e[rank] = cand_e[at];
         }
       }
-      wave_lds_sync();
     } else {
       // Rounds, each the largest left, ties to the lower expert; with a bias one
       // more, to see whether the last pick is sure.  Taken experts' bits: V <= 32.
       uint32_t taken = 0u;
       bool unsure = false;
-      float last_c = 0.0f, last_x = 0.0f;
+      float last_c = 0.0f;
       int last_e = -1;
       const int rounds = bias && k < d.E ? k + 1 : k;
       for (int j = 0; j < rounds; ++j) {
@@ -394,11 +428,9 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
         const float ce = __uint_as_float(float_from_order_key((uint32_t)(top >> 32)));
         if (j < k && lane == 0) chosen_e[j] = e;
         if (bias) {
-          const float xe = row[e];
           if (last_e >= 0 && fabsf(ce - last_c) <= margin * (1.0f + fminf(fabsf(ce), fabsf(last_c))))
-            unsure |= !same_inputs(e, xe, last_e, last_x);
+            unsure |= !same_inputs(e, last_e);
           last_c = ce;
-          last_x = xe;
           last_e = e;
         }
       }
@@ -408,6 +440,7 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
         for (int j = 0; j < k; ++j) {
           double best = -INFINITY;
           int at = d.E;  // none
+#pragma unroll 1
           for (int v = 0; v < V; ++v) {
             const int e = e0 + v;
             if (e >= d.E || ((taken >> v) & 1u) != 0u) continue;
@@ -431,26 +464,22 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
           if (lane == 0) chosen_e[j] = at;
         }
       }
-      wave_lds_sync();
-      if (lane < k) {
-        float xe = row[chosen_e[lane]];
-        if (xe != xe || (softmax && xe == INFINITY)) xe = -INFINITY;
-        chosen_x[lane] = xe;
-      }
-      wave_lds_sync();
     }
-    const int rank = lane;
-    const int my_e = lane < k ? chosen_e[lane] : 0;
-    const float my_x = lane < k ? chosen_x[lane] : 0.0f;
-    const bool chosen = rank < k;
-    const float sc = chosen ? score32(softmax, my_x, m, inv) : 0.0f;
+    wave_lds_sync();
+    // lane j: the j-th expert
+    const bool chosen = lane < k;
+    const int e = chosen ? chosen_e[lane] : 0;
+    const float raw = chosen ? row[e] : 0.0f;
+    float xe = fmaxf(raw, -INFINITY);
+    if (softmax && xe == INFINITY) xe = -INFINITY;
+    const float sc = chosen ? score32(softmax, xe, m, inv) : 0.0f;
     float factor = g.scale;
     if (g.renorm) factor = g.scale / (group_sum<P>(sc) + kTiny);
     if (chosen) {
-      topk_idx[t * k + rank] = my_e;
-      if (topk_val) topk_val[t * k + rank] = row[my_e];
-      weight[t * k + rank] = sc * factor;
-      atomicOr(&smask[my_e], 1ull << i);
+      topk_idx[t * k + lane] = e;
+      if (topk_val) topk_val[t * k + lane] = raw;
+      weight[t * k + lane] = sc * factor;
+      atomicOr(&smask[e], 1ull << i);
     }
   }
   if (want_prev) {
@@ -484,7 +513,7 @@ hipError_t launch_gate_pv(const Dims& d, const moex_gate_config& g, bool vec, co
                           const int32_t* prev_topk, int32_t* topk_idx, float* topk_val, float* weight,
                           uint64_t* tile_mask, uint64_t* prev_mask, int32_t* status, hipStream_t st) {
   constexpr int slices = 64 / gate_tpw<P>();
-  const size_t lds = gate_lds<P>(d.E, g.n_group, prev_topk != nullptr).total;
+  const size_t lds = gate_lds<P, V>(d.E, g.n_group, prev_topk != nullptr, bias != nullptr).total;
   if (lds > 65536) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(gate_kernel<P, V>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);

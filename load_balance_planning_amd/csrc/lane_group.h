@@ -121,5 +121,16 @@ __device__ __forceinline__ uint32_t group_sort_desc_u32(uint32_t v, int lig) {
   return v;
 }
 
+// Sort of a bitonic sequence (the last stage of the sort above), descending.
+template <int P>
+__device__ __forceinline__ uint32_t group_merge_desc_u32(uint32_t v, int lig) {
+  if (P >= 64) v = bitonic_step_u32<P, 32>(v, lig);
+  if (P >= 32) v = bitonic_step_u32<P, 16>(v, lig);
+  if (P >= 16) v = bitonic_step_u32<P, 8>(v, lig);
+  if (P >= 8) v = bitonic_step_u32<P, 4>(v, lig);
+  if (P >= 4) v = bitonic_step_u32<P, 2>(v, lig);
+  return bitonic_step_u32<P, 1>(v, lig);
+}
+
 }  // namespace
 }  // namespace moe
