@@ -11,6 +11,7 @@
 #include "experts.h"
 #include "fp8_block.h"
 #include "instances.h"
+#include "store_tile.h"
 
 namespace moe {
 namespace {
@@ -18,7 +19,6 @@ namespace {
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
-typedef float v16f __attribute__((ext_vector_type(16)));
 
 // 32 of a row's 128 bytes: the 16 of lane group g in each half.  (Both
 // operands use the same order, so any order of the block does.)
@@ -245,7 +245,7 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), 1) void matm
   // take the first and third of them, lanes 32..63 the others.
   const int at_c = piece_at<true>(wc + 16 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3), g);
   const int at_t = piece_at<false>(wt + r, g);
-  v16f acc[S::kC][S::kT];
+  acc16 acc[S::kC][S::kT];
 #pragma unroll
   for (int i = 0; i < S::kC; ++i)
 #pragma unroll
@@ -324,31 +324,12 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), 1) void matm
     multiply(f0);
     multiply(f1);
   }
-  const bool vec = n % 8 == 0 && ((uintptr_t)y & 15) == 0;
-#pragma unroll
-  for (int j = 0; j < S::kT; ++j) {
-    const int row = wt + 32 * j + r;
-    if (row >= rows_left) continue;
-#pragma unroll
-    for (int i = 0; i < S::kC; ++i) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {  // eight consecutive channels
-        const int c = wc + 32 * i + 16 * g + 8 * h;
-        if (c >= chans_left) continue;
-        uint16_t* dst = y + (r0 + row) * n + cbase + c;
-        u32x4 o;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = pack_bf16(acc[i][j][8 * h + 2 * q], acc[i][j][8 * h + 2 * q + 1]);
-        if (vec) {
-          *reinterpret_cast<u32x4*>(dst) = o;
-        } else {
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            if (c + q < chans_left) dst[q] = (uint16_t)(o[q / 2] >> (16 * (q & 1)));
-        }
-      }
-    }
-  }
+  __syncthreads();  // every wave has its last operands: LDS is free
+  static_assert(S::kWaves == 4, "a part of LDS for each wave");
+  static_assert(S::kWaveC * S::kWaveT * 2 <= (BC < BT ? BC : BT) * kBlk, "a wave's result fits its part");
+  unsigned char* own = wave == 0 ? c0_s : wave == 1 ? t0_s : wave == 2 ? c1_s : t1_s;
+  store_wave_tile(acc, own, y + (r0 + wt) * n + cbase + wc, n, rows_left - wt, chans_left - wc,
+                  n % 8 == 0 && ((uintptr_t)y & 15) == 0);
 #endif
 }
 

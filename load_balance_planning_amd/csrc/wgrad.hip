@@ -31,18 +31,26 @@
 #include "experts.h"
 #include "fp8_block.h"
 #include "instances.h"
+#include "store_tile.h"
 
 namespace moe {
 namespace {
 
-typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 constexpr int kStepRows = 64;
-constexpr int kCols = 256;                        // columns of either operand
-constexpr int kRowBytes = kCols * 2;
-constexpr int kSliceBytes = 16 * kRowBytes;
-constexpr int kOperandBytes = kStepRows * kRowBytes;  // one operand's step in LDS
+constexpr int kThreads = 256;
+
+// COLS columns of either operand per workgroup, half of them per wave.
+template <int COLS>
+struct GradShape {
+  static constexpr int kRowBytes = COLS * 2;
+  static constexpr int kSliceBytes = 16 * kRowBytes;
+  static constexpr int kOperandBytes = kStepRows * kRowBytes;  // one operand's step in LDS
+  static constexpr int kLanesPerRow = COLS / 16;               // threads of a row of the step
+  static constexpr int kRows = kStepRows * kLanesPerRow / kThreads;  // rows of a thread's piece
+  static constexpr int kWave = COLS / 2, kN = kWave / 32;      // a wave's columns, in instruction tiles
+};
 
 // The steps of an expert: 64 rows of one instance at a time, instances in
 // order.  Every lane of a wave steps alike.
@@ -85,34 +93,39 @@ __device__ __forceinline__ void next_step(Steps* s, const Instances& in, int* ro
   }
 }
 
-// Four rows of 16 columns as loaded.
+// A thread's rows of 16 columns as loaded.
+template <int ROWS>
 struct Piece {
-  u32x4 q[4];
-  uint32_t s[4];
+  u32x4 q[ROWS];
+  uint32_t s[ROWS];
 };
 
-__global__ __launch_bounds__(256, 1) void wgrad_kernel(Instances in, const uint8_t* __restrict__ dy,
+template <int COLS>
+__global__ __launch_bounds__(kThreads, COLS == 256 ? 1 : 2) void wgrad_kernel(Instances in, const uint8_t* __restrict__ dy,
                                                        const uint8_t* __restrict__ dys, const uint8_t* __restrict__ x,
                                                        const uint8_t* __restrict__ xs, int n, int k,
                                                        uint16_t* __restrict__ dw, int32_t* __restrict__ status) {
 #ifdef __HIP_DEVICE_COMPILE__
-  __shared__ __align__(256) unsigned char x0_s[kOperandBytes];
-  __shared__ __align__(256) unsigned char y0_s[kOperandBytes];
-  __shared__ __align__(256) unsigned char x1_s[kOperandBytes];
-  __shared__ __align__(256) unsigned char y1_s[kOperandBytes];
+  using S = GradShape<COLS>;
+  constexpr int kRowBytes = S::kRowBytes, kN = S::kN;
+  using Piece = Piece<S::kRows>;
+  __shared__ __align__(256) unsigned char x0_s[S::kOperandBytes];
+  __shared__ __align__(256) unsigned char y0_s[S::kOperandBytes];
+  __shared__ __align__(256) unsigned char x1_s[S::kOperandBytes];
+  __shared__ __align__(256) unsigned char y1_s[S::kOperandBytes];
   if (blockIdx.x == 0) check_instances(in, status);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int ntk = (k + kCols - 1) / kCols, ntn = (n + kCols - 1) / kCols;
+  const int ntk = (k + COLS - 1) / COLS, ntn = (n + COLS - 1) / COLS;
   const int tk = blockIdx.x % ntk, rest = blockIdx.x / ntk;
   const int tn = rest % ntn, e = rest / ntn;
   const int nbn = (n + kBlk - 1) / kBlk, nbk = (k + kBlk - 1) / kBlk;
   const int nsn = (nbn + 3) / 4 * 4, nsk = (nbk + 3) / 4 * 4;
   const int np = nbn * kBlk, kp = nbk * kBlk;
-  // this thread's piece of either operand: columns 16 c16 .. of the tile, rows 4 rq .. of the step
-  const int c16 = threadIdx.x & 15, rq = threadIdx.x >> 4;
-  const uint32_t off_x = (uint32_t)(4 * rq * kp + tk * kCols + 16 * c16), off_y = (uint32_t)(4 * rq * np + tn * kCols + 16 * c16);
-  const uint32_t soff_x = (uint32_t)(4 * rq * nsk + (tk * kCols + 16 * c16) / kBlk);
-  const uint32_t soff_y = (uint32_t)(4 * rq * nsn + (tn * kCols + 16 * c16) / kBlk);
+  // this thread's piece of either operand: columns 16 c16 .. of the tile, rows from row0 of the step
+  const int c16 = threadIdx.x % S::kLanesPerRow, row0 = threadIdx.x / S::kLanesPerRow * S::kRows;
+  const uint32_t off_x = (uint32_t)(row0 * kp + tk * COLS + 16 * c16), off_y = (uint32_t)(row0 * np + tn * COLS + 16 * c16);
+  const uint32_t soff_x = (uint32_t)(row0 * nsk + (tk * COLS + 16 * c16) / kBlk);
+  const uint32_t soff_y = (uint32_t)(row0 * nsn + (tn * COLS + 16 * c16) / kBlk);
   // Past the step's rows the descriptor ends: values and scales there are 0.
   // Columns past the row's end are some other row's; nothing stores them.
   auto load = [&](Piece* p, const uint8_t* q, const uint8_t* scale, int row, int rows, int cp, int ns, uint32_t off,
@@ -122,16 +135,16 @@ __global__ __launch_bounds__(256, 1) void wgrad_kernel(Instances in, const uint8
     const auto buf = buffer_of(q + (int64_t)row * cp, (uint32_t)rows * (uint32_t)cp);
     const auto sbuf = buffer_of(scale + (int64_t)row * ns, (uint32_t)(rows * ns));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < S::kRows; ++j) {
       p->q[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(buf, off + (uint32_t)(j * cp), 0, 0));
       p->s[j] = __builtin_amdgcn_raw_buffer_load_b8(sbuf, soff + (uint32_t)(j * ns), 0, 0);
     }
   };
-  // rows 2h and 2h + 1 of a piece, widened, to LDS
+  // the first (h = 0) or second half of a piece's rows, widened, to LDS
   const int swap = (c16 >> 2) & 1;
   auto widen = [&](const Piece& p, unsigned char* lds, int h) {
 #pragma unroll
-    for (int j = 2 * h; j < 2 * h + 2; ++j) {
+    for (int j = h * S::kRows / 2; j < (h + 1) * S::kRows / 2; ++j) {
       const float f = __uint_as_float(p.s[j] << 23);  // 255 gives NaN for the whole block
       u32x4 w[2];
 #pragma unroll
@@ -139,26 +152,27 @@ __global__ __launch_bounds__(256, 1) void wgrad_kernel(Instances in, const uint8
         w[i / 2][2 * (i & 1)] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p.q[j][i], f, false));
         w[i / 2][2 * (i & 1) + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p.q[j][i], f, true));
       }
-      unsigned char* row = lds + (4 * rq + j) * kRowBytes + (c16 ^ (2 * j)) * 32;
+      unsigned char* row = lds + (row0 + j) * kRowBytes + (c16 ^ (2 * ((row0 + j) & 3))) * 32;
       *reinterpret_cast<u32x4*>(row + 16 * swap) = w[0];
       *reinterpret_cast<u32x4*>(row + 16 - 16 * swap) = w[1];
     }
   };
-  const int wk = (wave & 1) * 128, wn = (wave >> 1) * 128;
+  const int wk = (wave & 1) * S::kWave, wn = (wave >> 1) * S::kWave;
   const int r = lane & 31, g = lane >> 5;
   // Reads: lane 4t + q of 16 lends the address of row t, four columns, which
   // go to lanes 4q .. 4q + 3.  dy's columns stay in order; x's are taken so that
   // matrix row 8a + 4h + j is column 16h + 4a + j.
   const int t = (lane >> 2) & 3, q = lane & 3, half = (lane >> 4) & 1;
-  int at_x[4], at_y[4];
+  int at_x[kN], at_y[kN];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kN; ++i) {
     const int row = (8 * g + t) * kRowBytes;
-    at_x[i] = row + (((wk + 32 * i) / 16 + (q & 1)) ^ (2 * t)) * 32 + (((8 * half + 4 * (q >> 1)) * 2) ^ (16 * (i >> 1)));
-    at_y[i] = row + (((wn + 32 * i) / 16 + half) ^ (2 * t)) * 32 + ((4 * q * 2) ^ (16 * (i >> 1)));
+    const int ux = (wk + 32 * i) / 16 + (q & 1), uy = (wn + 32 * i) / 16 + half;
+    at_x[i] = row + (ux ^ (2 * t)) * 32 + (((8 * half + 4 * (q >> 1)) * 2) ^ (16 * ((ux >> 2) & 1)));
+    at_y[i] = row + (uy ^ (2 * t)) * 32 + ((4 * q * 2) ^ (16 * ((uy >> 2) & 1)));
   }
   struct Slice {
-    v8bf x[4], y[4];
+    v8bf x[kN], y[kN];
   };
   auto read8 = [&](const unsigned char* s) {  // rows 8g .. 8g + 7 of the slice, this lane's column
     typedef short v4s __attribute__((ext_vector_type(4)));
@@ -173,30 +187,30 @@ __global__ __launch_bounds__(256, 1) void wgrad_kernel(Instances in, const uint8
   };
   auto read = [&](Slice* f, const unsigned char* x_s, const unsigned char* y_s, int slice) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f->x[i] = read8(x_s + at_x[i] + slice * kSliceBytes);
-      f->y[i] = read8(y_s + at_y[i] + slice * kSliceBytes);
+    for (int i = 0; i < kN; ++i) {
+      f->x[i] = read8(x_s + at_x[i] + slice * S::kSliceBytes);
+      f->y[i] = read8(y_s + at_y[i] + slice * S::kSliceBytes);
     }
   };
-  v16f acc[4][4];
+  acc16 acc[kN][kN];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kN; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < kN; ++j)
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
   auto multiply = [&](const Slice& f) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kN; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < kN; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.x[i], f.y[j], acc[i][j], 0, 0, 0);
   };
   // a slice's products with the other work between them: a read each, the
   // writes and loads spread out, vector instructions
   auto spread = [&](bool loads) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < (kN == 4 ? 16 : 0); ++i) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
@@ -264,45 +278,44 @@ __global__ __launch_bounds__(256, 1) void wgrad_kernel(Instances in, const uint8
       left = step(x1_s, y1_s, x0_s, y0_s, pa, &pb);
     } while (left > 0);
   }
-  const bool vec = k % 8 == 0 && ((uintptr_t)dw & 15) == 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int c = tn * kCols + wn + 32 * j + r;
-    if (c >= n) continue;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {  // eight consecutive columns
-        const int col = tk * kCols + wk + 32 * i + 16 * g + 8 * h;
-        if (col >= k) continue;
-        uint16_t* dst = dw + ((int64_t)e * n + c) * k + col;
-        u32x4 o;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = pack_bf16(acc[i][j][8 * h + 2 * q], acc[i][j][8 * h + 2 * q + 1]);
-        if (vec) {
-          *reinterpret_cast<u32x4*>(dst) = o;
-        } else {
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            if (col + q < k) dst[q] = (uint16_t)(o[q / 2] >> (16 * (q & 1)));
-        }
-      }
-    }
-  }
+  __syncthreads();  // every wave has its last operands: LDS is free
+  unsigned char* own = wave == 0 ? x0_s : wave == 1 ? y0_s : wave == 2 ? x1_s : y1_s;
+  const int c = tn * COLS + wn, col = tk * COLS + wk;
+  store_wave_tile(acc, own, dw + ((int64_t)e * n + c) * k + col, k, n - c, k - col,
+                  k % 8 == 0 && ((uintptr_t)dw & 15) == 0);
 #endif
 }
 
 }  // namespace
 
+namespace {
+
+int64_t grad_tiles(const Instances& in, int32_t n, int32_t k, int cols) {
+  return (int64_t)in.E * ((n + cols - 1) / cols) * ((k + cols - 1) / cols);
+}
+bool large_grad_tiles(const Instances& in, int32_t n, int32_t k) { return grad_tiles(in, n, k, 256) >= 512; }
+
+}  // namespace
+
 int64_t wgrad_tiles(const Instances& in, int32_t n, int32_t k) {
-  return (int64_t)in.E * ((n + kCols - 1) / kCols) * ((k + kCols - 1) / kCols);
+  return grad_tiles(in, n, k, large_grad_tiles(in, n, k) ? 256 : 128);
+}
+
+template <int COLS>
+hipError_t launch_grad_tiles(const Instances& in, const uint8_t* dy, const uint8_t* dys, const uint8_t* x,
+                             const uint8_t* xs, int32_t n, int32_t k, uint16_t* dw, int32_t* status, hipStream_t st) {
+  hipLaunchKernelGGL((wgrad_kernel<COLS>), dim3((unsigned)grad_tiles(in, n, k, COLS)), dim3(kThreads), 0, st, in, dy, dys, x, xs, n, k, dw,
+                     status);
+  return hipGetLastError();
 }
 
 hipError_t launch_wgrad(const Instances& in, const uint8_t* dy, const uint8_t* dys, const uint8_t* x,
                         const uint8_t* xs, int32_t n, int32_t k, uint16_t* dw, int32_t* status, hipStream_t st) {
-  hipLaunchKernelGGL(wgrad_kernel, dim3((unsigned)wgrad_tiles(in, n, k)), dim3(256), 0, st, in, dy, dys, x, xs, n, k,
-                     dw, status);
-  return hipGetLastError();
+  // 256 x 256 where there are two for every CU (128 experts of 1536 x 2048,
+  // 32768 rows: 374 us against 416 in 128 x 128); else 128 x 128, two
+  // workgroups to a CU (8 experts of 768 x 1024, 8192 rows: 25 us against 32)
+  return large_grad_tiles(in, n, k) ? launch_grad_tiles<256>(in, dy, dys, x, xs, n, k, dw, status, st)
+                                    : launch_grad_tiles<128>(in, dy, dys, x, xs, n, k, dw, status, st);
 }
 
 }  // namespace moe
