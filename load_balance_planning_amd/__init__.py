@@ -421,6 +421,11 @@ class DedupBuffers:
         return moe_dedup_out(*(_ptr(getattr(self, n)) for n, _ in moe_dedup_out._fields_))
 
 
+def _addr(t):
+    """Address of a tensor as ctypes takes it for a pointer argument (cheaper than an object of its own)."""
+    return None if t is None else t.data_ptr()
+
+
 @dataclass
 class Blocks:
     """Quantized rows or matrices (include/moe_experts.h): q float8_e4m3fn [..., cols padded to 128], scale
@@ -448,7 +453,12 @@ class Layer:
             raise RuntimeError("load_balance_planning_amd needs a HIP device")
         self.torch = torch
         self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
         self.cfg = cfg
+        self._index = self.device.index
+        # handle of torch's current stream on a device, without the Python object around it
+        self._current_stream = torch._C._cuda_getCurrentRawStream
         self.sizes = moe_plan_query(cfg)
         with torch.cuda.device(self.device):
             self.handle = moe_plan_create(cfg)
@@ -472,8 +482,9 @@ class Layer:
         self.dedup_out = None
 
     def _stream(self, stream=None) -> int:
-        s = self.torch.cuda.current_stream(self.device) if stream is None else stream
-        return s.cuda_stream
+        if stream is None:
+            return self._current_stream(self._index)
+        return stream.cuda_stream
 
     def route(self, logits, prev_topk=None, stream=None):
         self._check_tensor(logits, (self.cfg.T, self.cfg.E), self.torch.float32)
@@ -544,7 +555,7 @@ class Layer:
         if prev_topk is not None:
             self._check_tensor(prev_topk, (T, k), torch.int32)
         weight = torch.empty((T, k), dtype=torch.float32, device=self.device)
-        moex_gate(self.handle, gate, _ptr(logits), _ptr(bias), _ptr(prev_topk), self._route_s, _ptr(weight),
+        moex_gate(self.handle, gate, _addr(logits), _addr(bias), _addr(prev_topk), self._route_s, _addr(weight),
                   self._stream(stream))
         return self.route_out, weight
 
@@ -557,7 +568,7 @@ class Layer:
         self._check_tensor(topk_idx, (T, k), torch.int32)
         self._check_tensor(grad_weight, (T, k), torch.float32)
         self._check_tensor(out, (T, E), torch.float32)
-        moex_gate_grad(self.handle, gate, _ptr(logits), _ptr(topk_idx), _ptr(grad_weight), _ptr(out),
+        moex_gate_grad(self.handle, gate, _addr(logits), _addr(topk_idx), _addr(grad_weight), _addr(out),
                        self._stream(stream))
         return out
 
@@ -585,7 +596,7 @@ class Layer:
         rows, cols = x.shape
         self._check_16bit(x, (rows, cols), "x")
         out = self._empty_blocks((rows,), cols)
-        moex_quantize(self.handle, _ptr(x), rows, cols, _ptr(out.q), _ptr(out.scale), self._stream(stream))
+        moex_quantize(self.handle, _addr(x), rows, cols, _addr(out.q), _addr(out.scale), self._stream(stream))
         return out
 
     def quantize_weights(self, w, transposed: bool = False, stream=None):
@@ -598,8 +609,8 @@ class Layer:
         blocks = lambda c: -(-c // BLOCK)
         out = self._empty_blocks((E, n), k, (E, blocks(n)))
         out_t = self._empty_blocks((E, k), n, (E, blocks(k))) if transposed else Blocks(None, None, n)
-        moex_quantize_weights(self.handle, _ptr(w), E, n, k, _ptr(out.q), _ptr(out.scale), _ptr(out_t.q),
-                              _ptr(out_t.scale), self._stream(stream))
+        moex_quantize_weights(self.handle, _addr(w), E, n, k, _addr(out.q), _addr(out.scale), _addr(out_t.q),
+                              _addr(out_t.scale), self._stream(stream))
         return (out, out_t) if transposed else out
 
     def swiglu(self, y, stream=None) -> Blocks:
@@ -609,7 +620,7 @@ class Layer:
         rows, f = y.shape[0], y.shape[1] // 2
         self._check_16bit(y, (rows, 2 * f), "y")
         out = self._empty_blocks((rows,), f)
-        moex_swiglu(self.handle, _ptr(y), rows, f, _ptr(out.q), _ptr(out.scale), self._stream(stream))
+        moex_swiglu(self.handle, _addr(y), rows, f, _addr(out.q), _addr(out.scale), self._stream(stream))
         return out
 
     def swiglu_grad(self, y, grad, stream=None) -> Blocks:
@@ -620,20 +631,22 @@ class Layer:
         self._check_16bit(y, (rows, 2 * f), "y")
         self._check_16bit(grad, (rows, f), "grad")
         out = self._empty_blocks((rows,), 2 * f)
-        moex_swiglu_grad(self.handle, _ptr(y), _ptr(grad), rows, f, _ptr(out.q), _ptr(out.scale),
+        moex_swiglu_grad(self.handle, _addr(y), _addr(grad), rows, f, _addr(out.q), _addr(out.scale),
                          self._stream(stream))
         return out
 
     def _product_plan(self, plan, inst_offset):
         """The struct of the instances a product runs over; by default this layer's plan and dispatch offsets."""
         inst_offset = self.dispatch_out.inst_offset if inst_offset is None else inst_offset
-        cap = int(self.sizes.inst_cap)
+        cap = self.cfg.E + self.cfg.replica_budget
         self._check_tensor(inst_offset, (cap + 1,), self.torch.int32)
         if plan is None:
             return self._plan_s, inst_offset
         self._check_tensor(plan.n_inst, (1,), self.torch.int32)
         self._check_tensor(plan.inst_expert, (cap,), self.torch.int32)
-        return plan.struct(), inst_offset
+        s = moe_plan_out()  # the fields that the products read
+        s.n_inst, s.inst_expert = plan.n_inst.data_ptr(), plan.inst_expert.data_ptr()
+        return s, inst_offset
 
     def matmul(self, x: Blocks, w: Blocks, plan=None, inst_offset=None, out=None, stream=None):
         """Rows in dispatch order times their experts' matrices (moex_matmul): bf16 [T*k][n] of x, Blocks of rows
@@ -647,8 +660,8 @@ class Layer:
         self._check_blocks(w, (self.cfg.E, n), (self.cfg.E, -(-n // BLOCK)))
         out = torch.empty((rows, n), dtype=torch.bfloat16, device=self.device) if out is None else out
         self._check_16bit(out, (rows, n), "out")
-        moex_matmul(self.handle, plan_s, _ptr(inst_offset), _ptr(x.q), _ptr(x.scale), _ptr(w.q), _ptr(w.scale), n, k,
-                    _ptr(out), self._stream(stream))
+        moex_matmul(self.handle, plan_s, _addr(inst_offset), _addr(x.q), _addr(x.scale), _addr(w.q), _addr(w.scale), n, k,
+                    _addr(out), self._stream(stream))
         return out
 
     def wgrad(self, dy: Blocks, x: Blocks, plan=None, inst_offset=None, out=None, stream=None):
@@ -660,8 +673,8 @@ class Layer:
         self._check_blocks(x, (rows,))
         out = torch.empty((E, dy.cols, x.cols), dtype=torch.bfloat16, device=self.device) if out is None else out
         self._check_16bit(out, (E, dy.cols, x.cols), "out")
-        moex_wgrad(self.handle, plan_s, _ptr(inst_offset), _ptr(dy.q), _ptr(dy.scale), _ptr(x.q), _ptr(x.scale),
-                   dy.cols, x.cols, _ptr(out), self._stream(stream))
+        moex_wgrad(self.handle, plan_s, _addr(inst_offset), _addr(dy.q), _addr(dy.scale), _addr(x.q), _addr(x.scale),
+                   dy.cols, x.cols, _addr(out), self._stream(stream))
         return out
 
     def _slot_positions(self, slot_pos):
@@ -679,7 +692,7 @@ class Layer:
             self._check_tensor(weight, (T, k), torch.float32)
         out = torch.empty((T, H), dtype=expert_out.dtype, device=self.device) if out is None else out
         self._check_16bit(out, (T, H), "out")
-        moex_combine(self.handle, _ptr(weight), _ptr(slot_pos), _ptr(expert_out), _ptr(out), self._stream(stream))
+        moex_combine(self.handle, _addr(weight), _addr(slot_pos), _addr(expert_out), _addr(out), self._stream(stream))
         return out
 
     def combine_grad(self, expert_out, grad_out, weight, slot_pos=None, stream=None):
@@ -692,8 +705,8 @@ class Layer:
         self._check_tensor(weight, (T, k), torch.float32)
         grad_rows = torch.empty_like(expert_out)
         grad_weight = torch.empty((T, k), dtype=torch.float32, device=self.device)
-        moex_combine_grad(self.handle, _ptr(weight), _ptr(slot_pos), _ptr(expert_out), _ptr(grad_out),
-                          _ptr(grad_rows), _ptr(grad_weight), self._stream(stream))
+        moex_combine_grad(self.handle, _addr(weight), _addr(slot_pos), _addr(expert_out), _addr(grad_out),
+                          _addr(grad_rows), _addr(grad_weight), self._stream(stream))
         return grad_rows, grad_weight
 
     def place(self, cooc=None, max_swaps: int = -1, stream=None):
@@ -841,7 +854,7 @@ class Layer:
         return moe_plan_status(self.handle)
 
     def _check_tensor(self, t, shape, dtype):
-        if tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != self.device:
+        if t.shape != shape or t.get_device() != self._index or not t.is_contiguous():
             raise ValueError("expected a contiguous %s tensor of shape %s on %s" % (dtype, shape, self.device))
         if dtype is not None and t.dtype != dtype:
             raise TypeError("expected dtype %s, got %s" % (dtype, t.dtype))
