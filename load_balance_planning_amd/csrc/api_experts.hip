@@ -127,6 +127,8 @@ extern "C" int moex_matmul(moe_plan_t h, const moe_plan_out* plan, const int32_t
   const int rc = check_product(h, plan, inst_offset, n, k);
   if (rc != MOE_OK) return rc;
   if (h->d.T > 0 && (!blocks_ok(x, x_scale) || !blocks_ok(w, w_scale) || !y)) return MOE_ERR_INVALID_ARG;
+  // one 256-thread workgroup per tile, fewer than 2^32 work-items a launch
+  if (moe::matmul_tiles(instances(h->d, plan, inst_offset), n) >= (int64_t)1 << 24) return MOE_ERR_UNSUPPORTED;
   const DeviceScope on_device(h->device);
   if (!on_device.ok()) return MOE_ERR_HIP;
   return hip_rc(moe::launch_matmul(instances(h->d, plan, inst_offset), x, x_scale, w, w_scale, n, k, y, h->ws.status,
@@ -139,7 +141,6 @@ extern "C" int moex_wgrad(moe_plan_t h, const moe_plan_out* plan, const int32_t*
   const int rc = check_product(h, plan, inst_offset, n, k);
   if (rc != MOE_OK) return rc;
   if (!dw || (h->d.T > 0 && (!blocks_ok(dy, dy_scale) || !blocks_ok(x, x_scale)))) return MOE_ERR_INVALID_ARG;
-  // one 256-thread workgroup per tile, fewer than 2^32 work-items a launch
   if (moe::wgrad_tiles(instances(h->d, plan, inst_offset), n, k) >= (int64_t)1 << 24) return MOE_ERR_UNSUPPORTED;
   const DeviceScope on_device(h->device);
   if (!on_device.ok()) return MOE_ERR_HIP;

@@ -29,6 +29,9 @@ namespace {
 
 constexpr int kCombThreads = 256;
 constexpr int kRowsInFlight = 8;
+// Fewer tokens than this do not fill 256 CUs with a workgroup each.  64 tokens
+// of 8 rows of 7168: 11 -> 4.5 us, their gradient 8 -> 4.5 us.
+constexpr int kFewTokens = 512;
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -104,7 +107,8 @@ __global__ __launch_bounds__(kCombThreads) void combine_vec_kernel(Dims d, const
   const int64_t t = blockIdx.x;
   gate_weights<GIVEN>(d, t, topk_val, slot_pos, w_s, p_s, status);
   const int vpr = d.H / 8;
-  for (int base = 0; base < vpr; base += kCombThreads * VPT) {
+  // a row's columns in gridDim.y parts (few tokens), each of the same work
+  for (int base = blockIdx.y * kCombThreads * VPT; base < vpr; base += gridDim.y * kCombThreads * VPT) {
     float acc[VPT][8];
 #pragma unroll
     for (int u = 0; u < VPT; ++u)
@@ -199,24 +203,28 @@ __device__ __forceinline__ v4u scaled_row(float w, const v4u& g) {
   return y;
 }
 
-constexpr int kGradRows = 4;  // rows in flight per round (with VPT vectors each)
-
-template <int VPT>
+// ROWS of a token's k rows per workgroup; a token's workgroups are neighbours,
+// so that they find its gradient row in the caches.
+template <int VPT, int ROWS>
 __global__ __launch_bounds__(kCombThreads) void combine_grad_vec_kernel(
     Dims d, const float* __restrict__ weight, const int32_t* __restrict__ slot_pos,
     const uint16_t* __restrict__ expert_out, const uint16_t* __restrict__ grad_out,
     uint16_t* __restrict__ grad_rows, float* __restrict__ grad_weight, int32_t* __restrict__ status) {
   __shared__ float w_s[kMaxK];
   __shared__ int32_t p_s[kMaxK];
-  __shared__ float dot_s[kCombThreads / 64][kGradRows];
-  const int64_t t = blockIdx.x;
-  gate_weights<true>(d, t, weight, slot_pos, w_s, p_s, status);
+  __shared__ float dot_s[kCombThreads / 64][ROWS];
+  const int groups = (d.k + ROWS - 1) / ROWS;
   const int vpr = d.H / 8;
-  const v4u* __restrict__ g_row = reinterpret_cast<const v4u*>(grad_out) + t * vpr;
-  for (int j0 = 0; j0 < d.k; j0 += kGradRows) {
-    float dot[kGradRows];
+  const int64_t blocks = (int64_t)d.T * groups;
+  for (int64_t block = blockIdx.x; block < blocks; block += gridDim.x) {  // once, below 2^23 blocks
+    const int64_t t = block / groups;
+    const int j0 = (int)(block - t * groups) * ROWS;
+    __syncthreads();  // the last round's weights and sums have been read
+    gate_weights<true>(d, t, weight, slot_pos, w_s, p_s, status);
+    const v4u* __restrict__ g_row = reinterpret_cast<const v4u*>(grad_out) + t * vpr;
+    float dot[ROWS];
 #pragma unroll
-    for (int q = 0; q < kGradRows; ++q) dot[q] = 0.0f;
+    for (int q = 0; q < ROWS; ++q) dot[q] = 0.0f;
     for (int base = 0; base < vpr; base += kCombThreads * VPT) {
       v4u g[VPT];
 #pragma unroll
@@ -225,7 +233,7 @@ __global__ __launch_bounds__(kCombThreads) void combine_grad_vec_kernel(
         g[u] = c < vpr ? g_row[c] : v4u{0, 0, 0, 0};
       }
 #pragma unroll
-      for (int q = 0; q < kGradRows; ++q) {
+      for (int q = 0; q < ROWS; ++q) {
         const int p = j0 + q < d.k ? p_s[j0 + q] : -1;
         if (p < 0) continue;  // the same for the whole workgroup
         const v4u* x_row = reinterpret_cast<const v4u*>(expert_out) + (int64_t)p * vpr;
@@ -246,16 +254,15 @@ __global__ __launch_bounds__(kCombThreads) void combine_grad_vec_kernel(
       }
     }
 #pragma unroll
-    for (int q = 0; q < kGradRows; ++q) {
+    for (int q = 0; q < ROWS; ++q) {
       const float s = wave_sum(dot[q]);
       if ((threadIdx.x & 63) == 0) dot_s[threadIdx.x >> 6][q] = s;
     }
     __syncthreads();
-    if (threadIdx.x < kGradRows && j0 + (int)threadIdx.x < d.k) {
+    if (threadIdx.x < ROWS && j0 + (int)threadIdx.x < d.k) {
       const int q = threadIdx.x;
       grad_weight[t * d.k + j0 + q] = dot_s[0][q] + dot_s[1][q] + dot_s[2][q] + dot_s[3][q];
     }
-    __syncthreads();
   }
 }
 
@@ -293,9 +300,16 @@ hipError_t launch_sum(const Dims& d, const float* topk_val, const int32_t* slot_
   if (d.T == 0) return hipSuccess;
   const bool vec = (d.H % 8) == 0 && ((uintptr_t)expert_out % 16) == 0 && ((uintptr_t)out % 16) == 0;
   if (vec) {
-    // a row of at most kCombThreads vectors takes one round: no dead registers
-    if (d.H / 8 <= kCombThreads)
-      hipLaunchKernelGGL((combine_vec_kernel<1, GIVEN>), dim3(d.T), dim3(kCombThreads), 0, st, d, topk_val, slot_pos,
+    // A row of at most kCombThreads vectors takes one round: no dead registers.
+    // Tokens too few for the chip give each round a workgroup of its own.  Given
+    // weights take one vector a round always: four took 306 us against 192 for
+    // 8192 tokens of 8 rows of 7168, and 805 against 838 at best (loads without
+    // branches) for 32768.
+    const int rounds = (d.H / 8 + kCombThreads - 1) / kCombThreads;
+    const bool few = d.T < kFewTokens;
+    if (GIVEN || rounds == 1 || few)
+      hipLaunchKernelGGL((combine_vec_kernel<1, GIVEN>), dim3(d.T, few ? rounds : 1), dim3(kCombThreads), 0, st, d,
+                         topk_val, slot_pos,
                          reinterpret_cast<const uint4*>(expert_out), reinterpret_cast<uint4*>(out), status);
     else
       hipLaunchKernelGGL((combine_vec_kernel<4, GIVEN>), dim3(d.T), dim3(kCombThreads), 0, st, d, topk_val, slot_pos,
@@ -319,21 +333,37 @@ hipError_t launch_combine_weighted(const Dims& d, const float* weight, const int
   return launch_sum<true>(d, weight, slot_pos, expert_out, out, status, st);
 }
 
+namespace {
+
+template <int VPT, int ROWS>
+void launch_combine_grad_rows(const Dims& d, const float* weight, const int32_t* slot_pos, const uint16_t* expert_out,
+                              const uint16_t* grad_out, uint16_t* grad_expert_out, float* grad_weight,
+                              int32_t* status, hipStream_t st) {
+  const int64_t blocks = (int64_t)d.T * ((d.k + ROWS - 1) / ROWS);
+  const int64_t most = 1 << 23;  // a launch holds fewer than 2^32 work-items
+  hipLaunchKernelGGL((combine_grad_vec_kernel<VPT, ROWS>), dim3((unsigned)(blocks < most ? blocks : most)),
+                     dim3(kCombThreads), 0, st, d, weight, slot_pos, expert_out, grad_out, grad_expert_out,
+                     grad_weight, status);
+}
+
+}  // namespace
+
 hipError_t launch_combine_grad(const Dims& d, const float* weight, const int32_t* slot_pos,
                                const uint16_t* expert_out, const uint16_t* grad_out, uint16_t* grad_expert_out,
                                float* grad_weight, int32_t* status, hipStream_t st) {
   if (d.T == 0) return hipSuccess;
   const bool vec = (d.H % 8) == 0 && ((uintptr_t)expert_out % 16) == 0 && ((uintptr_t)grad_out % 16) == 0 &&
                    ((uintptr_t)grad_expert_out % 16) == 0;
+  // Four rows to a workgroup (one, two and eight measured within 3 % of it), or
+  // one where tokens are few; a row in one round of the threads or four vectors each.
+  const bool narrow = d.H / 8 <= kCombThreads;
+  auto launch = d.T < kFewTokens ? (narrow ? launch_combine_grad_rows<1, 1> : launch_combine_grad_rows<4, 1>)
+                                 : (narrow ? launch_combine_grad_rows<1, 4> : launch_combine_grad_rows<4, 4>);
   if (!vec)
     hipLaunchKernelGGL(combine_grad_u16_kernel, dim3(d.T), dim3(kCombThreads), 0, st, d, weight, slot_pos, expert_out,
                        grad_out, grad_expert_out, grad_weight, status);
-  else if (d.H / 8 <= kCombThreads)
-    hipLaunchKernelGGL((combine_grad_vec_kernel<1>), dim3(d.T), dim3(kCombThreads), 0, st, d, weight, slot_pos,
-                       expert_out, grad_out, grad_expert_out, grad_weight, status);
   else
-    hipLaunchKernelGGL((combine_grad_vec_kernel<4>), dim3(d.T), dim3(kCombThreads), 0, st, d, weight, slot_pos,
-                       expert_out, grad_out, grad_expert_out, grad_weight, status);
+    launch(d, weight, slot_pos, expert_out, grad_out, grad_expert_out, grad_weight, status, st);
   return hipGetLastError();
 }
 

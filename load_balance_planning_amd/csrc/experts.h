@@ -35,6 +35,7 @@ struct Instances {
   int32_t E;
   int64_t rows;  // T * k
 };
+int64_t matmul_tiles(const Instances& in, int32_t n);  // workgroups of launch_matmul's tile kernels (0: it loops)
 hipError_t launch_matmul(const Instances& in, const uint8_t* x, const uint8_t* xs, const uint8_t* w, const uint8_t* ws,
                          int32_t n, int32_t k, uint16_t* y, int32_t* status, hipStream_t st);
 int64_t wgrad_tiles(const Instances& in, int32_t n, int32_t k);  // workgroups of launch_wgrad

@@ -344,24 +344,36 @@ hipError_t launch_tiles(const Instances& in, const uint8_t* x, const uint8_t* xs
 
 }  // namespace
 
+namespace {
+
+// The tile of a product, 0 for the streaming kernel, by the mean of rows per expert (the loads themselves are on the device):
+//   up to 8   bound by the matrices, which the streaming kernel reads straight
+//             into registers (128 experts of 1536 x 2048, 512 rows: 75 us
+//             against 89 in 128 x 128 tiles; 2048 rows: 99 against 91)
+//   large     256 x 256 tiles, where rows fill them and there are two for
+//             every CU (32768 rows: 201 us against 209 in 128 x 128 tiles; 4096
+//             rows: 131 against 98; 8 experts of 768 x 1024, 8192 rows, 96
+//             tiles: 20 against 14)
+//   between   128 x 128 tiles, two workgroups to a CU
+int matmul_tile(const Instances& in, int n) {
+  if (in.rows <= (int64_t)8 * in.E) return 0;
+  const bool fills = in.rows / 256 * ((n + 255) / 256) >= 512;
+  return in.rows >= (int64_t)192 * in.E && fills ? 256 : 128;
+}
+
+}  // namespace
+
+int64_t matmul_tiles(const Instances& in, int32_t n) {
+  const int tile = matmul_tile(in, n);
+  return tile == 0 ? 0 : row_tile_ids(in, tile) * ((n + tile - 1) / tile);
+}
+
 hipError_t launch_matmul(const Instances& in, const uint8_t* x, const uint8_t* xs, const uint8_t* w, const uint8_t* ws,
                          int32_t n, int32_t k, uint16_t* y, int32_t* status, hipStream_t st) {
   if (in.rows == 0) return hipSuccess;
-  // By the mean of rows per expert (the loads themselves are on the device):
-  //   up to 8   bound by the matrices, which the streaming kernel reads straight
-  //             into registers (128 experts of 1536 x 2048, 512 rows: 75 us
-  //             against 89 in 128 x 128 tiles; 2048 rows: 99 against 91)
-  //   large     256 x 256 tiles, where rows fill them and there are two for
-  //             every CU (32768 rows: 201 us against 209 in 128 x 128 tiles; 4096
-  //             rows: 131 against 98; 8 experts of 768 x 1024, 8192 rows, 96
-  //             tiles: 20 against 14)
-  //   between   128 x 128 tiles, two workgroups to a CU
-  if (in.rows > (int64_t)8 * in.E) {
-    const int64_t big = in.rows / 256 * ((n + 255) / 256);
-    if (in.rows >= (int64_t)192 * in.E && big >= 512)
-      return launch_tiles<256, 256, 2, 2>(in, x, xs, w, ws, n, k, y, status, st);
-    return launch_tiles<128, 128, 2, 2>(in, x, xs, w, ws, n, k, y, status, st);
-  }
+  const int tile = matmul_tile(in, n);
+  if (tile == 256) return launch_tiles<256, 256, 2, 2>(in, x, xs, w, ws, n, k, y, status, st);
+  if (tile == 128) return launch_tiles<128, 128, 2, 2>(in, x, xs, w, ws, n, k, y, status, st);
   const int64_t tiles = row_tile_ids(in, kRowsS) * ((n + kChanS - 1) / kChanS);
   const int64_t grid = tiles < (1 << 20) ? tiles : (1 << 20);
   hipLaunchKernelGGL(matmul_rows16_kernel, dim3((unsigned)grid), dim3(256), 0, st, in, x, xs, w, ws, n, k, tiles, y,
