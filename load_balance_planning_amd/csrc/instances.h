@@ -41,32 +41,33 @@ __device__ __forceinline__ void check_instances(const Instances& in, int32_t* st
 // Row tiles of ROWS rows.  Instance i owns the tile ids from offset[i] / ROWS + i
 // on: offset[i+1] / ROWS - offset[i] / ROWS + 1 ids, at least as many as its
 // rows need, so ids rise with i, need no prefix sum, and there are at most
-// rows / ROWS + n_inst of them.  The instance of an id is found by one wave
-// in two loads of 64 offsets each (cap <= 3072).  Every lane of the wave calls
-// this and gets the same answer; false: no rows under this id.
+// rows / ROWS + n_inst of them.  The instance of an id is found by one wave in
+// two rounds of loads, 64 instances each (cap <= 3072; the count arrives with
+// the first, the instance's rows and expert with the second).  Every lane of
+// the wave calls this and gets the same answer, in scalars (rows < 2^31);
+// false: no rows under this id.
 template <int ROWS>
-__device__ __forceinline__ bool find_row_tile(const Instances& in, int n_inst, int64_t id, Span* span, int64_t* row) {
+__device__ __forceinline__ bool find_row_tile(const Instances& in, int64_t id, Span* span, int64_t* row) {
   const int lane = threadIdx.x & 63;
-  const int stride = (n_inst + 63) / 64;
-  auto at_or_before = [&](int i) { return i < n_inst && (int64_t)in.offset[i] / ROWS + i <= id; };
-  const uint64_t coarse = __ballot(at_or_before(lane * stride));
+  const int stride = (in.cap + 63) / 64;
+  const int probe = min(lane * stride, in.cap);  // offset has cap + 1 entries
+  const int at_probe = in.offset[probe];
+  const int n_inst = instance_count(in);
+  const uint64_t coarse = __ballot(lane * stride < n_inst && (int64_t)at_probe / ROWS + lane * stride <= id);
   if (coarse == 0ull) return false;
   const int first = (__popcll(coarse) - 1) * stride;
-  const uint64_t fine = __ballot(lane < stride && at_or_before(first + lane));
+  const int i = min(first + lane, in.cap - 1);
+  const int begin = in.offset[i], end = in.offset[i + 1], expert = in.expert[i];
+  const uint64_t fine = __ballot(lane < stride && first + lane < n_inst && (int64_t)begin / ROWS + first + lane <= id);
   if (fine == 0ull) return false;
-  const int i = first + __popcll(fine) - 1;
-  if (i >= n_inst || !instance_span(in, i, span)) return false;
-  *row = span->begin + (id - (span->begin / ROWS + i)) * ROWS;
-  return *row >= span->begin && *row < span->end;
-}
-
-// The same tile in scalar registers (rows < 2^31): every lane holds the same
-// values, which the compiler cannot see.
-__device__ __forceinline__ void keep_in_scalars(Span* s, int64_t* row) {
-  s->begin = __builtin_amdgcn_readfirstlane((int)s->begin);
-  s->end = __builtin_amdgcn_readfirstlane((int)s->end);
-  s->expert = __builtin_amdgcn_readfirstlane(s->expert);
-  *row = __builtin_amdgcn_readfirstlane((int)*row);
+  const int who = __popcll(fine) - 1;  // lane of the instance
+  span->begin = __builtin_amdgcn_readlane(begin, who);
+  span->end = __builtin_amdgcn_readlane(end, who);
+  span->expert = __builtin_amdgcn_readlane(expert, who);
+  const int64_t r = span->begin + (id - (span->begin / ROWS + first + who)) * ROWS;
+  *row = __builtin_amdgcn_readfirstlane((int)r);
+  return span->begin >= 0 && span->begin <= span->end && span->end <= in.rows &&
+         (unsigned)span->expert < (unsigned)in.E && r >= span->begin && r < span->end;
 }
 
 // Upper bound of the tile ids.

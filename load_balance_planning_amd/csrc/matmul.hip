@@ -49,13 +49,12 @@ __global__ __launch_bounds__(256) void matmul_rows16_kernel(Instances in, const 
   const int nb = (k + kBlk - 1) / kBlk, ns = (nb + 3) / 4 * 4;
   const int64_t kp = (int64_t)nb * kBlk;
   const int nbn = (n + kBlk - 1) / kBlk, nct = (n + kChanS - 1) / kChanS;
-  const int n_inst = instance_count(in);
   for (int64_t id = blockIdx.x; id < tiles; id += gridDim.x) {
     const int64_t rt = id / nct;
     const int c0 = (int)(id - rt * nct) * kChanS;
     Span sp;
     int64_t r0;
-    if (!find_row_tile<kRowsS>(in, n_inst, rt, &sp, &r0)) continue;  // the same for all waves
+    if (!find_row_tile<kRowsS>(in, rt, &sp, &r0)) continue;  // the same for all waves
     const int64_t row = min(r0 + r, sp.end - 1);
     const uint8_t* xp = x + row * kp;
     const uint8_t* xsp = xs + row * ns;
@@ -182,8 +181,7 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), 1) void matm
   const int cbase = __builtin_amdgcn_readfirstlane(in_band / band_rows * BC);
   Span sp;
   int64_t r0;
-  if (!find_row_tile<BT>(in, instance_count(in), rt, &sp, &r0)) return;
-  keep_in_scalars(&sp, &r0);
+  if (!find_row_tile<BT>(in, rt, &sp, &r0)) return;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 31, g = lane >> 5;

@@ -53,36 +53,43 @@ struct GradShape {
 };
 
 // The steps of an expert: 64 rows of one instance at a time, instances in
-// order.  Every lane of a wave steps alike.
+// order.  Every lane of a wave steps alike, and holds one of the 64 instances
+// from i0 on, whose bit is set in `mask` if it is a good one of the expert's.
 struct Steps {
   int n_inst, expert;
-  int i0;            // instances from here on are in `mask`
+  int i0;
   uint64_t mask;
-  int row, end;      // rows < 2^31
+  int begin, end_of;  // this lane's instance
+  int row, end;       // the instance under way (rows < 2^31)
 };
+__device__ __forceinline__ void steps_load(Steps* s, const Instances& in) {
+  const int mine = s->i0 + (threadIdx.x & 63), i = min(mine, in.cap - 1);
+  s->begin = in.offset[i];
+  s->end_of = in.offset[i + 1];
+  const int e = in.expert[i];
+  s->mask = __ballot(mine < s->n_inst && e == s->expert && s->begin >= 0 && s->begin <= s->end_of &&
+                     s->end_of <= in.rows);
+}
 __device__ __forceinline__ void steps_begin(Steps* s, const Instances& in, int expert) {
-  s->n_inst = __builtin_amdgcn_readfirstlane(instance_count(in));
   s->expert = expert;
-  s->i0 = -64;
-  s->mask = 0ull;
+  s->i0 = 0;
   s->row = s->end = 0;
+  s->n_inst = instance_count(in);
+  steps_load(s, in);
 }
 // The next step's first row and its rows (0: no more).
 __device__ __forceinline__ void next_step(Steps* s, const Instances& in, int* row, int* rows) {
-  const int lane = threadIdx.x & 63;
   while (s->row >= s->end) {
     if (s->mask == 0ull) {
       if (s->i0 + 64 >= s->n_inst) break;
       s->i0 += 64;
-      s->mask = __ballot(s->i0 + lane < s->n_inst && in.expert[min(s->i0 + lane, s->n_inst - 1)] == s->expert);
+      steps_load(s, in);
       continue;
     }
-    const int i = s->i0 + __ffsll((unsigned long long)s->mask) - 1;
+    const int who = __ffsll((unsigned long long)s->mask) - 1;
     s->mask &= s->mask - 1;
-    Span sp;
-    const bool ok = instance_span(in, i, &sp);
-    s->row = __builtin_amdgcn_readfirstlane(ok ? (int)sp.begin : 0);
-    s->end = __builtin_amdgcn_readfirstlane(ok ? (int)sp.end : 0);
+    s->row = __builtin_amdgcn_readlane(s->begin, who);
+    s->end = __builtin_amdgcn_readlane(s->end_of, who);
   }
   *row = s->row;
   *rows = min(kStepRows, s->end - s->row);
