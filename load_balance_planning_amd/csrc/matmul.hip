@@ -154,57 +154,111 @@ struct TileShape {
   static_assert(BC * kBlk % (16 * kThreads) == 0 && BT * kBlk % (16 * kThreads) == 0, "whole passes");
 };
 
+// The row tiles of the instances: pre[i] of them before instance i, as many as
+// the rows need (a bad instance has none).  All threads of a workgroup of 256.
+__device__ __forceinline__ int count_row_tiles(const Instances& in, int rows, int32_t* pre, int32_t* sums) {
+  const int n = instance_count(in), per = (n + 255) / 256;
+  const int first = threadIdx.x * per;
+  Span sp;
+  int mine = 0;
+  for (int i = first; i < min(first + per, n); ++i)
+    if (instance_span(in, i, &sp)) mine += (int)((sp.end - sp.begin + rows - 1) / rows);
+  int incl = mine;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int o = __shfl_up(incl, off);
+    incl += (threadIdx.x & 63) >= off ? o : 0;
+  }
+  if ((threadIdx.x & 63) == 63) sums[threadIdx.x >> 6] = incl;
+  __syncthreads();
+  int before = incl - mine;
+  for (int q = 0; q < (int)(threadIdx.x >> 6); ++q) before += sums[q];
+  for (int i = first; i < min(first + per, n); ++i) {
+    pre[i] = before;
+    if (instance_span(in, i, &sp)) before += (int)((sp.end - sp.begin + rows - 1) / rows);
+  }
+  const int total = sums[0] + sums[1] + sums[2] + sums[3];
+  if (threadIdx.x == 0) pre[n] = total;
+  __syncthreads();
+  return total;
+}
+
+// The instance of row tile t < pre[n]: the last with pre[i] <= t.  One wave, two rounds of 64.
+__device__ __forceinline__ int instance_of(const int32_t* pre, int n, int t) {
+  const int lane = threadIdx.x & 63, stride = (n + 63) / 64;
+  const uint64_t coarse = __ballot(lane * stride < n && pre[min(lane * stride, n)] <= t);
+  const int first = (__popcll(coarse) - 1) * stride;
+  const uint64_t fine = __ballot(lane < stride && first + lane < n && pre[min(first + lane, n)] <= t);
+  return first + __popcll(fine) - 1;
+}
+
+// Persistent: workgroup b takes every (gridDim.x / 8)-th tile of its XCD's run.
+// (A workgroup per tile left the CUs without one for 22 % of the time on short
+// axes: 131072 rows, 2048 x 1536, @@DX@@.)
 template <int BC, int BT, int WC, int WT>
-__global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), 1) void matmul_tile_kernel(
+__global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), BC == 256 ? 1 : 2) void matmul_tile_kernel(
     Instances in, const uint8_t* __restrict__ x, const uint8_t* __restrict__ xs, const uint8_t* __restrict__ w,
-    const uint8_t* __restrict__ ws, int n, int k, int64_t row_tiles, uint16_t* __restrict__ y,
-    int32_t* __restrict__ status) {
+    const uint8_t* __restrict__ ws, int n, int k, uint16_t* __restrict__ y, int32_t* __restrict__ status) {
 #ifdef __HIP_DEVICE_COMPILE__
   using S = TileShape<BC, BT, WC, WT>;
   __shared__ __align__(256) unsigned char c0_s[BC * kBlk];
   __shared__ __align__(256) unsigned char t0_s[BT * kBlk];
   __shared__ __align__(256) unsigned char c1_s[BC * kBlk];
   __shared__ __align__(256) unsigned char t1_s[BT * kBlk];
+  __shared__ int32_t pre[kMaxE + kMaxB + 1];
+  __shared__ int32_t sums[4];
   if (blockIdx.x == 0) check_instances(in, status);
   const int nct = (n + BC - 1) / BC;
+  const int n_inst = instance_count(in);
+  const int row_tiles = __builtin_amdgcn_readfirstlane(count_row_tiles(in, BT, pre, sums));
   // Workgroups go to the eight XCDs in turn: each XCD takes a run of
   // consecutive tiles, four row tiles by all channel tiles at a time, so that
   // the tiles that it works on at once share their operands in its L2.
-  const int64_t total = row_tiles * nct;
-  const int64_t per = (total + 7) / 8;
-  const int64_t id = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if ((int64_t)(blockIdx.x >> 3) >= per || id >= total) return;
-  const int64_t band = id / (4 * nct);
-  const int in_band = (int)(id - band * 4 * nct);
-  const int band_rows = (int)min((int64_t)4, row_tiles - band * 4);
-  const int64_t rt = band * 4 + in_band % band_rows;
-  const int cbase = __builtin_amdgcn_readfirstlane(in_band / band_rows * BC);
-  Span sp;
-  int64_t r0;
-  if (!find_row_tile<BT>(in, rt, &sp, &r0)) return;
+  const int total = row_tiles * nct;  // below 2^24
+  const int xcd = blockIdx.x & 7, slots = gridDim.x >> 3;
+  const int last = (int)((int64_t)total * (xcd + 1) / 8);
+  int tile = (int)((int64_t)total * xcd / 8) + (blockIdx.x >> 3);
+  if (tile >= last) return;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 31, g = lane >> 5;
   const int nb = (k + kBlk - 1) / kBlk, ns = (nb + 3) / 4 * 4;
   const uint32_t kp = (uint32_t)nb * kBlk;
   const int nbn = (n + kBlk - 1) / kBlk;
-  const int rows_left = (int)min((int64_t)BT, sp.end - r0), chans_left = min(BC, n - cbase);
   // where this thread's pieces come from: the same place of every pass
   constexpr int kRowsPerPass = S::kThreads / 8;
   static_assert(kRowsPerPass % 32 == 0, "the swizzle does not change from pass to pass");
   const int pair = threadIdx.x >> 4;
   const int place_c = (threadIdx.x & 15) ^ piece_swizzle<true>(pair);
   const int place_t = (threadIdx.x & 15) ^ piece_swizzle<false>(pair);
-  uint32_t off_c[S::kPassC], off_t[S::kPassT];
+  const int wc = wave % WC * S::kWaveC, wt = wave / WC * S::kWaveT;
+  // the tile: its rows, channels, expert
+  int r0, rows_left, cbase, chans_left, expert;
+  auto locate = [&](int t) {
+    const int band = t / (4 * nct), in_band = t - band * 4 * nct;
+    const int band_rows = min(4, row_tiles - band * 4);
+    const int rt = band * 4 + in_band % band_rows;
+    const int i = instance_of(pre, n_inst, rt);
+    cbase = __builtin_amdgcn_readfirstlane(in_band / band_rows * BC);
+    chans_left = min(BC, n - cbase);
+    r0 = __builtin_amdgcn_readfirstlane(in.offset[i] + (rt - pre[i]) * BT);
+    rows_left = min(BT, __builtin_amdgcn_readfirstlane(in.offset[i + 1]) - r0);
+    expert = __builtin_amdgcn_readfirstlane(in.expert[i]);
+  };
+  uint32_t off_c[S::kPassC], off_t[S::kPassT], xs_off[S::kT];
+  auto set_offsets = [&]() {
 #pragma unroll
-  for (int q = 0; q < S::kPassC; ++q)
-    off_c[q] = (uint32_t)min(q * kRowsPerPass + 2 * pair + (place_c >> 3), chans_left - 1) * kp + 16 * (place_c & 7);
+    for (int q = 0; q < S::kPassC; ++q)
+      off_c[q] = (uint32_t)min(q * kRowsPerPass + 2 * pair + (place_c >> 3), chans_left - 1) * kp + 16 * (place_c & 7);
 #pragma unroll
-  for (int q = 0; q < S::kPassT; ++q)
-    off_t[q] = (uint32_t)min(q * kRowsPerPass + 2 * pair + (place_t >> 3), rows_left - 1) * kp + 16 * (place_t & 7);
-  const auto w_buf = buffer_of(w + ((int64_t)sp.expert * n + cbase) * kp, (uint32_t)chans_left * kp);
-  const auto x_buf = buffer_of(x + r0 * kp, (uint32_t)rows_left * kp);
+    for (int q = 0; q < S::kPassT; ++q)
+      off_t[q] = (uint32_t)min(q * kRowsPerPass + 2 * pair + (place_t >> 3), rows_left - 1) * kp + 16 * (place_t & 7);
+#pragma unroll
+    for (int j = 0; j < S::kT; ++j) xs_off[j] = (uint32_t)(min(wt + 32 * j + r, rows_left - 1) * ns);
+  };
   auto load = [&](unsigned char* c_s, unsigned char* t_s, int b) {
+    const auto w_buf = buffer_of(w + ((int64_t)expert * n + cbase) * kp, (uint32_t)chans_left * kp);
+    const auto x_buf = buffer_of(x + (int64_t)r0 * kp, (uint32_t)rows_left * kp);
 #pragma unroll
     for (int q = 0; q < S::kPassC; ++q)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(w_buf, (lds_ptr)(c_s + (q * S::kThreads + wave * 64) * 16), 16, off_c[q],
@@ -214,16 +268,12 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), 1) void matm
       __builtin_amdgcn_raw_ptr_buffer_load_lds(x_buf, (lds_ptr)(t_s + (q * S::kThreads + wave * 64) * 16), 16, off_t[q],
                                                b * kBlk, 0, 0);
   };
-  const int wc = wave % WC * S::kWaveC, wt = wave / WC * S::kWaveT;
   // scales, four blocks to a word: of this lane's row in each instruction
   // tile, and of the wave's channels
-  const auto xs_buf = buffer_of(xs + r0 * ns, (uint32_t)(rows_left * ns));
-  uint32_t xs_off[S::kT];
-#pragma unroll
-  for (int j = 0; j < S::kT; ++j) xs_off[j] = (uint32_t)(min(wt + 32 * j + r, rows_left - 1) * ns);
-  const uint8_t* ws_base = ws + ((int64_t)sp.expert * nbn + min((cbase + wc) / kBlk, nbn - 1)) * ns;
   int sx[S::kT], sw, sx_next[S::kT], sw_next;
   auto load_scales = [&](int b) {
+    const auto xs_buf = buffer_of(xs + (int64_t)r0 * ns, (uint32_t)(rows_left * ns));
+    const uint8_t* ws_base = ws + ((int64_t)expert * nbn + min((cbase + wc) / kBlk, nbn - 1)) * ns;
 #pragma unroll
     for (int j = 0; j < S::kT; ++j) sx_next[j] = (int)__builtin_amdgcn_raw_buffer_load_b32(xs_buf, xs_off[j], b & ~3, 0);
     sw_next = *reinterpret_cast<const int*>(ws_base + (b & ~3));
@@ -244,12 +294,6 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), 1) void matm
   const int at_c = piece_at<true>(wc + 16 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3), g);
   const int at_t = piece_at<false>(wt + r, g);
   acc16 acc[S::kC][S::kT];
-#pragma unroll
-  for (int i = 0; i < S::kC; ++i)
-#pragma unroll
-    for (int j = 0; j < S::kT; ++j)
-#pragma unroll
-      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
   struct Half {
     v8i c[S::kC], t[S::kT];
   };
@@ -286,57 +330,78 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), 1) void matm
       if (loads) __builtin_amdgcn_sched_group_barrier(0x020, (S::kPassC + S::kPassT + kProducts - 1) / kProducts, 0);
     }
   };
-  Half f0, f1;
+  const bool vec = n % 8 == 0 && ((uintptr_t)y & 15) == 0;
+  static_assert(S::kWaves == 4, "a quarter of (c1_s, t1_s) for each wave");
+  constexpr int kOwn = (BC + BT) * kBlk / 4, kTurns = S::kWaveC * S::kWaveT * 2 / kOwn;
+  unsigned char* own = (wave < 2 ? c1_s : t1_s) + (wave & 1) * kOwn;
+  static_assert(kTurns >= 1 && BC == BT, "parts of one size");
+  locate(tile);
+  set_offsets();
   load_scales(0);
   load(c0_s, t0_s, 0);
-  sync_with_loads();
-  load(c1_s, t1_s, min(1, nb - 1));
-  read(&f0, c0_s, t0_s, 0);
-  // No branch inside a round: past the last block the loads and reads take
-  // some block again, which nothing uses.
-  for (int b = 0; b + 2 <= nb; b += 2) {
-    take_scales(b);
-    read(&f1, c0_s, t0_s, 1);
-    multiply(f0);
-    spread(false);
+  for (;;) {
+#pragma unroll
+    for (int i = 0; i < S::kC; ++i)
+#pragma unroll
+      for (int j = 0; j < S::kT; ++j)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
+    Half f0, f1;
     sync_with_loads();
-    load(c0_s, t0_s, min(b + 2, nb - 1));
-    read(&f0, c1_s, t1_s, 0);
-    multiply(f1);
-    spread(true);
-    next_scales();
-    read(&f1, c1_s, t1_s, 1);
-    multiply(f0);
-    spread(false);
-    sync_with_loads();
-    load_scales(min(b + 2, nb - 1));
-    load(c1_s, t1_s, min(b + 3, nb - 1));
+    load(c1_s, t1_s, min(1, nb - 1));
     read(&f0, c0_s, t0_s, 0);
-    multiply(f1);
-    spread(true);
+    // No branch inside a round: past the last block the loads and reads take
+    // some block again, which nothing uses.
+    for (int b = 0; b + 2 <= nb; b += 2) {
+      take_scales(b);
+      read(&f1, c0_s, t0_s, 1);
+      multiply(f0);
+      spread(false);
+      sync_with_loads();
+      load(c0_s, t0_s, min(b + 2, nb - 1));
+      read(&f0, c1_s, t1_s, 0);
+      multiply(f1);
+      spread(true);
+      next_scales();
+      read(&f1, c1_s, t1_s, 1);
+      multiply(f0);
+      spread(false);
+      sync_with_loads();
+      load_scales(min(b + 2, nb - 1));
+      load(c1_s, t1_s, min(b + 3, nb - 1));
+      read(&f0, c0_s, t0_s, 0);
+      multiply(f1);
+      spread(true);
+    }
+    if (nb & 1) {
+      take_scales(nb - 1);
+      read(&f1, c0_s, t0_s, 1);
+      multiply(f0);
+      multiply(f1);
+    }
+    sync_with_loads();  // every wave has its last operands, and no load into LDS is under way
+    // The next tile's first block comes in while this one's results go out.
+    const int done_r0 = r0, done_c = cbase, done_rows = rows_left, done_chans = chans_left;
+    tile += slots;
+    const bool more = tile < last;
+    if (more) {
+      locate(tile);
+      set_offsets();
+      load_scales(0);
+      load(c0_s, t0_s, 0);
+    }
+    store_wave_tile<kTurns>(acc, own, y + (int64_t)(done_r0 + wt) * n + done_c + wc, n, done_rows - wt, done_chans - wc, vec);
+    if (!more) break;
   }
-  sync_with_loads();  // also: no load into LDS may be under way when the workgroup ends
-  if (nb & 1) {
-    take_scales(nb - 1);
-    read(&f1, c0_s, t0_s, 1);
-    multiply(f0);
-    multiply(f1);
-  }
-  __syncthreads();  // every wave has its last operands: LDS is free
-  static_assert(S::kWaves == 4, "a part of LDS for each wave");
-  static_assert(S::kWaveC * S::kWaveT * 2 <= (BC < BT ? BC : BT) * kBlk, "a wave's result fits its part");
-  unsigned char* own = wave == 0 ? c0_s : wave == 1 ? t0_s : wave == 2 ? c1_s : t1_s;
-  store_wave_tile(acc, own, y + (r0 + wt) * n + cbase + wc, n, rows_left - wt, chans_left - wc,
-                  n % 8 == 0 && ((uintptr_t)y & 15) == 0);
 #endif
 }
 
 template <int BC, int BT, int WC, int WT>
 hipError_t launch_tiles(const Instances& in, const uint8_t* x, const uint8_t* xs, const uint8_t* w, const uint8_t* ws,
                         int n, int k, uint16_t* y, int32_t* status, hipStream_t st) {
-  const int64_t row_tiles = row_tile_ids(in, BT), total = row_tiles * ((n + BC - 1) / BC);
-  hipLaunchKernelGGL((matmul_tile_kernel<BC, BT, WC, WT>), dim3((unsigned)((total + 7) / 8 * 8)),
-                     dim3(TileShape<BC, BT, WC, WT>::kThreads), 0, st, in, x, xs, w, ws, n, k, row_tiles, y, status);
+  const int64_t most = row_tile_ids(in, BT) * ((n + BC - 1) / BC), resident = BC == 256 ? 256 : 512;
+  hipLaunchKernelGGL((matmul_tile_kernel<BC, BT, WC, WT>), dim3((unsigned)((most < resident ? most : resident) + 7) / 8 * 8),
+                     dim3(TileShape<BC, BT, WC, WT>::kThreads), 0, st, in, x, xs, w, ws, n, k, y, status);
   return hipGetLastError();
 }
 
