@@ -207,6 +207,10 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), BC == 256 ? 
   __shared__ __align__(256) unsigned char t1_s[BT * kBlk];
   __shared__ int32_t pre[kMaxE + kMaxB + 1];
   __shared__ int32_t sums[4];
+  // where results pass: a place of their own, or (where two workgroups share
+  // the CU's LDS) the second stage, whose next block then comes in later
+  constexpr bool kOwnPlace = BC == 256;
+  __shared__ __align__(16) unsigned char out_s[kOwnPlace ? 4 * 4096 : 16];
   if (blockIdx.x == 0) check_instances(in, status);
   const int nct = (n + BC - 1) / BC;
   const int n_inst = instance_count(in);
@@ -232,33 +236,38 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), BC == 256 ? 
   const int place_c = (threadIdx.x & 15) ^ piece_swizzle<true>(pair);
   const int place_t = (threadIdx.x & 15) ^ piece_swizzle<false>(pair);
   const int wc = wave % WC * S::kWaveC, wt = wave / WC * S::kWaveT;
-  // the tile: its rows, channels, expert
-  int r0, rows_left, cbase, chans_left, expert;
+  // a tile: its rows, channels, expert
+  struct Tile {
+    int r0, rows, c0, chans, expert;
+  };
   auto locate = [&](int t) {
     const int band = t / (4 * nct), in_band = t - band * 4 * nct;
     const int band_rows = min(4, row_tiles - band * 4);
     const int rt = band * 4 + in_band % band_rows;
     const int i = instance_of(pre, n_inst, rt);
-    cbase = __builtin_amdgcn_readfirstlane(in_band / band_rows * BC);
-    chans_left = min(BC, n - cbase);
-    r0 = __builtin_amdgcn_readfirstlane(in.offset[i] + (rt - pre[i]) * BT);
-    rows_left = min(BT, __builtin_amdgcn_readfirstlane(in.offset[i + 1]) - r0);
-    expert = __builtin_amdgcn_readfirstlane(in.expert[i]);
+    Tile o;
+    o.c0 = __builtin_amdgcn_readfirstlane(in_band / band_rows * BC);
+    o.chans = min(BC, n - o.c0);
+    o.r0 = __builtin_amdgcn_readfirstlane(in.offset[i] + (rt - pre[i]) * BT);
+    o.rows = min(BT, __builtin_amdgcn_readfirstlane(in.offset[i + 1]) - o.r0);
+    o.expert = __builtin_amdgcn_readfirstlane(in.expert[i]);
+    return o;
   };
+  Tile at;
   uint32_t off_c[S::kPassC], off_t[S::kPassT], xs_off[S::kT];
   auto set_offsets = [&]() {
 #pragma unroll
     for (int q = 0; q < S::kPassC; ++q)
-      off_c[q] = (uint32_t)min(q * kRowsPerPass + 2 * pair + (place_c >> 3), chans_left - 1) * kp + 16 * (place_c & 7);
+      off_c[q] = (uint32_t)min(q * kRowsPerPass + 2 * pair + (place_c >> 3), at.chans - 1) * kp + 16 * (place_c & 7);
 #pragma unroll
     for (int q = 0; q < S::kPassT; ++q)
-      off_t[q] = (uint32_t)min(q * kRowsPerPass + 2 * pair + (place_t >> 3), rows_left - 1) * kp + 16 * (place_t & 7);
+      off_t[q] = (uint32_t)min(q * kRowsPerPass + 2 * pair + (place_t >> 3), at.rows - 1) * kp + 16 * (place_t & 7);
 #pragma unroll
-    for (int j = 0; j < S::kT; ++j) xs_off[j] = (uint32_t)(min(wt + 32 * j + r, rows_left - 1) * ns);
+    for (int j = 0; j < S::kT; ++j) xs_off[j] = (uint32_t)(min(wt + 32 * j + r, at.rows - 1) * ns);
   };
   auto load = [&](unsigned char* c_s, unsigned char* t_s, int b) {
-    const auto w_buf = buffer_of(w + ((int64_t)expert * n + cbase) * kp, (uint32_t)chans_left * kp);
-    const auto x_buf = buffer_of(x + (int64_t)r0 * kp, (uint32_t)rows_left * kp);
+    const auto w_buf = buffer_of(w + ((int64_t)at.expert * n + at.c0) * kp, (uint32_t)at.chans * kp);
+    const auto x_buf = buffer_of(x + (int64_t)at.r0 * kp, (uint32_t)at.rows * kp);
 #pragma unroll
     for (int q = 0; q < S::kPassC; ++q)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(w_buf, (lds_ptr)(c_s + (q * S::kThreads + wave * 64) * 16), 16, off_c[q],
@@ -272,8 +281,8 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), BC == 256 ? 
   // tile, and of the wave's channels
   int sx[S::kT], sw, sx_next[S::kT], sw_next;
   auto load_scales = [&](int b) {
-    const auto xs_buf = buffer_of(xs + (int64_t)r0 * ns, (uint32_t)(rows_left * ns));
-    const uint8_t* ws_base = ws + ((int64_t)expert * nbn + min((cbase + wc) / kBlk, nbn - 1)) * ns;
+    const auto xs_buf = buffer_of(xs + (int64_t)at.r0 * ns, (uint32_t)(at.rows * ns));
+    const uint8_t* ws_base = ws + ((int64_t)at.expert * nbn + min((at.c0 + wc) / kBlk, nbn - 1)) * ns;
 #pragma unroll
     for (int j = 0; j < S::kT; ++j) sx_next[j] = (int)__builtin_amdgcn_raw_buffer_load_b32(xs_buf, xs_off[j], b & ~3, 0);
     sw_next = *reinterpret_cast<const int*>(ws_base + (b & ~3));
@@ -331,15 +340,18 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), BC == 256 ? 
     }
   };
   const bool vec = n % 8 == 0 && ((uintptr_t)y & 15) == 0;
-  static_assert(S::kWaves == 4, "a quarter of (c1_s, t1_s) for each wave");
-  constexpr int kOwn = (BC + BT) * kBlk / 4, kTurns = S::kWaveC * S::kWaveT * 2 / kOwn;
-  unsigned char* own = (wave < 2 ? c1_s : t1_s) + (wave & 1) * kOwn;
-  static_assert(kTurns >= 1 && BC == BT, "parts of one size");
-  locate(tile);
+  static_assert(S::kWaves == 4 && BC == BT, "four equal parts");
+  constexpr int kTI = kOwnPlace ? S::kC / 2 : 1, kTJ = kOwnPlace ? S::kT : 1;  // turns of 64 channels by 32 rows, or one
+  constexpr int kOwn = 2 * S::kWaveC * S::kWaveT / (kTI * kTJ);
+  static_assert(kOwn <= (kOwnPlace ? 4096 : BC * kBlk / 2), "a turn fits the wave's part");
+  unsigned char* own = kOwnPlace ? out_s + wave * 4096 : (wave < 2 ? c1_s : t1_s) + (wave & 1) * kOwn;
+  at = locate(tile);
   set_offsets();
   load_scales(0);
   load(c0_s, t0_s, 0);
+  if (kOwnPlace) load(c1_s, t1_s, min(1, nb - 1));
   for (;;) {
+    const Tile next = locate(min(tile + slots, last - 1));  // arrives while this tile's products run
 #pragma unroll
     for (int i = 0; i < S::kC; ++i)
 #pragma unroll
@@ -348,7 +360,7 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), BC == 256 ? 
         for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
     Half f0, f1;
     sync_with_loads();
-    load(c1_s, t1_s, min(1, nb - 1));
+    if (!kOwnPlace) load(c1_s, t1_s, min(1, nb - 1));
     read(&f0, c0_s, t0_s, 0);
     // No branch inside a round: past the last block the loads and reads take
     // some block again, which nothing uses.
@@ -380,17 +392,19 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), BC == 256 ? 
       multiply(f1);
     }
     sync_with_loads();  // every wave has its last operands, and no load into LDS is under way
-    // The next tile's first block comes in while this one's results go out.
-    const int done_r0 = r0, done_c = cbase, done_rows = rows_left, done_chans = chans_left;
+    // The next tile's first blocks come in while this one's results go out.
+    const Tile done = at;
     tile += slots;
     const bool more = tile < last;
     if (more) {
-      locate(tile);
+      at = next;
       set_offsets();
       load_scales(0);
       load(c0_s, t0_s, 0);
+      if (kOwnPlace) load(c1_s, t1_s, min(1, nb - 1));
     }
-    store_wave_tile<kTurns>(acc, own, y + (int64_t)(done_r0 + wt) * n + done_c + wc, n, done_rows - wt, done_chans - wc, vec);
+    store_wave_tile<kTI, kTJ>(acc, own, y + (int64_t)(done.r0 + wt) * n + done.c0 + wc, n, done.rows - wt,
+                              done.chans - wc, vec);
     if (!more) break;
   }
 #endif

@@ -288,7 +288,7 @@ __global__ __launch_bounds__(kThreads, COLS == 256 ? 1 : 2) void wgrad_kernel(In
   __syncthreads();  // every wave has its last operands: LDS is free
   unsigned char* own = wave == 0 ? x0_s : wave == 1 ? y0_s : wave == 2 ? x1_s : y1_s;
   const int c = tn * COLS + wn, col = tk * COLS + wk;
-  store_wave_tile<1>(acc, own, dw + ((int64_t)e * n + c) * k + col, k, n - c, k - col,
+  store_wave_tile<1, 1>(acc, own, dw + ((int64_t)e * n + c) * k + col, k, n - c, k - col,
                   k % 8 == 0 && ((uintptr_t)dw & 15) == 0);
 #endif
 }
