@@ -42,7 +42,7 @@ __device__ __forceinline__ void check_instances(const Instances& in, int32_t* st
 // on: offset[i+1] / ROWS - offset[i] / ROWS + 1 ids, at least as many as its
 // rows need, so ids rise with i, need no prefix sum, and there are at most
 // rows / ROWS + n_inst of them.  The instance of an id is found by one wave in
-// two rounds of loads, 64 instances each (cap <= 3072; the count arrives with
+// two rounds of loads, 64 instances each (cap <= 64 * 64; the count arrives with
 // the first, the instance's rows and expert with the second).  Every lane of
 // the wave calls this and gets the same answer, in scalars (rows < 2^31);
 // false: no rows under this id.
@@ -71,7 +71,7 @@ __device__ __forceinline__ bool find_row_tile(const Instances& in, int64_t id, S
 }
 
 // Upper bound of the tile ids.
-inline int64_t row_tile_ids(const Instances& in, int rows) { return in.rows / rows + in.cap; }
+__host__ __device__ inline int64_t row_tile_ids(const Instances& in, int rows) { return in.rows / rows + in.cap; }
 
 }  // namespace
 }  // namespace moe

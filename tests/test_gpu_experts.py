@@ -245,9 +245,9 @@ def test_products(mp, loads, experts, E, n, k, B):
 
 
 def test_products_of_many_instances(mp):
-    """The largest plan: 2048 experts and 1024 replicas, most of them empty."""
+    """A plan of 2048 experts and 1000 replicas, most of them empty."""
     rng = np.random.RandomState(0)
-    E, B = 2048, 1024
+    E, B = 2048, 1000
     loads = rng.multinomial(900, rng.dirichlet(np.full(E + B, 0.1)))
     check_products(mp, loads, np.concatenate([np.arange(E), rng.permutation(E)[:B]]), E, 24, 40, B)
 
@@ -292,8 +292,110 @@ def test_products_of_a_routed_layer_sampled(mp, T, E, k, n, kk):
     layer.close()
 
 
+def test_products_of_many_instances_in_tiles(mp):
+    """As above with enough rows for the tiled kernels: each workgroup counts the tiles of 3048 instances."""
+    rng = np.random.RandomState(3)
+    E, B = 2048, 1000
+    loads = rng.multinomial(17000, rng.dirichlet(np.full(E + B, 0.05)))
+    check_products(mp, loads, np.concatenate([np.arange(E), rng.permutation(E)[:B]]), E, 24, 40, B)
+
+
+def sampled_products(layer, plan, off, spans, E, n, k, seed, rows_per_span=24, columns=40):
+    """Products and gradients at sizes of the large tiles: sampled against 64 bits, and the same bytes on every run
+    while other kernels come and go."""
+    rows, dev = layer.cfg.T * layer.cfg.k, layer.device
+    g = torch.Generator(device=dev).manual_seed(seed)
+    n16 = lambda *s: torch.randn(*s, generator=g, device=dev).to(BF)
+    xb, db = layer.quantize(n16(rows, k)), layer.quantize(n16(rows, n))
+    wb, wt = layer.quantize_weights(0.05 * n16(E, n, k), transposed=True)
+    kw = dict(plan=plan, inst_offset=off)
+    y, dx, dw = layer.matmul(xb, wb, **kw), layer.matmul(db, wt, **kw), layer.wgrad(db, xb, **kw)
+    for _ in range(3):
+        noise = torch.randn(1 << 22, device=dev).sort().values  # other work on the chip
+        assert torch.equal(layer.matmul(xb, wb, **kw), y) and torch.equal(layer.matmul(db, wt, **kw), dx)
+        assert torch.equal(layer.wgrad(db, xb, **kw), dw)
+        del noise
+    assert layer.status() == 0
+    rng = np.random.RandomState(seed)
+    take = lambda b, at: refs.values(type(b)(b.q.view(torch.uint8)[at.to(dev)].view(torch.float8_e4m3fn),
+                                             b.scale.view(torch.uint8)[at.to(dev)].view(torch.float8_e8m0fnu), b.cols), len(at))
+    mats = lambda b, e, m: refs.values(type(b)(b.q[e], b.scale[e], b.cols), m, 128)
+    for e, a, b in spans:
+        if a == b:
+            continue
+        at = torch.tensor(np.unique(np.concatenate([[a, b - 1], rng.randint(a, b, rows_per_span)])), dtype=torch.long)
+        for got, (want, bound) in ((y, refs.product(take(xb, at), mats(wb, e, n))),
+                                   (dx, refs.product(take(db, at), mats(wt, e, k)))):
+            assert ((got[at.to(dev)].cpu().double() - want).abs() <= bound).all(), (e, a, b)
+    for e in sorted(set(rng.randint(0, E, 3).tolist()) | {0, E - 1}):
+        at = torch.cat([torch.arange(a, b) for f, a, b in spans if f == e] + [torch.arange(0)]).long()
+        c = torch.tensor(np.unique(np.concatenate([[0, n - 1], rng.randint(0, n, columns)])), dtype=torch.long)
+        want, bound = refs.outer(take(db, at)[:, c], take(xb, at))
+        assert ((dw[e].cpu()[c].double() - want).abs() <= bound).all(), e
+
+
+@pytest.mark.parametrize("loads,experts,E,n,k,B", [
+    ([5000, 300, 7000, 4084], [0, 1, 2, 3], 4, 2200, 1032, 0),            # 9 blocks, odd widths
+    ([4096, 4097, 4095, 0, 1, 4095], [0, 1, 2, 3, 0, 2], 4, 2304, 2048, 2),
+    ([9000, 7384], [1, 0], 2, 2100, 100, 0),                              # a single block of the long axis
+    ([100, 37, 250, 64, 1, 129, 65, 500, 300, 200, 77, 90, 31, 63, 128, 700], list(range(16)), 16, 1576, 2050, 0),
+])
+def test_large_tiles_sampled(mp, loads, experts, E, n, k, B):
+    print("large tiles loads=%s E=%d n=%d k=%d" % (loads, E, n, k), flush=True)
+    layer = layer_for(mp, sum(loads), E, B)
+    plan, off, spans = instances(mp, layer, loads, experts)
+    sampled_products(layer, plan, off, spans, E, n, k, n + k)
+    layer.close()
+
+
+def test_offsets_past_32_bits(mp):
+    """More than 2^32 bytes of rows: quantization, products and gradients at the end of the buffers."""
+    rows, E, n, k = 655360, 8, 136, 7168
+    print("past 32 bits: %d rows of %d" % (rows, k), flush=True)
+    layer = layer_for(mp, rows, E)
+    dev = layer.device
+    x = torch.randn(rows, k, device=dev, dtype=BF, generator=torch.Generator(device=dev).manual_seed(1))
+    xb = layer.quantize(x)
+    last = torch.arange(rows - 3, rows, device=dev)
+    q, s = refs.quantize(x[last].cpu().double())
+    assert torch.equal(xb.q[last].cpu().double(), q) and torch.equal(xb.scale.view(torch.uint8)[last].cpu(), s)
+    del x
+    loads = [rows // E] * E
+    plan, off, spans = instances(mp, layer, loads, list(range(E)))
+    w = layer.quantize_weights((0.02 * torch.randn(E, n, k, device=dev)).to(BF))
+    y = layer.matmul(xb, w, plan=plan, inst_offset=off)
+    xv = refs.values(mp.Blocks(xb.q[last], xb.scale[last], k), 3)
+    wv = refs.values(mp.Blocks(w.q[E - 1], w.scale[E - 1], k), n, 128)
+    want, bound = refs.product(xv, wv)
+    assert ((y[last].cpu().double() - want).abs() <= bound).all()
+    # a gradient that only the last rows feed
+    dy = torch.zeros(rows, n, dtype=BF, device=dev)
+    dy[last] = 1
+    dw = layer.wgrad(layer.quantize(dy), xb, plan=plan, inst_offset=off)
+    want, bound = refs.outer(torch.ones(3, n, dtype=torch.float64), xv)
+    assert ((dw[E - 1].cpu().double() - want).abs() <= bound).all() and (dw[: E - 1] == 0).all()
+    assert layer.status() == 0
+    layer.close()
+
+
+def test_no_tokens(mp):
+    layer = mp.Layer(mp.make_config(0, 4, 2, 1, 1, 64, 0), cooc=False)
+    dev = layer.device
+    layer.plan_out.n_inst.fill_(4)
+    layer.plan_out.inst_expert.copy_(torch.arange(4))
+    layer.dispatch_out.inst_offset.zero_()
+    rows = layer.quantize(torch.empty(0, 64, dtype=BF, device=dev))
+    w, wt = layer.quantize_weights(normal(1, 4, 48, 64).to(dev), transposed=True)
+    assert layer.matmul(rows, w).shape == (0, 48)
+    dw = torch.full((4, 48, 64), 7.0, dtype=BF, device=dev)
+    layer.wgrad(layer.quantize(torch.empty(0, 48, dtype=BF, device=dev)), rows, out=dw)
+    torch.cuda.synchronize()
+    assert layer.status() == 0 and (dw == 0).all()
+    layer.close()
+
+
 def test_bad_plans_set_the_status_and_leave_rows_alone(mp):
-    rows, E, n, k = 64, 4, 48, 96
+    rows, E, n, k = 64, 4, 48, 96   # 16 rows an expert: the tiled kernel
     layer = layer_for(mp, rows, E, 2)
     dev = layer.device
     xb, wb = layer.quantize(normal(1, rows, k).to(dev)), layer.quantize_weights(normal(2, E, n, k).to(dev))
@@ -330,6 +432,34 @@ def test_bad_plans_set_the_status_and_leave_rows_alone(mp):
     out = torch.full((rows, n), 7.0, dtype=BF, device=dev)
     layer.matmul(xb, wb, plan=p, inst_offset=o, out=out)
     assert layer.status() == 0 and (out[40:] == 7).all() and torch.equal(out[:40], good[:40])
+    layer.close()
+
+
+@pytest.mark.parametrize("rows,n", [(64, 48), (2048, 17000), (12, 48)])
+def test_offsets_that_fall(mp, rows, n):
+    """Every second instance holds all rows, those between would hold fewer than none: for each kernel (128 and 256
+    rows to a tile, and few rows) the status tells, and each row is its expert's product or as it was."""
+    E, k, B = 4, 96, 60
+    layer = layer_for(mp, rows, E, B)
+    dev = layer.device
+    xb = layer.quantize(normal(1, rows, k).to(dev))
+    wb = layer.quantize_weights(normal(2, E, n, k).to(dev))
+    db = layer.quantize(normal(3, rows, n).to(dev))
+    layer.plan_out.n_inst.fill_(E + B)
+    layer.plan_out.inst_expert.fill_(1)
+    layer.dispatch_out.inst_offset.copy_(torch.tensor([0, rows] * 32 + [0], dtype=torch.int32))
+    y = torch.full((rows, n), 7.0, dtype=BF, device=dev)
+    layer.matmul(xb, wb, out=y)
+    dw = layer.wgrad(db, xb)
+    assert dw.shape == (E, n, k)
+    torch.cuda.synchronize()
+    assert layer.status() & mp.MOE_STATUS_PLAN_CHECK
+    at = torch.arange(0, rows, 1 + rows // 50)
+    xv = refs.values(xb, rows)[at] if rows < 100 else refs.values(
+        mp.Blocks(xb.q[at.to(dev)], xb.scale[at.to(dev)], k), len(at))
+    want, bound = refs.product(xv, refs.values(mp.Blocks(wb.q[1], wb.scale[1], k), n, 128))
+    got = y[at.to(dev)].cpu().double()
+    assert (((got - want).abs() <= bound) | (got == 7)).all()
     layer.close()
 
 
