@@ -182,7 +182,8 @@ int moex_wgrad(moe_plan_t h, const moe_plan_out* plan, const int32_t* inst_offse
  * The return path with given weights, as moe_plan_combine with w[t][j] =
  * weight[t][j] (float [T][k], device; NULL: all 1, the gradient of the
  * dispatch for its hidden rows).  A position outside [0, T*k) sets
- * MOE_STATUS_PLAN_CHECK and the slot is skipped.
+ * MOE_STATUS_PLAN_CHECK and the slot is skipped.  out may not overlap
+ * expert_out.
  */
 int moex_combine(moe_plan_t h, const float* weight, const int32_t* slot_pos, const uint16_t* expert_out,
                  uint16_t* out, void* stream);
@@ -192,8 +193,10 @@ int moex_combine(moe_plan_t h, const float* weight, const int32_t* slot_pos, con
  *   grad_expert_out[slot_pos[t*k+j]][:] = bf16( weight[t][j] * grad_out[t][:] )
  *   grad_weight[t][j] = sum of grad_out[t][:] * expert_out[slot_pos[t*k+j]][:]  (fp32)
  * grad_expert_out uint16 [T*k][H] (every row that a slot points to is
- * written; it may not overlap expert_out); grad_weight float [T][k].  A
- * position outside [0, T*k) sets MOE_STATUS_PLAN_CHECK; its weight gradient is 0.
+ * written; it may not overlap expert_out); grad_weight float [T][k].  Each
+ * slot has a row of its own, as moe_plan_dispatch gives it (of slots that share
+ * one, one's gradient is left in it, whichever).  A position outside [0, T*k)
+ * sets MOE_STATUS_PLAN_CHECK; its weight gradient is 0.
  */
 int moex_combine_grad(moe_plan_t h, const float* weight, const int32_t* slot_pos, const uint16_t* expert_out,
                       const uint16_t* grad_out, uint16_t* grad_expert_out, float* grad_weight, void* stream);

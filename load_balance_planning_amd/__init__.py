@@ -554,7 +554,7 @@ class Layer:
             self._check_tensor(bias, (E,), torch.float32)
         if prev_topk is not None:
             self._check_tensor(prev_topk, (T, k), torch.int32)
-        weight = torch.empty((T, k), dtype=torch.float32, device=self.device)
+        weight = self._empty((T, k), torch.float32, stream)
         moex_gate(self.handle, gate, _addr(logits), _addr(bias), _addr(prev_topk), self._route_s, _addr(weight),
                   self._stream(stream))
         return self.route_out, weight
@@ -563,7 +563,7 @@ class Layer:
         """Gradient of gate()'s weights for the logits (moex_gate_grad); topk_idx defaults to this layer's."""
         torch, T, E, k = self.torch, self.cfg.T, self.cfg.E, self.cfg.k
         topk_idx = self.route_out.topk_idx if topk_idx is None else topk_idx
-        out = torch.empty((T, E), dtype=torch.float32, device=self.device) if out is None else out
+        out = self._empty((T, E), torch.float32, stream) if out is None else out
         self._check_tensor(logits, (T, E), torch.float32)
         self._check_tensor(topk_idx, (T, k), torch.int32)
         self._check_tensor(grad_weight, (T, k), torch.float32)
@@ -572,16 +572,24 @@ class Layer:
                        self._stream(stream))
         return out
 
-    def _empty_blocks(self, lead, cols, scale_lead=None) -> Blocks:
+    def _empty(self, shape, dtype, stream):
+        """A result of a call on `stream`, whose memory belongs to that stream: the allocator gives it to no other
+        stream's tensors while the call may still write it."""
+        if stream is None:
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
+        with self.torch.cuda.stream(stream):
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
+
+    def _empty_blocks(self, stream, lead, cols, scale_lead=None) -> Blocks:
         torch, scale_lead = self.torch, lead if scale_lead is None else scale_lead
-        return Blocks(torch.empty((*lead, Blocks.padded(cols)), dtype=torch.float8_e4m3fn, device=self.device),
-                      torch.empty((*scale_lead, Blocks.scales(cols)), dtype=torch.float8_e8m0fnu, device=self.device),
-                      cols)
+        return Blocks(self._empty((*lead, Blocks.padded(cols)), torch.float8_e4m3fn, stream),
+                      self._empty((*scale_lead, Blocks.scales(cols)), torch.float8_e8m0fnu, stream), cols)
 
     def _check_16bit(self, t, shape, name):
+        """bf16, or its bit patterns in a 16-bit integer type."""
         self._check_tensor(t, shape, None)
-        if t.element_size() != 2:
-            raise TypeError("%s must be a 16-bit (bf16) tensor" % name)
+        if t.element_size() != 2 or t.dtype == self.torch.float16:
+            raise TypeError("%s must be a bf16 tensor, not %s" % (name, t.dtype))
 
     def _check_blocks(self, b: Blocks, lead, scale_lead=None):
         torch = self.torch
@@ -595,7 +603,7 @@ class Layer:
             raise ValueError("x must be [rows][cols]")
         rows, cols = x.shape
         self._check_16bit(x, (rows, cols), "x")
-        out = self._empty_blocks((rows,), cols)
+        out = self._empty_blocks(stream, (rows,), cols)
         moex_quantize(self.handle, _addr(x), rows, cols, _addr(out.q), _addr(out.scale), self._stream(stream))
         return out
 
@@ -607,8 +615,8 @@ class Layer:
         E, n, k = w.shape
         self._check_16bit(w, (E, n, k), "w")
         blocks = lambda c: -(-c // BLOCK)
-        out = self._empty_blocks((E, n), k, (E, blocks(n)))
-        out_t = self._empty_blocks((E, k), n, (E, blocks(k))) if transposed else Blocks(None, None, n)
+        out = self._empty_blocks(stream, (E, n), k, (E, blocks(n)))
+        out_t = self._empty_blocks(stream, (E, k), n, (E, blocks(k))) if transposed else Blocks(None, None, n)
         moex_quantize_weights(self.handle, _addr(w), E, n, k, _addr(out.q), _addr(out.scale), _addr(out_t.q),
                               _addr(out_t.scale), self._stream(stream))
         return (out, out_t) if transposed else out
@@ -619,7 +627,7 @@ class Layer:
             raise ValueError("y must be [rows][2 f]")
         rows, f = y.shape[0], y.shape[1] // 2
         self._check_16bit(y, (rows, 2 * f), "y")
-        out = self._empty_blocks((rows,), f)
+        out = self._empty_blocks(stream, (rows,), f)
         moex_swiglu(self.handle, _addr(y), rows, f, _addr(out.q), _addr(out.scale), self._stream(stream))
         return out
 
@@ -630,7 +638,7 @@ class Layer:
         rows, f = y.shape[0], y.shape[1] // 2
         self._check_16bit(y, (rows, 2 * f), "y")
         self._check_16bit(grad, (rows, f), "grad")
-        out = self._empty_blocks((rows,), 2 * f)
+        out = self._empty_blocks(stream, (rows,), 2 * f)
         moex_swiglu_grad(self.handle, _addr(y), _addr(grad), rows, f, _addr(out.q), _addr(out.scale),
                          self._stream(stream))
         return out
@@ -658,7 +666,7 @@ class Layer:
             raise ValueError("x has %d columns, the matrices %d" % (x.cols, k))
         self._check_blocks(x, (rows,))
         self._check_blocks(w, (self.cfg.E, n), (self.cfg.E, -(-n // BLOCK)))
-        out = torch.empty((rows, n), dtype=torch.bfloat16, device=self.device) if out is None else out
+        out = self._empty((rows, n), torch.bfloat16, stream) if out is None else out
         self._check_16bit(out, (rows, n), "out")
         moex_matmul(self.handle, plan_s, _addr(inst_offset), _addr(x.q), _addr(x.scale), _addr(w.q), _addr(w.scale), n, k,
                     _addr(out), self._stream(stream))
@@ -671,7 +679,7 @@ class Layer:
         plan_s, inst_offset = self._product_plan(plan, inst_offset)
         self._check_blocks(dy, (rows,))
         self._check_blocks(x, (rows,))
-        out = torch.empty((E, dy.cols, x.cols), dtype=torch.bfloat16, device=self.device) if out is None else out
+        out = self._empty((E, dy.cols, x.cols), torch.bfloat16, stream) if out is None else out
         self._check_16bit(out, (E, dy.cols, x.cols), "out")
         moex_wgrad(self.handle, plan_s, _addr(inst_offset), _addr(dy.q), _addr(dy.scale), _addr(x.q), _addr(x.scale),
                    dy.cols, x.cols, _addr(out), self._stream(stream))
@@ -690,7 +698,7 @@ class Layer:
         self._check_16bit(expert_out, (T * k, H), "expert_out")
         if weight is not None:
             self._check_tensor(weight, (T, k), torch.float32)
-        out = torch.empty((T, H), dtype=expert_out.dtype, device=self.device) if out is None else out
+        out = self._empty((T, H), expert_out.dtype, stream) if out is None else out
         self._check_16bit(out, (T, H), "out")
         moex_combine(self.handle, _addr(weight), _addr(slot_pos), _addr(expert_out), _addr(out), self._stream(stream))
         return out
@@ -703,8 +711,8 @@ class Layer:
         self._check_16bit(expert_out, (T * k, H), "expert_out")
         self._check_16bit(grad_out, (T, H), "grad_out")
         self._check_tensor(weight, (T, k), torch.float32)
-        grad_rows = torch.empty_like(expert_out)
-        grad_weight = torch.empty((T, k), dtype=torch.float32, device=self.device)
+        grad_rows = self._empty((T * k, H), expert_out.dtype, stream)
+        grad_weight = self._empty((T, k), torch.float32, stream)
         moex_combine_grad(self.handle, _addr(weight), _addr(slot_pos), _addr(expert_out), _addr(grad_out),
                           _addr(grad_rows), _addr(grad_weight), self._stream(stream))
         return grad_rows, grad_weight

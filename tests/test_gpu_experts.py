@@ -570,6 +570,51 @@ def layer_inputs(mp, T, E, k, H, F, dev, seed=0):
                 w1=n(E, 2 * F, H, scale=H ** -0.5).to(BF).to(dev), w2=n(E, H, F, scale=F ** -0.5).to(BF).to(dev))
 
 
+def test_half_precision_is_refused(mp):
+    T, E, k, H = 8, 4, 2, 128
+    layer = mp.Layer(mp.make_config(T, E, k, 1, 1, H, 0), cooc=False)
+    z = lambda *s: torch.zeros(*s, dtype=torch.float16, device=layer.device)
+    b = lambda *s: z(*s).to(BF)
+    w = torch.ones(T, k, device=layer.device)
+    for call in (lambda: layer.quantize(z(4, H)), lambda: layer.quantize_weights(z(E, 8, H)),
+                 lambda: layer.swiglu(z(4, H)), lambda: layer.swiglu_grad(b(4, 2 * H), z(4, H)),
+                 lambda: layer.combine_weighted(z(T * k, H)), lambda: layer.combine_weighted(b(T * k, H), out=z(T, H)),
+                 lambda: layer.combine_grad(b(T * k, H), z(T, H), w)):
+        with pytest.raises(TypeError):
+            call()
+    layer.close()
+
+
+def test_results_belong_to_the_stream_of_the_call(mp):
+    """With stream=, a result that is dropped at once leaves its memory to that stream alone."""
+    layer = layer_for(mp, 64, 4)
+    dev, side = layer.device, torch.cuda.Stream()
+    x, w = normal(1, 64, 256).to(dev), normal(2, 4, 48, 256).to(dev)
+    want = layer.quantize(x)
+    plan, off, _ = instances(mp, layer, [16] * 4, list(range(4)))
+    kw = dict(plan=plan, inst_offset=off)
+    torch.cuda.synchronize()
+    xb = layer.quantize(x, stream=side)
+    wb, wt = layer.quantize_weights(w, transposed=True, stream=side)
+    y = layer.matmul(xb, wb, stream=side, **kw)
+    dw = layer.wgrad(layer.quantize(y, stream=side), xb, stream=side, **kw)
+    side.synchronize()
+    assert torch.equal(xb.q.view(torch.uint8), want.q.view(torch.uint8))
+    assert torch.equal(y, layer.matmul(xb, wb, **kw)) and dw.shape == (4, 48, 256)
+    torch.cuda.synchronize()
+    for t in (xb.q, wb.q, wt.q, y, dw):
+        like, at = (t.shape, t.dtype), t.data_ptr()
+        hold = torch.empty(like[0], dtype=like[1], device=dev)
+        assert hold.data_ptr() != at
+    freed = {t.data_ptr() for t in (y, dw)}
+    shapes = [t.shape for t in (y, dw)]
+    del y, dw, t
+    again = [torch.empty(s, dtype=BF, device=dev) for s in shapes for _ in range(4)]
+    assert not freed & {t.data_ptr() for t in again}
+    assert layer.status() == 0
+    layer.close()
+
+
 def test_a_layer_forward_and_backward(mp):
     """Against the same layer in 64 bits with automatic differentiation.  Each tensor that is quantized moves by at
     most 2^-4 of itself, element by element, and by 3 % in the root mean square (an e4m3 step is 1/8 to 1/16 of a
