@@ -34,7 +34,10 @@ def layer_of(mp, T, k, H):
 
 
 @pytest.mark.parametrize("T,k,H", [(1, 1, 1), (3, 2, 13), (64, 8, 512), (40, 6, 264), (17, 16, 7168), (9, 32, 24),
-                                   (12, 8, 2048), (12, 8, 2056), (5, 4, 8200), (30, 5, 1001), (7, 3, 16400)])
+                                   (12, 8, 2048), (12, 8, 2056), (5, 4, 8200), (30, 5, 1001), (7, 3, 16400),
+                                   # around 512 tokens, where a token's work is no longer split
+                                   (511, 2, 2056), (512, 3, 2056), (700, 5, 2048), (1000, 6, 264), (600, 2, 8200),
+                                   (513, 9, 1001), (520, 7, 4104)])
 def test_weighted_sum_and_gradients(mp, T, k, H):
     print("combine weighted T=%d k=%d H=%d" % (T, k, H), flush=True)
     rows, g, w, pos = data(T + k + H, T, k, H)
