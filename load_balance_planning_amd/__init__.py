@@ -576,9 +576,9 @@ class Layer:
         """A result of a call on `stream`, whose memory belongs to that stream: the allocator gives it to no other
         stream's tensors while the call may still write it."""
         if stream is None:
-            return self.torch.empty(shape, dtype=dtype, device=self.device)
+            return self.torch.empty(*shape, dtype=dtype, device=self.device)
         with self.torch.cuda.stream(stream):
-            return self.torch.empty(shape, dtype=dtype, device=self.device)
+            return self.torch.empty(*shape, dtype=dtype, device=self.device)
 
     def _empty_blocks(self, stream, lead, cols, scale_lead=None) -> Blocks:
         torch, scale_lead = self.torch, lead if scale_lead is None else scale_lead
