@@ -100,6 +100,35 @@ def test_router_with_groups(mp, shape, kind, biased):
     check(mp, x, b if biased else None, k, R, kind, shape[4:], True, 2.5)
 
 
+@pytest.mark.parametrize("shape", [(4104, 256, 8, 8, 8, 4, 2), (4097, 128, 8, 1, 1, 1, 1), (4100, 512, 8, 2, 1, 1, 1),
+                                   (4104, 896, 16, 8, 8, 4, 1), (4099, 8, 2, 1, 1, 1, 1), (4098, 160, 6, 2, 8, 3, 1),
+                                   (4101, 100, 4, 1, 1, 1, 1), (4104, 2048, 8, 8, 16, 5, 2), (4096, 384, 8, 1, 1, 1, 1)])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+def test_many_tokens(mp, shape, kind, biased):
+    """Above 4096 tokens a token has fewer lanes."""
+    T, E, k, R = shape[:4]
+    print("gate many tokens %s %s bias=%s" % (shape, kind, biased), flush=True)
+    x, b = logits(sum(shape), T, E)
+    check(mp, x, b if biased else None, k, R, kind, shape[4:], True, 2.5)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_ties_of_many_tokens(mp, kind):
+    T, E, k = 4110, 256, 8
+    g = torch.Generator().manual_seed(5)
+    coarse = (torch.randn(T, E, generator=g) * 4).round() / 4
+    coarse[100:110] = 0.0
+    coarse[200:210, ::3] = -torch.inf
+    coarse[300:310] = -torch.inf
+    near = torch.full((T, E), 1.5) + torch.randint(0, 50, (T, E), generator=g) * 2.0 ** -23
+    bias = torch.randint(0, 3, (E,), generator=g) * 2.0 ** -24
+    for groups in ((1, 1, 1), (8, 4, 2)):
+        check(mp, coarse, None, k, 1, kind, groups)
+        check(mp, coarse, torch.zeros(E), k, 1, kind, groups)
+        check(mp, near, bias, k, 1, kind, groups)
+
+
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 def test_ties_and_near_ties(mp, kind):
     """Logits on a coarse grid (equal choices by the dozen, with and without a bias of zeros) and logits a few units
