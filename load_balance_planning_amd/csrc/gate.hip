@@ -70,7 +70,7 @@ __host__ __device__ inline bool groups_of_lanes(int per) {
   return per % V == 0 && (lanes & (lanes - 1)) == 0;
 }
 
-// LDS of gate_kernel: presence masks; the bias; per token 2 P candidates
+// LDS of gate_kernel: presence masks; the bias, zeros up to P V; per token 2 P candidates
 // (64-bit choice, choice, expert) and P selected experts; with groups their
 // values and, unless they are whole lanes, a row of choices (8 words apart, for
 // other banks).
@@ -83,7 +83,7 @@ __host__ __device__ inline GateLds gate_lds(int E, int n_group, bool prev, bool 
   constexpr size_t TPW = gate_tpw<P>();
   GateLds l;
   l.bias = sizeof(uint64_t) * (size_t)E * (prev ? 2 : 1);
-  l.cand = l.bias + (biased ? ((size_t)E + 3) / 4 * 16 : 0);
+  l.cand = l.bias + (biased ? (size_t)P * V * sizeof(float) : 0);
   l.chosen = l.cand + TPW * 2 * P * 16;
   l.group = l.chosen + TPW * P * 4;
   l.choice = l.group + (n_group > 1 ? TPW * n_group * sizeof(double) : 0);
@@ -95,6 +95,11 @@ __host__ __device__ inline GateLds gate_lds(int E, int n_group, bool prev, bool 
 constexpr float kLog2e = 1.44269504f;
 constexpr float kUlp = 5.9604645e-8f;  // 2^-24
 
+// The two largest (a >= b) of a pair and a value: the median of three is the second.
+__device__ __forceinline__ void push_top2(float* a, float* b, float v) {
+  *b = __builtin_amdgcn_fmed3f(*a, *b, v);
+  *a = fmaxf(*a, v);
+}
 // The two largest of two pairs (a >= b, oa >= ob).
 __device__ __forceinline__ void merge_top2(float* a, float* b, float oa, float ob) {
   *b = fmaxf(fminf(*a, oa), fmaxf(*b, ob));
@@ -124,8 +129,10 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
   for (int e = tid; e < d.E; e += nthr) {
     smask[e] = 0ull;
     if (want_prev) pmask[e] = 0ull;
-    if (bias) {
-      const float b = bias[e];
+  }
+  if (bias) {
+    for (int e = tid; e < P * V; e += nthr) {
+      const float b = e < d.E ? bias[e] : 0.0f;
       const bool wrong = b != b || b == INFINITY;
       bad |= wrong;
       bias_s[e] = wrong ? 0.0f : b;
@@ -169,7 +176,7 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
     float xmax = -INFINITY;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      bad |= x[v] != x[v];
+      bad |= v % 2 == 0 && __builtin_isunordered(x[v], x[V > 1 ? v + 1 : v]);
       x[v] = fmaxf(x[v], -INFINITY);  // a NaN becomes -infinity
       xmax = fmaxf(xmax, x[v]);
     }
@@ -212,7 +219,7 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
         o32[v] = softmax ? o32[v] * inv : __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x[v] * -kLog2e));
       if (bias) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) o32[v] += full || e0 + v < d.E ? bias_s[e0 + v] : 0.0f;
+        for (int v = 0; v < V; ++v) o32[v] += bias_s[e0 + v];
       }
     }
     // in 64 bits, where a comparison needs it
@@ -243,7 +250,7 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
         const int lanes = per / V;
         float a = o32[0], b = -INFINITY;
 #pragma unroll
-        for (int v = 1; v < V; ++v) merge_top2(&a, &b, o32[v], -INFINITY);
+        for (int v = 1; v < V; ++v) push_top2(&a, &b, o32[v]);
         for (int off = 1; off < lanes; off <<= 1) merge_top2(&a, &b, __shfl_xor(a, off), __shfl_xor(b, off));
         if ((lane & (lanes - 1)) == 0 && e0 < d.E) gv[e0 / per] = g.group_top == 2 ? a + b : a;
       } else {
@@ -257,7 +264,7 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
           int at = q % per;  // lanes start at different places of their groups: other LDS banks
 #pragma unroll 4
           for (int j = 0; j < per; ++j) {
-            merge_top2(&a, &b, ch[q * per + at], -INFINITY);
+            push_top2(&a, &b, ch[q * per + at]);
             at = at + 1 == per ? 0 : at + 1;
           }
           gv[q] = g.group_top == 2 ? a + b : a;
@@ -348,7 +355,7 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
       // largest of them all, in bitonic order.
       float a = o32[0], b = -INFINITY;
 #pragma unroll
-      for (int v = 1; v < V; ++v) merge_top2(&a, &b, o32[v], -INFINITY);
+      for (int v = 1; v < V; ++v) push_top2(&a, &b, o32[v]);
       sorted = group_sort_desc_u32<P>(order_key(__float_as_uint(a)), lane);
       const uint32_t seconds = group_sort_desc_u32<P>(order_key(__float_as_uint(b)), lane);
       sorted = group_merge_desc_u32<P>(max(sorted, (uint32_t)__shfl_xor((int)seconds, P - 1)), lane);
@@ -360,17 +367,17 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
     }
     const float kth = __uint_as_float(float_from_order_key((uint32_t)__shfl((int)sorted, grp_base + k - 1)));
     const float tau = bias ? kth - margin * (1.0f + fabsf(kth)) : kth;
+    const int valid = full ? V : d.E - e0;  // slots past the row's end count for nothing
     int mine = 0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) mine += o32[v] >= tau ? 1 : 0;
-    if (!full && tau == -INFINITY) mine = max(0, min(V, d.E - e0));  // slots past the row's end count for nothing
+    for (int v = 0; v < V; ++v) mine += (int)(o32[v] >= tau) & (int)(v < valid);
     const int incl = group_incl_scan<P>(mine, lane);
     const int total = group_last<P>(incl);
     if (total <= 2 * P) {
       int w = incl - mine;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        if (o32[v] >= tau && (full || e0 + v < d.E)) {
+        if ((int)(o32[v] >= tau) & (int)(v < valid)) {
           cand_c[w] = o32[v];
           cand_e[w] = e0 + v;
           ++w;
