@@ -457,6 +457,8 @@ class Layer:
             self.device = torch.device("cuda", torch.cuda.current_device())
         self.cfg = cfg
         self._index = self.device.index
+        self._dims = (cfg.T, cfg.E, cfg.k, cfg.H)  # plain integers: a structure's fields cost more to read
+        self._cap = cfg.E + cfg.replica_budget
         # handle of torch's current stream on a device, without the Python object around it
         self._current_stream = torch._C._cuda_getCurrentRawStream
         self.sizes = moe_plan_query(cfg)
@@ -548,7 +550,7 @@ class Layer:
 
     def gate(self, logits, gate: moex_gate_config, bias=None, prev_topk=None, stream=None):
         """Routing with scores, bias, groups and weights (moex_gate): (route_out, weight [T][k])."""
-        torch, T, E, k = self.torch, self.cfg.T, self.cfg.E, self.cfg.k
+        torch, (T, E, k, _) = self.torch, self._dims
         self._check_tensor(logits, (T, E), torch.float32)
         if bias is not None:
             self._check_tensor(bias, (E,), torch.float32)
@@ -561,7 +563,7 @@ class Layer:
 
     def gate_grad(self, logits, gate: moex_gate_config, grad_weight, topk_idx=None, out=None, stream=None):
         """Gradient of gate()'s weights for the logits (moex_gate_grad); topk_idx defaults to this layer's."""
-        torch, T, E, k = self.torch, self.cfg.T, self.cfg.E, self.cfg.k
+        torch, (T, E, k, _) = self.torch, self._dims
         topk_idx = self.route_out.topk_idx if topk_idx is None else topk_idx
         out = self._empty((T, E), torch.float32, stream) if out is None else out
         self._check_tensor(logits, (T, E), torch.float32)
@@ -646,7 +648,7 @@ class Layer:
     def _product_plan(self, plan, inst_offset):
         """The struct of the instances a product runs over; by default this layer's plan and dispatch offsets."""
         inst_offset = self.dispatch_out.inst_offset if inst_offset is None else inst_offset
-        cap = self.cfg.E + self.cfg.replica_budget
+        cap = self._cap
         self._check_tensor(inst_offset, (cap + 1,), self.torch.int32)
         if plan is None:
             return self._plan_s, inst_offset
@@ -659,13 +661,14 @@ class Layer:
     def matmul(self, x: Blocks, w: Blocks, plan=None, inst_offset=None, out=None, stream=None):
         """Rows in dispatch order times their experts' matrices (moex_matmul): bf16 [T*k][n] of x, Blocks of rows
         [T*k][k], and w, Blocks of matrices [E][n][k]."""
-        torch, rows = self.torch, self.cfg.T * self.cfg.k
+        torch, (T, E, top, _) = self.torch, self._dims
+        rows = T * top
         plan_s, inst_offset = self._product_plan(plan, inst_offset)
         n, k = w.q.shape[1], w.cols
         if x.cols != k:
             raise ValueError("x has %d columns, the matrices %d" % (x.cols, k))
         self._check_blocks(x, (rows,))
-        self._check_blocks(w, (self.cfg.E, n), (self.cfg.E, -(-n // BLOCK)))
+        self._check_blocks(w, (E, n), (E, -(-n // BLOCK)))
         out = self._empty((rows, n), torch.bfloat16, stream) if out is None else out
         self._check_16bit(out, (rows, n), "out")
         moex_matmul(self.handle, plan_s, _addr(inst_offset), _addr(x.q), _addr(x.scale), _addr(w.q), _addr(w.scale), n, k,
@@ -675,7 +678,8 @@ class Layer:
     def wgrad(self, dy: Blocks, x: Blocks, plan=None, inst_offset=None, out=None, stream=None):
         """Gradient of the experts' matrices (moex_wgrad): bf16 [E][n][k] of dy, Blocks of rows [T*k][n], and x,
         Blocks of rows [T*k][k]."""
-        torch, rows, E = self.torch, self.cfg.T * self.cfg.k, self.cfg.E
+        torch, (T, E, top, _) = self.torch, self._dims
+        rows = T * top
         plan_s, inst_offset = self._product_plan(plan, inst_offset)
         self._check_blocks(dy, (rows,))
         self._check_blocks(x, (rows,))
@@ -687,13 +691,13 @@ class Layer:
 
     def _slot_positions(self, slot_pos):
         slot_pos = self.dispatch_out.slot_pos if slot_pos is None else slot_pos
-        self._check_tensor(slot_pos, (self.cfg.T * self.cfg.k,), self.torch.int32)
+        self._check_tensor(slot_pos, (self._dims[0] * self._dims[2],), self.torch.int32)
         return slot_pos
 
     def combine_weighted(self, expert_out, weight=None, slot_pos=None, out=None, stream=None):
         """Sum of each token's expert rows by the given weights [T][k] (moex_combine); without weights their plain
         sum, the gradient of the dispatch for its hidden rows."""
-        torch, T, k, H = self.torch, self.cfg.T, self.cfg.k, self.cfg.H
+        torch, (T, _, k, H) = self.torch, self._dims
         slot_pos = self._slot_positions(slot_pos)
         self._check_16bit(expert_out, (T * k, H), "expert_out")
         if weight is not None:
@@ -706,7 +710,7 @@ class Layer:
     def combine_grad(self, expert_out, grad_out, weight, slot_pos=None, stream=None):
         """Gradients of combine_weighted for the expert rows and the weights (moex_combine_grad):
         (grad_expert_out [T*k][H], grad_weight [T][k])."""
-        torch, T, k, H = self.torch, self.cfg.T, self.cfg.k, self.cfg.H
+        torch, (T, _, k, H) = self.torch, self._dims
         slot_pos = self._slot_positions(slot_pos)
         self._check_16bit(expert_out, (T * k, H), "expert_out")
         self._check_16bit(grad_out, (T, H), "grad_out")
