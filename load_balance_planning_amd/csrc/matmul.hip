@@ -136,12 +136,16 @@ __device__ __forceinline__ int piece_at(int row, int p) {
   return (row >> 1) * 256 + ((((row & 1) << 3) | p) ^ piece_swizzle<CHANNELS>(row >> 1)) * 16;
 }
 
-// Barrier after which every wave sees every wave's loads into LDS.  A barrier
-// alone does not wait for them: to the compiler they are loads, which a
-// workgroup fence need not order.
+// Barrier after which every wave sees every wave's loads into LDS, and has its
+// own reads.  A barrier alone does not wait for the loads: to the compiler they
+// are loads, which a workgroup fence need not order (and where it does, it waits
+// for all of them).
+// NEWER of the wave's last loads may still be under way (loads end in order).
+template <int NEWER = 0>
 __device__ __forceinline__ void sync_with_loads() {
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(NEWER) : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
 template <int BC, int BT, int WC, int WT>
@@ -217,6 +221,8 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), BC == 256 ? 
   // the CU's LDS) the second stage, whose next block then comes in later
   constexpr bool kOwnPlace = BC == 256;
   __shared__ __align__(16) unsigned char out_s[kOwnPlace ? 4 * 4096 : 16];
+  constexpr bool kFetch = BC == 256;
+  __shared__ uint32_t fetch_s[kFetch ? 4 * 64 : 1];
   if (blockIdx.x == 0) check_instances(in, status);
   const int nct = (n + BC - 1) / BC;
   const int n_inst = instance_count(in);
@@ -244,7 +250,7 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), BC == 256 ? 
   const int wc = wave % WC * S::kWaveC, wt = wave / WC * S::kWaveT;
   // a tile: its rows, channels, expert
   struct Tile {
-    int r0, rows, c0, chans, expert;
+    int r0, rows, c0, chans, expert, rt;
   };
   auto locate = [&](int t) {
     const int band = t / (4 * nct), in_band = t - band * 4 * nct;
@@ -257,10 +263,11 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), BC == 256 ? 
     o.r0 = __builtin_amdgcn_readfirstlane(in.offset[i] + (rt - pre[i]) * BT);
     o.rows = min(BT, __builtin_amdgcn_readfirstlane(in.offset[i + 1]) - o.r0);
     o.expert = __builtin_amdgcn_readfirstlane(in.expert[i]);
+    o.rt = rt;
     return o;
   };
   Tile at;
-  uint32_t off_c[S::kPassC], off_t[S::kPassT], xs_off[S::kT];
+  uint32_t off_c[S::kPassC], off_t[S::kPassT], xs_off[S::kT], off_f;
   auto set_offsets = [&]() {
 #pragma unroll
     for (int q = 0; q < S::kPassC; ++q)
@@ -270,6 +277,22 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), BC == 256 ? 
       off_t[q] = (uint32_t)min(q * kRowsPerPass + 2 * pair + (place_t >> 3), at.rows - 1) * kp + 16 * (place_t & 7);
 #pragma unroll
     for (int j = 0; j < S::kT; ++j) xs_off[j] = (uint32_t)(min(wt + 32 * j + r, at.rows - 1) * ns);
+    // this wave's share of the lines to fetch ahead
+    const int part = wave < 2 ? at.rt & 3 : (at.c0 / BC) & 3;
+    off_f = (uint32_t)min(4 * (32 * (wave & 1) + (lane & 31)) + part, (wave < 2 ? at.chans : at.rows) - 1) * kp;
+  };
+  // Block b's lines into the XCD's L2, a quarter of them per workgroup: those that
+  // share an operand take the others.  The workgroups of an XCD ask for a block's
+  // lines at about the same time, so without this all of them wait for memory
+  // (32768 rows, 32 experts of 5376 x 7168: 3200 cycles a block, and 2400 so; of
+  // 2048 x 1536, 131072 rows: 4100 and 2700; the clock falls with the load, and the
+  // times by less, 1263 -> 1236 us and 553 -> 524).  The bytes read go nowhere.
+  auto fetch = [&](int b) {
+    if (!kFetch) return;
+    asm volatile("" ::: "memory");  // behind the block loads before it
+    const auto buf = wave < 2 ? buffer_of(w + ((int64_t)at.expert * n + at.c0) * kp, (uint32_t)at.chans * kp)
+                              : buffer_of(x + (int64_t)at.r0 * kp, (uint32_t)at.rows * kp);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_ptr)(fetch_s + wave * 64), 4, off_f, b * kBlk, 0, 0);
   };
   auto load = [&](unsigned char* c_s, unsigned char* t_s, int b) {
     const auto w_buf = buffer_of(w + ((int64_t)at.expert * n + at.c0) * kp, (uint32_t)at.chans * kp);
@@ -338,6 +361,7 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), BC == 256 ? 
   // spread between them
   constexpr int kProducts = S::kC * S::kT, kReads = 2 * (S::kC + S::kT);
   auto spread = [&](bool loads) {
+    if (kFetch && !loads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // fetch
 #pragma unroll
     for (int q = 0; q < kProducts; ++q) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a product
@@ -356,6 +380,7 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), BC == 256 ? 
   load_scales(0);
   load(c0_s, t0_s, 0);
   if (kOwnPlace) load(c1_s, t1_s, min(1, nb - 1));
+  fetch(min(2, nb - 1));
   for (;;) {
     const Tile next = locate(min(tile + slots, last - 1));  // arrives while this tile's products run
 #pragma unroll
@@ -372,19 +397,21 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), BC == 256 ? 
     // some block again, which nothing uses.
     for (int b = 0; b + 2 <= nb; b += 2) {
       take_scales(b);
+      fetch(min(b + 3, nb - 1));
       read(&f1, c0_s, t0_s, 1);
       multiply(f0);
       spread(false);
-      sync_with_loads();
+      sync_with_loads<kFetch ? 1 : 0>();
       load(c0_s, t0_s, min(b + 2, nb - 1));
       read(&f0, c1_s, t1_s, 0);
       multiply(f1);
       spread(true);
       next_scales();
+      fetch(min(b + 4, nb - 1));
       read(&f1, c1_s, t1_s, 1);
       multiply(f0);
       spread(false);
-      sync_with_loads();
+      sync_with_loads<kFetch ? 1 : 0>();
       load_scales(min(b + 2, nb - 1));
       load(c1_s, t1_s, min(b + 3, nb - 1));
       read(&f0, c0_s, t0_s, 0);
@@ -408,6 +435,7 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), BC == 256 ? 
       load_scales(0);
       load(c0_s, t0_s, 0);
       if (kOwnPlace) load(c1_s, t1_s, min(1, nb - 1));
+      fetch(min(2, nb - 1));
     }
     store_wave_tile<kTI, kTJ>(acc, own, y + (int64_t)(done.r0 + wt) * n + done.c0 + wc, n, done.rows - wt,
                               done.chans - wc, vec);
