@@ -293,15 +293,27 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
       if ((__ballot(unsure) & grp_bits) != 0ull) {
         need64();
         wave_lds_sync();
-        for (int q = lane; q < g.n_group; q += P) {
+        // as many lanes to a group as it has experts, where it has that many
+        int L = 1;
+        while (L < P && L < per) L *= 2;
+        const int part = lane & (L - 1);
+        for (int q0 = 0; q0 < g.n_group; q0 += P / L) {
+          const int q = q0 + lane / L;
           double a = -INFINITY, b = -INFINITY;
+          if (q < g.n_group) {
 #pragma unroll 1
-          for (int j = 0; j < per; ++j) {
-            const double y = choice64(q * per + j);
-            b = fmax(b, fmin(a, y));
-            a = fmax(a, y);
+            for (int j = part; j < per; j += L) {
+              const double y = choice64(q * per + j);
+              b = fmax(b, fmin(a, y));
+              a = fmax(a, y);
+            }
           }
-          gv64[q] = g.group_top == 2 ? a + b : a;
+          for (int off = 1; off < L; off <<= 1) {
+            const double oa = __shfl_xor(a, off), ob = __shfl_xor(b, off);
+            b = fmax(fmin(a, oa), fmax(b, ob));
+            a = fmax(a, oa);
+          }
+          if (part == 0 && q < g.n_group) gv64[q] = g.group_top == 2 ? a + b : a;
         }
         wave_lds_sync();
         mask = 0ull;
