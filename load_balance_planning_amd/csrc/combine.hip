@@ -33,6 +33,13 @@ constexpr int kRowsInFlight = 8;
 // of 8 rows of 7168: 11 -> 4.5 us, their gradient 8 -> 4.5 us.
 constexpr int kFewTokens = 512;
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+// A row of H >= 8 values is read and written in ceil(H / 8) vectors of 16 bytes
+// from any address of a 16-bit type; the last begins at H - 8, so where H is no
+// multiple of 8 it has values of the one before again (value by value, such
+// rows took two to eight times as long: 8192 tokens of 8 rows of 7167, 553 us and 218;
+// 64 tokens of 8 rows of 7001, 39 and 5).
+typedef v4u v4u_any __attribute__((aligned(2)));
+__device__ __forceinline__ int vector_at(int v, int H) { return min(8 * v, H - 8); }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -100,13 +107,14 @@ __device__ __forceinline__ void gate_weights(const Dims& d, int64_t t, const flo
 template <int VPT, bool GIVEN>
 __global__ __launch_bounds__(kCombThreads) void combine_vec_kernel(Dims d, const float* __restrict__ topk_val,
                                                                    const int32_t* __restrict__ slot_pos,
-                                                                   const uint4* __restrict__ expert_out,
-                                                                   uint4* __restrict__ out, int32_t* __restrict__ status) {
+                                                                   const uint16_t* __restrict__ expert_out,
+                                                                   uint16_t* __restrict__ out,
+                                                                   int32_t* __restrict__ status) {
   __shared__ float w_s[kMaxK];
   __shared__ int32_t p_s[kMaxK];
   const int64_t t = blockIdx.x;
   gate_weights<GIVEN>(d, t, topk_val, slot_pos, w_s, p_s, status);
-  const int vpr = d.H / 8;
+  const int vpr = (d.H + 7) / 8;
   // a row's columns in gridDim.y parts (few tokens), each of the same work
   for (int base = blockIdx.y * kCombThreads * VPT; base < vpr; base += gridDim.y * kCombThreads * VPT) {
     float acc[VPT][8];
@@ -127,12 +135,13 @@ __global__ __launch_bounds__(kCombThreads) void combine_vec_kernel(Dims d, const
       uint4 x[kRowsInFlight][VPT];
 #pragma unroll
       for (int q = 0; q < kRowsInFlight; ++q) {
-        const uint4* row = expert_out + (int64_t)(pj[q] >= 0 ? pj[q] : 0) * vpr;
+        const uint16_t* row = expert_out + (int64_t)(pj[q] >= 0 ? pj[q] : 0) * d.H;
 #pragma unroll
         for (int u = 0; u < VPT; ++u) {
           const int c = base + threadIdx.x + u * kCombThreads;
-          const v4u y = c < vpr && pj[q] >= 0 ? __builtin_nontemporal_load(reinterpret_cast<const v4u*>(row) + c)
-                                              : v4u{0, 0, 0, 0};  // a skipped slot adds 0 * 0
+          v4u y = {0, 0, 0, 0};  // a skipped slot adds 0 * 0
+          if (c < vpr && pj[q] >= 0)
+            y = __builtin_nontemporal_load(reinterpret_cast<const v4u_any*>(row + vector_at(c, d.H)));
           x[q][u] = make_uint4(y.x, y.y, y.z, y.w);
         }
       }
@@ -142,23 +151,21 @@ __global__ __launch_bounds__(kCombThreads) void combine_vec_kernel(Dims d, const
 #pragma unroll
           for (int u = 0; u < VPT; ++u) fma_row(acc[u], wj[q], x[q][u]);
     }
-    uint4* dst = out + t * vpr;
+    uint16_t* dst = out + t * d.H;
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {
       const int c = base + threadIdx.x + u * kCombThreads;
       if (c < vpr) {
-        uint4 y;
-        y.x = to_bf16(acc[u][0]) | (to_bf16(acc[u][1]) << 16);
-        y.y = to_bf16(acc[u][2]) | (to_bf16(acc[u][3]) << 16);
-        y.z = to_bf16(acc[u][4]) | (to_bf16(acc[u][5]) << 16);
-        y.w = to_bf16(acc[u][6]) | (to_bf16(acc[u][7]) << 16);
-        dst[c] = y;
+        v4u y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = to_bf16(acc[u][2 * i]) | (to_bf16(acc[u][2 * i + 1]) << 16);
+        *reinterpret_cast<v4u_any*>(dst + vector_at(c, d.H)) = y;
       }
     }
   }
 }
 
-// Any H: one bf16 element per thread and step.
+// H < 8: one bf16 element per thread.
 template <bool GIVEN>
 __global__ __launch_bounds__(kCombThreads) void combine_u16_kernel(Dims d, const float* __restrict__ topk_val,
                                                                    const int32_t* __restrict__ slot_pos,
@@ -195,6 +202,13 @@ __device__ __forceinline__ void dot_row(float* dot, const v4u& g, const v4u& x) 
   }
 }
 
+// 8 bf16 values with zeros for the first `count` of them.
+__device__ __forceinline__ v4u without(v4u x, int count) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] &= (2 * i >= count ? 0xffffu : 0u) | (2 * i + 1 >= count ? 0xffff0000u : 0u);
+  return x;
+}
+
 // w times 8 bf16 values, rounded once.
 __device__ __forceinline__ v4u scaled_row(float w, const v4u& g) {
   v4u y;
@@ -214,14 +228,14 @@ __global__ __launch_bounds__(kCombThreads) void combine_grad_vec_kernel(
   __shared__ int32_t p_s[kMaxK];
   __shared__ float dot_s[kCombThreads / 64][ROWS];
   const int groups = (d.k + ROWS - 1) / ROWS;
-  const int vpr = d.H / 8;
+  const int vpr = (d.H + 7) / 8;
   const int64_t blocks = (int64_t)d.T * groups;
   for (int64_t block = blockIdx.x; block < blocks; block += gridDim.x) {  // once, below 2^23 blocks
     const int64_t t = block / groups;
     const int j0 = (int)(block - t * groups) * ROWS;
     __syncthreads();  // the last round's weights and sums have been read
     gate_weights<true>(d, t, weight, slot_pos, w_s, p_s, status);
-    const v4u* __restrict__ g_row = reinterpret_cast<const v4u*>(grad_out) + t * vpr;
+    const uint16_t* __restrict__ g_row = grad_out + t * d.H;
     float dot[ROWS];
 #pragma unroll
     for (int q = 0; q < ROWS; ++q) dot[q] = 0.0f;
@@ -230,26 +244,33 @@ __global__ __launch_bounds__(kCombThreads) void combine_grad_vec_kernel(
 #pragma unroll
       for (int u = 0; u < VPT; ++u) {
         const int c = base + threadIdx.x + u * kCombThreads;
-        g[u] = c < vpr ? g_row[c] : v4u{0, 0, 0, 0};
+        g[u] = v4u{0, 0, 0, 0};
+        if (c < vpr) g[u] = *reinterpret_cast<const v4u_any*>(g_row + vector_at(c, d.H));
       }
 #pragma unroll
       for (int q = 0; q < ROWS; ++q) {
         const int p = j0 + q < d.k ? p_s[j0 + q] : -1;
         if (p < 0) continue;  // the same for the whole workgroup
-        const v4u* x_row = reinterpret_cast<const v4u*>(expert_out) + (int64_t)p * vpr;
-        v4u* y_row = reinterpret_cast<v4u*>(grad_rows) + (int64_t)p * vpr;
+        const uint16_t* x_row = expert_out + (int64_t)p * d.H;
+        uint16_t* y_row = grad_rows + (int64_t)p * d.H;
         const float w = w_s[j0 + q];
         v4u x[VPT];
 #pragma unroll
         for (int u = 0; u < VPT; ++u) {
           const int c = base + threadIdx.x + u * kCombThreads;
-          x[u] = c < vpr ? __builtin_nontemporal_load(x_row + c) : v4u{0, 0, 0, 0};
+          x[u] = v4u{0, 0, 0, 0};
+          if (c < vpr) x[u] = __builtin_nontemporal_load(reinterpret_cast<const v4u_any*>(x_row + vector_at(c, d.H)));
         }
 #pragma unroll
         for (int u = 0; u < VPT; ++u) {
           const int c = base + threadIdx.x + u * kCombThreads;
-          if (c < vpr) __builtin_nontemporal_store(scaled_row(w, g[u]), y_row + c);
-          dot_row(&dot[q], g[u], x[u]);
+          if (c < vpr)
+            __builtin_nontemporal_store(scaled_row(w, g[u]), reinterpret_cast<v4u_any*>(y_row + vector_at(c, d.H)));
+          const int again = 8 * c - (d.H - 8);  // values that the vector before has counted
+          if (again > 0 && c < vpr)
+            dot_row(&dot[q], without(g[u], again), without(x[u], again));
+          else
+            dot_row(&dot[q], g[u], x[u]);
         }
       }
     }
@@ -266,7 +287,7 @@ __global__ __launch_bounds__(kCombThreads) void combine_grad_vec_kernel(
   }
 }
 
-// Any H: one bf16 element per thread and step.
+// H < 8: one bf16 element per thread.
 __global__ __launch_bounds__(kCombThreads) void combine_grad_u16_kernel(
     Dims d, const float* __restrict__ weight, const int32_t* __restrict__ slot_pos,
     const uint16_t* __restrict__ expert_out, const uint16_t* __restrict__ grad_out,
@@ -298,22 +319,23 @@ template <bool GIVEN>
 hipError_t launch_sum(const Dims& d, const float* topk_val, const int32_t* slot_pos, const uint16_t* expert_out,
                       uint16_t* out, int32_t* status, hipStream_t st) {
   if (d.T == 0) return hipSuccess;
-  const bool vec = (d.H % 8) == 0 && ((uintptr_t)expert_out % 16) == 0 && ((uintptr_t)out % 16) == 0;
-  if (vec) {
+  if (d.H >= 8) {
     // A row of at most kCombThreads vectors takes one round: no dead registers.
     // Tokens too few for the chip give each round a workgroup of its own.  Given
     // weights take one vector a round always: four took 306 us against 192 for
     // 8192 tokens of 8 rows of 7168, and 805 against 838 at best (loads without
     // branches) for 32768.
-    const int rounds = (d.H / 8 + kCombThreads - 1) / kCombThreads;
+    const int rounds = ((d.H + 7) / 8 + kCombThreads - 1) / kCombThreads;
     const bool few = d.T < kFewTokens;
-    if (GIVEN || rounds == 1 || few)
+    const bool one = GIVEN || rounds == 1 || few;
+    if constexpr (!GIVEN) {
+      if (!one)
+        hipLaunchKernelGGL((combine_vec_kernel<4, false>), dim3(d.T), dim3(kCombThreads), 0, st, d, topk_val, slot_pos,
+                           expert_out, out, status);
+    }
+    if (one)
       hipLaunchKernelGGL((combine_vec_kernel<1, GIVEN>), dim3(d.T, few ? rounds : 1), dim3(kCombThreads), 0, st, d,
-                         topk_val, slot_pos,
-                         reinterpret_cast<const uint4*>(expert_out), reinterpret_cast<uint4*>(out), status);
-    else
-      hipLaunchKernelGGL((combine_vec_kernel<4, GIVEN>), dim3(d.T), dim3(kCombThreads), 0, st, d, topk_val, slot_pos,
-                         reinterpret_cast<const uint4*>(expert_out), reinterpret_cast<uint4*>(out), status);
+                         topk_val, slot_pos, expert_out, out, status);
   } else {
     hipLaunchKernelGGL((combine_u16_kernel<GIVEN>), dim3(d.T), dim3(kCombThreads), 0, st, d, topk_val, slot_pos, expert_out,
                        out, status);
@@ -352,14 +374,12 @@ hipError_t launch_combine_grad(const Dims& d, const float* weight, const int32_t
                                const uint16_t* expert_out, const uint16_t* grad_out, uint16_t* grad_expert_out,
                                float* grad_weight, int32_t* status, hipStream_t st) {
   if (d.T == 0) return hipSuccess;
-  const bool vec = (d.H % 8) == 0 && ((uintptr_t)expert_out % 16) == 0 && ((uintptr_t)grad_out % 16) == 0 &&
-                   ((uintptr_t)grad_expert_out % 16) == 0;
   // Four rows to a workgroup (one, two and eight measured within 3 % of it), or
   // one where tokens are few; a row in one round of the threads or four vectors each.
-  const bool narrow = d.H / 8 <= kCombThreads;
+  const bool narrow = (d.H + 7) / 8 <= kCombThreads;
   auto launch = d.T < kFewTokens ? (narrow ? launch_combine_grad_rows<1, 1> : launch_combine_grad_rows<4, 1>)
                                  : (narrow ? launch_combine_grad_rows<1, 4> : launch_combine_grad_rows<4, 4>);
-  if (!vec)
+  if (d.H < 8)
     hipLaunchKernelGGL(combine_grad_u16_kernel, dim3(d.T), dim3(kCombThreads), 0, st, d, weight, slot_pos, expert_out,
                        grad_out, grad_expert_out, grad_weight, status);
   else

@@ -8,6 +8,9 @@ namespace moe {
 namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// The same from any address of a 16-bit type: rows of odd widths begin anywhere,
+// and the memory path takes 16 bytes from there in one instruction.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ float bf16_low(uint32_t w) { return __uint_as_float(w << 16); }

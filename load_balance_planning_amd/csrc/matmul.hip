@@ -86,8 +86,9 @@ __global__ __launch_bounds__(256) void matmul_rows16_kernel(Instances in, const 
     if (r0 + orow < sp.end) {
       uint16_t* dst = y + (r0 + orow) * n + c0 + oc;
       const uint32_t lo = pack_bf16(sum[0], sum[1]), hi = pack_bf16(sum[2], sum[3]);
-      if (c0 + oc + 3 < n && n % 4 == 0 && ((uintptr_t)y & 7) == 0) {
-        *reinterpret_cast<u32x2*>(dst) = u32x2{lo, hi};
+      if (c0 + oc + 3 < n) {
+        typedef u32x2 u32x2_any __attribute__((aligned(2)));
+        *reinterpret_cast<u32x2_any*>(dst) = u32x2{lo, hi};
       } else {
         if (c0 + oc < n) dst[0] = (uint16_t)lo;
         if (c0 + oc + 1 < n) dst[1] = (uint16_t)(lo >> 16);
@@ -162,7 +163,7 @@ struct TileShape {
 // the rows need (a bad instance has none).  All threads of a workgroup of 256.
 // Instances that lie one behind the other need at most rows / ROWS + 1 each, in
 // all row_tile_ids; offsets that fall may repeat rows without end, and get none.
-__device__ __forceinline__ int count_row_tiles(const Instances& in, int rows, int32_t* pre, int32_t* sums) {
+[[maybe_unused]] __device__ __forceinline__ int count_row_tiles(const Instances& in, int rows, int32_t* pre, int32_t* sums) {
   const int n = instance_count(in), per = (n + 255) / 256;
   const int first = threadIdx.x * per;
   Span sp;
@@ -194,7 +195,7 @@ __device__ __forceinline__ int count_row_tiles(const Instances& in, int rows, in
 }
 
 // The instance of row tile t < pre[n]: the last with pre[i] <= t.  One wave, two rounds of 64.
-__device__ __forceinline__ int instance_of(const int32_t* pre, int n, int t) {
+[[maybe_unused]] __device__ __forceinline__ int instance_of(const int32_t* pre, int n, int t) {
   const int lane = threadIdx.x & 63, stride = (n + 63) / 64;
   const uint64_t coarse = __ballot(lane * stride < n && pre[min(lane * stride, n)] <= t);
   const int first = (__popcll(coarse) - 1) * stride;
@@ -369,7 +370,6 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), BC == 256 ? 
       if (loads) __builtin_amdgcn_sched_group_barrier(0x020, (S::kPassC + S::kPassT + kProducts - 1) / kProducts, 0);
     }
   };
-  const bool vec = n % 8 == 0 && ((uintptr_t)y & 15) == 0;
   static_assert(S::kWaves == 4 && BC == BT, "four equal parts");
   constexpr int kTI = kOwnPlace ? S::kC / 2 : 1, kTJ = kOwnPlace ? S::kT : 1;  // turns of 64 channels by 32 rows, or one
   constexpr int kOwn = 2 * S::kWaveC * S::kWaveT / (kTI * kTJ);
@@ -438,7 +438,7 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), BC == 256 ? 
       fetch(min(2, nb - 1));
     }
     store_wave_tile<kTI, kTJ>(acc, own, y + (int64_t)(done.r0 + wt) * n + done.c0 + wc, n, done.rows - wt,
-                              done.chans - wc, vec);
+                              done.chans - wc);
     if (!more) break;
   }
 #endif

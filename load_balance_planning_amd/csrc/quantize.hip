@@ -34,24 +34,43 @@ __device__ __forceinline__ uint32_t max_of_8(uint32_t v) {
   return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, false));
 }
 
-// 16 bf16 values of a row from column c on; past `cols` zeros.  VEC: c and
-// cols are multiples of 8 and the row is 16-byte aligned.
-template <bool VEC>
-__device__ __forceinline__ void load16(const uint16_t* __restrict__ row, int c, int cols, float* f) {
-  if (VEC) {
+// Eight bf16 values from element `at` of a tensor.
+__device__ __forceinline__ u32x4 load8(const uint16_t* __restrict__ x, int64_t at) {
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(x + at));
+}
+// Those of a load that would leave the tensor's `total` elements, one by one;
+// zeros outside.
+__device__ __forceinline__ u32x4 load8_edge(const uint16_t* __restrict__ x, int64_t at, int64_t total) {
+  uint64_t half[2] = {0ull, 0ull};
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      u32x4 w = {0u, 0u, 0u, 0u};
-      if (c + 8 * h < cols) w = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(row + c + 8 * h));
+  for (int h = 0; h < 2; ++h)
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j)
+      if (at + 4 * h + j >= 0 && at + 4 * h + j < total) half[h] |= (uint64_t)x[at + 4 * h + j] << (16 * j);
+  return u32x4{(uint32_t)half[0], (uint32_t)(half[0] >> 32), (uint32_t)half[1], (uint32_t)(half[1] >> 32)};
+}
+__device__ __forceinline__ u32x4 load8(const uint16_t* __restrict__ x, int64_t at, int64_t total) {
+  return at >= 0 && at + 8 <= total ? load8(x, at) : load8_edge(x, at, total);
+}
+__device__ __forceinline__ void widen8(const u32x4& w, float* f) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f[8 * h + 2 * j] = bf16_low(w[j]);
-        f[8 * h + 2 * j + 1] = bf16_high(w[j]);
-      }
-    }
-  } else {
+  for (int j = 0; j < 4; ++j) {
+    f[2 * j] = bf16_low(w[j]);
+    f[2 * j + 1] = bf16_high(w[j]);
+  }
+}
+// The 16 values from element `at` on, `left` of them of the row (what follows is
+// the next row's): zeros behind those.
+__device__ __forceinline__ void load16(const uint16_t* __restrict__ x, int64_t at, int left, int64_t total, float* f) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) f[j] = c + j < cols ? bf16_low(row[c + j]) : 0.0f;
+  for (int h = 0; h < 2; ++h) {
+    u32x4 w = {0u, 0u, 0u, 0u};
+    if (8 * h < left) w = load8(x, at + 8 * h, total);
+    widen8(w, f + 8 * h);
+  }
+  if (left < 16) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) f[j] = j < left ? f[j] : 0.0f;
   }
 }
 
@@ -74,16 +93,12 @@ __device__ __forceinline__ void store_block(const float* f, uint8_t* __restrict_
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 __device__ __forceinline__ float swiglu(float g, float u) { return g * sigmoid(g) * u; }
-// d(swiglu)/d gate times the incoming gradient.
-__device__ __forceinline__ float swiglu_dgate(float g, float u, float da) {
-  const float s = sigmoid(g);
-  return da * u * (s * (1.0f + g * (1.0f - s)));
-}
-
 // KIND kPlain: x [rows][cols].  kSwiglu: x [rows][2 cols] (gate, up), cols = f.
 // kSwigluGrad: x [rows][cols] (gate, up) and grad [rows][cols / 2], cols = 2 f.
-// A block of 128 output columns per eight lanes.
-template <int KIND, bool VEC>
+// A block of 128 output columns per eight lanes.  Rows of any width are read 16
+// bytes at a time (element by element, widths that are no multiple of 8 took four
+// times as long: 27672 rows of f = 2690, 324 us and 86 so; its gradient, 20000 rows, 495 and 147).
+template <int KIND>
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const uint16_t* __restrict__ x,
                                                                  const uint16_t* __restrict__ grad, int64_t rows,
                                                                  int cols, uint8_t* __restrict__ q,
@@ -98,26 +113,50 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const uint16_t*
     const int c = b * kBlk + lane8 * kPerLane;
     float f[kPerLane];
     if (KIND == kPlain) {
-      load16<VEC>(x + r * cols, c, cols, f);
+      load16(x, r * cols + c, cols - c, rows * cols, f);
     } else if (KIND == kSwiglu) {
       float u[kPerLane];
-      const uint16_t* row = x + r * 2 * cols;
-      load16<VEC>(row, c, cols, f);
-      load16<VEC>(row + cols, c, cols, u);
+      load16(x, r * 2 * cols + c, cols - c, rows * 2 * cols, f);
+      load16(x, r * 2 * cols + cols + c, cols - c, rows * 2 * cols, u);
 #pragma unroll
       for (int j = 0; j < kPerLane; ++j) f[j] = c + j < cols ? swiglu(f[j], u[j]) : 0.0f;
     } else {
-      // columns [0, half) are the gate's, [half, 2 half) the up's; 16 columns
-      // may cross from one to the other
+      // Columns [0, half) are the gate's, [half, 2 half) the up's; 16 columns may
+      // cross from one to the other.  The up's columns need gate and gradient
+      // from `half` columns before: for those, that many elements earlier.
       const int half = cols / 2;
-      const uint16_t *row = x + r * cols, *grow = grad + r * half;
+      float u[kPerLane], da[kPerLane];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int o = c + 8 * h;
+        u32x4 g0 = {0u, 0u, 0u, 0u}, d0 = g0, u0 = g0, g1 = g0, d1 = g0;
+        if (o < half) {
+          g0 = load8(x, r * cols + o, rows * cols);
+          u0 = load8(x, r * cols + half + o, rows * cols);
+          d0 = load8(grad, r * half + o, rows * half);
+        }
+        if (o + 8 > half && o < cols) {
+          g1 = load8(x, r * cols + o - half, rows * cols);
+          d1 = load8(grad, r * half + o - half, rows * half);
+        }
+        float fg0[8], fg1[8], fd0[8], fd1[8];
+        widen8(g0, fg0);
+        widen8(g1, fg1);
+        widen8(d0, fd0);
+        widen8(d1, fd1);
+        widen8(u0, u + 8 * h);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          f[8 * h + j] = o + j < half ? fg0[j] : fg1[j];
+          da[8 * h + j] = o + j < half ? fd0[j] : fd1[j];
+        }
+      }
 #pragma unroll
       for (int j = 0; j < kPerLane; ++j) {
         const int o = c + j;
-        float v = 0.0f;
-        if (o < half) v = swiglu_dgate(bf16_low(row[o]), bf16_low(row[half + o]), bf16_low(grow[o]));
-        else if (o < cols) v = bf16_low(grow[o - half]) * (bf16_low(row[o - half]) * sigmoid(bf16_low(row[o - half])));
-        f[j] = v;
+        const float g = f[j], s = sigmoid(g);
+        const float v = o < half ? da[j] * u[j] * (s * (1.0f + g * (1.0f - s))) : da[j] * (g * s);
+        f[j] = o < cols ? v : 0.0f;
       }
     }
     store_block(f, q + (r * nb + b) * kBlk, scale + r * ns + b, lane8, b == nb - 1 ? ns - nb : 0);
@@ -137,9 +176,12 @@ __global__ __launch_bounds__(kThreads) void swiglu_grad_kernel(const uint16_t* _
     const int b = (int)(i - r * nb);
     const int c = b * kBlk + lane8 * kPerLane;
     float g[kPerLane], u[kPerLane], da[kPerLane];
-    load16<true>(y + r * 2 * f, c, f, g);
-    load16<true>(y + r * 2 * f + f, c, f, u);
-    load16<true>(grad + r * f, c, f, da);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      widen8(load8(y, r * 2 * f + c + 8 * h), g + 8 * h);
+      widen8(load8(y, r * 2 * f + f + c + 8 * h), u + 8 * h);
+      widen8(load8(grad, r * f + c + 8 * h), da + 8 * h);
+    }
 #pragma unroll
     for (int j = 0; j < kPerLane; ++j) {
       const float s = sigmoid(g[j]);
@@ -157,9 +199,9 @@ __global__ __launch_bounds__(kThreads) void swiglu_grad_kernel(const uint16_t* _
 // 8g+7, columns 8 c8 .. 8 c8+7, so a wave loads whole 256-byte row pieces and
 // every thread can transpose its 8 x 8 bytes itself.
 constexpr int kTransStride = kBlk + 16;  // LDS bytes of a row of the transposed block
-template <bool VEC>
-__global__ __launch_bounds__(kThreads) void quantize_weights_kernel(const uint16_t* __restrict__ w, int n, int k,
-                                                                    int nbn, int nbk, uint8_t* __restrict__ q,
+__global__ __launch_bounds__(kThreads) void quantize_weights_kernel(const uint16_t* __restrict__ w, int experts,
+                                                                    int n, int k, int nbn, int nbk,
+                                                                    uint8_t* __restrict__ q,
                                                                     uint8_t* __restrict__ scale,
                                                                     uint8_t* __restrict__ qt,
                                                                     uint8_t* __restrict__ scale_t) {
@@ -172,18 +214,20 @@ __global__ __launch_bounds__(kThreads) void quantize_weights_kernel(const uint16
   const int c = bk * kBlk + 8 * c8, r0 = bn * kBlk + 8 * rg;
   const uint16_t* __restrict__ base = w + (int64_t)e * n * k;
   u32x4 v[8];
+  const int rows = c < k ? min(8, n - r0) : 0;  // this thread's, possibly none
+  if (rows == 8 && c + 8 <= k) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    v[j] = u32x4{0u, 0u, 0u, 0u};
-    if (r0 + j < n) {
-      const uint16_t* row = base + (int64_t)(r0 + j) * k;
-      if (VEC) {
-        if (c < k) v[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(row + c));
-      } else {
+    for (int j = 0; j < 8; ++j) v[j] = load8(base, (int64_t)(r0 + j) * k + c);
+  } else {
+    const int64_t total = (int64_t)(experts - e) * n * k;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (c + i < k) v[j][i / 2] |= (uint32_t)row[c + i] << (16 * (i & 1));
-      }
+    for (int j = 0; j < 8; ++j) {
+      const int64_t at = (int64_t)(r0 + (j < rows ? j : 0)) * k + c;
+      v[j] = u32x4{0u, 0u, 0u, 0u};
+      if (j < rows) v[j] = at + 8 <= total ? load8(base, at) : load8_edge(base, at, total);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)  // columns from k on are the next row's
+        v[j][i] &= (c + 2 * i < k ? 0xffffu : 0u) | (c + 2 * i + 1 < k ? 0xffff0000u : 0u);
     }
   }
   uint32_t top = 0;
@@ -252,42 +296,31 @@ unsigned grid_of(int64_t blocks) {
   return (unsigned)(g < kMaxGrid ? g : kMaxGrid);
 }
 
-bool vec16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
 template <int KIND>
-hipError_t launch_rows(const uint16_t* x, const uint16_t* grad, int64_t rows, int cols, bool vec, uint8_t* q,
-                       uint8_t* scale, hipStream_t st) {
+hipError_t launch_rows(const uint16_t* x, const uint16_t* grad, int64_t rows, int cols, uint8_t* q, uint8_t* scale,
+                       hipStream_t st) {
   if (rows == 0) return hipSuccess;
-  const dim3 grid(grid_of(rows * (padded_cols(cols) / kBlk)));
-  if (vec)
-    hipLaunchKernelGGL((quantize_rows_kernel<KIND, true>), grid, dim3(kThreads), 0, st, x, grad, rows, cols, q, scale);
-  else
-    hipLaunchKernelGGL((quantize_rows_kernel<KIND, false>), grid, dim3(kThreads), 0, st, x, grad, rows, cols, q,
-                       scale);
+  hipLaunchKernelGGL((quantize_rows_kernel<KIND>), dim3(grid_of(rows * (padded_cols(cols) / kBlk))), dim3(kThreads), 0,
+                     st, x, grad, rows, cols, q, scale);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_quantize(const uint16_t* x, int64_t rows, int32_t cols, uint8_t* q, uint8_t* scale, hipStream_t st) {
-  return launch_rows<kPlain>(x, nullptr, rows, cols, cols % 8 == 0 && vec16(x), q, scale, st);
+  return launch_rows<kPlain>(x, nullptr, rows, cols, q, scale, st);
 }
 
 hipError_t launch_swiglu(const uint16_t* y, int64_t rows, int32_t f, uint8_t* q, uint8_t* scale, hipStream_t st) {
-  return launch_rows<kSwiglu>(y, nullptr, rows, f, f % 8 == 0 && vec16(y), q, scale, st);
+  return launch_rows<kSwiglu>(y, nullptr, rows, f, q, scale, st);
 }
 
 hipError_t launch_swiglu_grad(const uint16_t* y, const uint16_t* grad, int64_t rows, int32_t f, uint8_t* q,
                               uint8_t* scale, hipStream_t st) {
+  if (f % kBlk != 0) return launch_rows<kSwigluGrad>(y, grad, rows, 2 * f, q, scale, st);
   if (rows == 0) return hipSuccess;
-  if (f % kBlk == 0 && vec16(y) && vec16(grad)) {
-    hipLaunchKernelGGL(swiglu_grad_kernel, dim3(grid_of(rows * (f / kBlk))), dim3(kThreads), 0, st, y, grad, rows, f,
-                       q, scale);
-    return hipGetLastError();
-  }
-  // element by element: a block may hold gate and up columns
-  hipLaunchKernelGGL((quantize_rows_kernel<kSwigluGrad, false>), dim3(grid_of(rows * (padded_cols(2 * f) / kBlk))),
-                     dim3(kThreads), 0, st, y, grad, rows, 2 * f, q, scale);
+  hipLaunchKernelGGL(swiglu_grad_kernel, dim3(grid_of(rows * (f / kBlk))), dim3(kThreads), 0, st, y, grad, rows, f, q,
+                     scale);
   return hipGetLastError();
 }
 
@@ -296,12 +329,8 @@ hipError_t launch_quantize_weights(const uint16_t* w, int32_t experts, int32_t n
   const int nbn = (int)(padded_cols(n) / kBlk), nbk = (int)(padded_cols(k) / kBlk);
   const int64_t blocks = (int64_t)experts * nbn * nbk;
   if (blocks == 0) return hipSuccess;
-  if (k % 8 == 0 && vec16(w))
-    hipLaunchKernelGGL((quantize_weights_kernel<true>), dim3((unsigned)blocks), dim3(kThreads), 0, st, w, n, k, nbn,
-                       nbk, q, scale, qt, scale_t);
-  else
-    hipLaunchKernelGGL((quantize_weights_kernel<false>), dim3((unsigned)blocks), dim3(kThreads), 0, st, w, n, k, nbn,
-                       nbk, q, scale, qt, scale_t);
+  hipLaunchKernelGGL(quantize_weights_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, st, w, experts, n, k, nbn,
+                     nbk, q, scale, qt, scale_t);
   return hipGetLastError();
 }
 

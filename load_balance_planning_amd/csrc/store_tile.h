@@ -29,7 +29,7 @@ __device__ __forceinline__ void wave_sync() {
 }
 template <int TI, int TJ, int NI, int NJ>
 __device__ __forceinline__ void store_wave_tile(const acc16 (&acc)[NI][NJ], unsigned char* lds, uint16_t* out,
-                                                int64_t stride, int rows_left, int cols_left, bool vec) {
+                                                int64_t stride, int rows_left, int cols_left) {
   static_assert(NI % TI == 0 && NJ % TJ == 0, "whole turns");
   constexpr int kI = NI / TI, kJ = NJ / TJ, kPlaces = 4 * kI, kRowsAtOnce = 64 / kPlaces;
   int lane = threadIdx.x & 63;
@@ -61,8 +61,8 @@ __device__ __forceinline__ void store_wave_tile(const acc16 (&acc)[NI][NJ], unsi
       const int row = 32 * kJ * tj + part_row, col = 32 * kI * ti + 8 * p;
       if (row >= rows_left || col >= cols_left) continue;
       uint16_t* dst = out + row * stride + col;
-      if (vec && col + 8 <= cols_left) {
-        *reinterpret_cast<u32x4*>(dst) = o;
+      if (col + 8 <= cols_left) {
+        *reinterpret_cast<u32x4_any*>(dst) = o;
       } else {
 #pragma unroll
         for (int q = 0; q < 8; ++q)

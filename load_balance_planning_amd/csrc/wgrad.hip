@@ -70,7 +70,7 @@ __device__ __forceinline__ void steps_load(Steps* s, const Instances& in) {
   s->mask = __ballot(mine < s->n_inst && e == s->expert && s->begin >= 0 && s->begin <= s->end_of &&
                      s->end_of <= in.rows);
 }
-__device__ __forceinline__ void steps_begin(Steps* s, const Instances& in, int expert) {
+[[maybe_unused]] __device__ __forceinline__ void steps_begin(Steps* s, const Instances& in, int expert) {
   s->expert = expert;
   s->i0 = 0;
   s->row = s->end = 0;
@@ -78,7 +78,7 @@ __device__ __forceinline__ void steps_begin(Steps* s, const Instances& in, int e
   steps_load(s, in);
 }
 // The next step's first row and its rows (0: no more).
-__device__ __forceinline__ void next_step(Steps* s, const Instances& in, int* row, int* rows) {
+[[maybe_unused]] __device__ __forceinline__ void next_step(Steps* s, const Instances& in, int* row, int* rows) {
   while (s->row >= s->end) {
     if (s->mask == 0ull) {
       if (s->i0 + 64 >= s->n_inst) break;
@@ -173,7 +173,7 @@ __global__ __launch_bounds__(kThreads, COLS == 256 ? 1 : 2) void wgrad_kernel(In
     }
   };
   const int wk = (wave & 1) * S::kWave, wn = (wave >> 1) * S::kWave;
-  const int r = lane & 31, g = lane >> 5;
+  const int g = lane >> 5;
   // Reads: lane 4t + q of 16 lends the address of row t, four columns, which
   // go to lanes 4q .. 4q + 3.  dy's columns stay in order; x's are taken so that
   // matrix row 8a + 4h + j is column 16h + 4a + j.
@@ -296,8 +296,7 @@ __global__ __launch_bounds__(kThreads, COLS == 256 ? 1 : 2) void wgrad_kernel(In
   __syncthreads();  // every wave has its last operands: LDS is free
   unsigned char* own = wave == 0 ? x0_s : wave == 1 ? y0_s : wave == 2 ? x1_s : y1_s;
   const int c = tn * COLS + wn, col = tk * COLS + wk;
-  store_wave_tile<1, 1>(acc, own, dw + ((int64_t)e * n + c) * k + col, k, n - c, k - col,
-                  k % 8 == 0 && ((uintptr_t)dw & 15) == 0);
+  store_wave_tile<1, 1>(acc, own, dw + ((int64_t)e * n + c) * k + col, k, n - c, k - col);
 #endif
 }
 

@@ -37,7 +37,10 @@ def layer_of(mp, T, k, H):
                                    (12, 8, 2048), (12, 8, 2056), (5, 4, 8200), (30, 5, 1001), (7, 3, 16400),
                                    # around 512 tokens, where a token's work is no longer split
                                    (511, 2, 2056), (512, 3, 2056), (700, 5, 2048), (1000, 6, 264), (600, 2, 8200),
-                                   (513, 9, 1001), (520, 7, 4104)])
+                                   (513, 9, 1001), (520, 7, 4104),
+                                   # rows of less than a vector, of one, and whose last overlaps the one before
+                                   (5, 3, 7), (4, 2, 8), (6, 4, 9), (3, 8, 15), (40, 8, 2049), (600, 3, 7167), (30, 4, 2047),
+                                   (700, 2, 5), (515, 2, 10)])
 def test_weighted_sum_and_gradients(mp, T, k, H):
     print("combine weighted T=%d k=%d H=%d" % (T, k, H), flush=True)
     rows, g, w, pos = data(T + k + H, T, k, H)
@@ -88,6 +91,28 @@ def test_weights_that_are_no_softmax(mp):
     assert (out[0] == 0).all() and not torch.isfinite(out[1]).any() and torch.isnan(out[2]).all()
     assert torch.isfinite(out[3:]).all() and torch.isfinite(gw).all()
     assert (gr.cpu()[pos.long().view(T, k)[0]] == 0).all()
+    layer.close()
+
+
+@pytest.mark.parametrize("T,H", [(20, 13), (600, 13), (20, 2051)])
+def test_an_infinity_counts_once(mp, T, H):
+    """The last vectors of a row of odd width overlap: an infinity in both, with a gradient of zero or not."""
+    k = 2
+    rows, g, w, pos = data(3, T, k, H)
+    layer = layer_of(mp, T, k, H)
+    d = lambda t: t.to(layer.device)
+    at = H - H % 8 - 1                      # in the last vector and the one before
+    rows[pos[0], at] = torch.inf
+    rows[pos[2 * k], 0] = -torch.inf
+    g[0, at] = 2.0
+    g[2, 0] = 0.5
+    out = layer.combine_weighted(d(rows), d(w), slot_pos=d(pos)).cpu()
+    gr, gw = layer.combine_grad(d(rows), d(g), d(w), slot_pos=d(pos))
+    assert layer.status() == 0
+    gw = gw.cpu()
+    assert gw[0, 0] == torch.inf and gw[2, 0] == -torch.inf and torch.isfinite(gw.flatten()[[1, 2, 3, 5]]).all()
+    bad = ~torch.isfinite(out)
+    assert bad[0, at] and bad[2, 0] and int(bad.sum()) == 2 and torch.isfinite(gr).all()
     layer.close()
 
 

@@ -163,6 +163,47 @@ def test_unaligned_rows(mp, small):
     same_blocks(small.quantize_weights(wv), *refs.quantize(w.double(), 128))
 
 
+@pytest.mark.parametrize("rows,cols", [(2, 9), (7, 1001), (513, 2047), (1, 15), (4, 17), (3, 129)])
+def test_rows_of_odd_widths(mp, small, rows, cols):
+    test_rows(mp, small, rows, cols)
+
+
+@pytest.mark.parametrize("E,n,k", [(2, 33, 1001), (1, 500, 7), (3, 129, 255), (2, 9, 1), (1, 3, 2399)])
+def test_matrices_of_odd_widths(mp, small, E, n, k):
+    test_matrices(mp, small, E, n, k)
+
+
+@pytest.mark.parametrize("rows,f", [(1, 3), (2, 5), (9, 131), (300, 1455), (17, 63), (40, 119), (3, 129), (1, 8), (2, 12)])
+def test_gated_activation_of_odd_widths(mp, small, rows, f):
+    test_gated_activation_and_its_gradient(mp, small, rows, f)
+
+
+@pytest.mark.parametrize("value", [torch.inf, torch.nan])
+def test_neighbours_stay_apart(mp, small, value):
+    """Rows and matrices of odd widths are read past their ends: what stands there marks only its own blocks."""
+    rows, f = 12, 133
+    dev = small.device
+    marked = lambda b: b.scale.view(torch.uint8).cpu() == 255
+    x = normal(1, rows, f)
+    x[5] = value
+    m = marked(small.quantize(x.to(dev)))
+    assert m[5, :2].all() and int(m.sum()) == 2
+    y, da = normal(2, rows, 2 * f), normal(3, rows, f)
+    y[5] = value
+    m = marked(small.swiglu(y.to(dev)))
+    assert m[5, :2].all() and int(m.sum()) == 2
+    m = marked(small.swiglu_grad(y.to(dev), da.to(dev)))
+    assert m[5, :3].all() and int(m.sum()) == 3
+    da[7] = value
+    m = marked(small.swiglu_grad(normal(2, rows, 2 * f).to(dev), da.to(dev)))
+    assert m[7, :3].all() and int(m.sum()) == 3
+    w = normal(4, 3, 130, f)
+    w[1] = value
+    b, t = small.quantize_weights(w.to(dev), transposed=True)
+    for m in (marked(b), marked(t)):
+        assert m[1, :, :2].all() and int(m.sum()) == 4
+
+
 def test_no_rows(mp, small):
     b = small.quantize(torch.empty(0, 200, dtype=BF, device=small.device))
     assert b.q.shape == (0, 256) and b.scale.shape == (0, 4)
