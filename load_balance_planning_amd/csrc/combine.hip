@@ -90,9 +90,12 @@ __device__ __forceinline__ void gate_weights(const Dims& d, int64_t t, const flo
       for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off);
       w = e / s;
     }
+    int32_t p = on ? slot_pos[t * d.k + lane] : 0;
+    // Both have arrived before the branch: a load still under way on the path
+    // around it had every row's load below wait for all loads before it.
+    asm volatile("" : "+v"(w), "+v"(p));
     if (on) {
       w_s[lane] = w;
-      int32_t p = slot_pos[t * d.k + lane];
       const int64_t N = (int64_t)d.T * d.k;
       if (p < 0 || p >= N) {
         atomicOr(status, MOE_STATUS_PLAN_CHECK);
@@ -320,19 +323,19 @@ hipError_t launch_sum(const Dims& d, const float* topk_val, const int32_t* slot_
                       uint16_t* out, int32_t* status, hipStream_t st) {
   if (d.T == 0) return hipSuccess;
   if (d.H >= 8) {
-    // A row of at most kCombThreads vectors takes one round: no dead registers.
-    // Tokens too few for the chip give each round a workgroup of its own.  Given
-    // weights take one vector a round always: four took 306 us against 192 for
-    // 8192 tokens of 8 rows of 7168, and 805 against 838 at best (loads without
-    // branches) for 32768.
-    const int rounds = ((d.H + 7) / 8 + kCombThreads - 1) / kCombThreads;
+    // One vector a thread and round, or four.  Four read a row in one go, which
+    // pays where the rows are spread over more than some 2 GB and four fill the
+    // threads (rows of 7168, eight a token: 32768 tokens 791 us against 839, 24000
+    // tokens 580 against 609, 16384 tokens 385 against 378, 2048 tokens 52 against
+    // 51; 131072 tokens of rows of 2056: 1310 against 983).  Tokens too few for the
+    // chip give each round a workgroup of its own.
+    const int vpr = (d.H + 7) / 8, rounds = (vpr + kCombThreads - 1) / kCombThreads;
     const bool few = d.T < kFewTokens;
-    const bool one = GIVEN || rounds == 1 || few;
-    if constexpr (!GIVEN) {
-      if (!one)
-        hipLaunchKernelGGL((combine_vec_kernel<4, false>), dim3(d.T), dim3(kCombThreads), 0, st, d, topk_val, slot_pos,
-                           expert_out, out, status);
-    }
+    const bool wide = (int64_t)d.T * d.k * d.H >= (int64_t)1 << 30;
+    const bool one = few || !wide || (rounds & 3) == 1 || (rounds & 3) == 2;
+    if (!one)
+      hipLaunchKernelGGL((combine_vec_kernel<4, GIVEN>), dim3(d.T), dim3(kCombThreads), 0, st, d, topk_val, slot_pos,
+                         expert_out, out, status);
     if (one)
       hipLaunchKernelGGL((combine_vec_kernel<1, GIVEN>), dim3(d.T, few ? rounds : 1), dim3(kCombThreads), 0, st, d,
                          topk_val, slot_pos, expert_out, out, status);

@@ -77,6 +77,34 @@ def test_weighted_sum_and_gradients(mp, T, k, H):
     layer.close()
 
 
+@pytest.mark.parametrize("T,k,H", [(20000, 8, 7168), (33000, 6, 6003)])
+def test_large_layers_sampled(mp, T, k, H):
+    """More than 2^31 bytes of rows, where a thread takes four vectors of a row at a time; rows of odd width too."""
+    print("combine large T=%d k=%d H=%d" % (T, k, H), flush=True)
+    layer = layer_of(mp, T, k, H)
+    dev = layer.device
+    g0 = torch.Generator(device=dev).manual_seed(T)
+    n = lambda *s: torch.randn(*s, generator=g0, device=dev)
+    rows, g, w = torch.empty(T * k, H, dtype=BF, device=dev), n(T, H).to(BF), n(T, k)
+    for part in rows.split(20000):
+        part.copy_(n(*part.shape))
+    pos = torch.randperm(T * k, generator=g0, device=dev).int()
+    out = layer.combine_weighted(rows, w, slot_pos=pos)
+    gr, gw = layer.combine_grad(rows, g, w, slot_pos=pos)
+    assert layer.status() == 0
+    at = torch.cat([torch.tensor([0, T - 1]), torch.randint(0, T, (60,), generator=torch.Generator().manual_seed(1))])
+    p = pos.view(T, k)[at.to(dev)].long()
+    x, wt, gt = rows[p].cpu().double(), w[at.to(dev)].cpu().double(), g[at.to(dev)].cpu().double()
+    y, mag = (x * wt[..., None]).sum(1), (x.abs() * wt.abs()[..., None]).sum(1)
+    grow = 1 + 2.0 ** -8
+    assert ((out[at.to(dev)].cpu().double() - y).abs() <= 2.0 ** -8 * y.abs() + grow * (k + 2) * 2.0 ** -24 * mag).all()
+    want = wt[..., None] * gt[:, None]
+    assert ((gr[p].cpu().double() - want).abs() <= 2.0 ** -8 * (1 + 2.0 ** -23) * want.abs()).all()
+    dots = (x.abs() * gt.abs()[:, None]).sum(-1)
+    assert ((gw[at.to(dev)].cpu().double() - (x * gt[:, None]).sum(-1)).abs() <= (H / 64 + 16) * 2.0 ** -24 * dots).all()
+    layer.close()
+
+
 def test_weights_that_are_no_softmax(mp):
     T, k, H = 24, 4, 64
     rows, g, w, pos = data(1, T, k, H)
