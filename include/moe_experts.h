@@ -48,8 +48,12 @@
  * MOE_ERR_INVALID_ARG.
  *
  * No call here needs memory of its own beyond the handle's workspace, and all
- * but moex_gate leave that workspace alone (the status word aside); every call
- * can be captured into a HIP graph.
+ * but moex_gate leave that workspace alone (the status word aside): those may
+ * run on several streams of one handle at once, for instance an input gradient
+ * beside a weight gradient.  (moe_plan_status waits for the stream of the last
+ * call alone; wait for the others before it.)  moex_gate calls of one handle, and
+ * captured graphs that hold them, run one after the other.  Every call can be
+ * captured into a HIP graph.
  */
 #ifndef MOE_EXPERTS_H
 #define MOE_EXPERTS_H
@@ -112,7 +116,8 @@ int moex_gate(moe_plan_t h, const moex_gate_config* gate, const float* logits, c
  * logits float [T][E]; topk_idx int32 [T][k]; grad_weight float [T][k];
  * grad_logits float [T][E], fully overwritten.  An index outside [0, E) or
  * repeated within a token sets MOE_STATUS_BAD_TOPK (that token's gradient is
- * then unspecified), logits as in moex_gate MOE_STATUS_NAN_LOGIT.
+ * then unspecified), logits as in moex_gate MOE_STATUS_NAN_LOGIT (of a sigmoid
+ * router only the selected experts' logits are read).
  */
 int moex_gate_grad(moe_plan_t h, const moex_gate_config* gate, const float* logits, const int32_t* topk_idx,
                    const float* grad_weight, float* grad_logits, void* stream);

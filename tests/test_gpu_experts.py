@@ -714,6 +714,41 @@ def test_a_captured_layer_replays(mp):
     other.close()
 
 
+def test_one_layer_on_two_streams(mp):
+    """Input and weight gradients of one handle side by side, eager and as two captured graphs."""
+    loads, E, n, k = [700, 1, 0, 333, 500, 64], 6, 520, 392
+    layer = layer_for(mp, sum(loads), E)
+    dev = layer.device
+    plan, off, _ = instances(mp, layer, loads, list(range(E)))
+    kw = dict(plan=plan, inst_offset=off)
+    rows = sum(loads)
+    x, d = layer.quantize(normal(1, rows, k).to(dev)), layer.quantize(normal(2, rows, n).to(dev))
+    w, wt = layer.quantize_weights(normal(3, E, n, k).to(dev), transposed=True)
+    want_dx, want_dw = layer.matmul(d, wt, **kw), layer.wgrad(d, x, **kw)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        dx = [layer.matmul(d, wt, stream=streams[0], **kw) for _ in range(4)]
+        dw = [layer.wgrad(d, x, stream=streams[1], **kw) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(t, want_dx) for t in dx) and all(torch.equal(t, want_dw) for t in dw)
+    graphs, got = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for g, call in zip(graphs, (lambda: layer.matmul(d, wt, **kw), lambda: layer.wgrad(d, x, **kw))):
+        with torch.cuda.graph(g):
+            got.append(call())
+    for _ in range(5):
+        for t in got:
+            t.fill_(3)
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want_dx) and torch.equal(got[1], want_dw)
+    assert layer.status() == 0
+    layer.close()
+
+
 def test_two_layers_on_two_streams(mp):
     T, E, k, R, G, H, F = 128, 16, 4, 2, 1, 256, 128
     layers = [mp.Layer(mp.make_config(T, E, k, R, G, H, 2, expert_bytes=0)) for _ in range(2)]
