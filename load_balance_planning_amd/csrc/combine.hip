@@ -290,6 +290,105 @@ __global__ __launch_bounds__(kCombThreads) void combine_grad_vec_kernel(
   }
 }
 
+// Many tokens with rows of at most 64 vectors and given weights: P lanes (a power
+// of two) hold a token's row, a vector each, so a workgroup has 256 / P tokens
+// (8192 tokens of 8 rows of 512: 17 us with a token to a workgroup and 14 so, the
+// gradient 55 and 28; rows of 148: 15 and 6.5, 45 and 14; but 64 tokens of rows of
+// 512: 3.5 and 3.9, 3.2 and 7.5, whose gradient is split by rows there).
+constexpr int kNarrow = 64;
+inline bool narrow_rows(const Dims& d) { return d.H >= 8 && d.H <= 8 * kNarrow && d.T >= kFewTokens; }
+inline int narrow_lanes(int H) {
+  int P = 1;
+  while (8 * P < H) P *= 2;
+  return P;
+}
+// Row of slot j of token t and its weight; -1 and 0 past the k slots and for a
+// position outside the dispatch buffer, which is reported.
+__device__ __forceinline__ int narrow_slot(const Dims& d, int64_t t, int j, const float* __restrict__ weight,
+                                           const int32_t* __restrict__ slot_pos, float* w, int32_t* status) {
+  *w = 0.0f;
+  if (j >= d.k) return -1;
+  const int p = slot_pos[t * d.k + j];
+  if (p < 0 || p >= (int64_t)d.T * d.k) {
+    atomicOr(status, MOE_STATUS_PLAN_CHECK);
+    return -1;
+  }
+  *w = weight ? weight[t * d.k + j] : 1.0f;
+  return p;
+}
+
+__global__ __launch_bounds__(kCombThreads) void combine_narrow_kernel(Dims d, int P, const float* __restrict__ weight,
+                                                                      const int32_t* __restrict__ slot_pos,
+                                                                      const uint16_t* __restrict__ expert_out,
+                                                                      uint16_t* __restrict__ out,
+                                                                      int32_t* __restrict__ status) {
+  const int lane = threadIdx.x & (P - 1);
+  const int64_t t = (int64_t)blockIdx.x * (kCombThreads / P) + threadIdx.x / P;
+  if (t >= d.T) return;
+  const bool on = 8 * lane < d.H;
+  const int at = vector_at(lane, d.H);
+  float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int j = 0; j < d.k; j += kRowsInFlight) {
+    int p[kRowsInFlight];
+    float w[kRowsInFlight];
+    v4u x[kRowsInFlight];
+#pragma unroll
+    for (int q = 0; q < kRowsInFlight; ++q) p[q] = narrow_slot(d, t, j + q, weight, slot_pos, &w[q], status);
+#pragma unroll
+    for (int q = 0; q < kRowsInFlight; ++q) {
+      x[q] = v4u{0, 0, 0, 0};
+      if (on && p[q] >= 0)
+        x[q] = __builtin_nontemporal_load(reinterpret_cast<const v4u_any*>(expert_out + (int64_t)p[q] * d.H + at));
+    }
+#pragma unroll
+    for (int q = 0; q < kRowsInFlight; ++q)
+      if (j + q < d.k) fma_row(acc, w[q], make_uint4(x[q].x, x[q].y, x[q].z, x[q].w));
+  }
+  if (!on) return;
+  v4u y;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = to_bf16(acc[2 * i]) | (to_bf16(acc[2 * i + 1]) << 16);
+  *reinterpret_cast<v4u_any*>(out + t * d.H + at) = y;
+}
+
+__global__ __launch_bounds__(kCombThreads) void combine_grad_narrow_kernel(
+    Dims d, int P, const float* __restrict__ weight, const int32_t* __restrict__ slot_pos,
+    const uint16_t* __restrict__ expert_out, const uint16_t* __restrict__ grad_out,
+    uint16_t* __restrict__ grad_rows, float* __restrict__ grad_weight, int32_t* __restrict__ status) {
+  constexpr int kRows = 4;
+  const int lane = threadIdx.x & (P - 1);
+  const int64_t t = (int64_t)blockIdx.x * (kCombThreads / P) + threadIdx.x / P;
+  if (t >= d.T) return;  // whole tokens: the sums below stay within one
+  const bool on = 8 * lane < d.H;
+  const int at = vector_at(lane, d.H);
+  const int again = 8 * lane - (d.H - 8);  // values that the vector before has counted
+  v4u g = {0, 0, 0, 0};
+  if (on) g = *reinterpret_cast<const v4u_any*>(grad_out + t * d.H + at);
+  for (int j = 0; j < d.k; j += kRows) {
+    int p[kRows];
+    float w[kRows];
+    v4u x[kRows];
+#pragma unroll
+    for (int q = 0; q < kRows; ++q) p[q] = narrow_slot(d, t, j + q, weight, slot_pos, &w[q], status);
+#pragma unroll
+    for (int q = 0; q < kRows; ++q) {
+      x[q] = v4u{0, 0, 0, 0};
+      if (on && p[q] >= 0)
+        x[q] = __builtin_nontemporal_load(reinterpret_cast<const v4u_any*>(expert_out + (int64_t)p[q] * d.H + at));
+    }
+#pragma unroll
+    for (int q = 0; q < kRows; ++q) {
+      if (on && p[q] >= 0)
+        __builtin_nontemporal_store(scaled_row(w[q], g),
+                                    reinterpret_cast<v4u_any*>(grad_rows + (int64_t)p[q] * d.H + at));
+      float dot = 0.0f;
+      if (on && p[q] >= 0) dot_row(&dot, without(g, again), without(x[q], again));
+      for (int off = P / 2; off >= 1; off >>= 1) dot += __shfl_xor(dot, off);
+      if (lane == 0 && j + q < d.k) grad_weight[t * d.k + j + q] = dot;
+    }
+  }
+}
+
 // H < 8: one bf16 element per thread.
 __global__ __launch_bounds__(kCombThreads) void combine_grad_u16_kernel(
     Dims d, const float* __restrict__ weight, const int32_t* __restrict__ slot_pos,
@@ -322,6 +421,12 @@ template <bool GIVEN>
 hipError_t launch_sum(const Dims& d, const float* topk_val, const int32_t* slot_pos, const uint16_t* expert_out,
                       uint16_t* out, int32_t* status, hipStream_t st) {
   if (d.T == 0) return hipSuccess;
+  if (GIVEN && narrow_rows(d)) {
+    const int P = narrow_lanes(d.H), tokens = kCombThreads / P;
+    hipLaunchKernelGGL(combine_narrow_kernel, dim3((unsigned)((d.T + tokens - 1) / tokens)), dim3(kCombThreads), 0, st,
+                       d, P, topk_val, slot_pos, expert_out, out, status);
+    return hipGetLastError();
+  }
   if (d.H >= 8) {
     // One vector a thread and round, or four.  Four read a row in one go, which
     // pays where the rows are spread over more than some 2 GB and four fill the
@@ -377,6 +482,12 @@ hipError_t launch_combine_grad(const Dims& d, const float* weight, const int32_t
                                const uint16_t* expert_out, const uint16_t* grad_out, uint16_t* grad_expert_out,
                                float* grad_weight, int32_t* status, hipStream_t st) {
   if (d.T == 0) return hipSuccess;
+  if (narrow_rows(d)) {
+    const int P = narrow_lanes(d.H), tokens = kCombThreads / P;
+    hipLaunchKernelGGL(combine_grad_narrow_kernel, dim3((unsigned)((d.T + tokens - 1) / tokens)), dim3(kCombThreads), 0,
+                       st, d, P, weight, slot_pos, expert_out, grad_out, grad_expert_out, grad_weight, status);
+    return hipGetLastError();
+  }
   // Four rows to a workgroup (one, two and eight measured within 3 % of it), or
   // one where tokens are few; a row in one round of the threads or four vectors each.
   const bool narrow = (d.H + 7) / 8 <= kCombThreads;

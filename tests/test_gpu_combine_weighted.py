@@ -40,7 +40,10 @@ def layer_of(mp, T, k, H):
                                    (513, 9, 1001), (520, 7, 4104),
                                    # rows of less than a vector, of one, and whose last overlaps the one before
                                    (5, 3, 7), (4, 2, 8), (6, 4, 9), (3, 8, 15), (40, 8, 2049), (600, 3, 7167), (30, 4, 2047),
-                                   (700, 2, 5), (515, 2, 10)])
+                                   (700, 2, 5), (515, 2, 10),
+                                   # several tokens to a workgroup
+                                   (2000, 8, 512), (777, 4, 37), (512, 5, 8), (1500, 3, 505), (640, 32, 148), (2049, 1, 16),
+                                   (900, 9, 513)])
 def test_weighted_sum_and_gradients(mp, T, k, H):
     print("combine weighted T=%d k=%d H=%d" % (T, k, H), flush=True)
     rows, g, w, pos = data(T + k + H, T, k, H)
@@ -182,6 +185,30 @@ def test_positions_outside_and_refusals(mp, H):
         a = [layer.handle, None, p(P), p(R), p(G), None]
         a[at] = None
         assert mp.lib().moex_combine(*a) == mp.MOE_ERR_INVALID_ARG
+    layer.close()
+
+
+@pytest.mark.parametrize("H", [24, 509])
+def test_positions_outside_among_many_tokens(mp, H):
+    T, k = 700, 5
+    rows, g, w, pos = data(4, T, k, H)
+    layer = layer_of(mp, T, k, H)
+    d = lambda t: t.to(layer.device)
+    p = pos.clone()
+    for slot, bad in ((3 * k + 1, -1), (699 * k + 4, T * k), (300 * k, 2 ** 31 - 1)):
+        p[slot] = bad
+    off = ~((p >= 0) & (p < T * k)).view(T, k)
+    wz = w.masked_fill(off, 0.0)
+    out = layer.combine_weighted(d(rows), d(w), slot_pos=d(p))
+    assert layer.status() == mp.MOE_STATUS_PLAN_CHECK
+    want = layer.combine_weighted(d(rows), d(wz), slot_pos=d(pos))
+    assert torch.equal(out, want) and layer.status() == 0
+    gr, gw = layer.combine_grad(d(rows), d(g), d(w), slot_pos=d(p))
+    assert layer.status() == mp.MOE_STATUS_PLAN_CHECK
+    gr0, gw0 = layer.combine_grad(d(rows), d(g), d(w), slot_pos=d(pos))
+    assert (gw.cpu()[off] == 0).all() and torch.equal(gw.cpu()[~off], gw0.cpu()[~off])
+    ok = p.view(T, k)[~off].long()
+    assert torch.equal(gr.cpu()[ok], gr0.cpu()[ok])
     layer.close()
 
 
