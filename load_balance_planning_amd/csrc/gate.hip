@@ -245,6 +245,11 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
     if (g.n_group > 1) {
       double* gv64 = reinterpret_cast<double*>(smem_gate + lay.group) + (size_t)i * g.n_group;
       float* gv = reinterpret_cast<float*>(gv64);
+      // where a group's experts are not whole lanes', or are evaluated again, this
+      // many lanes take a group: all of them, as far as there are groups
+      int L = 1;
+      while (2 * L * g.n_group <= P) L *= 2;
+      const int part = lane & (L - 1);
       if (groups_of_lanes<V>(per)) {
         // the two largest of this lane's choices, then of the group's lanes
         const int lanes = per / V;
@@ -259,15 +264,15 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
         for (int v = 0; v < V; ++v)
           if (e0 + v < d.E) ch[e0 + v] = o32[v];
         wave_lds_sync();
-        for (int q = lane; q < g.n_group; q += P) {
+        for (int q0 = 0; q0 < g.n_group; q0 += P / L) {
+          const int q = q0 + lane / L;
           float a = -INFINITY, b = -INFINITY;
-          int at = q % per;  // lanes start at different places of their groups: other LDS banks
+          if (q < g.n_group) {
 #pragma unroll 4
-          for (int j = 0; j < per; ++j) {
-            push_top2(&a, &b, ch[q * per + at]);
-            at = at + 1 == per ? 0 : at + 1;
+            for (int j = part; j < per; j += L) push_top2(&a, &b, ch[q * per + j]);
           }
-          gv[q] = g.group_top == 2 ? a + b : a;
+          for (int off = 1; off < L; off <<= 1) merge_top2(&a, &b, __shfl_xor(a, off), __shfl_xor(b, off));
+          if (part == 0 && q < g.n_group) gv[q] = g.group_top == 2 ? a + b : a;
         }
       }
       wave_lds_sync();
@@ -293,10 +298,6 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
       if ((__ballot(unsure) & grp_bits) != 0ull) {
         need64();
         wave_lds_sync();
-        // as many lanes to a group as it has experts, where it has that many
-        int L = 1;
-        while (L < P && L < per) L *= 2;
-        const int part = lane & (L - 1);
         for (int q0 = 0; q0 < g.n_group; q0 += P / L) {
           const int q = q0 + lane / L;
           double a = -INFINITY, b = -INFINITY;
