@@ -247,8 +247,7 @@ __global__ __launch_bounds__(kCombThreads) void combine_grad_vec_kernel(
 #pragma unroll
       for (int u = 0; u < VPT; ++u) {
         const int c = base + threadIdx.x + u * kCombThreads;
-        g[u] = v4u{0, 0, 0, 0};
-        if (c < vpr) g[u] = *reinterpret_cast<const v4u_any*>(g_row + vector_at(c, d.H));
+        g[u] = c < vpr ? *reinterpret_cast<const v4u_any*>(g_row + vector_at(c, d.H)) : v4u{0, 0, 0, 0};
       }
 #pragma unroll
       for (int q = 0; q < ROWS; ++q) {
@@ -261,8 +260,8 @@ __global__ __launch_bounds__(kCombThreads) void combine_grad_vec_kernel(
 #pragma unroll
         for (int u = 0; u < VPT; ++u) {
           const int c = base + threadIdx.x + u * kCombThreads;
-          x[u] = v4u{0, 0, 0, 0};
-          if (c < vpr) x[u] = __builtin_nontemporal_load(reinterpret_cast<const v4u_any*>(x_row + vector_at(c, d.H)));
+          const v4u_any* at = reinterpret_cast<const v4u_any*>(x_row + vector_at(c, d.H));
+          x[u] = c < vpr ? __builtin_nontemporal_load(at) : v4u{0, 0, 0, 0};
         }
 #pragma unroll
         for (int u = 0; u < VPT; ++u) {
@@ -491,8 +490,9 @@ hipError_t launch_combine_grad(const Dims& d, const float* weight, const int32_t
   // Four rows to a workgroup (one, two and eight measured within 3 % of it), or
   // one where tokens are few; a row in one round of the threads or four vectors each.
   const bool narrow = (d.H + 7) / 8 <= kCombThreads;
-  auto launch = d.T < kFewTokens ? (narrow ? launch_combine_grad_rows<1, 1> : launch_combine_grad_rows<4, 1>)
-                                 : (narrow ? launch_combine_grad_rows<1, 4> : launch_combine_grad_rows<4, 4>);
+  const bool few = d.T < kFewTokens;
+  auto launch = few ? (narrow ? launch_combine_grad_rows<1, 1> : launch_combine_grad_rows<4, 1>)
+                    : (narrow ? launch_combine_grad_rows<1, 4> : launch_combine_grad_rows<4, 4>);
   if (d.H < 8)
     hipLaunchKernelGGL(combine_grad_u16_kernel, dim3(d.T), dim3(kCombThreads), 0, st, d, weight, slot_pos, expert_out,
                        grad_out, grad_expert_out, grad_weight, status);

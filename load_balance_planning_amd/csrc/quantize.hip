@@ -59,6 +59,11 @@ __device__ __forceinline__ void widen8(const u32x4& w, float* f) {
     f[2 * j + 1] = bf16_high(w[j]);
   }
 }
+__device__ __forceinline__ void load16(const uint16_t* __restrict__ x, int64_t at, float* f) {
+  const u32x4 lo = load8(x, at), hi = load8(x, at + 8);
+  widen8(lo, f);
+  widen8(hi, f + 8);
+}
 // The 16 values from element `at` on, `left` of them of the row (what follows is
 // the next row's): zeros behind those.
 __device__ __forceinline__ void load16(const uint16_t* __restrict__ x, int64_t at, int left, int64_t total, float* f) {
@@ -113,11 +118,20 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const uint16_t*
     const int c = b * kBlk + lane8 * kPerLane;
     float f[kPerLane];
     if (KIND == kPlain) {
-      load16(x, r * cols + c, cols - c, rows * cols, f);
+      if (c + kPerLane <= cols)
+        load16(x, r * cols + c, f);
+      else
+        load16(x, r * cols + c, cols - c, rows * cols, f);
     } else if (KIND == kSwiglu) {
       float u[kPerLane];
-      load16(x, r * 2 * cols + c, cols - c, rows * 2 * cols, f);
-      load16(x, r * 2 * cols + cols + c, cols - c, rows * 2 * cols, u);
+      const int64_t at = r * 2 * cols + c;
+      if (c + kPerLane <= cols) {
+        load16(x, at, f);
+        load16(x, at + cols, u);
+      } else {
+        load16(x, at, cols - c, rows * 2 * cols, f);
+        load16(x, at + cols, cols - c, rows * 2 * cols, u);
+      }
 #pragma unroll
       for (int j = 0; j < kPerLane; ++j) f[j] = c + j < cols ? swiglu(f[j], u[j]) : 0.0f;
     } else {
