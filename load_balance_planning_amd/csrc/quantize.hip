@@ -102,7 +102,8 @@ __device__ __forceinline__ float swiglu(float g, float u) { return g * sigmoid(g
 // kSwigluGrad: x [rows][cols] (gate, up) and grad [rows][cols / 2], cols = 2 f.
 // A block of 128 output columns per eight lanes.  Rows of any width are read 16
 // bytes at a time (element by element, widths that are no multiple of 8 took four
-// times as long: 27672 rows of f = 2690, 324 us and 86 so; its gradient, 20000 rows, 495 and 147).
+// times as long: 27672 rows of f = 2690, 324 us and 84 so; its gradient, 20000
+// rows, 495 and 149).
 template <int KIND>
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const uint16_t* __restrict__ x,
                                                                  const uint16_t* __restrict__ grad, int64_t rows,
