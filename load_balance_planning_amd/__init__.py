@@ -459,6 +459,7 @@ class Layer:
         self._index = self.device.index
         self._dims = (cfg.T, cfg.E, cfg.k, cfg.H)  # plain integers: a structure's fields cost more to read
         self._cap = cfg.E + cfg.replica_budget
+        self._bf16 = torch.bfloat16
         # handle of torch's current stream on a device, without the Python object around it
         self._current_stream = torch._C._cuda_getCurrentRawStream
         self.sizes = moe_plan_query(cfg)
@@ -565,11 +566,13 @@ class Layer:
         """Gradient of gate()'s weights for the logits (moex_gate_grad); topk_idx defaults to this layer's."""
         torch, (T, E, k, _) = self.torch, self._dims
         topk_idx = self.route_out.topk_idx if topk_idx is None else topk_idx
-        out = self._empty((T, E), torch.float32, stream) if out is None else out
         self._check_tensor(logits, (T, E), torch.float32)
         self._check_tensor(topk_idx, (T, k), torch.int32)
         self._check_tensor(grad_weight, (T, k), torch.float32)
-        self._check_tensor(out, (T, E), torch.float32)
+        if out is None:
+            out = self._empty((T, E), torch.float32, stream)
+        else:
+            self._check_tensor(out, (T, E), torch.float32)
         moex_gate_grad(self.handle, gate, _addr(logits), _addr(topk_idx), _addr(grad_weight), _addr(out),
                        self._stream(stream))
         return out
@@ -590,7 +593,7 @@ class Layer:
     def _check_16bit(self, t, shape, name):
         """bf16, or its bit patterns in a 16-bit integer type."""
         self._check_tensor(t, shape, None)
-        if t.element_size() != 2 or t.dtype == self.torch.float16:
+        if t.dtype is not self._bf16 and (t.element_size() != 2 or t.dtype is self.torch.float16):
             raise TypeError("%s must be a bf16 tensor, not %s" % (name, t.dtype))
 
     def _check_blocks(self, b: Blocks, lead, scale_lead=None):
@@ -669,8 +672,10 @@ class Layer:
             raise ValueError("x has %d columns, the matrices %d" % (x.cols, k))
         self._check_blocks(x, (rows,))
         self._check_blocks(w, (E, n), (E, -(-n // BLOCK)))
-        out = self._empty((rows, n), torch.bfloat16, stream) if out is None else out
-        self._check_16bit(out, (rows, n), "out")
+        if out is None:
+            out = self._empty((rows, n), torch.bfloat16, stream)
+        else:
+            self._check_16bit(out, (rows, n), "out")
         moex_matmul(self.handle, plan_s, _addr(inst_offset), _addr(x.q), _addr(x.scale), _addr(w.q), _addr(w.scale), n, k,
                     _addr(out), self._stream(stream))
         return out
@@ -683,8 +688,10 @@ class Layer:
         plan_s, inst_offset = self._product_plan(plan, inst_offset)
         self._check_blocks(dy, (rows,))
         self._check_blocks(x, (rows,))
-        out = self._empty((E, dy.cols, x.cols), torch.bfloat16, stream) if out is None else out
-        self._check_16bit(out, (E, dy.cols, x.cols), "out")
+        if out is None:
+            out = self._empty((E, dy.cols, x.cols), torch.bfloat16, stream)
+        else:
+            self._check_16bit(out, (E, dy.cols, x.cols), "out")
         moex_wgrad(self.handle, plan_s, _addr(inst_offset), _addr(dy.q), _addr(dy.scale), _addr(x.q), _addr(x.scale),
                    dy.cols, x.cols, _addr(out), self._stream(stream))
         return out
@@ -702,8 +709,10 @@ class Layer:
         self._check_16bit(expert_out, (T * k, H), "expert_out")
         if weight is not None:
             self._check_tensor(weight, (T, k), torch.float32)
-        out = self._empty((T, H), expert_out.dtype, stream) if out is None else out
-        self._check_16bit(out, (T, H), "out")
+        if out is None:
+            out = self._empty((T, H), expert_out.dtype, stream)
+        else:
+            self._check_16bit(out, (T, H), "out")
         moex_combine(self.handle, _addr(weight), _addr(slot_pos), _addr(expert_out), _addr(out), self._stream(stream))
         return out
 
