@@ -57,9 +57,11 @@ extern "C" int moex_gate(moe_plan_t h, const moex_gate_config* gate, const float
   if (!on_device.ok()) return MOE_ERR_HIP;
   hipStream_t st = begin_call(h, stream);
   const int32_t* prev = (prev_topk && out->trans) ? prev_topk : nullptr;
+  bool counted = false;
   hipError_t e = moe::launch_gate(d, *gate, logits, bias, prev, out->topk_idx, out->topk_val, weight,
-                                  h->ws.tile_mask, h->ws.prev_mask, h->ws.status, st);
-  if (e == hipSuccess)
+                                  h->ws.tile_mask, h->ws.prev_mask, out->cooc || prev, out->omega, out->expert_count,
+                                  &counted, h->ws.status, st);
+  if (e == hipSuccess && !counted)
     e = moe::launch_scan_pairs(d, h->ws.tile_mask, nullptr, out->omega, out->expert_count, h->ws.prev_mask,
                                out->cooc, prev ? out->trans : nullptr, h->ws.pair_part, st);
   return hip_rc(e);

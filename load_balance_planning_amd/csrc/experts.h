@@ -13,9 +13,12 @@ constexpr int kMaxGateGroups = 64;
 inline __host__ __device__ int64_t padded_cols(int64_t c) { return (c + kBlk - 1) / kBlk * kBlk; }
 inline __host__ __device__ int64_t scale_cols(int64_t c) { return (padded_cols(c) / kBlk + 3) / 4 * 4; }
 
+// The router; *counted: its few tokens were one workgroup's, which wrote omega and
+// count itself (only with masks_wanted false: the masks are then not written).
 hipError_t launch_gate(const Dims& d, const moex_gate_config& g, const float* logits, const float* bias,
                        const int32_t* prev_topk, int32_t* topk_idx, float* topk_val, float* weight,
-                       uint64_t* tile_mask, uint64_t* prev_mask, int32_t* status, hipStream_t st);
+                       uint64_t* tile_mask, uint64_t* prev_mask, bool masks_wanted, int32_t* omega, int32_t* count,
+                       bool* counted, int32_t* status, hipStream_t st);
 hipError_t launch_gate_grad(const Dims& d, const moex_gate_config& g, const float* logits, const int32_t* topk_idx,
                             const float* grad_weight, float* grad_logits, int32_t* status, hipStream_t st);
 

@@ -113,6 +113,32 @@ def test_many_tokens(mp, shape, kind, biased):
     check(mp, x, b if biased else None, k, R, kind, shape[4:], True, 2.5)
 
 
+@pytest.mark.parametrize("T,E,k,R", [(1, 8, 2, 1), (1, 256, 8, 1), (8, 256, 8, 1), (8, 256, 8, 4), (9, 256, 8, 1), (16, 64, 8, 4),
+                                     (17, 64, 8, 1), (32, 16, 2, 8), (33, 16, 2, 3), (8, 2048, 8, 8), (4, 896, 16, 2), (6, 30, 3, 6)])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_few_tokens_without_masks(mp, T, E, k, R, kind):
+    """Without co-selection or transition counts, one workgroup's tokens take one launch: the same outputs as with
+    them, into buffers that held other values, and the planner goes on from them."""
+    E = E if E % R == 0 else E + R - E % R
+    print("gate few tokens T=%d E=%d k=%d R=%d" % (T, E, k, R), flush=True)
+    x, b = logits(T * E, T, E)
+    check(mp, x, b, k, R, kind)
+    layer, gate, full, w = run(mp, x, b, k, R, kind)
+    lean = mp.Layer(mp.make_config(T, E, k, R, 1, 8, 0), cooc=False)
+    for t in (lean.route_out.topk_idx, lean.route_out.expert_count, lean.route_out.omega):
+        t.fill_(-7)
+    for _ in range(2):
+        r, w2 = lean.gate(x.to(lean.device), gate, bias=b.to(lean.device))
+        assert torch.equal(r.topk_idx, full.topk_idx) and torch.equal(w2, w) and torch.equal(r.topk_val, full.topk_val)
+        assert torch.equal(r.omega, full.omega) and torch.equal(r.expert_count, full.expert_count)
+    p, q = layer.plan(), lean.plan()
+    torch.cuda.synchronize()
+    assert torch.equal(p.inst_expert, q.inst_expert) and torch.equal(p.slot_inst, q.slot_inst)
+    assert layer.status() == 0 and lean.status() == 0
+    layer.close()
+    lean.close()
+
+
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 def test_ties_of_many_tokens(mp, kind):
     T, E, k = 4110, 256, 8
