@@ -32,10 +32,11 @@ namespace {
 
 constexpr float kTiny = 1e-20f;  // added to the sum of the selected scores
 
-// Tokens per workgroup: route.hip's rule (slices of at least 8 bits of a mask).
-template <int P>
+// Tokens per workgroup: route.hip's rule (slices of at least 8 bits of a mask), or,
+// where one workgroup takes ALL tokens, up to 32 and 1024 threads.
+template <int P, bool ALL>
 constexpr int gate_tpw() {
-  return 256 / P < 8 ? 8 : 256 / P;
+  return ALL ? (1024 / P < 32 ? 1024 / P : 32) : 256 / P < 8 ? 8 : 256 / P;
 }
 
 template <int P>
@@ -78,9 +79,9 @@ __host__ __device__ inline int choice_stride(int E) { return E + 8; }
 struct GateLds {
   size_t bias, cand, chosen, group, choice, total;
 };
-template <int P, int V>
+template <int P, int V, bool ALL>
 __host__ __device__ inline GateLds gate_lds(int E, int n_group, bool prev, bool biased) {
-  constexpr size_t TPW = gate_tpw<P>();
+  constexpr size_t TPW = gate_tpw<P, ALL>();
   GateLds l;
   l.bias = sizeof(uint64_t) * (size_t)E * (prev ? 2 : 1);
   l.cand = l.bias + (biased ? (size_t)P * V * sizeof(float) : 0);
@@ -106,25 +107,26 @@ __device__ __forceinline__ void merge_top2(float* a, float* b, float oa, float o
   *a = fmaxf(*a, oa);
 }
 
-template <int P, int V>
-__global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
+// ALL: one workgroup, which writes omega and count itself; else the tiles' masks,
+// from which a second launch counts.
+template <int P, int V, bool ALL>
+__global__ __launch_bounds__((gate_tpw<P, ALL>() * P)) void gate_kernel(
     Dims d, moex_gate_config g, bool vec, const float* __restrict__ logits, const float* __restrict__ bias,
     const int32_t* __restrict__ prev_topk, int32_t* __restrict__ topk_idx, float* __restrict__ topk_val,
     float* __restrict__ weight, uint64_t* __restrict__ tile_mask, uint64_t* __restrict__ prev_mask,
     int32_t* __restrict__ omega, int32_t* __restrict__ count, int32_t* __restrict__ status) {
-  constexpr int TPW = gate_tpw<P>();
+  constexpr int TPW = gate_tpw<P, ALL>();
   constexpr int SLICES = 64 / TPW;
   extern __shared__ __align__(16) unsigned char smem_gate[];
   const bool want_prev = prev_topk != nullptr;
-  const GateLds lay = gate_lds<P, V>(d.E, g.n_group, want_prev, bias != nullptr);
+  const GateLds lay = gate_lds<P, V, ALL>(d.E, g.n_group, want_prev, bias != nullptr);
   unsigned long long* smask = reinterpret_cast<unsigned long long*>(smem_gate);
   unsigned long long* pmask = smask + d.E;
   float* bias_s = reinterpret_cast<float*>(smem_gate + lay.bias);
   const int x_tile = blockIdx.x / SLICES, h = blockIdx.x - x_tile * SLICES;
   const int s = x_tile / d.C, c = x_tile - s * d.C;
-  const bool alone = omega != nullptr;  // this workgroup has all tokens, and writes the histograms
-  const int64_t t0 = alone ? 0 : (int64_t)s * d.Tr + (int64_t)c * kTile + h * TPW;
-  const int nt = alone ? d.T : max(0, min(TPW, d.Tr - c * kTile - h * TPW));
+  const int64_t t0 = ALL ? 0 : (int64_t)s * d.Tr + (int64_t)c * kTile + h * TPW;
+  const int nt = ALL ? d.T : max(0, min(TPW, d.Tr - c * kTile - h * TPW));
   const int tid = threadIdx.x, nthr = blockDim.x;
   bool bad = false;
   for (int e = tid; e < d.E; e += nthr) {
@@ -517,7 +519,7 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
   }
   if (bad) atomicOr(status, MOE_STATUS_NAN_LOGIT);
   __syncthreads();
-  if (alone) {
+  if (ALL) {
     for (int e = tid; e < d.E; e += nthr) {
       const unsigned long long mk = smask[e];
       count[e] = __popcll(mk);
@@ -537,25 +539,23 @@ __global__ __launch_bounds__((gate_tpw<P>() * P)) void gate_kernel(
   }
 }
 
-template <int P, int V>
+template <int P, int V, bool ALL>
 hipError_t launch_gate_pv(const Dims& d, const moex_gate_config& g, bool vec, const float* logits, const float* bias,
                           const int32_t* prev_topk, int32_t* topk_idx, float* topk_val, float* weight,
-                          uint64_t* tile_mask, uint64_t* prev_mask, bool masks_wanted, int32_t* omega, int32_t* count,
-                          bool* counted, int32_t* status, hipStream_t st) {
-  // All tokens in one workgroup: the second launch, which counts from the masks of
-  // many, is not needed (256 experts, 4 tokens: 8.7 us with it, 6.0 without; called from
-  // Python, 10.5 and 7.0).
-  *counted = !masks_wanted && d.T <= gate_tpw<P>();
-  constexpr int slices = 64 / gate_tpw<P>();
-  const size_t lds = gate_lds<P, V>(d.E, g.n_group, prev_topk != nullptr, bias != nullptr).total;
+                          uint64_t* tile_mask, uint64_t* prev_mask, int32_t* omega, int32_t* count, int32_t* status,
+                          hipStream_t st) {
+  constexpr int TPW = gate_tpw<P, ALL>();
+  const size_t lds = gate_lds<P, V, ALL>(d.E, g.n_group, prev_topk != nullptr, bias != nullptr).total;
   if (lds > 65536) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(gate_kernel<P, V>),
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(gate_kernel<P, V, ALL>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((gate_kernel<P, V>), dim3((unsigned)(*counted ? 1 : d.NT * slices)), dim3(gate_tpw<P>() * P), lds,
-                     st, d, g, vec, logits, bias, prev_topk, topk_idx, topk_val, weight, tile_mask, prev_mask,
-                     *counted ? omega : nullptr, count, status);
+  // all tokens: as many threads as they need, and at least a full workgroup's for the experts' loops
+  const int threads = ALL ? (d.T * P > 256 ? (d.T * P + 63) / 64 * 64 : 256) : TPW * P;
+  hipLaunchKernelGGL((gate_kernel<P, V, ALL>), dim3((unsigned)(ALL ? 1 : d.NT * (64 / TPW))), dim3(threads), lds, st, d,
+                     g, vec, logits, bias, prev_topk, topk_idx, topk_val, weight, tile_mask, prev_mask, omega, count,
+                     status);
   return hipGetLastError();
 }
 
@@ -712,10 +712,17 @@ hipError_t launch_gate(const Dims& d, const moex_gate_config& g, const float* lo
   while (P < 64 && (P < 2 * d.k || P * (d.T > 4096 ? 16 : P < 32 ? 4 : 8) < d.E)) P *= 2;
   int V = 1;
   while (P * V < d.E) V *= 2;
-#define MOE_GATE_CASE(P_, V_)                                                                                        \
-  if (P == (P_) && V == (V_))                                                                                        \
-    return launch_gate_pv<P_, V_>(d, g, vec, logits, bias, prev_topk, topk_idx, topk_val, weight, tile_mask,         \
-                                  prev_mask, masks_wanted, omega, count, counted, status, st);
+  // Few tokens and no need of masks: one workgroup, and no second launch (256
+  // experts, 4 of 8 groups: 4 tokens 8.7 us -> 5.9, 16 tokens 8.7 -> 6.5, 32 tokens
+  // 8.9 -> 8.2, and called from Python 9.1 -> 6.5, 9.4 -> 6.4, 9.5 -> 7.9; 64 tokens
+  // would take 10.7 in one).
+  *counted = !masks_wanted && d.T <= 32 && d.T * P <= 1024;
+#define MOE_GATE_CASE(P_, V_)                                                                                         \
+  if (P == (P_) && V == (V_))                                                                                         \
+    return *counted ? launch_gate_pv<P_, V_, true>(d, g, vec, logits, bias, prev_topk, topk_idx, topk_val, weight,    \
+                                                   tile_mask, prev_mask, omega, count, status, st)                    \
+                    : launch_gate_pv<P_, V_, false>(d, g, vec, logits, bias, prev_topk, topk_idx, topk_val, weight,   \
+                                                    tile_mask, prev_mask, omega, count, status, st);
 #define MOE_GATE_P(P_) \
   MOE_GATE_CASE(P_, 1) MOE_GATE_CASE(P_, 2) MOE_GATE_CASE(P_, 4) MOE_GATE_CASE(P_, 8) MOE_GATE_CASE(P_, 16)
   MOE_GATE_P(8)

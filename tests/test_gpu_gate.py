@@ -114,7 +114,8 @@ def test_many_tokens(mp, shape, kind, biased):
 
 
 @pytest.mark.parametrize("T,E,k,R", [(1, 8, 2, 1), (1, 256, 8, 1), (8, 256, 8, 1), (8, 256, 8, 4), (9, 256, 8, 1), (16, 64, 8, 4),
-                                     (17, 64, 8, 1), (32, 16, 2, 8), (33, 16, 2, 3), (8, 2048, 8, 8), (4, 896, 16, 2), (6, 30, 3, 6)])
+                                     (17, 64, 8, 1), (32, 16, 2, 8), (33, 16, 2, 3), (8, 2048, 8, 8), (4, 896, 16, 2), (6, 30, 3, 6), (32, 256, 8, 8), (31, 256, 8, 1), (16, 896, 16, 1),
+                                     (17, 896, 16, 1), (16, 2048, 8, 2), (24, 128, 6, 2), (32, 64, 20, 1)])
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 def test_few_tokens_without_masks(mp, T, E, k, R, kind):
     """Without co-selection or transition counts, one workgroup's tokens take one launch: the same outputs as with
