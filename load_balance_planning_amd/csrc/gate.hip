@@ -715,8 +715,9 @@ hipError_t launch_gate(const Dims& d, const moex_gate_config& g, const float* lo
   // Few tokens and no need of masks: one workgroup, and no second launch (256
   // experts, 4 of 8 groups: 4 tokens 8.7 us -> 5.9, 16 tokens 8.7 -> 6.5, 32 tokens
   // 8.9 -> 8.2, and called from Python 9.1 -> 6.5, 9.4 -> 6.4, 9.5 -> 7.9; 64 tokens
-  // would take 10.7 in one).
-  *counted = !masks_wanted && d.T <= 32 && d.T * P <= 1024;
+  // would take 10.7 in one).  Groups of more than 1024 experts may need rows of
+  // choices that, for 16 tokens, outgrow the CU's LDS.
+  *counted = !masks_wanted && d.T <= 32 && d.T * P <= 1024 && (g.n_group == 1 || d.E <= 1024);
 #define MOE_GATE_CASE(P_, V_)                                                                                         \
   if (P == (P_) && V == (V_))                                                                                         \
     return *counted ? launch_gate_pv<P_, V_, true>(d, g, vec, logits, bias, prev_topk, topk_idx, topk_val, weight,    \

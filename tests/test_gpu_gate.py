@@ -140,6 +140,22 @@ def test_few_tokens_without_masks(mp, T, E, k, R, kind):
     lean.close()
 
 
+@pytest.mark.parametrize("T,E,k,R,groups", [(16, 2000, 8, 2, (10, 4, 2)), (14, 1530, 4, 2, (5, 2, 2)), (16, 1020, 8, 1, (60, 9, 2)),
+                                            (32, 250, 8, 2, (10, 4, 2)), (32, 96, 4, 4, (32, 8, 2)), (5, 60, 2, 1, (20, 2, 1))])
+def test_few_tokens_with_groups_without_masks(mp, T, E, k, R, groups):
+    print("gate few tokens groups T=%d E=%d %s" % (T, E, groups), flush=True)
+    x, b = logits(T * E, T, E)
+    layer, gate, full, w = run(mp, x, b, k, R, "sigmoid", groups)
+    idx = refs.select(x.double(), b.double(), "sigmoid", k, *groups)
+    lean = mp.Layer(mp.make_config(T, E, k, R, 1, 8, 0), cooc=False)
+    r, w2 = lean.gate(x.to(lean.device), gate, bias=b.to(lean.device))
+    assert torch.equal(r.topk_idx.cpu().long(), idx) and torch.equal(full.topk_idx.cpu().long(), idx)
+    assert torch.equal(w2, w) and torch.equal(r.omega, full.omega) and torch.equal(r.expert_count, full.expert_count)
+    assert layer.status() == 0 and lean.status() == 0
+    layer.close()
+    lean.close()
+
+
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 def test_ties_of_many_tokens(mp, kind):
     T, E, k = 4110, 256, 8
