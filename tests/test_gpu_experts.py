@@ -419,6 +419,32 @@ def test_offsets_past_32_bits(mp):
     layer.close()
 
 
+@pytest.mark.parametrize("rows,n,k", [(6, 5, 2 ** 20), (12, 5, 2 ** 20), (6, 2 ** 20, 40), (12, 2 ** 20, 40)])
+def test_longest_axes(mp, rows, n, k):
+    """The largest widths, in the kernel for few rows and in tiles."""
+    print("longest axes %d x %d x %d" % (rows, n, k), flush=True)
+    layer = layer_for(mp, rows, 1)
+    dev = layer.device
+    plan, off, _ = instances(mp, layer, [rows], [0])
+    kw = dict(plan=plan, inst_offset=off)
+    x, d = layer.quantize(normal(1, rows, k).to(dev)), layer.quantize(normal(2, rows, n).to(dev))
+    w = layer.quantize_weights(normal(3, 1, n, k, scale=0.1).to(dev))
+    y, dw = layer.matmul(x, w, **kw), layer.wgrad(d, x, **kw)
+    assert layer.status() == 0
+    c = torch.cat([torch.arange(min(n, 200)), torch.arange(max(0, n - 200), n)]).unique()
+    xv = refs.values(x, rows)
+    wv = refs.values(mp.Blocks(w.q[0], w.scale[0], k), n, 128)[c]
+    want, bound = refs.product(xv, wv)
+    assert ((y.cpu().double()[:, c] - want).abs() <= bound).all()
+    want, bound = refs.outer(refs.values(d, rows)[:, c], xv)
+    assert ((dw[0].cpu()[c].double() - want).abs() <= bound).all()
+    layer.close()
+    with pytest.raises(mp.MoePlanError):
+        big = layer_for(mp, rows, 1)
+        big.matmul(big.quantize(torch.zeros(rows, 2 ** 20 + 1, dtype=BF, device=dev)),
+                   big.quantize_weights(torch.zeros(1, 2, 2 ** 20 + 1, dtype=BF, device=dev)))
+
+
 def test_no_tokens(mp):
     layer = mp.Layer(mp.make_config(0, 4, 2, 1, 1, 64, 0), cooc=False)
     dev = layer.device
