@@ -431,14 +431,12 @@ __global__ __launch_bounds__((gate_tpw<P, ALL>() * P)) void gate_kernel(
         }
       }
     } else {
-      // Rounds, each the largest left, ties to the lower expert; with a bias one
-      // more, to see whether the last pick is sure.  Taken experts' bits: V <= 32.
+      // Rounds, each the largest left, ties to the lower expert.  Taken experts' bits: V <= 32.
       uint32_t taken = 0u;
       bool unsure = false;
       float last_c = 0.0f;
       int last_e = -1;
-      const int rounds = bias && k < d.E ? k + 1 : k;
-      for (int j = 0; j < rounds; ++j) {
+      for (int j = 0; j < k; ++j) {
         uint64_t best = 0ull;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -449,13 +447,24 @@ __global__ __launch_bounds__((gate_tpw<P, ALL>() * P)) void gate_kernel(
         const int e = 0x7fffffff - (int)(uint32_t)top;
         if (e >= e0 && e < e0 + V) taken |= 1u << (e - e0);
         const float ce = __uint_as_float(float_from_order_key((uint32_t)(top >> 32)));
-        if (j < k && lane == 0) chosen_e[j] = e;
+        if (lane == 0) chosen_e[j] = e;
         if (bias) {
-          if (last_e >= 0 && fabsf(ce - last_c) <= margin * (1.0f + fminf(fabsf(ce), fabsf(last_c))))
+          if (last_e >= 0 && fabsf(ce - last_c) <= margin * (1.0f + fmaxf(fabsf(ce), fabsf(last_c))))
             unsure |= !same_inputs(e, last_e);
           last_c = ce;
           last_e = e;
         }
+      }
+      if (bias) {
+        // Neighbouring picks are now either of the same inputs or surely in order.
+        // An expert left over may belong before some of them if it is this near to
+        // the last one and has other inputs.
+        const float room = margin * (1.0f + fabsf(last_c));
+        uint32_t close = 0u;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          close |= e0 + v < d.E && last_c - o32[v] <= room ? 1u << v : 0u;  // (-infinity is sure: NaN or infinity here)
+        for (close &= ~taken; close != 0u; close &= close - 1u) unsure |= !same_inputs(e0 + __ffs((int)close) - 1, last_e);
       }
       if ((__ballot(unsure) & grp_bits) != 0ull) {
         need64();

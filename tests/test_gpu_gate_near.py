@@ -1,0 +1,100 @@
+"""moex_gate where fp32 does not tell the order: long ties with a few experts a little above or below, against the
+selection in 64 bits.
+
+Every case runs with co-selection counts (two launches) and without (one workgroup where the tokens are few)."""
+from __future__ import annotations
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from tests import expert_refs as refs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mp():
+    if not torch.cuda.is_available():
+        pytest.skip("no HIP device")
+    import load_balance_planning_amd as m
+    m.lib()
+    return m
+
+
+def check(mp, x, bias, k, kind, groups=(1, 1, 1), cooc=True, R=1):
+    """Indices, counts and weights; the weight's bound is that of tests/test_gpu_gate.py at a range of 200, and what a
+    score below 2^-126 loses: fp32 values are 2^-149 apart there, the exponential and its product with 1 / sum round by
+    half of that each, so a weight scale * s / (sum s + 1e-20) is off by up to scale * 2^-149 / (sum s + 1e-20)."""
+    T, E = x.shape
+    layer = mp.Layer(mp.make_config(T, E, k, R, 1, 8, 0), cooc=cooc)
+    for t in (layer.route_out.topk_idx, layer.route_out.expert_count, layer.route_out.omega):
+        t.fill_(-7)
+    r, w = layer.gate(x.to(layer.device), mp.make_gate(kind, *groups, True, 2.5),
+                      bias=None if bias is None else bias.to(layer.device))
+    torch.cuda.synchronize()
+    assert layer.status() == 0
+    idx = refs.select(x.double(), None if bias is None else bias.double(), kind, k, *groups)
+    got = r.topk_idx.cpu().long()
+    assert torch.equal(got, idx), "%d of %d tokens differ, first %s for %s" % (
+        int((got != idx).any(1).sum()), T, got[(got != idx).any(1)][:1].tolist(), idx[(got != idx).any(1)][:1].tolist())
+    want = refs.gate_weights(x.double(), idx, kind, True, 2.5)
+    total = refs.scores(x.double(), kind).gather(1, idx).sum(-1, keepdim=True) + 1e-20
+    assert ((w.cpu().double() - want).abs() <= (E / 8 + 2 * k + 432) * 2.0 ** -24 * want.abs() + 2.5 * 2.0 ** -149 / total
+            + 1e-37).all()
+    omega = torch.nn.functional.one_hot(idx, E).sum(1).view(R, T // R, E).sum(1).int()
+    assert torch.equal(r.omega.cpu(), omega) and torch.equal(r.expert_count.cpu(), omega.sum(0).int())
+    layer.close()
+
+
+def ties(T, E, seed, kind):
+    """Rows of equal logits in which a few experts, at any index, stand above or below by less than fp32 tells."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.zeros(T, E)
+    for t in range(T):
+        at = torch.randperm(E, generator=g)
+        if t % 5 == 0:
+            x[t, E - 1 - t % (E // 2)] = 1e-9                    # one above
+        elif t % 5 == 1:
+            x[t, at[:3]] = torch.tensor([1e-9, 3e-9, 2e-9])      # several, each its own
+        elif t % 5 == 2:
+            x[t, t % 7] = -1e-9                                  # one below, among the lowest
+        elif t % 5 == 3:
+            x[t, at[: E // 2]] = 1e-9                            # half of them
+    return x
+
+
+SHAPES = [(32, 256, 8), (64, 256, 8), (4100, 256, 8), (16, 896, 16), (40, 896, 16), (16, 2048, 8), (40, 2048, 8), (4098, 128, 4), (20, 60, 2)]
+
+
+@pytest.mark.parametrize("T,E,k", SHAPES)
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("cooc", [True, False])
+def test_long_ties_with_a_few_apart(mp, T, E, k, kind, cooc):
+    print("long ties T=%d E=%d k=%d %s cooc=%s" % (T, E, k, kind, cooc), flush=True)
+    R = 2 if E > 1024 else 1
+    x = ties(T, E, T + E, kind)
+    level = torch.full((E,), 0.25)
+    unit = level.clone()
+    unit[E - E // 5] = 0.25 + 2.0 ** -25    # below a unit of 0.75
+    for groups in ((1, 1, 1), (4, 2, 2), (4, 2, 1)):
+        for bias in (torch.zeros(E), level, unit):
+            check(mp, x, bias, k, kind, groups, cooc, R)
+        check(mp, torch.zeros(T, E), unit, k, kind, groups, cooc, R)
+
+
+@pytest.mark.parametrize("T,E,k", SHAPES)
+@pytest.mark.parametrize("cooc", [True, False])
+def test_small_scores_under_a_shared_bias(mp, T, E, k, cooc):
+    """Most experts masked, score 0; live ones whose scores vanish beside the bias in fp32 come before them."""
+    print("masked ties T=%d E=%d k=%d cooc=%s" % (T, E, k, cooc), flush=True)
+    R = 2 if E > 1024 else 1
+    g = torch.Generator().manual_seed(E)
+    x = torch.full((T, E), -torch.inf)
+    for t in range(T):
+        at = torch.randperm(E, generator=g)[: 1 + t % (k + 2)]
+        x[t, at] = -20.0 - torch.arange(len(at))
+        x[t, at[0]] = 0.0
+    for groups in ((1, 1, 1), (4, 3, 2)):
+        check(mp, x, torch.ones(E), k, "softmax", groups, cooc, R)
+        check(mp, x, torch.ones(E), k, "sigmoid", groups, cooc, R)
