@@ -246,8 +246,18 @@ __global__ __launch_bounds__((gate_tpw<P, ALL>() * P)) void gate_kernel(
     uint64_t kept = ~0ull;  // groups a token may choose from
     const int per = d.E / g.n_group;
     if (g.n_group > 1) {
+      // a group's value in 64 bits; before, in fp32, with what it may be off by
       double* gv64 = reinterpret_cast<double*>(smem_gate + lay.group) + (size_t)i * g.n_group;
-      float* gv = reinterpret_cast<float*>(gv64);
+      float2* gv = reinterpret_cast<float2*>(gv64);
+      // Either term may be off by margin / 2 (1 + |term|), however small their sum
+      // is (biases of opposite sign), and the addition by 2^-24 of the sum, margin
+      // / 16 of it at most.  A term of -infinity makes the value exact; a sum that
+      // leaves fp32 is off without bound.
+      auto group_value = [&](float a, float b) {
+        if (g.group_top != 2) b = 0.0f;
+        const float y = a + b, size = fabsf(a) + fabsf(b);
+        return make_float2(y, fminf(a, b) == -INFINITY ? 0.0f : margin * (1.25f + 0.625f * size));
+      };
       // where a group's experts are not whole lanes', or are evaluated again, this
       // many lanes take a group: all of them, as far as there are groups
       int L = 1;
@@ -260,7 +270,7 @@ __global__ __launch_bounds__((gate_tpw<P, ALL>() * P)) void gate_kernel(
 #pragma unroll
         for (int v = 1; v < V; ++v) push_top2(&a, &b, o32[v]);
         for (int off = 1; off < lanes; off <<= 1) merge_top2(&a, &b, __shfl_xor(a, off), __shfl_xor(b, off));
-        if ((lane & (lanes - 1)) == 0 && e0 < d.E) gv[e0 / per] = g.group_top == 2 ? a + b : a;
+        if ((lane & (lanes - 1)) == 0 && e0 < d.E) gv[e0 / per] = group_value(a, b);
       } else {
         float* ch = reinterpret_cast<float*>(smem_gate + lay.choice) + (size_t)i * choice_stride(d.E);
 #pragma unroll
@@ -275,7 +285,7 @@ __global__ __launch_bounds__((gate_tpw<P, ALL>() * P)) void gate_kernel(
             for (int j = part; j < per; j += L) push_top2(&a, &b, ch[q * per + j]);
           }
           for (int off = 1; off < L; off <<= 1) merge_top2(&a, &b, __shfl_xor(a, off), __shfl_xor(b, off));
-          if (part == 0 && q < g.n_group) gv[q] = g.group_top == 2 ? a + b : a;
+          if (part == 0 && q < g.n_group) gv[q] = group_value(a, b);
         }
       }
       wave_lds_sync();
@@ -285,13 +295,14 @@ __global__ __launch_bounds__((gate_tpw<P, ALL>() * P)) void gate_kernel(
         const int q = q0 + lane;
         bool in = false;
         if (q < g.n_group) {
-          const float y = gv[q], room = 2.0f * margin * (1.0f + fabsf(y));
+          const float2 y = gv[q];
           int ahead = 0, near = 0;
 #pragma unroll 4
           for (int o = 0; o < g.n_group; ++o) {
-            const float z = gv[o];
-            ahead += z > y + room ? 1 : 0;
-            near += z >= y - room ? 1 : 0;  // itself among them
+            const float2 z = gv[o];
+            const float room = y.y + z.y;
+            ahead += z.x - y.x > room ? 1 : 0;
+            near += y.x - z.x > room ? 0 : 1;  // itself, and what a NaN or an infinite room leaves open, among them
           }
           in = near <= g.topk_group;
           unsure |= !in && ahead < g.topk_group;

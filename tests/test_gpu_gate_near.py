@@ -1,5 +1,5 @@
-"""moex_gate where fp32 does not tell the order: long ties with a few experts a little above or below, against the
-selection in 64 bits.
+"""moex_gate where fp32 does not tell the order: long ties with a few experts a little above or below, group values
+whose terms cancel or whose sum leaves fp32, against the selection in 64 bits.
 
 Every case runs with co-selection counts (two launches) and without (one workgroup where the tokens are few)."""
 from __future__ import annotations
@@ -98,3 +98,40 @@ def test_small_scores_under_a_shared_bias(mp, T, E, k, cooc):
     for groups in ((1, 1, 1), (4, 3, 2)):
         check(mp, x, torch.ones(E), k, "softmax", groups, cooc, R)
         check(mp, x, torch.ones(E), k, "sigmoid", groups, cooc, R)
+
+
+@pytest.mark.parametrize("T", [24, 64, 4100])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("per,n_group", [(8, 8), (16, 16), (5, 12), (2, 64)])
+@pytest.mark.parametrize("C", [1e2, 1e3, 1e4, 1e30, 1.9e38])
+def test_group_values_whose_terms_cancel(mp, T, kind, per, n_group, C):
+    """One expert of each group at +C, the others at -C: the sums are of the scores' size, their error of C's."""
+    print("cancelling groups T=%d %s %d x %d C=%g" % (T, kind, n_group, per, C), flush=True)
+    E = per * n_group
+    g = torch.Generator().manual_seed(T + E)
+    x = 1e-4 * torch.randn(T, E, generator=g)
+    bias = torch.full((n_group, per), -C)
+    bias[torch.arange(n_group), torch.randint(0, per, (n_group,), generator=g)] = C
+    for cooc in (True, False):
+        check(mp, x, bias.flatten(), 2, kind, (n_group, 3, 2), cooc)
+
+
+@pytest.mark.parametrize("T", [24, 64, 4100])
+@pytest.mark.parametrize("cooc", [True, False])
+def test_group_values_past_fp32(mp, T, cooc):
+    """Sums of two biases that overflow in fp32, of either sign, beside groups of -infinity and ordinary ones."""
+    print("groups past fp32 T=%d cooc=%s" % (T, cooc), flush=True)
+    E, n_group, k = 64, 8, 4
+    g = torch.Generator().manual_seed(T)
+    x = torch.randn(T, E, generator=g)
+    for n_top in (1, 2, 3, 5, 7):
+        bias = torch.zeros(n_group, E // n_group)
+        bias[1], bias[4] = 3.3e38, 3.0e38      # both sums are infinite in fp32, and 1 is before 4,
+        bias[4, 0] = 3.4e38                    # though 4 has the largest expert
+        bias[2, :1] = 3.4e38                   # one large term
+        bias[0], bias[6] = -3.3e38, -3.0e38    # 6 before 0, both before -infinity
+        bias[5] = -torch.inf
+        bias[7, 1:] = -torch.inf               # its second largest is -infinity
+        for top in (1, 2):
+            check(mp, x, bias.flatten(), k, "sigmoid", (n_group, n_top, top), cooc)
+            check(mp, x, bias.flatten(), k, "softmax", (n_group, n_top, top), cooc)
