@@ -135,3 +135,75 @@ def test_group_values_past_fp32(mp, T, cooc):
         for top in (1, 2):
             check(mp, x, bias.flatten(), k, "sigmoid", (n_group, n_top, top), cooc)
             check(mp, x, bias.flatten(), k, "softmax", (n_group, n_top, top), cooc)
+
+
+# ---- the same borders in one workgroup (no co-selection counts, few tokens) as in two launches ------------------
+
+FEW = [(16, 256, 8, (1, 1, 1)), (32, 256, 8, (8, 4, 2)), (13, 896, 16, (8, 4, 2)), (16, 100, 5, (10, 3, 1)), (32, 64, 4, (1, 1, 1))]
+
+
+@pytest.mark.parametrize("T,E,k,groups", FEW)
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_ties_of_few_tokens(mp, T, E, k, groups, kind):
+    g = torch.Generator().manual_seed(E)
+    coarse = (torch.randn(T, E, generator=g) * 4).round() / 4
+    near = torch.full((T, E), 1.5) + torch.randint(0, 50, (T, E), generator=g) * 2.0 ** -23
+    bias = torch.randint(0, 3, (E,), generator=g) * 2.0 ** -24
+    for x, b in ((coarse, None), (coarse, torch.zeros(E)), (torch.zeros(T, E), torch.zeros(E)), (near, None), (near, bias),
+                 (near + torch.randn(T, E, generator=g), 1e-7 * torch.randn(E, generator=g))):
+        check(mp, x, b, k, kind, groups, cooc=False)
+
+
+@pytest.mark.parametrize("T,E,k,groups", FEW)
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+def test_masked_and_extreme_logits_of_few_tokens(mp, T, E, k, groups, kind, biased):
+    g = torch.Generator().manual_seed(E + 1)
+    x, b = torch.randn(T, E, generator=g), 0.1 * torch.randn(E, generator=g)
+    low = torch.finfo(torch.float32).min
+    x[0], x[1, 5:], x[2, 3:], x[3], x[4, ::2] = -torch.inf, -torch.inf, -torch.inf, low, low
+    x[5] = torch.linspace(-100, 100, E)
+    x[6] = torch.linspace(1e-30, 64e-30, E)
+    x[7, : E // 2], x[7, E // 2:] = -0.0, 0.0
+    if kind == "sigmoid":
+        x[8, :3] = torch.inf
+    check(mp, x, b if biased else None, k, kind, groups, cooc=False)
+    if biased:
+        b[: E // 2] = -torch.inf
+        check(mp, x, b, k, kind, groups, cooc=False)
+
+
+@pytest.mark.parametrize("T,E,k,groups", FEW)
+def test_wrong_inputs_of_few_tokens(mp, T, E, k, groups):
+    """The status tells, the indices stay distinct experts, and other tokens are as without the wrong one."""
+    g = torch.Generator().manual_seed(E + 2)
+    x, b = torch.randn(T, E, generator=g), 0.1 * torch.randn(E, generator=g)
+    nan_x, inf_x, nan_b = x.clone(), x.clone(), b.clone()
+    nan_x[3, 7], inf_x[3, 1], nan_b[9] = torch.nan, torch.inf, torch.nan
+    for xs, bias, kind, want in ((nan_x, None, "softmax", 1), (nan_x, b, "sigmoid", 1), (inf_x, b, "softmax", 1),
+                                 (inf_x, b, "sigmoid", 0), (x, nan_b, "sigmoid", 1), (x, torch.full((E,), torch.inf), "softmax", 1)):
+        layer = mp.Layer(mp.make_config(T, E, k, 1, 1, 8, 0), cooc=False)
+        r, _ = layer.gate(xs.to(layer.device), mp.make_gate(kind, *groups), bias=None if bias is None else bias.to(layer.device))
+        assert layer.status() == (mp.MOE_STATUS_NAN_LOGIT if want else 0)
+        idx = r.topk_idx.cpu().long()
+        assert all(len(set(row.tolist())) == k and 0 <= min(row) and max(row) < E for row in idx)
+        if bias is None or bias is b:
+            good = [t for t in range(T) if t != 3]
+            ref = refs.select(x.double(), None if bias is None else b.double(), kind, k, *groups)
+            assert torch.equal(idx[good], ref[good])
+        layer.close()
+
+
+@pytest.mark.parametrize("T,E,k,groups", FEW)
+def test_unaligned_logits_of_few_tokens(mp, T, E, k, groups):
+    g = torch.Generator().manual_seed(E + 3)
+    x, b = torch.randn(T, E, generator=g), 0.1 * torch.randn(E, generator=g)
+    layer = mp.Layer(mp.make_config(T, E, k, 1, 1, 8, 0), cooc=False)
+    gate, bd = mp.make_gate("sigmoid", *groups, True, 2.5), b.to(layer.device)
+    view = torch.empty(T * E + 1, device=layer.device)[1:].view(T, E).copy_(x)
+    r, w = layer.gate(view, gate, bias=bd)
+    idx = r.topk_idx.clone()
+    r, w2 = layer.gate(x.to(layer.device), gate, bias=bd)
+    assert torch.equal(r.topk_idx, idx) and torch.equal(w, w2) and layer.status() == 0
+    assert torch.equal(idx.cpu().long(), refs.select(x.double(), b.double(), "sigmoid", k, *groups))
+    layer.close()
