@@ -176,7 +176,7 @@ int moex_matmul(moe_plan_t h, const moe_plan_out* plan, const int32_t* inst_offs
  * dy: blocks of rows [T*k][n]; x: blocks of rows [T*k][k] (what the product
  * took); dw: uint16 [E][n][k] bf16, fully overwritten (zeros for an expert
  * without rows).  Each value is taken as bf16(e4m3 * scale), which is exact
- * down to bf16's subnormals, and summed in fp32.  Instances as in moex_matmul;
+ * down to bf16's subnormals (infinite past its range), and summed in fp32.  Instances as in moex_matmul;
  * a bad instance's rows are left out.
  */
 int moex_wgrad(moe_plan_t h, const moe_plan_out* plan, const int32_t* inst_offset, const uint8_t* dy,

@@ -160,7 +160,8 @@ __global__ __launch_bounds__(kThreads, COLS == 256 ? 1 : 2) void wgrad_kernel(In
   auto widen = [&](const Piece& p, unsigned char* lds, int h) {
 #pragma unroll
     for (int j = h * S::kRows / 2; j < (h + 1) * S::kRows / 2; ++j) {
-      const float f = __uint_as_float(p.s[j] << 23);  // 255 gives NaN for the whole block
+      // the conversion takes the exponent alone: byte 0 is 2^-127, and 255 gives NaN for the whole block
+      const float f = __uint_as_float(p.s[j] << 23);
       u32x4 w[2];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {

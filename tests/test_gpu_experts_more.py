@@ -1,0 +1,138 @@
+"""Scale bytes that the quantizer does not write, and products of very different size in one step of the matrix
+instruction."""
+from __future__ import annotations
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from tests import expert_refs as refs
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def mp():
+    if not torch.cuda.is_available():
+        pytest.skip("no HIP device")
+    import load_balance_planning_amd as m
+    m.lib()
+    return m
+
+
+def one_instance_each(mp, layer, loads):
+    cap, dev = int(layer.sizes.inst_cap), layer.device
+    off = torch.zeros(cap + 1, dtype=torch.int32, device=dev)
+    off[1:] = torch.tensor(loads).cumsum(0).to(dev)
+    plan = mp.PlanBuffers(torch.tensor([cap], dtype=torch.int32, device=dev),
+                          torch.arange(cap, dtype=torch.int32, device=dev), None, None, None, None, None, None)
+    return dict(plan=plan, inst_offset=off)
+
+
+def blocks(mp, q, s, cols, dev):
+    """Blocks of given bytes."""
+    return mp.Blocks(q.to(torch.uint8).to(dev).view(torch.float8_e4m3fn), s.to(torch.uint8).to(dev).view(torch.float8_e8m0fnu),
+                     cols)
+
+
+def e4m3_value(byte):
+    return torch.tensor([byte], dtype=torch.uint8).view(torch.float8_e4m3fn).double().item()
+
+
+@pytest.mark.parametrize("rows", [6, 40, 256])
+@pytest.mark.parametrize("byte", [0x38, 0x7e, 0x01, 0xc4])   # 1, 448, the least subnormal 2^-9, -3
+def test_any_scale_byte(mp, rows, byte):
+    """Row r of x is one value under scale byte r * step: y is that value times 2^(byte - 127), rounded to bf16, and so
+    is the weight gradient of that row alone, where the value in bf16 is finite; a marked block's are NaN.  Kernels for
+    few rows and for tiles (a mean of more than 8 rows an expert)."""
+    n, v = 16, e4m3_value(byte)
+    layer = mp.Layer(mp.make_config(rows, 1, 1, 1, 1, 8, 0), cooc=False)
+    dev = layer.device
+    print("scale bytes rows=%d value=%g" % (rows, v), flush=True)
+    kw = one_instance_each(mp, layer, [rows])
+    s = torch.full((rows, 4), 127)
+    s[:, 0] = torch.linspace(0, 255, rows).round().int()
+    x = blocks(mp, torch.full((rows, 128), byte), s, 128, dev)
+    w = layer.quantize_weights(torch.eye(n, 128).to(BF)[None].contiguous().to(dev))
+    y = layer.matmul(x, w, **kw).cpu()
+    want = (v * torch.exp2(s[:, 0].double() - 127)).float().to(BF)
+    marked = s[:, 0] == 255
+    # 2^-149 v and above is an fp32 value exactly; bf16's rounding is the only one
+    assert torch.equal(y[~marked], want[~marked, None].expand(-1, n)) and torch.isnan(y[marked]).all()
+    # as the rows' gradient: dy row r is (1, 0, 0, ..) in row r's instance
+    for r in range(0, rows, max(1, rows // 12)):
+        lone = s.clone()
+        lone[:, 0] = 127
+        lone[r, 0] = s[r, 0]
+        dy = torch.zeros(rows, n, dtype=BF)
+        dy[r, 0] = 1
+        dw = layer.wgrad(layer.quantize(dy.to(dev)), blocks(mp, torch.full((rows, 128), byte), lone, 128, dev), **kw).cpu()[0]
+        if marked[r] or torch.isinf(want[r]):
+            assert not torch.isfinite(dw[0]).any()
+        else:
+            assert (dw[0] == want[r]).all() and (dw[1:] == 0).all(), (r, int(s[r, 0]))
+        # and as the gradient's scale: x row r is ones
+        one = torch.zeros(rows, 128)
+        one[r] = 0x38
+        dw = layer.wgrad(blocks(mp, torch.full((rows, 128), byte), s.where(torch.arange(rows)[:, None] == r, 127), n, dev),
+                         blocks(mp, one, torch.full((rows, 4), 127), 128, dev), **kw).cpu()[0]
+        if marked[r] or torch.isinf(want[r]):
+            assert not torch.isfinite(dw).any()
+        else:
+            assert (dw == want[r]).all(), (r, int(s[r, 0]))
+    assert layer.status() == 0
+    layer.close()
+
+
+@pytest.mark.parametrize("bytes_", [(0, 0, 7, 254), (1, 254, 0, 130)])
+def test_any_scale_byte_of_matrices(mp, bytes_):
+    """The matrices' scales, one per 128 x 128, in both layouts and both kernels."""
+    n, k = 200, 256
+    for rows in (4, 64):
+        layer = mp.Layer(mp.make_config(rows, 1, 1, 1, 1, 8, 0), cooc=False)
+        dev = layer.device
+        kw = one_instance_each(mp, layer, [rows])
+        ws = torch.full((1, 2, 4), 127)
+        ws[0, :, :2] = torch.tensor(bytes_).view(2, 2)
+        w = blocks(mp, torch.full((1, n, k), 0x38), ws, k, dev)
+        for half in range(2):
+            q = torch.zeros(rows, k)
+            q[:, 128 * half] = 0x38      # one value of 1
+            y = layer.matmul(blocks(mp, q, torch.full((rows, 4), 127), k, dev), w, **kw).cpu()
+            for b in range(2):
+                want = torch.tensor(2.0, dtype=torch.float64) ** (bytes_[2 * b + half] - 127)
+                got = y[:, 128 * b: min(n, 128 * (b + 1))].double()
+                assert (got == want).all(), (rows, half, b)
+        assert layer.status() == 0
+        layer.close()
+
+
+@pytest.mark.parametrize("rows", [8, 64])
+@pytest.mark.parametrize("seed", range(3))
+def test_small_products_beside_large_ones(mp, rows, seed):
+    """Pairs of large products that cancel exactly, and small ones whose sum is all that is left: what the matrix
+    instruction drops when it aligns a step's products to the largest stays within the bound of refs.product, and bf16's
+    rounding of the small result does not hide it."""
+    g = torch.Generator().manual_seed(seed)
+    n, k = 64, 128
+    e4 = lambda *s: torch.randn(*s, generator=g).clamp(-3, 3).to(torch.float8_e4m3fn).double()
+    layer = mp.Layer(mp.make_config(rows, 1, 1, 1, 1, 8, 0), cooc=False)
+    dev = layer.device
+    kw = one_instance_each(mp, layer, [rows])
+    worst = 0.0
+    for shift in range(0, 15):
+        x, w = e4(rows, k), e4(n, k)
+        x[:, 1:32:2], w[:, 1:32:2] = x[:, 0:32:2], -w[:, 0:32:2]      # 16 pairs that cancel
+        x[:, 32:] = (x[:, 32:] * 2.0 ** -(shift // 2)).to(torch.float8_e4m3fn).double()
+        w[:, 32:] = (w[:, 32:] * 2.0 ** -(shift - shift // 2)).to(torch.float8_e4m3fn).double()
+        byte = lambda v: v.to(torch.float8_e4m3fn).view(torch.uint8)
+        y = layer.matmul(blocks(mp, byte(x), torch.full((rows, 4), 127), k, dev),
+                         blocks(mp, byte(w)[None], torch.full((1, 1, 4), 127), k, dev), **kw).cpu().double()
+        want, bound = refs.product(x, w)
+        err = (y - want).abs()
+        assert (err <= bound).all(), (shift, float((err - bound).max()))
+        top = (x.abs()[:, None] * w.abs()[None]).amax(-1)
+        worst = max(worst, float(((err - 2.0 ** -8 * want.abs()).clamp(min=0) / top).max()))
+    print("beyond bf16's rounding: %.3g of the largest product" % worst, flush=True)
+    layer.close()
