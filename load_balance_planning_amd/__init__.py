@@ -444,7 +444,13 @@ class Blocks:
 
 
 class Layer:
-    """One MoE layer's planner: a handle plus torch-allocated output buffers."""
+    """One MoE layer's planner: a handle plus torch-allocated output buffers.
+
+    route_out, plan_out and dispatch_out are one set of buffers, overwritten by the layer's next gate / route, plan
+    and dispatch.  Calls that take them by default (gate_grad's topk_idx, the products' plan and inst_offset, the
+    combines' slot_pos) are for the pass that ran last.  Where a layer runs forward several times before the first
+    backward pass (micro-batches, pipelining, recomputation), keep copies of that pass's topk_idx, n_inst,
+    inst_expert, inst_offset and slot_pos and pass them."""
 
     def __init__(self, cfg: moe_plan_config, device=None, cooc: bool = True, trans: bool = False,
                  topk_val: bool = True):
@@ -550,7 +556,8 @@ class Layer:
         return out
 
     def gate(self, logits, gate: moex_gate_config, bias=None, prev_topk=None, stream=None):
-        """Routing with scores, bias, groups and weights (moex_gate): (route_out, weight [T][k])."""
+        """Routing with scores, bias, groups and weights (moex_gate): (route_out, weight [T][k]).  The weights are the
+        call's own, route_out is the layer's and overwritten by its next gate() or route()."""
         torch, (T, E, k, _) = self.torch, self._dims
         self._check_tensor(logits, (T, E), torch.float32)
         if bias is not None:
@@ -563,7 +570,8 @@ class Layer:
         return self.route_out, weight
 
     def gate_grad(self, logits, gate: moex_gate_config, grad_weight, topk_idx=None, out=None, stream=None):
-        """Gradient of gate()'s weights for the logits (moex_gate_grad); topk_idx defaults to this layer's."""
+        """Gradient of gate()'s weights for the logits (moex_gate_grad).  topk_idx defaults to this layer's, which are
+        those of its last gate() or route(): pass a copy if there was another since the one these weights came from."""
         torch, (T, E, k, _) = self.torch, self._dims
         topk_idx = self.route_out.topk_idx if topk_idx is None else topk_idx
         self._check_tensor(logits, (T, E), torch.float32)
@@ -649,7 +657,8 @@ class Layer:
         return out
 
     def _product_plan(self, plan, inst_offset):
-        """The struct of the instances a product runs over; by default this layer's plan and dispatch offsets."""
+        """The struct of the instances a product runs over; by default this layer's plan and dispatch offsets, those of
+        its last plan() and dispatch().  Of a given plan, n_inst and inst_expert are read."""
         inst_offset = self.dispatch_out.inst_offset if inst_offset is None else inst_offset
         cap = self._cap
         self._check_tensor(inst_offset, (cap + 1,), self.torch.int32)

@@ -1,6 +1,8 @@
-"""Scale bytes that the quantizer does not write, and products of very different size in one step of the matrix
-instruction."""
+"""Scale bytes that the quantizer does not write, products of very different size in one step of the matrix
+instruction, and two forward passes of a layer before their backward passes."""
 from __future__ import annotations
+
+import dataclasses
 
 import pytest
 
@@ -182,4 +184,57 @@ def test_what_the_matrix_instruction_keeps(mp, rows):
     kept = pairs(2.0 ** -5)
     assert (product(*kept) == k * 6 / 8 * 2.0 ** -5).all()
     assert layer.status() == 0
+    layer.close()
+
+
+def forward(layer, st, m):
+    """A forward pass of an expert layer and what its backward pass needs, as copies."""
+    r, weight = layer.gate(m["logits"], st["gate"], bias=st["bias"])
+    layer.plan()
+    x = layer.quantize(layer.dispatch(m["hidden"]).dispatch)
+    y1 = layer.matmul(x, st["w1"][0])
+    a = layer.swiglu(y1)
+    y2 = layer.matmul(a, st["w2"][0])
+    out = layer.combine_weighted(y2, weight)
+    d, p = layer.dispatch_out, layer.plan_out
+    plan = dataclasses.replace(p, n_inst=p.n_inst.clone(), inst_expert=p.inst_expert.clone())
+    return out, dict(x=x, y1=y1, a=a, y2=y2, weight=weight, topk_idx=r.topk_idx.clone(), slot_pos=d.slot_pos.clone(),
+                     on=dict(plan=plan, inst_offset=d.inst_offset.clone()))
+
+
+def backward(layer, st, m, s):
+    at = dict(slot_pos=s["slot_pos"])
+    dy2, dweight = layer.combine_grad(s["y2"], m["grad"], s["weight"], **at)
+    dy2 = layer.quantize(dy2)
+    dw2 = layer.wgrad(dy2, s["a"], **s["on"])
+    dy1 = layer.swiglu_grad(s["y1"], layer.matmul(dy2, st["w2"][1], **s["on"]))
+    dw1 = layer.wgrad(dy1, s["x"], **s["on"])
+    dhidden = layer.combine_weighted(layer.matmul(dy1, st["w1"][1], **s["on"]), **at)
+    return dw1, dw2, dhidden, layer.gate_grad(m["logits"], st["gate"], dweight, topk_idx=s["topk_idx"])
+
+
+def test_two_forward_passes_before_their_backward_passes(mp):
+    """With the kept top-k, plan, offsets and positions, each backward pass is that of its own forward pass."""
+    T, E, k, R, G, H, F = 96, 16, 4, 2, 1, 256, 72
+    cfg = mp.make_config(T, E, k, R, G, H, 2, expert_bytes=0)
+    layer = mp.Layer(cfg)
+    dev = layer.device
+    g = torch.Generator().manual_seed(4)
+    n = lambda *s, scale=1.0: (scale * torch.randn(*s, generator=g)).to(dev)
+    st = dict(gate=mp.make_gate("sigmoid", 4, 2, 2, True, 2.5), bias=n(E, scale=0.1),
+              w1=layer.quantize_weights(n(E, 2 * F, H, scale=H ** -0.5).to(BF), transposed=True),
+              w2=layer.quantize_weights(n(E, H, F, scale=F ** -0.5).to(BF), transposed=True))
+    batches = [dict(logits=n(T, E), hidden=n(T, H).to(BF), grad=n(T, H).to(BF)) for _ in range(2)]
+    want = []
+    for m in batches:
+        alone = mp.Layer(cfg)
+        out, s = forward(alone, st, m)
+        want.append((out, *backward(alone, st, m, s)))
+        assert alone.status() == 0
+        alone.close()
+    saved = [forward(layer, st, m) for m in batches]
+    got = [(out, *backward(layer, st, m, s)) for m, (out, s) in zip(batches, saved)]
+    for a, b in zip(got, want):
+        assert all(torch.equal(t, u) for t, u in zip(a, b))
+    assert not torch.equal(saved[0][1]["topk_idx"], saved[1][1]["topk_idx"]) and layer.status() == 0
     layer.close()
