@@ -1,5 +1,5 @@
 """Scale bytes that the quantizer does not write, products of very different size in one step of the matrix
-instruction, and two forward passes of a layer before their backward passes."""
+instruction, two forward passes of a layer before their backward passes, and whose memory results on a stream are."""
 from __future__ import annotations
 
 import dataclasses
@@ -237,4 +237,41 @@ def test_two_forward_passes_before_their_backward_passes(mp):
     for a, b in zip(got, want):
         assert all(torch.equal(t, u) for t, u in zip(a, b))
     assert not torch.equal(saved[0][1]["topk_idx"], saved[1][1]["topk_idx"]) and layer.status() == 0
+    layer.close()
+
+
+def test_no_result_of_a_side_stream_goes_to_another(mp):
+    """Results of calls on a stream are dropped while the stream may still write them: tensors of the current stream,
+    of the same sizes, never get their memory."""
+    T, E, k, H, n = 64, 4, 1, 256, 48
+    layer, side = mp.Layer(mp.make_config(T, E, k, 1, 1, H, 0), cooc=False), torch.cuda.Stream()
+    dev = layer.device
+    g = torch.Generator().manual_seed(1)
+    rnd = lambda *s: torch.randn(*s, generator=g).to(dev)
+    kw = one_instance_each(mp, layer, [16] * 4)
+    x, w, lg, gw = rnd(T, H).to(BF), rnd(E, n, H).to(BF), rnd(T, E), rnd(T, k)
+    pos = torch.arange(T * k, dtype=torch.int32, device=dev)
+    router = mp.make_gate("sigmoid")
+    torch.cuda.synchronize()
+
+    def everything():
+        xb = layer.quantize(x, stream=side)
+        wb, wt = layer.quantize_weights(w, transposed=True, stream=side)
+        _, weight = layer.gate(lg, router, stream=side)
+        y = layer.matmul(xb, wb, stream=side, **kw)
+        yb = layer.quantize(y, stream=side)
+        a, da = layer.swiglu(x, stream=side), layer.swiglu_grad(x, x[:, : H // 2].contiguous(), stream=side)
+        return [xb.q, xb.scale, wb.q, wb.scale, wt.q, wt.scale, weight, y, yb.q, yb.scale, a.q, a.scale, da.q, da.scale,
+                layer.matmul(yb, wt, stream=side, **kw), layer.wgrad(yb, xb, stream=side, **kw),
+                layer.gate_grad(lg, router, gw, stream=side), layer.combine_weighted(x, gw, slot_pos=pos, stream=side),
+                *layer.combine_grad(x, x, gw, slot_pos=pos, stream=side)]
+
+    results = everything()
+    freed, shapes = {t.data_ptr() for t in results}, [(t.shape, t.dtype) for t in results]
+    assert len(freed) == len(results)
+    del results
+    taken = [torch.empty(s, dtype=d, device=dev) for s, d in shapes for _ in range(4)]
+    assert not freed & {t.data_ptr() for t in taken}
+    side.synchronize()
+    assert layer.status() == 0
     layer.close()
