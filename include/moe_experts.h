@@ -122,7 +122,10 @@ int moex_gate(moe_plan_t h, const moex_gate_config* gate, const float* logits, c
 int moex_gate_grad(moe_plan_t h, const moex_gate_config* gate, const float* logits, const int32_t* topk_idx,
                    const float* grad_weight, float* grad_logits, void* stream);
 
-/* x bf16 [rows][cols] to blocks of 1 x 128.  0 <= rows < 2^31, cols >= 1. */
+/*
+ * x bf16 [rows][cols] to blocks of 1 x 128.  rows >= 0, cols >= 1;
+ * MOE_ERR_UNSUPPORTED from 2^31 rows on and above 2^24 columns.
+ */
 int moex_quantize(moe_plan_t h, const uint16_t* x, int64_t rows, int32_t cols, uint8_t* q, uint8_t* scale,
                   void* stream);
 
@@ -131,20 +134,24 @@ int moex_quantize(moe_plan_t h, const uint16_t* x, int64_t rows, int32_t cols, u
  * [experts][ceil(n/128)][.], and (both or neither) the transposed matrices qt
  * [experts][k][np] with scale_t [experts][ceil(k/128)][.] -- the same values
  * and scales, in the layout that moex_matmul needs for the input gradient.
+ * experts >= 0, 1 <= n, k; MOE_ERR_UNSUPPORTED for n or k above 2^24 and for
+ * 2^24 blocks of 128 x 128 or more in all matrices together.
  */
 int moex_quantize_weights(moe_plan_t h, const uint16_t* w, int32_t experts, int32_t n, int32_t k, uint8_t* q,
                           uint8_t* scale, uint8_t* qt, uint8_t* scale_t, void* stream);
 
 /*
  * y bf16 [rows][2 f]: gate columns, then up columns.  a = y_gate * sigmoid(y_gate)
- * * y_up in fp32, quantized as a row of f columns.
+ * * y_up in fp32, quantized as a row of f columns.  rows and f as rows and cols
+ * of moex_quantize.
  */
 int moex_swiglu(moe_plan_t h, const uint16_t* y, int64_t rows, int32_t f, uint8_t* q, uint8_t* scale, void* stream);
 
 /*
  * Its gradient for y from grad bf16 [rows][f]: with s = sigmoid(y_gate),
  *   d gate = grad * y_up * s * (1 + y_gate (1 - s)),  d up = grad * y_gate * s
- * in fp32, quantized as a row of 2 f columns (d gate, then d up).
+ * in fp32, quantized as a row of 2 f columns (d gate, then d up).  rows and f
+ * as rows and cols of moex_quantize.
  */
 int moex_swiglu_grad(moe_plan_t h, const uint16_t* y, const uint16_t* grad, int64_t rows, int32_t f, uint8_t* q,
                      uint8_t* scale, void* stream);

@@ -275,3 +275,32 @@ def test_no_result_of_a_side_stream_goes_to_another(mp):
     side.synchronize()
     assert layer.status() == 0
     layer.close()
+
+
+def test_limits_of_sizes(mp):
+    """Each stated limit is the last size taken; the sizes past it are refused before any device work."""
+    layer = mp.Layer(mp.make_config(8, 4, 1, 1, 1, 8, 0), cooc=False)
+    lib, h, big, bad, dev = mp.lib(), layer.handle, mp.MOE_ERR_UNSUPPORTED, mp.MOE_ERR_INVALID_ARG, layer.device
+    x = torch.zeros(1 << 12, dtype=torch.uint8, device=dev)
+    p = x.data_ptr()
+    row = {"quantize": lambda r, c: lib.moex_quantize(h, p, r, c, p, p, None),
+           "swiglu": lambda r, c: lib.moex_swiglu(h, p, r, c, p, p, None),
+           "swiglu_grad": lambda r, c: lib.moex_swiglu_grad(h, p, p, r, c, p, p, None)}
+    for name, call in row.items():
+        assert call(1 << 31, 1) == big and call(1, (1 << 24) + 1) == big, name
+        assert call(-1, 1) == bad and call(1, 0) == bad, name
+        assert call(0, 1 << 24) == mp.MOE_OK, name
+    mats = lambda e, n, k: lib.moex_quantize_weights(h, p, e, n, k, p, p, None, None, None)
+    assert mats(1, (1 << 24) + 1, 1) == big and mats(1, 1, (1 << 24) + 1) == big
+    assert mats(1 << 24, 1, 1) == big and mats(1 << 14, 1 << 12, 1 << 12) == big
+    assert mats(-1, 1, 1) == bad and mats(1, 0, 1) == bad and mats(1, 1, 0) == bad
+    assert mats(0, 1 << 24, 1 << 24) == mp.MOE_OK
+    # the widest row: the last value of 2^24 and its block
+    wide = torch.zeros(1, 1 << 24, dtype=BF, device=dev)
+    wide[0, -1] = 3.0
+    b = layer.quantize(wide)
+    assert b.q[0, -1].item() * 2.0 ** (int(b.scale.view(torch.uint8)[0, -1]) - 127) == 3.0
+    assert int((b.q.view(torch.uint8) != 0).sum()) == 1
+    torch.cuda.synchronize()
+    assert layer.status() == 0 and int((x != 0).sum()) == 0
+    layer.close()
