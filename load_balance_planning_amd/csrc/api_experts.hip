@@ -96,8 +96,9 @@ extern "C" int moex_quantize_weights(moe_plan_t h, const uint16_t* w, int32_t ex
   if (n > (1 << 24) || k > (1 << 24)) return MOE_ERR_UNSUPPORTED;
   if (experts > 0 && (!w || !blocks_ok(q, scale))) return MOE_ERR_INVALID_ARG;
   if ((qt == nullptr) != (scale_t == nullptr) || (qt && !blocks_ok(qt, scale_t))) return MOE_ERR_INVALID_ARG;
-  const int64_t blocks = (int64_t)experts * (moe::padded_cols(n) / moe::kBlk) * (moe::padded_cols(k) / moe::kBlk);
-  if (blocks >= (int64_t)1 << 24) return MOE_ERR_UNSUPPORTED;  // one 256-thread workgroup each, fewer than 2^32 threads
+  // one 256-thread workgroup per block, fewer than 2^32 threads; by division, as the product can pass 64 bits
+  const int64_t per_matrix = (moe::padded_cols(n) / moe::kBlk) * (moe::padded_cols(k) / moe::kBlk);
+  if (experts > (((int64_t)1 << 24) - 1) / per_matrix) return MOE_ERR_UNSUPPORTED;
   const DeviceScope on_device(h->device);
   if (!on_device.ok()) return MOE_ERR_HIP;
   return hip_rc(moe::launch_quantize_weights(w, experts, n, k, q, scale, qt, scale_t, begin_call(h, stream)));

@@ -304,3 +304,14 @@ def test_limits_of_sizes(mp):
     torch.cuda.synchronize()
     assert layer.status() == 0 and int((x != 0).sum()) == 0
     layer.close()
+
+
+def test_counts_of_blocks_past_64_bits_are_refused(mp):
+    """experts * blocks per matrix would be 2^63, 2^64 and more, negative or small where it wraps."""
+    layer = mp.Layer(mp.make_config(8, 4, 1, 1, 1, 8, 0), cooc=False)
+    p = torch.zeros(64, dtype=torch.uint8, device=layer.device).data_ptr()
+    for experts, n, k in ((1 << 29, 1 << 24, 1 << 24), (1 << 30, 1 << 24, 1 << 24), ((1 << 31) - 1, 1 << 24, 1 << 24),
+                          ((1 << 30) + 1, (1 << 24) - 128, (1 << 24) - 256), (1 << 30, 1 << 23, 1 << 24)):
+        assert mp.lib().moex_quantize_weights(layer.handle, p, experts, n, k, p, p, None, None, None) == mp.MOE_ERR_UNSUPPORTED
+    assert layer.status() == 0
+    layer.close()
