@@ -492,12 +492,12 @@ int64_t matmul_tiles(const Instances& in, int32_t n) {
 
 hipError_t launch_matmul(const Instances& in, const uint8_t* x, const uint8_t* xs, const uint8_t* w, const uint8_t* ws,
                          int32_t n, int32_t k, uint16_t* y, int32_t* status, hipStream_t st) {
-  if (in.rows == 0) return hipSuccess;
   const int tile = matmul_tile(in, n);
   if (tile == 256) return launch_tiles<256, 256, 2, 2>(in, x, xs, w, ws, n, k, y, status, st);
   if (tile == 128) return launch_tiles<128, 128, 2, 2>(in, x, xs, w, ws, n, k, y, status, st);
-  const int64_t tiles = row_tile_ids(in, kRowsS) * ((n + kChanS - 1) / kChanS);
-  const int64_t grid = tiles < (1 << 20) ? tiles : (1 << 20);
+  // without rows one workgroup, which only looks at the plan
+  const int64_t tiles = in.rows == 0 ? 0 : row_tile_ids(in, kRowsS) * ((n + kChanS - 1) / kChanS);
+  const int64_t grid = tiles < 1 ? 1 : tiles < (1 << 20) ? tiles : (1 << 20);
   hipLaunchKernelGGL(matmul_rows16_kernel, dim3((unsigned)grid), dim3(256), 0, st, in, x, xs, w, ws, n, k, tiles, y,
                      status);
   return hipGetLastError();

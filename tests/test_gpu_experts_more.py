@@ -315,3 +315,24 @@ def test_counts_of_blocks_past_64_bits_are_refused(mp):
         assert mp.lib().moex_quantize_weights(layer.handle, p, experts, n, k, p, p, None, None, None) == mp.MOE_ERR_UNSUPPORTED
     assert layer.status() == 0
     layer.close()
+
+
+def test_a_bad_plan_of_no_tokens(mp):
+    """The status word tells of a bad count, expert or offset also where there are no rows."""
+    layer = mp.Layer(mp.make_config(0, 4, 2, 1, 1, 64, 0), cooc=False)
+    dev = layer.device
+    rows = layer.quantize(torch.empty(0, 64, dtype=BF, device=dev))
+    dy = layer.quantize(torch.empty(0, 48, dtype=BF, device=dev))
+    w = layer.quantize_weights(torch.zeros(4, 48, 64, dtype=BF, device=dev))
+    for change, want in ((lambda: None, 0), (lambda: layer.plan_out.n_inst.fill_(5), mp.MOE_STATUS_PLAN_CHECK),
+                         (lambda: layer.plan_out.inst_expert[2].fill_(4), mp.MOE_STATUS_PLAN_CHECK),
+                         (lambda: layer.dispatch_out.inst_offset[1].fill_(1), mp.MOE_STATUS_PLAN_CHECK)):
+        layer.plan_out.n_inst.fill_(4)
+        layer.plan_out.inst_expert.copy_(torch.arange(4))
+        layer.dispatch_out.inst_offset.zero_()
+        change()
+        assert layer.matmul(rows, w).shape == (0, 48)
+        assert layer.status() == want
+        assert (layer.wgrad(dy, rows) == 0).all()
+        assert layer.status() == want
+    layer.close()
