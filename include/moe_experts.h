@@ -185,7 +185,8 @@ int moex_matmul(moe_plan_t h, const moe_plan_out* plan, const int32_t* inst_offs
  * took); dw: uint16 [E][n][k] bf16, fully overwritten (zeros for an expert
  * without rows).  Each value is taken as bf16(e4m3 * scale), which is exact
  * down to bf16's subnormals (infinite past its range), and summed in fp32.
- * Instances as in moex_matmul; a bad instance's rows are left out.
+ * Instances as in moex_matmul; a bad instance's rows are left out, and past T*k
+ * rows (offsets that fall and rise again) those of an expert's others.
  */
 int moex_wgrad(moe_plan_t h, const moe_plan_out* plan, const int32_t* inst_offset, const uint8_t* dy,
                const uint8_t* dy_scale, const uint8_t* x, const uint8_t* x_scale, int32_t n, int32_t k, uint16_t* dw,

@@ -55,12 +55,16 @@ struct GradShape {
 // The steps of an expert: 64 rows of one instance at a time, instances in
 // order.  Every lane of a wave steps alike, and holds one of the 64 instances
 // from i0 on, whose bit is set in `mask` if it is a good one of the expert's.
+// Instances that lie one behind the other have T*k rows at most; offsets that
+// fall in between may repeat them, thousands of times in a large plan, and the
+// steps end at T*k.
 struct Steps {
   int n_inst, expert;
   int i0;
   uint64_t mask;
   int begin, end_of;  // this lane's instance
   int row, end;       // the instance under way (rows < 2^31)
+  int left;           // rows of instances not begun, at most
 };
 __device__ __forceinline__ void steps_load(Steps* s, const Instances& in) {
   const int mine = s->i0 + (threadIdx.x & 63), i = min(mine, in.cap - 1);
@@ -74,6 +78,7 @@ __device__ __forceinline__ void steps_load(Steps* s, const Instances& in) {
   s->expert = expert;
   s->i0 = 0;
   s->row = s->end = 0;
+  s->left = (int)in.rows;
   s->n_inst = instance_count(in);
   steps_load(s, in);
 }
@@ -89,7 +94,8 @@ __device__ __forceinline__ void steps_load(Steps* s, const Instances& in) {
     const int who = __ffsll((unsigned long long)s->mask) - 1;
     s->mask &= s->mask - 1;
     s->row = __builtin_amdgcn_readlane(s->begin, who);
-    s->end = __builtin_amdgcn_readlane(s->end_of, who);
+    s->end = s->row + min(s->left, __builtin_amdgcn_readlane(s->end_of, who) - s->row);
+    s->left -= s->end - s->row;
   }
   *row = s->row;
   *rows = min(kStepRows, s->end - s->row);

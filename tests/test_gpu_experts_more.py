@@ -336,3 +336,26 @@ def test_a_bad_plan_of_no_tokens(mp):
         assert (layer.wgrad(dy, rows) == 0).all()
         assert layer.status() == want
     layer.close()
+
+
+@pytest.mark.parametrize("rows,n,k", [(2048, 48, 96), (2048, 8200, 2100)])
+def test_repeated_rows_end_at_the_buffer_s_rows(mp, rows, n, k):
+    """Every second of 32 instances holds all rows, and those between fall back: an expert's rows are summed until
+    there were T*k of them, in both tile sizes."""
+    E, B = 4, 28
+    layer = mp.Layer(mp.make_config(rows, E, 1, 1, 1, 8, B), cooc=False)
+    dev = layer.device
+    g = torch.Generator().manual_seed(n)
+    x, dy = (layer.quantize(torch.randn(rows, c, generator=g).to(BF).to(dev)) for c in (k, n))
+    layer.plan_out.inst_expert.copy_(torch.arange(E + B) // 2 % E)   # two instances an expert, in turn: a whole and a bad one
+    layer.plan_out.n_inst.fill_(E + B)
+    layer.dispatch_out.inst_offset.copy_(torch.tensor([0, rows] * 16 + [0], dtype=torch.int32))
+    got = layer.wgrad(dy, x)
+    assert layer.status() == mp.MOE_STATUS_PLAN_CHECK
+    one = one_instance_each(mp, layer, [rows] + [0] * (E + B - 1))
+    one["plan"].n_inst.fill_(1)
+    want = layer.wgrad(dy, x, **one)[0]
+    assert layer.status() == 0 and bool(want.abs().sum() > 0)
+    for e in range(E):
+        assert torch.equal(got[e], want), e
+    layer.close()
