@@ -501,6 +501,8 @@ class Layer:
     def _stream(self, stream=None) -> int:
         if stream is None:
             return self._current_stream(self._index)
+        if stream.device_index != self._index:
+            raise ValueError("expected a stream of %s, got %s" % (self.device, stream))
         return stream.cuda_stream
 
     def route(self, logits, prev_topk=None, stream=None):
@@ -598,6 +600,7 @@ class Layer:
         stream's tensors while the call may still write it."""
         if stream is None:
             return self.torch.empty(*shape, dtype=dtype, device=self.device)
+        self._stream(stream)  # not one of another device
         with self.torch.cuda.stream(stream):
             return self.torch.empty(*shape, dtype=dtype, device=self.device)
 

@@ -31,3 +31,39 @@ def test_the_lookup_names_the_current_stream():
             assert lookup(index) == torch.cuda.current_stream(index).cuda_stream == stream.cuda_stream
             handles.add(lookup(index))
     assert len(handles) == 4
+
+
+def bare_layer(mp, index=0):
+    """A Layer without a device behind it, for the checks that come before any device work."""
+    layer = object.__new__(mp.Layer)
+    layer.torch, layer._index, layer.device, layer.handle = torch, index, torch.device("cuda", index), None
+    layer._current_stream = lambda i: 0x10 + i
+    return layer
+
+
+def test_a_stream_of_another_device_is_refused():
+    import load_balance_planning_amd as mp
+    layer = bare_layer(mp)
+    assert layer._stream() == 0x10
+    assert layer._stream(SimpleNamespace(device_index=0, cuda_stream=0x77)) == 0x77
+    other = SimpleNamespace(device_index=1, cuda_stream=0x78)
+    with pytest.raises(ValueError):
+        layer._stream(other)
+    with pytest.raises(ValueError):
+        layer._empty((4,), torch.float32, other)
+
+
+@pytest.mark.gpu
+def test_an_external_stream_is_taken():
+    if not torch.cuda.is_available():
+        pytest.skip("no HIP device")
+    import load_balance_planning_amd as mp
+    layer = mp.Layer(mp.make_config(8, 4, 1, 1, 1, 8, 0), cooc=False)
+    x = torch.ones(4, 8, dtype=torch.bfloat16, device=layer.device)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    b = layer.quantize(x, stream=torch.cuda.ExternalStream(side.cuda_stream))
+    side.synchronize()
+    assert (b.q[:, :8].float() * 2.0 ** (b.scale.view(torch.uint8)[:, :1].float() - 127) == 1).all()
+    assert layer.status() == 0
+    layer.close()
