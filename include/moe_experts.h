@@ -78,7 +78,7 @@ extern "C" {
  *   group_top   1 or 2: a group's value is the sum of its group_top largest
  *               choice values (at most E / n_group)
  *   renorm      non-zero: weights are divided by their sum + 1e-20
- *   scale       factor of the weights
+ *   scale       factor of the weights, at most 2^32 in magnitude
  */
 typedef struct {
   int32_t score, n_group, topk_group, group_top, renorm;

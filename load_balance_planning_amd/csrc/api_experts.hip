@@ -17,7 +17,9 @@ int check_gate(const moe::Dims& d, const moex_gate_config* g) {
     return MOE_ERR_INVALID_ARG;
   const int per = d.E / g->n_group;
   if (g->n_group > 1 && (g->group_top < 1 || g->group_top > 2 || g->group_top > per)) return MOE_ERR_INVALID_ARG;
-  if ((int64_t)g->topk_group * per < d.k || !isfinite(g->scale)) return MOE_ERR_INVALID_ARG;
+  if ((int64_t)g->topk_group * per < d.k) return MOE_ERR_INVALID_ARG;
+  // scale / (sum + 1e-20), and its product with a weight's gradient, stay finite; a NaN is refused too
+  if (!(fabsf(g->scale) <= 4294967296.0f)) return MOE_ERR_INVALID_ARG;
   if (g->n_group > moe::kMaxGateGroups) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

@@ -207,3 +207,27 @@ def test_unaligned_logits_of_few_tokens(mp, T, E, k, groups):
     assert torch.equal(r.topk_idx, idx) and torch.equal(w, w2) and layer.status() == 0
     assert torch.equal(idx.cpu().long(), refs.select(x.double(), b.double(), "sigmoid", k, *groups))
     layer.close()
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_the_largest_scale(mp, kind):
+    """At 2^32 a masked row has weights and gradients of zero, not of infinity times zero; above it the call is refused."""
+    T, E, k = 16, 32, 4
+    x = torch.randn(T, E, generator=torch.Generator().manual_seed(1))
+    x[3] = -torch.inf
+    layer = mp.Layer(mp.make_config(T, E, k, 1, 1, 8, 0), cooc=False)
+    xd, ones = x.to(layer.device), torch.ones(T, k, device=layer.device)
+    for scale in (2.0 ** 32, -2.0 ** 32):
+        gate = mp.make_gate(kind, scale=scale)
+        r, w = layer.gate(xd, gate)
+        g = layer.gate_grad(xd, gate, 1e6 * ones)
+        assert torch.isfinite(w).all() and torch.isfinite(g).all() and (w[3] == 0).all() and (g[3] == 0).all()
+        want = refs.gate_weights(x.double(), r.topk_idx.cpu().long(), kind, True, scale)
+        assert ((w.cpu().double() - want).abs() <= (E / 8 + 2 * k + 432) * 2.0 ** -24 * want.abs()).all()
+    for scale in (2.0 ** 33, -1e30, float("inf"), float("nan")):
+        for call in (lambda gate: layer.gate(xd, gate), lambda gate: layer.gate_grad(xd, gate, ones)):
+            with pytest.raises(mp.MoePlanError) as e:
+                call(mp.make_gate(kind, scale=scale))
+            assert e.value.code == mp.MOE_ERR_INVALID_ARG
+    assert layer.status() == 0
+    layer.close()
