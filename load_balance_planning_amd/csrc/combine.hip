@@ -32,35 +32,36 @@ constexpr int kRowsInFlight = 8;
 // Fewer tokens than this do not fill 256 CUs with a workgroup each.  64 tokens
 // of 8 rows of 7168: 11 -> 4.5 us, their gradient 8 -> 4.5 us.
 constexpr int kFewTokens = 512;
-typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 // A row of H >= 8 values is read and written in ceil(H / 8) vectors of 16 bytes
 // from any address of a 16-bit type; the last begins at H - 8, so where H is no
 // multiple of 8 it has values of the one before again (value by value, such
 // rows took two to eight times as long: 8192 tokens of 8 rows of 7167, 553 us and 218;
 // 64 tokens of 8 rows of 7001, 39 and 5).
-typedef v4u v4u_any __attribute__((aligned(2)));
 __device__ __forceinline__ int vector_at(int v, int H) { return min(8 * v, H - 8); }
 
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
-// fp32 -> bf16 bits, round to nearest even; NaN stays a quiet NaN.
-__device__ __forceinline__ uint32_t to_bf16(float f) {
-  const uint32_t u = __float_as_uint(f);
-  if ((u & 0x7fffffffu) > 0x7f800000u) return (u >> 16) | 0x40u;
-  return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
+// acc[0..7] += w * (8 bf16 values of v), each an fp32 FMA.
+__device__ __forceinline__ void fma_row(float* acc, float w, const u32x4& v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    acc[2 * i] = fmaf(w, bf16_low(v[i]), acc[2 * i]);
+    acc[2 * i + 1] = fmaf(w, bf16_high(v[i]), acc[2 * i + 1]);
+  }
 }
 
-// acc[0..7] += w * (8 bf16 values of v), each an fp32 FMA.
-__device__ __forceinline__ void fma_row(float* acc, float w, const uint4& v) {
-  acc[0] = fmaf(w, bf16_lo(v.x), acc[0]);
-  acc[1] = fmaf(w, bf16_hi(v.x), acc[1]);
-  acc[2] = fmaf(w, bf16_lo(v.y), acc[2]);
-  acc[3] = fmaf(w, bf16_hi(v.y), acc[3]);
-  acc[4] = fmaf(w, bf16_lo(v.z), acc[4]);
-  acc[5] = fmaf(w, bf16_hi(v.z), acc[5]);
-  acc[6] = fmaf(w, bf16_lo(v.w), acc[6]);
-  acc[7] = fmaf(w, bf16_hi(v.w), acc[7]);
+// The 8 sums, each rounded once.  Gives the bits of pack_bf16 for every fp32
+// value, in integer arithmetic: with the conversion instruction the four-vector
+// kernel took longer (32768 tokens of 8 rows of 7168, given weights: 776 and
+// 802 us; one vector a thread, 4096 tokens of rows of 2055: 32.6 and 32.1).
+__device__ __forceinline__ u32x4 rounded(const float* acc) {
+  auto bits = [](float f) {
+    const uint32_t u = __float_as_uint(f);
+    if ((u & 0x7fffffffu) > 0x7f800000u) return (u >> 16) | 0x40u;  // NaN stays a quiet NaN
+    return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
+  };
+  u32x4 y;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = bits(acc[2 * i]) | (bits(acc[2 * i + 1]) << 16);
+  return y;
 }
 
 // Weights and row positions of token t into LDS (first wave).  GIVEN: topk_val
@@ -135,17 +136,17 @@ __global__ __launch_bounds__(kCombThreads) void combine_vec_kernel(Dims d, const
         pj[q] = j + q < d.k ? p_s[j + q] : -1;
         wj[q] = pj[q] >= 0 ? w_s[j + q] : 0.0f;
       }
-      uint4 x[kRowsInFlight][VPT];
+      u32x4 x[kRowsInFlight][VPT];
 #pragma unroll
       for (int q = 0; q < kRowsInFlight; ++q) {
         const uint16_t* row = expert_out + (int64_t)(pj[q] >= 0 ? pj[q] : 0) * d.H;
 #pragma unroll
         for (int u = 0; u < VPT; ++u) {
           const int c = base + threadIdx.x + u * kCombThreads;
-          v4u y = {0, 0, 0, 0};  // a skipped slot adds 0 * 0
+          u32x4 y = {0, 0, 0, 0};  // a skipped slot adds 0 * 0
           if (c < vpr && pj[q] >= 0)
-            y = __builtin_nontemporal_load(reinterpret_cast<const v4u_any*>(row + vector_at(c, d.H)));
-          x[q][u] = make_uint4(y.x, y.y, y.z, y.w);
+            y = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(row + vector_at(c, d.H)));
+          x[q][u] = y;
         }
       }
 #pragma unroll
@@ -158,12 +159,7 @@ __global__ __launch_bounds__(kCombThreads) void combine_vec_kernel(Dims d, const
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {
       const int c = base + threadIdx.x + u * kCombThreads;
-      if (c < vpr) {
-        v4u y;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = to_bf16(acc[u][2 * i]) | (to_bf16(acc[u][2 * i + 1]) << 16);
-        *reinterpret_cast<v4u_any*>(dst + vector_at(c, d.H)) = y;
-      }
+      if (c < vpr) *reinterpret_cast<u32x4_any*>(dst + vector_at(c, d.H)) = rounded(acc[u]);
     }
   }
 }
@@ -183,9 +179,9 @@ __global__ __launch_bounds__(kCombThreads) void combine_u16_kernel(Dims d, const
     float acc = 0.0f;
     for (int j = 0; j < d.k; ++j) {
       const int p = p_s[j];
-      if (p >= 0) acc = fmaf(w_s[j], __uint_as_float((uint32_t)expert_out[(int64_t)p * d.H + c] << 16), acc);
+      if (p >= 0) acc = fmaf(w_s[j], bf16_low(expert_out[(int64_t)p * d.H + c]), acc);
     }
-    out[t * d.H + c] = (uint16_t)to_bf16(acc);
+    out[t * d.H + c] = (uint16_t)pack_bf16(acc, 0.0f);
   }
 }
 
@@ -197,7 +193,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // dot += 8 products of bf16 values, each an fp32 FMA.
-__device__ __forceinline__ void dot_row(float* dot, const v4u& g, const v4u& x) {
+__device__ __forceinline__ void dot_row(float* dot, const u32x4& g, const u32x4& x) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     *dot = fmaf(bf16_low(g[i]), bf16_low(x[i]), *dot);
@@ -206,15 +202,15 @@ __device__ __forceinline__ void dot_row(float* dot, const v4u& g, const v4u& x) 
 }
 
 // 8 bf16 values with zeros for the first `count` of them.
-__device__ __forceinline__ v4u without(v4u x, int count) {
+__device__ __forceinline__ u32x4 without(u32x4 x, int count) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) x[i] &= (2 * i >= count ? 0xffffu : 0u) | (2 * i + 1 >= count ? 0xffff0000u : 0u);
   return x;
 }
 
 // w times 8 bf16 values, rounded once.
-__device__ __forceinline__ v4u scaled_row(float w, const v4u& g) {
-  v4u y;
+__device__ __forceinline__ u32x4 scaled_row(float w, const u32x4& g) {
+  u32x4 y;
 #pragma unroll
   for (int i = 0; i < 4; ++i) y[i] = pack_bf16(w * bf16_low(g[i]), w * bf16_high(g[i]));
   return y;
@@ -243,11 +239,11 @@ __global__ __launch_bounds__(kCombThreads) void combine_grad_vec_kernel(
 #pragma unroll
     for (int q = 0; q < ROWS; ++q) dot[q] = 0.0f;
     for (int base = 0; base < vpr; base += kCombThreads * VPT) {
-      v4u g[VPT];
+      u32x4 g[VPT];
 #pragma unroll
       for (int u = 0; u < VPT; ++u) {
         const int c = base + threadIdx.x + u * kCombThreads;
-        g[u] = c < vpr ? *reinterpret_cast<const v4u_any*>(g_row + vector_at(c, d.H)) : v4u{0, 0, 0, 0};
+        g[u] = c < vpr ? *reinterpret_cast<const u32x4_any*>(g_row + vector_at(c, d.H)) : u32x4{0, 0, 0, 0};
       }
 #pragma unroll
       for (int q = 0; q < ROWS; ++q) {
@@ -256,18 +252,18 @@ __global__ __launch_bounds__(kCombThreads) void combine_grad_vec_kernel(
         const uint16_t* x_row = expert_out + (int64_t)p * d.H;
         uint16_t* y_row = grad_rows + (int64_t)p * d.H;
         const float w = w_s[j0 + q];
-        v4u x[VPT];
+        u32x4 x[VPT];
 #pragma unroll
         for (int u = 0; u < VPT; ++u) {
           const int c = base + threadIdx.x + u * kCombThreads;
-          const v4u_any* at = reinterpret_cast<const v4u_any*>(x_row + vector_at(c, d.H));
-          x[u] = c < vpr ? __builtin_nontemporal_load(at) : v4u{0, 0, 0, 0};
+          const u32x4_any* at = reinterpret_cast<const u32x4_any*>(x_row + vector_at(c, d.H));
+          x[u] = c < vpr ? __builtin_nontemporal_load(at) : u32x4{0, 0, 0, 0};
         }
 #pragma unroll
         for (int u = 0; u < VPT; ++u) {
           const int c = base + threadIdx.x + u * kCombThreads;
           if (c < vpr)
-            __builtin_nontemporal_store(scaled_row(w, g[u]), reinterpret_cast<v4u_any*>(y_row + vector_at(c, d.H)));
+            __builtin_nontemporal_store(scaled_row(w, g[u]), reinterpret_cast<u32x4_any*>(y_row + vector_at(c, d.H)));
           const int again = 8 * c - (d.H - 8);  // values that the vector before has counted
           if (again > 0 && c < vpr)
             dot_row(&dot[q], without(g[u], again), without(x[u], again));
@@ -330,24 +326,21 @@ __global__ __launch_bounds__(kCombThreads) void combine_narrow_kernel(Dims d, in
   for (int j = 0; j < d.k; j += kRowsInFlight) {
     int p[kRowsInFlight];
     float w[kRowsInFlight];
-    v4u x[kRowsInFlight];
+    u32x4 x[kRowsInFlight];
 #pragma unroll
     for (int q = 0; q < kRowsInFlight; ++q) p[q] = narrow_slot(d, t, j + q, weight, slot_pos, &w[q], status);
 #pragma unroll
     for (int q = 0; q < kRowsInFlight; ++q) {
-      x[q] = v4u{0, 0, 0, 0};
+      x[q] = u32x4{0, 0, 0, 0};
       if (on && p[q] >= 0)
-        x[q] = __builtin_nontemporal_load(reinterpret_cast<const v4u_any*>(expert_out + (int64_t)p[q] * d.H + at));
+        x[q] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(expert_out + (int64_t)p[q] * d.H + at));
     }
 #pragma unroll
     for (int q = 0; q < kRowsInFlight; ++q)
-      if (j + q < d.k) fma_row(acc, w[q], make_uint4(x[q].x, x[q].y, x[q].z, x[q].w));
+      if (j + q < d.k) fma_row(acc, w[q], x[q]);
   }
   if (!on) return;
-  v4u y;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) y[i] = to_bf16(acc[2 * i]) | (to_bf16(acc[2 * i + 1]) << 16);
-  *reinterpret_cast<v4u_any*>(out + t * d.H + at) = y;
+  *reinterpret_cast<u32x4_any*>(out + t * d.H + at) = rounded(acc);
 }
 
 __global__ __launch_bounds__(kCombThreads) void combine_grad_narrow_kernel(
@@ -361,25 +354,25 @@ __global__ __launch_bounds__(kCombThreads) void combine_grad_narrow_kernel(
   const bool on = 8 * lane < d.H;
   const int at = vector_at(lane, d.H);
   const int again = 8 * lane - (d.H - 8);  // values that the vector before has counted
-  v4u g = {0, 0, 0, 0};
-  if (on) g = *reinterpret_cast<const v4u_any*>(grad_out + t * d.H + at);
+  u32x4 g = {0, 0, 0, 0};
+  if (on) g = *reinterpret_cast<const u32x4_any*>(grad_out + t * d.H + at);
   for (int j = 0; j < d.k; j += kRows) {
     int p[kRows];
     float w[kRows];
-    v4u x[kRows];
+    u32x4 x[kRows];
 #pragma unroll
     for (int q = 0; q < kRows; ++q) p[q] = narrow_slot(d, t, j + q, weight, slot_pos, &w[q], status);
 #pragma unroll
     for (int q = 0; q < kRows; ++q) {
-      x[q] = v4u{0, 0, 0, 0};
+      x[q] = u32x4{0, 0, 0, 0};
       if (on && p[q] >= 0)
-        x[q] = __builtin_nontemporal_load(reinterpret_cast<const v4u_any*>(expert_out + (int64_t)p[q] * d.H + at));
+        x[q] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(expert_out + (int64_t)p[q] * d.H + at));
     }
 #pragma unroll
     for (int q = 0; q < kRows; ++q) {
       if (on && p[q] >= 0)
         __builtin_nontemporal_store(scaled_row(w[q], g),
-                                    reinterpret_cast<v4u_any*>(grad_rows + (int64_t)p[q] * d.H + at));
+                                    reinterpret_cast<u32x4_any*>(grad_rows + (int64_t)p[q] * d.H + at));
       float dot = 0.0f;
       if (on && p[q] >= 0) dot_row(&dot, without(g, again), without(x[q], again));
       for (int off = P / 2; off >= 1; off >>= 1) dot += __shfl_xor(dot, off);
@@ -405,7 +398,7 @@ __global__ __launch_bounds__(kCombThreads) void combine_grad_u16_kernel(
       for (int c = threadIdx.x; c < d.H; c += kCombThreads) {
         const float g = bf16_low(grad_out[t * d.H + c]);
         dot = fmaf(g, bf16_low(expert_out[(int64_t)p * d.H + c]), dot);
-        grad_rows[(int64_t)p * d.H + c] = (uint16_t)to_bf16(w_s[j] * g);
+        grad_rows[(int64_t)p * d.H + c] = (uint16_t)pack_bf16(w_s[j] * g, 0.0f);
       }
     }
     const float s = wave_sum(dot);

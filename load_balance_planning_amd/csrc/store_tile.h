@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "fp8_block.h"
+#include "lane_group.h"
 
 namespace moe {
 namespace {
@@ -22,11 +23,6 @@ typedef float acc16 __attribute__((ext_vector_type(16)));
 // TI x TJ turns of 32 NI / TI columns by 32 NJ / TJ rows (2048 NI NJ / (TI TJ)
 // bytes).  16-byte place p of row R lies at p ^ (R % places): eight lanes'
 // writes, one column of eight rows, go to eight places.
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
 template <int TI, int TJ, int NI, int NJ>
 __device__ __forceinline__ void store_wave_tile(const acc16 (&acc)[NI][NJ], unsigned char* lds, uint16_t* out,
                                                 int64_t stride, int rows_left, int cols_left) {
@@ -53,7 +49,7 @@ __device__ __forceinline__ void store_wave_tile(const acc16 (&acc)[NI][NJ], unsi
         }
       }
     }
-    wave_sync();
+    wave_lds_sync();
 #pragma unroll
     for (int s = 0; s < 32 * kJ / kRowsAtOnce; ++s) {
       const int part_row = s * kRowsAtOnce + lane / kPlaces;
@@ -69,7 +65,7 @@ __device__ __forceinline__ void store_wave_tile(const acc16 (&acc)[NI][NJ], unsi
           if (col + q < cols_left) dst[q] = (uint16_t)(o[q / 2] >> (16 * (q & 1)));
       }
     }
-    if (turn + 1 < TI * TJ) wave_sync();
+    if (turn + 1 < TI * TJ) wave_lds_sync();
   }
 }
 
