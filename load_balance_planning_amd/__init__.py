@@ -565,16 +565,16 @@ class Layer:
                          _ptr(expert_out), _ptr(out), self._stream(stream))
         return out
 
-    def gate(self, logits, gate: moex_gate_config, bias=None, prev_topk=None, stream=None):
+    def gate(self, logits, gate: moex_gate_config, bias=None, prev_topk=None, stream=None, out=None):
         """Routing with scores, bias, groups and weights (moex_gate): (route_out, weight [T][k]).  The weights are the
-        call's own, route_out is the layer's and overwritten by its next gate() or route()."""
+        call's own (or in `out`), route_out is the layer's and overwritten by its next gate() or route()."""
         torch, (T, E, k, _) = self.torch, self._dims
         self._check_tensor(logits, (T, E), torch.float32)
         if bias is not None:
             self._check_tensor(bias, (E,), torch.float32)
         if prev_topk is not None:
             self._check_tensor(prev_topk, (T, k), torch.int32)
-        weight = self._empty((T, k), torch.float32, stream)
+        weight = self._result(out, (T, k), torch.float32, stream)
         moex_gate(self.handle, gate, _addr(logits), _addr(bias), _addr(prev_topk), self._route_s, _addr(weight),
                   self._stream(stream))
         return self.route_out, weight
@@ -604,7 +604,19 @@ class Layer:
         with self.torch.cuda.stream(stream):
             return self.torch.empty(*shape, dtype=dtype, device=self.device)
 
-    def _empty_blocks(self, stream, lead, cols, scale_lead=None) -> Blocks:
+    def _result(self, out, shape, dtype, stream):
+        """`out`, checked, or memory of the call's own."""
+        if out is None:
+            return self._empty(shape, dtype, stream)
+        self._check_tensor(out, shape, dtype)
+        return out
+
+    def _result_blocks(self, out, stream, lead, cols, scale_lead=None) -> Blocks:
+        if out is not None:
+            if out.cols != cols:
+                raise ValueError("out has %d columns, the result %d" % (out.cols, cols))
+            self._check_blocks(out, lead, scale_lead)
+            return out
         torch, scale_lead = self.torch, lead if scale_lead is None else scale_lead
         return Blocks(self._empty((*lead, Blocks.padded(cols)), torch.float8_e4m3fn, stream),
                       self._empty((*scale_lead, Blocks.scales(cols)), torch.float8_e8m0fnu, stream), cols)
@@ -621,48 +633,50 @@ class Layer:
         self._check_tensor(b.scale, (*(lead if scale_lead is None else scale_lead), Blocks.scales(b.cols)),
                            torch.float8_e8m0fnu)
 
-    def quantize(self, x, stream=None) -> Blocks:
-        """bf16 rows [n][cols] to Blocks of rows (moex_quantize)."""
+    def quantize(self, x, stream=None, out=None) -> Blocks:
+        """bf16 rows [n][cols] to Blocks of rows (moex_quantize), new ones or `out`."""
         if x.dim() != 2:
             raise ValueError("x must be [rows][cols]")
         rows, cols = x.shape
         self._check_16bit(x, (rows, cols), "x")
-        out = self._empty_blocks(stream, (rows,), cols)
+        out = self._result_blocks(out, stream, (rows,), cols)
         moex_quantize(self.handle, _addr(x), rows, cols, _addr(out.q), _addr(out.scale), self._stream(stream))
         return out
 
-    def quantize_weights(self, w, transposed: bool = False, stream=None):
+    def quantize_weights(self, w, transposed: bool = False, stream=None, out=None):
         """bf16 matrices [E][n][k] to Blocks of matrices (moex_quantize_weights); with transposed also those of the
-        transposed matrices [E][k][n], from the same pass."""
+        transposed matrices [E][k][n], from the same pass.  `out`: the Blocks to write (with transposed the pair), for
+        instance those that a captured graph reads, after an optimizer step."""
         if w.dim() != 3:
             raise ValueError("w must be [experts][n][k]")
         E, n, k = w.shape
         self._check_16bit(w, (E, n, k), "w")
         blocks = lambda c: -(-c // BLOCK)
-        out = self._empty_blocks(stream, (E, n), k, (E, blocks(n)))
-        out_t = self._empty_blocks(stream, (E, k), n, (E, blocks(k))) if transposed else Blocks(None, None, n)
+        out, out_t = (None, None) if out is None else out if transposed else (out, None)
+        out = self._result_blocks(out, stream, (E, n), k, (E, blocks(n)))
+        out_t = self._result_blocks(out_t, stream, (E, k), n, (E, blocks(k))) if transposed else Blocks(None, None, n)
         moex_quantize_weights(self.handle, _addr(w), E, n, k, _addr(out.q), _addr(out.scale), _addr(out_t.q),
                               _addr(out_t.scale), self._stream(stream))
         return (out, out_t) if transposed else out
 
-    def swiglu(self, y, stream=None) -> Blocks:
-        """silu(gate) * up of rows [n][2 f] (gate columns, then up), quantized (moex_swiglu)."""
+    def swiglu(self, y, stream=None, out=None) -> Blocks:
+        """silu(gate) * up of rows [n][2 f] (gate columns, then up), quantized (moex_swiglu), new Blocks or `out`."""
         if y.dim() != 2 or y.shape[1] % 2:
             raise ValueError("y must be [rows][2 f]")
         rows, f = y.shape[0], y.shape[1] // 2
         self._check_16bit(y, (rows, 2 * f), "y")
-        out = self._empty_blocks(stream, (rows,), f)
+        out = self._result_blocks(out, stream, (rows,), f)
         moex_swiglu(self.handle, _addr(y), rows, f, _addr(out.q), _addr(out.scale), self._stream(stream))
         return out
 
-    def swiglu_grad(self, y, grad, stream=None) -> Blocks:
-        """Gradient of swiglu for y from grad [n][f], quantized (moex_swiglu_grad)."""
+    def swiglu_grad(self, y, grad, stream=None, out=None) -> Blocks:
+        """Gradient of swiglu for y from grad [n][f], quantized (moex_swiglu_grad), new Blocks or `out`."""
         if y.dim() != 2 or y.shape[1] % 2:
             raise ValueError("y must be [rows][2 f]")
         rows, f = y.shape[0], y.shape[1] // 2
         self._check_16bit(y, (rows, 2 * f), "y")
         self._check_16bit(grad, (rows, f), "grad")
-        out = self._empty_blocks(stream, (rows,), 2 * f)
+        out = self._result_blocks(out, stream, (rows,), 2 * f)
         moex_swiglu_grad(self.handle, _addr(y), _addr(grad), rows, f, _addr(out.q), _addr(out.scale),
                          self._stream(stream))
         return out
@@ -736,16 +750,21 @@ class Layer:
         moex_combine(self.handle, _addr(weight), _addr(slot_pos), _addr(expert_out), _addr(out), self._stream(stream))
         return out
 
-    def combine_grad(self, expert_out, grad_out, weight, slot_pos=None, stream=None):
+    def combine_grad(self, expert_out, grad_out, weight, slot_pos=None, stream=None, out=None):
         """Gradients of combine_weighted for the expert rows and the weights (moex_combine_grad):
-        (grad_expert_out [T*k][H], grad_weight [T][k])."""
+        (grad_expert_out [T*k][H], grad_weight [T][k]), new ones or the pair `out`."""
         torch, (T, _, k, H) = self.torch, self._dims
         slot_pos = self._slot_positions(slot_pos)
         self._check_16bit(expert_out, (T * k, H), "expert_out")
         self._check_16bit(grad_out, (T, H), "grad_out")
         self._check_tensor(weight, (T, k), torch.float32)
-        grad_rows = self._empty((T * k, H), expert_out.dtype, stream)
-        grad_weight = self._empty((T, k), torch.float32, stream)
+        if out is None:
+            grad_rows = self._empty((T * k, H), expert_out.dtype, stream)
+            grad_weight = self._empty((T, k), torch.float32, stream)
+        else:
+            grad_rows, grad_weight = out
+            self._check_16bit(grad_rows, (T * k, H), "out[0]")
+            self._check_tensor(grad_weight, (T, k), torch.float32)
         moex_combine_grad(self.handle, _addr(weight), _addr(slot_pos), _addr(expert_out), _addr(grad_out),
                           _addr(grad_rows), _addr(grad_weight), self._stream(stream))
         return grad_rows, grad_weight

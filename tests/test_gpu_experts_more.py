@@ -359,3 +359,73 @@ def test_repeated_rows_end_at_the_buffer_s_rows(mp, rows, n, k):
     for e in range(E):
         assert torch.equal(got[e], want), e
     layer.close()
+
+
+def test_results_into_given_memory(mp):
+    """Every call that returns new memory writes the same bytes into `out`, and refuses one of another shape or type."""
+    T, E, k, H, n = 48, 6, 2, 264, 136
+    layer = mp.Layer(mp.make_config(T, E, k, 1, 1, H, 0), cooc=False)
+    dev = layer.device
+    g = torch.Generator().manual_seed(8)
+    rnd = lambda *s: torch.randn(*s, generator=g).to(dev)
+    x, w, lg, gw = rnd(T * k, H).to(BF), rnd(E, n, H).to(BF), rnd(T, E), rnd(T, k)
+    pos = torch.randperm(T * k, generator=g).int().to(dev)
+    router = mp.make_gate("softmax")
+    half, grad = x[:, : H // 2].contiguous(), rnd(T, H).to(BF)
+
+    def flat(r):
+        if isinstance(r, mp.Blocks):
+            return [r.q, r.scale]
+        return [t for part in r for t in flat(part)] if isinstance(r, tuple) else [r]
+
+    calls = (lambda **o: layer.quantize(x, **o), lambda **o: layer.quantize_weights(w, **o),
+             lambda **o: layer.quantize_weights(w, transposed=True, **o), lambda **o: layer.swiglu(x, **o),
+             lambda **o: layer.swiglu_grad(x, half, **o), lambda **o: layer.gate(lg, router, **o)[1],
+             lambda **o: layer.combine_grad(x, grad, gw, slot_pos=pos, **o))
+    for i, call in enumerate(calls):
+        want, out = call(), call()
+        for t in flat(out):
+            t.view(torch.uint8).fill_(0x55)
+        got = call(out=out)
+        assert all(a is b for a, b in zip(flat(got), flat(out))), i
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(flat(got), flat(want))), i
+    blocks_ = layer.quantize(x)
+    for bad in (lambda: layer.quantize(x[:-1].contiguous(), out=blocks_), lambda: layer.quantize(half, out=blocks_),
+                lambda: layer.quantize(x, out=mp.Blocks(blocks_.q, blocks_.scale, H + 1)),
+                lambda: layer.swiglu(x, out=blocks_), lambda: layer.swiglu_grad(x, half, out=layer.quantize(half)),
+                lambda: layer.quantize_weights(w, out=blocks_), lambda: layer.gate(lg, router, out=gw[:-1].contiguous()),
+                lambda: layer.combine_grad(x, grad, gw, slot_pos=pos, out=(x[:-1].contiguous(), gw))):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: layer.gate(lg, router, out=gw.double()),
+                lambda: layer.quantize(x, out=mp.Blocks(blocks_.q.view(torch.uint8), blocks_.scale, H)),
+                lambda: layer.combine_grad(x, grad, gw, slot_pos=pos, out=(x.to(torch.float16), gw))):
+        with pytest.raises(TypeError):
+            bad()
+    assert layer.status() == 0
+    layer.close()
+
+
+def test_a_graph_sees_matrices_quantized_in_place(mp):
+    """A captured product, and matrices that an optimizer step changed, quantized into the Blocks that it reads."""
+    E, n, k, rows = 4, 136, 264, 64
+    layer = mp.Layer(mp.make_config(rows, E, 1, 1, 1, 8, 0), cooc=False)
+    dev = layer.device
+    kw = one_instance_each(mp, layer, [20, 0, 40, 4])
+    g = torch.Generator().manual_seed(9)
+    rnd = lambda *s: torch.randn(*s, generator=g).to(BF).to(dev)
+    x, d = layer.quantize(rnd(rows, k)), layer.quantize(rnd(rows, n))
+    pair = layer.quantize_weights(rnd(E, n, k), transposed=True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, dx = layer.matmul(x, pair[0], **kw), layer.matmul(d, pair[1], **kw)
+    for _ in range(4):
+        w = rnd(E, n, k)
+        layer.quantize_weights(w, transposed=True, out=pair)
+        graph.replay()
+        torch.cuda.synchronize()
+        new = layer.quantize_weights(w, transposed=True)
+        assert torch.equal(y, layer.matmul(x, new[0], **kw)) and torch.equal(dx, layer.matmul(d, new[1], **kw))
+    assert layer.status() == 0
+    layer.close()
