@@ -207,7 +207,7 @@ int moex_combine(moe_plan_t h, const float* weight, const int32_t* slot_pos, con
  *   grad_expert_out[slot_pos[t*k+j]][:] = bf16( weight[t][j] * grad_out[t][:] )
  *   grad_weight[t][j] = sum of grad_out[t][:] * expert_out[slot_pos[t*k+j]][:]  (fp32)
  * grad_expert_out uint16 [T*k][H] (every row that a slot points to is
- * written; it may not overlap expert_out); grad_weight float [T][k].  Each
+ * written; it may not overlap expert_out or grad_out); grad_weight float [T][k].  Each
  * slot has a row of its own, as moe_plan_dispatch gives it (of slots that share
  * one, one's gradient is left in it, whichever).  A position outside [0, T*k)
  * sets MOE_STATUS_PLAN_CHECK; its weight gradient is 0.

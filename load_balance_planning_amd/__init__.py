@@ -604,6 +604,13 @@ class Layer:
         with self.torch.cuda.stream(stream):
             return self.torch.empty(*shape, dtype=dtype, device=self.device)
 
+    @staticmethod
+    def _check_apart(out, t):
+        """Rows that a kernel still reads may not be the ones it writes (contiguous tensors)."""
+        a, b = out.data_ptr(), t.data_ptr()
+        if a < b + t.numel() * t.element_size() and b < a + out.numel() * out.element_size():
+            raise ValueError("out overlaps the rows that the call reads")
+
     def _result(self, out, shape, dtype, stream):
         """`out`, checked, or memory of the call's own."""
         if out is None:
@@ -747,6 +754,7 @@ class Layer:
             out = self._empty((T, H), expert_out.dtype, stream)
         else:
             self._check_16bit(out, (T, H), "out")
+            self._check_apart(out, expert_out)
         moex_combine(self.handle, _addr(weight), _addr(slot_pos), _addr(expert_out), _addr(out), self._stream(stream))
         return out
 
@@ -765,6 +773,8 @@ class Layer:
             grad_rows, grad_weight = out
             self._check_16bit(grad_rows, (T * k, H), "out[0]")
             self._check_tensor(grad_weight, (T, k), torch.float32)
+            self._check_apart(grad_rows, expert_out)
+            self._check_apart(grad_rows, grad_out)
         moex_combine_grad(self.handle, _addr(weight), _addr(slot_pos), _addr(expert_out), _addr(grad_out),
                           _addr(grad_rows), _addr(grad_weight), self._stream(stream))
         return grad_rows, grad_weight

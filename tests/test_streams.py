@@ -1,4 +1,4 @@
-"""Which stream the calls of a Layer go to."""
+"""Checks of a Layer before its calls: which stream they go to, and results that overlap what is read."""
 from __future__ import annotations
 
 from types import SimpleNamespace
@@ -65,5 +65,42 @@ def test_an_external_stream_is_taken():
     b = layer.quantize(x, stream=torch.cuda.ExternalStream(side.cuda_stream))
     side.synchronize()
     assert (b.q[:, :8].float() * 2.0 ** (b.scale.view(torch.uint8)[:, :1].float() - 127) == 1).all()
+    assert layer.status() == 0
+    layer.close()
+
+
+def test_results_over_the_rows_that_are_read_are_refused():
+    import load_balance_planning_amd as mp
+    rows = torch.zeros(8, 4, dtype=torch.bfloat16)
+    for out, fine in ((rows, False), (rows[7:], False), (rows[:1], False), (torch.zeros(8, 4), True)):
+        if fine:
+            mp.Layer._check_apart(out, rows)
+        else:
+            with pytest.raises(ValueError):
+                mp.Layer._check_apart(out, rows)
+    mp.Layer._check_apart(rows[4:], rows[:4])
+    mp.Layer._check_apart(rows[:4], rows[4:])
+
+
+@pytest.mark.gpu
+def test_combines_refuse_results_over_their_rows():
+    if not torch.cuda.is_available():
+        pytest.skip("no HIP device")
+    import load_balance_planning_amd as mp
+    T, k, H = 8, 2, 16
+    layer = mp.Layer(mp.make_config(T, 4, k, 1, 1, H, 0), cooc=False)
+    buf = torch.ones(2 * T * k, H, dtype=torch.bfloat16, device=layer.device)
+    rows, w = buf[: T * k], torch.ones(T, k, device=layer.device)
+    pos = torch.arange(T * k, dtype=torch.int32, device=layer.device)
+    g = torch.ones(T, H, dtype=torch.bfloat16, device=layer.device)
+    with pytest.raises(ValueError):
+        layer.combine_weighted(rows, w, slot_pos=pos, out=rows[T:])
+    for out in (rows, buf[T: T + T * k]):
+        with pytest.raises(ValueError):
+            layer.combine_grad(rows, g, w, slot_pos=pos, out=(out, w.clone()))
+    with pytest.raises(ValueError):
+        layer.combine_grad(rows, buf[T * k + 3: T * k + 3 + T], w, slot_pos=pos, out=(buf[T * k:], w.clone()))
+    assert (layer.combine_weighted(rows, w, slot_pos=pos, out=buf[T * k: T * k + T]) == 2).all()
+    assert (layer.combine_grad(rows, g, w, slot_pos=pos, out=(buf[T * k:], w.clone()))[0] == 1).all()
     assert layer.status() == 0
     layer.close()
