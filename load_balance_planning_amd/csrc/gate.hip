@@ -53,10 +53,13 @@ __device__ __forceinline__ F group_sum(F v) {
 }
 
 // Score of a logit; m and inv are the row's maximum and 1 / sum of exp(x - m)
-// (softmax).  -infinity scores 0 in either form.
+// (softmax).  -infinity scores 0 in either form.  Far below zero a sigmoid is
+// exp(x) to within fp32, where exp(-x) would leave it (at -89).
 __device__ __forceinline__ float score32(bool softmax, float x, float m, float inv) {
   if (x == -INFINITY) return 0.0f;
-  return softmax ? expf(x - m) * inv : 1.0f / (1.0f + expf(-x));
+  const bool far = x < -80.0f;
+  const float e = expf(softmax ? x - m : far ? x : -x);
+  return softmax ? e * inv : far ? e : 1.0f / (1.0f + e);
 }
 __device__ __forceinline__ double score64(bool softmax, float x, float m, double sum) {
   if (x == -INFINITY) return 0.0;

@@ -231,3 +231,31 @@ def test_the_largest_scale(mp, kind):
             assert e.value.code == mp.MOE_ERR_INVALID_ARG
     assert layer.status() == 0
     layer.close()
+
+
+@pytest.mark.parametrize("cooc", [True, False])
+def test_sigmoid_far_below_zero(mp, cooc):
+    """Scores down to fp32's smallest, alone in their row: weights of s / (s + 1e-20), and their gradients."""
+    T, E = 32, 8
+    x = torch.linspace(-104, -60, T * E).view(T, E)
+    for k in (1, 3):
+        check(mp, x, None, k, "sigmoid", cooc=cooc)
+        layer = mp.Layer(mp.make_config(T, E, k, 1, 1, 8, 0), cooc=cooc)
+        for renorm in (True, False):
+            gate, xd = mp.make_gate("sigmoid", renorm=renorm, scale=2.5), x.to(layer.device)
+            r, w = layer.gate(xd, gate)
+            gw = torch.randn(T, k, generator=torch.Generator().manual_seed(k))
+            got = layer.gate_grad(xd, gate, gw.to(layer.device)).cpu().double()
+            idx, x64 = r.topk_idx.cpu().long(), x.double().requires_grad_()
+            want, = torch.autograd.grad(refs.gate_weights(x64, idx, "sigmoid", renorm, 2.5), x64, gw.double())
+            # the share of the magnitudes that are added, and half of 2^-149 for each score that goes in
+            s = refs.scores(x.double(), "sigmoid").gather(1, idx)
+            size = 2.5 * gw.double().abs()
+            if renorm:
+                S = s.sum(-1, keepdim=True) + 1e-20
+                size = 2.5 / S * (gw.double().abs() + (gw.double().abs() * s).sum(-1, keepdim=True) / S)
+            bound = torch.zeros(T, E, dtype=torch.float64).scatter(
+                1, idx, size * (s * (2 * k + 432) * 2.0 ** -24 + (k + 1) * 2.0 ** -149)) + 2.0 ** -149
+            assert ((got - want).abs() <= bound).all()
+        assert layer.status() == 0
+        layer.close()
