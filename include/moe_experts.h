@@ -142,8 +142,9 @@ int moex_quantize_weights(moe_plan_t h, const uint16_t* w, int32_t experts, int3
 
 /*
  * y bf16 [rows][2 f]: gate columns, then up columns.  a = y_gate * sigmoid(y_gate)
- * * y_up in fp32, quantized as a row of f columns.  rows and f as rows and cols
- * of moex_quantize.
+ * * y_up in fp32, quantized as a row of f columns.  (A sigmoid below 2^-128,
+ * that of a gate below -88.7, counts as 0; in the gradient too.)  rows and f as
+ * rows and cols of moex_quantize.
  */
 int moex_swiglu(moe_plan_t h, const uint16_t* y, int64_t rows, int32_t f, uint8_t* q, uint8_t* scale, void* stream);
 

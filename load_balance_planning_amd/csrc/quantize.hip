@@ -96,6 +96,8 @@ __device__ __forceinline__ void store_block(const float* f, uint8_t* __restrict_
   if (lane8 <= pad_scales) scale[lane8] = lane8 == 0 ? (uint8_t)s : (uint8_t)127;
 }
 
+// 0 below x = -88.7, where exp(-x) leaves fp32.  exp(x) instead would keep values
+// below 2^-128 and costs 5 % (131072 rows of f = 768: 112 -> 118 us).
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 __device__ __forceinline__ float swiglu(float g, float u) { return g * sigmoid(g) * u; }
 // KIND kPlain: x [rows][cols].  kSwiglu: x [rows][2 cols] (gate, up), cols = f.

@@ -429,3 +429,33 @@ def test_a_graph_sees_matrices_quantized_in_place(mp):
         assert torch.equal(y, layer.matmul(x, new[0], **kw)) and torch.equal(dx, layer.matmul(d, new[1], **kw))
     assert layer.status() == 0
     layer.close()
+
+
+@pytest.mark.parametrize("f", [128, 200])
+def test_gates_far_below_zero(mp, f):
+    """Blocks whose gates are all far below zero, down to where fp32 ends.  expf and its argument are good to 2 + |x|
+    units, so a value is off by 2^-17 of itself; a sigmoid below 2^-128 counts as 0, which takes up to 2^-128 of what it
+    is multiplied by; then e4m3's half step."""
+    rows = 24
+    g = torch.Generator().manual_seed(f)
+    y = torch.randn(rows, 2 * f, generator=g)
+    y[:, :f] = -torch.linspace(78, 99, rows)[:, None] - 0.3 * torch.rand(rows, f, generator=g)
+    y, da = y.to(BF), torch.randn(rows, f, generator=g).to(BF)
+    layer = mp.Layer(mp.make_config(8, 8, 1, 1, 1, 8, 0), cooc=False)
+    dev = layer.device
+    y64 = y.double().requires_grad_()
+    act = refs.swiglu(y64)
+    grad, = torch.autograd.grad(act, y64, da.double())
+    gate, up, d = y.double()[:, :f].abs(), y.double()[:, f:].abs(), da.double().abs()
+    for got, want, size, c in ((layer.swiglu(y.to(dev)), act.detach(), gate * up, f),
+                               (layer.swiglu_grad(y.to(dev), da.to(dev)), grad,
+                                torch.cat([d * up * (1 + gate), d * gate], 1), 2 * f)):
+        scale = (got.scale.view(torch.uint8).cpu().double()[:, : refs.pad(c) // 128] - 127).exp2().repeat_interleave(128, -1)[:, :c]
+        off = 2.0 ** -17 * want.abs() + 2.0 ** -128 * size + 2.0 ** -148
+        half = torch.maximum(2.0 ** -4 * (want.abs() + off), 2.0 ** -10 * scale)
+        assert ((refs.values(got, rows) - want).abs() <= off + half).all()
+        # the block's scale is no larger than its largest value needs, or 1 where all are 0
+        top, zero = refs.block_max(want.abs() + off), refs.block_max(refs.values(got, rows)) == 0
+        assert ((scale[:, ::128] <= torch.exp2(refs.block_exponent(top).double())) | (zero & (scale[:, ::128] == 1))).all()
+    assert layer.status() == 0
+    layer.close()
