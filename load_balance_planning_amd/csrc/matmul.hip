@@ -123,8 +123,8 @@ __global__ __launch_bounds__(256) void matmul_rows16_kernel(Instances in, const 
 //
 // The wave tile decides what LDS has to deliver: 128 x 64 tiles of eight waves
 // read 192 KB a step and 64 KB are written, at 128 bytes a cycle as long as
-// the products themselves take (2048 cycles; the kernel ran at 40 % of the
-// matrix unit's rate), 128 x 128 tiles of four waves read 128 KB.
+// the products themselves take (2048 cycles), 128 x 128 tiles of four waves read
+// 128 KB.
 //
 // LDS rows are 128 bytes, eight 16-byte pieces.  A direct load writes its
 // lanes' pieces one after the other, so the placement is chosen on the memory
@@ -296,9 +296,8 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), BC == 256 ? 
   // Block b's lines into the XCD's L2, a quarter of them per workgroup: those that
   // share an operand take the others.  The workgroups of an XCD ask for a block's
   // lines at about the same time, so without this all of them wait for memory
-  // (32768 rows, 32 experts of 5376 x 7168: 3200 cycles a block, and 2400 so; of
-  // 2048 x 1536, 131072 rows: 4100 and 2700; the clock falls with the load, and the
-  // times by less, 1263 -> 1236 us and 553 -> 524).  The bytes read go nowhere.
+  // (32768 rows, 32 experts of 5376 x 7168: 1263 -> 1236 us; of 2048 x 1536, 131072
+  // rows: 553 -> 524).  The bytes read go nowhere.
   auto fetch = [&](int b) {
     if (!kFetch) return;
     asm volatile("" ::: "memory");  // behind the block loads before it

@@ -8,8 +8,8 @@
 // in a lane, memory has columns next to each other: LDS holds the values as
 // they come, rows of 256 columns, and the transposing LDS read hands every 16
 // lanes four rows of 16 columns, a column to a lane.  (Transposing in registers
-// on the way into LDS took twice the vector instructions: 1.14 against
-// 1.38 PFLOP/s on one dense 8192 cubed.)
+// on the way into LDS took twice the vector instructions, and a fifth longer on
+// one dense 8192 cubed.)
 //
 // 256 x 256 of dw[e] per workgroup of four waves, 128 x 128 each, in steps of
 // 64 rows: 2048 cycles of products, and some 4 other instructions to a product
