@@ -21,7 +21,8 @@
 // hundred), the token's lanes evaluate only those candidates, or the group
 // values, in 64 bits.  Where there are more candidates (long ties: a row of
 // equal or of masked logits), the token takes rounds of a maximum, first over
-// the fp32 choices, and over 64-bit ones if two picks lie too close.
+// the fp32 choices, and over 64-bit ones if two picks, or the last pick and an
+// expert left over, lie too close.
 #include <math.h>
 
 #include "experts.h"
