@@ -259,3 +259,71 @@ def test_sigmoid_far_below_zero(mp, cooc):
             assert ((got - want).abs() <= bound).all()
         assert layer.status() == 0
         layer.close()
+
+
+@pytest.mark.parametrize("T,E,k,groups", FEW)
+def test_few_tokens_captured(mp, T, E, k, groups):
+    """The router of one workgroup and its gradient in a graph: every replay equals the eager call on new inputs, with
+    eager work between the replays."""
+    layer, other = (mp.Layer(mp.make_config(T, E, k, 1, 1, 8, 0), cooc=False) for _ in range(2))
+    dev, g = layer.device, torch.Generator().manual_seed(E + T)
+    gate, bias = mp.make_gate("sigmoid", *groups, True, 2.5), (0.1 * torch.randn(E, generator=g)).to(dev)
+    x, gw = torch.randn(T, E, generator=g).to(dev), torch.randn(T, k, generator=g).to(dev)
+    layer.gate(x, gate, bias=bias)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r, w = layer.gate(x, gate, bias=bias)
+        dx = layer.gate_grad(x, gate, gw)
+    for _ in range(4):
+        x.copy_(torch.randn(T, E, generator=g))
+        for t in (w, dx, r.topk_idx, r.omega, r.expert_count):
+            t.fill_(-3)
+        graph.replay()
+        torch.cuda.synchronize()
+        r2, w2 = other.gate(x, gate, bias=bias)
+        assert torch.equal(r.topk_idx, r2.topk_idx) and torch.equal(w, w2) and torch.equal(dx, other.gate_grad(x, gate, gw))
+        assert torch.equal(r.omega, r2.omega) and torch.equal(r.expert_count, r2.expert_count)
+    assert layer.status() == 0 and other.status() == 0
+    layer.close()
+    other.close()
+
+
+def test_the_most_tokens(mp):
+    """Just below 2^22 tokens, the most a layer takes: router, gradient, weighted sum and its gradient, sampled."""
+    T, E, k, H = (1 << 22) - 2, 8, 2, 8
+    layer = mp.Layer(mp.make_config(T, E, k, 1, 1, H, 0), cooc=False)
+    dev = layer.device
+    g = torch.Generator(device=dev).manual_seed(6)
+    rnd = lambda *s: torch.randn(*s, generator=g, device=dev)
+    x, gate, gw = rnd(T, E), mp.make_gate("softmax", 4, 2, 1, True, 1.0), rnd(T, k)
+    r, w = layer.gate(x, gate)
+    dx = layer.gate_grad(x, gate, gw)
+    pos = torch.randperm(T * k, generator=g, device=dev).int()
+    rows, grad = rnd(T * k, H).bfloat16(), rnd(T, H).bfloat16()
+    out = layer.combine_weighted(rows, w, slot_pos=pos)
+    drows, dw = layer.combine_grad(rows, grad, w, slot_pos=pos)
+    assert layer.status() == 0
+    assert torch.equal(r.expert_count, torch.bincount(r.topk_idx.flatten(), minlength=E).int())
+    at = torch.cat([torch.arange(300), torch.arange(T - 300, T), torch.randint(0, T, (300,), generator=torch.Generator().manual_seed(1))])
+    xs, ws, gs = x[at.to(dev)].cpu(), w[at.to(dev)].cpu().double(), gw[at.to(dev)].cpu().double()
+    idx = refs.select(xs.double(), None, "softmax", k, 4, 2, 1)
+    assert torch.equal(r.topk_idx[at.to(dev)].cpu().long(), idx)
+    share = (E / 8 + 2 * k + 432) * 2.0 ** -24
+    want = refs.gate_weights(xs.double(), idx, "softmax", True, 1.0)
+    assert ((ws - want).abs() <= share * want).all()
+    x64 = xs.double().requires_grad_()
+    want, = torch.autograd.grad(refs.gate_weights(x64, idx, "softmax", True, 1.0), x64, gs)
+    # what is added, s_e (ds_e + sum s ds): each s ds is at most (|g| + sum |g| s / S) s / S, together 2 sum |g|, and so
+    # is s_e ds_e: 4 sum |g| at most
+    assert ((dx[at.to(dev)].cpu().double() - want).abs() <= share * 4 * gs.abs().sum(-1, keepdim=True)).all()
+    p = pos.view(T, k)[at.to(dev)].long()
+    xr, gr = rows[p].cpu().double(), grad[at.to(dev)].cpu().double()
+    want = (ws[..., None] * xr).sum(1)
+    assert ((out[at.to(dev)].cpu().double() - want).abs()
+            <= 2.0 ** -8 * want.abs() + 2 * k * 2.0 ** -24 * (ws[..., None] * xr).abs().sum(1)).all()
+    want = ws[..., None] * gr[:, None]
+    assert ((drows[p].cpu().double() - want).abs() <= (2.0 ** -8 + 2.0 ** -23) * want.abs()).all()
+    want = (gr[:, None] * xr).sum(-1)
+    assert ((dw[at.to(dev)].cpu().double() - want).abs() <= 2 * H * 2.0 ** -24 * (gr[:, None] * xr).abs().sum(-1)).all()
+    layer.close()
