@@ -167,13 +167,13 @@ int moex_swiglu_grad(moe_plan_t h, const uint16_t* y, const uint16_t* grad, int6
  * experts; y: uint16 [T*k][n] bf16.  Sums in fp32 by the matrix instruction,
  * rounded once.  (Within each eight consecutive j it cuts products off below
  * 2^-13 of the largest 2^(exponent of x + exponent of w) of the eight; scales
- * do not matter to that.)  For the input gradient, x is the quantized output gradient [T*k][n]
- * and w the transposed matrices.  An n_inst outside [0, E+B], offsets that
- * fall or leave [0, T*k], or an expert outside [0, E) set
- * MOE_STATUS_PLAN_CHECK; rows of such an instance, and rows of no instance,
- * are left as they were (with a bad offset, rows of other instances may be
- * too).  1 <= n, k; MOE_ERR_UNSUPPORTED above 2^20, and for 2^24 tiles of the
- * result or more (of at least 128 x 128 each; moex_wgrad too).
+ * do not matter to that.)  For the input gradient, x is the quantized output
+ * gradient [T*k][n] and w the transposed matrices.  An n_inst outside [0, E+B],
+ * offsets that fall or leave [0, T*k], or an expert outside [0, E) set
+ * MOE_STATUS_PLAN_CHECK; rows of such an instance, and rows of no instance, are
+ * left as they were (with a bad offset, rows of other instances may be too).  1
+ * <= n, k; MOE_ERR_UNSUPPORTED above 2^20, and for 2^24 tiles of the result or
+ * more (of at least 128 x 128 each; moex_wgrad too).
  */
 int moex_matmul(moe_plan_t h, const moe_plan_out* plan, const int32_t* inst_offset, const uint8_t* x,
                 const uint8_t* x_scale, const uint8_t* w, const uint8_t* w_scale, int32_t n, int32_t k, uint16_t* y,
