@@ -15,6 +15,7 @@
 // transposes its bytes in registers and the block's in LDS.
 #include "experts.h"
 #include "fp8_block.h"
+#include "row_load.h"
 
 namespace moe {
 namespace {
@@ -34,51 +35,6 @@ __device__ __forceinline__ uint32_t max_of_8(uint32_t v) {
   return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, false));
 }
 
-// Eight bf16 values from element `at` of a tensor.
-__device__ __forceinline__ u32x4 load8(const uint16_t* __restrict__ x, int64_t at) {
-  return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(x + at));
-}
-// Those of a load that would leave the tensor's `total` elements, one by one;
-// zeros outside.
-__device__ __forceinline__ u32x4 load8_edge(const uint16_t* __restrict__ x, int64_t at, int64_t total) {
-  uint64_t half[2] = {0ull, 0ull};
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll 1
-    for (int j = 0; j < 4; ++j)
-      if (at + 4 * h + j >= 0 && at + 4 * h + j < total) half[h] |= (uint64_t)x[at + 4 * h + j] << (16 * j);
-  return u32x4{(uint32_t)half[0], (uint32_t)(half[0] >> 32), (uint32_t)half[1], (uint32_t)(half[1] >> 32)};
-}
-__device__ __forceinline__ u32x4 load8(const uint16_t* __restrict__ x, int64_t at, int64_t total) {
-  return at >= 0 && at + 8 <= total ? load8(x, at) : load8_edge(x, at, total);
-}
-__device__ __forceinline__ void widen8(const u32x4& w, float* f) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    f[2 * j] = bf16_low(w[j]);
-    f[2 * j + 1] = bf16_high(w[j]);
-  }
-}
-__device__ __forceinline__ void load16(const uint16_t* __restrict__ x, int64_t at, float* f) {
-  const u32x4 lo = load8(x, at), hi = load8(x, at + 8);
-  widen8(lo, f);
-  widen8(hi, f + 8);
-}
-// The 16 values from element `at` on, `left` of them of the row (what follows is
-// the next row's): zeros behind those.
-__device__ __forceinline__ void load16(const uint16_t* __restrict__ x, int64_t at, int left, int64_t total, float* f) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    u32x4 w = {0u, 0u, 0u, 0u};
-    if (8 * h < left) w = load8(x, at + 8 * h, total);
-    widen8(w, f + 8 * h);
-  }
-  if (left < 16) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) f[j] = j < left ? f[j] : 0.0f;
-  }
-}
-
 // Quantizes the 16 values of each of a block's lanes and stores them.
 __device__ __forceinline__ void store_block(const float* f, uint8_t* __restrict__ q, uint8_t* __restrict__ scale,
                                             int lane8, int pad_scales) {
@@ -96,10 +52,6 @@ __device__ __forceinline__ void store_block(const float* f, uint8_t* __restrict_
   if (lane8 <= pad_scales) scale[lane8] = lane8 == 0 ? (uint8_t)s : (uint8_t)127;
 }
 
-// 0 below x = -88.7, where exp(-x) leaves fp32.  exp(x) instead would keep values
-// below 2^-128 and costs 5 % (131072 rows of f = 768: 112 -> 118 us).
-__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
-__device__ __forceinline__ float swiglu(float g, float u) { return g * sigmoid(g) * u; }
 // KIND kPlain: x [rows][cols].  kSwiglu: x [rows][2 cols] (gate, up), cols = f.
 // kSwigluGrad: x [rows][cols] (gate, up) and grad [rows][cols / 2], cols = 2 f.
 // A block of 128 output columns per eight lanes.  Rows of any width are read 16
