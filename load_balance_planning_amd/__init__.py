@@ -1,8 +1,8 @@
 """MI355X-native expert-parallel dispatch planning for MoE layers.
 
-A thin ctypes binding of the C ABI in include/moe_plan.h and
-include/moe_experts.h (library load_balance_planning_amd/libmoe_plan.so, HIP
-kernels for gfx950).  The
+A thin ctypes binding of the C ABI in include/moe_plan.h, include/moe_experts.h
+and include/moe_experts4.h (library load_balance_planning_amd/libmoe_plan.so,
+HIP kernels for gfx950).  The
 functions named like the C entry points only marshal arguments; every step of
 the path runs in the library's kernels.  `Layer` is a convenience wrapper that
 allocates the caller-owned buffers as torch tensors on the current HIP device
@@ -99,6 +99,9 @@ class moex_gate_config(ctypes.Structure):
 MOEX_SOFTMAX = 0
 MOEX_SIGMOID = 1
 BLOCK = 128  # columns (and, for matrices, rows) under one scale
+BLOCK4 = 32  # columns under one scale, in 4 bits
+LINE4 = 256  # what rows in 4 bits are padded to
+FEW_TOKENS = 64  # the most that Layer.experts takes
 
 EXPORTS = ("moe_plan_query", "moe_plan_create", "moe_plan_route", "moe_plan_hist", "moe_plan_plan",
            "moe_plan_dispatch", "moe_plan_step", "moe_plan_step_static", "moe_plan_combine", "moe_plan_place", "moe_plan_dedup_count",
@@ -109,6 +112,9 @@ EXPORTS = ("moe_plan_query", "moe_plan_create", "moe_plan_route", "moe_plan_hist
 # include/moe_experts.h
 EXPERT_EXPORTS = ("moex_gate", "moex_gate_grad", "moex_quantize", "moex_quantize_weights", "moex_swiglu",
                   "moex_swiglu_grad", "moex_matmul", "moex_wgrad", "moex_combine", "moex_combine_grad")
+# include/moe_experts4.h
+EXPERT4_EXPORTS = ("moex4_quantize", "moex4_quantize_weights", "moex4_values", "moex4_swiglu", "moex4_matmul",
+                   "moex4_experts")
 
 _LIB = None
 
@@ -160,7 +166,13 @@ def lib():
         l.moex_wgrad.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, vp, vp]
         l.moex_combine.argtypes = [vp] * 6
         l.moex_combine_grad.argtypes = [vp] * 8
-        for n in EXPORTS[:-1] + EXPERT_EXPORTS:
+        l.moex4_quantize.argtypes = [vp, vp, i64, i32, vp, vp, vp]
+        l.moex4_quantize_weights.argtypes = [vp, vp, i32, i32, i32, vp, vp, vp, vp, vp]
+        l.moex4_values.argtypes = [vp, vp, vp, i32, i64, i32, vp, vp]
+        l.moex4_swiglu.argtypes = [vp, vp, i64, i32, vp, vp, vp]
+        l.moex4_matmul.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, i32, i32, vp, vp]
+        l.moex4_experts.argtypes = [vp, vp, vp, vp, i32, i32] + [vp] * 8
+        for n in EXPORTS[:-1] + EXPERT_EXPORTS + EXPERT4_EXPORTS:
             getattr(l, n).restype = ctypes.c_int
         _LIB = l
     return _LIB
@@ -303,6 +315,35 @@ def moex_combine_grad(h, weight: int, slot_pos: int, expert_out: int, grad_out: 
                       grad_weight: int, stream: int):
     _check("moex_combine_grad", lib().moex_combine_grad(h, weight, slot_pos, expert_out, grad_out, grad_expert_out,
                                                         grad_weight, stream))
+
+
+def moex4_quantize(h, x: int, rows: int, cols: int, q: int, scale: int, stream: int):
+    _check("moex4_quantize", lib().moex4_quantize(h, x, rows, cols, q, scale, stream))
+
+
+def moex4_quantize_weights(h, w: int, experts: int, n: int, k: int, q: int, scale: int, qt, scale_t, stream: int):
+    _check("moex4_quantize_weights",
+           lib().moex4_quantize_weights(h, w, experts, n, k, q, scale, qt, scale_t, stream))
+
+
+def moex4_values(h, q: int, scale: int, matrices: int, rows: int, cols: int, x: int, stream: int):
+    _check("moex4_values", lib().moex4_values(h, q, scale, matrices, rows, cols, x, stream))
+
+
+def moex4_swiglu(h, y: int, rows: int, f: int, q: int, scale: int, stream: int):
+    _check("moex4_swiglu", lib().moex4_swiglu(h, y, rows, f, q, scale, stream))
+
+
+def moex4_matmul(h, plan: moe_plan_out, inst_offset: int, x_bits: int, x: int, x_scale: int, w: int, w_scale: int,
+                 n: int, k: int, y: int, stream: int):
+    _check("moex4_matmul", lib().moex4_matmul(h, ctypes.byref(plan), inst_offset, x_bits, x, x_scale, w, w_scale, n, k,
+                                              y, stream))
+
+
+def moex4_experts(h, hidden: int, topk_idx: int, weight: int, w_bits: int, f: int, w1: int, w1_scale: int, w2: int,
+                  w2_scale: int, act: int, act_scale: int, out: int, stream: int):
+    _check("moex4_experts", lib().moex4_experts(h, hidden, topk_idx, weight, w_bits, f, w1, w1_scale, w2, w2_scale, act,
+                                                act_scale, out, stream))
 
 
 def moe_plan_set_events(h, gather_begin, gather_end):
@@ -452,6 +493,26 @@ class Blocks:
         return -(-(-(-cols // BLOCK)) // 4) * 4
 
 
+@dataclass
+class Blocks4:
+    """Rows or matrices in 4 bits (include/moe_experts4.h): q float4_e2m1fn_x2 [..., cols padded to 256, / 2], two
+    values to a byte; scale float8_e8m0fnu [..., cols padded to 256, / 256][rows][8], one per 1 x 32: the eight of a
+    row's 256 columns, row by row."""
+    q: object
+    scale: object
+    cols: int
+
+    @staticmethod
+    def padded(cols: int) -> int:
+        return -(-cols // LINE4) * LINE4
+
+    @staticmethod
+    def shapes(lead, cols: int):
+        """Shapes of q and scale of rows (lead (rows,)) or matrices (lead (experts, rows))."""
+        lines = -(-cols // LINE4)
+        return (*lead, lines * (LINE4 // 2)), (*lead[:-1], lines, lead[-1], LINE4 // BLOCK4)
+
+
 class Layer:
     """One MoE layer's planner: a handle plus torch-allocated output buffers.
 
@@ -474,7 +535,7 @@ class Layer:
         self._index = self.device.index
         self._dims = (cfg.T, cfg.E, cfg.k, cfg.H)  # plain integers: a structure's fields cost more to read
         self._cap = cfg.E + cfg.replica_budget
-        self._bf16 = torch.bfloat16
+        self._bf16, self._fp4, self._e8m0 = torch.bfloat16, torch.float4_e2m1fn_x2, torch.float8_e8m0fnu
         self._current_stream = _current_stream(torch)
         self.sizes = moe_plan_query(cfg)
         with torch.cuda.device(self.device):
@@ -778,6 +839,125 @@ class Layer:
         moex_combine_grad(self.handle, _addr(weight), _addr(slot_pos), _addr(expert_out), _addr(grad_out),
                           _addr(grad_rows), _addr(grad_weight), self._stream(stream))
         return grad_rows, grad_weight
+
+    def _check_blocks4(self, b: Blocks4, lead):
+        q, scale = Blocks4.shapes(lead, b.cols)
+        self._check_tensor(b.q, q, self._fp4)
+        self._check_tensor(b.scale, scale, self._e8m0)
+
+    def _result_blocks4(self, out, stream, lead, cols) -> Blocks4:
+        if out is not None:
+            if out.cols != cols:
+                raise ValueError("out has %d columns, the result %d" % (out.cols, cols))
+            self._check_blocks4(out, lead)
+            return out
+        q, scale = Blocks4.shapes(lead, cols)
+        return Blocks4(self._empty(q, self._fp4, stream), self._empty(scale, self._e8m0, stream), cols)
+
+    def quantize4(self, x, stream=None, out=None) -> Blocks4:
+        """bf16 rows [n][cols] to Blocks4 of rows (moex4_quantize), new ones or `out`."""
+        if x.dim() != 2:
+            raise ValueError("x must be [rows][cols]")
+        rows, cols = x.shape
+        self._check_16bit(x, (rows, cols), "x")
+        out = self._result_blocks4(out, stream, (rows,), cols)
+        moex4_quantize(self.handle, _addr(x), rows, cols, _addr(out.q), _addr(out.scale), self._stream(stream))
+        return out
+
+    def quantize_weights4(self, w, transposed: bool = False, stream=None, out=None):
+        """bf16 matrices [E][n][k] to Blocks4 of matrices (moex4_quantize_weights); with transposed also those of the
+        transposed matrices [E][k][n], from the same pass.  `out`: the Blocks4 to write (with transposed the pair)."""
+        if w.dim() != 3:
+            raise ValueError("w must be [experts][n][k]")
+        E, n, k = w.shape
+        self._check_16bit(w, (E, n, k), "w")
+        out, out_t = (None, None) if out is None else out if transposed else (out, None)
+        out = self._result_blocks4(out, stream, (E, n), k)
+        out_t = self._result_blocks4(out_t, stream, (E, k), n) if transposed else Blocks4(None, None, n)
+        moex4_quantize_weights(self.handle, _addr(w), E, n, k, _addr(out.q), _addr(out.scale), _addr(out_t.q),
+                               _addr(out_t.scale), self._stream(stream))
+        return (out, out_t) if transposed else out
+
+    def values4(self, b: Blocks4, stream=None, out=None):
+        """The values of Blocks4 of rows or matrices, bf16 [..., cols] (moex4_values)."""
+        lead = tuple(b.q.shape[:-1])
+        if len(lead) not in (1, 2):
+            raise ValueError("expected Blocks4 of rows or of matrices")
+        self._check_blocks4(b, lead)
+        if out is None:
+            out = self._empty((*lead, b.cols), self._bf16, stream)
+        else:
+            self._check_16bit(out, (*lead, b.cols), "out")
+        moex4_values(self.handle, _addr(b.q), _addr(b.scale), lead[0] if len(lead) == 2 else 1, lead[-1], b.cols,
+                     _addr(out), self._stream(stream))
+        return out
+
+    def swiglu4(self, y, stream=None, out=None) -> Blocks4:
+        """silu(gate) * up of rows [n][2 f] (gate columns, then up) in 4 bits (moex4_swiglu), new Blocks4 or `out`."""
+        if y.dim() != 2 or y.shape[1] % 2:
+            raise ValueError("y must be [rows][2 f]")
+        rows, f = y.shape[0], y.shape[1] // 2
+        self._check_16bit(y, (rows, 2 * f), "y")
+        out = self._result_blocks4(out, stream, (rows,), f)
+        moex4_swiglu(self.handle, _addr(y), rows, f, _addr(out.q), _addr(out.scale), self._stream(stream))
+        return out
+
+    def matmul4(self, x, w: Blocks4, plan=None, inst_offset=None, out=None, stream=None):
+        """Rows in dispatch order times their experts' matrices in 4 bits (moex4_matmul): bf16 [T*k][n] of x, Blocks4 or
+        Blocks of rows [T*k][k], and w, Blocks4 of matrices [E][n][k]."""
+        T, E, top, _ = self._dims
+        rows = T * top
+        plan_s, inst_offset = self._product_plan(plan, inst_offset)
+        n, k = w.q.shape[1], w.cols
+        if x.cols != k:
+            raise ValueError("x has %d columns, the matrices %d" % (x.cols, k))
+        four = isinstance(x, Blocks4)
+        if four:
+            self._check_blocks4(x, (rows,))
+        else:
+            self._check_blocks(x, (rows,))
+        self._check_blocks4(w, (E, n))
+        if out is None:
+            out = self._empty((rows, n), self._bf16, stream)
+        else:
+            self._check_16bit(out, (rows, n), "out")
+        moex4_matmul(self.handle, plan_s, _addr(inst_offset), 4 if four else 8, _addr(x.q), _addr(x.scale), _addr(w.q),
+                     _addr(w.scale), n, k, _addr(out), self._stream(stream))
+        return out
+
+    def experts(self, hidden, weight, w1, w2, topk_idx=None, out=None, stream=None):
+        """The experts of a layer of at most 64 tokens, from hidden rows [T][H] and the router's weights [T][k] to the
+        combined rows [T][H], without plan and dispatch (moex4_experts).  w1 [E][2 f][H] (gate, then up) and w2
+        [E][H][f]: both Blocks4 or both Blocks.  topk_idx defaults to this layer's, of its last gate() or route()."""
+        T, E, k, H = self._dims
+        topk_idx = self.route_out.topk_idx if topk_idx is None else topk_idx
+        self._check_16bit(hidden, (T, H), "hidden")
+        self._check_tensor(topk_idx, (T, k), self.torch.int32)
+        self._check_tensor(weight, (T, k), self.torch.float32)
+        f, four = w2.cols, isinstance(w1, Blocks4)
+        if w1.cols != H:
+            raise ValueError("w1 has %d columns, hidden %d" % (w1.cols, H))
+        if four != isinstance(w2, Blocks4):
+            raise TypeError("w1 and w2 must both be Blocks4 or both Blocks")
+        if four:
+            self._check_blocks4(w1, (E, 2 * f))
+            self._check_blocks4(w2, (E, H))
+        else:
+            self._check_blocks(w1, (E, 2 * f), (E, -(-2 * f // BLOCK)))
+            self._check_blocks(w2, (E, H), (E, -(-H // BLOCK)))
+        if out is None:
+            out = self._empty((T, H), hidden.dtype, stream)
+        else:
+            self._check_16bit(out, (T, H), "out")
+            self._check_apart(out, hidden)
+        # the activations and, behind them, their scales
+        fp = Blocks4.padded(f)
+        act = self._empty((T * k * (fp + fp // BLOCK4),), self.torch.uint8, stream)
+        at = act.data_ptr()
+        moex4_experts(self.handle, _addr(hidden), _addr(topk_idx), _addr(weight), 4 if four else 8, f, _addr(w1.q),
+                      _addr(w1.scale), _addr(w2.q), _addr(w2.scale), at, at + T * k * fp, _addr(out),
+                      self._stream(stream))
+        return out
 
     def place(self, cooc=None, max_swaps: int = -1, stream=None):
         """Correlated expert placement from co-selection counts (moe_plan_place);
