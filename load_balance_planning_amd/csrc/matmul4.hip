@@ -9,6 +9,8 @@
 // has bytes 16 g on and 64 + 16 g on, with 32x32x64 bytes 16 g on and 32 + 16 g
 // on.  As in the 8-bit products the matrices are the first operand, so a lane's
 // results are channels of one row.
+#include <type_traits>
+
 #include "buffers.h"
 #include "experts4.h"
 #include "fp4_block.h"
@@ -124,6 +126,382 @@ __global__ __launch_bounds__(256) void matmul4_rows16_kernel(Instances in, const
   }
 }
 
+// ---- tiles ---------------------------------------------------------------------
+//
+// BC channels x BT rows per workgroup of 2 x 2 waves, as the 8-bit products have
+// them: both operands' blocks go to LDS by direct loads, a step ahead of the
+// products; a step is two halves, and while a half's products run the other
+// half's operands are read into a second set of registers; one barrier a step,
+// between its halves.
+//
+// Rows in 4 bits: a step is a line of both operands (128 bytes, 256 values: a
+// half is two 32x32x64 instructions deep).  Lane group g takes the four blocks of
+// 32 from 4 g on, so that its scales are one word, which the instruction indexes
+// by byte.  A line's scales come to LDS with it: 8 bytes a row, one load of 16
+// bytes a thread.
+//
+// Rows in 8 bits: a step is 128 values, 128 bytes of x and 64 of the matrix (a
+// half is one instruction deep).  The matrices' scales of two steps come to LDS
+// together; those of x, one byte a step, go to registers four steps at a time.
+//
+// LDS rows of 128 bytes are placed as the 8-bit products place them.  Of rows of
+// 64 bytes, four share 256 bytes: piece p of row R lies at place 4 (R % 4) + (p ^
+// s(R)), s the bits 2 and 4 of R, so that the 16 lanes of a read (rows that
+// differ in bits 0, 1, 2 and 4) find 16 different places.
+template <bool CHANNELS>
+__device__ __forceinline__ int piece_swizzle(int pair) {  // pair = R / 2
+  return CHANNELS ? (pair & 3) | ((pair >> 1) & 4) : pair & 7;
+}
+template <bool CHANNELS>
+__device__ __forceinline__ int piece_at(int row, int p) {
+  return (row >> 1) * 256 + ((((row & 1) << 3) | p) ^ piece_swizzle<CHANNELS>(row >> 1)) * 16;
+}
+[[maybe_unused]] __device__ __forceinline__ int quad_swizzle(int quad) { return (quad & 1) | ((quad >> 1) & 2); }  // quad = R / 4
+[[maybe_unused]] __device__ __forceinline__ int quad_piece_at(int row, int p) {
+  return (row >> 2) * 256 + (((row & 3) << 2) | (p ^ quad_swizzle(row >> 2))) * 16;
+}
+
+template <int XB, int BC, int BT>
+struct TileShape {
+  static constexpr int kThreads = 256;
+  static constexpr int kWaveC = BC / 2, kWaveT = BT / 2;               // a wave's channels and rows
+  static constexpr int kC = kWaveC / 32, kT = kWaveT / 32;             // in instruction tiles
+  static constexpr int kBytesC = XB == 4 ? 128 : 64, kBytesT = 128;    // of a row, a step
+  static constexpr int kDeep = XB == 4 ? 2 : 1;                        // instructions of a half
+  static constexpr int kPassC = BC * kBytesC / (16 * kThreads), kPassT = BT * kBytesT / (16 * kThreads);
+  static constexpr int kScales = XB == 4 ? 8 * (BC + BT) : 8 * BC;     // bytes of a line's scales
+  static_assert(BC % 128 == 0 && BC == BT, "four equal parts");
+};
+
+// A pointer that is the same for all lanes, in scalar registers.
+__device__ __forceinline__ const uint8_t* scalar(const uint8_t* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  return reinterpret_cast<const uint8_t*>((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 |
+                                          (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
+}
+
+// acc += c * t with scale byte OC of sc and OT of st.
+template <int XB, int OC, int OT>
+__device__ __forceinline__ acc16 multiply32(const v8i& c, const v8i& t, const acc16& acc, int sc, int st) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(c, t, acc, kFp4, XB == 4 ? kFp4 : kFp8, OC, sc, OT, st);
+}
+
+// Persistent: workgroup b takes every (gridDim.x / 8)-th tile of its XCD's run.
+template <int XB, int BC, int BT>
+__global__ __launch_bounds__(256, BC == 256 ? 1 : 2) void matmul4_tile_kernel(
+    Instances in, const uint8_t* __restrict__ x, const uint8_t* __restrict__ xs, const uint8_t* __restrict__ w,
+    const uint8_t* __restrict__ ws, int n, int k, uint16_t* __restrict__ y, int32_t* __restrict__ status) {
+#ifdef __HIP_DEVICE_COMPILE__
+  using S = TileShape<XB, BC, BT>;
+  __shared__ __align__(256) unsigned char c0_s[BC * S::kBytesC];
+  __shared__ __align__(256) unsigned char t0_s[BT * S::kBytesT];
+  __shared__ __align__(256) unsigned char c1_s[BC * S::kBytesC];
+  __shared__ __align__(256) unsigned char t1_s[BT * S::kBytesT];
+  __shared__ __align__(16) unsigned char z0_s[S::kScales];
+  __shared__ __align__(16) unsigned char z1_s[XB == 4 ? S::kScales : 16];
+  __shared__ int32_t sums[4];
+  extern __shared__ int32_t pre[];  // [cap + 1]
+  // where results pass: a place of their own, or (where two workgroups share
+  // the CU's LDS) the second stage, whose next block then comes in later
+  constexpr bool kOwnPlace = BC == 256;
+  __shared__ __align__(16) unsigned char out_s[kOwnPlace ? 4 * 4096 : 16];
+  constexpr bool kFetch = BC == 256;
+  __shared__ uint32_t fetch_s[kFetch ? 4 * 64 : 1];
+  if (blockIdx.x == 0) check_instances(in, status);
+  const int nct = (n + BC - 1) / BC;
+  const int n_inst = instance_count(in);
+  const int row_tiles = __builtin_amdgcn_readfirstlane(count_row_tiles(in, BT, pre, sums));
+  // Workgroups go to the eight XCDs in turn: each XCD takes a run of
+  // consecutive tiles, four row tiles by all channel tiles at a time, so that
+  // the tiles that it works on at once share their operands in its L2.
+  const int total = row_tiles * nct;  // below 2^24
+  const int xcd = blockIdx.x & 7, slots = gridDim.x >> 3;
+  const int last = (int)((int64_t)total * (xcd + 1) / 8);
+  int tile = (int)((int64_t)total * xcd / 8) + (blockIdx.x >> 3);
+  if (tile >= last) return;
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 31, g = lane >> 5;
+  const int lines = (k + kCols4 - 1) / kCols4;
+  const int nb8 = (k + kBlk - 1) / kBlk, ns8 = (nb8 + 3) / 4 * 4;
+  const int nb = XB == 4 ? lines : nb8;  // steps
+  const uint32_t kpc = (uint32_t)lines * (kCols4 / 2), kpt = XB == 4 ? kpc : (uint32_t)nb8 * kBlk;
+  // where this thread's pieces come from: the same place of every pass
+  const int pair = threadIdx.x >> 4;
+  const int place_t = (threadIdx.x & 15) ^ piece_swizzle<false>(pair);
+  const int place_c = (threadIdx.x & 15) ^ piece_swizzle<true>(pair);
+  const int wc = wave % 2 * S::kWaveC, wt = wave / 2 * S::kWaveT;
+  // a tile: its rows, channels, expert
+  struct Tile {
+    int r0, rows, c0, chans, expert, rt;
+  };
+  auto locate = [&](int t) {
+    const int band = t / (4 * nct), in_band = t - band * 4 * nct;
+    const int band_rows = min(4, row_tiles - band * 4);
+    const int rt = band * 4 + in_band % band_rows;
+    const int i = instance_of(pre, n_inst, rt);
+    Tile o;
+    o.c0 = __builtin_amdgcn_readfirstlane(in_band / band_rows * BC);
+    o.chans = min(BC, n - o.c0);
+    o.r0 = __builtin_amdgcn_readfirstlane(in.offset[i] + (rt - pre[i]) * BT);
+    o.rows = min(BT, __builtin_amdgcn_readfirstlane(in.offset[i + 1]) - o.r0);
+    o.expert = __builtin_amdgcn_readfirstlane(in.expert[i]);
+    o.rt = rt;
+    return o;
+  };
+  constexpr std::integral_constant<int, 0> zero{};
+  constexpr std::integral_constant<int, 1> one{};
+  Tile at;
+  uint32_t off_c[S::kPassC], off_t[S::kPassT], xs_off[S::kT], off_f;
+  // this wave's part of a line's scales: 128 channels' or (4 bits) rows' (where
+  // there are fewer parts than waves, two load the same)
+  constexpr int kParts = BC / 128;
+  const int z_part = wave & (XB == 4 ? 2 * kParts - 1 : kParts - 1);
+  const bool z_rows = z_part >= kParts;
+  const int z_at = (z_rows ? z_part - kParts : z_part) * 1024;
+  const int64_t z_step = 8 * (z_rows ? in.rows : n);
+  // the tile's operands and scales, in scalars
+  const uint8_t *w_from, *x_from, *z_from;
+  uint32_t w_bytes, x_bytes, z_bytes;
+  auto set_offsets = [&]() {
+    w_from = scalar(w + ((int64_t)at.expert * n + at.c0) * kpc);
+    x_from = scalar(x + (int64_t)at.r0 * kpt);
+    z_from = scalar(z_rows ? xs + (int64_t)at.r0 * 8 : ws + ((int64_t)at.expert * lines * n + at.c0) * 8);
+    w_bytes = __builtin_amdgcn_readfirstlane(at.chans * kpc);
+    x_bytes = __builtin_amdgcn_readfirstlane(at.rows * kpt);
+    z_bytes = __builtin_amdgcn_readfirstlane(8 * (z_rows ? at.rows : at.chans));
+#pragma unroll
+    for (int q = 0; q < S::kPassC; ++q)
+      off_c[q] = XB == 4 ? (uint32_t)min(q * 32 + 2 * pair + (place_c >> 3), at.chans - 1) * kpc + 16 * (place_c & 7)
+                         : (uint32_t)min(q * 64 + 4 * pair + ((threadIdx.x >> 2) & 3), at.chans - 1) * kpc +
+                               16 * ((threadIdx.x & 3) ^ quad_swizzle(pair));
+#pragma unroll
+    for (int q = 0; q < S::kPassT; ++q)
+      off_t[q] = (uint32_t)min(q * 32 + 2 * pair + (place_t >> 3), at.rows - 1) * kpt + 16 * (place_t & 7);
+    if (XB == 8) {
+#pragma unroll
+      for (int j = 0; j < S::kT; ++j) xs_off[j] = (uint32_t)(min(wt + 32 * j + r, at.rows - 1) * ns8);
+    }
+    // this wave's share of the lines to fetch ahead
+    const int part = wave < 2 ? at.rt & 3 : (at.c0 / BC) & 3;
+    off_f = (uint32_t)min(4 * (32 * (wave & 1) + (lane & 31)) + part, (wave < 2 ? at.chans : at.rows) - 1) *
+            (wave < 2 ? kpc : kpt);
+  };
+  // Block b's lines into the XCD's L2, a quarter of them per workgroup: those that
+  // share an operand take the others.  The bytes read go nowhere.
+  auto fetch = [&](int b) {
+    if (!kFetch) return;
+    asm volatile("" ::: "memory");  // behind the block loads before it
+    const auto buf = buffer_of(wave < 2 ? w_from : x_from, wave < 2 ? w_bytes : x_bytes);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_ptr)(fetch_s + wave * 64), 4, off_f,
+                                             b * (wave < 2 ? S::kBytesC : S::kBytesT), 0, 0);
+  };
+  // A step's blocks, and with them the scales of its line (rows in 8 bits: of the
+  // line that begins with an even step).
+  auto load = [&](unsigned char* c_s, unsigned char* t_s, unsigned char* z_s, int b, auto odd) {
+    const auto w_buf = buffer_of(w_from, w_bytes), x_buf = buffer_of(x_from, x_bytes);
+#pragma unroll
+    for (int q = 0; q < S::kPassC; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(w_buf, (lds_ptr)(c_s + (q * 256 + wave * 64) * 16), 16, off_c[q],
+                                               b * S::kBytesC, 0, 0);
+#pragma unroll
+    for (int q = 0; q < S::kPassT; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(x_buf, (lds_ptr)(t_s + (q * 256 + wave * 64) * 16), 16, off_t[q],
+                                               b * S::kBytesT, 0, 0);
+    if constexpr (XB == 4 || decltype(odd)::value == 0) {
+      const auto z_buf = buffer_of(z_from + (int64_t)(XB == 4 ? b : b >> 1) * z_step, z_bytes);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(z_buf, (lds_ptr)(z_s + z_part * 1024), 16, z_at + lane * 16, 0, 0, 0);
+    }
+  };
+  const int perm = 16 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3);  // channel of the lane's matrix row
+  // This lane's scales of a line: of the channels and (4 bits) of the rows.
+  struct Scales {
+    int c[XB == 4 ? 1 : 2][S::kC], t[S::kT];
+  };
+  auto read_scales = [&](Scales* s, const unsigned char* z_s) {
+#pragma unroll
+    for (int i = 0; i < S::kC; ++i) {
+      const unsigned char* at_z = z_s + (wc + 32 * i + perm) * 8;
+      if (XB == 4) {
+        s->c[0][i] = *reinterpret_cast<const int*>(at_z + 4 * g);
+      } else {  // both steps', shifted so that the lane's blocks are bytes 0 and 2
+        typedef uint32_t u32x2_s __attribute__((ext_vector_type(2)));
+        const u32x2_s v = *reinterpret_cast<const u32x2_s*>(at_z);
+        s->c[0][i] = (int)(v[0] >> (8 * g));
+        s->c[XB == 4 ? 0 : 1][i] = (int)(v[1] >> (8 * g));
+      }
+    }
+    if (XB == 4) {
+#pragma unroll
+      for (int j = 0; j < S::kT; ++j)
+        s->t[j] = *reinterpret_cast<const int*>(z_s + (BC + wt + 32 * j + r) * 8 + 4 * g);
+    }
+  };
+  // rows in 8 bits: scales of x, four steps to a word
+  int sx_next[S::kT];
+  auto load_sx = [&](int b) {
+    if (XB == 4) return;
+    const auto xs_buf = buffer_of(xs + (int64_t)at.r0 * ns8, (uint32_t)(at.rows * ns8));
+#pragma unroll
+    for (int j = 0; j < S::kT; ++j) sx_next[j] = (int)__builtin_amdgcn_raw_buffer_load_b32(xs_buf, xs_off[j], b & ~3, 0);
+  };
+  auto take_sx = [&](Scales* s, int b) {  // those of block b, b even, to the lowest byte
+    if (XB == 4) return;
+#pragma unroll
+    for (int j = 0; j < S::kT; ++j) s->t[j] = sx_next[j] >> (8 * (b & 2));
+  };
+  // LDS places of this lane's pieces in the first tiles; the others lie at
+  // constant distances.
+  const int first_c = XB == 4 ? piece_at<true>(wc + perm, 4 * g) : quad_piece_at(wc + perm, g);
+  const int first_t = piece_at<false>(wt + r, XB == 4 ? 4 * g : g);
+  acc16 acc[S::kC][S::kT];
+  // 4-bit operands are kept as what they are, 16 bytes: widened ones would hold
+  // registers of zeros from one half to the next
+  struct Half {
+    v4i c[S::kDeep][S::kC], t[2][S::kT];
+  };
+  auto piece = [&](const unsigned char* s, int place) { return *reinterpret_cast<const v4i*>(s + place); };
+  auto read = [&](Half* f, const unsigned char* c_s, const unsigned char* t_s, int half) {
+    // The places of the other pieces are made from these two each time: kept, they
+    // were 16 registers, and others were spilled.
+    int at_c = first_c, at_t = first_t;
+    asm volatile("" : "+v"(at_c), "+v"(at_t));
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int j = 0; j < S::kT; ++j)
+        f->t[m][j] = piece(t_s, (at_t ^ (XB == 4 ? 16 * (2 * half + m) : 64 * half + 32 * m)) + 32 * j * S::kBytesT);
+#pragma unroll
+    for (int m = 0; m < S::kDeep; ++m)
+#pragma unroll
+      for (int i = 0; i < S::kC; ++i)
+        f->c[m][i] = piece(c_s, (at_c ^ (XB == 4 ? 16 * (2 * half + m) : 32 * half)) + 32 * i * S::kBytesC);
+  };
+  // STEP: even or odd of its round; HALF of the step.
+  auto multiply = [&](const Half& f, const Scales& s, auto step, auto half) {
+    constexpr int kStep = decltype(step)::value, kHalf = decltype(half)::value;
+#pragma unroll
+    for (int i = 0; i < S::kC; ++i)
+#pragma unroll
+      for (int j = 0; j < S::kT; ++j) {
+        if constexpr (XB == 4) {
+          acc[i][j] = multiply32<XB, 2 * kHalf, 2 * kHalf>(operand4(f.c[0][i]), operand4(f.t[0][j]), acc[i][j],
+                                                           s.c[0][i], s.t[j]);
+          acc[i][j] = multiply32<XB, 2 * kHalf + 1, 2 * kHalf + 1>(operand4(f.c[1][i]), operand4(f.t[1][j]),
+                                                                   acc[i][j], s.c[0][i], s.t[j]);
+        } else {
+          acc[i][j] = multiply32<XB, 2 * kHalf, kStep>(operand4(f.c[0][i]), operand8(f.t[0][j], f.t[1][j]), acc[i][j],
+                                                       s.c[kStep][i], s.t[j]);
+        }
+      }
+  };
+  // a half's products, with the other half's reads (and LOADS direct loads)
+  // spread between them
+  constexpr int kProducts = S::kC * S::kT * S::kDeep;
+  constexpr int kReads = S::kDeep * (S::kC + S::kT * (XB == 4 ? 1 : 2)) + S::kC + (XB == 4 ? S::kT : 0);
+  auto spread = [&](bool loads) {
+    if (kFetch && !loads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // fetch
+#pragma unroll
+    for (int q = 0; q < kProducts; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a product
+      __builtin_amdgcn_sched_group_barrier(0x100, (kReads + kProducts - 1) / kProducts, 0);
+      if (loads) __builtin_amdgcn_sched_group_barrier(0x020, (S::kPassC + S::kPassT + kProducts) / kProducts, 0);
+    }
+  };
+  // turns of 64 channels by 32 rows; or all at once, of 8-bit rows one row after the other of instruction tiles
+  constexpr int kTI = kOwnPlace ? S::kC / 2 : 1, kTJ = kOwnPlace ? S::kT : XB == 4 ? 1 : 2;
+  constexpr int kOwn = 2 * S::kWaveC * S::kWaveT / (kTI * kTJ);
+  static_assert(kOwn <= (kOwnPlace ? 4096 : BT * S::kBytesT / (XB == 4 ? 2 : 4)), "a turn fits the wave's part");
+  unsigned char* own = kOwnPlace ? out_s + wave * 4096
+                       : XB == 4 ? (wave < 2 ? c1_s : t1_s) + (wave & 1) * kOwn
+                                 : t1_s + wave * kOwn;
+  at = locate(tile);
+  set_offsets();
+  load_sx(0);
+  load(c0_s, t0_s, z0_s, 0, zero);
+  if (kOwnPlace) load(c1_s, t1_s, z1_s, min(1, nb - 1), one);
+  fetch(min(2, nb - 1));
+  for (;;) {
+    const Tile next = locate(min(tile + slots, last - 1));  // arrives while this tile's products run
+#pragma unroll
+    for (int i = 0; i < S::kC; ++i)
+#pragma unroll
+      for (int j = 0; j < S::kT; ++j)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
+    Half f0, f1;
+    Scales s0, s1;  // of even and odd steps (4 bits), or s0 of a round (8 bits)
+    sync_with_loads();
+    if (!kOwnPlace) load(c1_s, t1_s, z1_s, min(1, nb - 1), one);
+    read(&f0, c0_s, t0_s, 0);
+    read_scales(&s0, z0_s);
+    // No branch inside a round: past the last block the loads and reads take
+    // some block again, which nothing uses.
+    for (int b = 0; b + 2 <= nb; b += 2) {
+      take_sx(&s0, b);
+      fetch(min(b + 3, nb - 1));
+      read(&f1, c0_s, t0_s, 1);
+      multiply(f0, s0, zero, zero);
+      spread(false);
+      sync_with_loads<kFetch ? 1 : 0>();
+      load(c0_s, t0_s, z0_s, min(b + 2, nb - 1), zero);
+      read(&f0, c1_s, t1_s, 0);
+      if (XB == 4) read_scales(&s1, z1_s);
+      multiply(f1, s0, zero, one);
+      spread(true);
+      fetch(min(b + 4, nb - 1));
+      read(&f1, c1_s, t1_s, 1);
+      multiply(f0, XB == 4 ? s1 : s0, one, zero);
+      spread(false);
+      sync_with_loads<kFetch ? 1 : 0>();
+      load_sx(min(b + 2, nb - 1));
+      load(c1_s, t1_s, z1_s, min(b + 3, nb - 1), one);
+      read(&f0, c0_s, t0_s, 0);
+      if (XB == 4) {
+        read_scales(&s0, z0_s);
+        multiply(f1, s1, one, one);
+      } else {
+        read_scales(&s1, z0_s);
+        multiply(f1, s0, one, one);
+        s0 = s1;
+      }
+      spread(true);
+    }
+    if (nb & 1) {
+      take_sx(&s0, nb - 1);
+      read(&f1, c0_s, t0_s, 1);
+      multiply(f0, s0, zero, zero);
+      multiply(f1, s0, zero, one);
+    }
+    sync_with_loads();  // every wave has its last operands, and no load into LDS is under way
+    // The next tile's first blocks come in while this one's results go out.
+    const Tile done = at;
+    tile += slots;
+    const bool more = tile < last;
+    if (more) {
+      at = next;
+      set_offsets();
+      load_sx(0);
+      load(c0_s, t0_s, z0_s, 0, zero);
+      if (kOwnPlace) load(c1_s, t1_s, z1_s, min(1, nb - 1), one);
+      fetch(min(2, nb - 1));
+    }
+    store_wave_tile<kTI, kTJ>(acc, own, y + (int64_t)(done.r0 + wt) * n + done.c0 + wc, n, done.rows - wt,
+                              done.chans - wc);
+    if (!more) break;
+  }
+#endif
+}
+
+template <int XB, int BC, int BT>
+hipError_t launch_tiles(const Instances& in, const uint8_t* x, const uint8_t* xs, const uint8_t* w, const uint8_t* ws,
+                        int n, int k, uint16_t* y, int32_t* status, hipStream_t st) {
+  const int64_t most = row_tile_ids(in, BT) * ((n + BC - 1) / BC), resident = BC == 256 ? 256 : 512;
+  hipLaunchKernelGGL((matmul4_tile_kernel<XB, BC, BT>), dim3((unsigned)((most < resident ? most : resident) + 7) / 8 * 8),
+                     dim3(256), sizeof(int32_t) * (in.cap + 1), st, in, x, xs, w, ws, n, k, y, status);
+  return hipGetLastError();
+}
+
 template <int XB>
 hipError_t launch_rows16(const Instances& in, const uint8_t* x, const uint8_t* xs, const uint8_t* w, const uint8_t* ws,
                          int n, int k, uint16_t* y, int32_t* status, hipStream_t st) {
@@ -137,12 +515,37 @@ hipError_t launch_rows16(const Instances& in, const uint8_t* x, const uint8_t* x
 
 }  // namespace
 
-int64_t matmul4_tiles(const Instances&, int32_t) { return 0; }
+namespace {
+
+constexpr int kCapWide = 1536;  // instances whose tile counts fit the LDS beside 256 x 256 tiles
+
+// The tile of a product, 0 for the streaming kernel, as the 8-bit products choose it.
+int matmul4_tile(const Instances& in, int n) {
+  if (in.rows <= (int64_t)8 * in.E) return 0;
+  const bool fills = in.rows / 256 * ((n + 255) / 256) >= 512 && in.cap <= kCapWide;
+  return in.rows >= (int64_t)192 * in.E && fills ? 256 : 128;
+}
+
+template <int XB>
+hipError_t launch(const Instances& in, const uint8_t* x, const uint8_t* xs, const uint8_t* w, const uint8_t* ws, int n,
+                  int k, uint16_t* y, int32_t* status, hipStream_t st) {
+  const int tile = matmul4_tile(in, n);
+  if (tile == 256) return launch_tiles<XB, 256, 256>(in, x, xs, w, ws, n, k, y, status, st);
+  if (tile == 128) return launch_tiles<XB, 128, 128>(in, x, xs, w, ws, n, k, y, status, st);
+  return launch_rows16<XB>(in, x, xs, w, ws, n, k, y, status, st);
+}
+
+}  // namespace
+
+int64_t matmul4_tiles(const Instances& in, int32_t n) {
+  const int tile = matmul4_tile(in, n);
+  return tile == 0 ? 0 : row_tile_ids(in, tile) * ((n + tile - 1) / tile);
+}
 
 hipError_t launch_matmul4(const Instances& in, int32_t x_bits, const uint8_t* x, const uint8_t* xs, const uint8_t* w,
                           const uint8_t* ws, int32_t n, int32_t k, uint16_t* y, int32_t* status, hipStream_t st) {
-  return x_bits == 4 ? launch_rows16<4>(in, x, xs, w, ws, n, k, y, status, st)
-                     : launch_rows16<8>(in, x, xs, w, ws, n, k, y, status, st);
+  return x_bits == 4 ? launch<4>(in, x, xs, w, ws, n, k, y, status, st)
+                     : launch<8>(in, x, xs, w, ws, n, k, y, status, st);
 }
 
 }  // namespace moe

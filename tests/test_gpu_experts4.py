@@ -269,6 +269,37 @@ def test_products_of_many_instances(mp):
     check_products(mp, loads, np.concatenate([np.arange(E), rng.permutation(E)[:B]]), E, 24, 40, B)
 
 
+@pytest.mark.parametrize("loads,E,n,k", [([4100, 4204], 2, 4000, 328), ([8192], 1, 4100, 700), ([300, 8000, 70], 3, 4096, 256)])
+def test_products_in_the_largest_tiles(mp, loads, E, n, k):
+    """Tiles of 256 x 256, several to a workgroup; rows at the tiles' ends and some others."""
+    rows = sum(loads)
+    print("products4 loads=%s E=%d n=%d k=%d" % (loads, E, n, k), flush=True)
+    layer = layer_for(mp, rows, E)
+    dev = layer.device
+    plan, off, spans = instances(mp, layer, loads, list(range(E)))
+    x, w = normal(1, rows, k), normal(2, E, n, k, scale=0.05)
+    x[:, k // 2:] *= 0.01
+    wb = layer.quantize_weights4(w.to(dev))
+    wv, sw = refs4.values(wb), refs4.spread(refs4.scales(wb), 32, k)
+    for b in (layer.quantize4(x.to(dev)), layer.quantize(x.to(dev))):
+        y = torch.full((rows, n), 7.0, dtype=BF, device=dev)
+        layer.matmul4(b, wb, plan=plan, inst_offset=off, out=y)
+        y = y.cpu()
+        assert torch.equal(layer.matmul4(b, wb, plan=plan, inst_offset=off).cpu(), y)
+        four = isinstance(b, mp.Blocks4)
+        xv = refs4.values(b) if four else refs.values(b, rows)
+        sx = None if four else refs4.spread(b.scale.cpu().double(), 128, k)
+        for e, a, z in spans:
+            at = torch.tensor(sorted({t for t in [*range(a, a + 40), *range(a + 240, a + 270), *range(z - 40, z),
+                                                  *range(a, z, 37)] if a <= t < z}))
+            want, off_ = xv[at] @ wv[e].t(), refs4.added(xv[at], wv[e])
+            if not four:
+                off_ = off_ + refs4.cut(xv[at], sx[at], wv[e], sw[e])
+            assert ((y[at].double() - want).abs() <= refs4.rounded(want, off_)).all()
+    assert layer.status() == 0
+    layer.close()
+
+
 def test_any_scale_bytes(mp, small):
     """Scales from 2^-127 to 2^127 of rows, and of matrices, as the products and the values take them."""
     dev = small.device
