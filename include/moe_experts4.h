@@ -112,19 +112,24 @@ int moex4_matmul(moe_plan_t h, const moe_plan_out* plan, const int32_t* inst_off
  * hidden bf16 [T][H]; topk_idx int32 [T][k]; weight float [T][k] (moex_gate's, or
  * any); w1 matrices [E][2 f][H], gate rows then up rows, w2 [E][H][f], w_bits 4:
  * in blocks of 32 as above, w_bits 8: moex_quantize_weights'; out bf16 [T][H],
- * fully overwritten; it may not overlap hidden or act.  Q rounds to e4m3 with
+ * fully overwritten; it may not overlap hidden or work.  Q rounds to e4m3 with
  * one E8M0 scale per 1 x 32, by moex_quantize's rules; all else is fp32, the
- * sums in a fixed order.
- * act, act_scale: memory for the activations, for one call at a time:
- * uint8 [T*k][f rounded up to 256] and uint8 [T*k][f rounded up to 256, / 32],
- * 16- and 8-byte aligned.  An index outside [0, E) or repeated within a token
- * sets MOE_STATUS_BAD_TOPK (an index outside is left out; which of a repeated
- * one's weights counts is not specified).  f >= 1; MOE_ERR_UNSUPPORTED for more
- * than 64 tokens and for f or H above 2^20.
+ * sums in a fixed order.  The first product takes values as bf16 (as
+ * moex4_values gives them; e4m3 * scale), so that its sums lose nothing; the
+ * second cuts products off as moex_matmul does.
+ * work: memory for one call at a time, 16-byte aligned, as many bytes as
+ * moex4_experts_work says for the handle and f (host only).  After the call it
+ * begins with the activations a, uint8 [T*k][fp], and their scales, uint8
+ * [T*k][fp/32], fp = f rounded up to 256, of the slots whose index is good.
+ * An index outside [0, E) or repeated within a token sets MOE_STATUS_BAD_TOPK (an
+ * index outside is left out; which of a repeated one's weights counts, or both,
+ * is not specified).  f >= 1; MOE_ERR_UNSUPPORTED for more than 64 tokens, for f
+ * or H above 2^20, and for matrices of 2^36 values or more.
  */
+int moex4_experts_work(moe_plan_t h, int32_t f, int64_t* bytes);
 int moex4_experts(moe_plan_t h, const uint16_t* hidden, const int32_t* topk_idx, const float* weight, int32_t w_bits,
                   int32_t f, const uint8_t* w1, const uint8_t* w1_scale, const uint8_t* w2, const uint8_t* w2_scale,
-                  uint8_t* act, uint8_t* act_scale, uint16_t* out, void* stream);
+                  uint8_t* work, uint16_t* out, void* stream);
 
 #ifdef __cplusplus
 }

@@ -114,7 +114,7 @@ EXPERT_EXPORTS = ("moex_gate", "moex_gate_grad", "moex_quantize", "moex_quantize
                   "moex_swiglu_grad", "moex_matmul", "moex_wgrad", "moex_combine", "moex_combine_grad")
 # include/moe_experts4.h
 EXPERT4_EXPORTS = ("moex4_quantize", "moex4_quantize_weights", "moex4_values", "moex4_swiglu", "moex4_matmul",
-                   "moex4_experts")
+                   "moex4_experts_work", "moex4_experts")
 
 _LIB = None
 
@@ -171,7 +171,8 @@ def lib():
         l.moex4_values.argtypes = [vp, vp, vp, i32, i64, i32, vp, vp]
         l.moex4_swiglu.argtypes = [vp, vp, i64, i32, vp, vp, vp]
         l.moex4_matmul.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, i32, i32, vp, vp]
-        l.moex4_experts.argtypes = [vp, vp, vp, vp, i32, i32] + [vp] * 8
+        l.moex4_experts_work.argtypes = [vp, i32, vp]
+        l.moex4_experts.argtypes = [vp, vp, vp, vp, i32, i32] + [vp] * 7
         for n in EXPORTS[:-1] + EXPERT_EXPORTS + EXPERT4_EXPORTS:
             getattr(l, n).restype = ctypes.c_int
         _LIB = l
@@ -340,10 +341,16 @@ def moex4_matmul(h, plan: moe_plan_out, inst_offset: int, x_bits: int, x: int, x
                                               y, stream))
 
 
+def moex4_experts_work(h, f: int) -> int:
+    out = ctypes.c_int64(0)
+    _check("moex4_experts_work", lib().moex4_experts_work(h, f, ctypes.byref(out)))
+    return out.value
+
+
 def moex4_experts(h, hidden: int, topk_idx: int, weight: int, w_bits: int, f: int, w1: int, w1_scale: int, w2: int,
-                  w2_scale: int, act: int, act_scale: int, out: int, stream: int):
-    _check("moex4_experts", lib().moex4_experts(h, hidden, topk_idx, weight, w_bits, f, w1, w1_scale, w2, w2_scale, act,
-                                                act_scale, out, stream))
+                  w2_scale: int, work: int, out: int, stream: int):
+    _check("moex4_experts", lib().moex4_experts(h, hidden, topk_idx, weight, w_bits, f, w1, w1_scale, w2, w2_scale, work,
+                                                out, stream))
 
 
 def moe_plan_set_events(h, gather_begin, gather_end):
@@ -536,6 +543,7 @@ class Layer:
         self._dims = (cfg.T, cfg.E, cfg.k, cfg.H)  # plain integers: a structure's fields cost more to read
         self._cap = cfg.E + cfg.replica_budget
         self._bf16, self._fp4, self._e8m0 = torch.bfloat16, torch.float4_e2m1fn_x2, torch.float8_e8m0fnu
+        self._few_bytes = {}  # memory of an experts() call, by the experts' width
         self._current_stream = _current_stream(torch)
         self.sizes = moe_plan_query(cfg)
         with torch.cuda.device(self.device):
@@ -950,13 +958,11 @@ class Layer:
         else:
             self._check_16bit(out, (T, H), "out")
             self._check_apart(out, hidden)
-        # the activations and, behind them, their scales
-        fp = Blocks4.padded(f)
-        act = self._empty((T * k * (fp + fp // BLOCK4),), self.torch.uint8, stream)
-        at = act.data_ptr()
+        if f not in self._few_bytes:
+            self._few_bytes[f] = moex4_experts_work(self.handle, f)
+        work = self._empty((self._few_bytes[f],), self.torch.uint8, stream)
         moex4_experts(self.handle, _addr(hidden), _addr(topk_idx), _addr(weight), 4 if four else 8, f, _addr(w1.q),
-                      _addr(w1.scale), _addr(w2.q), _addr(w2.scale), at, at + T * k * fp, _addr(out),
-                      self._stream(stream))
+                      _addr(w1.scale), _addr(w2.q), _addr(w2.scale), _addr(work), _addr(out), self._stream(stream))
         return out
 
     def place(self, cooc=None, max_swaps: int = -1, stream=None):

@@ -86,20 +86,42 @@ extern "C" int moex4_matmul(moe_plan_t h, const moe_plan_out* plan, const int32_
   return hip_rc(moe::launch_matmul4(in, x_bits, x, x_scale, w, w_scale, n, k, y, h->ws.status, begin_call(h, stream)));
 }
 
-extern "C" int moex4_experts(moe_plan_t h, const uint16_t* hidden, const int32_t* topk_idx, const float* weight,
-                             int32_t w_bits, int32_t f, const uint8_t* w1, const uint8_t* w1_scale, const uint8_t* w2,
-                             const uint8_t* w2_scale, uint8_t* act, uint8_t* act_scale, uint16_t* out, void* stream) {
-  if (!h || f < 1 || (w_bits != 4 && w_bits != 8)) return MOE_ERR_INVALID_ARG;
+namespace {
+
+// Sizes that the layer of few tokens takes: its kernels address an expert's scales with 32 bits.
+int check_few(moe_plan_t h, int32_t f) {
+  if (!h || f < 1) return MOE_ERR_INVALID_ARG;
   const moe::Dims& d = h->d;
   if (d.T > moe::kMaxFewTokens || f > (1 << 20) || d.H > (1 << 20)) return MOE_ERR_UNSUPPORTED;
-  if (d.T > 0) {
-    if (!hidden || !topk_idx || !weight || !out || !blocks4_ok(act, act_scale)) return MOE_ERR_INVALID_ARG;
+  if (2 * (int64_t)f * (moe::padded_cols4(d.H) / 32) >= (int64_t)1 << 31 ||
+      (int64_t)d.H * (moe::padded_cols4(f) / 32) >= (int64_t)1 << 31)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" int moex4_experts_work(moe_plan_t h, int32_t f, int64_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  const int rc = check_few(h, f);
+  if (rc == MOE_OK) *bytes = moe::experts_work_bytes(h->d, f);
+  return rc;
+}
+
+extern "C" int moex4_experts(moe_plan_t h, const uint16_t* hidden, const int32_t* topk_idx, const float* weight,
+                             int32_t w_bits, int32_t f, const uint8_t* w1, const uint8_t* w1_scale, const uint8_t* w2,
+                             const uint8_t* w2_scale, uint8_t* work, uint16_t* out, void* stream) {
+  if (w_bits != 4 && w_bits != 8) return MOE_ERR_INVALID_ARG;
+  const int rc = check_few(h, f);
+  if (rc != MOE_OK) return rc;
+  if (h->d.T > 0) {
+    if (!hidden || !topk_idx || !weight || !out || !work || !aligned(work, 16)) return MOE_ERR_INVALID_ARG;
     if (w_bits == 4 ? !blocks4_ok(w1, w1_scale) || !blocks4_ok(w2, w2_scale)
                     : !blocks_ok(w1, w1_scale) || !blocks_ok(w2, w2_scale))
       return MOE_ERR_INVALID_ARG;
   }
   const DeviceScope on_device(h->device);
   if (!on_device.ok()) return MOE_ERR_HIP;
-  return hip_rc(moe::launch_experts(d, hidden, topk_idx, weight, w_bits, f, w1, w1_scale, w2, w2_scale, act, act_scale,
-                                    out, h->ws.status, begin_call(h, stream)));
+  return hip_rc(moe::launch_experts(h->d, hidden, topk_idx, weight, w_bits, f, w1, w1_scale, w2, w2_scale, work, out,
+                                    h->ws.status, begin_call(h, stream)));
 }

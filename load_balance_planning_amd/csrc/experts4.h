@@ -22,9 +22,9 @@ int64_t matmul4_tiles(const Instances& in, int32_t n);  // workgroups of launch_
 hipError_t launch_matmul4(const Instances& in, int32_t x_bits, const uint8_t* x, const uint8_t* xs, const uint8_t* w,
                           const uint8_t* ws, int32_t n, int32_t k, uint16_t* y, int32_t* status, hipStream_t st);
 
+int64_t experts_work_bytes(const Dims& d, int32_t f);
 hipError_t launch_experts(const Dims& d, const uint16_t* hidden, const int32_t* topk_idx, const float* weight,
                           int32_t w_bits, int32_t f, const uint8_t* w1, const uint8_t* w1s, const uint8_t* w2,
-                          const uint8_t* w2s, uint8_t* act, uint8_t* act_scale, uint16_t* out, int32_t* status,
-                          hipStream_t st);
+                          const uint8_t* w2s, uint8_t* work, uint16_t* out, int32_t* status, hipStream_t st);
 
 }  // namespace moe

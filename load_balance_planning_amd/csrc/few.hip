@@ -5,13 +5,14 @@
 //
 // Q rounds to e4m3 with a power-of-two scale per 32.  What bounds both launches
 // is the matrices' bytes, once each, so the tokens of an expert are one operand
-// of the matrix instruction (16 columns of it, mostly empty) and an expert's
-// rows go straight from memory to registers.  With a scale per 32 of the summed
-// axis a workgroup of 32 channels quantizes its activations by itself; the
-// instruction takes such scales as they are.
+// of the matrix instruction (its columns, mostly empty) and an expert's rows go
+// straight from memory to registers.  With a scale per 32 of the summed axis a
+// workgroup of 32 channels quantizes its activations by itself, and a lane holds
+// whole blocks.
 //
 // Which tokens an expert has is found by every workgroup from the top-k (at most
-// 2048 numbers): a 64-bit mask of tokens per expert, in LDS.
+// 2048 numbers).
+#include "buffers.h"
 #include "experts4.h"
 #include "fp4_block.h"
 #include "lane_group.h"
@@ -23,29 +24,49 @@ namespace {
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kFp8 = 0, kFp4 = 4;  // the instruction's format codes
-constexpr int kColsF = 16;         // tokens of a tile
+[[maybe_unused]] constexpr int kFp8 = 0, kFp4 = 4;  // the instruction's format codes
 
-__device__ __forceinline__ v4i load16b(const uint8_t* p) { return *reinterpret_cast<const v4i*>(p); }
-
-// Experts that have tokens, ascending, and the slots t * k + j of each, tokens
-// ascending.  In dynamic LDS: masks u64 [E], first int32 [cap + 1], expert and
-// slot uint16 [cap], [T * k]; cap = min(E, T * k).
+// What there is to multiply: entries of an expert and up to 16 of its slots t * k +
+// j (tokens ascending; one operand of the instruction).  In dynamic LDS: masks u64
+// [E] of tokens, then per entry its first place in the list of slots, int32 [cap +
+// 1], and its expert, uint16 [cap], then the list, uint16 [T * k].  Experts ascend.
+constexpr int kCols = 16;
 struct Chosen {
   uint64_t* mask;
-  int32_t* first;    // slots of experts before this one; entry n: all
+  int32_t* first;
   uint16_t* expert;
   uint16_t* slot;
   int n;
+  struct One {
+    int expert, first, count;
+  };
+  __device__ __forceinline__ One one(int a) const {
+    One o;
+    o.expert = __builtin_amdgcn_readfirstlane(expert[a]);
+    o.first = __builtin_amdgcn_readfirstlane(first[a]);
+    o.count = __builtin_amdgcn_readfirstlane(first[a + 1]) - o.first;
+    return o;
+  }
+  // slot `which` of an entry, -1 if there are no more
+  __device__ __forceinline__ int slot_of(const One& o, int which) const {
+    return which < o.count ? slot[o.first + which] : -1;
+  }
 };
-__host__ __device__ inline int chosen_cap(const Dims& d) { return d.E < d.T * d.k ? d.E : d.T * d.k; }
+// Entries at most: an expert's first, and one more for every 16 slots.
+__host__ __device__ inline int chosen_cap(const Dims& d) {
+  const int slots = d.T * d.k;
+  return (d.E < slots ? d.E : slots) + (d.T > kCols ? slots / kCols : 0);
+}
 __host__ __device__ inline size_t chosen_lds(const Dims& d) {
   return ((size_t)8 * d.E + 4 * (chosen_cap(d) + 1) + 2 * chosen_cap(d) + 2 * d.T * d.k + 15) / 16 * 16;
 }
 
 template <int THREADS>
-__device__ __forceinline__ Chosen collect(const Dims& d, const int32_t* __restrict__ topk, unsigned char* lds,
+__device__ __forceinline__ Chosen collect_lds(const Dims& d, const int32_t* __restrict__ topk, unsigned char* lds,
                                           int32_t* status) {
   __shared__ int32_t sums[THREADS / 64];
   const int slots = d.T * d.k, cap = chosen_cap(d);
@@ -77,12 +98,12 @@ __device__ __forceinline__ Chosen collect(const Dims& d, const int32_t* __restri
   }
   if (bad && status && blockIdx.x == 0) atomicOr(status, MOE_STATUS_BAD_TOPK);
   __syncthreads();
-  // experts with tokens and their slots, counted together: 16 bits each
+  // entries and their slots, counted together: 16 bits each
   const int per = (d.E + THREADS - 1) / THREADS, from = threadIdx.x * per;
   int mine = 0;
   for (int i = from; i < min(from + per, d.E); ++i) {
     const int m = __popcll(c.mask[i]);
-    mine += m ? 0x10000 + m : 0;
+    mine += (m + kCols - 1) / kCols * 0x10000 + m;
   }
   int incl = mine;
 #pragma unroll
@@ -100,17 +121,15 @@ __device__ __forceinline__ Chosen collect(const Dims& d, const int32_t* __restri
   }
   c.n = all >> 16;
   for (int i = from; i < min(from + per, d.E); ++i) {
-    const uint64_t set = c.mask[i];
-    if (!set) continue;
-    const int m = __popcll(set);
-    c.expert[before >> 16] = (uint16_t)i;
-    c.first[before >> 16] = before & 0xffff;
-    // the slots' places need the mask no more than the place: it holds the tokens still
-    before += 0x10000 + m;
+    for (int m = __popcll(c.mask[i]); m > 0; m -= kCols) {
+      c.expert[before >> 16] = (uint16_t)i;
+      c.first[before >> 16] = before & 0xffff;
+      before += 0x10000 + min(m, kCols);
+    }
   }
   if (threadIdx.x == 0) c.first[c.n] = all & 0xffff;
   __syncthreads();
-  // each slot to its expert's list: the expert's index by bisection
+  // each slot to its place: the expert's first entry by bisection
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int s = threadIdx.x + i * THREADS;
@@ -129,323 +148,613 @@ __device__ __forceinline__ Chosen collect(const Dims& d, const int32_t* __restri
   return c;
 }
 
-// 16 values of a row from column c on, packed; zeros from column `cols` on.
-__device__ __forceinline__ void load16_packed(const uint16_t* __restrict__ x, int64_t row_at, int c, int cols,
-                                              int64_t total, uint32_t* w) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int o = c + 8 * h;
-    u32x4 v = {0u, 0u, 0u, 0u};
-    if (o + 8 <= cols) {
-      v = *reinterpret_cast<const u32x4_any*>(x + row_at + o);
-    } else if (o < cols) {
-      v = row_at + o + 8 <= total ? (u32x4) * reinterpret_cast<const u32x4_any*>(x + row_at + o)
-                                  : load8_edge(x, row_at + o, total);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] &= (o + 2 * i < cols ? 0xffffu : 0u) | (o + 2 * i + 1 < cols ? 0xffff0000u : 0u);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[4 * h + i] = v[i];
+// The same where there are at most 64 slots, one to a lane, in every wave's
+// registers: no barrier, and a few instructions a slot.  Entries in the order of
+// their first slots.
+struct ChosenSmall {
+  int e;      // of the lane's slot; -1: none
+  int order;  // of the slot among its expert's
+  int rank;   // of the slot's entry where it is the entry's first; -1 elsewhere
+  int n;
+  struct One {
+    int expert, count, list;  // list: lane i has the entry's slot i
+  };
+  __device__ __forceinline__ One one(int a) const {
+    const int lane = threadIdx.x & 63, lead = (int)__builtin_ctzll(__ballot(rank == a));
+    One o;
+    o.expert = __builtin_amdgcn_readlane(e, lead);
+    const bool mine = e == o.expert && order / kCols == __builtin_amdgcn_readlane(order, lead) / kCols;
+    const uint64_t set = __ballot(mine), below = (1ull << lane) - 1ull;
+    o.count = __popcll(set);
+    // other slots go behind, so that every lane has one place
+    const int place = mine ? __popcll(set & below) : o.count + __popcll(~set & below);
+    o.list = __builtin_amdgcn_ds_permute(4 * place, lane);
+    return o;
   }
+  __device__ __forceinline__ int slot_of(const One& o, int which) const {
+    const int s = __builtin_amdgcn_ds_bpermute(4 * (which & 63), o.list);
+    return which < o.count ? s : -1;
+  }
+};
+__device__ __forceinline__ ChosenSmall collect_small(const Dims& d, const int32_t* __restrict__ topk, int32_t* status) {
+  const int slots = d.T * d.k, lane = threadIdx.x & 63;
+  ChosenSmall c;
+  c.e = lane < slots ? topk[lane] : -1;
+  bool bad = lane < slots && (unsigned)c.e >= (unsigned)d.E;
+  if (bad) c.e = -1;
+  c.order = 0;
+  uint64_t leader = 0ull;
+  for (int i = 0; i < slots; ++i) {
+    const int ei = __builtin_amdgcn_readlane(c.e, i);
+    const uint64_t same = __ballot(c.e == ei);
+    const int order = __popcll(same & ((1ull << i) - 1ull));
+    if (ei >= 0 && order % kCols == 0) leader |= 1ull << i;
+    if (lane == i) c.order = order;
+    // a slot of the same token with the same expert
+    bad |= ei >= 0 && lane == i && (same & ~(1ull << i) & (((1ull << d.k) - 1ull) << (i / d.k * d.k))) != 0ull;
+  }
+  c.n = __popcll(leader);
+  c.rank = leader >> lane & 1ull ? __popcll(leader & ((1ull << lane) - 1ull)) : -1;
+  if (status && blockIdx.x == 0 && threadIdx.x < 64 && __ballot(bad) != 0ull && lane == 0)
+    atomicOr(status, MOE_STATUS_BAD_TOPK);
+  return c;
+}
+template <bool SMALL, int THREADS>
+__device__ __forceinline__ auto collect(const Dims& d, const int32_t* __restrict__ topk, unsigned char* lds,
+                                        int32_t* status) {
+  if constexpr (SMALL)
+    return collect_small(d, topk, status);
+  else
+    return collect_lds<THREADS>(d, topk, lds, status);
 }
 
-typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+// Eight values of a row from column c on; zeros from column `cols` on.
+[[maybe_unused]] __device__ __forceinline__ u32x4 load8_row(const uint16_t* __restrict__ x, int64_t row_at, int c, int cols,
+                                           int64_t total) {
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if (c >= cols) return v;
+  v = row_at + c + 8 <= total ? (u32x4) * reinterpret_cast<const u32x4_any*>(x + row_at + c)
+                              : load8_edge(x, row_at + c, total);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] &= (c + 2 * i < cols ? 0xffffu : 0u) | (c + 2 * i + 1 < cols ? 0xffff0000u : 0u);
+  return v;
+}
+
 __device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
 }
 
-// Four words of bf16 pairs over the scale 2^(s - 127) to eight e4m3 bytes.
-__device__ __forceinline__ uint32_t pack4_e4m3(uint32_t a, uint32_t b, float scale) {
-  typedef short s16x2 __attribute__((ext_vector_type(2)));
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  s16x2 o = {0, 0};
-  o = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(o, __builtin_bit_cast(bf16x2, a), scale, false);
-  o = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(o, __builtin_bit_cast(bf16x2, b), scale, true);
-  return __builtin_bit_cast(uint32_t, o);
-}
+// A word's pair.  (By value: a bit cast of a vector's element reads element 0.)
+__device__ __forceinline__ bf16x2 two_bf16(uint32_t w) { return __builtin_bit_cast(bf16x2, w); }
 
-// A 128-step of 16 tokens' rows as the instruction's second operand: this lane's
-// 16 values from column c + 16 g on and 16 from c + 64 + 16 g on, which are
-// halves of blocks g / 2 and 2 + g / 2 of 32; and block g's scale.
-__device__ __forceinline__ v8i quantize_step(const uint32_t* lo, const uint32_t* hi, int lane, int* scale) {
-  uint32_t ml = 0, mh = 0;
+// What eight values of a row become by rounding to e4m3 with a scale per 32, as
+// bf16 again: the four lanes of an aligned quad hold a block.  All NaN where that
+// holds a NaN or an infinity.
+[[maybe_unused]] __device__ __forceinline__ u32x4 round8(u32x4 x) {
+  typedef short s16x2 __attribute__((ext_vector_type(2)));
+  uint32_t top = x[0] & 0x7fff7fffu;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    ml = pk_max(ml, lo[i] & 0x7fff7fffu);
-    mh = pk_max(mh, hi[i] & 0x7fff7fffu);
-  }
-  uint32_t top = max(ml & 0xffffu, ml >> 16) | max(mh & 0xffffu, mh >> 16) << 16;  // one of each half
-  top = pk_max(top, (uint32_t)__builtin_amdgcn_ds_swizzle((int)top, (16 << 10) | 0x1F));  // with lane ^ 16
-  const uint32_t sl = scale_byte(top << 16), sh = scale_byte(top & 0xffff0000u);
-  const float fl = sl == 255u ? 1.0f : scale_value(sl), fh = sh == 255u ? 1.0f : scale_value(sh);
-  v8i o;
+  for (int i = 1; i < 4; ++i) top = pk_max(top, x[i] & 0x7fff7fffu);
+  top = max(top << 16, top & 0xffff0000u);
+  top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xf, 0xf, false));
+  top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x4E, 0xf, 0xf, false));
+  const float by = __uint_as_float(scale_byte(top) << 23);  // the conversions take its exponent, 255 for NaN
+  u32x4 o;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    o[i] = (int)pack4_e4m3(lo[2 * i], lo[2 * i + 1], fl);
-    o[4 + i] = (int)pack4_e4m3(hi[2 * i], hi[2 * i + 1], fh);
+  for (int i = 0; i < 4; i += 2) {
+    s16x2 q = {0, 0};
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(q, two_bf16(x[i]), by, false);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(q, two_bf16(x[i + 1]), by, true);
+    const uint32_t p = __builtin_bit_cast(uint32_t, q);
+    o[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p, by, false));
+    o[i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p, by, true));
   }
-  // groups 1 and 2 hold one another's scales
-  const int g = lane >> 4;
-  const uint32_t both = sl | sh << 8;
-  const uint32_t from = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (g == 1 || g == 2 ? lane ^ 48 : lane), (int)both);
-  *scale = (int)(g < 2 ? from : from >> 8);
   return o;
 }
 
-// One instruction's share (16 rows by 128 columns) of matrices in WB bits: from
-// line b, half h.  `row` is the lane's row of the expert's matrix of `rows` rows.
+// Only the device pass knows buffers.
+#ifdef __HIP_DEVICE_COMPILE__
+// Rows [row0, row0 + rows) of an expert's matrix of `all` rows and `cols` columns
+// in WB bits, and their scales to the end of the expert's table.  A lane's row is
+// a 32-bit offset; rows past the end read as zeros.
 template <int WB>
 struct Matrix {
-  const uint8_t* q;
-  const uint8_t* s;
-  int64_t row_bytes, scale_step;
+  __amdgpu_buffer_rsrc_t q, s;
+  uint32_t row_bytes, s_step;  // s_step: scale bytes from line to line (4 bits), from 128 rows to the next (8 bits)
 };
 template <int WB>
-__device__ __forceinline__ Matrix<WB> matrix_row(const uint8_t* __restrict__ w, const uint8_t* __restrict__ ws,
-                                                 int expert, int rows, int row, int cols, int g) {
+__device__ __forceinline__ Matrix<WB> matrix_rows(const uint8_t* __restrict__ w, const uint8_t* __restrict__ ws,
+                                                  int expert, int all, int row0, int rows, int cols) {
   Matrix<WB> m;
   if (WB == 4) {
     const int nb = (cols + kCols4 - 1) / kCols4;
-    m.row_bytes = (int64_t)nb * (kCols4 / 2);
-    m.q = w + ((int64_t)expert * rows + row) * m.row_bytes + 16 * g;
-    m.s = ws + ((int64_t)expert * nb * rows + row) * 8;
-    m.scale_step = (int64_t)rows * 8;
+    m.row_bytes = (uint32_t)nb * (kCols4 / 2);
+    m.s_step = (uint32_t)all * 8;
+    m.s = buffer_of(ws + ((int64_t)expert * nb * all + row0) * 8, (uint32_t)nb * m.s_step - 8 * row0);
   } else {
-    const int nb = (cols + kBlk - 1) / kBlk, ns = (nb + 3) / 4 * 4;
-    m.row_bytes = (int64_t)nb * kBlk;
-    m.q = w + ((int64_t)expert * rows + row) * m.row_bytes + 16 * g;
-    m.s = ws + ((int64_t)expert * ((rows + kBlk - 1) / kBlk) + row / kBlk) * ns;
-    m.scale_step = 2;
+    const int nb = (cols + kBlk - 1) / kBlk;
+    m.row_bytes = (uint32_t)nb * kBlk;
+    m.s_step = (uint32_t)(nb + 3) / 4 * 4;
+    const uint32_t table = (uint32_t)((all + kBlk - 1) / kBlk) * m.s_step;
+    m.s = buffer_of(ws + (int64_t)expert * table, table);
   }
+  m.q = buffer_of(w + ((int64_t)expert * all + row0) * m.row_bytes, (uint32_t)rows * m.row_bytes);
   return m;
 }
-// The operands of a line: both halves (8 bits: the second only if it is there).
-template <int WB>
-struct Line {
-  v8i v[2];
-  uint32_t s[2];
-};
-template <int WB>
-__device__ __forceinline__ Line<WB> load_line(const Matrix<WB>& m, int b, bool second, int g) {
-  Line<WB> l;
-  if (WB == 4) {
-    const u32x2 s = *reinterpret_cast<const u32x2*>(m.s + b * m.scale_step);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const v4i v = load16b(m.q + (int64_t)b * (kCols4 / 2) + 64 * h);
-      l.v[h] = v8i{v[0], v[1], v[2], v[3], 0, 0, 0, 0};
-      l.s[h] = s[h] >> (8 * g);
-    }
-  } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int at = 2 * b + (second ? h : 0);
-      const v4i lo = load16b(m.q + (int64_t)at * kBlk), hi = load16b(m.q + (int64_t)at * kBlk + 64);
-      l.v[h] = v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      l.s[h] = m.s[at];
-    }
-  }
-  return l;
-}
-template <int WB>
-__device__ __forceinline__ v4f multiply(const Line<WB>& l, int h, const v8i& x, int sx, const v4f& acc) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(l.v[h], x, acc, WB == 4 ? kFp4 : kFp8, kFp8, 0, (int)l.s[h],
-                                                          0, sx);
+__device__ __forceinline__ v4i load16b(__amdgpu_buffer_rsrc_t b, uint32_t at, uint32_t line) {
+  return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(b, (int)at, (int)line, 0));
 }
 
-// 32 gate and 32 up channels of one expert per unit; the four waves take every
-// fourth line of the long axis each and add their sums in LDS.
-constexpr int kUpThreads = 256, kChan = 32;
+// How many blocks of 128 columns a step has: 4 bits: a line of 256 columns, 8
+// bits: 128 columns.
+constexpr int halves(int bits) { return bits == 4 ? 2 : 1; }
+
+// acc += values * x over a step's half: lane (r, g) has row r's columns, 4 bits: 32
+// g .. + 31 of the half; 8 bits: 16 g .. + 15 and 64 + 16 g .. + 15.  s: their scale.
 template <int WB>
-__global__ __launch_bounds__(kUpThreads) void experts_up_kernel(Dims d, const uint16_t* __restrict__ hidden,
-                                                                const int32_t* __restrict__ topk,
-                                                                const uint8_t* __restrict__ w,
-                                                                const uint8_t* __restrict__ ws, int f,
-                                                                uint8_t* __restrict__ act,
-                                                                uint8_t* __restrict__ act_scale,
-                                                                int32_t* __restrict__ status) {
+__device__ __forceinline__ v4f multiply(u32x4 q0, u32x4 q1, uint32_t s, const u32x4* x, v4f acc) {
+  const float by = __uint_as_float(s << 23);  // the conversions take its exponent, 255 for NaN
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {  // eight columns
+    union {
+      bf16x2 two[4];
+      bf16x8 all;
+    } a, c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c.two[i] = two_bf16(x[p][i]);
+    if constexpr (WB == 4) {
+      const uint32_t q = q0[p];
+      a.two[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, by, 0);
+      a.two[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, by, 1);
+      a.two[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, by, 2);
+      a.two[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, by, 3);
+    } else {
+      const uint32_t lo = p < 2 ? q0[2 * p] : q1[2 * p - 4], hi = p < 2 ? q0[2 * p + 1] : q1[2 * p - 3];
+      a.two[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, by, false);
+      a.two[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, by, true);
+      a.two[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, by, false);
+      a.two[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, by, true);
+    }
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.all, c.all, acc, 0, 0, 0);
+  }
+  return acc;
+}
+#endif
+
+// 32 gate and 32 up channels of one entry per unit; the waves take steps of the
+// long axis in turn and add their sums in LDS.
+//
+// The products are the bf16 instruction's, of values that are exact in bf16: the
+// 8-bit one cuts products off at 2^-13 of a neighbour's, and sums so far off
+// (2^-16 of their root mean square) round some activations to the other e4m3
+// neighbour, 6 % of their value away.
+//
+// A step's loads are few, so that the cache's ports keep up with memory: the
+// matrices' lines; one load for the scales of all 64 rows; and of the tokens' rows
+// what there is of them, the lanes side by side (two tokens a load).  Scales and
+// rows (rounded) pass through LDS, the wave's own part of it, to the lanes that
+// multiply.  Loaded by those lanes each for itself, scales took 8 % and rows 14 %
+// of the time (28 experts of 2 x 2688 x 7168: 132 us), and registers for a second
+// step's loads cost more waves than they were worth.
+constexpr int kChan = 32;
+template <int WB, int WAVES, bool SMALL>
+__global__ __launch_bounds__(64 * WAVES, 2) void experts_up_kernel(Dims d, const uint16_t* __restrict__ hidden,
+                                                                   const int32_t* __restrict__ topk,
+                                                                   const uint8_t* __restrict__ w,
+                                                                   const uint8_t* __restrict__ ws, int f,
+                                                                   uint8_t* __restrict__ act,
+                                                                   uint8_t* __restrict__ act_scale,
+                                                                   uint32_t* __restrict__ counter, int counters,
+                                                                   int32_t* __restrict__ status) {
+#ifdef __HIP_DEVICE_COMPILE__
+  constexpr int kHalves = halves(WB), kChunks = 16 * kHalves;   // chunks of 8 columns of a token's step
+  constexpr int kAtOnce = 64 / kChunks, kSets = kCols / kAtOnce;  // tokens of a load, loads of 16 tokens
+  constexpr int kPart = kCols * (2 * kChan + 4) * 4, kRows = kCols * kChunks * 16;
   extern __shared__ __align__(16) unsigned char lds[];
-  __shared__ float part[4][kColsF][2 * kChan + 4];
-  const Chosen ch = collect<kUpThreads>(d, topk, lds, status);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  // a wave's rows of a step, and then its sums
+  __shared__ __align__(16) unsigned char own_s[WAVES][kRows > kPart ? kRows : kPart];
+  __shared__ __align__(16) uint32_t scale_s[WAVES][64 * kHalves];
+  if (blockIdx.x == 0)  // for the launch behind this one
+    for (int i = threadIdx.x; i < counters; i += 64 * WAVES) counter[i] = 0u;
+  const auto ch = collect<SMALL, 64 * WAVES>(d, topk, lds, status);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int chunks = (f + kChan - 1) / kChan, units = ch.n * chunks;
-  const int fp = (int)padded_cols4(f), steps = (d.H + kBlk - 1) / kBlk, lines = (steps + 1) / 2;
+  const int fp = (int)padded_cols4(f), steps = (d.H + kHalves * kBlk - 1) / (kHalves * kBlk);
+  const int whole = d.H / (kHalves * kBlk);  // steps before a row's end
   const int64_t total = (int64_t)d.T * d.H;
+  unsigned char* const rows_s = own_s[wave];
+  uint32_t* const sc_s = scale_s[wave];
+  // unit = a * chunks + chunk, stepped without divisions
+  const int step_a = (int)gridDim.x / chunks, step_c = (int)gridDim.x - step_a * chunks;
+  int a = (int)blockIdx.x / chunks, chunk = (int)blockIdx.x - a * chunks;
   for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const int a = unit / chunks, chunk = unit - a * chunks, c0 = chunk * kChan;
-    const int expert = ch.expert[a], first = ch.first[a], count = ch.first[a + 1] - first;
-    Matrix<WB> m[4];
+    const int c0 = chunk * kChan, valid = min(kChan, f - c0);
+    const auto one = ch.one(a);
+    const Matrix<WB> gate = matrix_rows<WB>(w, ws, one.expert, 2 * f, c0, valid, d.H);
+    const Matrix<WB> up = matrix_rows<WB>(w, ws, one.expert, 2 * f, f + c0, valid, d.H);
+    // this lane's rows of the matrices, and the one of the 64 whose scales it loads
+    const uint32_t at = (uint32_t)r * gate.row_bytes + 16 * g, at_16 = at + 16 * gate.row_bytes;
+    const int s_row = min(lane & 31, valid - 1) + (lane >= 32 ? f : 0);
+    const uint32_t s_at = WB == 4 ? (uint32_t)s_row * 8 : (uint32_t)((c0 + s_row) / kBlk) * gate.s_step;
+    uint32_t from[kSets];  // elements of the tokens' rows that this lane loads
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      m[i] = matrix_row<WB>(w, ws, expert, 2 * f, (i >> 1) * f + min(c0 + 16 * (i & 1) + r, f - 1), d.H, g);
-    for (int t0 = 0; t0 < count; t0 += kColsF) {
-      const int slot = t0 + r < count ? ch.slot[first + t0 + r] : -1;
-      const int64_t row_at = (int64_t)(max(slot, 0) / d.k) * d.H;
-      v4f acc[4];
+    for (int i = 0; i < kSets; ++i)
+      from[i] = (uint32_t)(max(ch.slot_of(one, i * kAtOnce + lane / kChunks), 0) / d.k) * d.H + 8 * (lane % kChunks);
+    struct Step {
+      u32x4 q[4][2];
+      u32x2 s;
+      u32x4 x[kSets];
+    };
+    auto load = [&](Step* o, int b) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = v4f{0, 0, 0, 0};
-      for (int b = wave; b < lines; b += 4) {
-        const bool second = 2 * b + 1 < steps;
-        Line<WB> l[4];
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) l[i] = load_line<WB>(m[i], b, second, g);
-        uint32_t x[2][2][8];
+        for (int p = 0; p < 2; ++p)
+          o->q[i][p] = __builtin_bit_cast(u32x4, load16b(i < 2 ? gate.q : up.q, (i & 1 ? at_16 : at) + 64 * p, b * kBlk));
+      if constexpr (WB == 4)
+        o->s = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(gate.s, (int)s_at, b * (int)gate.s_step, 0));
+      else
+        o->s[0] = __builtin_amdgcn_raw_buffer_load_b8(gate.s, (int)s_at, b, 0);
+      if (b >= whole) return;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+      for (int i = 0; i < kSets; ++i) {
+        if (i * kAtOnce >= one.count) break;
+        o->x[i] = *reinterpret_cast<const u32x4_any*>(hidden + from[i] + b * kHalves * kBlk);
+      }
+    };
+    v4f acc[4];
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
+    for (int i = 0; i < 4; ++i) acc[i] = v4f{0, 0, 0, 0};
+    Step next;
+    if (wave < steps) load(&next, wave);
+    for (int b = wave; b < steps; b += WAVES) {
+      // rows and scales to LDS: token t's chunk c lies at c ^ t, so that 16 tokens' lie apart
+      auto put = [&](int i, const u32x4& v) {
+        const int t = i * kAtOnce + lane / kChunks;
+        *reinterpret_cast<u32x4*>(rows_s + (t * kChunks + ((lane % kChunks) ^ t)) * 16) = round8(v);
+      };
+      if (b < whole) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[h][p][i] = 0u;
-            if (slot >= 0)
-              load16_packed(hidden, row_at, (2 * b + h) * kBlk + 64 * p + 16 * g, d.H, total, x[h][p]);
-          }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h == 1 && !second) break;
-          int sx;
-          const v8i xv = quantize_step(x[h][0], x[h][1], lane, &sx);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[i] = multiply<WB>(l[i], h, xv, sx, acc[i]);
+        for (int i = 0; i < kSets; ++i) {
+          if (i * kAtOnce >= one.count) break;
+          put(i, next.x[i]);
+        }
+      } else {  // the rows' end, loaded here: its edges would take the registers of every step
+#pragma unroll 1
+        for (int i = 0; i * kAtOnce < one.count; ++i) {
+          const int64_t row_at = (int64_t)(max(ch.slot_of(one, i * kAtOnce + lane / kChunks), 0) / d.k) * d.H;
+          put(i, load8_row(hidden, row_at, b * kHalves * kBlk + 8 * (lane % kChunks), d.H, total));
         }
       }
+      if (WB == 4)
+        *reinterpret_cast<u32x2*>(sc_s + 2 * lane) = next.s;
+      else
+        sc_s[lane] = next.s[0];
+      u32x4 q[4][2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<v4f*>(&part[wave][r][16 * i + 4 * g]) = acc[i];
-      __syncthreads();
-      {
-        const int row = threadIdx.x >> 4, c = 2 * (threadIdx.x & 15);
-        float v[2];
-        uint32_t top = 0;
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float gate = part[0][row][c + j], up = part[0][row][kChan + c + j];
+        for (int p = 0; p < 2; ++p) q[i][p] = next.q[i][p];
+      wave_lds_sync();
+      if (b + WAVES < steps) load(&next, b + WAVES);
+      u32x2 s[4];
 #pragma unroll
-          for (int q = 1; q < 4; ++q) {
-            gate += part[q][row][c + j];
-            up += part[q][row][kChan + c + j];
-          }
-          v[j] = c0 + c + j < f ? swiglu(gate, up) : 0.0f;
-          top = max(top, magnitude(v[j]));
-        }
-        top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xf, 0xf, false));
-        top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x4E, 0xf, 0xf, false));
-        top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x141, 0xf, 0xf, false));
-        top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x140, 0xf, 0xf, false));
-        if (t0 + row < count) {
-          const uint32_t s = scale_byte(top);
-          const float inv = inverse_scale(s);
-          const int64_t at = ch.slot[first + t0 + row];
-          uint8_t* dst = act + at * fp + c0 + c;
-          *reinterpret_cast<uint16_t*>(dst) = (uint16_t)pack_e4m3(v[0] * inv, v[1] * inv, 0.0f, 0.0f);
-          uint8_t* sc = act_scale + at * (fp / kBlk4) + chunk;
-          if (c == 0) *sc = (uint8_t)s;
-          if (chunk == chunks - 1)  // zeros up to the line's end
-            for (int z = 1; c0 + z * kChan < fp; ++z) {
-              *reinterpret_cast<uint16_t*>(dst + z * kChan) = 0;
-              if (c == 0) sc[z] = 127;
-            }
-        }
+      for (int i = 0; i < 4; ++i) {
+        if (WB == 4)
+          s[i] = *reinterpret_cast<const u32x2*>(sc_s + 2 * (16 * i + r));
+        else
+          s[i][0] = sc_s[16 * i + r];
       }
-      __syncthreads();
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        u32x4 x[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const int c = WB == 4 ? 16 * h + 4 * g + p : (p & 1) + 8 * (p >> 1) + 2 * g;
+          x[p] = *reinterpret_cast<const u32x4*>(rows_s + (r * kChunks + (c ^ r)) * 16);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          acc[i] = WB == 4 ? multiply<WB>(q[i][h], q[i][h], s[i][h] >> (8 * g) & 0xffu, x, acc[i])
+                           : multiply<WB>(q[i][0], q[i][1], s[i][0], x, acc[i]);
+      }
+      wave_lds_sync();
+    }
+    float* const part = reinterpret_cast<float*>(rows_s);  // [kCols][2 kChan + 4]
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<v4f*>(part + r * (2 * kChan + 4) + 16 * i + 4 * g) = acc[i];
+    __syncthreads();
+    if (WAVES == 4 || threadIdx.x < 256) {
+      const int row = threadIdx.x >> 4, c = 2 * (threadIdx.x & 15);
+      float v[2];
+      uint32_t top = 0;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float gv = 0.0f, uv = 0.0f;
+#pragma unroll
+        for (int q = 0; q < WAVES; ++q) {
+          const float* p = reinterpret_cast<const float*>(own_s[q]) + row * (2 * kChan + 4) + c + j;
+          gv += p[0];
+          uv += p[kChan];
+        }
+        v[j] = c0 + c + j < f ? swiglu(gv, uv) : 0.0f;
+        top = max(top, magnitude(v[j]));
+      }
+      top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xf, 0xf, false));
+      top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x4E, 0xf, 0xf, false));
+      top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x141, 0xf, 0xf, false));
+      top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x140, 0xf, 0xf, false));
+      const int64_t to = ch.slot_of(one, row);
+      if (to >= 0) {
+        const uint32_t s = scale_byte(top);
+        const float inv = inverse_scale(s);
+        uint8_t* dst = act + to * fp + c0 + c;
+        *reinterpret_cast<uint16_t*>(dst) = (uint16_t)pack_e4m3(v[0] * inv, v[1] * inv, 0.0f, 0.0f);
+        uint8_t* sc = act_scale + to * (fp / kBlk4) + chunk;
+        if (c == 0) *sc = (uint8_t)s;
+        if (chunk == chunks - 1)  // zeros up to the line's end
+          for (int z = 1; c0 + z * kChan < fp; ++z) {
+            *reinterpret_cast<uint16_t*>(dst + z * kChan) = 0;
+            if (c == 0) sc[z] = 127;
+          }
+      }
+    }
+    __syncthreads();
+    a += step_a;
+    chunk += step_c;
+    if (chunk >= chunks) {
+      chunk -= chunks;
+      ++a;
     }
   }
+#endif
 }
 
-// 16 channels of the result per workgroup, over all experts with tokens: its
-// waves take pieces of experts' long axes in turn and add them, times the slots'
-// weights, to sums of their own in LDS.
-constexpr int kDownThreads = 512, kDownWaves = kDownThreads / 64, kOut = 16;
-template <int WB>
-__global__ __launch_bounds__(kDownThreads) void experts_down_kernel(Dims d, const int32_t* __restrict__ topk,
-                                                                    const float* __restrict__ weight,
-                                                                    const uint8_t* __restrict__ w,
-                                                                    const uint8_t* __restrict__ ws, int f,
-                                                                    const uint8_t* __restrict__ act,
-                                                                    const uint8_t* __restrict__ act_scale,
-                                                                    uint16_t* __restrict__ out) {
+// 32 channels of the result and a share of the entries' long axes per workgroup:
+// its waves take runs of steps and add them, times the slots' weights, to sums of
+// their own in LDS.  The shares of the same channels meet in memory: the workgroup
+// that is the last to write its sums adds them all, in order, and writes the result.
+//
+// Activations and scales pass through LDS as in the launch before.
+constexpr int kDownWaves = 4, kDownThreads = 64 * kDownWaves, kOut = 32, kMaxShares = 16;
+template <int WB, bool SMALL>
+__global__ __launch_bounds__(kDownThreads, 2) void experts_down_kernel(Dims d, const int32_t* __restrict__ topk,
+                                                                       const float* __restrict__ weight,
+                                                                       const uint8_t* __restrict__ w,
+                                                                       const uint8_t* __restrict__ ws, int f,
+                                                                       const uint8_t* __restrict__ act,
+                                                                       const uint8_t* __restrict__ act_scale,
+                                                                       int chunks, int shares, float* partial,
+                                                                       uint32_t* counter,
+                                                                       uint16_t* __restrict__ out) {
+#ifdef __HIP_DEVICE_COMPILE__
+  constexpr int kHalves = halves(WB), kPieces = 8 * kHalves;      // 16-byte pieces of a slot's step
+  constexpr int kAtOnce = 64 / kPieces, kSets = kCols / kAtOnce;  // slots of a load, loads of 16 slots
   extern __shared__ __align__(16) unsigned char lds[];
-  const Chosen ch = collect<kDownThreads>(d, topk, lds, nullptr);
-  float* sums = reinterpret_cast<float*>(lds + chosen_lds(d));  // [waves][T][kOut]
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ __align__(16) unsigned char act_s[kDownWaves][kCols * kPieces * 16];
+  __shared__ __align__(16) uint32_t act_scale_s[kDownWaves][kCols * kHalves];
+  __shared__ __align__(16) uint32_t scale_s[kDownWaves][kOut * kHalves];
+  __shared__ uint32_t arrived;
+  float* sums = reinterpret_cast<float*>(lds);  // [waves][T][kOut], the choice behind it
+  const int per_wave = d.T * kOut;
+  for (int i = threadIdx.x; i < kDownWaves * per_wave; i += kDownThreads) sums[i] = 0.0f;
+  const auto ch = collect<SMALL, kDownThreads>(d, topk, lds + sizeof(float) * kDownWaves * per_wave, nullptr);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  for (int i = threadIdx.x; i < kDownWaves * d.T * kOut; i += kDownThreads) sums[i] = 0.0f;
   __syncthreads();
-  float* mine = sums + wave * d.T * kOut;
-  const int c0 = blockIdx.x * kOut, row = min(c0 + r, d.H - 1);
-  const int fp = (int)padded_cols4(f), steps = (f + kBlk - 1) / kBlk, lines = fp / kCols4;
-  // as long pieces as leave every wave one, up to four lines
-  const int piece = max(1, min(4, ch.n * lines / kDownWaves)), pieces = (lines + piece - 1) / piece;
-  for (int item = wave; item < ch.n * pieces; item += kDownWaves) {
-    const int a = item / pieces, b0 = (item - a * pieces) * piece, b1 = min(b0 + piece, lines);
-    const int expert = ch.expert[a], first = ch.first[a], count = ch.first[a + 1] - first;
-    const Matrix<WB> m = matrix_row<WB>(w, ws, expert, d.H, row, f, g);
-    for (int t0 = 0; t0 < count; t0 += kColsF) {
-      const int slot = t0 + r < count ? ch.slot[first + t0 + r] : -1;
-      const float by = slot >= 0 ? weight[slot] : 0.0f;
-      const uint8_t* xq = act + (int64_t)max(slot, 0) * fp + 16 * g;
-      const uint8_t* xs = act_scale + (int64_t)max(slot, 0) * (fp / kBlk4);
-      v4f acc = {0, 0, 0, 0};
-      for (int b = b0; b < b1; ++b) {
-        const bool second = 2 * b + 1 < steps;
-        const Line<WB> l = load_line<WB>(m, b, second, g);
-        const u32x2 s = *reinterpret_cast<const u32x2*>(xs + 8 * b);
+  float* mine = sums + wave * per_wave;
+  const int share = blockIdx.x / chunks, chunk = blockIdx.x - share * chunks;
+  const int c0 = chunk * kOut, valid = min(kOut, d.H - c0);
+  const int fp = (int)padded_cols4(f), steps = (f + kHalves * kBlk - 1) / (kHalves * kBlk);
+  const auto act_buf = buffer_of(act, (uint32_t)(d.T * d.k) * fp);
+  const auto act_s_buf = buffer_of(act_scale, (uint32_t)(d.T * d.k) * (fp / kBlk4));
+  // this wave's run of the ch.n * steps steps
+  const int all = ch.n * steps, parts = shares * kDownWaves, part = share * kDownWaves + wave;
+  const int from = (int)((int64_t)all * part / parts), to = (int)((int64_t)all * (part + 1) / parts);
+  if (from < to) {
+    int a = from / steps, b = from - a * steps;
+    auto one = ch.one(a);
+    Matrix<WB> m;
+    uint32_t x_at[kSets], sx_at;
+    // entry a: its matrix; the activations that this lane loads (past the buffers
+    // where there is no slot: zeros)
+    auto begin = [&]() {
+      one = ch.one(a);
+      m = matrix_rows<WB>(w, ws, one.expert, d.H, c0, valid, f);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h == 1 && !second) break;
-          const v4i lo = load16b(xq + b * kCols4 + 128 * h), hi = load16b(xq + b * kCols4 + 128 * h + 64);
-          acc = multiply<WB>(l, h, v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]},
-                             (int)(s[h] >> (8 * g)), acc);
+      for (int i = 0; i < kSets; ++i) {
+        const int s = ch.slot_of(one, i * kAtOnce + lane / kPieces);
+        x_at[i] = s >= 0 ? (uint32_t)s * fp + 16 * (lane % kPieces) : 0x80000000u;
+      }
+      const int s = ch.slot_of(one, lane / kHalves);
+      sx_at = s >= 0 ? (uint32_t)s * (fp / kBlk4) + 4 * (lane % kHalves) : 0x80000000u;
+    };
+    begin();
+    const uint32_t at = (uint32_t)r * m.row_bytes + 16 * g, at_16 = at + 16 * m.row_bytes;
+    const uint32_t s_at = WB == 4 ? min(lane & 31, valid - 1) * 8 : (uint32_t)(c0 / kBlk) * m.s_step;
+    struct Step {
+      v4i q[2][2];
+      u32x2 s;
+      v4i x[kSets];
+      uint32_t sx;
+    };
+    auto load = [&](Step* o) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) o->q[i][p] = load16b(m.q, (i ? at_16 : at) + 64 * p, b * kBlk);
+      if constexpr (WB == 4)
+        o->s = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(m.s, (int)s_at, b * (int)m.s_step, 0));
+      else
+        o->s[0] = __builtin_amdgcn_raw_buffer_load_b8(m.s, (int)s_at, b, 0);
+#pragma unroll
+      for (int i = 0; i < kSets; ++i) {
+        if (i * kAtOnce >= one.count) break;
+        o->x[i] = load16b(act_buf, x_at[i], b * kHalves * kBlk);
+      }
+      o->sx = __builtin_amdgcn_raw_buffer_load_b32(act_s_buf, (int)sx_at, 4 * kHalves * b, 0);
+    };
+    // 16-byte place of a slot's piece: 16 slots' lie apart
+    auto place = [&](int slot, int p) {
+      return WB == 4 ? slot * 16 + (p ^ slot) : (slot >> 1) * 16 + (((slot & 1) << 3 | p) ^ (slot >> 1));
+    };
+    auto add = [&](int s, const v4f* acc) {
+      if (s < 0) return;
+      const float by = weight[s];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        v4f* sum = reinterpret_cast<v4f*>(mine + (s / d.k) * kOut + 16 * i + 4 * g);
+        v4f v = *sum;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] += by * acc[i][j];
+        *sum = v;
+      }
+    };
+    Step next;
+    load(&next);
+    v4f acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    for (int item = from; item < to; ++item) {
+      const auto entry = one;
+      const bool last = ++b == steps;  // of this entry
+#pragma unroll
+      for (int i = 0; i < kSets; ++i) {
+        if (i * kAtOnce >= entry.count) break;
+        *reinterpret_cast<v4i*>(act_s[wave] + place(i * kAtOnce + lane / kPieces, lane % kPieces) * 16) = next.x[i];
+      }
+      if (lane < kCols * kHalves) act_scale_s[wave][lane] = next.sx;
+      if (WB == 4 && lane < kOut) *reinterpret_cast<u32x2*>(scale_s[wave] + 2 * lane) = next.s;
+      const uint32_t s8 = next.s[0];
+      v4i q[2][2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) q[i][p] = next.q[i][p];
+      wave_lds_sync();
+      if (item + 1 < to) {
+        if (last) {
+          b = 0;
+          ++a;
+          begin();
+        }
+        load(&next);
+      }
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        const v4i lo = *reinterpret_cast<const v4i*>(act_s[wave] + place(r, 8 * h + g) * 16);
+        const v4i hi = *reinterpret_cast<const v4i*>(act_s[wave] + place(r, 8 * h + 4 + g) * 16);
+        const v8i xv = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        const uint32_t sx = act_scale_s[wave][r * kHalves + h] >> (8 * g);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const v4i q0 = q[i][h], q1 = q[i][1];
+          const v8i qv = WB == 4 ? v8i{q0[0], q0[1], q0[2], q0[3], 0, 0, 0, 0}
+                                 : v8i{q0[0], q0[1], q0[2], q0[3], q1[0], q1[1], q1[2], q1[3]};
+          const uint32_t s = WB == 4 ? scale_s[wave][2 * (16 * i + r) + h] >> (8 * g) : s8;
+          acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(qv, xv, acc[i], WB == 4 ? kFp4 : kFp8, kFp8, 0, (int)s,
+                                                                    0, (int)sx);
         }
       }
-      if (slot >= 0) {
-        v4f* to = reinterpret_cast<v4f*>(mine + (slot / d.k) * kOut + 4 * g);
-        v4f v = *to;
+      if (last || item + 1 == to) {
+        add(ch.slot_of(entry, r), acc);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] += by * acc[j];
-        *to = v;
+        for (int i = 0; i < 2; ++i) acc[i] = v4f{0, 0, 0, 0};
       }
+      wave_lds_sync();
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < d.T * kOut; i += kDownThreads) {
-    const int t = i / kOut, c = c0 + i % kOut;
+  float* own = partial + ((int64_t)chunk * shares + share) * per_wave;
+  for (int i = threadIdx.x; i < per_wave; i += kDownThreads) {
     float v = sums[i];
 #pragma unroll
-    for (int q = 1; q < kDownWaves; ++q) v += sums[q * d.T * kOut + i];
-    if (c < d.H) out[(int64_t)t * d.H + c] = (uint16_t)pack_bf16(v, 0.0f);
+    for (int q = 1; q < kDownWaves; ++q) v += sums[q * per_wave + i];
+    if (shares > 1)
+      __hip_atomic_store(own + i, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    else if (c0 + i % kOut < d.H)
+      out[(int64_t)(i / kOut) * d.H + c0 + i % kOut] = (uint16_t)pack_bf16(v, 0.0f);
   }
+  if (shares == 1) return;
+  // The sums were written through to where all XCDs see them, and are there before
+  // the arrival: the store of a device-wide atomic ends, for its wave's counter,
+  // where it is visible.  (Fences instead write back and drop whole L2s: 384
+  // workgroups took 27 us longer.)
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x == 0) arrived = __hip_atomic_fetch_add(counter + chunk, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (arrived != (uint32_t)shares - 1u) return;
+  const float* every = partial + (int64_t)chunk * shares * per_wave;
+  for (int i = threadIdx.x; i < per_wave; i += kDownThreads) {
+    float v = 0.0f;
+    for (int q = 0; q < shares; ++q)
+      v += __hip_atomic_load(every + (int64_t)q * per_wave + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (c0 + i % kOut < d.H) out[(int64_t)(i / kOut) * d.H + c0 + i % kOut] = (uint16_t)pack_bf16(v, 0.0f);
+  }
+#endif
 }
 
-template <int WB>
+// Where a call's memory goes: activations [T * k][fp], their scales [T * k][fp /
+// 32], a counter per 32 channels, the shares' sums.
+struct Work {
+  int fp, chunks, shares;
+  int64_t scale, counter, partial, bytes;
+};
+Work work_of(const Dims& d, int f) {
+  Work k;
+  k.fp = (int)padded_cols4(f);
+  k.chunks = (d.H + kOut - 1) / kOut;
+  // two workgroups for every CU, if there are that many lines
+  const int64_t lines = (int64_t)chosen_cap(d) * (k.fp / kCols4);
+  const int64_t most = (lines + kDownWaves - 1) / kDownWaves, want = (512 + k.chunks - 1) / k.chunks;
+  k.shares = (int)(want < most ? want : most);
+  if (k.shares > kMaxShares) k.shares = kMaxShares;
+  if (k.shares < 1) k.shares = 1;
+  const int64_t slots = (int64_t)d.T * d.k;
+  k.scale = slots * k.fp;
+  k.counter = (k.scale + slots * (k.fp / kBlk4) + 15) / 16 * 16;
+  k.partial = k.counter + ((int64_t)k.chunks * 4 + 15) / 16 * 16;
+  k.bytes = k.partial + (k.shares > 1 ? (int64_t)k.chunks * k.shares * d.T * kOut * 4 : 0);
+  return k;
+}
+
+template <int WB, bool SMALL, int WAVES>
 hipError_t launch(const Dims& d, const uint16_t* hidden, const int32_t* topk_idx, const float* weight, int32_t f,
-                  const uint8_t* w1, const uint8_t* w1s, const uint8_t* w2, const uint8_t* w2s, uint8_t* act,
-                  uint8_t* act_scale, uint16_t* out, int32_t* status, hipStream_t st) {
+                  const uint8_t* w1, const uint8_t* w1s, const uint8_t* w2, const uint8_t* w2s, uint8_t* work,
+                  uint16_t* out, int32_t* status, hipStream_t st) {
+  const Work k = work_of(d, f);
   const int64_t units = (int64_t)chosen_cap(d) * ((f + kChan - 1) / kChan);
-  const size_t lds = chosen_lds(d), sums = (size_t)kDownWaves * d.T * kOut * sizeof(float);
-  hipLaunchKernelGGL((experts_up_kernel<WB>), dim3((unsigned)(units < 1024 ? units : 1024)), dim3(kUpThreads), lds, st,
-                     d, hidden, topk_idx, w1, w1s, f, act, act_scale, status);
+  const size_t lds = SMALL ? 0 : chosen_lds(d), sums = (size_t)kDownWaves * d.T * kOut * sizeof(float);
+  uint32_t* counter = reinterpret_cast<uint32_t*>(work + k.counter);
+  hipLaunchKernelGGL((experts_up_kernel<WB, WAVES, SMALL>), dim3((unsigned)(units < 512 ? units : 512)),
+                     dim3(64 * WAVES), lds, st, d, hidden, topk_idx, w1, w1s, f, work, work + k.scale, counter,
+                     k.chunks, status);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (lds + sums > 64 * 1024) {
-    e = hipFuncSetAttribute(reinterpret_cast<const void*>(experts_down_kernel<WB>),
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(experts_down_kernel<WB, SMALL>),
                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)(lds + sums));
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((experts_down_kernel<WB>), dim3((unsigned)((d.H + kOut - 1) / kOut)), dim3(kDownThreads),
-                     lds + sums, st, d, topk_idx, weight, w2, w2s, f, act, act_scale, out);
+  hipLaunchKernelGGL((experts_down_kernel<WB, SMALL>), dim3((unsigned)(k.chunks * k.shares)), dim3(kDownThreads),
+                     lds + sums, st, d, topk_idx, weight, w2, w2s, f, work, work + k.scale, k.chunks, k.shares,
+                     reinterpret_cast<float*>(work + k.partial), counter, out);
   return hipGetLastError();
 }
 
 }  // namespace
 
+int64_t experts_work_bytes(const Dims& d, int32_t f) { return work_of(d, f).bytes; }
+
 hipError_t launch_experts(const Dims& d, const uint16_t* hidden, const int32_t* topk_idx, const float* weight,
                           int32_t w_bits, int32_t f, const uint8_t* w1, const uint8_t* w1s, const uint8_t* w2,
-                          const uint8_t* w2s, uint8_t* act, uint8_t* act_scale, uint16_t* out, int32_t* status,
-                          hipStream_t st) {
+                          const uint8_t* w2s, uint8_t* work, uint16_t* out, int32_t* status, hipStream_t st) {
   if (d.T == 0) return hipSuccess;
-  return w_bits == 4
-             ? launch<4>(d, hidden, topk_idx, weight, f, w1, w1s, w2, w2s, act, act_scale, out, status, st)
-             : launch<8>(d, hidden, topk_idx, weight, f, w1, w1s, w2, w2s, act, act_scale, out, status, st);
+  // Eight waves to a unit where there are fewer units than CUs: half the lines one after the other.
+  const bool small = d.T * d.k <= 64, wide = (int64_t)chosen_cap(d) * ((f + kChan - 1) / kChan) <= 256;
+  auto go = w_bits == 4 ? small ? wide ? launch<4, true, 8> : launch<4, true, 4> : launch<4, false, 4>
+                        : small ? wide ? launch<8, true, 8> : launch<8, true, 4> : launch<8, false, 4>;
+  return go(d, hidden, topk_idx, weight, f, w1, w1s, w2, w2s, work, out, status, st);
 }
 
 }  // namespace moe

@@ -366,13 +366,15 @@ def call_with_act(mp, layer, hidden, idx, weight, w1, w2, f):
     """Layer.experts with the activations kept: (out, act values [T*k, f], their scales)."""
     T, k = idx.shape
     fp, dev = mp.Blocks4.padded(f), layer.device
-    act = torch.full((T * k, fp), 0x7f, dtype=torch.uint8, device=dev)
-    scale = torch.full((T * k, fp // 32), 255, dtype=torch.uint8, device=dev)
+    work = torch.full((mp.moex4_experts_work(layer.handle, f),), 0xff, dtype=torch.uint8, device=dev)
     out = torch.full((T, hidden.shape[1]), 7.0, dtype=BF, device=dev)
     p = lambda t: t.data_ptr()
     mp.moex4_experts(layer.handle, p(hidden), p(idx), p(weight), 4 if isinstance(w1, mp.Blocks4) else 8, f, p(w1.q),
-                     p(w1.scale), p(w2.q), p(w2.scale), p(act), p(scale), p(out), torch.cuda.current_stream().cuda_stream)
+                     p(w1.scale), p(w2.q), p(w2.scale), p(work), p(out), torch.cuda.current_stream().cuda_stream)
     torch.cuda.synchronize()
+    act = work[: T * k * fp].view(T * k, fp)
+    scale = work[T * k * fp: T * k * (fp + fp // 32)].view(T * k, fp // 32)
+    assert (act[:, f:] == 0).all()
     s = torch.exp2(scale.cpu().double() - 127).repeat_interleave(32, -1)[:, :f]
     return out.cpu(), act.cpu().view(torch.float8_e4m3fn).double()[:, :f] * s, s
 
@@ -385,14 +387,14 @@ def check_few(mp, T, E, k, H, f, bits, seed=0, hot=0.0):
         hidden[1] = 0
         hidden[2, : H // 2] *= 1e4
     out, act, s = call_with_act(mp, layer, hidden.to(layer.device), idx, weight, w1, w2, f)
-    x, sx = refs4.quantize8(hidden.double())
-    (w1v, s1), (w2v, s2) = read(w1, 2 * f), read(w2, H)
+    x, _ = refs4.quantize8(hidden.double())
+    (w1v, _), (w2v, s2) = read(w1, 2 * f), read(w2, H)
     idx_, weight_ = idx.cpu(), weight.cpu().double()
     want, off = torch.zeros(T, H, dtype=torch.float64), torch.zeros(T, H, dtype=torch.float64)
     for e in sorted(set(idx_.flatten().tolist())):
         t, j = (idx_ == e).nonzero(as_tuple=True)
         y = x[t] @ w1v[e].t()
-        dy = refs4.added(x[t], w1v[e]) + refs4.cut(x[t], sx[t], w1v[e], s1[e])
+        dy = refs4.added(x[t], w1v[e])  # exact values in bf16: nothing is cut off here
         gate, up = y[:, :f], y[:, f:]
         a = refs.swiglu(y)
         silu = gate / (1 + torch.exp(-gate))
@@ -489,6 +491,43 @@ def test_few_tokens_not_finite(mp, bits):
     assert torch.isnan(got[3]).all() and int(torch.isnan(got).any(-1).sum()) == 1
     w[3, 1] = 0.0
     assert torch.isfinite(layer.experts(hidden.to(layer.device), w, w1, w2, topk_idx=idx)).all()
+    layer.close()
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_few_tokens_marked_matrices(mp, bits):
+    """A marked block of a matrix makes NaN of what its expert's tokens sum over it, and of nothing else."""
+    for which, at in (("w1", (1, 5, 40)), ("w1", (1, 64 + 5, 40)), ("w2", (1, 70, 33))):
+        layer, idx, weight, w1, w2 = few_layer(mp, 12, 4, 2, 200, 64, bits, 9)
+        dev = layer.device
+        hidden = normal(6, 12, 200).to(dev)
+        good = layer.experts(hidden, weight, w1, w2, topk_idx=idx).cpu()
+        w = normal(10 if which == "w1" else 11, 4, *((128, 200) if which == "w1" else (200, 64)),
+                   scale=(200 if which == "w1" else 64) ** -0.5)
+        w[at] = torch.nan
+        bad = (layer.quantize_weights4 if bits == 4 else layer.quantize_weights)(w.to(dev))
+        got = layer.experts(hidden, weight, *((bad, w2) if which == "w1" else (w1, bad)), topk_idx=idx).cpu()
+        has = (idx.cpu() == 1).any(-1)
+        assert has.any() and not has.all() and torch.equal(got[~has], good[~has])
+        if which == "w1":
+            assert torch.isnan(got[has]).all()
+        else:  # of matrices in 8 bits a block is 128 rows
+            lost = range(0, 128) if bits == 8 else [70]
+            rest = [c for c in range(200) if c not in lost]
+            assert torch.isnan(got[has][:, list(lost)]).all() and torch.equal(got[has][:, rest], good[has][:, rest])
+        assert layer.status() == 0
+        layer.close()
+
+
+def test_few_tokens_take_any_scale_bytes(mp):
+    """Scales of the matrices far from 1, that cancel: w1's gate and up halves, and w2."""
+    layer, idx, weight, w1, w2 = few_layer(mp, 5, 4, 2, 300, 40, 4, 2)
+    hidden = normal(6, 5, 300).to(layer.device)
+    good = layer.experts(hidden, weight, w1, w2, topk_idx=idx)
+    up = w1.scale.view(torch.uint8)
+    up[:, :, 40:] -= 60
+    w2.scale.view(torch.uint8).add_(60)
+    assert torch.equal(layer.experts(hidden, weight, w1, w2, topk_idx=idx), good)
     layer.close()
 
 
