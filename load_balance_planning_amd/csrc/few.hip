@@ -24,6 +24,7 @@ namespace {
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float float2_ __attribute__((ext_vector_type(2)));
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -33,7 +34,8 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 // What there is to multiply: entries of an expert and up to 16 of its slots t * k +
 // j (tokens ascending; one operand of the instruction).  In dynamic LDS: masks u64
 // [E] of tokens, then per entry its first place in the list of slots, int32 [cap +
-// 1], and its expert, uint16 [cap], then the list, uint16 [T * k].  Experts ascend.
+// 1], and its expert, uint16 [cap], then the list, uint16 [T * k], and where each
+// expert's slots begin there, uint16 [E].  Experts ascend.
 constexpr int kCols = 16;
 struct Chosen {
   uint64_t* mask;
@@ -62,7 +64,7 @@ __host__ __device__ inline int chosen_cap(const Dims& d) {
   return (d.E < slots ? d.E : slots) + (d.T > kCols ? slots / kCols : 0);
 }
 __host__ __device__ inline size_t chosen_lds(const Dims& d) {
-  return ((size_t)8 * d.E + 4 * (chosen_cap(d) + 1) + 2 * chosen_cap(d) + 2 * d.T * d.k + 15) / 16 * 16;
+  return ((size_t)10 * d.E + 4 * (chosen_cap(d) + 1) + 2 * chosen_cap(d) + 2 * d.T * d.k + 15) / 16 * 16;
 }
 
 template <int THREADS>
@@ -75,6 +77,7 @@ __device__ __forceinline__ Chosen collect_lds(const Dims& d, const int32_t* __re
   c.first = reinterpret_cast<int32_t*>(lds + 8 * d.E);
   c.expert = reinterpret_cast<uint16_t*>(c.first + cap + 1);
   c.slot = c.expert + cap;
+  uint16_t* const where = c.slot + slots;
   constexpr int kPer = 2048 / THREADS;  // slots of a thread at most, and experts
   int e[kPer];
 #pragma unroll
@@ -121,6 +124,7 @@ __device__ __forceinline__ Chosen collect_lds(const Dims& d, const int32_t* __re
   }
   c.n = all >> 16;
   for (int i = from; i < min(from + per, d.E); ++i) {
+    where[i] = (uint16_t)before;
     for (int m = __popcll(c.mask[i]); m > 0; m -= kCols) {
       c.expert[before >> 16] = (uint16_t)i;
       c.first[before >> 16] = before & 0xffff;
@@ -129,28 +133,19 @@ __device__ __forceinline__ Chosen collect_lds(const Dims& d, const int32_t* __re
   }
   if (threadIdx.x == 0) c.first[c.n] = all & 0xffff;
   __syncthreads();
-  // each slot to its place: the expert's first entry by bisection
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int s = threadIdx.x + i * THREADS;
     if (s >= slots || (unsigned)e[i] >= (unsigned)d.E) continue;
-    int lo = 0, hi = c.n - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (c.expert[mid] < e[i])
-        lo = mid + 1;
-      else
-        hi = mid;
-    }
-    c.slot[c.first[lo] + __popcll(c.mask[e[i]] & ((1ull << (s / d.k)) - 1ull))] = (uint16_t)s;
+    c.slot[where[e[i]] + __popcll(c.mask[e[i]] & ((1ull << (s / d.k)) - 1ull))] = (uint16_t)s;
   }
   __syncthreads();
   return c;
 }
 
 // The same where there are at most 64 slots, one to a lane, in every wave's
-// registers: no barrier, and a few instructions a slot.  Entries in the order of
-// their first slots.
+// registers: slots of an expert are a mask in LDS (u64 [E]), and that is all.
+// Entries in the order of their first slots.
 struct ChosenSmall {
   int e;      // of the lane's slot; -1: none
   int order;  // of the slot among its expert's
@@ -176,25 +171,29 @@ struct ChosenSmall {
     return which < o.count ? s : -1;
   }
 };
-__device__ __forceinline__ ChosenSmall collect_small(const Dims& d, const int32_t* __restrict__ topk, int32_t* status) {
+template <int THREADS>
+__device__ __forceinline__ ChosenSmall collect_small(const Dims& d, const int32_t* __restrict__ topk, unsigned char* lds,
+                                                     int32_t* status) {
   const int slots = d.T * d.k, lane = threadIdx.x & 63;
+  unsigned long long* mask = reinterpret_cast<unsigned long long*>(lds);
   ChosenSmall c;
   c.e = lane < slots ? topk[lane] : -1;
-  bool bad = lane < slots && (unsigned)c.e >= (unsigned)d.E;
-  if (bad) c.e = -1;
-  c.order = 0;
-  uint64_t leader = 0ull;
-  for (int i = 0; i < slots; ++i) {
-    const int ei = __builtin_amdgcn_readlane(c.e, i);
-    const uint64_t same = __ballot(c.e == ei);
-    const int order = __popcll(same & ((1ull << i) - 1ull));
-    if (ei >= 0 && order % kCols == 0) leader |= 1ull << i;
-    if (lane == i) c.order = order;
-    // a slot of the same token with the same expert
-    bad |= ei >= 0 && lane == i && (same & ~(1ull << i) & (((1ull << d.k) - 1ull) << (i / d.k * d.k))) != 0ull;
+  for (int i = threadIdx.x; i < d.E; i += THREADS) mask[i] = 0ull;
+  __syncthreads();
+  const bool good = (unsigned)c.e < (unsigned)d.E;
+  bool bad = lane < slots && !good;
+  if (!good) c.e = -1;
+  uint64_t same = 0ull;
+  if (good) {  // every wave sets the same bits, and sees its own at least
+    atomicOr(mask + c.e, 1ull << lane);
+    same = *reinterpret_cast<volatile unsigned long long*>(mask + c.e);
   }
+  c.order = __popcll(same & ((1ull << lane) - 1ull));
+  const uint64_t leader = __ballot(good && c.order % kCols == 0);
   c.n = __popcll(leader);
   c.rank = leader >> lane & 1ull ? __popcll(leader & ((1ull << lane) - 1ull)) : -1;
+  // a slot of the same token with the same expert
+  bad |= good && (same & ~(1ull << lane) & (((1ull << d.k) - 1ull) << (lane / d.k * d.k))) != 0ull;
   if (status && blockIdx.x == 0 && threadIdx.x < 64 && __ballot(bad) != 0ull && lane == 0)
     atomicOr(status, MOE_STATUS_BAD_TOPK);
   return c;
@@ -203,7 +202,7 @@ template <bool SMALL, int THREADS>
 __device__ __forceinline__ auto collect(const Dims& d, const int32_t* __restrict__ topk, unsigned char* lds,
                                         int32_t* status) {
   if constexpr (SMALL)
-    return collect_small(d, topk, status);
+    return collect_small<THREADS>(d, topk, lds, status);
   else
     return collect_lds<THREADS>(d, topk, lds, status);
 }
@@ -365,49 +364,65 @@ __global__ __launch_bounds__(64 * WAVES, 2) void experts_up_kernel(Dims d, const
   const int64_t total = (int64_t)d.T * d.H;
   unsigned char* const rows_s = own_s[wave];
   uint32_t* const sc_s = scale_s[wave];
+  // A unit: entry a's 32 channels from c0 on; this lane's rows of the matrices, the
+  // one of the 64 whose scales it loads, and the elements of the tokens' rows.
+  struct Unit {
+    decltype(ch.one(0)) one;
+    Matrix<WB> gate, up;
+    int chunk;
+    uint32_t at, at_16, s_at, from[kSets];
+  };
+  auto begin = [&](int a, int chunk) {
+    Unit u;
+    u.one = ch.one(a);
+    u.chunk = chunk;
+    const int c0 = chunk * kChan, valid = min(kChan, f - c0);
+    u.gate = matrix_rows<WB>(w, ws, u.one.expert, 2 * f, c0, valid, d.H);
+    u.up = matrix_rows<WB>(w, ws, u.one.expert, 2 * f, f + c0, valid, d.H);
+    u.at = (uint32_t)r * u.gate.row_bytes + 16 * g;
+    u.at_16 = u.at + 16 * u.gate.row_bytes;
+    const int s_row = min(lane & 31, valid - 1) + (lane >= 32 ? f : 0);
+    u.s_at = WB == 4 ? (uint32_t)s_row * 8 : (uint32_t)((c0 + s_row) / kBlk) * u.gate.s_step;
+#pragma unroll
+    for (int i = 0; i < kSets; ++i) {
+      if (i * kAtOnce >= u.one.count) break;
+      u.from[i] = (uint32_t)(max(ch.slot_of(u.one, i * kAtOnce + lane / kChunks), 0) / d.k) * d.H + 8 * (lane % kChunks);
+    }
+    return u;
+  };
+  struct Step {
+    u32x4 q[4][2];
+    u32x2 s;
+    u32x4 x[kSets];
+  };
+  auto load = [&](Step* o, const Unit& u, int b) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        o->q[i][p] = __builtin_bit_cast(u32x4, load16b(i < 2 ? u.gate.q : u.up.q, (i & 1 ? u.at_16 : u.at) + 64 * p, b * kBlk));
+    if constexpr (WB == 4)
+      o->s = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(u.gate.s, (int)u.s_at, b * (int)u.gate.s_step, 0));
+    else
+      o->s[0] = __builtin_amdgcn_raw_buffer_load_b8(u.gate.s, (int)u.s_at, b, 0);
+    if (b >= whole) return;
+#pragma unroll
+    for (int i = 0; i < kSets; ++i) {
+      if (i * kAtOnce >= u.one.count) break;
+      o->x[i] = *reinterpret_cast<const u32x4_any*>(hidden + u.from[i] + b * kHalves * kBlk);
+    }
+  };
   // unit = a * chunks + chunk, stepped without divisions
   const int step_a = (int)gridDim.x / chunks, step_c = (int)gridDim.x - step_a * chunks;
-  int a = (int)blockIdx.x / chunks, chunk = (int)blockIdx.x - a * chunks;
-  for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const int c0 = chunk * kChan, valid = min(kChan, f - c0);
-    const auto one = ch.one(a);
-    const Matrix<WB> gate = matrix_rows<WB>(w, ws, one.expert, 2 * f, c0, valid, d.H);
-    const Matrix<WB> up = matrix_rows<WB>(w, ws, one.expert, 2 * f, f + c0, valid, d.H);
-    // this lane's rows of the matrices, and the one of the 64 whose scales it loads
-    const uint32_t at = (uint32_t)r * gate.row_bytes + 16 * g, at_16 = at + 16 * gate.row_bytes;
-    const int s_row = min(lane & 31, valid - 1) + (lane >= 32 ? f : 0);
-    const uint32_t s_at = WB == 4 ? (uint32_t)s_row * 8 : (uint32_t)((c0 + s_row) / kBlk) * gate.s_step;
-    uint32_t from[kSets];  // elements of the tokens' rows that this lane loads
-#pragma unroll
-    for (int i = 0; i < kSets; ++i)
-      from[i] = (uint32_t)(max(ch.slot_of(one, i * kAtOnce + lane / kChunks), 0) / d.k) * d.H + 8 * (lane % kChunks);
-    struct Step {
-      u32x4 q[4][2];
-      u32x2 s;
-      u32x4 x[kSets];
-    };
-    auto load = [&](Step* o, int b) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-          o->q[i][p] = __builtin_bit_cast(u32x4, load16b(i < 2 ? gate.q : up.q, (i & 1 ? at_16 : at) + 64 * p, b * kBlk));
-      if constexpr (WB == 4)
-        o->s = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(gate.s, (int)s_at, b * (int)gate.s_step, 0));
-      else
-        o->s[0] = __builtin_amdgcn_raw_buffer_load_b8(gate.s, (int)s_at, b, 0);
-      if (b >= whole) return;
-#pragma unroll
-      for (int i = 0; i < kSets; ++i) {
-        if (i * kAtOnce >= one.count) break;
-        o->x[i] = *reinterpret_cast<const u32x4_any*>(hidden + from[i] + b * kHalves * kBlk);
-      }
-    };
+  int a = (int)blockIdx.x / chunks, unit = blockIdx.x;
+  if (unit >= units) return;
+  Unit u = begin(a, unit - a * chunks);
+  Step next;
+  if (wave < steps) load(&next, u, wave);
+  for (;;) {
     v4f acc[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] = v4f{0, 0, 0, 0};
-    Step next;
-    if (wave < steps) load(&next, wave);
     for (int b = wave; b < steps; b += WAVES) {
       // rows and scales to LDS: token t's chunk c lies at c ^ t, so that 16 tokens' lie apart
       auto put = [&](int i, const u32x4& v) {
@@ -417,13 +432,13 @@ __global__ __launch_bounds__(64 * WAVES, 2) void experts_up_kernel(Dims d, const
       if (b < whole) {
 #pragma unroll
         for (int i = 0; i < kSets; ++i) {
-          if (i * kAtOnce >= one.count) break;
+          if (i * kAtOnce >= u.one.count) break;
           put(i, next.x[i]);
         }
       } else {  // the rows' end, loaded here: its edges would take the registers of every step
 #pragma unroll 1
-        for (int i = 0; i * kAtOnce < one.count; ++i) {
-          const int64_t row_at = (int64_t)(max(ch.slot_of(one, i * kAtOnce + lane / kChunks), 0) / d.k) * d.H;
+        for (int i = 0; i * kAtOnce < u.one.count; ++i) {
+          const int64_t row_at = (int64_t)(max(ch.slot_of(u.one, i * kAtOnce + lane / kChunks), 0) / d.k) * d.H;
           put(i, load8_row(hidden, row_at, b * kHalves * kBlk + 8 * (lane % kChunks), d.H, total));
         }
       }
@@ -437,7 +452,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void experts_up_kernel(Dims d, const
 #pragma unroll
         for (int p = 0; p < 2; ++p) q[i][p] = next.q[i][p];
       wave_lds_sync();
-      if (b + WAVES < steps) load(&next, b + WAVES);
+      if (b + WAVES < steps) load(&next, u, b + WAVES);
       u32x2 s[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -464,23 +479,35 @@ __global__ __launch_bounds__(64 * WAVES, 2) void experts_up_kernel(Dims d, const
     float* const part = reinterpret_cast<float*>(rows_s);  // [kCols][2 kChan + 4]
 #pragma unroll
     for (int i = 0; i < 4; ++i) *reinterpret_cast<v4f*>(part + r * (2 * kChan + 4) + 16 * i + 4 * g) = acc[i];
-    __syncthreads();
-    if (WAVES == 4 || threadIdx.x < 256) {
-      const int row = threadIdx.x >> 4, c = 2 * (threadIdx.x & 15);
-      float v[2];
-      uint32_t top = 0;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float gv = 0.0f, uv = 0.0f;
-#pragma unroll
-        for (int q = 0; q < WAVES; ++q) {
-          const float* p = reinterpret_cast<const float*>(own_s[q]) + row * (2 * kChan + 4) + c + j;
-          gv += p[0];
-          uv += p[kChan];
-        }
-        v[j] = c0 + c + j < f ? swiglu(gv, uv) : 0.0f;
-        top = max(top, magnitude(v[j]));
+    // the next unit's first step comes in under this one's sums
+    const auto one = u.one;
+    const int chunk = u.chunk, c0 = chunk * kChan;
+    unit += gridDim.x;
+    const bool more = unit < units;
+    if (more) {
+      int c = chunk + step_c;
+      a += step_a;
+      if (c >= chunks) {
+        c -= chunks;
+        ++a;
       }
+      u = begin(a, c);
+      if (wave < steps) load(&next, u, wave);
+    }
+    __syncthreads();
+    const int row = threadIdx.x >> 4, c = 2 * (threadIdx.x & 15);
+    if (row < kCols) {  // whole waves
+      float2_ gv = {0.0f, 0.0f}, uv = {0.0f, 0.0f};
+#pragma unroll
+      for (int q = 0; q < WAVES; ++q) {
+        const float* p = reinterpret_cast<const float*>(own_s[q]) + row * (2 * kChan + 4) + c;
+        gv += *reinterpret_cast<const float2_*>(p);
+        uv += *reinterpret_cast<const float2_*>(p + kChan);
+      }
+      float v[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) v[j] = c0 + c + j < f ? swiglu(gv[j], uv[j]) : 0.0f;
+      uint32_t top = max(magnitude(v[0]), magnitude(v[1]));
       top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xf, 0xf, false));
       top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x4E, 0xf, 0xf, false));
       top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x141, 0xf, 0xf, false));
@@ -500,35 +527,31 @@ __global__ __launch_bounds__(64 * WAVES, 2) void experts_up_kernel(Dims d, const
           }
       }
     }
+    if (!more) break;
     __syncthreads();
-    a += step_a;
-    chunk += step_c;
-    if (chunk >= chunks) {
-      chunk -= chunks;
-      ++a;
-    }
   }
 #endif
 }
 
-// 32 channels of the result and a share of the entries' long axes per workgroup:
+// Up to 32 channels of the result and a share of the entries' long axes per workgroup:
 // its waves take runs of steps and add them, times the slots' weights, to sums of
 // their own in LDS.  The shares of the same channels meet in memory: the workgroup
 // that is the last to write its sums adds them all, in order, and writes the result.
 //
 // Activations and scales pass through LDS as in the launch before.
-constexpr int kDownWaves = 4, kDownThreads = 64 * kDownWaves, kOut = 32, kMaxShares = 16;
-template <int WB, bool SMALL>
-__global__ __launch_bounds__(kDownThreads, 2) void experts_down_kernel(Dims d, const int32_t* __restrict__ topk,
+constexpr int kOut = 32, kMaxShares = 8;
+template <int WB, bool SMALL, int kDownWaves>
+__global__ __launch_bounds__(64 * kDownWaves, kDownWaves == 16 ? 4 : 2) void experts_down_kernel(Dims d, const int32_t* __restrict__ topk,
                                                                        const float* __restrict__ weight,
                                                                        const uint8_t* __restrict__ w,
                                                                        const uint8_t* __restrict__ ws, int f,
                                                                        const uint8_t* __restrict__ act,
                                                                        const uint8_t* __restrict__ act_scale,
-                                                                       int chunks, int shares, float* partial,
+                                                                       int width, int chunks, int shares, float* partial,
                                                                        uint32_t* counter,
                                                                        uint16_t* __restrict__ out) {
 #ifdef __HIP_DEVICE_COMPILE__
+  constexpr int kDownThreads = 64 * kDownWaves;
   constexpr int kHalves = halves(WB), kPieces = 8 * kHalves;      // 16-byte pieces of a slot's step
   constexpr int kAtOnce = 64 / kPieces, kSets = kCols / kAtOnce;  // slots of a load, loads of 16 slots
   extern __shared__ __align__(16) unsigned char lds[];
@@ -545,7 +568,7 @@ __global__ __launch_bounds__(kDownThreads, 2) void experts_down_kernel(Dims d, c
   __syncthreads();
   float* mine = sums + wave * per_wave;
   const int share = blockIdx.x / chunks, chunk = blockIdx.x - share * chunks;
-  const int c0 = chunk * kOut, valid = min(kOut, d.H - c0);
+  const int c0 = chunk * width, valid = min(width, d.H - c0);
   const int fp = (int)padded_cols4(f), steps = (f + kHalves * kBlk - 1) / (kHalves * kBlk);
   const auto act_buf = buffer_of(act, (uint32_t)(d.T * d.k) * fp);
   const auto act_s_buf = buffer_of(act_scale, (uint32_t)(d.T * d.k) * (fp / kBlk4));
@@ -572,7 +595,8 @@ __global__ __launch_bounds__(kDownThreads, 2) void experts_down_kernel(Dims d, c
     };
     begin();
     const uint32_t at = (uint32_t)r * m.row_bytes + 16 * g, at_16 = at + 16 * m.row_bytes;
-    const uint32_t s_at = WB == 4 ? min(lane & 31, valid - 1) * 8 : (uint32_t)(c0 / kBlk) * m.s_step;
+    const int s_row = min(lane & 31, valid - 1);
+    const uint32_t s_at = WB == 4 ? s_row * 8 : (uint32_t)((c0 + s_row) / kBlk) * m.s_step;
     struct Step {
       v4i q[2][2];
       u32x2 s;
@@ -623,8 +647,12 @@ __global__ __launch_bounds__(kDownThreads, 2) void experts_down_kernel(Dims d, c
         *reinterpret_cast<v4i*>(act_s[wave] + place(i * kAtOnce + lane / kPieces, lane % kPieces) * 16) = next.x[i];
       }
       if (lane < kCols * kHalves) act_scale_s[wave][lane] = next.sx;
-      if (WB == 4 && lane < kOut) *reinterpret_cast<u32x2*>(scale_s[wave] + 2 * lane) = next.s;
-      const uint32_t s8 = next.s[0];
+      if (lane < kOut) {
+        if (WB == 4)
+          *reinterpret_cast<u32x2*>(scale_s[wave] + 2 * lane) = next.s;
+        else
+          scale_s[wave][lane] = next.s[0];
+      }
       v4i q[2][2];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -650,7 +678,7 @@ __global__ __launch_bounds__(kDownThreads, 2) void experts_down_kernel(Dims d, c
           const v4i q0 = q[i][h], q1 = q[i][1];
           const v8i qv = WB == 4 ? v8i{q0[0], q0[1], q0[2], q0[3], 0, 0, 0, 0}
                                  : v8i{q0[0], q0[1], q0[2], q0[3], q1[0], q1[1], q1[2], q1[3]};
-          const uint32_t s = WB == 4 ? scale_s[wave][2 * (16 * i + r) + h] >> (8 * g) : s8;
+          const uint32_t s = scale_s[wave][kHalves * (16 * i + r) + h] >> (WB == 4 ? 8 * g : 0);
           acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(qv, xv, acc[i], WB == 4 ? kFp4 : kFp8, kFp8, 0, (int)s,
                                                                     0, (int)sx);
         }
@@ -664,15 +692,22 @@ __global__ __launch_bounds__(kDownThreads, 2) void experts_down_kernel(Dims d, c
     }
   }
   __syncthreads();
-  float* own = partial + ((int64_t)chunk * shares + share) * per_wave;
-  for (int i = threadIdx.x; i < per_wave; i += kDownThreads) {
-    float v = sums[i];
+  auto write = [&](int i, float v) {  // sum i of [T][kOut]
+    const int c = i % kOut;
+    if (c < valid) out[(int64_t)(i / kOut) * d.H + c0 + c] = (uint16_t)pack_bf16(v, 0.0f);
+  };
+  typedef unsigned long long pair_;
+  pair_* own = reinterpret_cast<pair_*>(partial + ((int64_t)chunk * shares + share) * per_wave);
+  for (int i = threadIdx.x; i < per_wave / 2; i += kDownThreads) {
+    float2_ v = {0.0f, 0.0f};
 #pragma unroll
-    for (int q = 1; q < kDownWaves; ++q) v += sums[q * per_wave + i];
-    if (shares > 1)
-      __hip_atomic_store(own + i, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    else if (c0 + i % kOut < d.H)
-      out[(int64_t)(i / kOut) * d.H + c0 + i % kOut] = (uint16_t)pack_bf16(v, 0.0f);
+    for (int q = 0; q < kDownWaves; ++q) v += *reinterpret_cast<const float2_*>(sums + q * per_wave + 2 * i);
+    if (shares > 1) {
+      __hip_atomic_store(own + i, __builtin_bit_cast(pair_, v), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    } else {
+      write(2 * i, v[0]);
+      write(2 * i + 1, v[1]);
+    }
   }
   if (shares == 1) return;
   // The sums were written through to where all XCDs see them, and are there before
@@ -684,12 +719,19 @@ __global__ __launch_bounds__(kDownThreads, 2) void experts_down_kernel(Dims d, c
   if (threadIdx.x == 0) arrived = __hip_atomic_fetch_add(counter + chunk, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
   if (arrived != (uint32_t)shares - 1u) return;
-  const float* every = partial + (int64_t)chunk * shares * per_wave;
-  for (int i = threadIdx.x; i < per_wave; i += kDownThreads) {
-    float v = 0.0f;
-    for (int q = 0; q < shares; ++q)
-      v += __hip_atomic_load(every + (int64_t)q * per_wave + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (c0 + i % kOut < d.H) out[(int64_t)(i / kOut) * d.H + c0 + i % kOut] = (uint16_t)pack_bf16(v, 0.0f);
+  const pair_* every = reinterpret_cast<const pair_*>(partial) + (int64_t)chunk * shares * (per_wave / 2);
+  for (int i = threadIdx.x; i < per_wave / 2; i += kDownThreads) {
+    pair_ got[kMaxShares];  // all loads before the first sum
+#pragma unroll
+    for (int q = 0; q < kMaxShares; ++q)
+      got[q] = __hip_atomic_load(every + (int64_t)min(q, shares - 1) * (per_wave / 2) + i, __ATOMIC_RELAXED,
+                                 __HIP_MEMORY_SCOPE_AGENT);
+    float2_ v = {0.0f, 0.0f};
+#pragma unroll
+    for (int q = 0; q < kMaxShares; ++q)
+      if (q < shares) v += __builtin_bit_cast(float2_, got[q]);
+    write(2 * i, v[0]);
+    write(2 * i + 1, v[1]);
   }
 #endif
 }
@@ -697,17 +739,29 @@ __global__ __launch_bounds__(kDownThreads, 2) void experts_down_kernel(Dims d, c
 // Where a call's memory goes: activations [T * k][fp], their scales [T * k][fp /
 // 32], a counter per 32 channels, the shares' sums.
 struct Work {
-  int fp, chunks, shares;
+  int fp, waves, width, chunks, shares;
   int64_t scale, counter, partial, bytes;
 };
 Work work_of(const Dims& d, int f) {
   Work k;
   k.fp = (int)padded_cols4(f);
-  k.chunks = (d.H + kOut - 1) / kOut;
-  // two workgroups for every CU, if there are that many lines
+  // Sixteen waves to a workgroup, one for every CU, where their sums fit the LDS,
+  // else two of four waves.
+  k.waves = d.T <= 16 ? 16 : 4;
+  const int want = k.waves == 16 ? 256 : 512;
+  // As wide as 32 channels; but of many channels so that their number divides among
+  // the CUs (7168 channels: 256 workgroups of 28 and not 224 of 32).
+  const int rounds = (d.H + 256 * kOut - 1) / (256 * kOut);
+  k.width = kOut;
+  if (d.H > 128 * kOut) {
+    const int even = ((d.H + 256 * rounds - 1) / (256 * rounds) + 3) / 4 * 4;
+    k.width = even < kOut ? even : kOut;
+  }
+  k.chunks = (d.H + k.width - 1) / k.width;
   const int64_t lines = (int64_t)chosen_cap(d) * (k.fp / kCols4);
-  const int64_t most = (lines + kDownWaves - 1) / kDownWaves, want = (512 + k.chunks - 1) / k.chunks;
-  k.shares = (int)(want < most ? want : most);
+  // shares cost a pass through memory: four lines a wave at least
+  const int64_t most = lines / (4 * k.waves), fill = want / k.chunks;
+  k.shares = (int)(fill < most ? fill : most);
   if (k.shares > kMaxShares) k.shares = kMaxShares;
   if (k.shares < 1) k.shares = 1;
   const int64_t slots = (int64_t)d.T * d.k;
@@ -719,27 +773,34 @@ Work work_of(const Dims& d, int f) {
 }
 
 template <int WB, bool SMALL, int WAVES>
+hipError_t launch_down(const Dims& d, const Work& k, size_t lds, const int32_t* topk_idx, const float* weight, int32_t f,
+                       const uint8_t* w2, const uint8_t* w2s, uint8_t* work, uint16_t* out, hipStream_t st) {
+  lds += (size_t)WAVES * d.T * kOut * sizeof(float);
+  if (lds > 64 * 1024 - 32 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(experts_down_kernel<WB, SMALL, WAVES>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((experts_down_kernel<WB, SMALL, WAVES>), dim3((unsigned)(k.chunks * k.shares)), dim3(64 * WAVES),
+                     lds, st, d, topk_idx, weight, w2, w2s, f, work, work + k.scale, k.width, k.chunks, k.shares,
+                     reinterpret_cast<float*>(work + k.partial), reinterpret_cast<uint32_t*>(work + k.counter), out);
+  return hipGetLastError();
+}
+
+template <int WB, bool SMALL, int WAVES>
 hipError_t launch(const Dims& d, const uint16_t* hidden, const int32_t* topk_idx, const float* weight, int32_t f,
                   const uint8_t* w1, const uint8_t* w1s, const uint8_t* w2, const uint8_t* w2s, uint8_t* work,
                   uint16_t* out, int32_t* status, hipStream_t st) {
   const Work k = work_of(d, f);
   const int64_t units = (int64_t)chosen_cap(d) * ((f + kChan - 1) / kChan);
-  const size_t lds = SMALL ? 0 : chosen_lds(d), sums = (size_t)kDownWaves * d.T * kOut * sizeof(float);
-  uint32_t* counter = reinterpret_cast<uint32_t*>(work + k.counter);
+  const size_t lds = SMALL ? (size_t)8 * d.E : chosen_lds(d);
   hipLaunchKernelGGL((experts_up_kernel<WB, WAVES, SMALL>), dim3((unsigned)(units < 512 ? units : 512)),
-                     dim3(64 * WAVES), lds, st, d, hidden, topk_idx, w1, w1s, f, work, work + k.scale, counter,
-                     k.chunks, status);
-  hipError_t e = hipGetLastError();
+                     dim3(64 * WAVES), lds, st, d, hidden, topk_idx, w1, w1s, f, work, work + k.scale,
+                     reinterpret_cast<uint32_t*>(work + k.counter), k.chunks, status);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (lds + sums > 64 * 1024) {
-    e = hipFuncSetAttribute(reinterpret_cast<const void*>(experts_down_kernel<WB, SMALL>),
-                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)(lds + sums));
-    if (e != hipSuccess) return e;
-  }
-  hipLaunchKernelGGL((experts_down_kernel<WB, SMALL>), dim3((unsigned)(k.chunks * k.shares)), dim3(kDownThreads),
-                     lds + sums, st, d, topk_idx, weight, w2, w2s, f, work, work + k.scale, k.chunks, k.shares,
-                     reinterpret_cast<float*>(work + k.partial), counter, out);
-  return hipGetLastError();
+  return k.waves == 16 ? launch_down<WB, SMALL, 16>(d, k, lds, topk_idx, weight, f, w2, w2s, work, out, st)
+                       : launch_down<WB, SMALL, 4>(d, k, lds, topk_idx, weight, f, w2, w2s, work, out, st);
 }
 
 }  // namespace

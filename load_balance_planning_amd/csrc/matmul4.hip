@@ -46,6 +46,7 @@ __global__ __launch_bounds__(256) void matmul4_rows16_kernel(Instances in, const
                                                              int64_t tiles, uint16_t* __restrict__ y,
                                                              int32_t* __restrict__ status) {
   __shared__ float part[4][kRowsS][kChanS + 4];
+  __shared__ __align__(8) uint32_t scale_s[4][2 * kChanS];
   if (blockIdx.x == 0) check_instances(in, status);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, g = lane >> 4;
@@ -53,6 +54,7 @@ __global__ __launch_bounds__(256) void matmul4_rows16_kernel(Instances in, const
   const int nb8 = (k + kBlk - 1) / kBlk, ns8 = (nb8 + 3) / 4 * 4;      // blocks of an 8-bit row
   const int64_t line = kCols4 / 2;
   const int nct = (n + kChanS - 1) / kChanS;
+  uint32_t* const sc_s = scale_s[wave];
   for (int64_t id = blockIdx.x; id < tiles; id += gridDim.x) {
     const int64_t rt = id / nct;
     const int c0 = (int)(id - rt * nct) * kChanS;
@@ -61,19 +63,25 @@ __global__ __launch_bounds__(256) void matmul4_rows16_kernel(Instances in, const
     if (!find_row_tile<kRowsS>(in, rt, &sp, &r0)) continue;  // the same for all waves
     const int64_t row = min(r0 + r, sp.end - 1);
     const uint8_t* wp[4];
-    const uint8_t* wsp[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int c = min(c0 + 16 * (r >> 2) + 4 * i + (r & 3), n - 1);
       wp[i] = w + ((int64_t)sp.expert * n + c) * nb * line + 16 * g;
-      wsp[i] = ws + ((int64_t)sp.expert * nb * n + c) * 8;
     }
+    // the 64 channels' scales, one to a lane: they pass to the lanes that need them through LDS
+    const uint8_t* wsp = ws + ((int64_t)sp.expert * nb * n + min(c0 + lane, n - 1)) * 8;
     v4f acc[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] = v4f{0, 0, 0, 0};
     for (int b = wave; b < nb; b += 4) {
       v8i xv[2];
       uint32_t sx[2];
+      v4i wv[4][2];
+      const u32x2 ws8 = *reinterpret_cast<const u32x2*>(wsp + (int64_t)b * n * 8);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) wv[i][h] = load16b(wp[i] + b * line + 64 * h);
       if (XB == 4) {
         const uint8_t* xp = x + (row * nb + b) * line + 16 * g;
         const u32x2 s = *reinterpret_cast<const u32x2*>(xs + ((int64_t)b * in.rows + row) * 8);
@@ -92,15 +100,18 @@ __global__ __launch_bounds__(256) void matmul4_rows16_kernel(Instances in, const
           sx[h] = xs[row * ns8 + b8];
         }
       }
+      *reinterpret_cast<u32x2*>(sc_s + 2 * lane) = ws8;
+      wave_lds_sync();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const u32x2 s = *reinterpret_cast<const u32x2*>(wsp[i] + (int64_t)b * n * 8);
+        const u32x2 s = *reinterpret_cast<const u32x2*>(sc_s + 2 * (16 * (r >> 2) + 4 * i + (r & 3)));
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand4(load16b(wp[i] + b * line + 64 * h)), xv[h],
-                                                                    acc[i], kFp4, XB == 4 ? kFp4 : kFp8, 0,
-                                                                    (int)(s[h] >> (8 * g)), 0, (int)sx[h]);
+          acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand4(wv[i][h]), xv[h], acc[i], kFp4,
+                                                                    XB == 4 ? kFp4 : kFp8, 0, (int)(s[h] >> (8 * g)), 0,
+                                                                    (int)sx[h]);
       }
+      wave_lds_sync();
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) *reinterpret_cast<v4f*>(&part[wave][r][16 * g + 4 * i]) = acc[i];
