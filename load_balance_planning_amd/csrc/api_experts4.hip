@@ -80,7 +80,7 @@ extern "C" int moex4_matmul(moe_plan_t h, const moe_plan_out* plan, const int32_
     return MOE_ERR_INVALID_ARG;
   const moe::Instances in{plan->n_inst, plan->inst_expert, inst_offset, h->d.cap, h->d.E, (int64_t)h->d.T * h->d.k};
   // one 256-thread workgroup per tile, fewer than 2^32 work-items a launch
-  if (moe::matmul4_tiles(in, n) >= (int64_t)1 << 24) return MOE_ERR_UNSUPPORTED;
+  if (moe::matmul4_tiles(in, x_bits, n, k) >= (int64_t)1 << 24) return MOE_ERR_UNSUPPORTED;
   const DeviceScope on_device(h->device);
   if (!on_device.ok()) return MOE_ERR_HIP;
   return hip_rc(moe::launch_matmul4(in, x_bits, x, x_scale, w, w_scale, n, k, y, h->ws.status, begin_call(h, stream)));

@@ -145,20 +145,22 @@ __global__ __launch_bounds__(256) void matmul4_rows16_kernel(Instances in, const
 // half's operands are read into a second set of registers; one barrier a step,
 // between its halves.
 //
-// Rows in 4 bits: a step is a line of both operands (128 bytes, 256 values: a
-// half is two 32x32x64 instructions deep).  Lane group g takes the four blocks of
-// 32 from 4 g on, so that its scales are one word, which the instruction indexes
-// by byte.  A line's scales come to LDS with it: 8 bytes a row, one load of 16
-// bytes a thread.
+// Steps of a line (4 bits, square tiles): 128 bytes of both operands, 256 values; a
+// half is two 32x32x64 instructions deep.  Lane group g takes the four blocks of 32
+// from 4 g on, so that its scales are one word, which the instruction indexes by
+// byte.  A line's scales come to LDS with it: 8 bytes a row, one load of 16 bytes a
+// thread.
 //
-// Rows in 8 bits: a step is 128 values, 128 bytes of x and 64 of the matrix (a
-// half is one instruction deep).  The matrices' scales of two steps come to LDS
-// together; those of x, one byte a step, go to registers four steps at a time.
+// Steps of half a line (256 x 128 tiles, and all of rows in 8 bits): 128 values, 64
+// bytes of 4-bit rows and 128 of 8-bit ones; a half is one instruction deep.  The
+// scales of two steps come to LDS together; those of 8-bit rows, one byte a step,
+// go to registers four steps at a time.
 //
 // LDS rows of 128 bytes are placed as the 8-bit products place them.  Of rows of
 // 64 bytes, four share 256 bytes: piece p of row R lies at place 4 (R % 4) + (p ^
-// s(R)), s the bits 2 and 4 of R, so that the 16 lanes of a read (rows that
-// differ in bits 0, 1, 2 and 4) find 16 different places.
+// s(R)), s two bits in which the rows of 16 lanes differ beside R % 4 and that are
+// the same in every instruction tile: bits 2 and 3 of R for the rows operand, 2
+// and 4 for the channels.
 template <bool CHANNELS>
 __device__ __forceinline__ int piece_swizzle(int pair) {  // pair = R / 2
   return CHANNELS ? (pair & 3) | ((pair >> 1) & 4) : pair & 7;
@@ -167,25 +169,32 @@ template <bool CHANNELS>
 __device__ __forceinline__ int piece_at(int row, int p) {
   return (row >> 1) * 256 + ((((row & 1) << 3) | p) ^ piece_swizzle<CHANNELS>(row >> 1)) * 16;
 }
-[[maybe_unused]] __device__ __forceinline__ int quad_swizzle(int quad) { return (quad & 1) | ((quad >> 1) & 2); }  // quad = R / 4
-[[maybe_unused]] __device__ __forceinline__ int quad_piece_at(int row, int p) {
-  return (row >> 2) * 256 + (((row & 3) << 2) | (p ^ quad_swizzle(row >> 2))) * 16;
+template <bool CHANNELS>
+__device__ __forceinline__ int quad_swizzle(int quad) {  // quad = R / 4
+  return CHANNELS ? (quad & 1) | ((quad >> 1) & 2) : quad & 3;
+}
+template <bool CHANNELS>
+__device__ __forceinline__ int quad_piece_at(int row, int p) {
+  return (row >> 2) * 256 + (((row & 3) << 2) | (p ^ quad_swizzle<CHANNELS>(row >> 2))) * 16;
 }
 
 template <int XB, int BC, int BT>
 struct TileShape {
   static constexpr int kThreads = 256;
+  static constexpr bool kAlone = BC == 256 && BT == 256;               // one workgroup to a CU
+  static constexpr bool kLines = XB == 4 && BC == BT;                  // steps of a line
   static constexpr int kWaveC = BC / 2, kWaveT = BT / 2;               // a wave's channels and rows
   static constexpr int kC = kWaveC / 32, kT = kWaveT / 32;             // in instruction tiles
-  static constexpr int kBytesC = XB == 4 ? 128 : 64, kBytesT = 128;    // of a row, a step
-  static constexpr int kDeep = XB == 4 ? 2 : 1;                        // instructions of a half
+  static constexpr int kBytesC = kLines ? 128 : 64, kBytesT = XB == 4 ? kBytesC : 128;  // of a row, a step
+  static constexpr int kDeep = kLines ? 2 : 1;                         // instructions of a half
+  static constexpr int kPieces = XB == 4 ? kDeep : 2;                  // of a row's 16-byte pieces, a half
   static constexpr int kPassC = BC * kBytesC / (16 * kThreads), kPassT = BT * kBytesT / (16 * kThreads);
-  static constexpr int kScales = XB == 4 ? 8 * (BC + BT) : 8 * BC;     // bytes of a line's scales
-  static_assert(BC % 128 == 0 && BC == BT, "four equal parts");
+  static constexpr int kScaled = XB == 4 ? BC + BT : BC;               // rows whose scales go to LDS
+  static_assert(BC % 128 == 0 && BT % 128 == 0, "whole parts");
 };
 
 // A pointer that is the same for all lanes, in scalar registers.
-__device__ __forceinline__ const uint8_t* scalar(const uint8_t* p) {
+[[maybe_unused]] __device__ __forceinline__ const uint8_t* scalar(const uint8_t* p) {
   const uint64_t v = reinterpret_cast<uint64_t>(p);
   return reinterpret_cast<const uint8_t*>((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 |
                                           (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
@@ -199,7 +208,7 @@ __device__ __forceinline__ acc16 multiply32(const v8i& c, const v8i& t, const ac
 
 // Persistent: workgroup b takes every (gridDim.x / 8)-th tile of its XCD's run.
 template <int XB, int BC, int BT>
-__global__ __launch_bounds__(256, BC == 256 ? 1 : 2) void matmul4_tile_kernel(
+__global__ __launch_bounds__(256, (TileShape<XB, BC, BT>::kAlone ? 1 : 2)) void matmul4_tile_kernel(
     Instances in, const uint8_t* __restrict__ x, const uint8_t* __restrict__ xs, const uint8_t* __restrict__ w,
     const uint8_t* __restrict__ ws, int n, int k, uint16_t* __restrict__ y, int32_t* __restrict__ status) {
 #ifdef __HIP_DEVICE_COMPILE__
@@ -208,15 +217,15 @@ __global__ __launch_bounds__(256, BC == 256 ? 1 : 2) void matmul4_tile_kernel(
   __shared__ __align__(256) unsigned char t0_s[BT * S::kBytesT];
   __shared__ __align__(256) unsigned char c1_s[BC * S::kBytesC];
   __shared__ __align__(256) unsigned char t1_s[BT * S::kBytesT];
-  __shared__ __align__(16) unsigned char z0_s[S::kScales];
-  __shared__ __align__(16) unsigned char z1_s[XB == 4 ? S::kScales : 16];
+  __shared__ __align__(16) unsigned char z0_s[8 * S::kScaled];
+  __shared__ __align__(16) unsigned char z1_s[S::kLines ? 8 * S::kScaled : 16];
   __shared__ int32_t sums[4];
   extern __shared__ int32_t pre[];  // [cap + 1]
   // where results pass: a place of their own, or (where two workgroups share
   // the CU's LDS) the second stage, whose next block then comes in later
-  constexpr bool kOwnPlace = BC == 256;
+  constexpr bool kOwnPlace = S::kAlone;
   __shared__ __align__(16) unsigned char out_s[kOwnPlace ? 4 * 4096 : 16];
-  constexpr bool kFetch = BC == 256;
+  constexpr bool kFetch = S::kAlone;
   __shared__ uint32_t fetch_s[kFetch ? 4 * 64 : 1];
   if (blockIdx.x == 0) check_instances(in, status);
   const int nct = (n + BC - 1) / BC;
@@ -235,7 +244,7 @@ __global__ __launch_bounds__(256, BC == 256 ? 1 : 2) void matmul4_tile_kernel(
   const int r = lane & 31, g = lane >> 5;
   const int lines = (k + kCols4 - 1) / kCols4;
   const int nb8 = (k + kBlk - 1) / kBlk, ns8 = (nb8 + 3) / 4 * 4;
-  const int nb = XB == 4 ? lines : nb8;  // steps
+  const int nb = S::kLines ? lines : nb8;  // steps
   const uint32_t kpc = (uint32_t)lines * (kCols4 / 2), kpt = XB == 4 ? kpc : (uint32_t)nb8 * kBlk;
   // where this thread's pieces come from: the same place of every pass
   const int pair = threadIdx.x >> 4;
@@ -266,10 +275,10 @@ __global__ __launch_bounds__(256, BC == 256 ? 1 : 2) void matmul4_tile_kernel(
   uint32_t off_c[S::kPassC], off_t[S::kPassT], xs_off[S::kT], off_f;
   // this wave's part of a line's scales: 128 channels' or (4 bits) rows' (where
   // there are fewer parts than waves, two load the same)
-  constexpr int kParts = BC / 128;
-  const int z_part = wave & (XB == 4 ? 2 * kParts - 1 : kParts - 1);
-  const bool z_rows = z_part >= kParts;
-  const int z_at = (z_rows ? z_part - kParts : z_part) * 1024;
+  constexpr int kPartsC = BC / 128, kParts = S::kScaled / 128;
+  const int z_part = wave % kParts;
+  const bool z_rows = z_part >= kPartsC;
+  const int z_at = (z_rows ? z_part - kPartsC : z_part) * 1024;
   const int64_t z_step = 8 * (z_rows ? in.rows : n);
   // the tile's operands and scales, in scalars
   const uint8_t *w_from, *x_from, *z_from;
@@ -281,14 +290,19 @@ __global__ __launch_bounds__(256, BC == 256 ? 1 : 2) void matmul4_tile_kernel(
     w_bytes = __builtin_amdgcn_readfirstlane(at.chans * kpc);
     x_bytes = __builtin_amdgcn_readfirstlane(at.rows * kpt);
     z_bytes = __builtin_amdgcn_readfirstlane(8 * (z_rows ? at.rows : at.chans));
+    const int quad_row = (threadIdx.x >> 2) & 3, quad_place = threadIdx.x & 3;
 #pragma unroll
     for (int q = 0; q < S::kPassC; ++q)
-      off_c[q] = XB == 4 ? (uint32_t)min(q * 32 + 2 * pair + (place_c >> 3), at.chans - 1) * kpc + 16 * (place_c & 7)
-                         : (uint32_t)min(q * 64 + 4 * pair + ((threadIdx.x >> 2) & 3), at.chans - 1) * kpc +
-                               16 * ((threadIdx.x & 3) ^ quad_swizzle(pair));
+      off_c[q] = S::kBytesC == 128
+                     ? (uint32_t)min(q * 32 + 2 * pair + (place_c >> 3), at.chans - 1) * kpc + 16 * (place_c & 7)
+                     : (uint32_t)min(q * 64 + 4 * pair + quad_row, at.chans - 1) * kpc +
+                           16 * (quad_place ^ quad_swizzle<true>(pair));
 #pragma unroll
     for (int q = 0; q < S::kPassT; ++q)
-      off_t[q] = (uint32_t)min(q * 32 + 2 * pair + (place_t >> 3), at.rows - 1) * kpt + 16 * (place_t & 7);
+      off_t[q] = S::kBytesT == 128
+                     ? (uint32_t)min(q * 32 + 2 * pair + (place_t >> 3), at.rows - 1) * kpt + 16 * (place_t & 7)
+                     : (uint32_t)min(q * 64 + 4 * pair + quad_row, at.rows - 1) * kpt +
+                           16 * (quad_place ^ quad_swizzle<false>(pair));
     if (XB == 8) {
 #pragma unroll
       for (int j = 0; j < S::kT; ++j) xs_off[j] = (uint32_t)(min(wt + 32 * j + r, at.rows - 1) * ns8);
@@ -307,8 +321,8 @@ __global__ __launch_bounds__(256, BC == 256 ? 1 : 2) void matmul4_tile_kernel(
     __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_ptr)(fetch_s + wave * 64), 4, off_f,
                                              b * (wave < 2 ? S::kBytesC : S::kBytesT), 0, 0);
   };
-  // A step's blocks, and with them the scales of its line (rows in 8 bits: of the
-  // line that begins with an even step).
+  // A step's blocks, and with them the scales of its line (steps of half a line: of
+  // the line that begins with an even step).
   auto load = [&](unsigned char* c_s, unsigned char* t_s, unsigned char* z_s, int b, auto odd) {
     const auto w_buf = buffer_of(w_from, w_bytes), x_buf = buffer_of(x_from, x_bytes);
 #pragma unroll
@@ -319,33 +333,35 @@ __global__ __launch_bounds__(256, BC == 256 ? 1 : 2) void matmul4_tile_kernel(
     for (int q = 0; q < S::kPassT; ++q)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(x_buf, (lds_ptr)(t_s + (q * 256 + wave * 64) * 16), 16, off_t[q],
                                                b * S::kBytesT, 0, 0);
-    if constexpr (XB == 4 || decltype(odd)::value == 0) {
-      const auto z_buf = buffer_of(z_from + (int64_t)(XB == 4 ? b : b >> 1) * z_step, z_bytes);
+    if constexpr (S::kLines || decltype(odd)::value == 0) {
+      const auto z_buf = buffer_of(z_from + (int64_t)(S::kLines ? b : b >> 1) * z_step, z_bytes);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(z_buf, (lds_ptr)(z_s + z_part * 1024), 16, z_at + lane * 16, 0, 0, 0);
     }
   };
   const int perm = 16 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3);  // channel of the lane's matrix row
-  // This lane's scales of a line: of the channels and (4 bits) of the rows.
+  // This lane's scales, of a step or (steps of half a line) of a round's two, shifted
+  // so that those it needs are the lowest bytes (8 bits: bytes 0 and 2).
+  constexpr int kOf = S::kLines ? 1 : 2;
   struct Scales {
-    int c[XB == 4 ? 1 : 2][S::kC], t[S::kT];
+    int c[kOf][S::kC], t[kOf][S::kT];
+  };
+  auto read_one = [&](const unsigned char* at_z, int* first, int* second) {
+    if constexpr (S::kLines) {
+      *first = *reinterpret_cast<const int*>(at_z + 4 * g);
+    } else {
+      typedef uint32_t u32x2_s __attribute__((ext_vector_type(2)));
+      const u32x2_s v = *reinterpret_cast<const u32x2_s*>(at_z);
+      constexpr int kBits = XB == 4 ? 16 : 8;
+      *first = (int)(v[0] >> (kBits * g));
+      *second = (int)(v[1] >> (kBits * g));
+    }
   };
   auto read_scales = [&](Scales* s, const unsigned char* z_s) {
 #pragma unroll
-    for (int i = 0; i < S::kC; ++i) {
-      const unsigned char* at_z = z_s + (wc + 32 * i + perm) * 8;
-      if (XB == 4) {
-        s->c[0][i] = *reinterpret_cast<const int*>(at_z + 4 * g);
-      } else {  // both steps', shifted so that the lane's blocks are bytes 0 and 2
-        typedef uint32_t u32x2_s __attribute__((ext_vector_type(2)));
-        const u32x2_s v = *reinterpret_cast<const u32x2_s*>(at_z);
-        s->c[0][i] = (int)(v[0] >> (8 * g));
-        s->c[XB == 4 ? 0 : 1][i] = (int)(v[1] >> (8 * g));
-      }
-    }
+    for (int i = 0; i < S::kC; ++i) read_one(z_s + (wc + 32 * i + perm) * 8, &s->c[0][i], &s->c[kOf - 1][i]);
     if (XB == 4) {
 #pragma unroll
-      for (int j = 0; j < S::kT; ++j)
-        s->t[j] = *reinterpret_cast<const int*>(z_s + (BC + wt + 32 * j + r) * 8 + 4 * g);
+      for (int j = 0; j < S::kT; ++j) read_one(z_s + (BC + wt + 32 * j + r) * 8, &s->t[0][j], &s->t[kOf - 1][j]);
     }
   };
   // rows in 8 bits: scales of x, four steps to a word
@@ -359,17 +375,19 @@ __global__ __launch_bounds__(256, BC == 256 ? 1 : 2) void matmul4_tile_kernel(
   auto take_sx = [&](Scales* s, int b) {  // those of block b, b even, to the lowest byte
     if (XB == 4) return;
 #pragma unroll
-    for (int j = 0; j < S::kT; ++j) s->t[j] = sx_next[j] >> (8 * (b & 2));
+    for (int j = 0; j < S::kT; ++j) s->t[0][j] = sx_next[j] >> (8 * (b & 2));
   };
   // LDS places of this lane's pieces in the first tiles; the others lie at
   // constant distances.
-  const int first_c = XB == 4 ? piece_at<true>(wc + perm, 4 * g) : quad_piece_at(wc + perm, g);
-  const int first_t = piece_at<false>(wt + r, XB == 4 ? 4 * g : g);
+  const int first_c = S::kLines ? piece_at<true>(wc + perm, 4 * g) : quad_piece_at<true>(wc + perm, XB == 4 ? 2 * g : g);
+  const int first_t = S::kLines ? piece_at<false>(wt + r, 4 * g)
+                      : XB == 4 ? quad_piece_at<false>(wt + r, 2 * g)
+                                : piece_at<false>(wt + r, g);
   acc16 acc[S::kC][S::kT];
   // 4-bit operands are kept as what they are, 16 bytes: widened ones would hold
   // registers of zeros from one half to the next
   struct Half {
-    v4i c[S::kDeep][S::kC], t[2][S::kT];
+    v4i c[S::kDeep][S::kC], t[S::kPieces][S::kT];
   };
   auto piece = [&](const unsigned char* s, int place) { return *reinterpret_cast<const v4i*>(s + place); };
   auto read = [&](Half* f, const unsigned char* c_s, const unsigned char* t_s, int half) {
@@ -378,15 +396,15 @@ __global__ __launch_bounds__(256, BC == 256 ? 1 : 2) void matmul4_tile_kernel(
     int at_c = first_c, at_t = first_t;
     asm volatile("" : "+v"(at_c), "+v"(at_t));
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int m = 0; m < S::kPieces; ++m)
 #pragma unroll
       for (int j = 0; j < S::kT; ++j)
-        f->t[m][j] = piece(t_s, (at_t ^ (XB == 4 ? 16 * (2 * half + m) : 64 * half + 32 * m)) + 32 * j * S::kBytesT);
+        f->t[m][j] = piece(t_s, (at_t ^ (XB == 4 ? 16 * (S::kDeep * half + m) : 64 * half + 32 * m)) + 32 * j * S::kBytesT);
 #pragma unroll
     for (int m = 0; m < S::kDeep; ++m)
 #pragma unroll
       for (int i = 0; i < S::kC; ++i)
-        f->c[m][i] = piece(c_s, (at_c ^ (XB == 4 ? 16 * (2 * half + m) : 32 * half)) + 32 * i * S::kBytesC);
+        f->c[m][i] = piece(c_s, (at_c ^ (XB == 4 ? 16 * (S::kDeep * half + m) : 32 * half)) + 32 * i * S::kBytesC);
   };
   // STEP: even or odd of its round; HALF of the step.
   auto multiply = [&](const Half& f, const Scales& s, auto step, auto half) {
@@ -395,21 +413,24 @@ __global__ __launch_bounds__(256, BC == 256 ? 1 : 2) void matmul4_tile_kernel(
     for (int i = 0; i < S::kC; ++i)
 #pragma unroll
       for (int j = 0; j < S::kT; ++j) {
-        if constexpr (XB == 4) {
+        if constexpr (S::kLines) {
           acc[i][j] = multiply32<XB, 2 * kHalf, 2 * kHalf>(operand4(f.c[0][i]), operand4(f.t[0][j]), acc[i][j],
-                                                           s.c[0][i], s.t[j]);
+                                                           s.c[0][i], s.t[0][j]);
           acc[i][j] = multiply32<XB, 2 * kHalf + 1, 2 * kHalf + 1>(operand4(f.c[1][i]), operand4(f.t[1][j]),
-                                                                   acc[i][j], s.c[0][i], s.t[j]);
+                                                                   acc[i][j], s.c[0][i], s.t[0][j]);
+        } else if constexpr (XB == 4) {
+          acc[i][j] = multiply32<XB, kHalf, kHalf>(operand4(f.c[0][i]), operand4(f.t[0][j]), acc[i][j], s.c[kStep][i],
+                                                   s.t[kStep][j]);
         } else {
           acc[i][j] = multiply32<XB, 2 * kHalf, kStep>(operand4(f.c[0][i]), operand8(f.t[0][j], f.t[1][j]), acc[i][j],
-                                                       s.c[kStep][i], s.t[j]);
+                                                       s.c[kStep][i], s.t[0][j]);
         }
       }
   };
   // a half's products, with the other half's reads (and LOADS direct loads)
   // spread between them
   constexpr int kProducts = S::kC * S::kT * S::kDeep;
-  constexpr int kReads = S::kDeep * (S::kC + S::kT * (XB == 4 ? 1 : 2)) + S::kC + (XB == 4 ? S::kT : 0);
+  constexpr int kReads = S::kDeep * S::kC + S::kPieces * S::kT + S::kC + (XB == 4 ? S::kT : 0);
   auto spread = [&](bool loads) {
     if (kFetch && !loads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // fetch
 #pragma unroll
@@ -419,13 +440,19 @@ __global__ __launch_bounds__(256, BC == 256 ? 1 : 2) void matmul4_tile_kernel(
       if (loads) __builtin_amdgcn_sched_group_barrier(0x020, (S::kPassC + S::kPassT + kProducts) / kProducts, 0);
     }
   };
-  // turns of 64 channels by 32 rows; or all at once, of 8-bit rows one row after the other of instruction tiles
-  constexpr int kTI = kOwnPlace ? S::kC / 2 : 1, kTJ = kOwnPlace ? S::kT : XB == 4 ? 1 : 2;
+  // turns of 64 channels by 32 rows in a place of their own; or in the second stage,
+  // both parts (4 bits: all at once; 8 bits: half the wave's rows at a time) or one
+  constexpr int kParts1 = S::kLines ? 2 : BC == 256 && XB == 8 ? 2 : 1;  // parts of the stage
+  constexpr int kTI = kOwnPlace ? S::kC / 2 : S::kLines || kParts1 == 2 || XB == 8 ? 1 : 2;
+  constexpr int kTJ = kOwnPlace ? S::kT : S::kLines ? 1 : 2;
   constexpr int kOwn = 2 * S::kWaveC * S::kWaveT / (kTI * kTJ);
-  static_assert(kOwn <= (kOwnPlace ? 4096 : BT * S::kBytesT / (XB == 4 ? 2 : 4)), "a turn fits the wave's part");
-  unsigned char* own = kOwnPlace ? out_s + wave * 4096
-                       : XB == 4 ? (wave < 2 ? c1_s : t1_s) + (wave & 1) * kOwn
-                                 : t1_s + wave * kOwn;
+  unsigned char* const one_part = XB == 4 ? c1_s : t1_s;
+  static_assert(kOwnPlace ? kOwn <= 4096
+                : kParts1 == 2 ? 2 * kOwn <= BC * S::kBytesC && 2 * kOwn <= BT * S::kBytesT
+                               : 4 * kOwn <= (XB == 4 ? BC * S::kBytesC : BT * S::kBytesT), "a turn fits the wave's part");
+  unsigned char* own = kOwnPlace      ? out_s + wave * 4096
+                       : kParts1 == 2 ? (wave < 2 ? c1_s : t1_s) + (wave & 1) * kOwn
+                                      : one_part + wave * kOwn;
   at = locate(tile);
   set_offsets();
   load_sx(0);
@@ -441,7 +468,7 @@ __global__ __launch_bounds__(256, BC == 256 ? 1 : 2) void matmul4_tile_kernel(
 #pragma unroll
         for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
     Half f0, f1;
-    Scales s0, s1;  // of even and odd steps (4 bits), or s0 of a round (8 bits)
+    Scales s0, s1;  // of even and odd steps, or s0 of a round
     sync_with_loads();
     if (!kOwnPlace) load(c1_s, t1_s, z1_s, min(1, nb - 1), one);
     read(&f0, c0_s, t0_s, 0);
@@ -457,18 +484,18 @@ __global__ __launch_bounds__(256, BC == 256 ? 1 : 2) void matmul4_tile_kernel(
       sync_with_loads<kFetch ? 1 : 0>();
       load(c0_s, t0_s, z0_s, min(b + 2, nb - 1), zero);
       read(&f0, c1_s, t1_s, 0);
-      if (XB == 4) read_scales(&s1, z1_s);
+      if (S::kLines) read_scales(&s1, z1_s);
       multiply(f1, s0, zero, one);
       spread(true);
       fetch(min(b + 4, nb - 1));
       read(&f1, c1_s, t1_s, 1);
-      multiply(f0, XB == 4 ? s1 : s0, one, zero);
+      multiply(f0, S::kLines ? s1 : s0, one, zero);
       spread(false);
       sync_with_loads<kFetch ? 1 : 0>();
       load_sx(min(b + 2, nb - 1));
       load(c1_s, t1_s, z1_s, min(b + 3, nb - 1), one);
       read(&f0, c0_s, t0_s, 0);
-      if (XB == 4) {
+      if (S::kLines) {
         read_scales(&s0, z0_s);
         multiply(f1, s1, one, one);
       } else {
@@ -507,7 +534,8 @@ __global__ __launch_bounds__(256, BC == 256 ? 1 : 2) void matmul4_tile_kernel(
 template <int XB, int BC, int BT>
 hipError_t launch_tiles(const Instances& in, const uint8_t* x, const uint8_t* xs, const uint8_t* w, const uint8_t* ws,
                         int n, int k, uint16_t* y, int32_t* status, hipStream_t st) {
-  const int64_t most = row_tile_ids(in, BT) * ((n + BC - 1) / BC), resident = BC == 256 ? 256 : 512;
+  const int64_t most = row_tile_ids(in, BT) * ((n + BC - 1) / BC);
+  const int64_t resident = TileShape<XB, BC, BT>::kAlone ? 256 : 512;
   hipLaunchKernelGGL((matmul4_tile_kernel<XB, BC, BT>), dim3((unsigned)((most < resident ? most : resident) + 7) / 8 * 8),
                      dim3(256), sizeof(int32_t) * (in.cap + 1), st, in, x, xs, w, ws, n, k, y, status);
   return hipGetLastError();
@@ -530,27 +558,50 @@ namespace {
 
 constexpr int kCapWide = 1536;  // instances whose tile counts fit the LDS beside 256 x 256 tiles
 
-// The tile of a product, 0 for the streaming kernel, as the 8-bit products choose it.
-int matmul4_tile(const Instances& in, int n) {
-  if (in.rows <= (int64_t)8 * in.E) return 0;
-  const bool fills = in.rows / 256 * ((n + 255) / 256) >= 512 && in.cap <= kCapWide;
-  return in.rows >= (int64_t)192 * in.E && fills ? 256 : 128;
+// The tile of a product, by the mean of rows per expert (the loads themselves are
+// on the device); channels 0: the streaming kernel, up to 8 rows an expert.  us in
+// 128 x 128, 256 x 128 and 256 x 256 (channels x rows):
+//   rows experts     n     k   4 bits             8 bits
+//   2048       1  4096  4096    24.8  30.9  34.0   37.5  37.7  52.3
+//   4096       8  1536  2048    17.1  19.9  24.8   23.0  22.5  33.5
+//  16384       8  2048  4096    88.6  97.5 100.8  149.1 122.9 163.8
+//  32768     128  1536  2048   111.5 105.4 122.1  154.9 132.2 181.6
+//  32768      32  7168  2688     513   469   495
+//   8192       1  8192  8192   300.0 297.6 261.9  514.6 413.9 414.8
+// So rows in 8 bits take 256 x 128 (two workgroups to a CU, one's products under
+// the other's results; the LDS keeps up with them) but where that would leave
+// channels or CUs idle.  Rows in 4 bits need more of the LDS than the products
+// last in any tile but the largest: that one for many tiles and long axes, 256 x
+// 128 for very many tiles, which amortize its results.
+struct Tile4 {
+  int channels, rows;
+};
+Tile4 matmul4_tile(const Instances& in, int x_bits, int n, int k) {
+  if (in.rows <= (int64_t)8 * in.E) return {0, 0};
+  const int64_t flat = in.rows / 128 * ((n + 255) / 256), square = in.rows / 256 * ((n + 255) / 256);
+  const int blocks = (n + 127) / 128;
+  if (blocks == 1 || blocks == 3) return {128, 128};
+  if (x_bits == 8) return flat >= 192 ? Tile4{256, 128} : Tile4{128, 128};
+  if (k > 4096 && square >= 1024 && in.rows >= (int64_t)192 * in.E && in.cap <= kCapWide) return {256, 256};
+  return flat >= 1536 ? Tile4{256, 128} : Tile4{128, 128};
 }
 
 template <int XB>
 hipError_t launch(const Instances& in, const uint8_t* x, const uint8_t* xs, const uint8_t* w, const uint8_t* ws, int n,
                   int k, uint16_t* y, int32_t* status, hipStream_t st) {
-  const int tile = matmul4_tile(in, n);
-  if (tile == 256) return launch_tiles<XB, 256, 256>(in, x, xs, w, ws, n, k, y, status, st);
-  if (tile == 128) return launch_tiles<XB, 128, 128>(in, x, xs, w, ws, n, k, y, status, st);
-  return launch_rows16<XB>(in, x, xs, w, ws, n, k, y, status, st);
+  const Tile4 tile = matmul4_tile(in, XB, n, k);
+  if (tile.channels == 0) return launch_rows16<XB>(in, x, xs, w, ws, n, k, y, status, st);
+  if (tile.channels == 128) return launch_tiles<XB, 128, 128>(in, x, xs, w, ws, n, k, y, status, st);
+  if constexpr (XB == 4)
+    if (tile.rows == 256) return launch_tiles<XB, 256, 256>(in, x, xs, w, ws, n, k, y, status, st);
+  return launch_tiles<XB, 256, 128>(in, x, xs, w, ws, n, k, y, status, st);
 }
 
 }  // namespace
 
-int64_t matmul4_tiles(const Instances& in, int32_t n) {
-  const int tile = matmul4_tile(in, n);
-  return tile == 0 ? 0 : row_tile_ids(in, tile) * ((n + tile - 1) / tile);
+int64_t matmul4_tiles(const Instances& in, int32_t x_bits, int32_t n, int32_t k) {
+  const Tile4 tile = matmul4_tile(in, x_bits, n, k);
+  return tile.channels == 0 ? 0 : row_tile_ids(in, tile.rows) * ((n + tile.channels - 1) / tile.channels);
 }
 
 hipError_t launch_matmul4(const Instances& in, int32_t x_bits, const uint8_t* x, const uint8_t* xs, const uint8_t* w,

@@ -269,9 +269,13 @@ def test_products_of_many_instances(mp):
     check_products(mp, loads, np.concatenate([np.arange(E), rng.permutation(E)[:B]]), E, 24, 40, B)
 
 
-@pytest.mark.parametrize("loads,E,n,k", [([4100, 4204], 2, 4000, 328), ([8192], 1, 4100, 700), ([300, 8000, 70], 3, 4096, 256)])
+@pytest.mark.parametrize("loads,E,n,k", [
+    ([4100, 4204], 2, 4000, 328), ([8192], 1, 4100, 700), ([300, 8000, 70], 3, 4096, 256),
+    ([16500, 16400], 2, 2000, 4400),            # 256 x 256 for rows in 4 bits, an odd number of lines of 256
+    ([20000, 130, 19990], 3, 1500, 650),        # 256 x 128 for both
+    ([9000, 8000], 2, 700, 384)])
 def test_products_in_the_largest_tiles(mp, loads, E, n, k):
-    """Tiles of 256 x 256, several to a workgroup; rows at the tiles' ends and some others."""
+    """Tiles of 256 x 128 and 256 x 256, several to a workgroup; rows at the tiles' ends and some others."""
     rows = sum(loads)
     print("products4 loads=%s E=%d n=%d k=%d" % (loads, E, n, k), flush=True)
     layer = layer_for(mp, rows, E)
@@ -291,7 +295,7 @@ def test_products_in_the_largest_tiles(mp, loads, E, n, k):
         sx = None if four else refs4.spread(b.scale.cpu().double(), 128, k)
         for e, a, z in spans:
             at = torch.tensor(sorted({t for t in [*range(a, a + 40), *range(a + 240, a + 270), *range(z - 40, z),
-                                                  *range(a, z, 37)] if a <= t < z}))
+                                                  *range(a, z, max(37, (z - a) // 300))] if a <= t < z}))
             want, off_ = xv[at] @ wv[e].t(), refs4.added(xv[at], wv[e])
             if not four:
                 off_ = off_ + refs4.cut(xv[at], sx[at], wv[e], sw[e])
