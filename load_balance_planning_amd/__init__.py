@@ -516,8 +516,10 @@ class Blocks4:
     @staticmethod
     def shapes(lead, cols: int):
         """Shapes of q and scale of rows (lead (rows,)) or matrices (lead (experts, rows))."""
-        lines = -(-cols // LINE4)
-        return (*lead, lines * (LINE4 // 2)), (*lead[:-1], lines, lead[-1], LINE4 // BLOCK4)
+        lines = -(-cols // 256)
+        if len(lead) == 1:
+            return (lead[0], 128 * lines), (lines, lead[0], 8)
+        return (lead[0], lead[1], 128 * lines), (lead[0], lines, lead[1], 8)
 
 
 class Layer:
@@ -853,6 +855,11 @@ class Layer:
         self._check_tensor(b.q, q, self._fp4)
         self._check_tensor(b.scale, scale, self._e8m0)
 
+    def _check_16bit_here(self, t, name):
+        """_check_16bit of a tensor whose shape is the call's own."""
+        if t.dtype is not self._bf16 or t.get_device() != self._index or not t.is_contiguous():
+            self._check_16bit(t, t.shape, name)
+
     def _result_blocks4(self, out, stream, lead, cols) -> Blocks4:
         if out is not None:
             if out.cols != cols:
@@ -860,6 +867,9 @@ class Layer:
             self._check_blocks4(out, lead)
             return out
         q, scale = Blocks4.shapes(lead, cols)
+        if stream is None:
+            empty, device = self.torch.empty, self.device
+            return Blocks4(empty(q, dtype=self._fp4, device=device), empty(scale, dtype=self._e8m0, device=device), cols)
         return Blocks4(self._empty(q, self._fp4, stream), self._empty(scale, self._e8m0, stream), cols)
 
     def quantize4(self, x, stream=None, out=None) -> Blocks4:
@@ -867,9 +877,10 @@ class Layer:
         if x.dim() != 2:
             raise ValueError("x must be [rows][cols]")
         rows, cols = x.shape
-        self._check_16bit(x, (rows, cols), "x")
+        self._check_16bit_here(x, "x")
         out = self._result_blocks4(out, stream, (rows,), cols)
-        moex4_quantize(self.handle, _addr(x), rows, cols, _addr(out.q), _addr(out.scale), self._stream(stream))
+        moex4_quantize(self.handle, x.data_ptr(), rows, cols, out.q.data_ptr(), out.scale.data_ptr(),
+                       self._stream(stream))
         return out
 
     def quantize_weights4(self, w, transposed: bool = False, stream=None, out=None):
@@ -896,8 +907,8 @@ class Layer:
             out = self._empty((*lead, b.cols), self._bf16, stream)
         else:
             self._check_16bit(out, (*lead, b.cols), "out")
-        moex4_values(self.handle, _addr(b.q), _addr(b.scale), lead[0] if len(lead) == 2 else 1, lead[-1], b.cols,
-                     _addr(out), self._stream(stream))
+        moex4_values(self.handle, b.q.data_ptr(), b.scale.data_ptr(), lead[0] if len(lead) == 2 else 1, lead[-1], b.cols,
+                     out.data_ptr(), self._stream(stream))
         return out
 
     def swiglu4(self, y, stream=None, out=None) -> Blocks4:
@@ -939,7 +950,9 @@ class Layer:
         [E][H][f]: both Blocks4 or both Blocks.  topk_idx defaults to this layer's, of its last gate() or route()."""
         T, E, k, H = self._dims
         topk_idx = self.route_out.topk_idx if topk_idx is None else topk_idx
-        self._check_16bit(hidden, (T, H), "hidden")
+        if hidden.shape != (T, H) or hidden.dtype is not self._bf16:
+            self._check_16bit(hidden, (T, H), "hidden")
+        self._check_16bit_here(hidden, "hidden")
         self._check_tensor(topk_idx, (T, k), self.torch.int32)
         self._check_tensor(weight, (T, k), self.torch.float32)
         f, four = w2.cols, isinstance(w1, Blocks4)
@@ -953,16 +966,18 @@ class Layer:
         else:
             self._check_blocks(w1, (E, 2 * f), (E, -(-2 * f // BLOCK)))
             self._check_blocks(w2, (E, H), (E, -(-H // BLOCK)))
+        nbytes = self._few_bytes.get(f)
+        if nbytes is None:
+            nbytes = self._few_bytes[f] = moex4_experts_work(self.handle, f)
         if out is None:
-            out = self._empty((T, H), hidden.dtype, stream)
+            out = self.torch.empty_like(hidden) if stream is None else self._empty((T, H), hidden.dtype, stream)
         else:
             self._check_16bit(out, (T, H), "out")
             self._check_apart(out, hidden)
-        if f not in self._few_bytes:
-            self._few_bytes[f] = moex4_experts_work(self.handle, f)
-        work = self._empty((self._few_bytes[f],), self.torch.uint8, stream)
-        moex4_experts(self.handle, _addr(hidden), _addr(topk_idx), _addr(weight), 4 if four else 8, f, _addr(w1.q),
-                      _addr(w1.scale), _addr(w2.q), _addr(w2.scale), _addr(work), _addr(out), self._stream(stream))
+        work = self._empty((nbytes,), self.torch.uint8, stream)
+        moex4_experts(self.handle, hidden.data_ptr(), topk_idx.data_ptr(), weight.data_ptr(), 4 if four else 8, f,
+                      w1.q.data_ptr(), w1.scale.data_ptr(), w2.q.data_ptr(), w2.scale.data_ptr(), work.data_ptr(),
+                      out.data_ptr(), self._stream(stream))
         return out
 
     def place(self, cooc=None, max_swaps: int = -1, stream=None):

@@ -559,10 +559,22 @@ namespace {
 constexpr int kCapWide = 1536;  // instances whose tile counts fit the LDS beside 256 x 256 tiles
 
 // The tile of a product, by the mean of rows per expert (the loads themselves are
-// on the device); channels 0: the streaming kernel, up to 8 rows an expert.  us in
-// 128 x 128, 256 x 128 and 256 x 256 (channels x rows):
+// on the device).
+//
+// Few rows: bound by the matrices, which the streaming kernel reads straight into
+// registers.  us in it and in tiles, the matrices not in the caches:
+//   experts     n     k  rows an expert   4 bits        8 bits
+//       128  1536  2048               4    48.0  51.2    43.1  61.4
+//       128  1536  2048              12    58.7  53.2    55.4  57.9
+//        32  5376  7168               8   146.6 137.2   135.8 160
+//        32  5376  7168              16   174.9 140.6   168.0 171.0
+//         8  1536  2048              24     8.5  10.6     9.6  13.0
+// (few matrices: the tiles' latency counts).
+//
+// us in 128 x 128, 256 x 128 and 256 x 256 (channels x rows):
 //   rows experts     n     k   4 bits             8 bits
 //   2048       1  4096  4096    24.8  30.9  34.0   37.5  37.7  52.3
+//   1024       8  4096  4096                       40.8  41.4
 //   4096       8  1536  2048    17.1  19.9  24.8   23.0  22.5  33.5
 //  16384       8  2048  4096    88.6  97.5 100.8  149.1 122.9 163.8
 //  32768     128  1536  2048   111.5 105.4 122.1  154.9 132.2 181.6
@@ -577,13 +589,15 @@ struct Tile4 {
   int channels, rows;
 };
 Tile4 matmul4_tile(const Instances& in, int x_bits, int n, int k) {
-  if (in.rows <= (int64_t)8 * in.E) return {0, 0};
-  const int64_t flat = in.rows / 128 * ((n + 255) / 256), square = in.rows / 256 * ((n + 255) / 256);
+  const bool small = (double)in.E * n * k < (double)(1 << 26);
+  if (in.rows <= (int64_t)(small ? 32 : x_bits == 4 ? 6 : 12) * in.E) return {0, 0};
+  const int64_t across = (n + 255) / 256, used = in.rows < in.E ? in.rows : in.E;
   const int blocks = (n + 127) / 128;
   if (blocks == 1 || blocks == 3) return {128, 128};
-  if (x_bits == 8) return flat >= 192 ? Tile4{256, 128} : Tile4{128, 128};
-  if (k > 4096 && square >= 1024 && in.rows >= (int64_t)192 * in.E && in.cap <= kCapWide) return {256, 256};
-  return flat >= 1536 ? Tile4{256, 128} : Tile4{128, 128};
+  if (x_bits == 8) return (in.rows / 128 + used) * across >= 300 ? Tile4{256, 128} : Tile4{128, 128};
+  if (k > 4096 && in.rows / 256 * across >= 1024 && in.rows >= (int64_t)192 * in.E && in.cap <= kCapWide)
+    return {256, 256};
+  return in.rows / 128 * across >= 1536 ? Tile4{256, 128} : Tile4{128, 128};
 }
 
 template <int XB>
