@@ -70,15 +70,14 @@ __host__ __device__ inline size_t chosen_lds(const Dims& d) {
 template <int THREADS>
 __device__ __forceinline__ Chosen collect_lds(const Dims& d, const int32_t* __restrict__ topk, unsigned char* lds,
                                           int32_t* status) {
-  __shared__ int32_t sums[THREADS / 64];
-  const int slots = d.T * d.k, cap = chosen_cap(d);
+  const int slots = d.T * d.k, cap = chosen_cap(d), lane = threadIdx.x & 63;
   Chosen c;
   c.mask = reinterpret_cast<uint64_t*>(lds);
   c.first = reinterpret_cast<int32_t*>(lds + 8 * d.E);
   c.expert = reinterpret_cast<uint16_t*>(c.first + cap + 1);
   c.slot = c.expert + cap;
   uint16_t* const where = c.slot + slots;
-  constexpr int kPer = 2048 / THREADS;  // slots of a thread at most, and experts
+  constexpr int kPer = 2048 / THREADS;  // slots of a thread at most
   int e[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -101,27 +100,16 @@ __device__ __forceinline__ Chosen collect_lds(const Dims& d, const int32_t* __re
   }
   if (bad && status && blockIdx.x == 0) atomicOr(status, MOE_STATUS_BAD_TOPK);
   __syncthreads();
-  // entries and their slots, counted together: 16 bits each
-  const int per = (d.E + THREADS - 1) / THREADS, from = threadIdx.x * per;
+  // Entries and their slots, counted together, 16 bits each.  Every wave goes over all
+  // experts and writes the same, so that none waits for another.
+  const int per = (d.E + 63) / 64, from = lane * per;
   int mine = 0;
   for (int i = from; i < min(from + per, d.E); ++i) {
     const int m = __popcll(c.mask[i]);
     mine += (m + kCols - 1) / kCols * 0x10000 + m;
   }
-  int incl = mine;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int o = __shfl_up(incl, off);
-    incl += (threadIdx.x & 63) >= off ? o : 0;
-  }
-  if ((threadIdx.x & 63) == 63) sums[threadIdx.x >> 6] = incl;
-  __syncthreads();
-  int before = incl - mine, all = 0;
-#pragma unroll
-  for (int q = 0; q < THREADS / 64; ++q) {
-    before += q < (int)(threadIdx.x >> 6) ? sums[q] : 0;
-    all += sums[q];
-  }
+  const int incl = group_incl_scan<64>(mine, lane), all = __builtin_amdgcn_readlane(incl, 63);
+  int before = incl - mine;
   c.n = all >> 16;
   for (int i = from; i < min(from + per, d.E); ++i) {
     where[i] = (uint16_t)before;
@@ -131,8 +119,8 @@ __device__ __forceinline__ Chosen collect_lds(const Dims& d, const int32_t* __re
       before += 0x10000 + min(m, kCols);
     }
   }
-  if (threadIdx.x == 0) c.first[c.n] = all & 0xffff;
-  __syncthreads();
+  if (lane == 0) c.first[c.n] = all & 0xffff;
+  wave_lds_sync();
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int s = threadIdx.x + i * THREADS;
@@ -561,12 +549,13 @@ __global__ __launch_bounds__(64 * kDownWaves, kDownWaves == 16 ? 4 : 2) void exp
   __shared__ uint32_t arrived;
   float* sums = reinterpret_cast<float*>(lds);  // [waves][T][kOut], the choice behind it
   const int per_wave = d.T * kOut;
-  for (int i = threadIdx.x; i < kDownWaves * per_wave; i += kDownThreads) sums[i] = 0.0f;
   const auto ch = collect<SMALL, kDownThreads>(d, topk, lds + sizeof(float) * kDownWaves * per_wave, nullptr);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  __syncthreads();
   float* mine = sums + wave * per_wave;
+  auto clear = [&]() {  // this wave's sums
+    for (int i = lane; i < per_wave / 4; i += 64) *reinterpret_cast<v4f*>(mine + 4 * i) = v4f{0, 0, 0, 0};
+  };
   const int share = blockIdx.x / chunks, chunk = blockIdx.x - share * chunks;
   const int c0 = chunk * width, valid = min(width, d.H - c0);
   const int fp = (int)padded_cols4(f), steps = (f + kHalves * kBlk - 1) / (kHalves * kBlk);
@@ -637,6 +626,7 @@ __global__ __launch_bounds__(64 * kDownWaves, kDownWaves == 16 ? 4 : 2) void exp
     };
     Step next;
     load(&next);
+    clear();  // while the first step comes in
     v4f acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
     for (int item = from; item < to; ++item) {
       const auto entry = one;
@@ -690,6 +680,8 @@ __global__ __launch_bounds__(64 * kDownWaves, kDownWaves == 16 ? 4 : 2) void exp
       }
       wave_lds_sync();
     }
+  } else {
+    clear();
   }
   __syncthreads();
   auto write = [&](int i, float v) {  // sum i of [T][kOut]
