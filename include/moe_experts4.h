@@ -121,9 +121,8 @@ int moex4_matmul(moe_plan_t h, const moe_plan_out* plan, const int32_t* inst_off
  * moex4_experts_work says for the handle and f (host only).  After the call it
  * begins with the activations a, uint8 [T*k][fp], and their scales, uint8
  * [T*k][fp/32], fp = f rounded up to 256, of the slots whose index is good.
- * An index outside [0, E) or repeated within a token sets MOE_STATUS_BAD_TOPK (an
- * index outside is left out; which of a repeated one's weights counts, or both,
- * is not specified).  f >= 1; MOE_ERR_UNSUPPORTED for more than 64 tokens, for f
+ * An index outside [0, E) or repeated within a token sets MOE_STATUS_BAD_TOPK; such
+ * a slot is left out, of a repeated index all but the first.  f >= 1; MOE_ERR_UNSUPPORTED for more than 64 tokens, for f
  * or H above 2^20, and for matrices of 2^36 values or more.
  */
 int moex4_experts_work(moe_plan_t h, int32_t f, int64_t* bytes);

@@ -77,6 +77,7 @@ __device__ __forceinline__ Chosen collect_lds(const Dims& d, const int32_t* __re
   c.expert = reinterpret_cast<uint16_t*>(c.first + cap + 1);
   c.slot = c.expert + cap;
   uint16_t* const where = c.slot + slots;
+  __shared__ int repeated;
   constexpr int kPer = 2048 / THREADS;  // slots of a thread at most
   int e[kPer];
 #pragma unroll
@@ -85,6 +86,7 @@ __device__ __forceinline__ Chosen collect_lds(const Dims& d, const int32_t* __re
     e[i] = s < slots ? topk[s] : -1;
   }
   for (int i = threadIdx.x; i < d.E; i += THREADS) c.mask[i] = 0ull;
+  if (threadIdx.x == 0) repeated = 0;
   __syncthreads();
   bool bad = false;
 #pragma unroll
@@ -96,10 +98,22 @@ __device__ __forceinline__ Chosen collect_lds(const Dims& d, const int32_t* __re
       continue;
     }
     const uint64_t bit = 1ull << (s / d.k);
-    bad |= (atomicOr(reinterpret_cast<unsigned long long*>(c.mask + e[i]), (unsigned long long)bit) & bit) != 0ull;
+    if ((atomicOr(reinterpret_cast<unsigned long long*>(c.mask + e[i]), (unsigned long long)bit) & bit) != 0ull) {
+      bad = true;
+      repeated = 1;
+    }
   }
   if (bad && status && blockIdx.x == 0) atomicOr(status, MOE_STATUS_BAD_TOPK);
   __syncthreads();
+  if (repeated) {  // the first of a token's slots with an expert is the one that counts
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int s = threadIdx.x + i * THREADS;
+      if (s >= slots) continue;
+      for (int before = s / d.k * d.k; before < s; ++before)
+        if (topk[before] == e[i]) e[i] = -1;
+    }
+  }
   // Entries and their slots, counted together, 16 bits each.  Every wave goes over all
   // experts and writes the same, so that none waits for another.
   const int per = (d.E + 63) / 64, from = lane * per;
@@ -176,12 +190,18 @@ __device__ __forceinline__ ChosenSmall collect_small(const Dims& d, const int32_
     atomicOr(mask + c.e, 1ull << lane);
     same = *reinterpret_cast<volatile unsigned long long*>(mask + c.e);
   }
+  // an earlier slot of the same token with the same expert is the one that counts
+  const uint64_t earlier = ((1ull << lane) - 1ull) & ~((1ull << (lane / d.k * d.k)) - 1ull);
+  const uint64_t repeated = __ballot((same & earlier) != 0ull);
+  if (repeated >> lane & 1ull) {
+    bad = true;
+    c.e = -1;
+  }
+  same &= ~repeated;
   c.order = __popcll(same & ((1ull << lane) - 1ull));
-  const uint64_t leader = __ballot(good && c.order % kCols == 0);
+  const uint64_t leader = __ballot(c.e >= 0 && c.order % kCols == 0);
   c.n = __popcll(leader);
   c.rank = leader >> lane & 1ull ? __popcll(leader & ((1ull << lane) - 1ull)) : -1;
-  // a slot of the same token with the same expert
-  bad |= good && (same & ~(1ull << lane) & (((1ull << d.k) - 1ull) << (lane / d.k * d.k))) != 0ull;
   if (status && blockIdx.x == 0 && threadIdx.x < 64 && __ballot(bad) != 0ull && lane == 0)
     atomicOr(status, MOE_STATUS_BAD_TOPK);
   return c;
@@ -768,7 +788,7 @@ template <int WB, bool SMALL, int WAVES>
 hipError_t launch_down(const Dims& d, const Work& k, size_t lds, const int32_t* topk_idx, const float* weight, int32_t f,
                        const uint8_t* w2, const uint8_t* w2s, uint8_t* work, uint16_t* out, hipStream_t st) {
   lds += (size_t)WAVES * d.T * kOut * sizeof(float);
-  if (lds > 64 * 1024 - 32 * 1024) {
+  if (lds > 32768) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(experts_down_kernel<WB, SMALL, WAVES>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;

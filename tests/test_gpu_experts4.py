@@ -269,6 +269,15 @@ def test_products_of_many_instances(mp):
     check_products(mp, loads, np.concatenate([np.arange(E), rng.permutation(E)[:B]]), E, 24, 40, B)
 
 
+@pytest.mark.parametrize("n,k", [(24, 40), (520, 40)])
+def test_tiles_of_many_instances(mp, n, k):
+    """The same with 70000 rows: tiles whose lists of instances are the longest."""
+    rng = np.random.RandomState(1)
+    E, B = 2048, 1000
+    loads = rng.multinomial(70000, rng.dirichlet(np.full(E + B, 0.3)))
+    check_products(mp, loads, np.concatenate([np.arange(E), rng.permutation(E)[:B]]), E, n, k, B)
+
+
 @pytest.mark.parametrize("loads,E,n,k", [
     ([4100, 4204], 2, 4000, 328), ([8192], 1, 4100, 700), ([300, 8000, 70], 3, 4096, 256),
     ([16500, 16400], 2, 2000, 4400),            # 256 x 256 for rows in 4 bits, an odd number of lines of 256
@@ -439,8 +448,9 @@ def test_few_tokens(mp, T, E, k, H, f, bits):
 
 
 def test_few_tokens_of_many_experts(mp):
-    """2048 experts and 32 of them a token: 2048 slots, and the largest lists in LDS."""
+    """2048 experts and 32 of them a token: 2048 slots, and the largest lists in LDS; and with sixteen waves."""
     check_few(mp, 64, 2048, 32, 40, 24, 4, seed=3)
+    check_few(mp, 16, 2048, 32, 40, 24, 4, seed=4)
 
 
 def test_few_tokens_none(mp):
@@ -474,6 +484,25 @@ def test_few_tokens_bad_indices(mp, bits):
     none = torch.full_like(idx, -1)
     assert (layer.experts(hidden, weight, w1, w2, topk_idx=none).cpu() == 0).all()
     assert layer.status() == mp.MOE_STATUS_BAD_TOPK
+    layer.close()
+
+
+@pytest.mark.parametrize("T,k", [(6, 3), (20, 4), (64, 8)])
+def test_few_tokens_repeated_indices(mp, T, k):
+    """Of a token's slots with the same expert the first counts: the others are as indices outside the experts."""
+    layer, idx, weight, w1, w2 = few_layer(mp, T, 16, k, 200, 96, 4, T)
+    hidden = normal(T, T, 200).to(layer.device)
+    idx[1] = idx[1, 0]  # all of them
+    idx[T - 2, k - 1] = idx[T - 2, 0]
+    idx[T - 1, 2] = idx[T - 1, 1]
+    seen = torch.zeros_like(idx, dtype=torch.bool)
+    for j in range(1, k):
+        seen[:, j] = (idx[:, :j] == idx[:, j:j + 1]).any(1)
+    want = layer.experts(hidden, weight, w1, w2, topk_idx=idx.masked_fill(seen, -1)).cpu()
+    assert layer.status() == mp.MOE_STATUS_BAD_TOPK
+    got = layer.experts(hidden, weight, w1, w2, topk_idx=idx).cpu()
+    assert layer.status() == mp.MOE_STATUS_BAD_TOPK
+    assert torch.equal(got, want)
     layer.close()
 
 
