@@ -356,10 +356,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void experts_up_kernel(Dims d, const
 #ifdef __HIP_DEVICE_COMPILE__
   constexpr int kHalves = halves(WB), kChunks = 16 * kHalves;   // chunks of 8 columns of a token's step
   constexpr int kAtOnce = 64 / kChunks, kSets = kCols / kAtOnce;  // tokens of a load, loads of 16 tokens
-  constexpr int kPart = kCols * (2 * kChan + 4) * 4, kRows = kCols * kChunks * 16;
+  constexpr int kPartRow = 2 * kChan + 4, kRows = kCols * kChunks * 16;
   extern __shared__ __align__(16) unsigned char lds[];
-  // a wave's rows of a step, and then its sums
-  __shared__ __align__(16) unsigned char own_s[WAVES][kRows > kPart ? kRows : kPart];
+  constexpr int kTurns = WAVES == 4 ? 2 : 1;  // places of sums: with two a unit needs one barrier
+  __shared__ __align__(16) unsigned char own_s[WAVES][kRows];  // a wave's rows of a step
+  __shared__ __align__(16) float part_s[kTurns][WAVES][kCols * kPartRow];
   __shared__ __align__(16) uint32_t scale_s[WAVES][64 * kHalves];
   if (blockIdx.x == 0)  // for the launch behind this one
     for (int i = threadIdx.x; i < counters; i += 64 * WAVES) counter[i] = 0u;
@@ -427,7 +428,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void experts_up_kernel(Dims d, const
   Unit u = begin(a, unit - a * chunks);
   Step next;
   if (wave < steps) load(&next, u, wave);
-  for (;;) {
+  for (int turn = 0;; ++turn) {
     v4f acc[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] = v4f{0, 0, 0, 0};
@@ -484,9 +485,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void experts_up_kernel(Dims d, const
       }
       wave_lds_sync();
     }
-    float* const part = reinterpret_cast<float*>(rows_s);  // [kCols][2 kChan + 4]
+    const auto& parts = part_s[turn % kTurns];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<v4f*>(part + r * (2 * kChan + 4) + 16 * i + 4 * g) = acc[i];
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<v4f*>(&part_s[turn % kTurns][wave][r * kPartRow + 16 * i + 4 * g]) = acc[i];
     // the next unit's first step comes in under this one's sums
     const auto one = u.one;
     const int chunk = u.chunk, c0 = chunk * kChan;
@@ -503,12 +504,13 @@ __global__ __launch_bounds__(64 * WAVES, 2) void experts_up_kernel(Dims d, const
       if (wave < steps) load(&next, u, wave);
     }
     __syncthreads();
-    const int row = threadIdx.x >> 4, c = 2 * (threadIdx.x & 15);
-    if (row < kCols) {  // whole waves
+    // the entry's first slots fall to another wave each turn
+    const int row = (int)((threadIdx.x >> 4) + 4 * turn) % (4 * WAVES), c = 2 * (threadIdx.x & 15);
+    if (row < kCols && row / 4 * 4 < one.count) {  // whole waves
       float2_ gv = {0.0f, 0.0f}, uv = {0.0f, 0.0f};
 #pragma unroll
       for (int q = 0; q < WAVES; ++q) {
-        const float* p = reinterpret_cast<const float*>(own_s[q]) + row * (2 * kChan + 4) + c;
+        const float* p = parts[q] + row * kPartRow + c;
         gv += *reinterpret_cast<const float2_*>(p);
         uv += *reinterpret_cast<const float2_*>(p + kChan);
       }
@@ -536,7 +538,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void experts_up_kernel(Dims d, const
       }
     }
     if (!more) break;
-    __syncthreads();
+    if (kTurns == 1) __syncthreads();
   }
 #endif
 }
