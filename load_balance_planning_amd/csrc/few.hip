@@ -569,12 +569,12 @@ __global__ __launch_bounds__(64 * kDownWaves, kDownWaves == 16 ? 4 : 2) void exp
   __shared__ __align__(16) uint32_t act_scale_s[kDownWaves][kCols * kHalves];
   __shared__ __align__(16) uint32_t scale_s[kDownWaves][kOut * kHalves];
   __shared__ uint32_t arrived;
-  float* sums = reinterpret_cast<float*>(lds);  // [waves][T][kOut], the choice behind it
-  const int per_wave = d.T * kOut;
-  const auto ch = collect<SMALL, kDownThreads>(d, topk, lds + sizeof(float) * kDownWaves * per_wave, nullptr);
+  float* sums = reinterpret_cast<float*>(lds);  // [waves][T + 1][kOut], the choice behind it
+  const int per_wave = d.T * kOut, stride = per_wave + kOut;
+  const auto ch = collect<SMALL, kDownThreads>(d, topk, lds + sizeof(float) * kDownWaves * stride, nullptr);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  float* mine = sums + wave * per_wave;
+  float* mine = sums + wave * stride;
   auto clear = [&]() {  // this wave's sums
     for (int i = lane; i < per_wave / 4; i += 64) *reinterpret_cast<v4f*>(mine + 4 * i) = v4f{0, 0, 0, 0};
   };
@@ -634,12 +634,14 @@ __global__ __launch_bounds__(64 * kDownWaves, kDownWaves == 16 ? 4 : 2) void exp
     auto place = [&](int slot, int p) {
       return WB == 4 ? slot * 16 + (p ^ slot) : (slot >> 1) * 16 + (((slot & 1) << 3 | p) ^ (slot >> 1));
     };
+    // Lanes without a slot add to the row behind the tokens'.  (A branch of lanes draws
+    // the products in under it, where masked operands are wrong.)
     auto add = [&](int s, const v4f* acc) {
-      if (s < 0) return;
-      const float by = weight[s];
+      const float by = weight[max(s, 0)];
+      float* const row = mine + (s >= 0 ? s / d.k : d.T) * kOut + 4 * g;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        v4f* sum = reinterpret_cast<v4f*>(mine + (s / d.k) * kOut + 16 * i + 4 * g);
+        v4f* sum = reinterpret_cast<v4f*>(row + 16 * i);
         v4f v = *sum;
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] += by * acc[i][j];
@@ -715,7 +717,7 @@ __global__ __launch_bounds__(64 * kDownWaves, kDownWaves == 16 ? 4 : 2) void exp
   for (int i = threadIdx.x; i < per_wave / 2; i += kDownThreads) {
     float2_ v = {0.0f, 0.0f};
 #pragma unroll
-    for (int q = 0; q < kDownWaves; ++q) v += *reinterpret_cast<const float2_*>(sums + q * per_wave + 2 * i);
+    for (int q = 0; q < kDownWaves; ++q) v += *reinterpret_cast<const float2_*>(sums + q * stride + 2 * i);
     if (shares > 1) {
       __hip_atomic_store(own + i, __builtin_bit_cast(pair_, v), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     } else {
@@ -789,7 +791,7 @@ Work work_of(const Dims& d, int f) {
 template <int WB, bool SMALL, int WAVES>
 hipError_t launch_down(const Dims& d, const Work& k, size_t lds, const int32_t* topk_idx, const float* weight, int32_t f,
                        const uint8_t* w2, const uint8_t* w2s, uint8_t* work, uint16_t* out, hipStream_t st) {
-  lds += (size_t)WAVES * d.T * kOut * sizeof(float);
+  lds += (size_t)WAVES * (d.T + 1) * kOut * sizeof(float);
   if (lds > 32768) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(experts_down_kernel<WB, SMALL, WAVES>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
