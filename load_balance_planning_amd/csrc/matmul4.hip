@@ -48,7 +48,7 @@ __global__ __launch_bounds__(256) void matmul4_rows16_kernel(Instances in, const
   __shared__ float part[4][kRowsS][kChanS + 4];
   __shared__ __align__(8) uint32_t scale_s[4][2 * kChanS];
   if (blockIdx.x == 0) check_instances(in, status);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int nb = (k + kCols4 - 1) / kCols4;                             // lines of a 4-bit row
   const int nb8 = (k + kBlk - 1) / kBlk, ns8 = (nb8 + 3) / 4 * 4;      // blocks of an 8-bit row
