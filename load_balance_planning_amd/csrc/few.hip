@@ -765,18 +765,21 @@ Work work_of(const Dims& d, int f) {
   // else two of four waves.
   k.waves = d.T <= 16 ? 16 : 4;
   const int want = k.waves == 16 ? 256 : 512;
+  // shares cost a pass through memory: four lines a wave at least
+  const int64_t lines = (int64_t)chosen_cap(d) * (k.fp / kCols4), most = lines / (4 * k.waves);
   // As wide as 32 channels; but of many channels so that their number divides among
-  // the CUs (7168 channels: 256 workgroups of 28 and not 224 of 32).
-  const int rounds = (d.H + 256 * kOut - 1) / (256 * kOut);
+  // the CUs (7168 channels: 256 workgroups of 28 and not 224 of 32), and where there
+  // is nothing to share so narrow that all CUs have some (a token with 8 experts of 768
+  // x 2048: 7.5 us in 64 workgroups, 6.0 in 256).  Shares of wide pieces are better
+  // than narrow ones (8 tokens, 32 experts of 2048 channels in 8 bits: 23 us, 33).
   k.width = kOut;
-  if (d.H > 128 * kOut) {
+  if (d.H > 128 * kOut || most < 2) {
+    const int rounds = (d.H + 256 * kOut - 1) / (256 * kOut);
     const int even = ((d.H + 256 * rounds - 1) / (256 * rounds) + 3) / 4 * 4;
-    k.width = even < kOut ? even : kOut;
+    k.width = even < 8 ? 8 : even < kOut ? even : kOut;
   }
   k.chunks = (d.H + k.width - 1) / k.width;
-  const int64_t lines = (int64_t)chosen_cap(d) * (k.fp / kCols4);
-  // shares cost a pass through memory: four lines a wave at least
-  const int64_t most = lines / (4 * k.waves), fill = want / k.chunks;
+  const int64_t fill = want / k.chunks;
   k.shares = (int)(fill < most ? fill : most);
   if (k.shares > kMaxShares) k.shares = kMaxShares;
   if (k.shares < 1) k.shares = 1;
