@@ -39,9 +39,10 @@ extern "C" int moex4_quantize_weights(moe_plan_t h, const uint16_t* w, int32_t e
   if (n > (1 << 24) || k > (1 << 24)) return MOE_ERR_UNSUPPORTED;
   if (experts > 0 && (!w || !blocks4_ok(q, scale))) return MOE_ERR_INVALID_ARG;
   if ((qt == nullptr) != (scale_t == nullptr) || (qt && !blocks4_ok(qt, scale_t))) return MOE_ERR_INVALID_ARG;
-  // one 256-thread workgroup per piece, fewer than 2^32 threads; by division, as the product can pass 64 bits
+  // one 256-thread workgroup per piece and up to seven more, fewer than 2^32 threads; by division, as the product
+  // can pass 64 bits
   const int64_t per_matrix = (moe::padded_cols4(n) / moe::kBlk) * (moe::padded_cols4(k) / moe::kBlk);
-  if (experts > (((int64_t)1 << 24) - 1) / per_matrix) return MOE_ERR_UNSUPPORTED;
+  if (experts > (((int64_t)1 << 24) - 8) / per_matrix) return MOE_ERR_UNSUPPORTED;
   const DeviceScope on_device(h->device);
   if (!on_device.ok()) return MOE_ERR_HIP;
   return hip_rc(moe::launch_quantize_weights4(w, experts, n, k, q, scale, qt, scale_t, begin_call(h, stream)));

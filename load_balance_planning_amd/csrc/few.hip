@@ -25,8 +25,6 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float float2_ __attribute__((ext_vector_type(2)));
-typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 [[maybe_unused]] constexpr int kFp8 = 0, kFp4 = 4;  // the instruction's format codes
@@ -147,7 +145,8 @@ __device__ __forceinline__ Chosen collect_lds(const Dims& d, const int32_t* __re
 
 // The same where there are at most 64 slots, one to a lane, in every wave's
 // registers: slots of an expert are a mask in LDS (u64 [E]), and that is all.
-// Entries in the order of their first slots.
+// Entries in the order of their first slots.  (A token: 0.8 us less in the first
+// launch and 0.5 in the second than by lists; 64 slots: 0 and 0.9.)
 struct ChosenSmall {
   int e;      // of the lane's slot; -1: none
   int order;  // of the slot among its expert's
@@ -226,13 +225,6 @@ __device__ __forceinline__ auto collect(const Dims& d, const int32_t* __restrict
   for (int i = 0; i < 4; ++i) v[i] &= (c + 2 * i < cols ? 0xffffu : 0u) | (c + 2 * i + 1 < cols ? 0xffff0000u : 0u);
   return v;
 }
-
-__device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
-  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
-}
-
-// A word's pair.  (By value: a bit cast of a vector's element reads element 0.)
-__device__ __forceinline__ bf16x2 two_bf16(uint32_t w) { return __builtin_bit_cast(bf16x2, w); }
 
 // What eight values of a row become by rounding to e4m3 with a scale per 32, as
 // bf16 again: the four lanes of an aligned quad hold a block.  All NaN where that
@@ -341,8 +333,10 @@ __device__ __forceinline__ v4f multiply(u32x4 q0, u32x4 q1, uint32_t s, const u3
 // what there is of them, the lanes side by side (two tokens a load).  Scales and
 // rows (rounded) pass through LDS, the wave's own part of it, to the lanes that
 // multiply.  Loaded by those lanes each for itself, scales took 8 % and rows 14 %
-// of the time (28 experts of 2 x 2688 x 7168: 132 us), and registers for a second
-// step's loads cost more waves than they were worth.
+// of the time (8 tokens, 29 experts of 2 x 2688 x 7168: 132 us then, 107 now, 5.6
+// TB/s of matrices).  Few workgroups at a time, two to a CU, read best: 1024 of them
+// 154 us where 512 took 132.  Short axes lose to what a unit costs beside its steps
+// (64 tokens, 128 experts of 2 x 768 x 2048: two steps a wave, 45 us, 4.4 TB/s).
 constexpr int kChan = 32;
 template <int WB, int WAVES, bool SMALL>
 __global__ __launch_bounds__(64 * WAVES, 2) void experts_up_kernel(Dims d, const uint16_t* __restrict__ hidden,
@@ -548,7 +542,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void experts_up_kernel(Dims d, const
 // their own in LDS.  The shares of the same channels meet in memory: the workgroup
 // that is the last to write its sums adds them all, in order, and writes the result.
 //
-// Activations and scales pass through LDS as in the launch before.
+// Activations and scales pass through LDS as in the launch before.  8 tokens, 29
+// experts of 7168 x 2688: 56 us, 5.6 TB/s; 64 tokens, 128 experts of 2048 x 768: 26.5
+// us, of which some 10 are the choice of experts and the shares' meeting.  A second
+// step's loads ahead brought nothing (26.7).
 constexpr int kOut = 32, kMaxShares = 8;
 template <int WB, bool SMALL, int kDownWaves>
 __global__ __launch_bounds__(64 * kDownWaves, kDownWaves == 16 ? 4 : 2) void experts_down_kernel(Dims d, const int32_t* __restrict__ topk,
@@ -761,8 +758,10 @@ struct Work {
 Work work_of(const Dims& d, int f) {
   Work k;
   k.fp = (int)padded_cols4(f);
-  // Sixteen waves to a workgroup, one for every CU, where their sums fit the LDS,
-  // else two of four waves.
+  // Sixteen waves to a workgroup, one for every CU, where their sums (128 bytes a
+  // token and wave) fit the LDS beside their steps; else two of four waves.  (A token
+  // with 8 experts of 2048 x 768: 5.9 us in sixteen, 7.8 in four; 16 tokens of 128 such
+  // experts in 8 bits 23.1 and 23.4; 8 tokens, 29 experts of 7168 x 2688 55.8, 54.8.)
   k.waves = d.T <= 16 ? 16 : 4;
   const int want = k.waves == 16 ? 256 : 512;
   // shares cost a pass through memory: four lines a wave at least
@@ -813,6 +812,7 @@ hipError_t launch(const Dims& d, const uint16_t* hidden, const int32_t* topk_idx
   const Work k = work_of(d, f);
   const int64_t units = (int64_t)chosen_cap(d) * ((f + kChan - 1) / kChan);
   const size_t lds = SMALL ? (size_t)8 * d.E : chosen_lds(d);
+  // 512 workgroups are two to a CU (one where there are very many experts)
   hipLaunchKernelGGL((experts_up_kernel<WB, WAVES, SMALL>), dim3((unsigned)(units < 512 ? units : 512)),
                      dim3(64 * WAVES), lds, st, d, hidden, topk_idx, w1, w1s, f, work, work + k.scale,
                      reinterpret_cast<uint32_t*>(work + k.counter), k.chunks, status);
@@ -830,7 +830,9 @@ hipError_t launch_experts(const Dims& d, const uint16_t* hidden, const int32_t* 
                           int32_t w_bits, int32_t f, const uint8_t* w1, const uint8_t* w1s, const uint8_t* w2,
                           const uint8_t* w2s, uint8_t* work, uint16_t* out, int32_t* status, hipStream_t st) {
   if (d.T == 0) return hipSuccess;
-  // Eight waves to a unit where there are fewer units than CUs: half the lines one after the other.
+  // Eight waves to a unit where there are fewer units than CUs: half the lines one after
+  // the other (a token, 8 experts of 2 x 768 x 2048: 7.4 us, in four waves 7.8; 7 tokens
+  // of 2 x 380 x 1000 in 8 bits 6.5, 7.0).
   const bool small = d.T * d.k <= 64, wide = (int64_t)chosen_cap(d) * ((f + kChan - 1) / kChan) <= 256;
   auto go = w_bits == 4 ? small ? wide ? launch<4, true, 8> : launch<4, true, 4> : launch<4, false, 4>
                         : small ? wide ? launch<8, true, 8> : launch<8, true, 4> : launch<8, false, 4>;

@@ -5,7 +5,8 @@
 //   s = smallest power of two with max|x| <= 6 s,  q = e2m1(x / s)
 //
 // All of these move bytes once: 2 read and 0.53 written per value (matrices in
-// both layouts 2 and 1.06, activation 4 and 0.53, values 0.53 and 2).
+// both layouts 2 and 1.06, activation 4 and 0.53, values 0.53 and 2).  A copy of
+// 2 GiB moves 4.8 TB/s here, and reads alone 6.1.
 #include "experts4.h"
 #include "fp4_block.h"
 #include "row_load.h"
@@ -26,8 +27,10 @@ __device__ __forceinline__ uint32_t max_of_4(uint32_t v) {
 }
 
 // Sixteen rows by 256 columns per workgroup, 16 values to a thread: whole
-// 128-byte lines of results, and their scales are one line too.  SWIGLU: x
-// [rows][2 cols], gate and up.
+// 128-byte lines of results, and their scales are one line too.  Memory-bound:
+// 131072 rows of 2048 117 us (5.8 TB/s).  SWIGLU: x [rows][2 cols], gate and up;
+// the exponential and the division (42 vector instructions a value in all) take
+// as long as memory: 32768 rows of 2688 92 us (4.35 TB/s).
 constexpr int kTileRows = 16;
 template <bool SWIGLU>
 __global__ __launch_bounds__(kThreads) void quantize4_rows_kernel(const uint16_t* __restrict__ x, int64_t rows,
@@ -73,7 +76,15 @@ __global__ __launch_bounds__(kThreads) void quantize4_rows_kernel(const uint16_t
 // 8g+7, columns 8 c8 .. 8 c8+7, so a wave loads whole 256-byte row pieces.  A
 // block of 32 columns is four neighbouring threads', one of 32 rows those of a
 // wave with the same columns; the transposed bytes pass through LDS.
+//
+// Values stay bf16 pairs: the conversion divides by the scale, and magnitudes
+// compare as integers.  Memory-bound, both layouts: 128 matrices of 1536 x 2048 268
+// us (4.6 TB/s), 8 of 4096 x 7168 124 us (5.8; their results stay in the last
+// cache).  In fp32, the pieces dealt to the XCDs one by one, and with 8-way
+// conflicts in LDS: 296 and 154.
 constexpr int kTransStride4 = kBlk / 2 + 16;  // LDS bytes of a row of the transposed piece
+// Its 16-byte pieces are exchanged so that eight rows' lie in different banks.
+__device__ __forceinline__ int trans_place(int row, int piece) { return 16 * (piece ^ ((row >> 4) & 3)); }
 __global__ __launch_bounds__(kThreads) void quantize4_weights_kernel(const uint16_t* __restrict__ w, int experts,
                                                                      int n, int k, int pn, int pk,
                                                                      uint8_t* __restrict__ q,
@@ -82,9 +93,11 @@ __global__ __launch_bounds__(kThreads) void quantize4_weights_kernel(const uint1
                                                                      uint8_t* __restrict__ scale_t) {
   __shared__ __align__(16) uint8_t tr[kBlk * kTransStride4];
   __shared__ uint32_t s_row[kBlk], s_col[kBlk];  // four scales each
-  const int bk = blockIdx.x % pk;
-  const int rest = blockIdx.x / pk;
-  const int bn = rest % pn, e = rest / pn;
+  // Every XCD takes a run of pieces: two side by side write a 128-byte line together,
+  // in one L2 then.
+  const int id = (int)(blockIdx.x & 7) * (int)(gridDim.x >> 3) + (int)(blockIdx.x >> 3);
+  const int rest = id / pk, bk = id - rest * pk, e = rest / pn, bn = rest - e * pn;
+  if (e >= experts) return;
   const int c8 = threadIdx.x % 16, rg = threadIdx.x / 16;
   const int c = bk * kBlk + 8 * c8, r0 = bn * kBlk + 8 * rg;
   const uint16_t* __restrict__ base = w + (int64_t)e * n * k;
@@ -108,38 +121,35 @@ __global__ __launch_bounds__(kThreads) void quantize4_weights_kernel(const uint1
   const int nbk = pk / 2, nbn = pn / 2;  // lines of 256 values
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    float f[8];
-    widen8(v[j], f);
-    uint32_t top = 0;
+    uint32_t top = v[j][0] & 0x7fff7fffu;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, magnitude(f[i]));
-    const uint32_t s = scale_byte4(max_of_4(top));
-    const float inv = inverse_scale(s);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] *= inv;
-    const uint32_t o = s == 255u ? 0u : pack_e2m1(f);
+    for (int i = 1; i < 4; ++i) top = pk_max(top, v[j][i] & 0x7fff7fffu);
+    const uint32_t s = scale_byte4(max_of_4(max(top << 16, top & 0xffff0000u)));
+    const uint32_t o = pack_e2m1(v[j][0], v[j][1], v[j][2], v[j][3], s);
     if (r0 + j < n)
       *reinterpret_cast<uint32_t*>(q + (((int64_t)e * n + r0 + j) * pk + bk) * (kBlk / 2) + 4 * c8) = o;
     if ((c8 & 3) == 0) reinterpret_cast<uint8_t*>(s_row)[(8 * rg + j) * 4 + (c8 >> 2)] = (uint8_t)s;
   }
   if (qt) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float f[8];
+    for (int i = 0; i < 4; ++i) {  // two columns
+      uint32_t top = v[0][i] & 0x7fff7fffu;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = i & 1 ? bf16_high(v[j][i / 2]) : bf16_low(v[j][i / 2]);
-      uint32_t top = 0;
+      for (int j = 1; j < 8; ++j) top = pk_max(top, v[j][i] & 0x7fff7fffu);
+      top = pk_max(top, (uint32_t)__shfl_xor((int)top, 16));
+      top = pk_max(top, (uint32_t)__shfl_xor((int)top, 32));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top = max(top, magnitude(f[j]));
-      top = max(top, (uint32_t)__shfl_xor((int)top, 16));
-      top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-      const uint32_t s = scale_byte4(top);
-      const float inv = inverse_scale(s);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t x[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] *= inv;
-      const uint32_t o = s == 255u ? 0u : pack_e2m1(f);
-      *reinterpret_cast<uint32_t*>(tr + (8 * c8 + i) * kTransStride4 + 4 * rg) = o;
-      if ((rg & 3) == 0) reinterpret_cast<uint8_t*>(s_col)[(8 * c8 + i) * 4 + (rg >> 2)] = (uint8_t)s;
+        for (int j = 0; j < 4; ++j)
+          x[j] = __builtin_amdgcn_perm(v[2 * j + 1][i], v[2 * j][i], h ? 0x07060302u : 0x05040100u);
+        const uint32_t s = scale_byte4(h ? top & 0xffff0000u : top << 16);
+        const int col = 8 * c8 + 2 * i + h;
+        *reinterpret_cast<uint32_t*>(tr + col * kTransStride4 + trans_place(col, rg >> 2) + 4 * (rg & 3)) =
+            pack_e2m1(x[0], x[1], x[2], x[3], s);
+        if ((rg & 3) == 0) reinterpret_cast<uint8_t*>(s_col)[col * 4 + (rg >> 2)] = (uint8_t)s;
+      }
     }
   }
   __syncthreads();
@@ -159,11 +169,12 @@ __global__ __launch_bounds__(kThreads) void quantize4_weights_kernel(const uint1
     const int row = bk * kBlk + i / 4;
     if (row < k)
       *reinterpret_cast<u32x4*>(qt + (((int64_t)e * k + row) * pn + bn) * (kBlk / 2) + 16 * (i % 4)) =
-          *reinterpret_cast<const u32x4*>(tr + (i / 4) * kTransStride4 + 16 * (i % 4));
+          *reinterpret_cast<const u32x4*>(tr + (i / 4) * kTransStride4 + trans_place(i / 4, i % 4));
   }
 }
 
-// 32 rows by 256 columns per workgroup, 8 values of four rows to a thread.
+// 32 rows by 256 columns per workgroup, 8 values of four rows to a thread: four
+// loads under way each.  128 matrices of 1536 x 2048 176 us (5.8 TB/s).
 constexpr int kValueRows = 32;
 __global__ __launch_bounds__(kThreads) void values4_kernel(const uint8_t* __restrict__ q,
                                                            const uint8_t* __restrict__ scale, int matrices,
@@ -236,7 +247,7 @@ hipError_t launch_quantize_weights4(const uint16_t* w, int32_t experts, int32_t 
   const int pn = (int)(padded_cols4(n) / kBlk), pk = (int)(padded_cols4(k) / kBlk);
   const int64_t pieces = (int64_t)experts * pn * pk;
   if (pieces == 0) return hipSuccess;
-  hipLaunchKernelGGL(quantize4_weights_kernel, dim3((unsigned)pieces), dim3(kThreads), 0, st, w, experts, n, k, pn, pk,
+  hipLaunchKernelGGL(quantize4_weights_kernel, dim3((unsigned)((pieces + 7) / 8 * 8)), dim3(kThreads), 0, st, w, experts, n, k, pn, pk,
                      q, scale, qt, scale_t);
   return hipGetLastError();
 }
