@@ -29,7 +29,7 @@ __device__ __forceinline__ uint32_t max_of_4(uint32_t v) {
 // Sixteen rows by 256 columns per workgroup, 16 values to a thread: whole
 // 128-byte lines of results, and their scales are one line too.  Memory-bound:
 // 131072 rows of 2048 117 us (5.8 TB/s).  SWIGLU: x [rows][2 cols], gate and up;
-// the exponential and the division (42 vector instructions a value in all) take
+// the exponential and the division (40 vector instructions a value in all) take
 // as long as memory: 32768 rows of 2688 92 us (4.35 TB/s).
 constexpr int kTileRows = 16;
 template <bool SWIGLU>
