@@ -545,7 +545,7 @@ class Layer:
         self._dims = (cfg.T, cfg.E, cfg.k, cfg.H)  # plain integers: a structure's fields cost more to read
         self._cap = cfg.E + cfg.replica_budget
         self._bf16, self._fp4, self._e8m0 = torch.bfloat16, torch.float4_e2m1fn_x2, torch.float8_e8m0fnu
-        self._few_bytes = {}  # memory of an experts() call, by the experts' width
+        self._few = {}  # experts(): the bytes of its memory and its arguments' shapes, by the experts' width and bits
         self._current_stream = _current_stream(torch)
         self.sizes = moe_plan_query(cfg)
         with torch.cuda.device(self.device):
@@ -944,37 +944,47 @@ class Layer:
                      _addr(w.scale), n, k, _addr(out), self._stream(stream))
         return out
 
+    def _few_shapes(self, f: int, four: bool):
+        """Of experts(): the bytes that a call works in, and (shape, dtype) of top-k, weights and the matrices' parts."""
+        torch, (T, E, k, H) = self.torch, self._dims
+        shapes = [((T, k), torch.int32), ((T, k), torch.float32)]
+        for n, cols in ((2 * f, H), (H, f)):
+            if four:
+                q, scale = Blocks4.shapes((E, n), cols)
+            else:
+                q, scale = (E, n, Blocks.padded(cols)), (E, -(-n // BLOCK), Blocks.scales(cols))
+            shapes += [(q, self._fp4 if four else torch.float8_e4m3fn), (scale, self._e8m0)]
+        return moex4_experts_work(self.handle, f), shapes
+
     def experts(self, hidden, weight, w1, w2, topk_idx=None, out=None, stream=None):
         """The experts of a layer of at most 64 tokens, from hidden rows [T][H] and the router's weights [T][k] to the
         combined rows [T][H], without plan and dispatch (moex4_experts).  w1 [E][2 f][H] (gate, then up) and w2
         [E][H][f]: both Blocks4 or both Blocks.  topk_idx defaults to this layer's, of its last gate() or route()."""
-        T, E, k, H = self._dims
+        torch, (T, _, _, H) = self.torch, self._dims
         topk_idx = self.route_out.topk_idx if topk_idx is None else topk_idx
-        if hidden.shape != (T, H) or hidden.dtype is not self._bf16:
-            self._check_16bit(hidden, (T, H), "hidden")
-        self._check_16bit_here(hidden, "hidden")
-        self._check_tensor(topk_idx, (T, k), self.torch.int32)
-        self._check_tensor(weight, (T, k), self.torch.float32)
         f, four = w2.cols, isinstance(w1, Blocks4)
         if w1.cols != H:
             raise ValueError("w1 has %d columns, hidden %d" % (w1.cols, H))
         if four != isinstance(w2, Blocks4):
             raise TypeError("w1 and w2 must both be Blocks4 or both Blocks")
-        if four:
-            self._check_blocks4(w1, (E, 2 * f))
-            self._check_blocks4(w2, (E, H))
-        else:
-            self._check_blocks(w1, (E, 2 * f), (E, -(-2 * f // BLOCK)))
-            self._check_blocks(w2, (E, H), (E, -(-H // BLOCK)))
-        nbytes = self._few_bytes.get(f)
-        if nbytes is None:
-            nbytes = self._few_bytes[f] = moex4_experts_work(self.handle, f)
+        known = self._few.get((f, four))
+        if known is None:
+            known = self._few[f, four] = self._few_shapes(f, four)
+        nbytes, shapes = known
+        if hidden.shape != (T, H) or hidden.dtype is not self._bf16:
+            self._check_16bit(hidden, (T, H), "hidden")
+        self._check_16bit_here(hidden, "hidden")
+        index = self._index
+        for t, (shape, dtype) in zip((topk_idx, weight, w1.q, w1.scale, w2.q, w2.scale), shapes):
+            if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+                self._check_tensor(t, shape, dtype)
         if out is None:
-            out = self.torch.empty_like(hidden) if stream is None else self._empty((T, H), hidden.dtype, stream)
+            out = torch.empty_like(hidden) if stream is None else self._empty((T, H), hidden.dtype, stream)
         else:
             self._check_16bit(out, (T, H), "out")
             self._check_apart(out, hidden)
-        work = self._empty((nbytes,), self.torch.uint8, stream)
+        work = torch.empty(nbytes, dtype=torch.uint8, device=self.device) if stream is None else \
+            self._empty((nbytes,), torch.uint8, stream)
         moex4_experts(self.handle, hidden.data_ptr(), topk_idx.data_ptr(), weight.data_ptr(), 4 if four else 8, f,
                       w1.q.data_ptr(), w1.scale.data_ptr(), w2.q.data_ptr(), w2.scale.data_ptr(), work.data_ptr(),
                       out.data_ptr(), self._stream(stream))

@@ -64,15 +64,16 @@ def test_the_binding_names_the_scales_types():
     assert (m.BLOCK4, m.LINE4, m.FEW_TOKENS) == (32, 256, 64)
 
 
-def cpu_layer(m, T=8, E=4, k=2, H=64):
+def cpu_layer(m, monkeypatch, T=8, E=4, k=2, H=64):
     """A Layer of host tensors without a handle: every check of its calls passes or refuses, and behind them the library
     refuses the handle."""
     torch = pytest.importorskip("torch")
     layer = object.__new__(m.Layer)
     layer.torch, layer._index, layer.device, layer.handle = torch, -1, torch.device("cpu"), None
     layer._bf16, layer._fp4, layer._e8m0 = torch.bfloat16, torch.float4_e2m1fn_x2, torch.float8_e8m0fnu
-    layer._dims, layer._cap, layer._few_bytes = (T, E, k, H), E, {32: 4096}
+    layer._dims, layer._cap, layer._few = (T, E, k, H), E, {}
     layer._current_stream = lambda i: 0
+    monkeypatch.setattr(m, "moex4_experts_work", lambda h, f: 4096)
     layer._empty = lambda shape, dtype, stream=None: torch.empty(shape, dtype=dtype)
     return torch, layer
 
@@ -83,9 +84,9 @@ def blocks4(m, torch, lead, cols):
                      torch.full(scale, 127, dtype=torch.uint8).view(torch.float8_e8m0fnu), cols)
 
 
-def test_refusals_before_the_library():
+def test_refusals_before_the_library(monkeypatch):
     import load_balance_planning_amd as m
-    torch, layer = cpu_layer(m)
+    torch, layer = cpu_layer(m, monkeypatch)
     T, E, k, H = layer._dims
     b = lambda lead, cols: blocks4(m, torch, lead, cols)
     x, y = torch.zeros(5, 70, dtype=torch.bfloat16), torch.zeros(T, H, dtype=torch.bfloat16)
