@@ -336,7 +336,9 @@ __device__ __forceinline__ v4f multiply(u32x4 q0, u32x4 q1, uint32_t s, const u3
 // of the time (8 tokens, 29 experts of 2 x 2688 x 7168: 132 us then, 107 now, 5.6
 // TB/s of matrices).  Few workgroups at a time, two to a CU, read best: 1024 of them
 // 154 us where 512 took 132.  Short axes lose to what a unit costs beside its steps
-// (64 tokens, 128 experts of 2 x 768 x 2048: two steps a wave, 45 us, 4.4 TB/s).
+// (64 tokens, 128 experts of 2 x 768 x 2048: two steps a wave, 45 us, 4.4 TB/s);
+// the next unit's loads under a unit's last products too, or as many units to every
+// workgroup, were slower (48.5, 48.2).
 constexpr int kChan = 32;
 template <int WB, int WAVES, bool SMALL>
 __global__ __launch_bounds__(64 * WAVES, 2) void experts_up_kernel(Dims d, const uint16_t* __restrict__ hidden,
@@ -794,9 +796,13 @@ template <int WB, bool SMALL, int WAVES>
 hipError_t launch_down(const Dims& d, const Work& k, size_t lds, const int32_t* topk_idx, const float* weight, int32_t f,
                        const uint8_t* w2, const uint8_t* w2s, uint8_t* work, uint16_t* out, hipStream_t st) {
   lds += (size_t)WAVES * (d.T + 1) * kOut * sizeof(float);
+  // what 64 tokens with 32 of 2048 experts take is the most: every call sets the same,
+  // those of other threads too
+  constexpr int kMost = 72 * 1024;
+  if (lds > kMost) return hipErrorInvalidValue;
   if (lds > 32768) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(experts_down_kernel<WB, SMALL, WAVES>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, kMost);
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL((experts_down_kernel<WB, SMALL, WAVES>), dim3((unsigned)(k.chunks * k.shares)), dim3(64 * WAVES),

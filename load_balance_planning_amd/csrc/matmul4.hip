@@ -163,7 +163,9 @@ __global__ __launch_bounds__(256) void matmul4_rows16_kernel(Instances in, const
 // cubed 4.2 PFLOP/s in 4 bits and 2.66 with rows in 8 bits.  What short axes lose is
 // the results of a tile (9 us beside 26 of products for 16 steps of 256 x 128);
 // wave priorities that set the two workgroups of a CU apart, or favour either
-// phase, change nothing (457 us, 454 to 457).
+// phase, change nothing (457 us, 454 to 457), nor do workgroups that begin up to 16
+// us later than others (454 to 464); bands of eight row tiles 455 there, and 499
+// where four take 470 (32768 rows of 32 experts of 7168 x 2688).
 //
 // LDS rows of 128 bytes are placed as the 8-bit products place them.  Of rows of
 // 64 bytes, four share 256 bytes: piece p of row R lies at place 4 (R % 4) + (p ^
