@@ -18,7 +18,8 @@ hipError_t launch_quantize_weights4(const uint16_t* w, int32_t experts, int32_t 
 hipError_t launch_values4(const uint8_t* q, const uint8_t* scale, int32_t matrices, int64_t rows, int32_t cols,
                           uint16_t* x, hipStream_t st);
 
-int64_t matmul4_tiles(const Instances& in, int32_t x_bits, int32_t n, int32_t k);  // workgroups of launch_matmul4's tile kernels (0: it loops)
+// Most tiles of launch_matmul4 (0: its kernel loops over any number).
+int64_t matmul4_tiles(const Instances& in, int32_t x_bits, int32_t n, int32_t k);
 hipError_t launch_matmul4(const Instances& in, int32_t x_bits, const uint8_t* x, const uint8_t* xs, const uint8_t* w,
                           const uint8_t* ws, int32_t n, int32_t k, uint16_t* y, int32_t* status, hipStream_t st);
 

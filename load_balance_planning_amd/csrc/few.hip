@@ -67,7 +67,7 @@ __host__ __device__ inline size_t chosen_lds(const Dims& d) {
 
 template <int THREADS>
 __device__ __forceinline__ Chosen collect_lds(const Dims& d, const int32_t* __restrict__ topk, unsigned char* lds,
-                                          int32_t* status) {
+                                              int32_t* status) {
   const int slots = d.T * d.k, cap = chosen_cap(d), lane = threadIdx.x & 63;
   Chosen c;
   c.mask = reinterpret_cast<uint64_t*>(lds);
@@ -173,8 +173,8 @@ struct ChosenSmall {
   }
 };
 template <int THREADS>
-__device__ __forceinline__ ChosenSmall collect_small(const Dims& d, const int32_t* __restrict__ topk, unsigned char* lds,
-                                                     int32_t* status) {
+__device__ __forceinline__ ChosenSmall collect_small(const Dims& d, const int32_t* __restrict__ topk,
+                                                     unsigned char* lds, int32_t* status) {
   const int slots = d.T * d.k, lane = threadIdx.x & 63;
   unsigned long long* mask = reinterpret_cast<unsigned long long*>(lds);
   ChosenSmall c;
@@ -215,8 +215,8 @@ __device__ __forceinline__ auto collect(const Dims& d, const int32_t* __restrict
 }
 
 // Eight values of a row from column c on; zeros from column `cols` on.
-[[maybe_unused]] __device__ __forceinline__ u32x4 load8_row(const uint16_t* __restrict__ x, int64_t row_at, int c, int cols,
-                                           int64_t total) {
+[[maybe_unused]] __device__ __forceinline__ u32x4 load8_row(const uint16_t* __restrict__ x, int64_t row_at, int c,
+                                                            int cols, int64_t total) {
   u32x4 v = {0u, 0u, 0u, 0u};
   if (c >= cols) return v;
   v = row_at + c + 8 <= total ? (u32x4) * reinterpret_cast<const u32x4_any*>(x + row_at + c)
@@ -341,14 +341,10 @@ __device__ __forceinline__ v4f multiply(u32x4 q0, u32x4 q1, uint32_t s, const u3
 // workgroup, were slower (48.5, 48.2).
 constexpr int kChan = 32;
 template <int WB, int WAVES, bool SMALL>
-__global__ __launch_bounds__(64 * WAVES, 2) void experts_up_kernel(Dims d, const uint16_t* __restrict__ hidden,
-                                                                   const int32_t* __restrict__ topk,
-                                                                   const uint8_t* __restrict__ w,
-                                                                   const uint8_t* __restrict__ ws, int f,
-                                                                   uint8_t* __restrict__ act,
-                                                                   uint8_t* __restrict__ act_scale,
-                                                                   uint32_t* __restrict__ counter, int counters,
-                                                                   int32_t* __restrict__ status) {
+__global__ __launch_bounds__(64 * WAVES, 2) void experts_up_kernel(
+    Dims d, const uint16_t* __restrict__ hidden, const int32_t* __restrict__ topk, const uint8_t* __restrict__ w,
+    const uint8_t* __restrict__ ws, int f, uint8_t* __restrict__ act, uint8_t* __restrict__ act_scale,
+    uint32_t* __restrict__ counter, int counters, int32_t* __restrict__ status) {
 #ifdef __HIP_DEVICE_COMPILE__
   constexpr int kHalves = halves(WB), kChunks = 16 * kHalves;   // chunks of 8 columns of a token's step
   constexpr int kAtOnce = 64 / kChunks, kSets = kCols / kAtOnce;  // tokens of a load, loads of 16 tokens
@@ -391,7 +387,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void experts_up_kernel(Dims d, const
 #pragma unroll
     for (int i = 0; i < kSets; ++i) {
       if (i * kAtOnce >= u.one.count) break;
-      u.from[i] = (uint32_t)(max(ch.slot_of(u.one, i * kAtOnce + lane / kChunks), 0) / d.k) * d.H + 8 * (lane % kChunks);
+      const int s = max(ch.slot_of(u.one, i * kAtOnce + lane / kChunks), 0);
+      u.from[i] = (uint32_t)(s / d.k) * d.H + 8 * (lane % kChunks);
     }
     return u;
   };
@@ -405,9 +402,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void experts_up_kernel(Dims d, const
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int p = 0; p < 2; ++p)
-        o->q[i][p] = __builtin_bit_cast(u32x4, load16b(i < 2 ? u.gate.q : u.up.q, (i & 1 ? u.at_16 : u.at) + 64 * p, b * kBlk));
+        o->q[i][p] = __builtin_bit_cast(
+            u32x4, load16b(i < 2 ? u.gate.q : u.up.q, (i & 1 ? u.at_16 : u.at) + 64 * p, b * kBlk));
     if constexpr (WB == 4)
-      o->s = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(u.gate.s, (int)u.s_at, b * (int)u.gate.s_step, 0));
+      o->s = __builtin_bit_cast(
+          u32x2, __builtin_amdgcn_raw_buffer_load_b64(u.gate.s, (int)u.s_at, b * (int)u.gate.s_step, 0));
     else
       o->s[0] = __builtin_amdgcn_raw_buffer_load_b8(u.gate.s, (int)u.s_at, b, 0);
     if (b >= whole) return;
@@ -483,7 +482,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void experts_up_kernel(Dims d, const
     }
     const auto& parts = part_s[turn % kTurns];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<v4f*>(&part_s[turn % kTurns][wave][r * kPartRow + 16 * i + 4 * g]) = acc[i];
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<v4f*>(&part_s[turn % kTurns][wave][r * kPartRow + 16 * i + 4 * g]) = acc[i];
     // the next unit's first step comes in under this one's sums
     const auto one = u.one;
     const int chunk = u.chunk, c0 = chunk * kChan;
@@ -550,15 +550,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void experts_up_kernel(Dims d, const
 // step's loads ahead brought nothing (26.7).
 constexpr int kOut = 32, kMaxShares = 8;
 template <int WB, bool SMALL, int kDownWaves>
-__global__ __launch_bounds__(64 * kDownWaves, kDownWaves == 16 ? 4 : 2) void experts_down_kernel(Dims d, const int32_t* __restrict__ topk,
-                                                                       const float* __restrict__ weight,
-                                                                       const uint8_t* __restrict__ w,
-                                                                       const uint8_t* __restrict__ ws, int f,
-                                                                       const uint8_t* __restrict__ act,
-                                                                       const uint8_t* __restrict__ act_scale,
-                                                                       int width, int chunks, int shares, float* partial,
-                                                                       uint32_t* counter,
-                                                                       uint16_t* __restrict__ out) {
+__global__ __launch_bounds__(64 * kDownWaves, kDownWaves == 16 ? 4 : 2) void experts_down_kernel(
+    Dims d, const int32_t* __restrict__ topk, const float* __restrict__ weight, const uint8_t* __restrict__ w,
+    const uint8_t* __restrict__ ws, int f, const uint8_t* __restrict__ act, const uint8_t* __restrict__ act_scale,
+    int width, int chunks, int shares, float* partial, uint32_t* counter, uint16_t* __restrict__ out) {
 #ifdef __HIP_DEVICE_COMPILE__
   constexpr int kDownThreads = 64 * kDownWaves;
   constexpr int kHalves = halves(WB), kPieces = 8 * kHalves;      // 16-byte pieces of a slot's step
@@ -692,8 +687,8 @@ __global__ __launch_bounds__(64 * kDownWaves, kDownWaves == 16 ? 4 : 2) void exp
           const v8i qv = WB == 4 ? v8i{q0[0], q0[1], q0[2], q0[3], 0, 0, 0, 0}
                                  : v8i{q0[0], q0[1], q0[2], q0[3], q1[0], q1[1], q1[2], q1[3]};
           const uint32_t s = scale_s[wave][kHalves * (16 * i + r) + h] >> (WB == 4 ? 8 * g : 0);
-          acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(qv, xv, acc[i], WB == 4 ? kFp4 : kFp8, kFp8, 0, (int)s,
-                                                                    0, (int)sx);
+          acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(qv, xv, acc[i], WB == 4 ? kFp4 : kFp8, kFp8, 0,
+                                                                    (int)s, 0, (int)sx);
         }
       }
       if (last || item + 1 == to) {
@@ -731,7 +726,8 @@ __global__ __launch_bounds__(64 * kDownWaves, kDownWaves == 16 ? 4 : 2) void exp
   // workgroups took 27 us longer.)
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
-  if (threadIdx.x == 0) arrived = __hip_atomic_fetch_add(counter + chunk, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (threadIdx.x == 0)
+    arrived = __hip_atomic_fetch_add(counter + chunk, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
   if (arrived != (uint32_t)shares - 1u) return;
   const pair_* every = reinterpret_cast<const pair_*>(partial) + (int64_t)chunk * shares * (per_wave / 2);
@@ -752,7 +748,7 @@ __global__ __launch_bounds__(64 * kDownWaves, kDownWaves == 16 ? 4 : 2) void exp
 }
 
 // Where a call's memory goes: activations [T * k][fp], their scales [T * k][fp /
-// 32], a counter per 32 channels, the shares' sums.
+// 32], a counter per piece of channels, the shares' sums.
 struct Work {
   int fp, waves, width, chunks, shares;
   int64_t scale, counter, partial, bytes;
@@ -772,7 +768,7 @@ Work work_of(const Dims& d, int f) {
   // the CUs (7168 channels: 256 workgroups of 28 and not 224 of 32), and where there
   // is nothing to share so narrow that all CUs have some (a token with 8 experts of 768
   // x 2048: 7.5 us in 64 workgroups, 6.0 in 256).  Shares of wide pieces are better
-  // than narrow ones (8 tokens, 32 experts of 2048 channels in 8 bits: 23 us, 33).
+  // than narrow ones (16 tokens, 8 each of 128 experts, in 8 bits: 23 us and 33).
   k.width = kOut;
   if (d.H > 128 * kOut || most < 2) {
     const int rounds = (d.H + 256 * kOut - 1) / (256 * kOut);
@@ -793,8 +789,9 @@ Work work_of(const Dims& d, int f) {
 }
 
 template <int WB, bool SMALL, int WAVES>
-hipError_t launch_down(const Dims& d, const Work& k, size_t lds, const int32_t* topk_idx, const float* weight, int32_t f,
-                       const uint8_t* w2, const uint8_t* w2s, uint8_t* work, uint16_t* out, hipStream_t st) {
+hipError_t launch_down(const Dims& d, const Work& k, size_t lds, const int32_t* topk_idx, const float* weight,
+                       int32_t f, const uint8_t* w2, const uint8_t* w2s, uint8_t* work, uint16_t* out,
+                       hipStream_t st) {
   lds += (size_t)WAVES * (d.T + 1) * kOut * sizeof(float);
   // what 64 tokens with 32 of 2048 experts take is the most: every call sets the same,
   // those of other threads too

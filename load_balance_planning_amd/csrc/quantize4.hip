@@ -156,7 +156,8 @@ __global__ __launch_bounds__(kThreads) void quantize4_weights_kernel(const uint1
   if (threadIdx.x < kBlk) {
     const int r = bn * kBlk + threadIdx.x;
     if (r < n)
-      *reinterpret_cast<uint32_t*>(scale + (((int64_t)e * nbk + bk / 2) * n + r) * 8 + 4 * (bk & 1)) = s_row[threadIdx.x];
+      *reinterpret_cast<uint32_t*>(scale + (((int64_t)e * nbk + bk / 2) * n + r) * 8 + 4 * (bk & 1)) =
+          s_row[threadIdx.x];
   } else if (qt) {
     const int i = threadIdx.x - kBlk, r = bk * kBlk + i;
     if (r < k)
@@ -247,8 +248,8 @@ hipError_t launch_quantize_weights4(const uint16_t* w, int32_t experts, int32_t 
   const int pn = (int)(padded_cols4(n) / kBlk), pk = (int)(padded_cols4(k) / kBlk);
   const int64_t pieces = (int64_t)experts * pn * pk;
   if (pieces == 0) return hipSuccess;
-  hipLaunchKernelGGL(quantize4_weights_kernel, dim3((unsigned)((pieces + 7) / 8 * 8)), dim3(kThreads), 0, st, w, experts, n, k, pn, pk,
-                     q, scale, qt, scale_t);
+  hipLaunchKernelGGL(quantize4_weights_kernel, dim3((unsigned)((pieces + 7) / 8 * 8)), dim3(kThreads), 0, st, w,
+                     experts, n, k, pn, pk, q, scale, qt, scale_t);
   return hipGetLastError();
 }
 
