@@ -851,9 +851,10 @@ class Layer:
         return grad_rows, grad_weight
 
     def _check_blocks4(self, b: Blocks4, lead):
-        q, scale = Blocks4.shapes(lead, b.cols)
-        self._check_tensor(b.q, q, self._fp4)
-        self._check_tensor(b.scale, scale, self._e8m0)
+        shapes, index = Blocks4.shapes(lead, b.cols), self._index
+        for t, shape, dtype in ((b.q, shapes[0], self._fp4), (b.scale, shapes[1], self._e8m0)):
+            if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+                self._check_tensor(t, shape, dtype)
 
     def _check_16bit_here(self, t, name):
         """_check_16bit of a tensor whose shape is the call's own."""
@@ -869,7 +870,8 @@ class Layer:
         q, scale = Blocks4.shapes(lead, cols)
         if stream is None:
             empty, device = self.torch.empty, self.device
-            return Blocks4(empty(q, dtype=self._fp4, device=device), empty(scale, dtype=self._e8m0, device=device), cols)
+            return Blocks4(empty(*q, dtype=self._fp4, device=device), empty(*scale, dtype=self._e8m0, device=device),
+                           cols)
         return Blocks4(self._empty(q, self._fp4, stream), self._empty(scale, self._e8m0, stream), cols)
 
     def quantize4(self, x, stream=None, out=None) -> Blocks4:
@@ -889,7 +891,7 @@ class Layer:
         if w.dim() != 3:
             raise ValueError("w must be [experts][n][k]")
         E, n, k = w.shape
-        self._check_16bit(w, (E, n, k), "w")
+        self._check_16bit_here(w, "w")
         out, out_t = (None, None) if out is None else out if transposed else (out, None)
         out = self._result_blocks4(out, stream, (E, n), k)
         out_t = self._result_blocks4(out_t, stream, (E, k), n) if transposed else Blocks4(None, None, n)
@@ -899,12 +901,13 @@ class Layer:
 
     def values4(self, b: Blocks4, stream=None, out=None):
         """The values of Blocks4 of rows or matrices, bf16 [..., cols] (moex4_values)."""
-        lead = tuple(b.q.shape[:-1])
+        torch, lead = self.torch, tuple(b.q.shape[:-1])
         if len(lead) not in (1, 2):
             raise ValueError("expected Blocks4 of rows or of matrices")
         self._check_blocks4(b, lead)
         if out is None:
-            out = self._empty((*lead, b.cols), self._bf16, stream)
+            out = torch.empty(*lead, b.cols, dtype=self._bf16, device=self.device) if stream is None else \
+                self._empty((*lead, b.cols), self._bf16, stream)
         else:
             self._check_16bit(out, (*lead, b.cols), "out")
         moex4_values(self.handle, b.q.data_ptr(), b.scale.data_ptr(), lead[0] if len(lead) == 2 else 1, lead[-1], b.cols,
@@ -916,9 +919,9 @@ class Layer:
         if y.dim() != 2 or y.shape[1] % 2:
             raise ValueError("y must be [rows][2 f]")
         rows, f = y.shape[0], y.shape[1] // 2
-        self._check_16bit(y, (rows, 2 * f), "y")
+        self._check_16bit_here(y, "y")
         out = self._result_blocks4(out, stream, (rows,), f)
-        moex4_swiglu(self.handle, _addr(y), rows, f, _addr(out.q), _addr(out.scale), self._stream(stream))
+        moex4_swiglu(self.handle, y.data_ptr(), rows, f, out.q.data_ptr(), out.scale.data_ptr(), self._stream(stream))
         return out
 
     def matmul4(self, x, w: Blocks4, plan=None, inst_offset=None, out=None, stream=None):
