@@ -86,7 +86,7 @@ int moex4_values(moe_plan_t h, const uint8_t* q, const uint8_t* scale, int32_t m
 
 /*
  * y bf16 [rows][2 f]: gate columns, then up columns.  moex_swiglu's value in
- * fp32, quantized as a row of f columns.  rows and f as rows and cols of
+ * fp32 (within 2^-20 of it), quantized as a row of f columns.  rows and f as rows and cols of
  * moex4_quantize.
  */
 int moex4_swiglu(moe_plan_t h, const uint16_t* y, int64_t rows, int32_t f, uint8_t* q, uint8_t* scale, void* stream);

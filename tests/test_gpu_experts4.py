@@ -159,6 +159,30 @@ def test_gated_activation(mp, small, rows, f):
     assert (refs4.codes(b)[:, f:] == 0).all()
 
 
+def test_gated_activation_far_out(mp, small):
+    """Gates to the ends of their range, a block each.  Below -88.72 the sigmoid is 0 (its exponential leaves fp32); the
+    bounds are those above."""
+    pairs = [(-88.5, 60), (-88.0, 60), (-87.0, 120), (-60.0, 3), (-20.25, 0), (-1e-3, 0), (-1e-30, 30), (0.0, 0), (1e-30, 0),
+             (5.0, 100), (20.0, 0), (88.0, -90), (88.5, 0), (100.0, 0), (128.0, 0), (200.0, 0), (1e4, 0), (3e38, -1),
+             (-89.0, 0), (-100.0, 120), (-200.0, 0), (-1e10, 0), (-3.3e38, 0)]
+    g = torch.tensor([p[0] for p in pairs]).to(BF)[:, None].expand(-1, 32)
+    u = (2.0 ** torch.tensor([float(p[1]) for p in pairs])).to(BF)[:, None].expand(-1, 32)
+    y = torch.cat([g, u], 1).contiguous()
+    b = small.swiglu4(y.to(small.device))
+    want = torch.where(g.double() < -88.72, 0.0, refs.swiglu(y.double()))
+    got, s = refs4.values(b), refs4.scales(b)
+    each = refs4.spread(s, 32, 32)
+    ratio = want.abs() / each
+    half = torch.where(ratio < 2, 0.25, torch.where(ratio < 4, 0.5, 1.0)) * each
+    assert ((got - want).abs() <= half * (1 + 2.0 ** -10) + 2.0 ** -18 * want.abs()).all()
+    assert ((want == 0) | (ratio > 2.99)).all() and (got[want == 0] == 0).all()
+    odd = y.clone()
+    inf = float("inf")
+    odd[0, 3], odd[1, 5], odd[2, 40], odd[3, 0], odd[4, 33] = inf, -inf, float("nan"), float("nan"), -inf
+    marked = (u8(small.swiglu4(odd.to(small.device)).scale)[0, :, 0] == 255).nonzero().flatten().tolist()
+    assert marked == [0, 1, 2, 3, 4]
+
+
 def test_unaligned_rows(mp, small):
     """bf16 inputs and results that start 2 bytes past a 16-byte boundary."""
     x = normal(4, 20, 264)
