@@ -18,6 +18,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
+from functools import cached_property
 
 from . import build as _build
 
@@ -544,7 +545,7 @@ class Layer:
         self._index = self.device.index
         self._dims = (cfg.T, cfg.E, cfg.k, cfg.H)  # plain integers: a structure's fields cost more to read
         self._cap = cfg.E + cfg.replica_budget
-        self._bf16, self._fp4, self._e8m0 = torch.bfloat16, torch.float4_e2m1fn_x2, torch.float8_e8m0fnu
+        self._bf16 = torch.bfloat16
         self._few = {}  # experts(): the bytes of its memory and its arguments' shapes, by the experts' width and bits
         self._current_stream = _current_stream(torch)
         self.sizes = moe_plan_query(cfg)
@@ -568,6 +569,16 @@ class Layer:
         self._disp_s = self.dispatch_out.struct()
         self.place_out = None
         self.dedup_out = None
+
+    # What only the calls of 4-bit blocks need of torch, looked up by the first of them: planning and the calls of bf16
+    # rows run with a torch that has no such types.
+    @cached_property
+    def _fp4(self):
+        return self.torch.float4_e2m1fn_x2
+
+    @cached_property
+    def _e8m0(self):
+        return self.torch.float8_e8m0fnu
 
     def _stream(self, stream=None) -> int:
         if stream is None:
