@@ -112,8 +112,9 @@ int moex4_matmul(moe_plan_t h, const moe_plan_out* plan, const int32_t* inst_off
  * hidden bf16 [T][H]; topk_idx int32 [T][k]; weight float [T][k] (moex_gate's, or
  * any); w1 matrices [E][2 f][H], gate rows then up rows, w2 [E][H][f], w_bits 4:
  * in blocks of 32 as above, w_bits 8: moex_quantize_weights'; out bf16 [T][H],
- * fully overwritten; it may not overlap hidden or work.  Q rounds to e4m3 with
- * one E8M0 scale per 1 x 32, by moex_quantize's rules; all else is fp32, the
+ * fully overwritten; neither it nor work may overlap anything that the call
+ * reads, or the other.  Q rounds to e4m3 with one E8M0 scale per 1 x 32, by
+ * moex_quantize's rules; all else is fp32, the
  * sums in a fixed order.  The first product takes values as bf16 (as
  * moex4_values gives them; e4m3 * scale), so that its sums lose nothing; the
  * second cuts products off as moex_matmul does.

@@ -688,10 +688,10 @@ class Layer:
 
     @staticmethod
     def _check_apart(out, t):
-        """Rows that a kernel still reads may not be the ones it writes (contiguous tensors)."""
+        """Memory that a kernel still reads may not be what it writes (contiguous tensors)."""
         a, b = out.data_ptr(), t.data_ptr()
         if a < b + t.numel() * t.element_size() and b < a + out.numel() * out.element_size():
-            raise ValueError("out overlaps the rows that the call reads")
+            raise ValueError("out overlaps memory that the call reads")
 
     def _result(self, out, shape, dtype, stream):
         """`out`, checked, or memory of the call's own."""
@@ -996,7 +996,8 @@ class Layer:
             out = torch.empty_like(hidden) if stream is None else self._empty((T, H), hidden.dtype, stream)
         else:
             self._check_16bit(out, (T, H), "out")
-            self._check_apart(out, hidden)
+            for t in (hidden, topk_idx, weight, w1.q, w1.scale, w2.q, w2.scale):
+                self._check_apart(out, t)
         work = torch.empty(nbytes, dtype=torch.uint8, device=self.device) if stream is None else \
             self._empty((nbytes,), torch.uint8, stream)
         moex4_experts(self.handle, hidden.data_ptr(), topk_idx.data_ptr(), weight.data_ptr(), 4 if four else 8, f,

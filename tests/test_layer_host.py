@@ -31,3 +31,41 @@ def test_a_layer_needs_no_narrow_types_of_torch(monkeypatch):
             x = torch.zeros(5, 70, dtype=torch.bfloat16)
             with pytest.raises(AttributeError, match=name):
                 layer.quantize4(x)
+
+
+def matrices4(m, E, n, k):
+    q, scale = m.Blocks4.shapes((E, n), k)
+    return m.Blocks4(torch.zeros(q, dtype=torch.uint8).view(torch.float4_e2m1fn_x2),
+                     torch.full(scale, 127, dtype=torch.uint8).view(torch.float8_e8m0fnu), k)
+
+
+def test_few_tokens_results_lie_over_nothing_that_is_read(monkeypatch):
+    """`out` in the memory of any argument of experts(), at its beginning and at its end, is refused; beside them all
+    it passes to the library (which refuses the handle)."""
+    import load_balance_planning_amd as m
+    T, E, k, H, f = 4, 8, 8, 64, 32
+    layer = made_on_host(m, monkeypatch, T, E, k, H)
+    monkeypatch.setattr(m, "moex4_experts_work", lambda h, f: 4096)
+    layer._few = {}
+    size = T * H * 2
+    # every argument in one buffer, each with room for a result before and behind it
+    w1, w2 = matrices4(m, E, 2 * f, H), matrices4(m, E, H, f)
+    args = dict(hidden=torch.zeros(T, H, dtype=torch.bfloat16), topk_idx=torch.zeros(T, k, dtype=torch.int32),
+                weight=torch.zeros(T, k), q1=w1.q, s1=w1.scale, q2=w2.q, s2=w2.scale)
+    buf = torch.zeros(len(args) * (size + (1 << 16)), dtype=torch.uint8)
+    at, placed, ends = 0, {}, {}
+    for name, t in args.items():
+        at += size
+        n = t.numel() * t.element_size()
+        placed[name] = buf[at:at + n].view(t.dtype).view(t.shape)
+        ends[name] = (at, at + n)
+        at += n + 512
+    call = lambda out: layer.experts(placed["hidden"], placed["weight"], m.Blocks4(placed["q1"], placed["s1"], H),
+                                     m.Blocks4(placed["q2"], placed["s2"], f), topk_idx=placed["topk_idx"], out=out)
+    result = lambda begin: buf[begin:begin + size].view(torch.bfloat16).view(T, H)
+    for name, (begin, end) in ends.items():
+        for over in (begin - size + 2, begin, end - 2):
+            with pytest.raises(ValueError, match="overlaps"):
+                call(result(over))
+        with pytest.raises(m.MoePlanError):
+            call(result(begin - size))
