@@ -687,11 +687,21 @@ class Layer:
             return self.torch.empty(*shape, dtype=dtype, device=self.device)
 
     @staticmethod
+    def _overlap(t, u) -> bool:
+        """Whether two contiguous tensors share memory."""
+        a, b = t.data_ptr(), u.data_ptr()
+        return a < b + u.numel() * u.element_size() and b < a + t.numel() * t.element_size()
+
+    @staticmethod
     def _check_apart(out, t):
-        """Memory that a kernel still reads may not be what it writes (contiguous tensors)."""
-        a, b = out.data_ptr(), t.data_ptr()
-        if a < b + t.numel() * t.element_size() and b < a + out.numel() * out.element_size():
+        """Memory that a kernel still reads may not be what it writes."""
+        if Layer._overlap(out, t):
             raise ValueError("out overlaps memory that the call reads")
+
+    def _check_pair(self, a, b):
+        """The two layouts that one call writes, each in memory of its own."""
+        if self._overlap(a.q, b.q) or self._overlap(a.scale, b.scale):
+            raise ValueError("the two results of out overlap")
 
     def _result(self, out, shape, dtype, stream):
         """`out`, checked, or memory of the call's own."""
@@ -743,7 +753,10 @@ class Layer:
         blocks = lambda c: -(-c // BLOCK)
         out, out_t = (None, None) if out is None else out if transposed else (out, None)
         out = self._result_blocks(out, stream, (E, n), k, (E, blocks(n)))
+        given = out_t is not None
         out_t = self._result_blocks(out_t, stream, (E, k), n, (E, blocks(k))) if transposed else Blocks(None, None, n)
+        if given:
+            self._check_pair(out, out_t)
         moex_quantize_weights(self.handle, _addr(w), E, n, k, _addr(out.q), _addr(out.scale), _addr(out_t.q),
                               _addr(out_t.scale), self._stream(stream))
         return (out, out_t) if transposed else out
@@ -905,7 +918,10 @@ class Layer:
         self._check_16bit_here(w, "w")
         out, out_t = (None, None) if out is None else out if transposed else (out, None)
         out = self._result_blocks4(out, stream, (E, n), k)
+        given = out_t is not None
         out_t = self._result_blocks4(out_t, stream, (E, k), n) if transposed else Blocks4(None, None, n)
+        if given:
+            self._check_pair(out, out_t)
         moex4_quantize_weights(self.handle, _addr(w), E, n, k, _addr(out.q), _addr(out.scale), _addr(out_t.q),
                                _addr(out_t.scale), self._stream(stream))
         return (out, out_t) if transposed else out

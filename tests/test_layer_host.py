@@ -69,3 +69,23 @@ def test_few_tokens_results_lie_over_nothing_that_is_read(monkeypatch):
                 call(result(over))
         with pytest.raises(m.MoePlanError):
             call(result(begin - size))
+
+
+@pytest.mark.parametrize("four", [True, False])
+def test_both_layouts_into_the_same_memory_are_refused(monkeypatch, four):
+    """Square matrices, whose two layouts have the same shapes."""
+    import load_balance_planning_amd as m
+    layer = made_on_host(m, monkeypatch)
+    w = torch.zeros(2, 256, 256, dtype=torch.bfloat16)
+    if four:
+        quant, one = layer.quantize_weights4, lambda: matrices4(m, 2, 256, 256)
+    else:
+        quant = layer.quantize_weights
+        one = lambda: m.Blocks(torch.zeros(2, 256, 256, dtype=torch.uint8).view(torch.float8_e4m3fn),
+                               torch.zeros(2, 2, 4, dtype=torch.uint8).view(torch.float8_e8m0fnu), 256)
+    a, b = one(), one()
+    for pair in ((a, a), (a, type(a)(b.q, a.scale, 256)), (a, type(a)(a.q, b.scale, 256))):
+        with pytest.raises(ValueError, match="overlap"):
+            quant(w, transposed=True, out=pair)
+    with pytest.raises(m.MoePlanError):  # past every check: the library refuses the handle
+        quant(w, transposed=True, out=(a, b))
