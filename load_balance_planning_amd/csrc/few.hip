@@ -21,13 +21,8 @@
 namespace moe {
 namespace {
 
-typedef int v4i __attribute__((ext_vector_type(4)));
-typedef int v8i __attribute__((ext_vector_type(8)));
-typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float float2_ __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
-[[maybe_unused]] constexpr int kFp8 = 0, kFp4 = 4;  // the instruction's format codes
 
 // What there is to multiply: entries of an expert and up to 16 of its slots t * k +
 // j (tokens ascending; one operand of the instruction).  In dynamic LDS: masks u64

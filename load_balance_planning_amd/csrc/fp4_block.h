@@ -9,6 +9,9 @@ namespace {
 constexpr int kBlk4 = 32;     // columns under one scale
 constexpr int kCols4 = 256;   // columns of a 128-byte line, whose 8 scales lie together
 
+// The scaled matrix instruction's codes of its operands' formats.
+[[maybe_unused]] constexpr int kFp8 = 0, kFp4 = 4;
+
 // Scale byte of a block whose largest magnitude is amax: the smallest 2^(s - 127)
 // with amax <= 6 * 2^(s - 127) -- 6 is 1.5 * 2^2.  127 and 255 as scale_byte.
 __device__ __forceinline__ uint32_t scale_byte4(uint32_t amax_bits) {

@@ -12,6 +12,10 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // and the memory path takes 16 bytes from there in one instruction.
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+// Operands and results of the matrix instructions.
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ float bf16_low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }

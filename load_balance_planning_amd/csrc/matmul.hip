@@ -28,10 +28,6 @@
 namespace moe {
 namespace {
 
-typedef int v4i __attribute__((ext_vector_type(4)));
-typedef int v8i __attribute__((ext_vector_type(8)));
-typedef float v4f __attribute__((ext_vector_type(4)));
-
 // 32 of a row's 128 bytes: the 16 of lane group g in each half.  (Both
 // operands use the same order, so any order of the block does.)
 __device__ __forceinline__ v8i load_block(const uint8_t* __restrict__ row, int g) {
@@ -127,28 +123,9 @@ __global__ __launch_bounds__(256) void matmul_rows16_kernel(Instances in, const 
 // the products themselves take (2048 cycles), 128 x 128 tiles of four waves read
 // 128 KB.
 //
-// LDS rows are 128 bytes, eight 16-byte pieces.  A direct load writes its
-// lanes' pieces one after the other, so the placement is chosen on the memory
-// side: the piece of linear place L belongs to row pair L / 16, and within the
-// pair's 256 bytes piece p of row R lies at place (8 (R % 2) + p) ^ s(R).  The
-// 16 lanes of a read then find their pieces in 16 different places of 256
-// bytes: s takes three bits in which the rows of 16 lanes differ and which do
-// not change from one instruction tile to the next (one address serves all
-// reads of a step, the rest are immediate offsets) -- bits 1, 2, 3 of R for
-// the rows operand, and 1, 2, 4 for the channels.
-//
 // A lane's 16 results are matrix rows 8a + 4h + j, h its half of the wave, of
 // one column.  Matrix row 8a + 4h + j stands for channel 16h + 4a + j, so they
 // are 16 consecutive channels of one row of y.
-template <bool CHANNELS>
-__device__ __forceinline__ int piece_swizzle(int pair) {  // pair = R / 2
-  return CHANNELS ? (pair & 3) | ((pair >> 1) & 4) : pair & 7;
-}
-template <bool CHANNELS>
-__device__ __forceinline__ int piece_at(int row, int p) {
-  return (row >> 1) * 256 + ((((row & 1) << 3) | p) ^ piece_swizzle<CHANNELS>(row >> 1)) * 16;
-}
-
 template <int BC, int BT, int WC, int WT>
 struct TileShape {
   static constexpr int kWaves = WC * WT, kThreads = 64 * kWaves;

@@ -21,18 +21,12 @@
 namespace moe {
 namespace {
 
-typedef int v4i __attribute__((ext_vector_type(4)));
-typedef int v8i __attribute__((ext_vector_type(8)));
-typedef float v4f __attribute__((ext_vector_type(4)));
-
 // The instruction's operand of 16 bytes of 4-bit values; it reads no more.
 __device__ __forceinline__ v8i operand4(v4i v) { return v8i{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
 __device__ __forceinline__ v8i operand8(v4i lo, v4i hi) {
   return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 }
 __device__ __forceinline__ v4i load16b(const uint8_t* p) { return *reinterpret_cast<const v4i*>(p); }
-
-constexpr int kFp8 = 0, kFp4 = 4;  // the instruction's format codes
 
 // 16 rows x 64 channels per workgroup; its four waves take every fourth line of
 // the long axis each (256 values: two instructions), straight from memory to
@@ -167,19 +161,11 @@ __global__ __launch_bounds__(256) void matmul4_rows16_kernel(Instances in, const
 // us later than others (454 to 464); bands of eight row tiles 455 there, and 499
 // where four take 470 (32768 rows of 32 experts of 7168 x 2688).
 //
-// LDS rows of 128 bytes are placed as the 8-bit products place them.  Of rows of
+// LDS rows of 128 bytes are placed as piece_at says.  Of rows of
 // 64 bytes, four share 256 bytes: piece p of row R lies at place 4 (R % 4) + (p ^
 // s(R)), s two bits in which the rows of 16 lanes differ beside R % 4 and that are
 // the same in every instruction tile: bits 2 and 3 of R for the rows operand, 2
 // and 4 for the channels.
-template <bool CHANNELS>
-__device__ __forceinline__ int piece_swizzle(int pair) {  // pair = R / 2
-  return CHANNELS ? (pair & 3) | ((pair >> 1) & 4) : pair & 7;
-}
-template <bool CHANNELS>
-__device__ __forceinline__ int piece_at(int row, int p) {
-  return (row >> 1) * 256 + ((((row & 1) << 3) | p) ^ piece_swizzle<CHANNELS>(row >> 1)) * 16;
-}
 template <bool CHANNELS>
 __device__ __forceinline__ int quad_swizzle(int quad) {  // quad = R / 4
   return CHANNELS ? (quad & 1) | ((quad >> 1) & 2) : quad & 3;

@@ -1,11 +1,29 @@
-// What the experts' products in tiles share: the barrier that waits for loads into
-// LDS, and the row tiles of a plan's instances.
+// What the experts' products in tiles share: where rows lie in LDS, the barrier that
+// waits for loads into it, and the row tiles of a plan's instances.
 #pragma once
 
 #include "instances.h"
 
 namespace moe {
 namespace {
+
+// LDS rows are 128 bytes, eight 16-byte pieces.  A direct load writes its
+// lanes' pieces one after the other, so the placement is chosen on the memory
+// side: the piece of linear place L belongs to row pair L / 16, and within the
+// pair's 256 bytes piece p of row R lies at place (8 (R % 2) + p) ^ s(R).  The
+// 16 lanes of a read then find their pieces in 16 different places of 256
+// bytes: s takes three bits in which the rows of 16 lanes differ and which do
+// not change from one instruction tile to the next (one address serves all
+// reads of a step, the rest are immediate offsets) -- bits 1, 2, 3 of R for
+// the rows operand, and 1, 2, 4 for the channels.
+template <bool CHANNELS>
+__device__ __forceinline__ int piece_swizzle(int pair) {  // pair = R / 2
+  return CHANNELS ? (pair & 3) | ((pair >> 1) & 4) : pair & 7;
+}
+template <bool CHANNELS>
+__device__ __forceinline__ int piece_at(int row, int p) {
+  return (row >> 1) * 256 + ((((row & 1) << 3) | p) ^ piece_swizzle<CHANNELS>(row >> 1)) * 16;
+}
 
 // Barrier after which every wave sees every wave's loads into LDS, and has its
 // own reads.  A barrier alone does not wait for the loads: to the compiler they
