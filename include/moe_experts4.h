@@ -114,10 +114,10 @@ int moex4_matmul(moe_plan_t h, const moe_plan_out* plan, const int32_t* inst_off
  * in blocks of 32 as above, w_bits 8: moex_quantize_weights'; out bf16 [T][H],
  * fully overwritten; neither it nor work may overlap anything that the call
  * reads, or the other.  Q rounds to e4m3 with one E8M0 scale per 1 x 32, by
- * moex_quantize's rules; all else is fp32, the
- * sums in a fixed order.  The first product takes values as bf16 (as
- * moex4_values gives them; e4m3 * scale), so that its sums lose nothing; the
- * second cuts products off as moex_matmul does.
+ * moex_quantize's rules; all else is fp32, the sums in a fixed order.  The first
+ * product takes values as bf16 (as moex4_values gives them; e4m3 * scale), so that
+ * its sums lose nothing but what bf16 has not: steps below 2^-133, and values from
+ * 2^128 on, which are infinite; the second cuts products off as moex_matmul does.
  * work: memory for one call at a time, 16-byte aligned, as many bytes as
  * moex4_experts_work says for the handle and f (host only).  After the call it
  * begins with the activations a, uint8 [T*k][fp], and their scales, uint8

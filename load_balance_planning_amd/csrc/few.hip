@@ -329,11 +329,11 @@ __device__ __forceinline__ v4f multiply(u32x4 q0, u32x4 q1, uint32_t s, const u3
 // rows (rounded) pass through LDS, the wave's own part of it, to the lanes that
 // multiply.  Loaded by those lanes each for itself, scales took 8 % and rows 14 %
 // of the time (8 tokens, 29 experts of 2 x 2688 x 7168: 132 us then, 107 now, 5.6
-// TB/s of matrices).  Few workgroups at a time, two to a CU, read best: 1024 of them
-// 154 us where 512 took 132.  Short axes lose to what a unit costs beside its steps
-// (64 tokens, 128 experts of 2 x 768 x 2048: two steps a wave, 45 us, 4.4 TB/s);
-// the next unit's loads under a unit's last products too, or as many units to every
-// workgroup, were slower (48.5, 48.2).
+// TB/s of matrices).  Workgroups that are all resident, two to a CU, choose experts
+// once: 1024 of them take 48.6 us where 512 take 44.9 (64 tokens, 128 experts of 2 x
+// 768 x 2048, 4.4 TB/s; with long axes 106 and 107).  Such short axes lose to what a
+// unit costs beside its steps, two a wave; the next unit's loads under a unit's last
+// products too, or as many units to every workgroup, were slower (48.5, 48.2).
 constexpr int kChan = 32;
 template <int WB, int WAVES, bool SMALL>
 __global__ __launch_bounds__(64 * WAVES, 2) void experts_up_kernel(

@@ -152,14 +152,16 @@ __global__ __launch_bounds__(256) void matmul4_rows16_kernel(Instances in, const
 // scales of two steps come to LDS together; those of 8-bit rows, one byte a step,
 // go to registers four steps at a time.
 //
-// Bound by the matrix unit at the card's power limit: half busy at 1.8 GHz (131072
-// rows of 128 experts in 8 bits, 65536 rows of 32 wide ones in 4), one dense 8192
-// cubed 4.2 PFLOP/s in 4 bits and 2.66 with rows in 8 bits.  What short axes lose is
-// the results of a tile (9 us beside 26 of products for 16 steps of 256 x 128);
-// wave priorities that set the two workgroups of a CU apart, or favour either
-// phase, change nothing (457 us, 454 to 457), nor do workgroups that begin up to 16
-// us later than others (454 to 464); bands of eight row tiles 455 there, and 499
-// where four take 470 (32768 rows of 32 experts of 7168 x 2688).
+// One dense 8192 cubed reaches 4.2 PFLOP/s in 4 bits and 2.66 with rows in 8 bits.
+// Short axes leave the matrix unit idle half of the time: 131072 rows of 128
+// experts of 1536 x 2048 in 8 bits take 458 us (1.8 PFLOP/s), and 362 in a timing
+// copy that does not store.  A tile's results (9 us beside 26 of products for 16
+// steps of 256 x 128) lie under the other workgroup's products only: the wait at
+// the next tile's head is for every memory operation, the stores too, and its
+// second block goes where the results still pass.  Not the reason: wave priorities
+// that set the two workgroups of a CU apart, or favour either phase (454 to 457),
+// workgroups that begin up to 16 us later than others (454 to 464), bands of eight
+// row tiles (455; 499 where four take 470, 32768 rows of 32 experts of 7168 x 2688).
 //
 // LDS rows of 128 bytes are placed as piece_at says.  Of rows of
 // 64 bytes, four share 256 bytes: piece p of row R lies at place 4 (R % 4) + (p ^
@@ -556,27 +558,42 @@ namespace {
 constexpr int kCapWide = 1536;  // instances whose tile counts fit the LDS beside 256 x 256 tiles
 
 // The tile of a product, by the mean of rows per expert (the loads themselves are
-// on the device).
+// on the device).  us in a graph of such launches, in turn with other matrices
+// where there are few rows (they are not in the caches then).  "*": what the rule
+// takes.
 //
 // Few rows: bound by the matrices, which the streaming kernel reads straight into
-// registers.  us in it and in tiles, the matrices not in the caches:
-//   experts     n     k  rows an expert   4 bits        8 bits
-//       128  1536  2048               4    48.0  51.2    43.1  61.4
-//       128  1536  2048              12    58.7  53.2    55.4  57.9
-//        32  5376  7168               8   146.6 137.2   135.8 160
-//        32  5376  7168              16   174.9 140.6   168.0 171.0
-//         8  1536  2048              24     8.5  10.6     9.6  13.0
-// (few matrices: the tiles' latency counts).
+// registers, 16 rows at a time; in it and in 128 x 128 and 256 x 128 tiles:
+//   experts     n     k  rows an expert   4 bits                   8 bits
+//       128  1536  2048               4    44.6*  48.1   48.2      41.1*  59.8   53.2
+//       128  1536  2048              12    55.3   50.5*  49.6      52.8*  60.9   54.1
+//        32  5376  7168               8   147.3  126.0* 140.7     125.5* 166.0  153.9
+//        32  5376  7168              16   182.5  128.1* 142.5     169.3  168.1  157.3*
+//         8  1536  2048              24     8.8*  11.9   16.3       9.4*  14.3   18.8
+//         8  3000  4096               6    16.2*  21.0   29.5      15.1*  27.5   34.1
+//         8  3000  4096              12    21.6   21.2*  29.8      21.4*  27.9   34.4
+//         1  2048  4096              64     7.8   15.5*  22.8       9.4   21.2*  27.9
+//         1  8192  8192              32    14.9   35.7*  54.8      17.0   51.0*  63.9
+//         1  8192  8192             128    42.8   39.8*  58.1      53.5   58.5*  71.1
+// Few matrices leave the tiles to their latency, one workgroup walking a long axis
+// alone.  The rule sees that below 2^26 values only: larger single matrices with 7
+// (8 bits: 13) to some 100 rows lose up to 2.4 and 3 times.  So do a few hot experts
+// among very many idle ones the other way: their mean says streaming, which reads a
+// matrix once per 16 rows.
 //
 // us in 128 x 128, 256 x 128 and 256 x 256 (channels x rows):
-//   rows experts     n     k   4 bits             8 bits
-//   2048       1  4096  4096    24.8  30.9  34.0   37.5  37.7  52.3
-//   1024       8  4096  4096                       40.8  41.4
-//   4096       8  1536  2048    17.1  19.9  24.8   23.0  22.5  33.5
-//  16384       8  2048  4096    88.6  97.5 100.8  149.1 122.9 163.8
-//  32768     128  1536  2048   111.5 105.4 122.1  154.9 132.2 181.6
-//  32768      32  7168  2688     513   469   495
-//   8192       1  8192  8192   300.0 297.6 261.9  514.6 413.9 414.8
+//   rows experts     n     k   4 bits                     8 bits
+//   2048       1  4096  4096    27.2*   30.4    33.6        39.4*    36.9
+//   1024       8  4096  4096    29.7*   34.9    40.0        40.2*    40.5
+//   4096       8  1536  2048    18.1*   19.3    24.4        22.2*    21.7
+//  16384       8  2048  4096    91.9*  101.1   106.5       153.4    124.6*
+//  16384       8  4096  4096   181.7   180.9*  177.7       291.9    235.8*
+//  16384       8  4096  4608   198.5   202.4   202.6*      311.7    265.1*
+//  32768       8  4096  4608   391.5   391.7   354.9*      612.8    517.1*
+//  32768     128  1536  2048   117.9   109.0*  127.5       158.0    133.7*
+//  32768      32  7168  2688   535.5   479.1*  506.3       730.3    618.2*
+//  32768      32  5376  7168   910.2   877.4   796.1*     1377.8   1180.2*
+//   8192       1  8192  8192   305.7   301.0   266.8*      522.3    420.3*
 // So rows in 8 bits take 256 x 128 (two workgroups to a CU, one's products under
 // the other's results; the LDS keeps up with them) but where that would leave
 // channels or CUs idle.  Rows in 4 bits need more of the LDS than the products

@@ -89,10 +89,11 @@ __global__ __launch_bounds__(kThreads) void quantize4_rows_kernel(const uint16_t
 // wave with the same columns; the transposed bytes pass through LDS.
 //
 // Values stay bf16 pairs: the conversion divides by the scale, and magnitudes
-// compare as integers.  Memory-bound, both layouts: 128 matrices of 1536 x 2048 268
-// us (4.6 TB/s), 8 of 4096 x 7168 124 us (5.8; their results stay in the last
-// cache).  In fp32, the pieces dealt to the XCDs one by one, and with 8-way
-// conflicts in LDS: 296 and 154.
+// compare as integers.  Memory-bound: 128 matrices of 1536 x 2048 in both layouts
+// 200 us (6.1 TB/s) where values4_kernel reads the results next, 267 (4.6) one such
+// launch right behind the other, in one layout 164 (6.2) so; 8 of 4096 x 7168 in
+// both 124 (5.8).  In fp32, the pieces dealt to the XCDs one by one, and with 8-way
+// conflicts in LDS, one behind the other: 296 and 154.
 constexpr int kTransStride4 = kBlk / 2 + 16;  // LDS bytes of a row of the transposed piece
 // Its 16-byte pieces are exchanged so that eight rows' lie in different banks.
 __device__ __forceinline__ int trans_place(int row, int piece) { return 16 * (piece ^ ((row >> 4) & 3)); }

@@ -89,3 +89,28 @@ def test_both_layouts_into_the_same_memory_are_refused(monkeypatch, four):
             quant(w, transposed=True, out=pair)
     with pytest.raises(m.MoePlanError):  # past every check: the library refuses the handle
         quant(w, transposed=True, out=(a, b))
+
+
+@pytest.mark.parametrize("lead,cols", [((5,), 256), ((3,), 32), ((4,), 300), ((2, 7), 1000), ((3, 40), 2688)])
+def test_matrices_in_the_published_order(lead, cols):
+    """The README's way to bring values and scales, both row by row, into Blocks4: the same values, padding of zeros."""
+    import os
+    import load_balance_planning_amd as m
+    from tests import expert4_refs as refs4
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    code = text[text.index("def published_blocks4"):]
+    scope = {"torch": torch, "mp": m}
+    exec(code[: code.index("```")], scope)
+    g = torch.Generator().manual_seed(cols)
+    n = -(-cols // 32)
+    code4 = torch.randint(0, 16, (*lead, 2 * -(-cols // 2)), generator=g)
+    code4[..., cols:] = 0
+    scale = torch.randint(90, 160, (*lead, n), generator=g)
+    table = torch.cat([refs4.CODES, -refs4.CODES])
+    want = (table[code4][..., :cols] * torch.exp2(scale.double() - 127).repeat_interleave(32, -1)[..., :cols])
+    q = (code4[..., ::2] | code4[..., 1::2] << 4).to(torch.uint8)
+    b = scope["published_blocks4"](q, scale.to(torch.uint8), cols)
+    assert (tuple(b.q.shape), tuple(b.scale.shape)) == m.Blocks4.shapes(lead, cols)
+    assert b.q.is_contiguous() and b.scale.is_contiguous()
+    assert torch.equal(refs4.values(b), want)
+    assert (refs4.codes(b)[..., cols:] == 0).all() and (refs4.scales(b)[..., n:] == 1).all()
