@@ -303,3 +303,51 @@ def test_the_gated_activation_is_within_its_bound(mp, small):
     q, s = refs4.quantize(refs.swiglu(y.double()))
     assert torch.equal(u8(b.scale), s) and (s[0, :, 0] == 127).all()
     assert torch.equal(refs4.codes(b), q)
+
+
+# ---- the largest sizes ---------------------------------------------------------------
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("T,E,k,H,f", [(64, 32, 32, 8, 1 << 20), (64, 4, 2, 1 << 20, 24)])
+def test_the_widest_layers_of_few_tokens(mp, T, E, k, H, f, bits):
+    """2^31 bytes of activations, and rows of 2^20: tokens of a full call as by themselves.  (The shares of the second
+    product are others then: fp32 sums in another order, bf16's half step each way, and activations whose fp32 value
+    lies at a border of e4m3.)"""
+    print("experts T=%d E=%d k=%d H=%d f=%d bits=%d" % (T, E, k, H, f, bits), flush=True)
+    layer, one = (mp.Layer(mp.make_config(t, E, k, 1, 1, H, 0), cooc=False) for t in (T, 1))
+    dev = layer.device
+    g = torch.Generator(device=dev).manual_seed(1)
+    n = lambda *s, by: torch.randn(*s, generator=g, device=dev, dtype=BF) * by
+    quant = layer.quantize_weights4 if bits == 4 else layer.quantize_weights
+    w1 = quant(n(E, 2 * f, H, by=H ** -0.5))
+    w2 = quant(n(E, H, f, by=f ** -0.5))
+    hidden = n(T, H, by=1.0)
+    idx = torch.rand(T, E, generator=g, device=dev).argsort(-1)[:, :k].to(torch.int32)
+    weight = torch.rand(T, k, generator=g, device=dev)
+    out = layer.experts(hidden, weight, w1, w2, topk_idx=idx).float()
+    assert torch.isfinite(out).all() and (out != 0).float().mean() > 0.9
+    for t in (0, T // 2, T - 1):
+        alone = one.experts(hidden[t:t + 1], weight[t:t + 1], w1, w2, topk_idx=idx[t:t + 1]).float()
+        assert torch.allclose(alone[0], out[t], rtol=2.0 ** -7, atol=2e-3 * float(out[t].abs().max())), t
+    assert layer.status() == 0 and one.status() == 0
+    layer.close()
+    one.close()
+
+
+def test_the_widest_rows_and_matrices(mp, small):
+    """2^24 columns, and matrices of 2^24 rows: each block as elsewhere."""
+    dev, cols = small.device, 1 << 24
+    x = torch.randn(2, cols, device=dev, dtype=BF, generator=torch.Generator(device=dev).manual_seed(1))
+    rows, lines = small.quantize4(x), small.quantize4(x.view(-1, 256))
+    assert torch.equal(u8(rows.q).view(-1, 128), u8(lines.q))
+    assert torch.equal(u8(rows.scale).transpose(0, 1).reshape(-1, 8), u8(lines.scale)[0])
+    assert torch.equal(small.values4(rows).view(-1, 256), small.values4(lines))
+    wide = small.swiglu4(torch.cat([x[:1], x[1:]], 1))      # one row: gate, then up
+    parts = small.swiglu4(torch.cat([x[0].view(-1, 256), x[1].view(-1, 256)], 1))
+    assert torch.equal(u8(wide.q).view(-1, 128), u8(parts.q))
+    assert torch.equal(u8(wide.scale).view(-1, 8), u8(parts.scale)[0])
+    del lines, parts, wide
+    one, turned = small.quantize_weights4(x[:1].t().contiguous().view(1, cols, 1), transposed=True)
+    alone, row = small.quantize4(x[0].view(cols, 1)), small.quantize4(x[:1])
+    assert torch.equal(u8(one.q)[0], u8(alone.q)) and torch.equal(u8(one.scale)[0], u8(alone.scale))
+    assert torch.equal(u8(turned.q)[0], u8(row.q)) and torch.equal(u8(turned.scale)[0], u8(row.scale))
