@@ -132,7 +132,7 @@ extern "C" int moex_matmul(moe_plan_t h, const moe_plan_out* plan, const int32_t
   const int rc = check_product(h, plan, inst_offset, n, k);
   if (rc != MOE_OK) return rc;
   if (h->d.T > 0 && (!blocks_ok(x, x_scale) || !blocks_ok(w, w_scale) || !y)) return MOE_ERR_INVALID_ARG;
-  // one 256-thread workgroup per tile, fewer than 2^32 work-items a launch
+  // the resident workgroups number tiles in 32 bits; no call reaches this whose result fits the card's memory
   if (moe::matmul_tiles(instances(h->d, plan, inst_offset), n) >= (int64_t)1 << 24) return MOE_ERR_UNSUPPORTED;
   const DeviceScope on_device(h->device);
   if (!on_device.ok()) return MOE_ERR_HIP;

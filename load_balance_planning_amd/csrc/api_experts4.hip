@@ -80,8 +80,7 @@ extern "C" int moex4_matmul(moe_plan_t h, const moe_plan_out* plan, const int32_
   if (h->d.T > 0 && (!(x_bits == 4 ? blocks4_ok(x, x_scale) : blocks_ok(x, x_scale)) || !blocks4_ok(w, w_scale) || !y))
     return MOE_ERR_INVALID_ARG;
   const moe::Instances in{plan->n_inst, plan->inst_expert, inst_offset, h->d.cap, h->d.E, (int64_t)h->d.T * h->d.k};
-  // moex_matmul's limit, which no call reaches whose result fits the card's memory.  (The resident workgroups number
-  // tiles, and step past the last, in 32 bits: 2^30 would do.)
+  // moex_matmul's limit; no call reaches it whose result fits the card's memory
   if (moe::matmul4_tiles(in, x_bits, n, k) >= (int64_t)1 << 24) return MOE_ERR_UNSUPPORTED;
   const DeviceScope on_device(h->device);
   if (!on_device.ok()) return MOE_ERR_HIP;

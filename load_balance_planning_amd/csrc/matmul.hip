@@ -161,13 +161,9 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), BC == 256 ? 
   const int nct = (n + BC - 1) / BC;
   const int n_inst = instance_count(in);
   const int row_tiles = __builtin_amdgcn_readfirstlane(count_row_tiles(in, BT, pre, sums));
-  // Workgroups go to the eight XCDs in turn: each XCD takes a run of
-  // consecutive tiles, four row tiles by all channel tiles at a time, so that
-  // the tiles that it works on at once share their operands in its L2.
-  const int total = row_tiles * nct;  // below 2^24
-  const int xcd = blockIdx.x & 7, slots = gridDim.x >> 3;
-  const int last = (int)((int64_t)total * (xcd + 1) / 8);
-  int tile = (int)((int64_t)total * xcd / 8) + (blockIdx.x >> 3);
+  int tile, last;
+  const int slots = gridDim.x >> 3;
+  xcd_run(row_tiles * nct, &tile, &last);
   if (tile >= last) return;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -182,24 +178,7 @@ __global__ __launch_bounds__((TileShape<BC, BT, WC, WT>::kThreads), BC == 256 ? 
   const int place_c = (threadIdx.x & 15) ^ piece_swizzle<true>(pair);
   const int place_t = (threadIdx.x & 15) ^ piece_swizzle<false>(pair);
   const int wc = wave % WC * S::kWaveC, wt = wave / WC * S::kWaveT;
-  // a tile: its rows, channels, expert
-  struct Tile {
-    int r0, rows, c0, chans, expert, rt;
-  };
-  auto locate = [&](int t) {
-    const int band = t / (4 * nct), in_band = t - band * 4 * nct;
-    const int band_rows = min(4, row_tiles - band * 4);
-    const int rt = band * 4 + in_band % band_rows;
-    const int i = instance_of(pre, n_inst, rt);
-    Tile o;
-    o.c0 = __builtin_amdgcn_readfirstlane(in_band / band_rows * BC);
-    o.chans = min(BC, n - o.c0);
-    o.r0 = __builtin_amdgcn_readfirstlane(in.offset[i] + (rt - pre[i]) * BT);
-    o.rows = min(BT, __builtin_amdgcn_readfirstlane(in.offset[i + 1]) - o.r0);
-    o.expert = __builtin_amdgcn_readfirstlane(in.expert[i]);
-    o.rt = rt;
-    return o;
-  };
+  auto locate = [&](int t) { return locate_tile<BC, BT>(in, pre, n_inst, row_tiles, nct, n, t); };
   Tile at;
   uint32_t off_c[S::kPassC], off_t[S::kPassT], xs_off[S::kT], off_f;
   auto set_offsets = [&]() {

@@ -1,5 +1,6 @@
 // What the experts' products in tiles share: where rows lie in LDS, the barrier that
-// waits for loads into it, and the row tiles of a plan's instances.
+// waits for loads into it, the row tiles of a plan's instances, and which tiles a
+// workgroup takes.
 #pragma once
 
 #include "instances.h"
@@ -79,6 +80,37 @@ template <int NEWER = 0>
   const int first = (__popcll(coarse) - 1) * stride;
   const uint64_t fine = __ballot(lane < stride && first + lane < n && pre[min(first + lane, n)] <= t);
   return first + __popcll(fine) - 1;
+}
+
+// The tiles of a workgroup: from *tile on every (gridDim.x / 8)-th below *last.
+// Workgroups go to the eight XCDs in turn: each XCD takes a run of consecutive
+// tiles (below 2^24 in all), four row tiles by all channel tiles at a time, so that
+// the tiles that it works on at once share their operands in its L2.
+[[maybe_unused]] __device__ __forceinline__ void xcd_run(int total, int* tile, int* last) {
+  const int xcd = blockIdx.x & 7;
+  *last = (int)((int64_t)total * (xcd + 1) / 8);
+  *tile = (int)((int64_t)total * xcd / 8) + (blockIdx.x >> 3);
+}
+
+// A tile: its rows, channels, expert.
+struct Tile {
+  int r0, rows, c0, chans, expert, rt;
+};
+template <int BC, int BT>
+[[maybe_unused]] __device__ __forceinline__ Tile locate_tile(const Instances& in, const int32_t* pre, int n_inst,
+                                                             int row_tiles, int nct, int n, int t) {
+  const int band = t / (4 * nct), in_band = t - band * 4 * nct;
+  const int band_rows = min(4, row_tiles - band * 4);
+  const int rt = band * 4 + in_band % band_rows;
+  const int i = instance_of(pre, n_inst, rt);
+  Tile o;
+  o.c0 = __builtin_amdgcn_readfirstlane(in_band / band_rows * BC);
+  o.chans = min(BC, n - o.c0);
+  o.r0 = __builtin_amdgcn_readfirstlane(in.offset[i] + (rt - pre[i]) * BT);
+  o.rows = min(BT, __builtin_amdgcn_readfirstlane(in.offset[i + 1]) - o.r0);
+  o.expert = __builtin_amdgcn_readfirstlane(in.expert[i]);
+  o.rt = rt;
+  return o;
 }
 
 }  // namespace
