@@ -687,21 +687,14 @@ class Layer:
             return self.torch.empty(*shape, dtype=dtype, device=self.device)
 
     @staticmethod
-    def _overlap(t, u) -> bool:
-        """Whether two contiguous tensors share memory."""
-        a, b = t.data_ptr(), u.data_ptr()
-        return a < b + u.numel() * u.element_size() and b < a + t.numel() * t.element_size()
-
-    @staticmethod
-    def _check_apart(out, t):
-        """Memory that a kernel still reads may not be what it writes."""
-        if Layer._overlap(out, t):
-            raise ValueError("out overlaps memory that the call reads")
-
-    def _check_pair(self, a, b):
-        """The two layouts that one call writes, each in memory of its own."""
-        if self._overlap(a.q, b.q) or self._overlap(a.scale, b.scale):
-            raise ValueError("the two results of out overlap")
+    def _check_apart(out, *others):
+        """Memory that a kernel writes may not be what it still reads, or another of its results (contiguous tensors)."""
+        begin = out.data_ptr()
+        end = begin + out.nbytes
+        for t in others:
+            at = t.data_ptr()
+            if at < end and begin < at + t.nbytes:
+                raise ValueError("out overlaps memory that the call reads or writes")
 
     def _result(self, out, shape, dtype, stream):
         """`out`, checked, or memory of the call's own."""
@@ -756,7 +749,8 @@ class Layer:
         given = out_t is not None
         out_t = self._result_blocks(out_t, stream, (E, k), n, (E, blocks(k))) if transposed else Blocks(None, None, n)
         if given:
-            self._check_pair(out, out_t)
+            self._check_apart(out.q, out_t.q, out_t.scale)
+            self._check_apart(out.scale, out_t.q, out_t.scale)
         moex_quantize_weights(self.handle, _addr(w), E, n, k, _addr(out.q), _addr(out.scale), _addr(out_t.q),
                               _addr(out_t.scale), self._stream(stream))
         return (out, out_t) if transposed else out
@@ -868,8 +862,7 @@ class Layer:
             grad_rows, grad_weight = out
             self._check_16bit(grad_rows, (T * k, H), "out[0]")
             self._check_tensor(grad_weight, (T, k), torch.float32)
-            self._check_apart(grad_rows, expert_out)
-            self._check_apart(grad_rows, grad_out)
+            self._check_apart(grad_rows, expert_out, grad_out)
         moex_combine_grad(self.handle, _addr(weight), _addr(slot_pos), _addr(expert_out), _addr(grad_out),
                           _addr(grad_rows), _addr(grad_weight), self._stream(stream))
         return grad_rows, grad_weight
@@ -921,7 +914,8 @@ class Layer:
         given = out_t is not None
         out_t = self._result_blocks4(out_t, stream, (E, k), n) if transposed else Blocks4(None, None, n)
         if given:
-            self._check_pair(out, out_t)
+            self._check_apart(out.q, out_t.q, out_t.scale)
+            self._check_apart(out.scale, out_t.q, out_t.scale)
         moex4_quantize_weights(self.handle, _addr(w), E, n, k, _addr(out.q), _addr(out.scale), _addr(out_t.q),
                                _addr(out_t.scale), self._stream(stream))
         return (out, out_t) if transposed else out
@@ -1012,8 +1006,7 @@ class Layer:
             out = torch.empty_like(hidden) if stream is None else self._empty((T, H), hidden.dtype, stream)
         else:
             self._check_16bit(out, (T, H), "out")
-            for t in (hidden, topk_idx, weight, w1.q, w1.scale, w2.q, w2.scale):
-                self._check_apart(out, t)
+            self._check_apart(out, hidden, topk_idx, weight, w1.q, w1.scale, w2.q, w2.scale)
         work = torch.empty(nbytes, dtype=torch.uint8, device=self.device) if stream is None else \
             self._empty((nbytes,), torch.uint8, stream)
         moex4_experts(self.handle, hidden.data_ptr(), topk_idx.data_ptr(), weight.data_ptr(), 4 if four else 8, f,
