@@ -93,7 +93,7 @@ def test_both_layouts_into_the_same_memory_are_refused(monkeypatch, four):
 
 @pytest.mark.parametrize("lead,cols", [((5,), 256), ((3,), 32), ((4,), 300), ((2, 7), 1000), ((3, 40), 2688)])
 def test_matrices_in_the_published_order(lead, cols):
-    """The README's way to bring values and scales, both row by row, into Blocks4: the same values, padding of zeros."""
+    """The documented way to bring values and scales, both row by row, into Blocks4: the same values, padding of zeros."""
     import os
     import load_balance_planning_amd as m
     from tests import expert4_refs as refs4
